@@ -83,8 +83,9 @@ typedef enum {
 
 /* Bits OR-ed into *dev_status by the device. */
 #define QVG_DEV_NONFINITE 0x1u /* X held a NaN or an infinity */
-#define QVG_DEV_TIMEOUT 0x2u   /* a pipeline wait in the assignment kernel gave up */
-#define QVG_DEV_BAD_INDEX 0x4u /* a stored cluster index was >= C; it was clamped to C-1 */
+#define QVG_DEV_TIMEOUT 0x2u   /* a pipeline wait in a tensor-core kernel gave up */
+#define QVG_DEV_BAD_INDEX 0x4u /* a stored cluster index was >= C (it was clamped to C-1), or a
+                                  slot, page or length out of range */
 
 typedef enum { QVG_F16 = 0, QVG_BF16 = 1, QVG_F32 = 2 } qvg_dtype;
 
@@ -322,13 +323,179 @@ qvg_status qvg_attention(const qvg_attention_params *params, const void *Q,
                          void *workspace, size_t workspace_bytes, uint32_t *dev_status,
                          void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * A paged cache of recent tokens.
+ *
+ * qvg_quantize compresses whole chunks of tokens.  The tokens of the chunk that is still
+ * growing, and any that are to stay uncompressed, live in pages: qvg_rope turns queries (and
+ * gradients) by their positions, qvg_page_write stores new keys (turned on the way if asked)
+ * and values in 16 or 8 bits, qvg_page_attention lets the new tokens attend to the pages,
+ * qvg_page_read gives rows back in the layout qvg_quantize takes.
+ *
+ * A page holds page_tokens consecutive tokens of one sequence, all heads.  Arrays
+ * (row-major, caller-owned device memory, 16-byte aligned):
+ *   k, v              [n_pages][n_heads][page_tokens][128] of the page format
+ *   k_scale, v_scale  float [n_pages][n_heads][page_tokens], 8-bit formats only
+ * A slot is page * page_tokens + row.  Token t of sequence b is row t % page_tokens of page
+ * page_table[b][t / page_tokens]; page_table is int32 [n_seqs][max_pages], and entries that
+ * no token below the sequence's length falls in are never read.
+ * page_tokens: 16, 32, 64 or 128.
+ * ------------------------------------------------------------------------------------ */
+
+/* Page formats.  The 16-bit ones hold the value rounded to nearest even.  The 8-bit ones hold
+ * codes and one scale per (token, head, key or value): with a = max_k |x_k| over the row,
+ *   E4M3: s = a / 448, code = E4M3(x * (448 / a)), to nearest even;
+ *   INT8: s = a / 127, code = rint(x * (127 / a)),
+ * in fp32, and the stored value is s * code.  A row with a < 2^-100 is stored as zeros
+ * (s = 0); a row that holds a NaN or an infinity gets s = NaN, so that it reads as NaN, and
+ * QVG_DEV_NONFINITE is reported. */
+typedef enum {
+    QVG_PAGE_F16 = 0,
+    QVG_PAGE_BF16 = 1,
+    QVG_PAGE_E4M3 = 2,
+    QVG_PAGE_INT8 = 3
+} qvg_page_format;
+
+typedef struct {
+    void *k;
+    void *v;
+    float *k_scale; /* NULL for the 16-bit formats */
+    float *v_scale;
+} qvg_pages;
+
+/* Rotary positions.  Pair p of a row, 0 <= p < rot_dim / 2, is turned by the angle
+ * 2 pi * positions[axis(p)][token] * freqs[p] / 2^64 and multiplied by mscale; channels from
+ * rot_dim on stay as they are.  Pair p is channels (2p, 2p + 1) when interleaved, else
+ * (p, p + rot_dim / 2).  Axis a owns the next sections[a] pairs.
+ * freqs[p] is the pair's turns per position as a 64-bit fraction, round(f * 2^64) mod 2^64:
+ * the product with an integer position wraps exactly, so far positions lose nothing. */
+typedef struct {
+    int32_t rot_dim;     /* a multiple of 8, 8 .. 128 */
+    int32_t interleaved; /* 0 or 1 */
+    int32_t n_axes;      /* 1 .. 4 */
+    int32_t sections[4]; /* pairs of each axis; they add up to rot_dim / 2 */
+    float mscale;        /* finite */
+    int64_t pos_stride;  /* elements between the axes' rows of positions */
+    const int64_t *positions; /* [n_axes][n_tokens], 8-byte aligned */
+    const uint64_t *freqs;    /* [rot_dim / 2] */
+} qvg_rotary;
+
+/* Strides in elements; a row's 128 channels are contiguous, and row starts are 16-byte
+ * aligned.  An input stride may be 0 (one row for every head, say). */
+typedef struct {
+    int64_t n_tokens; /* >= 0; 0 enqueues nothing */
+    int32_t n_heads;
+    int32_t d;        /* 128 */
+    int32_t dtype;    /* qvg_dtype of X and Y */
+    int32_t backward; /* 0: Y = R X.  1: Y = R^T X, the gradient of X given that of Y (the
+                         angles negated, mscale kept) */
+    int64_t x_token_stride, x_head_stride;
+    int64_t y_token_stride, y_head_stride;
+} qvg_rope_params;
+
+/* Turn X [n_tokens][n_heads][128] into Y.  In place when Y is X with the same strides;
+ * otherwise the two may not overlap.  fp32 arithmetic, one rounding to dtype. */
+qvg_status qvg_rope(const qvg_rope_params *params, const qvg_rotary *rotary, const void *X,
+                    void *Y, void *stream);
+
+typedef struct {
+    int64_t n_tokens;    /* >= 0; 0 enqueues nothing */
+    int32_t n_heads;     /* key/value heads */
+    int32_t d;           /* 128 */
+    int32_t page_tokens;
+    int32_t format;      /* qvg_page_format */
+    int64_t n_pages;     /* n_pages * n_heads * page_tokens < 2^31 */
+    int32_t in_dtype;    /* qvg_dtype of K and V */
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+} qvg_page_write_params;
+
+/* Store K and V [n_tokens][n_heads][128] at slots[token] (int64, 8-byte aligned, one slot at
+ * most once).  A negative slot skips its token; one past the pool is skipped and reported as
+ * QVG_DEV_BAD_INDEX.  rotary: NULL, or the turn that keys (not values) get in fp32 before
+ * they are rounded. */
+qvg_status qvg_page_write(const qvg_page_write_params *params, const void *K, const void *V,
+                          const int64_t *slots, const qvg_rotary *rotary, const qvg_pages *pages,
+                          uint32_t *dev_status, void *stream);
+
+typedef struct {
+    int32_t n_seqs;
+    int32_t n_heads;
+    int32_t d;           /* 128 */
+    int32_t page_tokens;
+    int32_t format;
+    int32_t out_dtype;   /* qvg_dtype of X */
+    int64_t n_pages;
+    int32_t max_pages;   /* entries of a page-table row */
+    int64_t first;       /* tokens [first, first + count) of every sequence are read */
+    int64_t count;       /* >= 0; 0 enqueues nothing */
+    int64_t x_seq_stride, x_tensor_stride; /* elements of X between sequences / tensors */
+} qvg_page_read_params;
+
+/* Give tokens back as X [n_seqs][2 * n_heads][count][128]: head h's keys in tensor 2h, its
+ * values in tensor 2h + 1 (one sequence is then an X of qvg_quantize).  Rows at and past a
+ * sequence's length (seq_lens int32 [n_seqs]) are zeros.  A page-table entry outside the pool
+ * gives zeros and QVG_DEV_BAD_INDEX; a length past the table is cut to it and reported so. */
+qvg_status qvg_page_read(const qvg_page_read_params *params, const qvg_pages *pages,
+                         const int32_t *page_table, const int32_t *seq_lens, void *X,
+                         uint32_t *dev_status, void *stream);
+
+typedef struct {
+    int32_t n_seqs;
+    int32_t n_q_heads;   /* a multiple of n_heads: query heads h * g .. h * g + g - 1, with
+                            g = n_q_heads / n_heads <= 128, share key/value head h */
+    int32_t n_heads;
+    int32_t d;           /* 128 */
+    int32_t page_tokens;
+    int32_t format;      /* QVG_PAGE_F16 with fp16 queries, QVG_PAGE_BF16 with bf16 queries,
+                            or an 8-bit format */
+    int32_t q_dtype;     /* QVG_F16 or QVG_BF16 */
+    int32_t out_dtype;   /* qvg_dtype of O */
+    int64_t n_pages;
+    int32_t max_pages;   /* entries of a page-table row */
+    int32_t causal;      /* 1: a query sees keys up to its own position; 0: every key */
+    int64_t window;      /* > 0: only the last `window` positions up to the query's own (and,
+                            unless causal, all after it); 0: no limit */
+    int64_t total_q;     /* query tokens of all sequences; 0 enqueues nothing */
+    int64_t max_q;       /* no sequence has more query tokens */
+    int64_t max_kv;      /* about the longest sequence: sizes the split of the work only */
+    float scale;         /* multiplies q.k before the softmax; finite */
+    int64_t q_token_stride, q_head_stride;
+    int64_t o_token_stride, o_head_stride;
+} qvg_page_attention_params;
+
+/* Workspace bytes qvg_page_attention needs (0 if the parameters are invalid, or none is). */
+size_t qvg_page_attention_workspace_bytes(const qvg_page_attention_params *params);
+
+/* Softmax attention of new tokens over the pages.  Sequence b has seq_lens[b] cached tokens,
+ * the last q_len of which are its queries' own: query i sits at position
+ * seq_lens[b] - q_len + i.  cu_q (int32 [n_seqs + 1], NULL: max_q queries each) holds where
+ * each sequence's queries start among the rows of Q [total_q][n_q_heads][128].
+ *   O_i = sum_j p_j v_j,  p = softmax over the keys j that i sees of scale * (q_i . k_j)
+ *   lse_i = log sum_j exp(scale * (q_i . k_j))    (lse: float [total_q][n_q_heads] or NULL)
+ * A query that sees no key gets O = 0 and lse = -infinity.  What a query does not see cannot
+ * change its row, NaN and infinities included.
+ * Scores, softmax and sums are fp32.  The weights p enter the product with the values in
+ * 16 bits, relative to a running maximum (q_dtype; bf16 for the 8-bit formats, after the
+ * value's scale is multiplied in); O is rounded once to out_dtype.
+ * Out-of-range page-table entries (read as page 0), lengths past the table (cut), and cu_q
+ * out of order, past total_q or with more than max_q queries (cut; the rows left out are
+ * not written) are reported as QVG_DEV_BAD_INDEX; a wait in a kernel's pipeline that gives
+ * up is reported as QVG_DEV_TIMEOUT, the rows concerned unspecified. */
+qvg_status qvg_page_attention(const qvg_page_attention_params *params, const void *Q,
+                              const qvg_pages *pages, const int32_t *page_table,
+                              const int32_t *seq_lens, const int32_t *cu_q, void *O, float *lse,
+                              void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                              void *stream);
+
 /* Static description of a status code. */
 const char *qvg_status_string(qvg_status status);
 
 /* Library version, (major << 16) | minor.
  *   1.0  quantize, reassign, dequantize, the static-scratch quantize.
  *   1.1  qvg_quant_params.qscheme and .centroid_format, qvg_dequant_params.qscheme (both
- *        structs grew: rebuild callers), qvg_attention. */
+ *        structs grew: rebuild callers), qvg_attention.  The paged cache (qvg_rope,
+ *        qvg_page_*) came later without a change to what 1.1 had. */
 uint32_t qvg_version(void);
 
 #ifdef __cplusplus

@@ -6,7 +6,9 @@ libqvg's kernels (video_kv_cache_gb300.qvg is the ctypes binding).
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
+from fractions import Fraction
 
 import torch
 
@@ -220,3 +222,304 @@ def attention(Q: torch.Tensor, k_cache: CompressedKV, v_cache: CompressedKV | No
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_attention")
     return out
+
+
+# ------------------------------------------------------------------------------------
+# The paged cache of recent tokens: rotary positions, writing, reading, attention
+# ------------------------------------------------------------------------------------
+
+_PAGE_FORMAT = {torch.float16: _c.QVG_PAGE_F16, torch.bfloat16: _c.QVG_PAGE_BF16,
+                torch.float8_e4m3fn: _c.QVG_PAGE_E4M3, torch.int8: _c.QVG_PAGE_INT8}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(x: torch.Tensor, what: str):
+    """x as rows [tokens][heads][128] of contiguous channels."""
+    _need(x.is_cuda and x.dim() == 3 and x.shape[2] == D and (x.stride(2) == 1 or x.numel() == 0),
+          "%s must be a CUDA tensor [tokens][heads][128] with contiguous channels" % what)
+    _need(x.dtype in _DT, "%s must be fp16, bf16 or fp32" % what)
+
+
+def _index(x: torch.Tensor, dtype, shape, what: str):
+    _need(x.is_cuda and x.dtype == dtype and tuple(x.shape) == tuple(shape) and x.is_contiguous(),
+          "%s must be a contiguous CUDA tensor %s of %s" % (what, list(shape), dtype))
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream that the call uses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_strides(x: torch.Tensor):
+    """Token and head stride; 0 where there is one row only, whose stride says nothing."""
+    return (x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
+
+
+@dataclass
+class RopeTable:
+    """Frequencies and layout of a rotary position code (see qvg_rotary)."""
+    freqs: torch.Tensor       # int64 [rot_dim / 2]: turns per position as 64-bit fractions
+    rot_dim: int
+    sections: tuple           # pairs of each position axis
+    interleaved: bool = False
+    mscale: float = 1.0
+
+    def __post_init__(self):
+        self.sections = tuple(int(s) for s in self.sections)
+        _need(1 <= len(self.sections) <= 4 and sum(self.sections) == self.rot_dim // 2,
+              "1 to 4 sections must add up to rot_dim / 2 pairs")
+        _index(self.freqs, torch.int64, (self.rot_dim // 2,), "freqs")
+
+    def rotary(self, positions: torch.Tensor, n: int) -> _c.qvg_rotary:
+        axes = len(self.sections)
+        if positions.dim() == 1:
+            positions = positions.view(1, -1)
+        _need(positions.is_cuda and positions.dtype == torch.int64 and positions.shape == (axes, n)
+              and (n <= 1 or positions.stride(1) == 1) and (axes == 1 or positions.stride(0) >= n),
+              "positions must be int64 [%d][%d] on the GPU, each axis contiguous" % (axes, n))
+        return _c.qvg_rotary(self.rot_dim, int(self.interleaved), axes,
+                             (*self.sections, *(0,) * (4 - axes)), self.mscale,
+                             positions.stride(0), positions.data_ptr(), self.freqs.data_ptr())
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, sections=None, scaling: str = "none",
+                     factor: float = 1.0, original_len: int = 4096, fast_turns: float = 32.0,
+                     slow_turns: float = 1.0):
+    """(radians per position of each pair, mscale): pair i of an axis with n pairs turns
+    base ** (-i / n) a position.  ``scaling`` fits longer contexts by ``factor``:
+      * "linear": every frequency divided by the factor (position interpolation);
+      * "stretched": a larger base, which slows the slowest pair by the factor and leaves the
+        fastest as it is;
+      * "by_parts" (YaRN, arXiv 2309.00071): pairs that turn more than ``fast_turns`` times in
+        ``original_len`` positions stay, those below ``slow_turns`` are divided by the factor,
+        a linear ramp between; mscale is 0.1 ln(factor) + 1."""
+    _need(scaling in ("none", "linear", "stretched", "by_parts"), "unknown scaling %r" % (scaling,))
+    _need(rot_dim >= 2 and rot_dim % 2 == 0 and base > 0 and factor >= 1,
+          "rot_dim must be even, base positive and factor at least 1")
+    sections = (rot_dim // 2,) if sections is None else tuple(sections)
+    _need(sum(sections) == rot_dim // 2, "sections must add up to rot_dim / 2")
+    out, mscale = [], 1.0
+    for n in sections:
+        b = base * factor ** (n / (n - 1.0)) if scaling == "stretched" and n > 1 else base
+        out += [b ** (-i / n) for i in range(n)]
+    if scaling == "linear":
+        out = [f / factor for f in out]
+    elif scaling == "by_parts":
+        turns = [original_len * f / (2 * math.pi) for f in out]
+        keep = [min(1.0, max(0.0, (t - slow_turns) / (fast_turns - slow_turns))) for t in turns]
+        out = [f * k + f / factor * (1 - k) for f, k in zip(out, keep)]
+        mscale = 0.1 * math.log(factor) + 1.0
+    return torch.tensor(out, dtype=torch.float64), mscale
+
+
+def rope_table(rot_dim: int = D, *, freqs=None, sections=None, interleaved: bool = False,
+               mscale: float | None = None, device="cuda", **kw) -> RopeTable:
+    """A rotary table on the device, from given radians per position of each pair or from
+    ``rope_frequencies(rot_dim, sections=sections, **kw)``.  ``sections`` gives the pairs of
+    each position axis (frame, row and column of a video token, say); one axis by default."""
+    if freqs is None:
+        freqs, made = rope_frequencies(rot_dim, sections=sections, **kw)
+        mscale = made if mscale is None else mscale
+    else:
+        _need(not kw, "freqs are given: %s would have no effect" % ", ".join(kw))
+    turns = torch.as_tensor(freqs, dtype=torch.float64).cpu() / (2 * math.pi)
+    _need(turns.shape == (rot_dim // 2,) and bool(torch.isfinite(turns).all()),
+          "freqs must be rot_dim / 2 finite numbers")
+    words = [round(Fraction(f) * 2 ** 64) % 2 ** 64 for f in turns.tolist()]
+    words = torch.tensor([w - 2 ** 64 if w >= 2 ** 63 else w for w in words], dtype=torch.int64)
+    return RopeTable(words.to(device), rot_dim, (rot_dim // 2,) if sections is None else sections,
+                     bool(interleaved), 1.0 if mscale is None else float(mscale))
+
+
+def rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, *,
+         out: torch.Tensor | None = None, backward: bool = False, stream=None) -> torch.Tensor:
+    """Turn X [n][heads][128] (fp16 / bf16 / fp32, any token and head strides) by its positions
+    (int64 [n], or [axes][n] for a table with several axes).  ``out`` may be X itself.
+    ``backward`` gives the gradient of X from that of the result."""
+    _rows(X, "X")
+    n, heads, _ = X.shape
+    if out is None:
+        out = _empty((n, heads, D), X.dtype, X.device, stream)
+    _rows(out, "out")
+    _need(out.shape == X.shape and out.dtype == X.dtype, "out must have the shape and type of X")
+    prm = _c.qvg_rope_params(n, heads, D, _DT[X.dtype], int(backward), *_row_strides(X),
+                             *_row_strides(out))
+    rc = _c.qvg_rope(prm, table.rotary(positions, n), X.data_ptr(), out.data_ptr(),
+                     _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_rope")
+    return out
+
+
+@dataclass
+class PagedKV:
+    """Pages of recent keys and values (layouts as in include/qvg.h).  The type of ``k`` and
+    ``v`` is the page format: fp16, bf16, float8_e4m3fn or int8; the last two have scales."""
+    k: torch.Tensor                        # [pages][heads][page_tokens][128]
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None    # fp32 [pages][heads][page_tokens]
+    v_scale: torch.Tensor | None = None
+
+    def __post_init__(self):
+        _need(self.k.dim() == 4 and self.k.shape[3] == D and self.k.dtype in _PAGE_FORMAT,
+              "pages are [pages][heads][page_tokens][128] of fp16, bf16, float8_e4m3fn or int8")
+        for t in (self.k, self.v):
+            _index(t, self.k.dtype, self.k.shape, "k and v")
+        wide = self.k.dtype in (torch.float16, torch.bfloat16)
+        for t in (self.k_scale, self.v_scale):
+            if wide:
+                _need(t is None, "16-bit pages have no scales")
+            else:
+                _need(t is not None, "8-bit pages need k_scale and v_scale")
+                _index(t, torch.float32, self.k.shape[:3], "scales")
+
+    @property
+    def n_pages(self):
+        return self.k.shape[0]
+
+    @property
+    def heads(self):
+        return self.k.shape[1]
+
+    @property
+    def page_tokens(self):
+        return self.k.shape[2]
+
+    @property
+    def format(self):
+        return _PAGE_FORMAT[self.k.dtype]
+
+    def buffers(self) -> _c.qvg_pages:
+        return _c.qvg_pages(self.k.data_ptr(), self.v.data_ptr(), _ptr(self.k_scale),
+                            _ptr(self.v_scale))
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
+
+
+def allocate_pages(n_pages: int, heads: int, page_tokens: int = 64, dtype=torch.bfloat16,
+                   device="cuda") -> PagedKV:
+    """An empty paged cache; ``dtype`` picks the page format."""
+    _need(dtype in _PAGE_FORMAT, "pages are fp16, bf16, float8_e4m3fn or int8")
+    shape = (n_pages, heads, page_tokens)
+    wide = dtype in (torch.float16, torch.bfloat16)
+
+    def scales():
+        return None if wide else torch.empty(shape, dtype=torch.float32, device=device)
+    return PagedKV(torch.empty((*shape, D), dtype=dtype, device=device),
+                   torch.empty((*shape, D), dtype=dtype, device=device), scales(), scales())
+
+
+def page_write(kv: PagedKV, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, *,
+               rope: RopeTable | None = None, positions: torch.Tensor | None = None,
+               status: torch.Tensor | None = None, stream=None) -> None:
+    """Store new tokens K and V [n][heads][128] at ``slots`` (int64 [n]: page * page_tokens +
+    row; negative: skipped), rounded to the pages' format; with ``rope`` the keys are first
+    turned by their positions."""
+    _rows(K, "K")
+    _rows(V, "V")
+    n = K.shape[0]
+    _need(K.shape == V.shape and K.dtype == V.dtype and K.shape[1] == kv.heads,
+          "K and V must be [n][%d][128] of one type" % kv.heads)
+    _index(slots, torch.int64, (n,), "slots")
+    _need((rope is None) == (positions is None), "rope and positions go together")
+    prm = _c.qvg_page_write_params(n, kv.heads, D, kv.page_tokens, kv.format, kv.n_pages,
+                                   _DT[K.dtype], *_row_strides(K), *_row_strides(V))
+    rc = _c.qvg_page_write(prm, K.data_ptr(), V.data_ptr(), slots.data_ptr(),
+                           None if rope is None else rope.rotary(positions, n), kv.buffers(),
+                           _ptr(status), _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_write")
+
+
+def _tables(page_table, seq_lens):
+    _need(page_table.dim() == 2, "page_table must be [sequences][pages]")
+    _index(page_table, torch.int32, page_table.shape, "page_table")
+    _index(seq_lens, torch.int32, page_table.shape[:1], "seq_lens")
+
+
+def page_read(kv: PagedKV, page_table: torch.Tensor, seq_lens: torch.Tensor, count: int, *,
+              first: int = 0, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+              status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Tokens [first, first + count) of every sequence as [sequences][2 * heads][count][128],
+    keys and values interleaved: ``out[b]`` is an X of ``quantize``.  Rows past a sequence's
+    length are zeros.  ``out`` may have larger sequence and tensor strides."""
+    _tables(page_table, seq_lens)
+    n_seqs, shape = page_table.shape[0], (page_table.shape[0], 2 * kv.heads, count, D)
+    if out is None:
+        out = _empty(shape, out_dtype, kv.k.device, stream)
+    _need(out.is_cuda and tuple(out.shape) == shape and out.dtype in _DT and
+          (count == 0 or (out.stride(3) == 1 and (count == 1 or out.stride(2) == D))),
+          "out must be %s with contiguous tokens" % (list(shape),))
+    prm = _c.qvg_page_read_params(n_seqs, kv.heads, D, kv.page_tokens, kv.format, _DT[out.dtype],
+                                  kv.n_pages, page_table.shape[1], first, count,
+                                  out.stride(0) if n_seqs > 1 else 0, out.stride(1))
+    rc = _c.qvg_page_read(prm, kv.buffers(), page_table.data_ptr(), seq_lens.data_ptr(),
+                          out.data_ptr(), _ptr(status), _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_read")
+    return out
+
+
+def page_attention(Q: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
+                   seq_lens: torch.Tensor, *, cu_q: torch.Tensor | None = None,
+                   max_q: int | None = None, max_kv: int | None = None, causal: bool = True,
+                   window: int = 0, scale: float | None = None, out_dtype=None,
+                   out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   return_lse: bool = False, workspace: torch.Tensor | None = None,
+                   status: torch.Tensor | None = None, stream=None):
+    """Attention of new tokens Q [total_q][q_heads][128] (fp16 / bf16) over the pages
+    (qvg_page_attention).  ``seq_lens`` counts each sequence's cached tokens, the queries' own
+    among them; ``cu_q`` (int32 [sequences + 1]) holds where each one's queries start, and
+    ``max_q`` a bound on their number; without ``cu_q`` every sequence has total_q / sequences.
+    ``max_kv`` (about the longest sequence, the page table's capacity by default) sizes the
+    split of the work.  Returns the output, and with ``return_lse`` the fp32 log-sum-exp
+    [total_q][q_heads] beside it."""
+    _rows(Q, "Q")
+    _tables(page_table, seq_lens)
+    total, q_heads, _ = Q.shape
+    n_seqs, max_pages = page_table.shape
+    if cu_q is None:
+        _need(total % n_seqs == 0 and (max_q is None or max_q == total // n_seqs),
+              "without cu_q every sequence has total_q / sequences queries")
+        max_q = total // n_seqs
+    else:
+        _index(cu_q, torch.int32, (n_seqs + 1,), "cu_q")
+        max_q = total if max_q is None else max_q
+    if out is None:
+        out = _empty((total, q_heads, D), Q.dtype if out_dtype is None else out_dtype, Q.device,
+                     stream)
+    _rows(out, "out")
+    _need(out.shape == Q.shape, "out must have the shape of Q")
+    if lse is None and return_lse:
+        lse = _empty((total, q_heads), torch.float32, Q.device, stream)
+    if lse is not None:
+        _index(lse, torch.float32, (total, q_heads), "lse")
+    prm = _c.qvg_page_attention_params(
+        n_seqs, q_heads, kv.heads, D, kv.page_tokens, kv.format, _DT[Q.dtype], _DT[out.dtype],
+        kv.n_pages, max_pages, int(causal), window, total, max_q,
+        max_pages * kv.page_tokens if max_kv is None else max_kv,
+        D ** -0.5 if scale is None else scale, *_row_strides(Q), *_row_strides(out))
+    if workspace is None:
+        need = _c.qvg_page_attention_workspace_bytes(prm)
+        if need:
+            workspace = _empty((need,), torch.uint8, Q.device, stream)
+    rc = _c.qvg_page_attention(prm, Q.data_ptr(), kv.buffers(), page_table.data_ptr(),
+                               seq_lens.data_ptr(), _ptr(cu_q), out.data_ptr(), _ptr(lse),
+                               _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                               _ptr(status), _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_attention")
+    return (out, lse) if return_lse else out

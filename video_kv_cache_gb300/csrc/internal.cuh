@@ -385,4 +385,76 @@ inline int64_t attn_split_len(int64_t N, int64_t heads) {
 }
 cudaError_t launch_attention(const APlan &p, cudaStream_t st);
 
+// ------------------------------------------------------------------------------------
+// The paged cache
+// ------------------------------------------------------------------------------------
+enum : int { PF_F16 = 0, PF_BF16 = 1, PF_E4M3 = 2, PF_INT8 = 3 };
+
+struct Rotary {
+    int rot, interleaved;  // rot = 0: no turn
+    int end[3];            // first pair past axis 0, 1, 2 (what follows belongs to the last axis)
+    float mscale;
+    int64_t pos_stride;
+    const int64_t *pos;
+    const uint64_t *freqs;
+};
+
+struct RopePlan {
+    int64_t n;
+    int heads, dtype, backward;
+    int64_t xt, xh, yt, yh;
+    Rotary r;
+    const void *X;
+    void *Y;
+};
+cudaError_t launch_rope(const RopePlan &p, cudaStream_t st);
+
+struct PWritePlan {
+    int64_t n;
+    int heads, page, fmt, dtype;
+    int64_t n_pages;
+    int64_t kt, kh, vt, vh;
+    Rotary r;
+    const void *K, *V;
+    const int64_t *slots;
+    void *k, *v;
+    float *ks, *vs;
+    uint32_t *status;
+};
+cudaError_t launch_page_write(const PWritePlan &p, cudaStream_t st);
+
+struct PReadPlan {
+    int B, heads, page, fmt, dtype, max_pages;
+    int64_t n_pages, first, count, xs, xt;
+    const void *k, *v;
+    const float *ks, *vs;
+    const int32_t *table, *lens;
+    void *X;
+    uint32_t *status;
+};
+cudaError_t launch_page_read(const PReadPlan &p, cudaStream_t st);
+
+struct PAttnPlan {
+    int B, HQ, H, G;  // sequences, query heads, key/value heads, query heads per key/value head
+    int page, max_pages, fmt, q_dtype, out_dtype, causal;
+    int64_t n_pages, window, total_q, max_q, max_kv;
+    float scale_log2;  // scale * log2(e): the softmax runs in powers of two
+    int64_t qt, qh, ot, oh;
+    const void *Q, *k, *v;
+    const float *ks, *vs;
+    const int32_t *table, *lens, *cu;
+    void *O;
+    float *lse;
+    int S;        // splits of each row tile's keys
+    float *part;  // [S][total_q * HQ][128] partial outputs, relative to their maximum
+    float *ml;    // [S][total_q * HQ][2] running maximum (log2) and weight sum
+    uint32_t *status;
+};
+cudaError_t launch_page_attention(const PAttnPlan &p, cudaStream_t st);
+int page_attention_splits(const PAttnPlan &p);
+
+// Entry-point helpers shared by the C ABI's translation units (qvg_api.cu).
+qvg_status device_info(int *num_sms);
+bool fault_inject_launch();
+
 }  // namespace qvg

@@ -1,0 +1,64 @@
+// Rotary positions: pair (x, y) of a row becomes m (x cos a - y sin a, x sin a + y cos a) with
+// a = 2 pi * position * frequency; the gradient is the same with the angle negated.
+//
+// Bound by memory: each row is read and written once (512 bytes a row in 16 bits against
+// about 20 warp instructions).  Sixteen lanes hold a row (rows.cuh) and take up to eight heads
+// of one token, so the sines and cosines, four pairs a lane, are computed once for all of them.
+#include "rows.cuh"
+
+namespace qvg {
+
+namespace {
+constexpr int kRopeHeads = 8;  // heads of one token that a half-warp turns
+constexpr int kRopeRows = 4;   // of which this many are in flight at once
+}  // namespace
+
+template <int DT, bool INTER>
+__global__ void __launch_bounds__(256) k_rope(RopePlan p) {
+    pdl_begin();
+    const int l = threadIdx.x & 15;
+    const int groups = (p.heads + kRopeHeads - 1) / kRopeHeads;
+    const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int64_t token = unit / groups;
+    if (token >= p.n) return;
+    const int h0 = (int)(unit - token * groups) * kRopeHeads, h1 = min(p.heads, h0 + kRopeHeads);
+    const Pieces at = pieces_of(l, p.r);
+    Turn t;
+    if (at.turned) t = turn_of(p.r, token, l, p.backward ? -1.f : 1.f);
+    for (int h = h0; h < h1; h += kRopeRows) {
+        Raw4<DT> ra[kRopeRows], rb[kRopeRows];
+#pragma unroll
+        for (int u = 0; u < kRopeRows; u++) {
+            if (h + u < h1) {
+                const int64_t x = token * p.xt + (h + u) * p.xh;
+                ra[u] = load_raw4<DT>(p.X, x + at.a);
+                rb[u] = load_raw4<DT>(p.X, x + at.b);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeRows; u++) {
+            if (h + u < h1) {
+                float a[4], b[4];
+                unpack4(ra[u], a);
+                unpack4(rb[u], b);
+                if (at.turned) apply_turn<INTER>(a, b, t);
+                const int64_t y = token * p.yt + (h + u) * p.yh;
+                store4<DT>(p.Y, y + at.a, a);
+                store4<DT>(p.Y, y + at.b, b);
+            }
+        }
+    }
+}
+
+cudaError_t launch_rope(const RopePlan &p, cudaStream_t st) {
+    const int64_t units = p.n * ((p.heads + kRopeHeads - 1) / kRopeHeads);
+    const dim3 grid((unsigned)((units + 15) / 16));
+    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(256), 0, st, p); };
+    if (p.r.interleaved)
+        return p.dtype == DT_F32 ? go(k_rope<DT_F32, true>)
+               : p.dtype == DT_BF16 ? go(k_rope<DT_BF16, true>) : go(k_rope<DT_F16, true>);
+    return p.dtype == DT_F32 ? go(k_rope<DT_F32, false>)
+           : p.dtype == DT_BF16 ? go(k_rope<DT_BF16, false>) : go(k_rope<DT_F16, false>);
+}
+
+}  // namespace qvg

@@ -1,0 +1,139 @@
+// What the paged-attention kernels share: a sequence's geometry, what a query sees, and how a
+// finished row is written.
+#pragma once
+
+#include "page_codes.cuh"
+#include "rows.cuh"
+
+namespace qvg {
+
+struct SeqInfo {
+    int64_t q0;  // first row of Q
+    int qn;      // query tokens
+    int len;     // cached tokens
+};
+
+// Sequence b's rows and length, cut to what the arguments allow.  One thread passes report =
+// true to have what was cut reported.
+__device__ __forceinline__ SeqInfo seq_info(const PAttnPlan &p, int b, bool report) {
+    SeqInfo s;
+    const int64_t cap = min((int64_t)p.max_pages * p.page, (int64_t)0x7FFFFF00);
+    const int64_t len = __ldg(p.lens + b);
+    s.len = (int)min(max(len, (int64_t)0), cap);
+    int64_t q0 = b * p.max_q, q1 = q0 + p.max_q;
+    if (p.cu) {
+        q0 = __ldg(p.cu + b);
+        q1 = __ldg(p.cu + b + 1);
+    }
+    const int64_t a = min(max(q0, (int64_t)0), p.total_q);
+    const int64_t e = min(max(q1, a), min(p.total_q, a + p.max_q));
+    s.q0 = a;
+    s.qn = (int)(e - a);
+    if (report && (s.len != len || a != q0 || e != q1)) or_status(p.status, QVG_DEV_BAD_INDEX);
+    return s;
+}
+
+// Keys [lo, hi) that query i of the sequence sees (empty when lo >= hi).
+__device__ __forceinline__ int seen_lo(const PAttnPlan &p, const SeqInfo &s, int i) {
+    if (p.window <= 0) return 0;
+    return (int)min(max((int64_t)s.len - s.qn + i + 1 - p.window, (int64_t)0), (int64_t)s.len);
+}
+__device__ __forceinline__ int seen_hi(const PAttnPlan &p, const SeqInfo &s, int i) {
+    return p.causal ? max(s.len - s.qn + i + 1, 0) : s.len;
+}
+
+// Page of a token, checked against the pool.
+__device__ __forceinline__ int64_t page_of(const PAttnPlan &p, int b, int token, int shift, bool &bad) {
+    const int page = __ldg(p.table + (int64_t)b * p.max_pages + (token >> shift));
+    if ((unsigned)page < (uint64_t)p.n_pages) return page;
+    bad = true;
+    return 0;
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The maximum a row's exponents are taken against: a row that has seen only -infinity (or
+// nothing) takes 0, so that its weights are 2^-inf = 0 and not NaN.
+__device__ __forceinline__ float exp_base(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ bool is_finite(float x) {
+    return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
+}
+
+// A 16-bit value that is NaN or infinite, multiplied by the zero weight of a query that does
+// not see its key, makes that query's row NaN.  So a row that did not come out finite, where
+// a mask hides keys from some rows of a tile, is computed once more by one warp, over the
+// keys that it sees and no others.  (8-bit codes are finite, and a hidden key's scale is
+// never multiplied in: they need none of this.)
+__device__ __forceinline__ bool redo_possible(const PAttnPlan &p) {
+    return (p.causal || p.window > 0) && (p.fmt == PF_F16 || p.fmt == PF_BF16);
+}
+// Row (query i of sequence b, query head hq): lane l gets channels 4l .. 4l+3, unnormalised.
+__device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, int hq, float o[4], float &m,
+                                      float &l) {
+    const int lane = threadIdx.x & 31;
+    const SeqInfo s = seq_info(p, b, false);
+    const int shift = 31 - __clz(p.page), h = hq / p.G;
+    const int lo = seen_lo(p, s, i), hi = seen_hi(p, s, i);
+    float q[4];
+#pragma unroll
+    for (int c = 0; c < 4; c++)
+        q[c] = load_x1(p.Q, p.q_dtype, (s.q0 + i) * p.qt + hq * p.qh + 4 * lane + c);
+    m = -INFINITY;
+    l = 0.f;
+    o[0] = o[1] = o[2] = o[3] = 0.f;
+    const int dt = p.fmt == PF_F16 ? DT_F16 : DT_BF16;
+    for (int j = lo; j < hi; j++) {
+        bool bad = false;
+        const int64_t row = ((page_of(p, b, j, shift, bad) * p.H + h) << shift) + (j & (p.page - 1));
+        float d = 0.f, v[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            d += q[c] * load_x1(p.k, dt, row * kD + 4 * lane + c);
+            v[c] = load_x1(p.v, dt, row * kD + 4 * lane + c);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+        const float sc = d * p.scale_log2, mn = fmaxf(m, sc), base = exp_base(mn);
+        const float corr = fast_exp2(m - base), w = fast_exp2(sc - base);
+        l = l * corr + w;
+#pragma unroll
+        for (int c = 0; c < 4; c++) o[c] = o[c] * corr + w * v[c];
+        m = mn;
+    }
+}
+
+__device__ __forceinline__ void store_out1(const PAttnPlan &p, int64_t off, float v) {
+    if (p.out_dtype == DT_F32)
+        static_cast<float *>(p.O)[off] = v;
+    else if (p.out_dtype == DT_BF16)
+        static_cast<__nv_bfloat16 *>(p.O)[off] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half *>(p.O)[off] = __float2half_rn(v);
+}
+// Four consecutive channels of the output.
+__device__ __forceinline__ void store_out4(const PAttnPlan &p, int64_t off, const float v[4]) {
+    if (p.out_dtype == DT_F32)
+        store4<DT_F32>(p.O, off, v);
+    else if (p.out_dtype == DT_BF16)
+        store4<DT_BF16>(p.O, off, v);
+    else
+        store4<DT_F16>(p.O, off, v);
+}
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? -INFINITY : l);  // NaN stays NaN
+}
+
+cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st);
+
+}  // namespace qvg

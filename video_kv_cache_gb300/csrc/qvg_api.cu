@@ -112,6 +112,8 @@ qvg_status check_quant_buffers(const qvg_quant_params *prm, const void *X, const
     return QVG_OK;
 }
 
+}  // namespace
+
 qvg_status device_info(int *num_sms) {
     int dev = 0, major = 0, minor = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QVG_ERR_CUDA;
@@ -122,6 +124,8 @@ qvg_status device_info(int *num_sms) {
     if (major != 10 || minor != 3) return QVG_ERR_DEVICE;
     return QVG_OK;
 }
+
+namespace {
 
 #define QVG_CUDA(call)                                \
     do {                                              \
@@ -151,6 +155,11 @@ FaultMode fault_mode() {
     if (!strcmp(v, "assign")) return kFaultAssign;
     return kFaultNone;
 }
+}  // namespace
+
+bool fault_inject_launch() { return fault_mode() == kFaultLaunch; }
+
+namespace {
 
 // The T smoothing stages: cold-start or warm centroids, then `iters` Lloyd rounds each.
 qvg_status run_stages(QPlan &p, const AssignMaps *maps, int num_sms, cudaStream_t st) {

@@ -1,0 +1,121 @@
+// A row of 128 channels held by 16 lanes, two pieces of four channels a lane: what the rotary
+// and paged-cache kernels load, turn and store.
+#pragma once
+
+#include "internal.cuh"
+
+namespace qvg {
+
+// Channel of the first element of each of lane l's two pieces (l < 16).  Within the turned
+// part each lane holds four whole pairs; the other lanes hold the channels behind it.
+struct Pieces {
+    int a, b;
+    bool turned;
+};
+__device__ __forceinline__ Pieces pieces_of(int l, const Rotary &r) {
+    Pieces c;
+    c.turned = 8 * l < r.rot;
+    const bool half = c.turned && !r.interleaved;
+    c.a = half ? 4 * l : 8 * l;
+    c.b = half ? r.rot / 2 + 4 * l : 8 * l + 4;
+    return c;
+}
+
+template <int DT>
+struct Raw4 {
+    uint2 w;
+};
+template <>
+struct Raw4<DT_F32> {
+    float4 w;
+};
+
+template <int DT>
+__device__ __forceinline__ Raw4<DT> load_raw4(const void *X, int64_t off) {
+    Raw4<DT> r;
+    if constexpr (DT == DT_F32)
+        r.w = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(X) + off));
+    else
+        r.w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(X) + off));
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack4(const Raw4<DT> &r, float v[4]) {
+    if constexpr (DT == DT_F32) {
+        v[0] = r.w.x; v[1] = r.w.y; v[2] = r.w.z; v[3] = r.w.w;
+    } else if constexpr (DT == DT_BF16) {
+        v[0] = __uint_as_float(r.w.x << 16);
+        v[1] = __uint_as_float(r.w.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(r.w.y << 16);
+        v[3] = __uint_as_float(r.w.y & 0xFFFF0000u);
+    } else {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&r.w.x));
+        const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&r.w.y));
+        v[0] = p.x; v[1] = p.y; v[2] = q.x; v[3] = q.y;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(void *Y, int64_t off, const float v[4]) {
+    if constexpr (DT == DT_F32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(Y) + off) = make_float4(v[0], v[1], v[2], v[3]);
+    else if constexpr (DT == DT_BF16)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(Y) + off) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(Y) + off) =
+            make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+}
+
+// The turn of a lane's four pairs for one token: sines and cosines times mscale.  position *
+// frequency is exact modulo a turn in 64 bits; its top 32 bits, read as a signed fraction of
+// a turn, are converted to fp32 (relative error 2^-24) and go to sincospif, which reduces
+// nothing and errs by a few units in the last place.
+struct Turn {
+    float c[4], s[4];
+};
+__device__ __forceinline__ Turn turn_of(const Rotary &r, int64_t token, int l, float sign) {
+    Turn t;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const int p = 4 * l + k;
+        const int axis = (p >= r.end[0]) + (p >= r.end[1]) + (p >= r.end[2]);
+        const uint64_t w = __ldg(reinterpret_cast<const unsigned long long *>(r.freqs) + p) *
+                           (uint64_t)__ldg(reinterpret_cast<const long long *>(r.pos) + axis * r.pos_stride + token);
+        float s, c;
+        sincospif((float)(int32_t)(uint32_t)(w >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+        t.c[k] = c * r.mscale;
+        t.s[k] = s * (r.mscale * sign);
+    }
+    return t;
+}
+
+__device__ __forceinline__ void turn_pair(float &x, float &y, float c, float s) {
+    const float u = x * c - y * s, v = x * s + y * c;
+    x = u;
+    y = v;
+}
+// Applies the turn to a lane's pieces: pairs inside each piece, or across the two.
+template <bool INTER>
+__device__ __forceinline__ void apply_turn(float a[4], float b[4], const Turn &t) {
+    if constexpr (INTER) {
+        turn_pair(a[0], a[1], t.c[0], t.s[0]);
+        turn_pair(a[2], a[3], t.c[1], t.s[1]);
+        turn_pair(b[0], b[1], t.c[2], t.s[2]);
+        turn_pair(b[2], b[3], t.c[3], t.s[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++) turn_pair(a[k], b[k], t.c[k], t.s[k]);
+    }
+}
+
+}  // namespace qvg

@@ -30,6 +30,7 @@ QVG_F16, QVG_BF16, QVG_F32 = 0, 1, 2
 QVG_QSCHEME_SYMMETRIC, QVG_QSCHEME_MIDRISE = 0, 1
 QVG_STEP_PLANES, QVG_STEP_GEMM, QVG_STEP_REFINE = 1, 2, 4
 QVG_CENTROIDS_F32, QVG_CENTROIDS_F16, QVG_CENTROIDS_BF16 = 0, 1, 2
+QVG_PAGE_F16, QVG_PAGE_BF16, QVG_PAGE_E4M3, QVG_PAGE_INT8 = 0, 1, 2, 3
 
 
 class qvg_quant_params(ctypes.Structure):
@@ -106,6 +107,100 @@ class qvg_attention_params(ctypes.Structure):
     ]
 
 
+class qvg_pages(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class qvg_rotary(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * 4),
+        ("mscale", ctypes.c_float),
+        ("pos_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("freqs", ctypes.c_void_p),
+    ]
+
+
+class qvg_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("n_heads", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("backward", ctypes.c_int32),
+        ("x_token_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("y_token_stride", ctypes.c_int64),
+        ("y_head_stride", ctypes.c_int64),
+    ]
+
+
+class qvg_page_write_params(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("n_heads", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("in_dtype", ctypes.c_int32),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+    ]
+
+
+class qvg_page_read_params(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("first", ctypes.c_int64),
+        ("count", ctypes.c_int64),
+        ("x_seq_stride", ctypes.c_int64),
+        ("x_tensor_stride", ctypes.c_int64),
+    ]
+
+
+class qvg_page_attention_params(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("n_q_heads", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("q_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int64),
+        ("total_q", ctypes.c_int64),
+        ("max_q", ctypes.c_int64),
+        ("max_kv", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("o_token_stride", ctypes.c_int64),
+        ("o_head_stride", ctypes.c_int64),
+    ]
+
+
 # Every symbol include/qvg.h declares, with its ctypes signature.
 SIGNATURES = {
     "qvg_quantize_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(qvg_quant_params)]),
@@ -135,6 +230,22 @@ SIGNATURES = {
                                      ctypes.POINTER(qvg_buffers), ctypes.POINTER(qvg_buffers),
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                      ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_rope": (ctypes.c_int, [ctypes.POINTER(qvg_rope_params), ctypes.POINTER(qvg_rotary),
+                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_page_write": (ctypes.c_int, [ctypes.POINTER(qvg_page_write_params), ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.POINTER(qvg_rotary), ctypes.POINTER(qvg_pages),
+                                      ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_page_read": (ctypes.c_int, [ctypes.POINTER(qvg_page_read_params),
+                                     ctypes.POINTER(qvg_pages), ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_page_attention_workspace_bytes": (ctypes.c_size_t,
+                                           [ctypes.POINTER(qvg_page_attention_params)]),
+    "qvg_page_attention": (ctypes.c_int, [ctypes.POINTER(qvg_page_attention_params),
+                                          ctypes.c_void_p, ctypes.POINTER(qvg_pages),
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
     "qvg_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "qvg_version": (ctypes.c_uint32, []),
 }
@@ -225,6 +336,37 @@ def qvg_attention(params: qvg_attention_params, Q: int, k_cache: qvg_buffers,
                   dev_status: int | None, stream: int | None) -> int:
     return int(load().qvg_attention(_ref(params), Q, _ref(k_cache), _ref(v_cache), O,
                                     workspace, workspace_bytes, dev_status, stream))
+
+
+def qvg_rope(params: qvg_rope_params, rotary: qvg_rotary, X: int, Y: int,
+             stream: int | None) -> int:
+    return int(load().qvg_rope(_ref(params), _ref(rotary), X, Y, stream))
+
+
+def qvg_page_write(params: qvg_page_write_params, K: int, V: int, slots: int,
+                   rotary: qvg_rotary | None, pages: qvg_pages, dev_status: int | None,
+                   stream: int | None) -> int:
+    return int(load().qvg_page_write(_ref(params), K, V, slots, _ref(rotary), _ref(pages),
+                                     dev_status, stream))
+
+
+def qvg_page_read(params: qvg_page_read_params, pages: qvg_pages, page_table: int,
+                  seq_lens: int, X: int, dev_status: int | None, stream: int | None) -> int:
+    return int(load().qvg_page_read(_ref(params), _ref(pages), page_table, seq_lens, X,
+                                    dev_status, stream))
+
+
+def qvg_page_attention_workspace_bytes(params: qvg_page_attention_params) -> int:
+    return int(load().qvg_page_attention_workspace_bytes(_ref(params)))
+
+
+def qvg_page_attention(params: qvg_page_attention_params, Q: int, pages: qvg_pages,
+                       page_table: int, seq_lens: int, cu_q: int | None, O: int,
+                       lse: int | None, workspace: int | None, workspace_bytes: int,
+                       dev_status: int | None, stream: int | None) -> int:
+    return int(load().qvg_page_attention(_ref(params), Q, _ref(pages), page_table, seq_lens,
+                                         cu_q, O, lse, workspace, workspace_bytes, dev_status,
+                                         stream))
 
 
 def qvg_status_string(code: int) -> str:
