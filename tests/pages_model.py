@@ -66,7 +66,9 @@ def attend(Q, K, V, scale, causal, window, u_p, out_dtype):
     A score is 128 exact products summed in fp32 (128 roundings or truncations of at most
     2^-23 of sum |q k|), times the scale in powers of two (3 roundings): its error e_j, plus
     2^-21 for the exponential, bounds the relative error of a weight.  Weights meet the values
-    rounded by u_p; sums over n keys add n 2^-23, a rescaling at most each 16 keys 2^-22.  The
+    rounded by u_p, or, where fp16 weights fall below its normal range, by half its smallest
+    step: 2^-25 of a weight of 1 (the largest weight is at least 1, and so is their sum) times a
+    value, and for 8-bit pages 2^-25 of the largest product of scale and code; sums over n keys add n 2^-23, a rescaling at most each 16 keys 2^-22.  The
     log-sum-exp inherits the mean e_j and 2^-21 of its own size."""
     nq, n = Q.shape[0], K.shape[0]
     pos = torch.arange(n - nq, n)[:, None]
@@ -91,6 +93,8 @@ def attend(Q, K, V, scale, causal, window, u_p, out_dtype):
     mean_e = (w * e).sum(-1, keepdim=True)
     sums = n * 2.0 ** -23 + (n / 16 + 8) * 2.0 ** -22
     bound = (w * (e + u_p + sums)) @ Vs.abs() + out.abs() * (mean_e + sums)
+    if u_p == HALF_EPS[torch.float16] and n:
+        bound = bound + n * 2.0 ** -25 * Vs.abs().amax()
     bound = bound * 1.01 + out.abs() * HALF_EPS[out_dtype] + TINY[out_dtype]
     lse_bound = mean_e[:, 0] + sums + 2.0 ** -21 * (lse.abs() + 1)
     return out, lse, bound, lse_bound

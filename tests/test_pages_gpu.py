@@ -271,7 +271,7 @@ def _cache(g, kv_lens, heads, fmt, page, hidden_values=None):
         x = torch.randn((pages, heads, page, 128), generator=g)
         if fmt in pm.TOP:
             codes, scale = pm.stored(x, fmt)
-            pools[name] = codes
+            pools[name] = torch.where(written[:, None, :, None], codes.view(torch.uint8), torch.tensor(0x7F, dtype=torch.uint8)).view(fmt)
             pools[name + "_scale"] = torch.where(written[:, None], scale, torch.tensor(math.nan))
         else:
             pools[name] = torch.where(written[:, None, :, None], x, torch.tensor(math.nan)).to(fmt)
@@ -291,7 +291,7 @@ def _check(Q, kv, table, kv_lens, q_lens, causal, window, scale=None, out=None, 
                                   status=status, **kw)
     torch.cuda.synchronize()
     assert int(status) == 0
-    u_p = pm.HALF_EPS[Q.dtype if kv.k.dtype not in pm.TOP else BF]
+    u_p = pm.HALF_EPS[Q.dtype if kv.k.dtype not in pm.TOP else HF]
     Qc = Q.double().cpu()
     for b, (nq, n) in enumerate(zip(q_lens, kv_lens)):
         if nq == 0:
@@ -381,6 +381,24 @@ def test_page_attention_strides_types_and_default_arguments():
     _check(Q, kv, table, kv_lens, q_lens, True, 0, scale=-0.3)
     one = torch.randn((40, 1, 128), generator=g).to(HF).cuda().expand(40, 4, 128)
     _check(one, kv, table, kv_lens, q_lens, True, 0)
+    _check(Q, kv, table, kv_lens, q_lens, True, 0, scale=0.0)
+
+
+@pytest.mark.parametrize("nq", [1, 60])
+def test_value_scales_of_many_sizes(nq):
+    # value scales from 2^-60 to 2^60, rising, falling and mixed along the keys, so that the
+    # reference they are held against has to move; the weights are large where scales are small
+    g = _gen(14)
+    n, page = 700, 16
+    for order in ("rising", "falling", "mixed"):
+        kv, table = _cache(g, [n], 1, E4, page)
+        e = torch.linspace(-60, 60, n) * (-1 if order == "falling" else 1)
+        if order == "mixed":
+            e = e[torch.randperm(n, generator=g)]
+        for j in range(n):
+            kv.v_scale[int(table[0, j // page]), 0, j % page] = 2.0 ** float(e[j])
+        Q = torch.randn((nq, 2, 128), generator=g).to(HF)
+        _check(Q, kv, table, [n], [nq], True, 0, out_dtype=F32)  # past fp16's largest number
 
 
 @pytest.mark.parametrize("fmt", [BF, I8])

@@ -58,7 +58,7 @@
 
 #include <algorithm>
 
-#include "internal.cuh"
+#include "tcgen.cuh"
 
 namespace qvg {
 
@@ -70,69 +70,10 @@ constexpr int kTileM = kAssignTileM;
 constexpr uint32_t kKBlockBytes = kTileM * 64 * 2;  // 16 KB: 64 fp16 channels of 128 rows
 constexpr int kABlocks = 2;                           // A blocks per tile (128 channels)
 constexpr uint32_t kAuxABytes = kTileM * 128;         // the constant tf32 block: 128 rows of 128 B
-constexpr uint32_t kSpinLimit = 1u << 22;
-// maximum of three fp32 values (one instruction on sm_100-class GPUs; NaN inputs are
-// ignored unless all three are NaN, as with fmaxf)
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 // coefficients of the bound (see the error bound above)
 constexpr float kDnRel = 0x1.03p0f;   // 1.01
 constexpr float kAccRel = 0x1p-15f;
 
-// Bounded wait on a phase.  Gives up when another role already gave up, or after
-// kSpinLimit tries or limit_ns of wall time, whichever comes first (then it raises the
-// abort flag itself).
-__device__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                          uint64_t limit_ns) {
-    if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (uint32_t n = 0; n < kSpinLimit; n++) {
-        if (mbar_try_suspend(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if ((n & 15u) == 15u && global_ns() - t0 > limit_ns) break;
-    }
-    *abort_flag = 1;
-    return false;
-}
-// Bounded wait used during teardown, which must not stop at the abort flag.
-__device__ void mbar_wait_final(uint32_t bar, uint32_t parity) {
-    for (uint32_t n = 0; n < kSpinLimit; n++) {
-        if (mbar_try(bar, parity)) return;
-        if (n >= 1024) __nanosleep(128);
-    }
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                            int c2, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 // The offset MMA: tf32 operands; accumulate = 0 overwrites the accumulator.
 __device__ __forceinline__ void tc_mma_tf32(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -142,54 +83,6 @@ __device__ __forceinline__ void tc_mma_tf32(uint32_t d, uint64_t a, uint64_t b, 
         "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// 32 consecutive fp32 columns of this thread's TMEM lane; the wait is in the same asm
-// statement, so no use of the values can be scheduled before the data has arrived.
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, float v[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int q = 0; q < 32; q++) v[q] = __uint_as_float(r[q]);
-}
-
-// 64 consecutive fp32 columns (two chunks) in one load.
-__device__ __forceinline__ void tc_ld64(uint32_t taddr, float v[64]) {
-    uint32_t r[64];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
-          "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
-          "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
-          "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
-          "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int q = 0; q < 64; q++) v[q] = __uint_as_float(r[q]);
 }
 
 // (tensor, tile within the tensor) of a flat tile index, advanced by a fixed step without a
@@ -239,17 +132,6 @@ __device__ __forceinline__ uint32_t chunk_cands(const float *v, float lim) {
         w = shift_in_sign(w, d.y);
     }
     return ~w;
-}
-
-// Shared-memory matrix descriptor: K-major operand, 128-byte swizzle, rows of 128 bytes,
-// 8-row groups 1024 bytes apart (the layout a TMA box of 128-byte rows writes with
-// CU_TENSOR_MAP_SWIZZLE_128B).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4)   // start address
-           | ((uint64_t)1 << 16)                 // leading-dimension offset (unused here)
-           | ((uint64_t)(1024 >> 4) << 32)       // stride between 8-row groups
-           | ((uint64_t)1 << 46)                 // descriptor version
-           | ((uint64_t)2 << 61);                // 128-byte swizzle
 }
 
 // Instruction descriptors: fp32 accumulator (bits 4-5 = 1), A and B formats at bits 7-9 and
@@ -642,25 +524,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // --------------------------------------------------------------------------------------
 // Host side
 // --------------------------------------------------------------------------------------
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
-    // Resolved once per process; the pointer never changes afterwards.
-    static EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiledFn>(ptr);
-    }();
-    return fn;
-}
 
 // barriers, TMEM slot, abort flag, and per epilogue group the column-half exchange (best
 // score and candidate words per row)

@@ -52,7 +52,7 @@ template <bool QB, int FMT>
 __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan p) {
     pdl_begin();
     constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
-    constexpr bool PVB = WIDE ? QB : true;      // type of the weights and values
+    constexpr bool PVB = WIDE && QB;            // type of the weights and values; 8-bit codes: fp16
     constexpr int ROWB = WIDE ? 2 * kD : kD;    // bytes of a cached row
     constexpr int NCH = ROWB / 64;              // 16-byte chunks of a row per lane
     __shared__ float s_o[kRowsWarps][kRowsM][kRowsPad];
@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
     }
 
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    int vexp = -100;  // exponent of the reference that the values' scales are taken against
 #pragma unroll
     for (int t = 0; t < 16; t++) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
@@ -180,6 +181,23 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
             }
         }
         load_k(next);  // the keys are consumed: the next tile's are on their way meanwhile
+        // 8-bit: the weights take in the values' scales relative to 2^vexp, an exponent that
+        // follows the largest scale seen; times 2^8 they fill fp16's range
+        float vmul = 0.f, vcorr = 1.f;
+        if constexpr (!WIDE) {
+            float big = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const int key = key0 + (k & 1) + (k >> 1) * 8;
+                if (key >= lo && key < hi) big = fmaxf(big, fabsf(vsc[k]));
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const int ve = max(vexp, min((int)(__float_as_uint(big) >> 23) - 127, 121));
+            vcorr = __uint_as_float((uint32_t)max(127 + vexp - ve, 0) << 23);
+            vmul = __uint_as_float((uint32_t)(127 + 8 - ve) << 23);
+            vexp = ve;
+        }
         float corr[2];
         uint32_t pa[4];
 #pragma unroll
@@ -197,12 +215,16 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
                 float w0 = fast_exp2(s[u][2 * x] - base), w1 = fast_exp2(s[u][2 * x + 1] - base);
                 sum += w0 + w1;
                 if constexpr (!WIDE) {  // a hidden key's scale may be NaN: its weight stays 0
-                    w0 = s[u][2 * x] == -INFINITY ? 0.f : w0 * vsc[2 * u];
-                    w1 = s[u][2 * x + 1] == -INFINITY ? 0.f : w1 * vsc[2 * u + 1];
+                    w0 = s[u][2 * x] == -INFINITY ? 0.f : w0 * (vsc[2 * u] * vmul);
+                    w1 = s[u][2 * x + 1] == -INFINITY ? 0.f : w1 * (vsc[2 * u + 1] * vmul);
                 }
                 pa[2 * u + x] = PVB ? pack_bf16(w0, w1) : pack_f16(w0, w1);
             }
             l[x] = l[x] * corr[x] + sum;
+        }
+        if constexpr (!WIDE) {
+            corr[0] *= vcorr;
+            corr[1] *= vcorr;
         }
         if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
@@ -213,16 +235,17 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
                 o[n][3] *= corr[1];
             }
         }
-        if constexpr (WIDE) {  // values that no row of the tile sees may hold anything
-            if (t * 16 < lo || t * 16 + 16 > hi) {
+        // values that no row of the tile sees may hold anything
+        if (t * 16 < lo || t * 16 + 16 > hi) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const int key = key0 + (k & 1) + (k >> 1) * 8;
-                    if (key < lo || key >= hi)
+            for (int k = 0; k < 4; k++) {
+                const int key = key0 + (k & 1) + (k >> 1) * 8;
+                if (key < lo || key >= hi)
 #pragma unroll
-                        for (int c = 0; c < NCH / 2; c++) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
-                }
+                    for (int c = 0; c < NCH / 2; c++) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
             }
+        }
+        if constexpr (WIDE) {
 #pragma unroll
             for (int c = 0; c < 2; c++)
 #pragma unroll
@@ -237,7 +260,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
             for (int w = 0; w < 4; w++) {
                 uint2 c[4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) c[k] = codes_to_bf16<FMT == PF_E4M3>(word_of(vr[k][0], w));
+                for (int k = 0; k < 4; k++) c[k] = codes_to_f16<FMT == PF_E4M3>(word_of(vr[k][0], w));
                 mma16816<PVB>(o[4 * w], pa, __byte_perm(c[0].x, c[1].x, 0x5410), __byte_perm(c[2].x, c[3].x, 0x5410));
                 mma16816<PVB>(o[4 * w + 1], pa, __byte_perm(c[0].x, c[1].x, 0x7632), __byte_perm(c[2].x, c[3].x, 0x7632));
                 mma16816<PVB>(o[4 * w + 2], pa, __byte_perm(c[0].y, c[1].y, 0x5410), __byte_perm(c[2].y, c[3].y, 0x5410));
@@ -250,6 +273,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
     if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
 
     // join the warps
+    const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp - 8) << 23);
 #pragma unroll
     for (int x = 0; x < 2; x++) {
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -264,7 +288,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
             for (int e = 0; e < 2; e++) {
                 const int col = 2 * q + e;
                 const int ch = WIDE ? (n >> 3) * 64 + col * 8 + (n & 7) : col * 16 + n;
-                s_o[warp][g + 8 * x][ch] = o[n][2 * x + e];
+                s_o[warp][g + 8 * x][ch] = o[n][2 * x + e] * unit;
             }
     }
     __syncthreads();
@@ -387,13 +411,30 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
     if (p.lse && lane == 0) p.lse[token * p.HQ + hq] = row_lse(mx, l);
 }
 
-// Splits: enough CTAs to give every SM three of them (what their registers allow) about once,
-// while each warp keeps at least four tiles.
+// Splits of the keys.  Few rows: enough CTAs to give every SM three of them (what their
+// registers allow) about once, while each warp keeps at least four tiles.  Many rows: CTAs run
+// one an SM, so the time is about the number of rounds times the tiles of one CTA; the split
+// that makes it least is taken, counting a tile's worth of work for starting a CTA and the
+// traffic of the partial results (two tiles for a pair of row tiles).
 int page_attention_splits(const PAttnPlan &p) {
-    const int64_t tiles = (p.max_q * p.G + kRowsM - 1) / kRowsM * p.H * p.B;
-    const int64_t want = (152 * 3 + tiles - 1) / tiles;
-    const int64_t most = (p.max_kv + 16 * kRowsWarps * 4 - 1) / (16 * kRowsWarps * 4);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 256}));
+    const int64_t rows = p.max_q * p.G, cells = (int64_t)p.H * p.B;
+    if (rows <= kRowsMost) {
+        const int64_t want = (152 * 3 + cells - 1) / cells;
+        const int64_t most = (p.max_kv + 16 * kRowsWarps * 4 - 1) / (16 * kRowsWarps * 4);
+        return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 256}));
+    }
+    const int64_t pairs = (rows + 255) / 256 * cells, tiles = (p.max_kv + 127) / 128;
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= 64 && s <= std::max<int64_t>(1, tiles / 4); s++) {
+        const double rounds = (double)((pairs * s + 151) / 152);
+        const double t = rounds * ((double)((tiles + s - 1) / s) + 2.0) + (s > 1 ? 2.0 * s * pairs / 152 + 4.0 : 0.0);
+        if (t < least * 0.97) {
+            least = t;
+            best = s;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st) {
@@ -409,12 +450,14 @@ cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st) {
         e = p.fmt == PF_E4M3   ? go(k_page_attn_rows<false, PF_E4M3>)
             : p.fmt == PF_INT8 ? go(k_page_attn_rows<false, PF_INT8>)
                                : go(k_page_attn_rows<false, PF_F16>);
-    if (e != cudaSuccess || p.S == 1) return e;
-    return launch_kernel(k_page_combine, dim3((unsigned)((p.total_q * p.HQ + 7) / 8)), dim3(256), 0, st, p);
+    return e;
 }
 
 cudaError_t launch_page_attention(const PAttnPlan &p, cudaStream_t st) {
-    return launch_page_attention_rows(p, st);
+    const cudaError_t e =
+        p.max_q * p.G <= kRowsMost ? launch_page_attention_rows(p, st) : launch_page_attention_tc(p, st);
+    if (e != cudaSuccess || p.S == 1) return e;
+    return launch_kernel(k_page_combine, dim3((unsigned)((p.total_q * p.HQ + 7) / 8)), dim3(256), 0, st, p);
 }
 
 }  // namespace qvg

@@ -1,0 +1,627 @@
+// Attention of many query rows over paged keys and values, on the tensor cores (tcgen05 + TMEM
+// + TMA).
+//   O = softmax(scale Q K^T, over the visible keys) V
+//
+// Bound by the tensor cores: 4 * 128 operations per visible (query row, key) pair.  A CTA takes
+// two tiles of 128 rows (query tokens x grouped query heads of one key/value head) and walks
+// the keys in tiles of 128; both row tiles use every key tile that is loaded.  One pass, with a
+// running maximum and weight sum per row:
+//   * warp 9 loads: a tile's pages by TMA into a ring of 32 KB slots (K and V alternate), in the
+//     128-byte swizzled layout that serves K as a K-major operand and V as an MN-major one;
+//   * warp 8, one thread: S_t = Q_t K^T into TMEM, then O_t += P_t V with P_t read from TMEM;
+//   * warps 0-3 and 4-7: the softmax of row tile 0 and 1, a row a thread: its 128 scores from
+//     TMEM, their maximum, powers of two against it, the weights in 16 bits back into TMEM over
+//     the scores.  While one tile's softmax runs, the tensor cores work on the other's.
+// The running maximum is raised only when a row's scores pass it by more than 2^8: the weights
+// stay below 2^8 and O_t in TMEM is rescaled (by the softmax warps themselves) a few times in
+// all instead of once a tile; the result is the same, since numerator and weight sum share the
+// base.
+// TMEM: S/P of the two row tiles (128 columns each; the weights of a tile take the first 64 of
+// its scores' columns), then O of the two (128 each): all 512 columns, one CTA an SM.
+//
+// 8-bit pages: four more warps widen the codes (exactly) to 16 bits into the ring, from raw
+// tiles that TMA brings.  The keys' scales multiply the scores, the values' the weights, which
+// are held in fp16 against a running reference 2^e near the largest scale: rounding them costs
+// 2^-11, as the values' own codes are exact.
+//
+// Masks: a tile that some row does not see whole is compared key by key; a weight that is
+// hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
+// product runs over the 16-key steps in sight, and the rest of the outer steps is zeroed.
+#include "page_attn.cuh"
+#include "tcgen.cuh"
+
+namespace qvg {
+
+namespace {
+constexpr int kTcM = 128;                  // rows of a row tile
+constexpr int kTcN = 128;                  // keys of a key tile
+constexpr uint32_t kHalf = kTcM * 128;     // 64 channels of 128 rows: 16 KB
+constexpr uint32_t kSlot = 2 * kHalf;      // a whole 16-bit tile: 32 KB
+constexpr uint32_t kRaw = kTcN * kD;       // a tile of 8-bit codes: 16 KB
+constexpr uint64_t kPageWaitNs = 2000000000ull;  // a wait in the pipeline gives up after this
+constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
+
+template <int FMT>
+struct TcShape {
+    static constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
+    static constexpr int SLOTS = WIDE ? 5 : 3;     // ring of 16-bit tiles
+    static constexpr int RAWS = 3;                 // ring of raw 8-bit tiles
+    static constexpr int THREADS = WIDE ? 384 : 512;
+    static constexpr uint32_t SMEM_TILES = 2 * kSlot + SLOTS * kSlot + (WIDE ? 0 : RAWS * kRaw);
+};
+
+// Everything the roles share besides the tiles (the 16-bit formats have no scales).
+template <int FMT>
+struct TcShared {
+    uint64_t full[5], empty[5];         // ring of 16-bit tiles
+    uint64_t raw_full[3], raw_empty[3];
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t sc_full[2], sc_empty[2];   // scales of a key tile
+    uint64_t edge, fin;
+    uint32_t tmem;
+    int abort;
+    int vexp[2];                        // exponent of the values' reference scale, per tile parity
+    float wmax[4];
+    __align__(16) float ks[2][TcShape<FMT>::WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
+    __align__(16) float vs[2][TcShape<FMT>::WIDE ? 4 : kTcN];  // values' scales over the reference
+};
+
+template <int FMT>
+constexpr size_t tc_smem() {
+    constexpr size_t bytes = 1024 + TcShape<FMT>::SMEM_TILES + sizeof(TcShared<FMT>);
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+    return bytes;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+// 32 consecutive columns of this thread's TMEM lane written.
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t r[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of an MN-major operand (values: 64 channels of a key are one 128-byte row) in the
+// 128-byte swizzled layout: 64-channel blocks kHalf apart, groups of 8 keys 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kHalf >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// fp32 accumulator, A and B bf16 or fp16, M = N = 128; B MN-major for the value product.
+__device__ __forceinline__ uint32_t attn_idesc(bool bf16, bool b_mn) {
+    const uint32_t f = bf16 ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(kTcN >> 3) << 17) |
+           ((uint32_t)(kTcM >> 4) << 24);
+}
+// Whether all 128 threads of named barrier 1 say so; every one of them gets the same answer.
+__device__ __forceinline__ bool all_of_128(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0u;
+}
+template <int REGS>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+}  // namespace
+
+// grid (pairs of row tiles x splits, key/value heads, sequences)
+template <bool QB, int FMT>
+__global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
+    k_page_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const __grid_constant__ PAttnPlan p, int pairs) {
+    pdl_begin();
+    using T = TcShape<FMT>;
+    constexpr bool WIDE = T::WIDE;
+    constexpr bool PVB = WIDE && QB;  // type of weights and values; 8-bit codes: fp16
+    constexpr int SLOTS = T::SLOTS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char *sQ = sm, *sKV = sm + 2 * kSlot, *sRaw = sKV + SLOTS * kSlot;
+    TcShared<FMT> &sh = *reinterpret_cast<TcShared<FMT> *>(sm + T::SMEM_TILES);
+    volatile int *abort_flag = &sh.abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // longest first: under a causal mask the last rows see the most
+    const int pair = pairs - 1 - (int)blockIdx.x / p.S, split = (int)blockIdx.x % p.S;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const SeqInfo sq = seq_info(p, b, threadIdx.x == 0 && blockIdx.x == 0 && h == 0);
+    const int rows = sq.qn * p.G, r0 = pair * 2 * kTcM;
+    if (r0 >= rows) return;
+    const int nt = rows - r0 > kTcM ? 2 : 1;  // row tiles in use
+    const int lo = seen_lo(p, sq, r0 / p.G), hi = seen_hi(p, sq, (min(rows, r0 + 2 * kTcM) - 1) / p.G);
+    int n = 0, j0 = 0;  // this split's key tiles
+    if (lo < hi) {
+        const int t_lo = lo / kTcN, all = (hi + kTcN - 1) / kTcN - t_lo, per = (all + p.S - 1) / p.S;
+        j0 = t_lo + split * per;
+        n = max(0, min(per, all - split * per));
+    }
+
+    // Q: both row tiles, swizzled; rows past the end are zeros.  The sign of a negative scale
+    // goes into Q, so that the maximum of the scores is the maximum of what is exponentiated.
+    {
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        for (int x = threadIdx.x; x < 2 * kTcM * 16; x += T::THREADS) {
+            const int row = x >> 4, c = x & 15, r = r0 + row, i = r / p.G;
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+                w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
+                                                          (int64_t)(h * p.G + r - i * p.G) * p.qh) + c);
+                w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+            }
+            const uint32_t at = (row >> 7) * kSlot + (c >> 3) * kHalf + (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4 *>(sQ + at) = w;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SLOTS; s++) {
+            mbar_init(smem_u32(&sh.full[s]), WIDE ? 1 : 4);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        for (int s = 0; s < T::RAWS; s++) {
+            mbar_init(smem_u32(&sh.raw_full[s]), 1);
+            mbar_init(smem_u32(&sh.raw_empty[s]), 4);
+        }
+        for (int t = 0; t < 2; t++) {
+            mbar_init(smem_u32(&sh.s_full[t]), 1);
+            mbar_init(smem_u32(&sh.p_full[t]), 4);
+            mbar_init(smem_u32(&sh.o_done[t]), 1);
+            mbar_init(smem_u32(&sh.sc_full[t]), 4);
+            mbar_init(smem_u32(&sh.sc_empty[t]), 4 * nt);
+        }
+        mbar_init(smem_u32(&sh.edge), 1);
+        mbar_init(smem_u32(&sh.fin), 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    auto wait = [&](uint64_t &bar, uint32_t parity) {
+        return mbar_wait(smem_u32(&bar), parity & 1u, abort_flag, kPageWaitNs);
+    };
+
+    if (warp >= 8) {
+        if constexpr (!WIDE) {
+            if (warp < 12) regs_dec<56>(); else regs_dec<88>();
+        }
+        if (warp == 8) {
+            // ---------------------------------------------------------------- MMA issuer
+            if (lane == 0 && n > 0) {
+                const uint32_t id_qk = attn_idesc(QB, false), id_pv = attn_idesc(PVB, true);
+                const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
+                auto scores = [&](int t, int slot) {
+                    const uint64_t a = sw128_desc(q_addr + t * kSlot), k = sw128_desc(kv_addr + slot * kSlot);
+#pragma unroll
+                    for (int kk = 0; kk < 8; kk++) {
+                        const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        tc_mma(tmem + t * 128, a + off, k + off, id_qk, kk > 0);
+                    }
+                    tc_commit(smem_u32(&sh.s_full[t]));
+                };
+                bool ok = wait(sh.full[0], 0);
+                if (ok) {
+                    tc_fence_after();
+                    for (int t = 0; t < nt; t++) scores(t, 0);
+                    tc_commit(smem_u32(&sh.empty[0]));
+                }
+                int first = 1;  // the first product overwrites O
+                for (int j = 0; ok && j < n; j++) {
+                    const uint32_t iv = 2 * j + 1, ik = iv + 1;  // ring items: V of this tile, K of the next
+                    const int sv = iv % SLOTS, sk = ik % SLOTS;
+                    // the 16-key steps of the tile that some row sees
+                    const int k0 = (j0 + j) * kTcN;
+                    const int st0 = max(lo - k0, 0) >> 4, st1 = (min(hi - k0, kTcN) + 15) >> 4;
+                    for (int t = 0; ok && t < nt; t++) {
+                        ok = wait(sh.p_full[t], j) && (t > 0 || wait(sh.full[sv], iv / SLOTS));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t v = sw128_mn_desc(kv_addr + sv * kSlot);
+                        for (int s = st0; s < st1; s++)
+                            tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, v + ((s * 2048) >> 4), id_pv,
+                                      !(first && s == st0));
+                        tc_commit(smem_u32(&sh.o_done[t]));
+                        if (t == nt - 1) {
+                            tc_commit(smem_u32(&sh.empty[sv]));
+                            first = 0;
+                        }
+                        if (j + 1 < n) {
+                            ok = t > 0 || wait(sh.full[sk], ik / SLOTS);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(t, sk);
+                            if (t == nt - 1) tc_commit(smem_u32(&sh.empty[sk]));
+                        }
+                    }
+                }
+                // every MMA issued so far completes before TMEM is released
+                tc_commit(smem_u32(&sh.fin));
+                mbar_wait_final(smem_u32(&sh.fin), 0);
+            }
+        } else if (warp == 9) {
+            // ---------------------------------------------------------------- TMA loads
+            const int shift = 31 - __clz(p.page), per_tile = kTcN >> shift;
+            bool bad = false, ok = true;
+            uint32_t edges = 0, issued = 0;
+            constexpr int RING = WIDE ? SLOTS : T::RAWS;
+            for (uint32_t it = 0; ok && it < 2u * n; it++) {
+                const int k0 = (j0 + (int)(it >> 1)) * kTcN, slot = it % RING;
+                const bool value = it & 1;
+                uint64_t &full = WIDE ? sh.full[slot] : sh.raw_full[slot];
+                ok = wait(WIDE ? sh.empty[slot] : sh.raw_empty[slot], it / RING + 1);
+                if (!ok) break;
+                // the pages of this tile that hold a key some row sees, a lane each
+                const int token = k0 + (lane << shift);
+                const bool mine = lane < per_tile && token < hi && token + p.page > lo;
+                const uint32_t pages = __popc(__ballot_sync(0xffffffffu, mine));
+                const int64_t row = mine ? (page_of(p, b, token, shift, bad) * p.H + h) << shift : 0;
+                // a value tile at the edge of what is seen, whose outer rows must be zeroed
+                const bool edge = WIDE && value && (((lo - k0) & 15 && lo > k0) || ((hi - k0) & 15 && hi < k0 + kTcN));
+                const uint32_t bar = smem_u32(edge ? &sh.edge : &full);
+                if (lane == 0) mbar_expect_tx(bar, (pages << shift) * (WIDE ? 2u * kD : (uint32_t)kD));
+                __syncwarp();
+                if (mine) {
+                    const CUtensorMap *map = value ? &tmV : &tmK;
+                    if constexpr (WIDE) {
+                        const uint32_t dst = smem_u32(sKV) + slot * kSlot + ((uint32_t)lane << shift) * 128;
+                        tma_load_2d(dst, map, 0, (int)row, bar);
+                        tma_load_2d(dst + kHalf, map, 64, (int)row, bar);
+                    } else {
+                        tma_load_2d(smem_u32(sRaw) + slot * kRaw + ((uint32_t)lane << shift) * kD, map, 0, (int)row, bar);
+                    }
+                }
+                issued = it + 1;
+                if (edge) {
+                    // rows of the outer 16-key steps that no row of the CTA sees: zeros
+                    mbar_wait_final(bar, edges++ & 1u);
+                    const int v0 = max(lo - k0, 0), v1 = min(hi - k0, kTcN);
+                    for (int x = lane; x < 2 * 16 * 16; x += 32) {
+                        const int side = x >> 8, r = side ? (v1 & ~15) + ((x >> 4) & 15) : (v0 & ~15) + ((x >> 4) & 15);
+                        const int c = x & 15;
+                        if (side ? (r >= v1 && (v1 & 15)) : r < v0)
+                            *reinterpret_cast<uint4 *>(sKV + slot * kSlot + (c >> 3) * kHalf + r * 128 + (c & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&full));
+                }
+            }
+            if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
+            // every copy this CTA started lands before the CTA ends (edge tiles were waited for;
+            // their slots' phases were completed by hand)
+            const uint32_t from = issued > (uint32_t)RING ? issued - RING : 0u;
+            for (uint32_t it = from; it < issued; it++)
+                mbar_wait_final(smem_u32(WIDE ? &sh.full[it % RING] : &sh.raw_full[it % RING]), (it / RING) & 1u);
+        } else if (!WIDE && warp >= 12) {
+            // ---------------------------------------------------------------- 8-bit codes widened
+            const int shift = 31 - __clz(p.page), x = threadIdx.x - 384;
+            const float mult = fabsf(p.scale_log2);
+            int e = -126;
+            bool ok = true, bad = false;  // a wait that gave up: the four warps leave together
+            for (uint32_t it = 0; it < 2u * n; it++) {
+                const int j = it >> 1, k0 = (j0 + j) * kTcN, slot = it % SLOTS, raw = it % T::RAWS;
+                const bool value = it & 1;
+                if (!value) {
+                    // scales of the tile's keys, one a thread; outside what is seen they are 0
+                    const int key = k0 + x, buf = j & 1;
+                    float ks = 0.f, vs = 0.f;
+                    if (key >= lo && key < hi) {
+                        const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
+                        ks = __ldg(p.ks + row);
+                        vs = __ldg(p.vs + row);
+                    }
+                    float m = fabsf(vs);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    ok = ok && wait(sh.sc_empty[buf], (j >> 1) + 1);
+                    if (lane == 0) sh.wmax[warp - 12] = m;
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    m = fmaxf(fmaxf(sh.wmax[0], sh.wmax[1]), fmaxf(sh.wmax[2], sh.wmax[3]));
+                    ok = all_of_128(ok);
+                    if (!ok) break;
+                    // the reference moves only when a scale passes it by 2^3: the weights stay
+                    // below 2^8 (kLazy) * 2^3 * 2^4 < fp16's largest
+                    const int ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
+                    if (j == 0 || ee > e + 2) e = ee;
+                    sh.ks[buf][x] = ks * mult;
+                    sh.vs[buf][x] = vs * __uint_as_float((uint32_t)(127 + 4 - e) << 23);
+                    if (x == 0) sh.vexp[buf] = e;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
+                }
+                ok = ok && wait(sh.raw_full[raw], it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    ok = false;
+                    continue;
+                }
+                const unsigned char *src = sRaw + raw * kRaw;
+                unsigned char *dst = sKV + slot * kSlot;
+#pragma unroll 4
+                for (int u = 0; u < 8; u++) {
+                    const int chunk = u * 128 + x, r = chunk >> 3, c = chunk & 7;  // 16 codes
+                    const int key = k0 + r;
+                    uint4 w = *reinterpret_cast<const uint4 *>(src + r * kD + c * 16);
+                    if (key < lo || key >= hi) w = make_uint4(0u, 0u, 0u, 0u);
+                    uint2 y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const uint32_t code = k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w;
+                        y[k] = QB && !value ? codes_to_bf16<FMT == PF_E4M3>(code) : codes_to_f16<FMT == PF_E4M3>(code);
+                    }
+                    // chunks 2c, 2c + 1 of the row's 16; the two halves of a row start with
+                    // different ones, so that eight lanes' stores meet every bank once
+                    unsigned char *half = dst + (c >> 2) * kHalf + r * 128;
+                    const int c0 = 2 * (c & 3), sw = r & 7, swap = c >> 2;
+                    const uint4 a0 = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y), a1 = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
+                    *reinterpret_cast<uint4 *>(half + (((c0 + swap) ^ sw) << 4)) = swap ? a1 : a0;
+                    *reinterpret_cast<uint4 *>(half + (((c0 + 1 - swap) ^ sw) << 4)) = swap ? a0 : a1;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.full[slot]));
+                    mbar_arrive(smem_u32(&sh.raw_empty[raw]));
+                }
+            }
+            if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
+        }
+    } else {
+        // -------------------------------------------------------------------- softmax
+        if constexpr (!WIDE) regs_inc<184>();
+        const int t = warp >> 2, row = (warp & 3) * 32 + lane, r = r0 + t * kTcM + row;
+        if (t < nt) {
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
+            const int i = min(r, rows - 1) / p.G, hq = h * p.G + min(r, rows - 1) - i * p.G;
+            const int r_lo = seen_lo(p, sq, i), r_hi = seen_hi(p, sq, i);
+            const float mult = fabsf(p.scale_log2);
+            float m = -INFINITY, l = 0.f;
+            int e = 0;
+            bool ok = true;
+            for (int j = 0; j < n; j++) {
+                const int k0 = (j0 + j) * kTcN, buf = j & 1;
+                ok = wait(sh.s_full[t], j) && (WIDE || wait(sh.sc_full[buf], j >> 1));
+                if (__any_sync(0xffffffffu, !ok)) break;
+                tc_fence_after();
+                float s[128];
+                tc_ld64(s_at, s);
+                tc_ld64(s_at + 64, s + 64);
+                if constexpr (!WIDE) {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][c]);
+                        s[c] *= f.x; s[c + 1] *= f.y; s[c + 2] *= f.z; s[c + 3] *= f.w;
+                    }
+                }
+                const bool masked = __any_sync(0xffffffffu, k0 < r_lo || k0 + kTcN > r_hi);
+                if (masked) {
+                    const int a = r_lo - k0, z = r_hi - k0;
+#pragma unroll
+                    for (int c = 0; c < 128; c++) s[c] = c >= a && c < z ? s[c] : -INFINITY;
+                }
+                float mx = fmax3(s[0], s[1], s[2]), my = fmax3(s[3], s[4], s[5]);
+#pragma unroll
+                for (int c = 6; c < 126; c += 4) {
+                    mx = fmax3(mx, s[c], s[c + 1]);
+                    my = fmax3(my, s[c + 2], s[c + 3]);
+                }
+                mx = fmax3(fmaxf(mx, my), s[126], s[127]);
+                if constexpr (WIDE) mx *= mult;
+                bool raise = mx > m + kLazy, move = false;  // -inf + 8: any score raises it
+                int e_new = e;
+                if constexpr (!WIDE) {
+                    e_new = sh.vexp[buf];
+                    move = j > 0 && e_new != e;
+                }
+                if (j == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, raise || move)) {
+                    const float m_new = raise ? mx : m;
+                    float f = fast_exp2(m - exp_base(m_new));
+                    if (!raise) f = 1.f;
+                    l *= f;
+                    m = m_new;
+                    if constexpr (!WIDE) f = ldexpf(f, e - e_new);
+                    ok = wait(sh.o_done[t], j - 1);
+                    if (__any_sync(0xffffffffu, !ok)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) {
+                        float o[32];
+                        tc_ld32(o_at + c, o);
+                        uint32_t w[32];
+#pragma unroll
+                        for (int k = 0; k < 32; k++) w[k] = __float_as_uint(o[k] * f);
+                        tc_st32(o_at + c, w);
+                    }
+                    tc_wait_st();
+                }
+                e = e_new;
+                const float base = exp_base(m);
+                const float2 nb = make_float2(-base, -base), sc2 = make_float2(mult, mult);
+                float2 la = make_float2(0.f, 0.f), lb = la;
+#pragma unroll
+                for (int hc = 0; hc < 128; hc += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        float2 x = make_float2(s[hc + c], s[hc + c + 1]);
+                        x = WIDE ? __ffma2_rn(x, sc2, nb) : __fadd2_rn(x, nb);
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                        if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
+                        if constexpr (!WIDE) {
+                            const float2 f = *reinterpret_cast<const float2 *>(&sh.vs[buf][hc + c]);
+                            const float2 y = make_float2(x.x * f.x, x.y * f.y);
+                            // a hidden key's scale may be NaN: its weight stays 0
+                            x.x = masked && s[hc + c] == -INFINITY ? 0.f : y.x;
+                            x.y = masked && s[hc + c + 1] == -INFINITY ? 0.f : y.y;
+                        }
+                        w[c >> 1] = PVB ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
+                    }
+                    tc_st32(s_at + (hc >> 1), w);
+                }
+                const float2 ls = __fadd2_rn(la, lb);
+                l += ls.x + ls.y;
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.p_full[t]));
+                    if constexpr (!WIDE) mbar_arrive(smem_u32(&sh.sc_empty[buf]));
+                }
+            }
+            if (n > 0) ok = ok && wait(sh.o_done[t], n - 1);
+            ok = !__any_sync(0xffffffffu, !ok);
+            tc_fence_after();
+            if (ok) {
+                const bool live = r < rows, whole = p.S == 1;
+                float inv = 1.f;
+                if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+                if constexpr (!WIDE) inv = ldexpf(inv, e - 4);
+                const int64_t tok = sq.q0 + i;
+                const int64_t part = ((int64_t)split * p.total_q + tok) * p.HQ + hq;
+                const int64_t out = tok * p.ot + hq * p.oh;
+                bool odd = false;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    float o[32];
+                    __syncwarp();
+                    if (n > 0) {
+                        tc_ld32(o_at + c, o);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k++) o[k] = 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; k++) {
+                        o[k] *= inv;
+                        odd |= !is_finite(o[k]);
+                    }
+                    if (live) {
+                        if (!whole) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) store4<DT_F32>(p.part, part * kD + c + k, o + k);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) store_out4(p, out + c + k, o + k);
+                        }
+                    }
+                }
+                if (!whole) {
+                    if (live) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, l);
+                } else {
+                    if (live && p.lse) p.lse[tok * p.HQ + hq] = row_lse(m, l);
+                    if (redo_possible(p)) {
+                        uint32_t todo = __ballot_sync(0xffffffffu, odd && live);
+                        while (todo) {
+                            const int src = __ffs(todo) - 1;
+                            todo &= todo - 1;
+                            const int ri = __shfl_sync(0xffffffffu, i, src), rh = __shfl_sync(0xffffffffu, hq, src);
+                            float ro[4], rm, rl;
+                            redo_row(p, b, ri, rh, ro, rm, rl);
+                            const float f = rl == 0.f ? 0.f : __fdiv_rn(1.f, rl);
+#pragma unroll
+                            for (int c = 0; c < 4; c++) ro[c] *= f;
+                            store_out4(p, (sq.q0 + ri) * p.ot + rh * p.oh + 4 * lane, ro);
+                            if (p.lse && lane == 0) p.lse[(sq.q0 + ri) * p.HQ + rh] = row_lse(rm, rl);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) or_status(p.status, QVG_DEV_TIMEOUT);
+    if (warp == 8) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+namespace {
+template <bool QB, int FMT>
+cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
+    using T = TcShape<FMT>;
+    constexpr size_t smem = tc_smem<FMT>();
+    const auto kernel = k_page_attn_tc<QB, FMT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int pairs = (int)((p.max_q * p.G + 2 * kTcM - 1) / (2 * kTcM));
+    return launch_kernel(kernel, dim3((unsigned)(pairs * p.S), p.H, p.B), dim3(T::THREADS), smem, st, mk, mv, p, pairs);
+}
+}  // namespace
+
+cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
+    // the pool as rows of 128 channels; a box is a page's rows (of 64 channels in 16 bits)
+    const CUtensorMapDataType dt = !wide              ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : p.fmt == PF_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)(p.n_pages * p.H * p.page)};
+    const cuuint64_t strides[1] = {(cuuint64_t)(wide ? 2 * kD : kD)};
+    const cuuint32_t box[2] = {wide ? 64u : (cuuint32_t)kD, (cuuint32_t)p.page}, estr[2] = {1, 1};
+    CUtensorMap maps[2];
+    const void *pools[2] = {p.k, p.v};
+    for (int x = 0; x < 2; x++)
+        if (enc(&maps[x], dt, 2, const_cast<void *>(pools[x]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    if (p.q_dtype == DT_BF16)
+        return p.fmt == PF_E4M3   ? launch_tc<true, PF_E4M3>(p, maps[0], maps[1], st)
+               : p.fmt == PF_INT8 ? launch_tc<true, PF_INT8>(p, maps[0], maps[1], st)
+                                  : launch_tc<true, PF_BF16>(p, maps[0], maps[1], st);
+    return p.fmt == PF_E4M3   ? launch_tc<false, PF_E4M3>(p, maps[0], maps[1], st)
+           : p.fmt == PF_INT8 ? launch_tc<false, PF_INT8>(p, maps[0], maps[1], st)
+                              : launch_tc<false, PF_F16>(p, maps[0], maps[1], st);
+}
+
+}  // namespace qvg

@@ -79,7 +79,7 @@ __device__ __forceinline__ bool redo_possible(const PAttnPlan &p) {
     return (p.causal || p.window > 0) && (p.fmt == PF_F16 || p.fmt == PF_BF16);
 }
 // Row (query i of sequence b, query head hq): lane l gets channels 4l .. 4l+3, unnormalised.
-__device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, int hq, float o[4], float &m,
+static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, int hq, float o[4], float &m,
                                       float &l) {
     const int lane = threadIdx.x & 31;
     const SeqInfo s = seq_info(p, b, false);
@@ -134,6 +134,10 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? -INFINITY : l);  // NaN stays NaN
 }
 
+// Up to this many query rows (tokens x grouped heads) a sequence, attention is bound by reading
+// the cache and runs on warp-level instructions; above, on the tensor cores.
+constexpr int kRowsMost = 16;
 cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st);
+cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st);
 
 }  // namespace qvg
