@@ -89,8 +89,10 @@ def new_workspace(H: int, N: int, C: int, T: int, device="cuda") -> torch.Tensor
 
 
 def _stream_handle(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle of the current stream, without the Stream object around it
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def quantize(X: torch.Tensor, C: int, T: int, bits: int, group: int, iters: int, seed: int = 0,
@@ -238,15 +240,19 @@ def _need(ok, what):
 
 
 def _rows(x: torch.Tensor, what: str):
-    """x as rows [tokens][heads][128] of contiguous channels."""
-    _need(x.is_cuda and x.dim() == 3 and x.shape[2] == D and (x.stride(2) == 1 or x.numel() == 0),
-          "%s must be a CUDA tensor [tokens][heads][128] with contiguous channels" % what)
-    _need(x.dtype in _DT, "%s must be fp16, bf16 or fp32" % what)
+    """(tokens, heads, token stride, head stride) of rows [tokens][heads][128] of contiguous
+    channels; a stride is 0 where there is one row only, whose stride says nothing."""
+    shape, stride = x.shape, x.stride()
+    if not (x.is_cuda and len(shape) == 3 and shape[2] == D and stride[2] == 1 and x.dtype in _DT):
+        _need(x.is_cuda and len(shape) == 3 and shape[2] == D and (stride[2] == 1 or x.numel() == 0),
+              "%s must be a CUDA tensor [tokens][heads][128] with contiguous channels" % what)
+        _need(x.dtype in _DT, "%s must be fp16, bf16 or fp32" % what)
+    return (shape[0], shape[1], stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
 
 
 def _index(x: torch.Tensor, dtype, shape, what: str):
-    _need(x.is_cuda and x.dtype == dtype and tuple(x.shape) == tuple(shape) and x.is_contiguous(),
-          "%s must be a contiguous CUDA tensor %s of %s" % (what, list(shape), dtype))
+    if not (x.dtype == dtype and x.shape == shape and x.is_cuda and x.is_contiguous()):
+        raise ValueError("%s must be a contiguous CUDA tensor %s of %s" % (what, list(shape), dtype))
 
 
 def _empty(shape, dtype, device, stream):
@@ -261,12 +267,7 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _row_strides(x: torch.Tensor):
-    """Token and head stride; 0 where there is one row only, whose stride says nothing."""
-    return (x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
-
-
-@dataclass
+@dataclass(frozen=True)
 class RopeTable:
     """Frequencies and layout of a rotary position code (see qvg_rotary)."""
     freqs: torch.Tensor       # int64 [rot_dim / 2]: turns per position as 64-bit fractions
@@ -276,21 +277,27 @@ class RopeTable:
     mscale: float = 1.0
 
     def __post_init__(self):
-        self.sections = tuple(int(s) for s in self.sections)
-        _need(1 <= len(self.sections) <= 4 and sum(self.sections) == self.rot_dim // 2,
+        sections = tuple(int(s) for s in self.sections)
+        object.__setattr__(self, "sections", sections)
+        _need(1 <= len(sections) <= 4 and sum(sections) == self.rot_dim // 2,
               "1 to 4 sections must add up to rot_dim / 2 pairs")
         _index(self.freqs, torch.int64, (self.rot_dim // 2,), "freqs")
+        axes = len(sections)
+        object.__setattr__(self, "_fixed", _c.qvg_rotary(
+            self.rot_dim, int(self.interleaved), axes, (*sections, *(0,) * (4 - axes)),
+            self.mscale, 0, None, self.freqs.data_ptr()))
 
     def rotary(self, positions: torch.Tensor, n: int) -> _c.qvg_rotary:
-        axes = len(self.sections)
-        if positions.dim() == 1:
-            positions = positions.view(1, -1)
-        _need(positions.is_cuda and positions.dtype == torch.int64 and positions.shape == (axes, n)
-              and (n <= 1 or positions.stride(1) == 1) and (axes == 1 or positions.stride(0) >= n),
-              "positions must be int64 [%d][%d] on the GPU, each axis contiguous" % (axes, n))
-        return _c.qvg_rotary(self.rot_dim, int(self.interleaved), axes,
-                             (*self.sections, *(0,) * (4 - axes)), self.mscale,
-                             positions.stride(0), positions.data_ptr(), self.freqs.data_ptr())
+        axes, shape, stride = len(self.sections), positions.shape, positions.stride()
+        if len(shape) == 1:
+            shape, stride = (1, shape[0]), (n, stride[0])
+        if not (positions.is_cuda and positions.dtype == torch.int64 and shape == (axes, n)
+                and (n <= 1 or stride[1] == 1) and (axes == 1 or stride[0] >= n)):
+            raise ValueError("positions must be int64 [%d][%d] on the GPU, each axis contiguous" % (axes, n))
+        r = _c.qvg_rotary.from_buffer_copy(self._fixed)
+        r.pos_stride = stride[0]
+        r.positions = positions.data_ptr()
+        return r
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, sections=None, scaling: str = "none",
@@ -347,14 +354,14 @@ def rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, *,
     """Turn X [n][heads][128] (fp16 / bf16 / fp32, any token and head strides) by its positions
     (int64 [n], or [axes][n] for a table with several axes).  ``out`` may be X itself.
     ``backward`` gives the gradient of X from that of the result."""
-    _rows(X, "X")
-    n, heads, _ = X.shape
+    n, heads, xt, xh = _rows(X, "X")
     if out is None:
         out = _empty((n, heads, D), X.dtype, X.device, stream)
-    _rows(out, "out")
-    _need(out.shape == X.shape and out.dtype == X.dtype, "out must have the shape and type of X")
-    prm = _c.qvg_rope_params(n, heads, D, _DT[X.dtype], int(backward), *_row_strides(X),
-                             *_row_strides(out))
+        yt, yh = heads * D, D
+    else:
+        on, oh, yt, yh = _rows(out, "out")
+        _need(on == n and oh == heads and out.dtype == X.dtype, "out must have the shape and type of X")
+    prm = _c.qvg_rope_params(n, heads, D, _DT[X.dtype], 1 if backward else 0, xt, xh, yt, yh)
     rc = _c.qvg_rope(prm, table.rotary(positions, n), X.data_ptr(), out.data_ptr(),
                      _stream_handle(stream))
     if rc != _c.QVG_OK:
@@ -362,7 +369,7 @@ def rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, *,
     return out
 
 
-@dataclass
+@dataclass(frozen=True)
 class PagedKV:
     """Pages of recent keys and values (layouts as in include/qvg.h).  The type of ``k`` and
     ``v`` is the page format: fp16, bf16, float8_e4m3fn or int8; the last two have scales."""
@@ -372,37 +379,26 @@ class PagedKV:
     v_scale: torch.Tensor | None = None
 
     def __post_init__(self):
-        _need(self.k.dim() == 4 and self.k.shape[3] == D and self.k.dtype in _PAGE_FORMAT,
+        shape = self.k.shape
+        _need(len(shape) == 4 and shape[3] == D and self.k.dtype in _PAGE_FORMAT,
               "pages are [pages][heads][page_tokens][128] of fp16, bf16, float8_e4m3fn or int8")
         for t in (self.k, self.v):
-            _index(t, self.k.dtype, self.k.shape, "k and v")
+            _index(t, self.k.dtype, shape, "k and v")
         wide = self.k.dtype in (torch.float16, torch.bfloat16)
         for t in (self.k_scale, self.v_scale):
             if wide:
                 _need(t is None, "16-bit pages have no scales")
             else:
                 _need(t is not None, "8-bit pages need k_scale and v_scale")
-                _index(t, torch.float32, self.k.shape[:3], "scales")
-
-    @property
-    def n_pages(self):
-        return self.k.shape[0]
-
-    @property
-    def heads(self):
-        return self.k.shape[1]
-
-    @property
-    def page_tokens(self):
-        return self.k.shape[2]
-
-    @property
-    def format(self):
-        return _PAGE_FORMAT[self.k.dtype]
+                _index(t, torch.float32, shape[:3], "scales")
+        for name, value in (("n_pages", shape[0]), ("heads", shape[1]), ("page_tokens", shape[2]),
+                            ("format", _PAGE_FORMAT[self.k.dtype]),
+                            ("_buffers", _c.qvg_pages(self.k.data_ptr(), self.v.data_ptr(),
+                                                      _ptr(self.k_scale), _ptr(self.v_scale)))):
+            object.__setattr__(self, name, value)
 
     def buffers(self) -> _c.qvg_pages:
-        return _c.qvg_pages(self.k.data_ptr(), self.v.data_ptr(), _ptr(self.k_scale),
-                            _ptr(self.v_scale))
+        return self._buffers
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
@@ -428,26 +424,27 @@ def page_write(kv: PagedKV, K: torch.Tensor, V: torch.Tensor, slots: torch.Tenso
     """Store new tokens K and V [n][heads][128] at ``slots`` (int64 [n]: page * page_tokens +
     row; negative: skipped), rounded to the pages' format; with ``rope`` the keys are first
     turned by their positions."""
-    _rows(K, "K")
-    _rows(V, "V")
-    n = K.shape[0]
-    _need(K.shape == V.shape and K.dtype == V.dtype and K.shape[1] == kv.heads,
-          "K and V must be [n][%d][128] of one type" % kv.heads)
+    n, heads, kt, kh = _rows(K, "K")
+    vn, v_heads, vt, vh = _rows(V, "V")
+    _need(vn == n and v_heads == heads == kv.heads and K.dtype == V.dtype,
+          "K and V must be [n][heads][128] of one type, with the heads of the pages")
     _index(slots, torch.int64, (n,), "slots")
     _need((rope is None) == (positions is None), "rope and positions go together")
-    prm = _c.qvg_page_write_params(n, kv.heads, D, kv.page_tokens, kv.format, kv.n_pages,
-                                   _DT[K.dtype], *_row_strides(K), *_row_strides(V))
+    prm = _c.qvg_page_write_params(n, heads, D, kv.page_tokens, kv.format, kv.n_pages,
+                                   _DT[K.dtype], kt, kh, vt, vh)
     rc = _c.qvg_page_write(prm, K.data_ptr(), V.data_ptr(), slots.data_ptr(),
-                           None if rope is None else rope.rotary(positions, n), kv.buffers(),
+                           None if rope is None else rope.rotary(positions, n), kv._buffers,
                            _ptr(status), _stream_handle(stream))
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_page_write")
 
 
 def _tables(page_table, seq_lens):
-    _need(page_table.dim() == 2, "page_table must be [sequences][pages]")
-    _index(page_table, torch.int32, page_table.shape, "page_table")
-    _index(seq_lens, torch.int32, page_table.shape[:1], "seq_lens")
+    shape = page_table.shape
+    _need(len(shape) == 2, "page_table must be [sequences][pages]")
+    _index(page_table, torch.int32, shape, "page_table")
+    _index(seq_lens, torch.int32, shape[:1], "seq_lens")
+    return shape[0], shape[1]
 
 
 def page_read(kv: PagedKV, page_table: torch.Tensor, seq_lens: torch.Tensor, count: int, *,
@@ -456,17 +453,18 @@ def page_read(kv: PagedKV, page_table: torch.Tensor, seq_lens: torch.Tensor, cou
     """Tokens [first, first + count) of every sequence as [sequences][2 * heads][count][128],
     keys and values interleaved: ``out[b]`` is an X of ``quantize``.  Rows past a sequence's
     length are zeros.  ``out`` may have larger sequence and tensor strides."""
-    _tables(page_table, seq_lens)
-    n_seqs, shape = page_table.shape[0], (page_table.shape[0], 2 * kv.heads, count, D)
+    n_seqs, max_pages = _tables(page_table, seq_lens)
+    shape = (n_seqs, 2 * kv.heads, count, D)
     if out is None:
         out = _empty(shape, out_dtype, kv.k.device, stream)
-    _need(out.is_cuda and tuple(out.shape) == shape and out.dtype in _DT and
-          (count == 0 or (out.stride(3) == 1 and (count == 1 or out.stride(2) == D))),
-          "out must be %s with contiguous tokens" % (list(shape),))
+    stride = out.stride()
+    _need(out.is_cuda and out.shape == shape and out.dtype in _DT and
+          (count == 0 or (stride[3] == 1 and (count == 1 or stride[2] == D))),
+          "out must be [sequences][2 * heads][count][128] with contiguous tokens")
     prm = _c.qvg_page_read_params(n_seqs, kv.heads, D, kv.page_tokens, kv.format, _DT[out.dtype],
-                                  kv.n_pages, page_table.shape[1], first, count,
-                                  out.stride(0) if n_seqs > 1 else 0, out.stride(1))
-    rc = _c.qvg_page_read(prm, kv.buffers(), page_table.data_ptr(), seq_lens.data_ptr(),
+                                  kv.n_pages, max_pages, first, count,
+                                  stride[0] if n_seqs > 1 else 0, stride[1])
+    rc = _c.qvg_page_read(prm, kv._buffers, page_table.data_ptr(), seq_lens.data_ptr(),
                           out.data_ptr(), _ptr(status), _stream_handle(stream))
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_page_read")
@@ -487,10 +485,8 @@ def page_attention(Q: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
     ``max_kv`` (about the longest sequence, the page table's capacity by default) sizes the
     split of the work.  Returns the output, and with ``return_lse`` the fp32 log-sum-exp
     [total_q][q_heads] beside it."""
-    _rows(Q, "Q")
-    _tables(page_table, seq_lens)
-    total, q_heads, _ = Q.shape
-    n_seqs, max_pages = page_table.shape
+    total, q_heads, qt, qh = _rows(Q, "Q")
+    n_seqs, max_pages = _tables(page_table, seq_lens)
     if cu_q is None:
         _need(total % n_seqs == 0 and (max_q is None or max_q == total // n_seqs),
               "without cu_q every sequence has total_q / sequences queries")
@@ -501,22 +497,24 @@ def page_attention(Q: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
     if out is None:
         out = _empty((total, q_heads, D), Q.dtype if out_dtype is None else out_dtype, Q.device,
                      stream)
-    _rows(out, "out")
-    _need(out.shape == Q.shape, "out must have the shape of Q")
+        ot, oh = q_heads * D, D
+    else:
+        on, o_heads, ot, oh = _rows(out, "out")
+        _need(on == total and o_heads == q_heads, "out must have the shape of Q")
     if lse is None and return_lse:
         lse = _empty((total, q_heads), torch.float32, Q.device, stream)
-    if lse is not None:
+    elif lse is not None:
         _index(lse, torch.float32, (total, q_heads), "lse")
     prm = _c.qvg_page_attention_params(
         n_seqs, q_heads, kv.heads, D, kv.page_tokens, kv.format, _DT[Q.dtype], _DT[out.dtype],
-        kv.n_pages, max_pages, int(causal), window, total, max_q,
+        kv.n_pages, max_pages, 1 if causal else 0, window, total, max_q,
         max_pages * kv.page_tokens if max_kv is None else max_kv,
-        D ** -0.5 if scale is None else scale, *_row_strides(Q), *_row_strides(out))
+        D ** -0.5 if scale is None else scale, qt, qh, ot, oh)
     if workspace is None:
         need = _c.qvg_page_attention_workspace_bytes(prm)
         if need:
             workspace = _empty((need,), torch.uint8, Q.device, stream)
-    rc = _c.qvg_page_attention(prm, Q.data_ptr(), kv.buffers(), page_table.data_ptr(),
+    rc = _c.qvg_page_attention(prm, Q.data_ptr(), kv._buffers, page_table.data_ptr(),
                                seq_lens.data_ptr(), _ptr(cu_q), out.data_ptr(), _ptr(lse),
                                _ptr(workspace), 0 if workspace is None else workspace.numel(),
                                _ptr(status), _stream_handle(stream))

@@ -52,7 +52,7 @@ template <bool QB, int FMT>
 __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan p) {
     pdl_begin();
     constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
-    constexpr bool PVB = WIDE && QB;            // type of the weights and values; 8-bit codes: fp16
+    constexpr bool PVB = WIDE && QB;            // type of all operands; 8-bit pages: fp16
     constexpr int ROWB = WIDE ? 2 * kD : kD;    // bytes of a cached row
     constexpr int NCH = ROWB / 64;              // 16-byte chunks of a row per lane
     __shared__ float s_o[kRowsWarps][kRowsM][kRowsPad];
@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
 
     // Q in the order the keys' chunks come in
     uint32_t qa[8][4];
+    float qmul[2] = {1.f, 1.f};  // 8-bit pages: powers of two taken out of the rows of Q
+    uint4 qraw[2][4];
 #pragma unroll
     for (int x = 0; x < 2; x++) {
         const int r = r0 + g + 8 * x, i = r / p.G;
@@ -91,10 +93,31 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
             const int ch = WIDE ? (j * 4 + q) * 8 : ((j >> 1) * 4 + q) * 16 + (j & 1) * 8;
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows) w = __ldg(reinterpret_cast<const uint4 *>(src + ch));
+            if constexpr (!WIDE && QB) qraw[x][j] = w;
             qa[2 * j][x] = w.x;
             qa[2 * j][2 + x] = w.y;
             qa[2 * j + 1][x] = w.z;
             qa[2 * j + 1][2 + x] = w.w;
+        }
+    }
+
+    if constexpr (!WIDE && QB) {
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+            uint32_t big = 0;
+#pragma unroll
+            for (int j = 0; j < 4; j++) big = max(big, bf16x2_max_bits(qraw[x][j]));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            qmul[x] = bf16_pow2(big);
+            const float inv = 1.f / qmul[x];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                qa[2 * j][x] = bf16x2_to_f16x2(qraw[x][j].x, inv);
+                qa[2 * j][2 + x] = bf16x2_to_f16x2(qraw[x][j].y, inv);
+                qa[2 * j + 1][x] = bf16x2_to_f16x2(qraw[x][j].z, inv);
+                qa[2 * j + 1][2 + x] = bf16x2_to_f16x2(qraw[x][j].w, inv);
+            }
         }
     }
 
@@ -161,8 +184,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
 #pragma unroll
                     for (int w = 0; w < 4; w++) {
                         const uint32_t codes = word_of(kr[u][c], w);
-                        const uint2 k2 = QB ? codes_to_bf16<FMT == PF_E4M3>(codes) : codes_to_f16<FMT == PF_E4M3>(codes);
-                        mma16816<QB>(s[u], qa[4 * c + w], k2.x, k2.y);
+                        const uint2 k2 = codes_to_f16<FMT == PF_E4M3>(codes);
+                        mma16816<PVB>(s[u], qa[4 * c + w], k2.x, k2.y);
                     }
                 }
             }
@@ -174,7 +197,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) k_page_attn_rows(PAttnPlan
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 float f = p.scale_log2;
-                if constexpr (!WIDE) f *= ksc[2 * u + (e & 1)];
+                if constexpr (!WIDE) f *= ksc[2 * u + (e & 1)] * qmul[e >> 1];
                 s[u][e] *= f;
                 const int key = key0 + 8 * u + (e & 1), x = e >> 1;
                 if (!whole && (key < row_lo[x] || key >= row_hi[x])) s[u][e] = -INFINITY;

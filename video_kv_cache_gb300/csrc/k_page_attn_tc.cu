@@ -6,12 +6,15 @@
 // two tiles of 128 rows (query tokens x grouped query heads of one key/value head) and walks
 // the keys in tiles of 128; both row tiles use every key tile that is loaded.  One pass, with a
 // running maximum and weight sum per row:
-//   * warp 9 loads: a tile's pages by TMA into a ring of 32 KB slots (K and V alternate), in the
-//     128-byte swizzled layout that serves K as a K-major operand and V as an MN-major one;
-//   * warp 8, one thread: S_t = Q_t K^T into TMEM, then O_t += P_t V with P_t read from TMEM;
-//   * warps 0-3 and 4-7: the softmax of row tile 0 and 1, a row a thread: its 128 scores from
-//     TMEM, their maximum, powers of two against it, the weights in 16 bits back into TMEM over
-//     the scores.  While one tile's softmax runs, the tensor cores work on the other's.
+//   * one warp loads: a tile's pages by TMA into a ring of 32 KB slots (K and V alternate), in
+//     the 128-byte swizzled layout that serves K as a K-major operand and V as an MN-major one;
+//   * one warp issues S_t = Q_t K^T into TMEM, then O_t += P_t V with P_t read from TMEM;
+//   * warps 0-7 and 8-15: the softmax of row tile 0 and 1, two threads a row with 64 scores
+//     each (one would hold 128 in registers and spill, and its chain of latencies is what the
+//     tensor cores wait for): scores from TMEM, their maximum, exchanged between the two
+//     through shared memory, powers of two against it, and the weights in 16 bits back into
+//     TMEM over the scores.  While one tile's softmax runs, the tensor cores work on the
+//     other's.
 // The running maximum is raised only when a row's scores pass it by more than 2^8: the weights
 // stay below 2^8 and O_t in TMEM is rescaled (by the softmax warps themselves) a few times in
 // all instead of once a tile; the result is the same, since numerator and weight sum share the
@@ -19,10 +22,11 @@
 // TMEM: S/P of the two row tiles (128 columns each; the weights of a tile take the first 64 of
 // its scores' columns), then O of the two (128 each): all 512 columns, one CTA an SM.
 //
-// 8-bit pages: four more warps widen the codes (exactly) to 16 bits into the ring, from raw
-// tiles that TMA brings.  The keys' scales multiply the scores, the values' the weights, which
-// are held in fp16 against a running reference 2^e near the largest scale: rounding them costs
-// 2^-11, as the values' own codes are exact.
+// 8-bit pages: four more warps widen the codes (exactly) to fp16 into the ring, from raw tiles
+// that TMA brings.  bf16 queries are made fp16 too, each row scaled by a power of two that
+// brings its largest channel to 1 .. 2: what falls below fp16's range is 2^-25 of that.  The
+// keys' scales multiply the scores, the values' the weights, which are held in fp16 against a
+// running reference 2^e near the largest scale: rounding them costs 2^-11.
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
@@ -39,20 +43,28 @@ constexpr uint32_t kHalf = kTcM * 128;     // 64 channels of 128 rows: 16 KB
 constexpr uint32_t kSlot = 2 * kHalf;      // a whole 16-bit tile: 32 KB
 constexpr uint32_t kRaw = kTcN * kD;       // a tile of 8-bit codes: 16 KB
 constexpr uint64_t kPageWaitNs = 2000000000ull;  // a wait in the pipeline gives up after this
+constexpr int kValueShift = 4;             // weights with values' scales over 2^e are held times 2^4
 constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
 
 template <int FMT>
 struct TcShape {
     static constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
-    static constexpr int SLOTS = WIDE ? 5 : 3;     // ring of 16-bit tiles
-    static constexpr int RAWS = 3;                 // ring of raw 8-bit tiles
-    static constexpr int THREADS = WIDE ? 384 : 512;
+    static constexpr int SLOTS = WIDE ? 5 : 3;       // ring of 16-bit tiles
+    static constexpr int RAWS = 3;                   // ring of raw 8-bit tiles
+    // 16 softmax warps; MMA, loads and two idle ones (registers move by groups of four warps);
+    // 8-bit: four that widen
+    static constexpr int THREADS = WIDE ? 640 : 768;
+    // registers at launch (65,536 over the warps of an SM quarter), and after they were shared
+    // out anew: the groups' sum stays what the launch had
+    static constexpr int REGS = WIDE ? 96 : 80, REGS_SOFTMAX = WIDE ? 104 : 96, REGS_REST = WIDE ? 64 : 48;
+    static_assert(512 * REGS_SOFTMAX + (THREADS - 512) * REGS_REST <= THREADS * REGS, "register shares");
     static constexpr uint32_t SMEM_TILES = 2 * kSlot + SLOTS * kSlot + (WIDE ? 0 : RAWS * kRaw);
 };
 
 // Everything the roles share besides the tiles (the 16-bit formats have no scales).
 template <int FMT>
 struct TcShared {
+    static constexpr bool WIDE = TcShape<FMT>::WIDE;
     uint64_t full[5], empty[5];         // ring of 16-bit tiles
     uint64_t raw_full[3], raw_empty[3];
     uint64_t s_full[2], p_full[2], o_done[2];
@@ -62,13 +74,17 @@ struct TcShared {
     int abort;
     int vexp[2];                        // exponent of the values' reference scale, per tile parity
     float wmax[4];
-    __align__(16) float ks[2][TcShape<FMT>::WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
-    __align__(16) float vs[2][TcShape<FMT>::WIDE ? 4 : kTcN];  // values' scales over the reference
+    // the two threads of a row: their maxima of this tile, by tile parity; at the end the same
+    // 2 KB take their weight sums as floats
+    __align__(16) uint16_t xmax[2][2][2][kTcM];
+    __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
+    __align__(16) float vs[2][WIDE ? 4 : kTcN];  // values' scales over the reference
+    float qmul[WIDE ? 4 : 2 * kTcM];             // powers of two taken out of the rows of Q
 };
 
 template <int FMT>
 constexpr size_t tc_smem() {
-    constexpr size_t bytes = 1024 + TcShape<FMT>::SMEM_TILES + sizeof(TcShared<FMT>);
+    constexpr size_t bytes = TcShape<FMT>::SMEM_TILES + sizeof(TcShared<FMT>);
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     return bytes;
 }
@@ -79,6 +95,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0u;
+}
 // D[tmem] (+)= A[tmem] B[smem]
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -88,16 +114,23 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "r"(accumulate)
         : "memory");
 }
-// 32 consecutive columns of this thread's TMEM lane written.
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t r[32]) {
+// 16 consecutive columns of this thread's TMEM lane written / read.
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t r[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t r[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -114,18 +147,36 @@ __device__ __forceinline__ uint32_t attn_idesc(bool bf16, bool b_mn) {
     return (1u << 4) | (f << 7) | (f << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(kTcN >> 3) << 17) |
            ((uint32_t)(kTcM >> 4) << 24);
 }
-// Whether all 128 threads of named barrier 1 say so; every one of them gets the same answer.
-__device__ __forceinline__ bool all_of_128(bool v) {
+// Meets the other threads of a named barrier; whether every one of them says so (the same
+// answer for all).  Roles that meet at barriers decide together this way whether to go on.
+template <int THREADS>
+__device__ __forceinline__ bool meet(int id, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.aligned.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}\n"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "r"(id), "n"(THREADS)
         : "memory");
     return r != 0u;
+}
+// Bounded wait on a phase: polls, and looks at the clock and the abort flag now and then.
+__device__ __forceinline__ bool page_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (mbar_try(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; n < kSpinLimit; n++) {
+        if (mbar_try(bar, parity)) return true;
+        if ((n & 63u) == 0u) {
+            if (*abort_flag) return false;
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kPageWaitNs) break;
+        }
+    }
+    *abort_flag = 1;
+    return false;
 }
 template <int REGS>
 __device__ __forceinline__ void regs_inc() {
@@ -134,6 +185,18 @@ __device__ __forceinline__ void regs_inc() {
 template <int REGS>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+// 64 columns of this thread's TMEM lane multiplied by f.
+__device__ __forceinline__ void rescale64(uint32_t at, float f) {
+#pragma unroll
+    for (int c = 0; c < 64; c += 16) {
+        uint32_t w[16];
+        tc_ld16(at + c, w);
+#pragma unroll
+        for (int k = 0; k < 16; k++) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+        tc_st16(at + c, w);
+    }
+    tc_wait_st();
 }
 }  // namespace
 
@@ -145,11 +208,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     pdl_begin();
     using T = TcShape<FMT>;
     constexpr bool WIDE = T::WIDE;
-    constexpr bool PVB = WIDE && QB;  // type of weights and values; 8-bit codes: fp16
+    constexpr bool BF = WIDE && QB;  // type of all operands; 8-bit pages: fp16
     constexpr int SLOTS = T::SLOTS;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *sm = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    constexpr int MMA_WARP = 16, LOAD_WARP = 17, WIDEN_WARP = 20;
+    extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *sQ = sm, *sKV = sm + 2 * kSlot, *sRaw = sKV + SLOTS * kSlot;
     TcShared<FMT> &sh = *reinterpret_cast<TcShared<FMT> *>(sm + T::SMEM_TILES);
     volatile int *abort_flag = &sh.abort;
@@ -174,13 +236,18 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     // goes into Q, so that the maximum of the scores is the maximum of what is exponentiated.
     {
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        for (int x = threadIdx.x; x < 2 * kTcM * 16; x += T::THREADS) {
+        for (int x = threadIdx.x; x < 2 * kTcM * 16; x += T::THREADS) {  // whole warps, 16 lanes a row
             const int row = x >> 4, c = x & 15, r = r0 + row, i = r / p.G;
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows) {
                 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
                                                           (int64_t)(h * p.G + r - i * p.G) * p.qh) + c);
                 w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+            }
+            if constexpr (!WIDE) {
+                float mul = 1.f;
+                if constexpr (QB) w = normalised_f16(w, mul, 16);
+                if (c == 0) sh.qmul[row] = mul;
             }
             const uint32_t at = (row >> 7) * kSlot + (c >> 3) * kHalf + (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
             *reinterpret_cast<uint4 *>(sQ + at) = w;
@@ -198,10 +265,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         }
         for (int t = 0; t < 2; t++) {
             mbar_init(smem_u32(&sh.s_full[t]), 1);
-            mbar_init(smem_u32(&sh.p_full[t]), 4);
+            mbar_init(smem_u32(&sh.p_full[t]), 8);
             mbar_init(smem_u32(&sh.o_done[t]), 1);
             mbar_init(smem_u32(&sh.sc_full[t]), 4);
-            mbar_init(smem_u32(&sh.sc_empty[t]), 4 * nt);
+            mbar_init(smem_u32(&sh.sc_empty[t]), 8 * nt);
         }
         mbar_init(smem_u32(&sh.edge), 1);
         mbar_init(smem_u32(&sh.fin), 1);
@@ -209,7 +276,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 8) {
+    if (warp == MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                      "r"(512u)
                      : "memory");
@@ -219,21 +286,21 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    auto wait = [&](uint64_t &bar, uint32_t parity) {
-        return mbar_wait(smem_u32(&bar), parity & 1u, abort_flag, kPageWaitNs);
-    };
+    auto wait = [&](uint64_t &bar, uint32_t parity) { return page_wait(smem_u32(&bar), parity & 1u, abort_flag); };
 
-    if (warp >= 8) {
-        if constexpr (!WIDE) {
-            if (warp < 12) regs_dec<56>(); else regs_dec<88>();
-        }
-        if (warp == 8) {
+    if (warp >= MMA_WARP) {
+        regs_dec<T::REGS_REST>();
+        if (warp == MMA_WARP) {
             // ---------------------------------------------------------------- MMA issuer
-            if (lane == 0 && n > 0) {
-                const uint32_t id_qk = attn_idesc(QB, false), id_pv = attn_idesc(PVB, true);
-                const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
+            // What this thread does between two batches of MMAs is time that the tensor cores
+            // stand still, so a batch is as long as it can be (O_t += P_t V, then the next
+            // tile's S_t) and follows one wait, that for P_t; the ring was waited for before.
+            if (n > 0 && elect_one()) {
+                const uint32_t id_qk = attn_idesc(BF, false), id_pv = attn_idesc(BF, true);
+                const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(smem_u32(sKV)),
+                               v_desc = sw128_mn_desc(smem_u32(sKV));
                 auto scores = [&](int t, int slot) {
-                    const uint64_t a = sw128_desc(q_addr + t * kSlot), k = sw128_desc(kv_addr + slot * kSlot);
+                    const uint64_t a = q_desc + (uint64_t)(t * (kSlot >> 4)), k = k_desc + (uint64_t)(slot * (kSlot >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 8; kk++) {
                         const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
@@ -247,30 +314,31 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     for (int t = 0; t < nt; t++) scores(t, 0);
                     tc_commit(smem_u32(&sh.empty[0]));
                 }
-                int first = 1;  // the first product overwrites O
                 for (int j = 0; ok && j < n; j++) {
                     const uint32_t iv = 2 * j + 1, ik = iv + 1;  // ring items: V of this tile, K of the next
                     const int sv = iv % SLOTS, sk = ik % SLOTS;
                     // the 16-key steps of the tile that some row sees
                     const int k0 = (j0 + j) * kTcN;
                     const int st0 = max(lo - k0, 0) >> 4, st1 = (min(hi - k0, kTcN) + 15) >> 4;
+                    const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
+                    const bool more = j + 1 < n;
+                    ok = wait(sh.full[sv], iv / SLOTS) && (!more || wait(sh.full[sk], ik / SLOTS));
                     for (int t = 0; ok && t < nt; t++) {
-                        ok = wait(sh.p_full[t], j) && (t > 0 || wait(sh.full[sv], iv / SLOTS));
+                        ok = wait(sh.p_full[t], j);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t v = sw128_mn_desc(kv_addr + sv * kSlot);
-                        for (int s = st0; s < st1; s++)
-                            tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, v + ((s * 2048) >> 4), id_pv,
-                                      !(first && s == st0));
-                        tc_commit(smem_u32(&sh.o_done[t]));
-                        if (t == nt - 1) {
-                            tc_commit(smem_u32(&sh.empty[sv]));
-                            first = 0;
+                        const uint32_t o = tmem + 256 + t * 128, w = tmem + t * 128;
+                        if (st0 == 0 && st1 == 8) {
+#pragma unroll
+                            for (int s = 0; s < 8; s++)
+                                tc_mma_ts(o, w + s * 8, v + (uint64_t)((s * 2048) >> 4), id_pv, j + s > 0);
+                        } else {
+                            for (int s = st0; s < st1; s++)
+                                tc_mma_ts(o, w + s * 8, v + (uint64_t)((s * 2048) >> 4), id_pv, j > 0 || s > st0);
                         }
-                        if (j + 1 < n) {
-                            ok = t > 0 || wait(sh.full[sk], ik / SLOTS);
-                            if (!ok) break;
-                            tc_fence_after();
+                        tc_commit(smem_u32(&sh.o_done[t]));
+                        if (t == nt - 1) tc_commit(smem_u32(&sh.empty[sv]));
+                        if (more) {
                             scores(t, sk);
                             if (t == nt - 1) tc_commit(smem_u32(&sh.empty[sk]));
                         }
@@ -280,23 +348,35 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 tc_commit(smem_u32(&sh.fin));
                 mbar_wait_final(smem_u32(&sh.fin), 0);
             }
-        } else if (warp == 9) {
+        } else if (warp == LOAD_WARP) {
             // ---------------------------------------------------------------- TMA loads
             const int shift = 31 - __clz(p.page), per_tile = kTcN >> shift;
             bool bad = false, ok = true;
             uint32_t edges = 0, issued = 0;
             constexpr int RING = WIDE ? SLOTS : T::RAWS;
+            // the pages of a tile that hold a key some row sees, a lane each; looked up one
+            // tile ahead
+            auto in_sight = [&](int k0) {
+                const int token = k0 + (lane << shift);
+                return lane < per_tile && token < hi && token + p.page > lo;
+            };
+            auto row_of = [&](int k0) {
+                return in_sight(k0) ? (int)((page_of(p, b, k0 + (lane << shift), shift, bad) * p.H + h) << shift) : 0;
+            };
+            int row = 0, row_next = n > 0 ? row_of(j0 * kTcN) : 0;
             for (uint32_t it = 0; ok && it < 2u * n; it++) {
                 const int k0 = (j0 + (int)(it >> 1)) * kTcN, slot = it % RING;
                 const bool value = it & 1;
+                if (!value) {
+                    row = row_next;
+                    if (it + 2 < 2u * n) row_next = row_of(k0 + kTcN);
+                }
                 uint64_t &full = WIDE ? sh.full[slot] : sh.raw_full[slot];
                 ok = wait(WIDE ? sh.empty[slot] : sh.raw_empty[slot], it / RING + 1);
+                ok = !__any_sync(0xffffffffu, !ok);
                 if (!ok) break;
-                // the pages of this tile that hold a key some row sees, a lane each
-                const int token = k0 + (lane << shift);
-                const bool mine = lane < per_tile && token < hi && token + p.page > lo;
+                const bool mine = in_sight(k0);
                 const uint32_t pages = __popc(__ballot_sync(0xffffffffu, mine));
-                const int64_t row = mine ? (page_of(p, b, token, shift, bad) * p.H + h) << shift : 0;
                 // a value tile at the edge of what is seen, whose outer rows must be zeroed
                 const bool edge = WIDE && value && (((lo - k0) & 15 && lo > k0) || ((hi - k0) & 15 && hi < k0 + kTcN));
                 const uint32_t bar = smem_u32(edge ? &sh.edge : &full);
@@ -306,10 +386,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     const CUtensorMap *map = value ? &tmV : &tmK;
                     if constexpr (WIDE) {
                         const uint32_t dst = smem_u32(sKV) + slot * kSlot + ((uint32_t)lane << shift) * 128;
-                        tma_load_2d(dst, map, 0, (int)row, bar);
-                        tma_load_2d(dst + kHalf, map, 64, (int)row, bar);
+                        tma_load_2d(dst, map, 0, row, bar);
+                        tma_load_2d(dst + kHalf, map, 64, row, bar);
                     } else {
-                        tma_load_2d(smem_u32(sRaw) + slot * kRaw + ((uint32_t)lane << shift) * kD, map, 0, (int)row, bar);
+                        tma_load_2d(smem_u32(sRaw) + slot * kRaw + ((uint32_t)lane << shift) * kD, map, 0, row, bar);
                     }
                 }
                 issued = it + 1;
@@ -335,69 +415,72 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             const uint32_t from = issued > (uint32_t)RING ? issued - RING : 0u;
             for (uint32_t it = from; it < issued; it++)
                 mbar_wait_final(smem_u32(WIDE ? &sh.full[it % RING] : &sh.raw_full[it % RING]), (it / RING) & 1u);
-        } else if (!WIDE && warp >= 12) {
+        } else if (!WIDE && warp >= WIDEN_WARP) {
             // ---------------------------------------------------------------- 8-bit codes widened
-            const int shift = 31 - __clz(p.page), x = threadIdx.x - 384;
+            const int shift = 31 - __clz(p.page), x = threadIdx.x - 32 * WIDEN_WARP;
             const float mult = fabsf(p.scale_log2);
             int e = -126;
-            bool ok = true, bad = false;  // a wait that gave up: the four warps leave together
+            bool ok = true, bad = false;
+            // scales of a tile's keys, one a thread, read one tile ahead; outside what is seen
+            // they are 0
+            float ks = 0.f, vs = 0.f;
+            auto load_scales = [&](int key) {
+                ks = vs = 0.f;
+                if (key >= lo && key < hi) {
+                    const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
+                    ks = __ldg(p.ks + row);
+                    vs = __ldg(p.vs + row);
+                }
+            };
+            if (n > 0) load_scales(j0 * kTcN + x);
+            // 16 codes (chunk c of a row) a thread, rows 16 apart: eight lanes that are served
+            // together have eight rows of one chunk, which the swizzle of the raw tile and that
+            // of the widened one both spread over all banks
+            const int c = (x >> 3) & 7, r8 = x & 7, rb = r8 + ((x >> 6) << 3);
+            const unsigned char *src0 = sRaw + rb * kD + ((c ^ r8) << 4);
+            unsigned char *dst0 = sKV + (c >> 2) * kHalf + rb * 128;
+            const int d0 = ((2 * (c & 3)) ^ r8) << 4, d1 = ((2 * (c & 3) + 1) ^ r8) << 4;
             for (uint32_t it = 0; it < 2u * n; it++) {
                 const int j = it >> 1, k0 = (j0 + j) * kTcN, slot = it % SLOTS, raw = it % T::RAWS;
-                const bool value = it & 1;
-                if (!value) {
-                    // scales of the tile's keys, one a thread; outside what is seen they are 0
-                    const int key = k0 + x, buf = j & 1;
-                    float ks = 0.f, vs = 0.f;
-                    if (key >= lo && key < hi) {
-                        const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
-                        ks = __ldg(p.ks + row);
-                        vs = __ldg(p.vs + row);
-                    }
+                if (!(it & 1)) {
+                    const int buf = j & 1;
                     float m = fabsf(vs);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                     ok = ok && wait(sh.sc_empty[buf], (j >> 1) + 1);
-                    if (lane == 0) sh.wmax[warp - 12] = m;
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (lane == 0) sh.wmax[warp - WIDEN_WARP] = m;
+                    ok = meet<128>(1, ok);
+                    if (!ok) break;  // the four warps leave together
                     m = fmaxf(fmaxf(sh.wmax[0], sh.wmax[1]), fmaxf(sh.wmax[2], sh.wmax[3]));
-                    ok = all_of_128(ok);
-                    if (!ok) break;
+                    meet<128>(1, true);
                     // the reference moves only when a scale passes it by 2^3: the weights stay
                     // below 2^8 (kLazy) * 2^3 * 2^4 < fp16's largest
                     const int ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
                     if (j == 0 || ee > e + 2) e = ee;
                     sh.ks[buf][x] = ks * mult;
-                    sh.vs[buf][x] = vs * __uint_as_float((uint32_t)(127 + 4 - e) << 23);
+                    sh.vs[buf][x] = vs * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23);
                     if (x == 0) sh.vexp[buf] = e;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
+                    if (j + 1 < n) load_scales(k0 + kTcN + x);
                 }
                 ok = ok && wait(sh.raw_full[raw], it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1);
-                if (__any_sync(0xffffffffu, !ok)) {
-                    ok = false;
-                    continue;
-                }
-                const unsigned char *src = sRaw + raw * kRaw;
-                unsigned char *dst = sKV + slot * kSlot;
-#pragma unroll 4
+                ok = !__any_sync(0xffffffffu, !ok);
+                if (!ok) continue;
+                const bool whole = k0 >= lo && k0 + kTcN <= hi;
+                const unsigned char *src = src0 + raw * kRaw;
+                unsigned char *dst = dst0 + slot * kSlot;
+#pragma unroll 2
                 for (int u = 0; u < 8; u++) {
-                    const int chunk = u * 128 + x, r = chunk >> 3, c = chunk & 7;  // 16 codes
-                    const int key = k0 + r;
-                    uint4 w = *reinterpret_cast<const uint4 *>(src + r * kD + c * 16);
-                    if (key < lo || key >= hi) w = make_uint4(0u, 0u, 0u, 0u);
-                    uint2 y[4];
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const uint32_t code = k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w;
-                        y[k] = QB && !value ? codes_to_bf16<FMT == PF_E4M3>(code) : codes_to_f16<FMT == PF_E4M3>(code);
+                    uint4 w = *reinterpret_cast<const uint4 *>(src + u * 16 * kD);
+                    if (!whole) {  // what no row sees may hold anything
+                        const int key = k0 + rb + u * 16;
+                        if (key < lo || key >= hi) w = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    // chunks 2c, 2c + 1 of the row's 16; the two halves of a row start with
-                    // different ones, so that eight lanes' stores meet every bank once
-                    unsigned char *half = dst + (c >> 2) * kHalf + r * 128;
-                    const int c0 = 2 * (c & 3), sw = r & 7, swap = c >> 2;
-                    const uint4 a0 = make_uint4(y[0].x, y[0].y, y[1].x, y[1].y), a1 = make_uint4(y[2].x, y[2].y, y[3].x, y[3].y);
-                    *reinterpret_cast<uint4 *>(half + (((c0 + swap) ^ sw) << 4)) = swap ? a1 : a0;
-                    *reinterpret_cast<uint4 *>(half + (((c0 + 1 - swap) ^ sw) << 4)) = swap ? a0 : a1;
+                    const uint2 y0 = codes_to_f16<FMT == PF_E4M3>(w.x), y1 = codes_to_f16<FMT == PF_E4M3>(w.y),
+                                y2 = codes_to_f16<FMT == PF_E4M3>(w.z), y3 = codes_to_f16<FMT == PF_E4M3>(w.w);
+                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d0) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d1) = make_uint4(y2.x, y2.y, y3.x, y3.y);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -410,47 +493,66 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         }
     } else {
         // -------------------------------------------------------------------- softmax
-        if constexpr (!WIDE) regs_inc<184>();
-        const int t = warp >> 2, row = (warp & 3) * 32 + lane, r = r0 + t * kTcM + row;
+        regs_inc<T::REGS_SOFTMAX>();
+        const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+        const int row = quarter * 32 + lane, r = r0 + t * kTcM + row;
+        const int id = 2 + t * 4 + quarter;  // named barrier of the two warps of these rows
         if (t < nt) {
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
+            const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+            const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128 + half * 64;
             const int i = min(r, rows - 1) / p.G, hq = h * p.G + min(r, rows - 1) - i * p.G;
             const int r_lo = seen_lo(p, sq, i), r_hi = seen_hi(p, sq, i);
-            const float mult = fabsf(p.scale_log2);
+            const float mult = WIDE ? fabsf(p.scale_log2) : sh.qmul[t * kTcM + row];
+            const float2 sc2 = make_float2(mult, mult);
             float m = -INFINITY, l = 0.f;
             int e = 0;
-            bool ok = true;
+            bool ok = true;  // the two warps of the rows agree on it every tile
             for (int j = 0; j < n; j++) {
-                const int k0 = (j0 + j) * kTcN, buf = j & 1;
-                ok = wait(sh.s_full[t], j) && (WIDE || wait(sh.sc_full[buf], j >> 1));
-                if (__any_sync(0xffffffffu, !ok)) break;
-                tc_fence_after();
-                float s[128];
-                tc_ld64(s_at, s);
-                tc_ld64(s_at + 64, s + 64);
-                if constexpr (!WIDE) {
+                const int k0 = (j0 + j) * kTcN + half * 64, buf = j & 1;
+                float s[64];
+                ok = ok && wait(sh.s_full[t], j) && (WIDE || wait(sh.sc_full[buf], j >> 1));
+                ok = !__any_sync(0xffffffffu, !ok);
+                float mx = -INFINITY;
+                bool masked = false;
+                if (ok) {
+                    tc_fence_after();
+                    tc_ld32(s_at + half * 64, s);
+                    tc_ld32(s_at + half * 64 + 32, s + 32);
+                    if constexpr (!WIDE) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][c]);
-                        s[c] *= f.x; s[c + 1] *= f.y; s[c + 2] *= f.z; s[c + 3] *= f.w;
+                        for (int c = 0; c < 64; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][half * 64 + c]);
+                            s[c] *= f.x; s[c + 1] *= f.y; s[c + 2] *= f.z; s[c + 3] *= f.w;
+                        }
                     }
-                }
-                const bool masked = __any_sync(0xffffffffu, k0 < r_lo || k0 + kTcN > r_hi);
-                if (masked) {
-                    const int a = r_lo - k0, z = r_hi - k0;
+                    masked = __any_sync(0xffffffffu, k0 < r_lo || k0 + 64 > r_hi);
+                    if (masked) {
+                        const int a = r_lo - k0, z = r_hi - k0;
 #pragma unroll
-                    for (int c = 0; c < 128; c++) s[c] = c >= a && c < z ? s[c] : -INFINITY;
-                }
-                float mx = fmax3(s[0], s[1], s[2]), my = fmax3(s[3], s[4], s[5]);
+                        for (int c = 0; c < 64; c++) s[c] = c >= a && c < z ? s[c] : -INFINITY;
+                    }
+                    float m0 = fmax3(s[0], s[1], s[2]), m1 = fmax3(s[3], s[4], s[5]), m2 = fmax3(s[6], s[7], s[8]),
+                          m3 = fmax3(s[9], s[10], s[11]);
 #pragma unroll
-                for (int c = 6; c < 126; c += 4) {
-                    mx = fmax3(mx, s[c], s[c + 1]);
-                    my = fmax3(my, s[c + 2], s[c + 3]);
+                    for (int c = 12; c < 60; c += 8) {
+                        m0 = fmax3(m0, s[c], s[c + 1]);
+                        m1 = fmax3(m1, s[c + 2], s[c + 3]);
+                        m2 = fmax3(m2, s[c + 4], s[c + 5]);
+                        m3 = fmax3(m3, s[c + 6], s[c + 7]);
+                    }
+                    m0 = fmax3(m0, s[60], s[61]);
+                    m1 = fmax3(m1, s[62], s[63]);
+                    mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * mult;
                 }
-                mx = fmax3(fmaxf(mx, my), s[126], s[127]);
-                if constexpr (WIDE) mx *= mult;
-                bool raise = mx > m + kLazy, move = false;  // -inf + 8: any score raises it
+                // the larger of the two threads' maxima, both cut to 16 bits: any base near the
+                // maximum serves, and the two threads must take the same
+                const uint32_t cut = __float_as_uint(mx) >> 16;
+                sh.xmax[buf][t][half][row] = (uint16_t)cut;
+                ok = meet<64>(id, ok);
+                if (!ok) continue;
+                mx = fmaxf(__uint_as_float(cut << 16), __uint_as_float((uint32_t)sh.xmax[buf][t][half ^ 1][row] << 16));
+                const bool raise = mx > m + kLazy;  // -inf + 8: any score raises it
+                bool move = false;
                 int e_new = e;
                 if constexpr (!WIDE) {
                     e_new = sh.vexp[buf];
@@ -460,49 +562,39 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     m = mx;
                 } else if (__any_sync(0xffffffffu, raise || move)) {
                     const float m_new = raise ? mx : m;
-                    float f = fast_exp2(m - exp_base(m_new));
-                    if (!raise) f = 1.f;
+                    float f = raise ? fast_exp2(m - exp_base(m_new)) : 1.f;
                     l *= f;
                     m = m_new;
                     if constexpr (!WIDE) f = ldexpf(f, e - e_new);
-                    ok = wait(sh.o_done[t], j - 1);
-                    if (__any_sync(0xffffffffu, !ok)) break;
+                    // (a wait that gives up raises the abort flag; what follows is void then)
+                    wait(sh.o_done[t], j - 1);
+                    __syncwarp();
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        float o[32];
-                        tc_ld32(o_at + c, o);
-                        uint32_t w[32];
-#pragma unroll
-                        for (int k = 0; k < 32; k++) w[k] = __float_as_uint(o[k] * f);
-                        tc_st32(o_at + c, w);
-                    }
-                    tc_wait_st();
+                    rescale64(o_at, f);
                 }
                 e = e_new;
                 const float base = exp_base(m);
-                const float2 nb = make_float2(-base, -base), sc2 = make_float2(mult, mult);
+                const float2 nb = make_float2(-base, -base);
                 float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
-                for (int hc = 0; hc < 128; hc += 64) {
-                    uint32_t w[32];
+                for (int q = 0; q < 64; q += 32) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        float2 x = make_float2(s[hc + c], s[hc + c + 1]);
-                        x = WIDE ? __ffma2_rn(x, sc2, nb) : __fadd2_rn(x, nb);
+                    for (int c = q; c < q + 32; c += 2) {
+                        float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, nb);
                         x.x = fast_exp2(x.x);
                         x.y = fast_exp2(x.y);
                         if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
                         if constexpr (!WIDE) {
-                            const float2 f = *reinterpret_cast<const float2 *>(&sh.vs[buf][hc + c]);
-                            const float2 y = make_float2(x.x * f.x, x.y * f.y);
-                            // a hidden key's scale may be NaN: its weight stays 0
-                            x.x = masked && s[hc + c] == -INFINITY ? 0.f : y.x;
-                            x.y = masked && s[hc + c + 1] == -INFINITY ? 0.f : y.y;
+                            x = __fmul2_rn(x, *reinterpret_cast<const float2 *>(&sh.vs[buf][half * 64 + c]));
+                            if (masked) {  // a hidden key's scale may be NaN: its weight stays 0
+                                if (s[c] == -INFINITY) x.x = 0.f;
+                                if (s[c + 1] == -INFINITY) x.y = 0.f;
+                            }
                         }
-                        w[c >> 1] = PVB ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
+                        w[(c - q) >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
-                    tc_st32(s_at + (hc >> 1), w);
+                    tc_st16(s_at + half * 32 + (q >> 1), w);
                 }
                 const float2 ls = __fadd2_rn(la, lb);
                 l += ls.x + ls.y;
@@ -515,19 +607,24 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 }
             }
             if (n > 0) ok = ok && wait(sh.o_done[t], n - 1);
-            ok = !__any_sync(0xffffffffu, !ok);
+            // the row's weight sum
+            float *xl = reinterpret_cast<float *>(sh.xmax) + t * 2 * kTcM;
+            meet<64>(id, true);
+            xl[half * kTcM + row] = l;
+            ok = meet<64>(id, ok);
+            l += xl[(half ^ 1) * kTcM + row];
             tc_fence_after();
             if (ok) {
                 const bool live = r < rows, whole = p.S == 1;
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-                if constexpr (!WIDE) inv = ldexpf(inv, e - 4);
+                if constexpr (!WIDE) inv = ldexpf(inv, e - kValueShift);
                 const int64_t tok = sq.q0 + i;
                 const int64_t part = ((int64_t)split * p.total_q + tok) * p.HQ + hq;
                 const int64_t out = tok * p.ot + hq * p.oh;
                 bool odd = false;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < 64; c += 32) {
                     float o[32];
                     __syncwarp();
                     if (n > 0) {
@@ -542,21 +639,31 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         odd |= !is_finite(o[k]);
                     }
                     if (live) {
+                        const int ch = half * 64 + c;
                         if (!whole) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) store4<DT_F32>(p.part, part * kD + c + k, o + k);
+                            for (int k = 0; k < 32; k += 4) store4<DT_F32>(p.part, part * kD + ch + k, o + k);
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) store_out4(p, out + c + k, o + k);
+                            for (int k = 0; k < 32; k += 4) store_out4(p, out + ch + k, o + k);
                         }
                     }
                 }
                 if (!whole) {
-                    if (live) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, l);
+                    if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, l);
                 } else {
-                    if (live && p.lse) p.lse[tok * p.HQ + hq] = row_lse(m, l);
+                    if (live && half == 0 && p.lse) p.lse[tok * p.HQ + hq] = row_lse(m, l);
                     if (redo_possible(p)) {
-                        uint32_t todo = __ballot_sync(0xffffffffu, odd && live);
+                        // both halves written, then the first half's warp takes its share of
+                        // the rows that either found odd
+                        uint32_t *xo = reinterpret_cast<uint32_t *>(xl + half * kTcM) + quarter;
+                        const uint32_t mine = __ballot_sync(0xffffffffu, odd && live);
+                        meet<64>(id, true);
+                        if (lane == 0) *xo = mine;
+                        __threadfence_block();
+                        meet<64>(id, true);
+                        uint32_t todo = mine | *(reinterpret_cast<uint32_t *>(xl + (half ^ 1) * kTcM) + quarter);
+                        todo &= half ? 0xAAAAAAAAu : 0x55555555u;
                         while (todo) {
                             const int src = __ffs(todo) - 1;
                             todo &= todo - 1;
@@ -578,7 +685,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) or_status(p.status, QVG_DEV_TIMEOUT);
-    if (warp == 8) {
+    if (warp == MMA_WARP) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
@@ -612,7 +719,7 @@ cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
     const void *pools[2] = {p.k, p.v};
     for (int x = 0; x < 2; x++)
         if (enc(&maps[x], dt, 2, const_cast<void *>(pools[x]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     if (p.q_dtype == DT_BF16)
