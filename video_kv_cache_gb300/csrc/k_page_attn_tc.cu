@@ -67,16 +67,14 @@ struct TcShared {
     static constexpr bool WIDE = TcShape<FMT>::WIDE;
     uint64_t full[5], empty[5];         // ring of 16-bit tiles
     uint64_t raw_full[3], raw_empty[3];
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2], p_full[2][2], o_done[2];
     uint64_t sc_full[2], sc_empty[2];   // scales of a key tile
     uint64_t edge, fin;
     uint32_t tmem;
     int abort;
     int vexp[2];                        // exponent of the values' reference scale, per tile parity
     float wmax[4];
-    // the two threads of a row: their maxima of this tile, by tile parity; at the end the same
-    // 2 KB take their weight sums as floats
-    __align__(16) uint16_t xmax[2][2][2][kTcM];
+    float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
     __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
     __align__(16) float vs[2][WIDE ? 4 : kTcN];  // values' scales over the reference
     float qmul[WIDE ? 4 : 2 * kTcM];             // powers of two taken out of the rows of Q
@@ -265,7 +263,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         }
         for (int t = 0; t < 2; t++) {
             mbar_init(smem_u32(&sh.s_full[t]), 1);
-            mbar_init(smem_u32(&sh.p_full[t]), 8);
+            mbar_init(smem_u32(&sh.p_full[t][0]), 8);
+            mbar_init(smem_u32(&sh.p_full[t][1]), 8);
             mbar_init(smem_u32(&sh.o_done[t]), 1);
             mbar_init(smem_u32(&sh.sc_full[t]), 4);
             mbar_init(smem_u32(&sh.sc_empty[t]), 8 * nt);
@@ -324,17 +323,31 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     const bool more = j + 1 < n;
                     ok = wait(sh.full[sv], iv / SLOTS) && (!more || wait(sh.full[sk], ik / SLOTS));
                     for (int t = 0; ok && t < nt; t++) {
-                        ok = wait(sh.p_full[t], j);
+                        ok = wait(sh.p_full[t][0], j);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t o = tmem + 256 + t * 128, w = tmem + t * 128;
-                        if (st0 == 0 && st1 == 8) {
-#pragma unroll
-                            for (int s = 0; s < 8; s++)
-                                tc_mma_ts(o, w + s * 8, v + (uint64_t)((s * 2048) >> 4), id_pv, j + s > 0);
+                        auto product = [&](int s, bool accumulate) {
+                            tc_mma_ts(o, w + s * 8, v + (uint64_t)((s * 2048) >> 4), id_pv, accumulate);
+                        };
+                        // the steps of the first 32 keys of either half, then the others
+                        const bool whole = st0 == 0 && st1 == 8;
+                        if (whole) {
+                            product(0, j > 0);
+                            product(1, true);
+                            product(4, true);
+                            product(5, true);
+                        }
+                        ok = wait(sh.p_full[t][1], j);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (whole) {
+                            product(2, true);
+                            product(3, true);
+                            product(6, true);
+                            product(7, true);
                         } else {
-                            for (int s = st0; s < st1; s++)
-                                tc_mma_ts(o, w + s * 8, v + (uint64_t)((s * 2048) >> 4), id_pv, j > 0 || s > st0);
+                            for (int s = st0; s < st1; s++) product(s, j > 0 || s > st0);
                         }
                         tc_commit(smem_u32(&sh.o_done[t]));
                         if (t == nt - 1) tc_commit(smem_u32(&sh.empty[sv]));
@@ -470,7 +483,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const bool whole = k0 >= lo && k0 + kTcN <= hi;
                 const unsigned char *src = src0 + raw * kRaw;
                 unsigned char *dst = dst0 + slot * kSlot;
-#pragma unroll 2
+#pragma unroll 4
                 for (int u = 0; u < 8; u++) {
                     uint4 w = *reinterpret_cast<const uint4 *>(src + u * 16 * kD);
                     if (!whole) {  // what no row sees may hold anything
@@ -506,7 +519,9 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             const float2 sc2 = make_float2(mult, mult);
             float m = -INFINITY, l = 0.f;
             int e = 0;
-            bool ok = true;  // the two warps of the rows agree on it every tile
+            // (a wait that gives up raises the abort flag: a warp skips its work from then on, but
+            // keeps meeting the other at every barrier)
+            bool ok = true;
             for (int j = 0; j < n; j++) {
                 const int k0 = (j0 + j) * kTcN + half * 64, buf = j & 1;
                 float s[64];
@@ -544,34 +559,36 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     m1 = fmax3(m1, s[62], s[63]);
                     mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * mult;
                 }
-                // the larger of the two threads' maxima, both cut to 16 bits: any base near the
-                // maximum serves, and the two threads must take the same
-                const uint32_t cut = __float_as_uint(mx) >> 16;
-                sh.xmax[buf][t][half][row] = (uint16_t)cut;
-                ok = meet<64>(id, ok);
-                if (!ok) continue;
-                mx = fmaxf(__uint_as_float(cut << 16), __uint_as_float((uint32_t)sh.xmax[buf][t][half ^ 1][row] << 16));
+                // The base moves for a row when its scores pass it by 2^8 (the first tile sets
+                // it), for all rows of the two warps that share them together, or when the
+                // reference of 8-bit values moved.  Nothing else needs the other thread.
                 const bool raise = mx > m + kLazy;  // -inf + 8: any score raises it
-                bool move = false;
                 int e_new = e;
-                if constexpr (!WIDE) {
-                    e_new = sh.vexp[buf];
-                    move = j > 0 && e_new != e;
-                }
-                if (j == 0) {
-                    m = mx;
-                } else if (__any_sync(0xffffffffu, raise || move)) {
-                    const float m_new = raise ? mx : m;
-                    float f = raise ? fast_exp2(m - exp_base(m_new)) : 1.f;
+                if constexpr (!WIDE) e_new = ok ? sh.vexp[buf] : e;
+                if (!meet<64>(id, ok && !raise && j > 0 && e_new == e)) {
+                    // the larger of the two threads' maxima
+                    sh.xmax[t][half][row] = mx;
+                    meet<64>(id, true);
+                    mx = fmaxf(mx, sh.xmax[t][half ^ 1][row]);
+                    meet<64>(id, true);
+                    const bool up = mx > m + kLazy;
+                    const float m_new = up || j == 0 ? mx : m;
+                    float f = up ? fast_exp2(m - exp_base(m_new)) : 1.f;
                     l *= f;
                     m = m_new;
                     if constexpr (!WIDE) f = ldexpf(f, e - e_new);
-                    // (a wait that gives up raises the abort flag; what follows is void then)
-                    wait(sh.o_done[t], j - 1);
-                    __syncwarp();
-                    tc_fence_after();
-                    rescale64(o_at, f);
+                    if (j > 0) {
+                        ok = ok && wait(sh.o_done[t], j - 1);
+                        ok = !__any_sync(0xffffffffu, !ok);
+                        tc_fence_after();
+                        rescale64(o_at, f);
+                        // weights of one thread start a product into all of the row's O: both
+                        // halves of O are rescaled before either goes on
+                        tc_fence_before();
+                        meet<64>(id, true);
+                    }
                 }
+                if (!ok) continue;
                 e = e_new;
                 const float base = exp_base(m);
                 const float2 nb = make_float2(-base, -base);
@@ -595,20 +612,21 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         w[(c - q) >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
                     tc_st16(s_at + half * 32 + (q >> 1), w);
+                    // the product starts with the first 32 keys of either half
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t][q >> 5]));
                 }
                 const float2 ls = __fadd2_rn(la, lb);
                 l += ls.x + ls.y;
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sh.p_full[t]));
-                    if constexpr (!WIDE) mbar_arrive(smem_u32(&sh.sc_empty[buf]));
+                if constexpr (!WIDE) {
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.sc_empty[buf]));
                 }
             }
             if (n > 0) ok = ok && wait(sh.o_done[t], n - 1);
             // the row's weight sum
-            float *xl = reinterpret_cast<float *>(sh.xmax) + t * 2 * kTcM;
+            float *xl = sh.xmax[t][0];
             meet<64>(id, true);
             xl[half * kTcM + row] = l;
             ok = meet<64>(id, ok);
