@@ -73,6 +73,7 @@ struct TcShared {
     uint32_t tmem;
     int abort;
     int vexp[2];                        // exponent of the values' reference scale, per tile parity
+    __align__(16) uint32_t vnan[2][4];                // keys whose value scale is not finite, a bit each
     float wmax[4];
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
     __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
@@ -234,21 +235,28 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     // goes into Q, so that the maximum of the scores is the maximum of what is exponentiated.
     {
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        for (int x = threadIdx.x; x < 2 * kTcM * 16; x += T::THREADS) {  // whole warps, 16 lanes a row
-            const int row = x >> 4, c = x & 15, r = r0 + row, i = r / p.G;
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows) {
-                w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
-                                                          (int64_t)(h * p.G + r - i * p.G) * p.qh) + c);
-                w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
-            }
+        constexpr int CHUNKS = 2 * kTcM * 16, EACH = (CHUNKS + T::THREADS - 1) / T::THREADS;
+        uint4 w[EACH];  // every read in flight before the first is used; whole warps, 16 lanes a row
+#pragma unroll
+        for (int u = 0; u < EACH; u++) {
+            const int x = threadIdx.x + u * T::THREADS, r = r0 + (x >> 4), i = r / p.G;
+            w[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (x < CHUNKS && r < rows)
+                w[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
+                                                             (int64_t)(h * p.G + r - i * p.G) * p.qh) + (x & 15));
+        }
+#pragma unroll
+        for (int u = 0; u < EACH; u++) {
+            const int x = threadIdx.x + u * T::THREADS, row = x >> 4, c = x & 15;
+            if (x >= CHUNKS) break;
+            w[u].x ^= flip; w[u].y ^= flip; w[u].z ^= flip; w[u].w ^= flip;
             if constexpr (!WIDE) {
                 float mul = 1.f;
-                if constexpr (QB) w = normalised_f16(w, mul, 16);
+                if constexpr (QB) w[u] = normalised_f16(w[u], mul, 16);
                 if (c == 0) sh.qmul[row] = mul;
             }
             const uint32_t at = (row >> 7) * kSlot + (c >> 3) * kHalf + (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4 *>(sQ + at) = w;
+            *reinterpret_cast<uint4 *>(sQ + at) = w[u];
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -457,6 +465,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const int j = it >> 1, k0 = (j0 + j) * kTcN, slot = it % SLOTS, raw = it % T::RAWS;
                 if (!(it & 1)) {
                     const int buf = j & 1;
+                    // a scale that is not finite: 0 here, and a bit that makes the rows NaN that see
+                    // the key (and no others)
+                    const uint32_t odd = __ballot_sync(0xffffffffu, !is_finite(vs));
+                    if (!is_finite(vs)) vs = 0.f;
                     float m = fabsf(vs);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -472,6 +484,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     if (j == 0 || ee > e + 2) e = ee;
                     sh.ks[buf][x] = ks * mult;
                     sh.vs[buf][x] = vs * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23);
+                    if (lane == 0) sh.vnan[buf][warp - WIDEN_WARP] = odd;
                     if (x == 0) sh.vexp[buf] = e;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
@@ -513,8 +526,13 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         if (t < nt) {
             const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128 + half * 64;
-            const int i = min(r, rows - 1) / p.G, hq = h * p.G + min(r, rows - 1) - i * p.G;
-            const int r_lo = seen_lo(p, sq, i), r_hi = seen_hi(p, sq, i);
+            // the tiles that every row of this warp sees whole: [open, shut)
+            int open, shut;
+            {
+                const int a = min(r - lane, rows - 1) / p.G, z = min(r - lane + 31, rows - 1) / p.G;
+                open = (seen_lo(p, sq, z) + kTcN - 1) / kTcN - j0;
+                shut = seen_hi(p, sq, a) / kTcN - j0;
+            }
             const float mult = WIDE ? fabsf(p.scale_log2) : sh.qmul[t * kTcM + row];
             const float2 sc2 = make_float2(mult, mult);
             float m = -INFINITY, l = 0.f;
@@ -523,12 +541,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             // keeps meeting the other at every barrier)
             bool ok = true;
             for (int j = 0; j < n; j++) {
-                const int k0 = (j0 + j) * kTcN + half * 64, buf = j & 1;
+                const int buf = j & 1;
                 float s[64];
                 ok = ok && wait(sh.s_full[t], j) && (WIDE || wait(sh.sc_full[buf], j >> 1));
                 ok = !__any_sync(0xffffffffu, !ok);
                 float mx = -INFINITY;
-                bool masked = false;
                 if (ok) {
                     tc_fence_after();
                     tc_ld32(s_at + half * 64, s);
@@ -537,12 +554,21 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
 #pragma unroll
                         for (int c = 0; c < 64; c += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][half * 64 + c]);
-                            s[c] *= f.x; s[c + 1] *= f.y; s[c + 2] *= f.z; s[c + 3] *= f.w;
+                            const float2 x = __fmul2_rn(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
+                            const float2 y = __fmul2_rn(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
+                            s[c] = x.x; s[c + 1] = x.y; s[c + 2] = y.x; s[c + 3] = y.y;
+                        }
+                        const uint4 odd = *reinterpret_cast<const uint4 *>(sh.vnan[buf]);
+                        if (odd.x | odd.y | odd.z | odd.w) {
+                            const int k0 = (j0 + j) * kTcN + half * 64, i = min(r, rows - 1) / p.G;
+                            const uint64_t bits = half ? odd.z | (uint64_t)odd.w << 32 : odd.x | (uint64_t)odd.y << 32;
+                            for (int c = 0; c < 64; c++)
+                                if (bits >> c & 1 && k0 + c >= seen_lo(p, sq, i) && k0 + c < seen_hi(p, sq, i)) l = NAN;
                         }
                     }
-                    masked = __any_sync(0xffffffffu, k0 < r_lo || k0 + 64 > r_hi);
-                    if (masked) {
-                        const int a = r_lo - k0, z = r_hi - k0;
+                    if (j < open || j >= shut) {
+                        const int k0 = (j0 + j) * kTcN + half * 64, i = min(r, rows - 1) / p.G;
+                        const int a = seen_lo(p, sq, i) - k0, z = seen_hi(p, sq, i) - k0;
 #pragma unroll
                         for (int c = 0; c < 64; c++) s[c] = c >= a && c < z ? s[c] : -INFINITY;
                     }
@@ -596,6 +622,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
 #pragma unroll
                 for (int q = 0; q < 64; q += 32) {
                     uint32_t w[16];
+                    float4 vs4 = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
                     for (int c = q; c < q + 32; c += 2) {
                         float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, nb);
@@ -603,11 +630,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         x.y = fast_exp2(x.y);
                         if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
                         if constexpr (!WIDE) {
-                            x = __fmul2_rn(x, *reinterpret_cast<const float2 *>(&sh.vs[buf][half * 64 + c]));
-                            if (masked) {  // a hidden key's scale may be NaN: its weight stays 0
-                                if (s[c] == -INFINITY) x.x = 0.f;
-                                if (s[c + 1] == -INFINITY) x.y = 0.f;
-                            }
+                            if (!(c & 2)) vs4 = *reinterpret_cast<const float4 *>(&sh.vs[buf][half * 64 + c]);
+                            x = __fmul2_rn(x, c & 2 ? make_float2(vs4.z, vs4.w) : make_float2(vs4.x, vs4.y));
                         }
                         w[(c - q) >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
@@ -633,6 +657,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             l += xl[(half ^ 1) * kTcM + row];
             tc_fence_after();
             if (ok) {
+                const int i = min(r, rows - 1) / p.G, hq = h * p.G + min(r, rows - 1) - i * p.G;
                 const bool live = r < rows, whole = p.S == 1;
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
