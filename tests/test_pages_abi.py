@@ -186,10 +186,10 @@ def test_page_attention_refusals(lib, mem, monkeypatch):
     assert call(_attention(total_q=5), cu=None) == 1  # unequal shares need cu_q
     assert qvg.qvg_page_attention(None, mem, good, mem, mem, mem, mem, None, mem, 1, None, None) == 1
     assert qvg.qvg_page_attention_workspace_bytes(None) == 0
-    # long keys and few rows: the keys are split, which needs workspace
-    long = _attention(max_kv=320)
+    # long keys and few rows: the keys are split many ways, which needs workspace
+    long = _attention(n_seqs=1, total_q=3, n_pages=2000, max_pages=1250, max_kv=20000)
     need = qvg.qvg_page_attention_workspace_bytes(long)
-    rows = 6 * 4
+    rows = 3 * 4
     assert need > 0 and need % (rows * (128 + 2) * 4) == 0
     assert call(long, n=need - 1) == call(long, ws=None) == call(long, ws=mem + 4) == qvg.QVG_ERR_WORKSPACE
     assert call(_attention(total_q=0, max_q=0), Q=None, table=None, lens=None, O=None, ws=None, n=0) == 0

@@ -281,20 +281,30 @@ __device__ __forceinline__ void pdl_begin() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// With cluster > 1, CTAs that are neighbours along x form clusters of that many.
 template <typename... Params, typename... Args>
-cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t st, Args &&...args) {
+cudaError_t launch_kernel_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, int cluster,
+                                  cudaStream_t st, Args &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t st, Args &&...args) {
+    return launch_kernel_cluster(kernel, grid, block, smem, 1, st, std::forward<Args>(args)...);
 }
 
 // ------------------------------------------------------------------------------------
@@ -452,6 +462,7 @@ struct PAttnPlan {
 };
 cudaError_t launch_page_attention(const PAttnPlan &p, cudaStream_t st);
 int page_attention_splits(const PAttnPlan &p);
+bool page_attention_parts(const PAttnPlan &p);  // whether they need a workspace
 
 // Entry-point helpers shared by the C ABI's translation units (qvg_api.cu).
 qvg_status device_info(int *num_sms);

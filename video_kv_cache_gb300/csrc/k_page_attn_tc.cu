@@ -32,7 +32,6 @@
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
 // product runs over the 16-key steps in sight, and the rest of the outer steps is zeroed.
 #include "page_attn.cuh"
-#include "tcgen.cuh"
 
 namespace qvg {
 
@@ -42,7 +41,6 @@ constexpr int kTcN = 128;                  // keys of a key tile
 constexpr uint32_t kHalf = kTcM * 128;     // 64 channels of 128 rows: 16 KB
 constexpr uint32_t kSlot = 2 * kHalf;      // a whole 16-bit tile: 32 KB
 constexpr uint32_t kRaw = kTcN * kD;       // a tile of 8-bit codes: 16 KB
-constexpr uint64_t kPageWaitNs = 2000000000ull;  // a wait in the pipeline gives up after this
 constexpr int kValueShift = 4;             // weights with values' scales over 2^e are held times 2^4
 constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
 
@@ -88,12 +86,6 @@ constexpr size_t tc_smem() {
     return bytes;
 }
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -160,22 +152,6 @@ __device__ __forceinline__ bool meet(int id, bool v) {
         : "r"((uint32_t)v), "r"(id), "n"(THREADS)
         : "memory");
     return r != 0u;
-}
-// Bounded wait on a phase: polls, and looks at the clock and the abort flag now and then.
-__device__ __forceinline__ bool page_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    if (mbar_try(bar, parity)) return true;
-    uint64_t t0 = 0;
-    for (uint32_t n = 1; n < kSpinLimit; n++) {
-        if (mbar_try(bar, parity)) return true;
-        if ((n & 63u) == 0u) {
-            if (*abort_flag) return false;
-            const uint64_t now = global_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kPageWaitNs) break;
-        }
-    }
-    *abort_flag = 1;
-    return false;
 }
 template <int REGS>
 __device__ __forceinline__ void regs_inc() {
@@ -748,23 +724,8 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
 }  // namespace
 
 cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
-    // the pool as rows of 128 channels; a box is a page's rows (of 64 channels in 16 bits)
-    const CUtensorMapDataType dt = !wide              ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : p.fmt == PF_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)(p.n_pages * p.H * p.page)};
-    const cuuint64_t strides[1] = {(cuuint64_t)(wide ? 2 * kD : kD)};
-    const cuuint32_t box[2] = {wide ? 64u : (cuuint32_t)kD, (cuuint32_t)p.page}, estr[2] = {1, 1};
     CUtensorMap maps[2];
-    const void *pools[2] = {p.k, p.v};
-    for (int x = 0; x < 2; x++)
-        if (enc(&maps[x], dt, 2, const_cast<void *>(pools[x]), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
+    if (!page_map(p, p.k, p.page, &maps[0]) || !page_map(p, p.v, p.page, &maps[1])) return cudaErrorInvalidValue;
     if (p.q_dtype == DT_BF16)
         return p.fmt == PF_E4M3   ? launch_tc<true, PF_E4M3>(p, maps[0], maps[1], st)
                : p.fmt == PF_INT8 ? launch_tc<true, PF_INT8>(p, maps[0], maps[1], st)

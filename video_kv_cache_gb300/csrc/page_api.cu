@@ -131,10 +131,11 @@ PAttnPlan attention_plan(const qvg_page_attention_params *prm) {
 
 // Workspace: the splits' partial rows, then their (maximum, sum) pairs.
 size_t attention_part_bytes(const PAttnPlan &p) {
-    return p.S > 1 ? (size_t)p.S * p.total_q * p.HQ * kD * sizeof(float) : 0;
+    return p.total_q && page_attention_parts(p) ? (size_t)p.S * p.total_q * p.HQ * kD * sizeof(float) : 0;
 }
 size_t attention_bytes(const PAttnPlan &p) {
-    return p.S > 1 ? attention_part_bytes(p) + (size_t)p.S * p.total_q * p.HQ * 2 * sizeof(float) : 0;
+    const size_t part = attention_part_bytes(p);
+    return part ? part + (size_t)p.S * p.total_q * p.HQ * 2 * sizeof(float) : 0;
 }
 
 // Checks that come after the arguments': the injected failure, the device.

@@ -4,6 +4,7 @@
 
 #include "page_codes.cuh"
 #include "rows.cuh"
+#include "tcgen.cuh"
 
 namespace qvg {
 
@@ -134,10 +135,51 @@ __device__ __forceinline__ float row_lse(float m, float l) {
     return l > 0.f ? (m + fast_log2(l)) * kLn2 : (l == 0.f ? -INFINITY : l);  // NaN stays NaN
 }
 
+// Bounded wait on a phase: polls, and looks at the clock and the abort flag now and then.
+constexpr uint64_t kPageWaitNs = 2000000000ull;  // a wait in the pipeline gives up after this
+__device__ __forceinline__ bool page_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (mbar_try(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; n < kSpinLimit; n++) {
+        if (mbar_try(bar, parity)) return true;
+        if ((n & 63u) == 0u) {
+            if (*abort_flag) return false;
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kPageWaitNs) break;
+        }
+    }
+    *abort_flag = 1;
+    return false;
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// The pool as rows of 128 channels, in boxes of `rows` rows that are 128 bytes wide (of a row
+// of 8-bit codes, or of 64 channels in 16 bits), swizzled.
+inline bool page_map(const PAttnPlan &p, const void *pool, int rows, CUtensorMap *map) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
+    const CUtensorMapDataType dt = !wide              ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : p.fmt == PF_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)(p.n_pages * p.H * p.page)};
+    const cuuint64_t strides[1] = {(cuuint64_t)(wide ? 2 * kD : kD)};
+    const cuuint32_t box[2] = {wide ? 64u : (cuuint32_t)kD, (cuuint32_t)rows}, estr[2] = {1, 1};
+    return enc(map, dt, 2, const_cast<void *>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Up to this many query rows (tokens x grouped heads) a sequence, attention is bound by reading
-// the cache and runs on warp-level instructions; above, on the tensor cores.
-constexpr int kRowsMost = 16;
-cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st);
+// the cache and runs on warp-level instructions (k_page_attn_rows.cu); above, on the tensor
+// cores' own (k_page_attn_tc.cu).
+constexpr int kRowsM = 16;
 cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st);
 
 }  // namespace qvg
