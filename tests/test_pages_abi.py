@@ -189,7 +189,7 @@ def test_page_attention_refusals(lib, mem, monkeypatch):
     # long keys and few rows: the keys are split many ways, which needs workspace
     long = _attention(n_seqs=1, total_q=3, n_pages=2000, max_pages=1250, max_kv=20000)
     need = qvg.qvg_page_attention_workspace_bytes(long)
-    rows = 3 * 4
+    rows = 2 * 16  # a 16-row tile of either key/value head, for each split
     assert need > 0 and need % (rows * (128 + 2) * 4) == 0
     assert call(long, n=need - 1) == call(long, ws=None) == call(long, ws=mem + 4) == qvg.QVG_ERR_WORKSPACE
     assert call(_attention(total_q=0, max_q=0), Q=None, table=None, lens=None, O=None, ws=None, n=0) == 0

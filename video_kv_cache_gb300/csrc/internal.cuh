@@ -455,14 +455,18 @@ struct PAttnPlan {
     const int32_t *table, *lens, *cu;
     void *O;
     float *lse;
-    int S;        // splits of each row tile's keys
-    float *part;  // [S][total_q * HQ][128] partial outputs, relative to their maximum
-    float *ml;    // [S][total_q * HQ][2] running maximum (log2) and weight sum
+    // How the work is cut: items of `unit` query rows of one key/value head, `units` of them for
+    // max_q tokens, the longest first.  The first `whole` items are a CTA each; the others' keys
+    // are split S ways, a CTA each, and joined.
+    int unit, units, S;
+    int64_t whole;
+    float *part;  // [items that are split][S][unit][128] partial outputs, relative to their maximum
+    float *ml;    // [..][S][unit][2] running maximum (log2) and weight sum
     uint32_t *status;
 };
 cudaError_t launch_page_attention(const PAttnPlan &p, cudaStream_t st);
-int page_attention_splits(const PAttnPlan &p);
-bool page_attention_parts(const PAttnPlan &p);  // whether they need a workspace
+void page_attention_cut(PAttnPlan &p);
+int64_t page_attention_part_rows(const PAttnPlan &p);  // rows of partial results in the workspace
 
 // Entry-point helpers shared by the C ABI's translation units (qvg_api.cu).
 qvg_status device_info(int *num_sms);

@@ -4,17 +4,21 @@
 //
 // Bound by memory: every cached byte is read once per key/value head and used for all rows
 // (query tokens x grouped query heads, at most 16).  One warp of a CTA streams the keys' and
-// values' pages by TMA into a ring of 64-key stages (about 100 KB in flight a CTA, two CTAs an
-// SM: several times what the memory's latency needs); four warps take a 16-key tile of each
+// values' pages by TMA into a ring of stages of 64 or 128 keys (about 100 KB in flight a CTA, two
+// CTAs an SM: several times what the memory's latency needs); four warps take a quarter of each
 // stage, with a running maximum and weight sum per row, on warp-level matrix instructions:
-//   * scores: a dot product may take its channels in any order, so lane (g, q) = (lane / 4,
-//     lane % 4) reads 16-byte chunks q, q + 4, ... of key g's row and feeds them to successive
+//   * scores S^T = K Q^T: the keys are the product's 16 rows and the queries its columns, eight
+//     at a time, so that one or two grouped heads' worth of rows wastes little.  A dot product
+//     may take its channels in any order, so lane (g, q) = (lane / 4, lane % 4) reads 16-byte
+//     chunks q, q + 4, ... of the rows of keys g and g + 8 and feeds them to successive
 //     16-channel steps; Q is held in the same order.
-//   * values: output channels may be numbered in any order, so column g of product tile t is
-//     channel 8g + t (16g + t for 8-bit codes): lane (g, q) reads whole chunks of keys 2q,
-//     2q + 1, 2q + 8 and 2q + 9, pairs them up by byte permutations, and ends with whole runs
-//     of channels to write.  The stages are swizzled (128 bytes), which keeps these reads off
-//     each other's banks.
+//   * outputs O^T = V^T P^T: the weights turn from the scores' layout into an operand's by one
+//     8 x 8 transposition instruction each.  Output channels may be numbered in any order, so
+//     row g of product tile t is channel 8g + t and row g + 8 channel 64 + 8g + t (8-bit codes:
+//     16g + t and 16g + 8 + t): lane (g, q) reads whole chunks of keys 2q, 2q + 1, 2q + 8 and
+//     2q + 9, pairs them up by byte permutations, and ends with whole runs of channels to
+//     write.  The stages are swizzled (128 bytes), which keeps these reads off each other's
+//     banks.
 // The keys are cut into S splits, a CTA each.  The warps' results are joined in shared memory;
 // the splits', where there are at most eight, by a cluster of the S CTAs through each other's
 // shared memory (one launch, no workspace), else through memory by k_page_combine.
@@ -26,31 +30,38 @@ namespace qvg {
 namespace {
 constexpr int kRowsWarps = 4;              // warps that compute
 constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
-constexpr int kStageKeys = 16 * kRowsWarps;
 constexpr int kRowsPad = 132;              // padded row of the join, floats
 constexpr int kRowsCluster = 8;            // most splits joined by a cluster
 
-template <int FMT>
+// RT: groups of eight query rows, one or two.
+template <int FMT, int RT>
 struct RowsShape {
     static constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
-    static constexpr int STAGES = WIDE ? 3 : 6;
-    static constexpr uint32_t TILE = kStageKeys * kD * (WIDE ? 2 : 1);  // keys or values of a stage
+    // 16-key tiles that a warp takes at a time: widening codes is a chain of short
+    // instructions, which needs more of them side by side than feeding 16-bit rows does
+    static constexpr int KT = WIDE ? 1 : 2;
+    static constexpr int KEYS = 16 * KT * kRowsWarps;              // of a stage
+    static constexpr int CTAS = 2;    // an SM
+    static constexpr int STAGES = 3;  // 32 KB each; two stages and three CTAs, or smaller stages, are slower
+    static constexpr uint32_t TILE = KEYS * kD * (WIDE ? 2 : 1);   // bytes of its keys, or values
 };
-template <int FMT>
+template <int FMT, int RT>
 struct RowsShared {
-    float ks[RowsShape<FMT>::STAGES][RowsShape<FMT>::WIDE ? 4 : kStageKeys];
-    float vs[RowsShape<FMT>::STAGES][RowsShape<FMT>::WIDE ? 4 : kStageKeys];
-    uint64_t full[RowsShape<FMT>::STAGES], empty[RowsShape<FMT>::STAGES];
-    float m[kRowsWarps][kRowsM], l[kRowsWarps][kRowsM];
-    float2 ml[kRowsM];  // this split's maximum and sum, for the cluster
+    using T = RowsShape<FMT, RT>;
+    __align__(16) float ks[T::STAGES][T::WIDE ? 4 : T::KEYS];
+    __align__(16) float vs[T::STAGES][T::WIDE ? 4 : T::KEYS];
+    uint64_t full[T::STAGES], empty[T::STAGES];
+    float m[kRowsWarps][8 * RT], l[kRowsWarps][8 * RT];
+    float2 ml[8 * RT];  // this split's maxima and sums, for the cluster
     int abort;
 };
 // The join's rows take the ring's place once the keys are through.
-template <int FMT>
+template <int FMT, int RT>
 constexpr size_t rows_smem() {
-    constexpr size_t bytes = RowsShape<FMT>::STAGES * 2 * RowsShape<FMT>::TILE + sizeof(RowsShared<FMT>);
-    static_assert(2 * (bytes + 1024) <= 228 * 1024, "two CTAs an SM");
-    static_assert((kRowsWarps + 1) * kRowsM * kRowsPad * 4 <= RowsShape<FMT>::STAGES * 2 * RowsShape<FMT>::TILE, "join");
+    using T = RowsShape<FMT, RT>;
+    constexpr size_t bytes = T::STAGES * 2 * T::TILE + sizeof(RowsShared<FMT, RT>);
+    static_assert(T::CTAS * (bytes + 1024) <= 228 * 1024, "CTAs of an SM");
+    static_assert((kRowsWarps + 1) * 8 * RT * kRowsPad * 4 <= T::STAGES * 2 * T::TILE, "join");
     return bytes;
 }
 
@@ -68,6 +79,12 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
             "{%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The 8 x 8 matrix of 16-bit values whose row g lane 4g .. 4g + 3 hold in pairs, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
 }
 __device__ __forceinline__ uint32_t word_of(const uint4 &v, int w) {
     return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
@@ -95,20 +112,20 @@ __device__ __forceinline__ void cluster_meet() {
 
 // grid (splits, key/value heads, sequences).  QB: bf16 queries; FMT: the page format, the
 // 16-bit ones (PF_F16 / PF_BF16) equal to the query's type.  joined: the splits are a cluster.
-template <bool QB, int FMT>
-__global__ void __launch_bounds__(kRowsThreads, 2)
+template <bool QB, int FMT, int RT>
+__global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
     k_page_attn_rows(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PAttnPlan p, int joined) {
     pdl_begin();
-    using T = RowsShape<FMT>;
+    using T = RowsShape<FMT, RT>;
     constexpr bool WIDE = T::WIDE;
     constexpr bool PVB = WIDE && QB;            // type of all operands; 8-bit pages: fp16
     constexpr int ROWB = WIDE ? 2 * kD : kD;    // bytes of a cached row
     constexpr int NCH = ROWB / 64;              // 16-byte chunks of a row per lane
-    constexpr int STAGES = T::STAGES;
+    constexpr int STAGES = T::STAGES, KT = T::KT, KEYS = T::KEYS, ROWS = 8 * RT;
     extern __shared__ __align__(1024) unsigned char sm[];
-    RowsShared<FMT> &sh = *reinterpret_cast<RowsShared<FMT> *>(sm + STAGES * 2 * T::TILE);
-    float(*s_o)[kRowsM][kRowsPad] = reinterpret_cast<float(*)[kRowsM][kRowsPad]>(sm);
+    RowsShared<FMT, RT> &sh = *reinterpret_cast<RowsShared<FMT, RT> *>(sm + STAGES * 2 * T::TILE);
+    float(*s_o)[ROWS][kRowsPad] = reinterpret_cast<float(*)[ROWS][kRowsPad]>(sm);
     volatile int *abort_flag = &sh.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -117,11 +134,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     if (rows == 0) return;
     const int shift = 31 - __clz(p.page);
 
-    // what the rows see, this split's share of it, in stages of 64 keys
+    // what the rows see, this split's share of it, in stages
     const int lo = seen_lo(p, sq, 0), hi = seen_hi(p, sq, sq.qn - 1);
     int first = 0, n = 0;
     if (lo < hi) {
-        const int s_lo = lo / kStageKeys, all = (hi + kStageKeys - 1) / kStageKeys - s_lo, per = (all + p.S - 1) / p.S;
+        const int s_lo = lo / KEYS, all = (hi + KEYS - 1) / KEYS - s_lo, per = (all + p.S - 1) / p.S;
         first = s_lo + split * per;
         n = max(0, min(per, all - split * per));
     }
@@ -135,11 +152,18 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     }
     __syncthreads();
 
-    float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[RT][8][4], m[RT][2], l[RT][2];
+#pragma unroll
+    for (int y = 0; y < RT; y++) {
+        m[y][0] = m[y][1] = -INFINITY;
+        l[y][0] = l[y][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 8; t++) o[y][t][0] = o[y][t][1] = o[y][t][2] = o[y][t][3] = 0.f;
+    }
     int vexp = -100;  // exponent of the reference that the values' scales are taken against
     if (warp == kRowsWarps) {
         // -------------------------------------------------------------------- TMA loads
-        const int box = min(p.page, kStageKeys), boxes = kStageKeys / box;
+        const int box = min(p.page, KEYS), boxes = KEYS / box;
         bool bad = false, ok = true;
         int issued = 0;
         // the boxes of a stage that hold a key some row sees, a lane each; their pages are
@@ -153,10 +177,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
             if (!in_sight(k0)) return 0;
             return (int)(((page_of(p, b, token, shift, bad) * p.H + h) << shift) + (token & (p.page - 1)));
         };
-        int next = n > 0 ? row_of(first * kStageKeys) : 0;
+        int next = n > 0 ? row_of(first * KEYS) : 0;
         for (int it = 0; it < n; it++) {
-            const int k0 = (first + it) * kStageKeys, s = it % STAGES, row = next;
-            if (it + 1 < n) next = row_of(k0 + kStageKeys);
+            const int k0 = (first + it) * KEYS, s = it % STAGES, row = next;
+            if (it + 1 < n) next = row_of(k0 + KEYS);
             ok = page_wait(smem_u32(&sh.empty[s]), (it / STAGES + 1) & 1, abort_flag);
             if (__any_sync(0xffffffffu, !ok)) break;
             const uint32_t bar = smem_u32(&sh.full[s]), count = __popc(__ballot_sync(0xffffffffu, in_sight(k0)));
@@ -182,16 +206,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
             mbar_wait_final(smem_u32(&sh.full[it % STAGES]), (it / STAGES) & 1);
     } else {
         // -------------------------------------------------------------------- attention
-        // the two rows whose scores this lane holds
-        int row_lo[2], row_hi[2];
-        // Q in the order the keys' chunks come in
-        uint32_t qa[8][4];
-        float qmul[2] = {1.f, 1.f};  // 8-bit pages: powers of two taken out of the rows of Q
+        // Q in the order the keys' chunks come in: lane (g, q) holds row g of each group
+        uint32_t qb[RT][8][2];
+        float qmul[RT][2];  // 8-bit pages: powers of two taken out of the rows whose scores this lane has
+        int row_lo[RT][2], row_hi[RT][2];
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
-            const int r = g + 8 * x, i = min(r, rows - 1) / p.G;
-            row_lo[x] = seen_lo(p, sq, i);
-            row_hi[x] = seen_hi(p, sq, i);
+        for (int y = 0; y < RT; y++) {
+            const int r = 8 * y + g, i = min(r, rows - 1) / p.G;
             const uint16_t *src = static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt + (int64_t)(h * p.G + r - i * p.G) * p.qh;
             uint4 w[4];
 #pragma unroll
@@ -199,14 +220,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
                 const int ch = WIDE ? (j * 4 + q) * 8 : ((j >> 1) * 4 + q) * 16 + (j & 1) * 8;
                 w[j] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch)) : make_uint4(0u, 0u, 0u, 0u);
             }
+            float mul = 1.f;
             if constexpr (!WIDE && QB) {
                 uint32_t big = 0;
 #pragma unroll
                 for (int j = 0; j < 4; j++) big = max(big, bf16x2_max_bits(w[j]));
                 big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
                 big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                qmul[x] = bf16_pow2(big);
-                const float inv = 1.f / qmul[x];
+                mul = bf16_pow2(big);
+                const float inv = 1.f / mul;
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     w[j] = make_uint4(bf16x2_to_f16x2(w[j].x, inv), bf16x2_to_f16x2(w[j].y, inv),
@@ -214,167 +236,203 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
             }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                qa[2 * j][x] = w[j].x;
-                qa[2 * j][2 + x] = w[j].y;
-                qa[2 * j + 1][x] = w[j].z;
-                qa[2 * j + 1][2 + x] = w[j].w;
+                qb[y][2 * j][0] = w[j].x;
+                qb[y][2 * j][1] = w[j].y;
+                qb[y][2 * j + 1][0] = w[j].z;
+                qb[y][2 * j + 1][1] = w[j].w;
+            }
+            // the scores' columns of this lane are rows 2q and 2q + 1
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                qmul[y][x] = __shfl_sync(0xffffffffu, mul, (2 * q + x) * 4) * p.scale_log2;
+                const int i = min(8 * y + 2 * q + x, rows - 1) / p.G;
+                row_lo[y][x] = seen_lo(p, sq, i);
+                row_hi[y][x] = seen_hi(p, sq, i);
             }
         }
-#pragma unroll
-        for (int t = 0; t < 16; t++) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 
-        // chunk c of row r of a swizzled tile of `rows of 128 bytes` (16 bits: two halves)
+        // chunk c of row r of a swizzled tile (16 bits: two halves of 128-byte rows)
         auto chunk = [](const unsigned char *tile, int r, int c) {
             return *reinterpret_cast<const uint4 *>(tile + (c >> 3) * (T::TILE / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
         };
         for (int it = 0; it < n; it++) {
-            const int st = it % STAGES, t0 = (first + it) * kStageKeys + warp * 16;  // this warp's first key
+            const int st = it % STAGES, w0 = warp * 16 * KT, t0 = (first + it) * KEYS + w0;  // this warp's first key
             const bool ok = page_wait(smem_u32(&sh.full[st]), (it / STAGES) & 1, abort_flag);
             if (__any_sync(0xffffffffu, !ok)) break;
-            if (t0 < hi && t0 + 16 > lo) {
+            if (t0 < hi && t0 + 16 * KT > lo) {
                 const unsigned char *kt = sm + st * 2 * T::TILE, *vt = kt + T::TILE;
-                float s[2][4] = {};
+                // s[z][y][..]: keys t0 + 16 z + g (0, 1) and + 8 (2, 3), rows 8 y + 2 q, + 1
+                float s[KT][RT][4] = {};
 #pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    uint4 kr[NCH];
+                for (int c = 0; c < NCH; c++) {
 #pragma unroll
-                    for (int c = 0; c < NCH; c++) kr[c] = chunk(kt, warp * 16 + u * 8 + g, c * 4 + q);
-#pragma unroll
-                    for (int c = 0; c < NCH; c++) {
+                    for (int z = 0; z < KT; z++) {
+                        const uint4 ka = chunk(kt, w0 + z * 16 + g, c * 4 + q), kb = chunk(kt, w0 + z * 16 + g + 8, c * 4 + q);
                         if constexpr (WIDE) {
-                            mma16816<QB>(s[u], qa[2 * c], kr[c].x, kr[c].y);
-                            mma16816<QB>(s[u], qa[2 * c + 1], kr[c].z, kr[c].w);
+                            const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
+#pragma unroll
+                            for (int y = 0; y < RT; y++) {
+                                mma16816<QB>(s[z][y], a0, qb[y][2 * c][0], qb[y][2 * c][1]);
+                                mma16816<QB>(s[z][y], a1, qb[y][2 * c + 1][0], qb[y][2 * c + 1][1]);
+                            }
                         } else {
 #pragma unroll
                             for (int w = 0; w < 4; w++) {
-                                const uint2 k2 = codes_to_f16<FMT == PF_E4M3>(word_of(kr[c], w));
-                                mma16816<false>(s[u], qa[4 * c + w], k2.x, k2.y);
+                                const uint2 ua = codes_to_f16<FMT == PF_E4M3>(word_of(ka, w)), ub = codes_to_f16<FMT == PF_E4M3>(word_of(kb, w));
+                                const uint32_t a[4] = {ua.x, ub.x, ua.y, ub.y};
+#pragma unroll
+                                for (int y = 0; y < RT; y++) mma16816<false>(s[z][y], a, qb[y][4 * c + w][0], qb[y][4 * c + w][1]);
                             }
                         }
                     }
                 }
-                // the values are on their way to registers during the softmax
-                uint4 vr[4][NCH / 2];
+                const bool edge = t0 < lo || t0 + 16 * KT > hi;
+                float vsc[KT][2];
 #pragma unroll
-                for (int k = 0; k < 4; k++)
-#pragma unroll
-                    for (int c = 0; c < NCH / 2; c++)
-                        vr[k][c] = chunk(vt, warp * 16 + 2 * q + (k & 1) + (k >> 1) * 8, c * 8 + g);
-                // columns 8u + 2q, + 1 of rows g, g + 8
-                const int key0 = t0 + 2 * q;
-                const bool edge = t0 < lo || t0 + 16 > hi;
-                float vsc[4];
-#pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    float2 f = make_float2(p.scale_log2, p.scale_log2);
+                for (int z = 0; z < KT; z++) {
+                    float k2[2] = {1.f, 1.f};
                     if constexpr (!WIDE) {
-                        const float2 k2 = *reinterpret_cast<const float2 *>(&sh.ks[st][warp * 16 + 8 * u + 2 * q]);
-                        const float2 v2 = *reinterpret_cast<const float2 *>(&sh.vs[st][warp * 16 + 8 * u + 2 * q]);
-                        f.x *= k2.x;
-                        f.y *= k2.y;
-                        vsc[2 * u] = v2.x;
-                        vsc[2 * u + 1] = v2.y;
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            k2[e] = sh.ks[st][w0 + 16 * z + 8 * e + g];
+                            vsc[z][e] = sh.vs[st][w0 + 16 * z + 8 * e + g];
+                        }
                     }
-                    s[u][0] *= f.x * qmul[0];
-                    s[u][1] *= f.y * qmul[0];
-                    s[u][2] *= f.x * qmul[1];
-                    s[u][3] *= f.y * qmul[1];
+#pragma unroll
+                    for (int y = 0; y < RT; y++) {
+                        s[z][y][0] *= qmul[y][0] * k2[0];
+                        s[z][y][1] *= qmul[y][1] * k2[0];
+                        s[z][y][2] *= qmul[y][0] * k2[1];
+                        s[z][y][3] *= qmul[y][1] * k2[1];
+                    }
                     if (edge || sq.qn > 1) {
 #pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const int key = key0 + 8 * u + (e & 1), x = e >> 1;
-                            if (key < row_lo[x] || key >= row_hi[x]) s[u][e] = -INFINITY;
-                        }
+                        for (int y = 0; y < RT; y++)
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const int key = t0 + 16 * z + 8 * (e >> 1) + g;
+                                if (key < row_lo[y][e & 1] || key >= row_hi[y][e & 1]) s[z][y][e] = -INFINITY;
+                            }
                     }
                 }
                 // 8-bit: the weights take in the values' scales relative to 2^vexp, an exponent
                 // that follows the largest scale seen; times 2^8 they fill fp16's range
-                float vmul = 0.f, vcorr = 1.f;
+                float vcorr = 1.f;
                 if constexpr (!WIDE) {
                     float big = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const int key = key0 + (k & 1) + (k >> 1) * 8;
-                        if (key >= lo && key < hi) big = fmaxf(big, fabsf(vsc[k]));
-                    }
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    for (int z = 0; z < KT; z++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int key = t0 + 16 * z + 8 * e + g;
+                            if (!edge || (key >= lo && key < hi)) big = fmaxf(big, fabsf(vsc[z][e]));
+                        }
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
                     const int ve = max(vexp, min((int)(__float_as_uint(big) >> 23) - 127, 121));
                     vcorr = __uint_as_float((uint32_t)max(127 + vexp - ve, 0) << 23);
-                    vmul = __uint_as_float((uint32_t)(127 + 8 - ve) << 23);
+                    const float vmul = __uint_as_float((uint32_t)(127 + 8 - ve) << 23);
+#pragma unroll
+                    for (int z = 0; z < KT; z++) {
+                        vsc[z][0] *= vmul;
+                        vsc[z][1] *= vmul;
+                    }
                     vexp = ve;
                 }
-                float corr[2];
-                uint32_t pa[4];
+                uint32_t pb[KT][RT][2];
 #pragma unroll
-                for (int x = 0; x < 2; x++) {
-                    float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    mx = fmaxf(m[x], mx);
-                    const float base = exp_base(mx);
-                    corr[x] = fast_exp2(m[x] - base);
-                    m[x] = mx;
-                    float sum = 0.f;
+                for (int y = 0; y < RT; y++) {
+                    float corr[2], base[2], sum[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        float w0 = fast_exp2(s[u][2 * x] - base), w1 = fast_exp2(s[u][2 * x + 1] - base);
-                        sum += w0 + w1;
-                        if constexpr (!WIDE) {  // a hidden key's scale may be NaN: its weight stays 0
-                            w0 = s[u][2 * x] == -INFINITY ? 0.f : w0 * (vsc[2 * u] * vmul);
-                            w1 = s[u][2 * x + 1] == -INFINITY ? 0.f : w1 * (vsc[2 * u + 1] * vmul);
+                    for (int x = 0; x < 2; x++) {
+                        float mx = m[y][x];
+#pragma unroll
+                        for (int z = 0; z < KT; z++) mx = fmax3(mx, s[z][y][x], s[z][y][2 + x]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        base[x] = exp_base(mx);
+                        corr[x] = fast_exp2(m[y][x] - base[x]);
+                        m[y][x] = mx;
+                    }
+#pragma unroll
+                    for (int z = 0; z < KT; z++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            float w0 = fast_exp2(s[z][y][2 * e] - base[0]), w1 = fast_exp2(s[z][y][2 * e + 1] - base[1]);
+                            sum[0] += w0;
+                            sum[1] += w1;
+                            if constexpr (!WIDE) {
+                                w0 *= vsc[z][e];
+                                w1 *= vsc[z][e];
+                                if (edge || sq.qn > 1) {  // a hidden key's scale may be NaN: its weight stays 0
+                                    if (s[z][y][2 * e] == -INFINITY) w0 = 0.f;
+                                    if (s[z][y][2 * e + 1] == -INFINITY) w1 = 0.f;
+                                }
+                            }
+                            pb[z][y][e] = transpose8x8(PVB ? pack_bf16(w0, w1) : pack_f16(w0, w1));
                         }
-                        pa[2 * u + x] = PVB ? pack_bf16(w0, w1) : pack_f16(w0, w1);
-                    }
-                    l[x] = l[x] * corr[x] + sum;
-                }
-                if constexpr (!WIDE) {
-                    corr[0] *= vcorr;
-                    corr[1] *= vcorr;
-                }
-                if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
-                    for (int k = 0; k < 16; k++) {
-                        o[k][0] *= corr[0];
-                        o[k][1] *= corr[0];
-                        o[k][2] *= corr[1];
-                        o[k][3] *= corr[1];
+                    for (int x = 0; x < 2; x++) {
+                        l[y][x] = l[y][x] * corr[x] + sum[x];
+                        corr[x] *= vcorr;
+                    }
+                    if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+                        for (int t = 0; t < 8; t++) {
+                            o[y][t][0] *= corr[0];
+                            o[y][t][1] *= corr[1];
+                            o[y][t][2] *= corr[0];
+                            o[y][t][3] *= corr[1];
+                        }
                     }
                 }
-                // values that no row sees may hold anything
-                if (edge) {
+#pragma unroll
+                for (int z = 0; z < KT; z++) {
+                    uint4 vr[4][NCH / 2];  // keys 2q, 2q + 1, 2q + 8, 2q + 9
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        const int key = key0 + (k & 1) + (k >> 1) * 8;
-                        if (key < lo || key >= hi)
+                        const int at = 16 * z + 2 * q + (k & 1) + (k >> 1) * 8;
 #pragma unroll
-                            for (int c = 0; c < NCH / 2; c++) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
-                if constexpr (WIDE) {
-#pragma unroll
-                    for (int c = 0; c < 2; c++)
-#pragma unroll
-                        for (int w = 0; w < 4; w++) {
-                            const uint32_t v0 = word_of(vr[0][c], w), v1 = word_of(vr[1][c], w),
-                                           v2 = word_of(vr[2][c], w), v3 = word_of(vr[3][c], w);
-                            mma16816<PVB>(o[c * 8 + 2 * w], pa, __byte_perm(v0, v1, 0x5410), __byte_perm(v2, v3, 0x5410));
-                            mma16816<PVB>(o[c * 8 + 2 * w + 1], pa, __byte_perm(v0, v1, 0x7632), __byte_perm(v2, v3, 0x7632));
+                        for (int c = 0; c < NCH / 2; c++) {
+                            vr[k][c] = chunk(vt, w0 + at, c * 8 + g);
+                            // values that no row sees may hold anything
+                            if (edge && (t0 + at < lo || t0 + at >= hi)) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
                         }
-                } else {
+                    }
+                    if constexpr (WIDE) {
 #pragma unroll
-                    for (int w = 0; w < 4; w++) {
-                        // the codes of two keys interleaved, then widened pair by pair
-                        const uint32_t v0 = word_of(vr[0][0], w), v1 = word_of(vr[1][0], w),
-                                       v2 = word_of(vr[2][0], w), v3 = word_of(vr[3][0], w);
-                        const uint2 a = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x5140)),
-                                    c = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x7362)),
-                                    d = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v2, v3, 0x5140)),
-                                    e = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v2, v3, 0x7362));
-                        mma16816<false>(o[4 * w], pa, a.x, d.x);
-                        mma16816<false>(o[4 * w + 1], pa, a.y, d.y);
-                        mma16816<false>(o[4 * w + 2], pa, c.x, e.x);
-                        mma16816<false>(o[4 * w + 3], pa, c.y, e.y);
+                        for (int t = 0; t < 8; t++) {
+                            const int w = t >> 1, sel = t & 1 ? 0x7632 : 0x5410;
+                            const uint32_t a[4] = {__byte_perm(word_of(vr[0][0], w), word_of(vr[1][0], w), sel),
+                                                   __byte_perm(word_of(vr[0][1], w), word_of(vr[1][1], w), sel),
+                                                   __byte_perm(word_of(vr[2][0], w), word_of(vr[3][0], w), sel),
+                                                   __byte_perm(word_of(vr[2][1], w), word_of(vr[3][1], w), sel)};
+#pragma unroll
+                            for (int y = 0; y < RT; y++) mma16816<PVB>(o[y][t], a, pb[z][y][0], pb[z][y][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 2; w++) {
+                            // the codes of two keys interleaved, then widened pair by pair:
+                            // channels 4w .. 4w + 3 of the first and of the last eight
+                            uint2 a[2][2][2];  // [first / last eight][keys 2q.. / 2q + 8..][channels 0, 1 / 2, 3]
+#pragma unroll
+                            for (int e = 0; e < 2; e++)
+#pragma unroll
+                                for (int k = 0; k < 2; k++) {
+                                    const uint32_t v0 = word_of(vr[2 * k][0], w + 2 * e), v1 = word_of(vr[2 * k + 1][0], w + 2 * e);
+                                    a[e][k][0] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x5140));
+                                    a[e][k][1] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x7362));
+                                }
+#pragma unroll
+                            for (int t = 0; t < 4; t++) {
+                                const int x = t >> 1;
+                                const uint32_t f[4] = {t & 1 ? a[0][0][x].y : a[0][0][x].x, t & 1 ? a[1][0][x].y : a[1][0][x].x,
+                                                       t & 1 ? a[0][1][x].y : a[0][1][x].x, t & 1 ? a[1][1][x].y : a[1][1][x].x};
+#pragma unroll
+                                for (int y = 0; y < RT; y++) mma16816<false>(o[y][4 * w + t], f, pb[z][y][0], pb[z][y][1]);
+                            }
+                        }
                     }
                 }
             }
@@ -389,29 +447,32 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     if (warp < kRowsWarps) {
         const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp - 8) << 23);
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-            if (q == 0) {
-                sh.m[warp][g + 8 * x] = m[x];
-                sh.l[warp][g + 8 * x] = l[x];
-            }
+        for (int y = 0; y < RT; y++)
 #pragma unroll
-            for (int k = 0; k < 16; k++)
+            for (int x = 0; x < 2; x++) {
+                const int r = 8 * y + 2 * q + x;
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int col = 2 * q + e;
-                    const int ch = WIDE ? (k >> 3) * 64 + col * 8 + (k & 7) : col * 16 + k;
-                    s_o[warp][g + 8 * x][ch] = o[k][2 * x + e] * unit;
+                for (int d = 4; d < 32; d <<= 1) l[y][x] += __shfl_xor_sync(0xffffffffu, l[y][x], d);
+                if (g == 0) {
+                    sh.m[warp][r] = m[y][x];
+                    sh.l[warp][r] = l[y][x];
                 }
-        }
+#pragma unroll
+                for (int e = 0; e < 2; e++) {  // eight channels each
+                    float *dst = &s_o[warp][r][WIDE ? 64 * e + 8 * g : 16 * g + 8 * e];
+                    *reinterpret_cast<float4 *>(dst) = make_float4(o[y][0][2 * e + x] * unit, o[y][1][2 * e + x] * unit,
+                                                                   o[y][2][2 * e + x] * unit, o[y][3][2 * e + x] * unit);
+                    *reinterpret_cast<float4 *>(dst + 4) = make_float4(o[y][4][2 * e + x] * unit, o[y][5][2 * e + x] * unit,
+                                                                       o[y][6][2 * e + x] * unit, o[y][7][2 * e + x] * unit);
+                }
+            }
     }
     __syncthreads();
     // eight lanes a row, 16 channels each (in runs of four, so that the lanes' reads and
-    // writes are next to one another); the fifth warp only keeps the barriers
+    // writes are next to one another); the other warps only keep the barriers
     const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
     float M = -INFINITY, L = 0.f, v[16] = {};
-    const bool mine = warp < kRowsWarps;
+    const bool mine = r < ROWS;
     if (mine) {
 #pragma unroll
         for (int w = 0; w < kRowsWarps; w++) M = fmaxf(M, sh.m[w][r]);
@@ -428,7 +489,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     bool live = mine && r < rows;
     if (p.S > 1 && !joined) {
         if (!live) return;
-        const int64_t at = ((int64_t)split * p.total_q + sq.q0 + row_i) * p.HQ + hq;
+        const int64_t at = (((int64_t)b * p.H + h) * p.S + split) * kRowsM + r;
 #pragma unroll
         for (int c = 0; c < 4; c++) store4<DT_F32>(p.part, at * kD + c * 32 + part * 4, v + 4 * c);
         if (part == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = make_float2(M, L);
@@ -501,32 +562,22 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     if (p.lse && part == 0) p.lse[(sq.q0 + row_i) * p.HQ + hq] = row_lse(M, L);
 }
 
-// One warp per query row (of all sequences): the splits' partial rows rescaled to the largest
-// maximum and summed.  Lane l writes channels 4l .. 4l+3.  Rows of no sequence are skipped.
+// One warp per row of the items that were split: the splits' partial rows rescaled to the
+// largest maximum and summed.  Lane l writes channels 4l .. 4l+3.
 __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
     pdl_begin();
     const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (w >= p.total_q * p.HQ) return;
-    const int64_t token = w / p.HQ;
-    const int hq = (int)(w - token * p.HQ);
-    // the row's sequence: the last one that starts at or before it
-    int b;
-    if (p.cu) {
-        int a = 0, e = p.B;  // cu[a] <= token < cu[e], where the order of cu allows
-        while (e - a > 1) {
-            const int mid = (a + e) / 2;
-            if (__ldg(p.cu + mid) <= token) a = mid; else e = mid;
-        }
-        b = a;
-    } else {
-        b = (int)min(token / p.max_q, (int64_t)p.B - 1);
-    }
+    const int64_t cells = (int64_t)p.B * p.H, t = w / p.unit, item = p.whole + t;
+    if (item >= p.units * cells) return;
+    const int cell = (int)(item / p.units), u = (int)(item - (int64_t)cell * p.units), b = cell / p.H, h = cell - b * p.H;
+    const int local = (int)(w - t * p.unit), r = (p.units - 1 - u) * p.unit + local;
     const SeqInfo sq = seq_info(p, b, false);
-    if (token < sq.q0 || token >= sq.q0 + sq.qn) return;
-    const int64_t stride = p.total_q * p.HQ;
+    if (r >= sq.qn * p.G) return;
+    const int i = r / p.G, hq = h * p.G + r - i * p.G;
+    const int64_t at = t * p.S * p.unit + local;  // + split * unit
     float mx = -INFINITY;
-    for (int s = lane; s < p.S; s += 32) mx = fmaxf(mx, p.ml[2 * (s * stride + w)]);
+    for (int s = lane; s < p.S; s += 32) mx = fmaxf(mx, p.ml[2 * (at + s * p.unit)]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
     const float base = exp_base(mx);
@@ -536,69 +587,88 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
         float2 ml[SB];
         float4 po[SB];
 #pragma unroll
-        for (int u = 0; u < SB; u++)
-            if (s0 + u < p.S) {
-                const int64_t at = (s0 + u) * stride + w;
-                ml[u] = *reinterpret_cast<const float2 *>(p.ml + 2 * at);
-                po[u] = *reinterpret_cast<const float4 *>(p.part + at * kD + 4 * lane);
+        for (int k = 0; k < SB; k++)
+            if (s0 + k < p.S) {
+                const int64_t x = at + (s0 + k) * p.unit;
+                ml[k] = *reinterpret_cast<const float2 *>(p.ml + 2 * x);
+                po[k] = *reinterpret_cast<const float4 *>(p.part + x * kD + 4 * lane);
             }
 #pragma unroll
-        for (int u = 0; u < SB; u++)
-            if (s0 + u < p.S) {
-                const float f = fast_exp2(ml[u].x - base);
-                l += f * ml[u].y;
-                o[0] += f * po[u].x;
-                o[1] += f * po[u].y;
-                o[2] += f * po[u].z;
-                o[3] += f * po[u].w;
+        for (int k = 0; k < SB; k++)
+            if (s0 + k < p.S) {
+                const float f = fast_exp2(ml[k].x - base);
+                l += f * ml[k].y;
+                o[0] += f * po[k].x;
+                o[1] += f * po[k].y;
+                o[2] += f * po[k].z;
+                o[3] += f * po[k].w;
             }
     }
     if (redo_possible(p) &&
         __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3])))
-        redo_row(p, b, (int)(token - sq.q0), hq, o, mx, l);
+        redo_row(p, b, i, hq, o, mx, l);
     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll
     for (int c = 0; c < 4; c++) o[c] *= inv;
-    store_out4(p, token * p.ot + hq * p.oh + 4 * lane, o);
-    if (p.lse && lane == 0) p.lse[token * p.HQ + hq] = row_lse(mx, l);
+    store_out4(p, (sq.q0 + i) * p.ot + hq * p.oh + 4 * lane, o);
+    if (p.lse && lane == 0) p.lse[(sq.q0 + i) * p.HQ + hq] = row_lse(mx, l);
 }
 
-// Splits of the keys.  Few rows: enough CTAs to give every SM two of them (what their shared
-// memory allows) about once, while each keeps at least four stages; not more than a cluster
-// joins unless twice as many are wanted.  Many rows: CTAs run one an SM, so the time is about
-// the number of rounds times the tiles of one CTA; the split that makes it least is taken,
-// counting a few tiles' worth of work for starting a CTA and for the partial results.
-int page_attention_splits(const PAttnPlan &p) {
+// How the work is cut.
+//   Few rows: one item a key/value head and sequence.  An SM holds two CTAs; where a cluster
+//   (up to eight) can join the splits, three times as many are made, so that sequences of
+//   different lengths even out; where more are needed to fill the SMs once, they join through
+//   memory.  A split keeps two stages at least.
+//   Many rows: items of 256 rows, a CTA an SM.  Whole items fill whole rounds of the SMs, and
+//   the last round's are split so that they fill it too: the split that takes the least time
+//   is chosen, counting six key tiles' worth of time to start a CTA and four more to join.
+//   (Splitting every item alike would write 57 MB of partial results for 4680 x 32760 x 12
+//   heads, one and a half rounds, instead of 19.)  Sequences with different numbers of queries
+//   leave items empty, and the last ones say nothing about the last round: there all items
+//   are split alike, if they are too few for one round.
+void page_attention_cut(PAttnPlan &p) {
     const int64_t rows = p.max_q * p.G, cells = (int64_t)p.H * p.B;
+    p.whole = 0;
     if (rows <= kRowsM) {
-        const int64_t want = (152 * 2 + cells - 1) / cells;
-        const int64_t most = (p.max_kv + kStageKeys * 4 - 1) / (kStageKeys * 4);
-        const int64_t s = std::max<int64_t>(1, std::min<int64_t>({want, most, 256}));
-        return (int)(s > kRowsCluster && s < 2 * kRowsCluster ? kRowsCluster : s);
+        p.unit = kRowsM;
+        p.units = 1;
+        const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = (152 * 2 + cells - 1) / cells;
+        const int64_t want = once < 2 * kRowsCluster ? std::min<int64_t>(kRowsCluster, 3 * 152 * 2 / cells) : std::min<int64_t>(once, 256);
+        p.S = (int)std::max<int64_t>(1, std::min(want, most));
+        return;
     }
-    const int64_t pairs = (rows + 255) / 256 * cells, tiles = (p.max_kv + 127) / 128;
-    int best = 1;
-    double least = 1e300;
-    for (int s = 1; s <= 64 && s <= std::max<int64_t>(1, tiles / 4); s++) {
-        const double rounds = (double)((pairs * s + 151) / 152);
-        const double t = rounds * ((double)((tiles + s - 1) / s) + 6.0) + (s > 1 ? 2.0 * s * pairs / 152 + 4.0 : 0.0);
-        if (t < least * 0.97) {
+    p.unit = 256;
+    p.units = (int)((rows + 255) / 256);
+    const int64_t items = p.units * cells, tiles = (p.max_kv + 127) / 128;
+    const bool alike = p.total_q == p.max_q * p.B;
+    const int64_t busy = alike ? items : std::min(items, p.total_q * p.G / 256 * p.H + cells);
+    const int64_t rest = alike ? items % 152 : busy < 152 ? busy : 0, rounds = alike ? items / 152 : 0;
+    p.whole = items;
+    p.S = 1;
+    double least = (double)((rounds + 1) * (tiles + 6));
+    for (int s = 2; rest && s <= 64 && s <= tiles / 4; s++) {
+        const double t = (double)(rounds * (tiles + 6)) +
+                         (double)((rest * s + 151) / 152) * ((double)((tiles + s - 1) / s) + 6.0) + 4.0;
+        if (t < least * 0.98) {
             least = t;
-            best = s;
+            p.S = s;
+            p.whole = alike ? items - rest : 0;
         }
     }
-    return best;
 }
-// Whether the splits go through memory (else there is one, or a cluster joins them).
-bool page_attention_parts(const PAttnPlan &p) {
-    return p.S > (p.max_q * p.G <= kRowsM ? kRowsCluster : 1);
+int64_t page_attention_part_rows(const PAttnPlan &p) {
+    if (p.S == 1 || (p.unit == kRowsM && p.S <= kRowsCluster)) return 0;
+    return ((int64_t)p.units * p.H * p.B - p.whole) * p.S * p.unit;
 }
 
 namespace {
-template <bool QB, int FMT>
-cudaError_t launch_rows(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
-    constexpr size_t smem = rows_smem<FMT>();
-    const auto kernel = k_page_attn_rows<QB, FMT>;
+template <bool QB, int FMT, int RT>
+cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
+    constexpr size_t smem = rows_smem<FMT, RT>();
+    const auto kernel = k_page_attn_rows<QB, FMT, RT>;
+    CUtensorMap mk, mv;
+    const int box = std::min(p.page, RowsShape<FMT, RT>::KEYS);
+    if (!page_map(p, p.k, box, &mk) || !page_map(p, p.v, box, &mv)) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int joined = p.S > 1 && p.S <= kRowsCluster;
@@ -606,25 +676,27 @@ cudaError_t launch_rows(const PAttnPlan &p, const CUtensorMap &mk, const CUtenso
                                  mk, mv, p, joined);
 }
 
+template <bool QB, int FMT>
+cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
+    return p.max_q * p.G <= 8 ? launch_rows<QB, FMT, 1>(p, st) : launch_rows<QB, FMT, 2>(p, st);
+}
+
 cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st) {
-    CUtensorMap mk, mv;
-    const int box = std::min(p.page, kStageKeys);
-    if (!page_map(p, p.k, box, &mk) || !page_map(p, p.v, box, &mv)) return cudaErrorInvalidValue;
     if (p.q_dtype == DT_BF16)
-        return p.fmt == PF_E4M3   ? launch_rows<true, PF_E4M3>(p, mk, mv, st)
-               : p.fmt == PF_INT8 ? launch_rows<true, PF_INT8>(p, mk, mv, st)
-                                  : launch_rows<true, PF_BF16>(p, mk, mv, st);
-    return p.fmt == PF_E4M3   ? launch_rows<false, PF_E4M3>(p, mk, mv, st)
-           : p.fmt == PF_INT8 ? launch_rows<false, PF_INT8>(p, mk, mv, st)
-                              : launch_rows<false, PF_F16>(p, mk, mv, st);
+        return p.fmt == PF_E4M3   ? launch_rows<true, PF_E4M3>(p, st)
+               : p.fmt == PF_INT8 ? launch_rows<true, PF_INT8>(p, st)
+                                  : launch_rows<true, PF_BF16>(p, st);
+    return p.fmt == PF_E4M3   ? launch_rows<false, PF_E4M3>(p, st)
+           : p.fmt == PF_INT8 ? launch_rows<false, PF_INT8>(p, st)
+                              : launch_rows<false, PF_F16>(p, st);
 }
 }  // namespace
 
 cudaError_t launch_page_attention(const PAttnPlan &p, cudaStream_t st) {
     const cudaError_t e =
         p.max_q * p.G <= kRowsM ? launch_page_attention_rows(p, st) : launch_page_attention_tc(p, st);
-    if (e != cudaSuccess || !page_attention_parts(p)) return e;
-    return launch_kernel(k_page_combine, dim3((unsigned)((p.total_q * p.HQ + 7) / 8)), dim3(256), 0, st, p);
+    if (e != cudaSuccess || page_attention_part_rows(p) == 0) return e;
+    return launch_kernel(k_page_combine, dim3((unsigned)(page_attention_part_rows(p) / p.S / 8)), dim3(256), 0, st, p);
 }
 
 }  // namespace qvg

@@ -175,11 +175,11 @@ __device__ __forceinline__ void rescale64(uint32_t at, float f) {
 }
 }  // namespace
 
-// grid (pairs of row tiles x splits, key/value heads, sequences)
+// grid (items taken whole + splits of the others), see page_attention_cut
 template <bool QB, int FMT>
 __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     k_page_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                   const __grid_constant__ PAttnPlan p, int pairs) {
+                   const __grid_constant__ PAttnPlan p) {
     pdl_begin();
     using T = TcShape<FMT>;
     constexpr bool WIDE = T::WIDE;
@@ -192,17 +192,24 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     volatile int *abort_flag = &sh.abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // longest first: under a causal mask the last rows see the most
-    const int pair = pairs - 1 - (int)blockIdx.x / p.S, split = (int)blockIdx.x % p.S;
-    const int h = blockIdx.y, b = blockIdx.z;
-    const SeqInfo sq = seq_info(p, b, threadIdx.x == 0 && blockIdx.x == 0 && h == 0);
+    // this CTA's item and split of it: one head's items after one another, so that those that
+    // run together find its keys and values in L2 (152 CTAs that each read their own would take
+    // the whole bandwidth of the memory), the longest first (under a causal mask the last rows
+    // see the most)
+    const bool whole_item = blockIdx.x < p.whole;
+    const int64_t tail = whole_item ? 0 : (blockIdx.x - p.whole) / p.S;
+    const int split = whole_item ? 0 : (int)((blockIdx.x - p.whole) - tail * p.S), S = whole_item ? 1 : p.S;
+    const int64_t item = whole_item ? blockIdx.x : p.whole + tail;
+    const int cell = (int)(item / p.units), pair = p.units - 1 - (int)(item - (int64_t)cell * p.units);
+    const int b = cell / p.H, h = cell - b * p.H;
+    const SeqInfo sq = seq_info(p, b, threadIdx.x == 0 && pair == 0 && split == 0 && h == 0);
     const int rows = sq.qn * p.G, r0 = pair * 2 * kTcM;
     if (r0 >= rows) return;
     const int nt = rows - r0 > kTcM ? 2 : 1;  // row tiles in use
     const int lo = seen_lo(p, sq, r0 / p.G), hi = seen_hi(p, sq, (min(rows, r0 + 2 * kTcM) - 1) / p.G);
     int n = 0, j0 = 0;  // this split's key tiles
     if (lo < hi) {
-        const int t_lo = lo / kTcN, all = (hi + kTcN - 1) / kTcN - t_lo, per = (all + p.S - 1) / p.S;
+        const int t_lo = lo / kTcN, all = (hi + kTcN - 1) / kTcN - t_lo, per = (all + S - 1) / S;
         j0 = t_lo + split * per;
         n = max(0, min(per, all - split * per));
     }
@@ -634,12 +641,12 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             tc_fence_after();
             if (ok) {
                 const int i = min(r, rows - 1) / p.G, hq = h * p.G + min(r, rows - 1) - i * p.G;
-                const bool live = r < rows, whole = p.S == 1;
+                const bool live = r < rows, whole = S == 1;
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
                 if constexpr (!WIDE) inv = ldexpf(inv, e - kValueShift);
                 const int64_t tok = sq.q0 + i;
-                const int64_t part = ((int64_t)split * p.total_q + tok) * p.HQ + hq;
+                const int64_t part = (tail * S + split) * p.unit + t * kTcM + row;
                 const int64_t out = tok * p.ot + hq * p.oh;
                 bool odd = false;
 #pragma unroll
@@ -718,8 +725,8 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
     const auto kernel = k_page_attn_tc<QB, FMT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int pairs = (int)((p.max_q * p.G + 2 * kTcM - 1) / (2 * kTcM));
-    return launch_kernel(kernel, dim3((unsigned)(pairs * p.S), p.H, p.B), dim3(T::THREADS), smem, st, mk, mv, p, pairs);
+    const int64_t items = (int64_t)p.units * p.H * p.B, grid = p.whole + (items - p.whole) * p.S;
+    return launch_kernel(kernel, dim3((unsigned)grid), dim3(T::THREADS), smem, st, mk, mv, p);
 }
 }  // namespace
 

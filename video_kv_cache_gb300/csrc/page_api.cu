@@ -93,6 +93,8 @@ qvg_status check_attention(const qvg_page_attention_params *p) {
     if (p->total_q * (int64_t)p->n_q_heads >= (int64_t(1) << 31) ||
         p->max_q * (p->n_q_heads / p->n_heads) >= (int64_t(1) << 26) || p->max_q >= (int64_t(1) << 26))
         return QVG_ERR_UNSUPPORTED;
+    if (((p->max_q * (p->n_q_heads / p->n_heads) + 255) / 256) * p->n_heads * (int64_t)p->n_seqs >= (int64_t(1) << 30))
+        return QVG_ERR_UNSUPPORTED;
     if (!std::isfinite(p->scale)) return QVG_ERR_INVALID_ARG;
     if (!stride_ok(p->q_token_stride, 0, p->q_dtype, false) || !stride_ok(p->q_head_stride, 0, p->q_dtype, false) ||
         !stride_ok(p->o_token_stride, p->total_q, p->out_dtype, true) ||
@@ -125,18 +127,13 @@ PAttnPlan attention_plan(const qvg_page_attention_params *prm) {
     p.qh = prm->q_head_stride;
     p.ot = prm->o_token_stride;
     p.oh = prm->o_head_stride;
-    p.S = prm->total_q ? page_attention_splits(p) : 1;
+    if (prm->total_q) page_attention_cut(p);
     return p;
 }
 
 // Workspace: the splits' partial rows, then their (maximum, sum) pairs.
-size_t attention_part_bytes(const PAttnPlan &p) {
-    return p.total_q && page_attention_parts(p) ? (size_t)p.S * p.total_q * p.HQ * kD * sizeof(float) : 0;
-}
-size_t attention_bytes(const PAttnPlan &p) {
-    const size_t part = attention_part_bytes(p);
-    return part ? part + (size_t)p.S * p.total_q * p.HQ * 2 * sizeof(float) : 0;
-}
+size_t attention_part_bytes(const PAttnPlan &p) { return (size_t)page_attention_part_rows(p) * kD * sizeof(float); }
+size_t attention_bytes(const PAttnPlan &p) { return (size_t)page_attention_part_rows(p) * (kD + 2) * sizeof(float); }
 
 // Checks that come after the arguments': the injected failure, the device.
 qvg_status ready() {
@@ -273,7 +270,7 @@ qvg_status qvg_page_read(const qvg_page_read_params *prm, const qvg_pages *pages
 }
 
 size_t qvg_page_attention_workspace_bytes(const qvg_page_attention_params *prm) {
-    if (check_attention(prm) != QVG_OK) return 0;
+    if (check_attention(prm) != QVG_OK || prm->total_q == 0) return 0;
     return attention_bytes(attention_plan(prm));
 }
 

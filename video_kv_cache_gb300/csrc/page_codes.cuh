@@ -2,8 +2,6 @@
 // brought into fp16 beside them.
 #pragma once
 
-#include <cuda_fp8.h>
-
 #include "internal.cuh"
 
 namespace qvg {
@@ -12,9 +10,14 @@ namespace qvg {
 template <bool E4M3>
 __device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
     if constexpr (E4M3) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-        return make_uint2((uint32_t)a.x | (uint32_t)a.y << 16, (uint32_t)b.x | (uint32_t)b.y << 16);
+        uint2 r;
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}\n"
+            : "=r"(r.x), "=r"(r.y)
+            : "r"(w));
+        return r;
     } else {
         const uint32_t u = w ^ 0x80808080u;
         const uint32_t t0 = __byte_perm(u, 0x64646464u, 0x4140), t1 = __byte_perm(u, 0x64646464u, 0x4342);
