@@ -59,7 +59,7 @@ def pool_rows(pool, scale, table_row, n, page):
     return x.transpose(0, 1).flatten(1, 2)[:, :n]
 
 
-def attend(Q, K, V, scale, causal, window, u_p, out_dtype):
+def attend(Q, K, V, scale, causal, window, u_p, out_dtype, u_k=0.0, u_v=0.0):
     """One sequence, one query head.  Q [nq][128], K and V [n][128], 64 bits.
     Returns (out, lse, bound on out's error, bound on lse's error).
 
@@ -68,7 +68,9 @@ def attend(Q, K, V, scale, causal, window, u_p, out_dtype):
     2^-21 for the exponential, bounds the relative error of a weight.  Weights meet the values
     rounded by u_p, or, where fp16 weights fall below its normal range, by half its smallest
     step: 2^-25 of a weight of 1 (the largest weight is at least 1, and so is their sum) times a
-    value, and for 8-bit pages 2^-25 of the largest product of scale and code; sums over n keys add n 2^-23, a rescaling at most each 16 keys 2^-22.  The
+    value, and for 8-bit pages 2^-25 of the largest product of scale and code; keys and
+    values times their scales are rounded by u_k and u_v (keys far below the largest by 2^-30 of
+    it); sums over n keys add n 2^-23, a rescaling at most each 16 keys 2^-22.  The
     log-sum-exp inherits the mean e_j and 2^-21 of its own size."""
     nq, n = Q.shape[0], K.shape[0]
     pos = torch.arange(n - nq, n)[:, None]
@@ -88,11 +90,13 @@ def attend(Q, K, V, scale, causal, window, u_p, out_dtype):
     Vs = torch.where(seen.any(0)[:, None], V, torch.zeros_like(V)) if n else V
     out = w @ Vs
     lse = (m + torch.log(total))[:, 0]
-    e = abs(scale) * 2.0 ** -16 * (Q.abs() @ K.abs().T) + 2.0 ** -22 * (s.abs() + m.abs())
+    e = abs(scale) * (2.0 ** -16 + u_k) * (Q.abs() @ K.abs().T) + 2.0 ** -22 * (s.abs() + m.abs())
+    if u_k and n:
+        e = e + abs(scale) * 2.0 ** -30 * Q.abs().sum(-1, keepdim=True) * K.nan_to_num().abs().amax()
     e = torch.where(seen, e, torch.zeros_like(e)) + 2.0 ** -21
     mean_e = (w * e).sum(-1, keepdim=True)
     sums = n * 2.0 ** -23 + (n / 16 + 8) * 2.0 ** -22
-    bound = (w * (e + u_p + sums)) @ Vs.abs() + out.abs() * (mean_e + sums)
+    bound = (w * (e + (1 + u_p) * (1 + u_v) - 1 + sums)) @ Vs.abs() + out.abs() * (mean_e + sums)
     if u_p == HALF_EPS[torch.float16] and n:
         bound = bound + n * 2.0 ** -25 * Vs.abs().amax()
     bound = bound * 1.01 + out.abs() * HALF_EPS[out_dtype] + TINY[out_dtype]

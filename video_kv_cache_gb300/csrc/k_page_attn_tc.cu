@@ -22,11 +22,17 @@
 // TMEM: S/P of the two row tiles (128 columns each; the weights of a tile take the first 64 of
 // its scores' columns), then O of the two (128 each): all 512 columns, one CTA an SM.
 //
-// 8-bit pages: four more warps widen the codes (exactly) to fp16 into the ring, from raw tiles
-// that TMA brings.  bf16 queries are made fp16 too, each row scaled by a power of two that
-// brings its largest channel to 1 .. 2: what falls below fp16's range is 2^-25 of that.  The
-// keys' scales multiply the scores, the values' the weights, which are held in fp16 against a
-// running reference 2^e near the largest scale: rounding them costs 2^-11.
+// 8-bit pages: four more warps widen the codes to fp16 into the ring, from raw tiles that TMA
+// brings.  bf16 queries are made fp16 too, each row scaled by a power of two that brings its
+// largest channel to 1 .. 2: what falls below fp16's range is 2^-25 of that.  The keys' and
+// values' scales are multiplied in while widening, relative to a power of two (of the tile's
+// largest scale for keys; for values, whose sums outlive the tile, of the largest so far), and
+// the product rounded to fp16 once: 2^-11 of each key and value, an eighth or less of what the
+// codes' own rounding was.  Taking the scales to the softmax instead keeps the scores exact to
+// fp32, but every one of its threads then reads the scale of every key from shared memory, and
+// that traffic, next to the tensor cores' own, is what the kernel would wait for (2.56 ms
+// instead of 1.6 ms for 4096 x 32768 x 32 heads over E4M3 pages): it is done for the keys only
+// where the caller asks for the log-sum-exp, an fp32 result that shows the difference.
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
@@ -41,7 +47,7 @@ constexpr int kTcN = 128;                  // keys of a key tile
 constexpr uint32_t kHalf = kTcM * 128;     // 64 channels of 128 rows: 16 KB
 constexpr uint32_t kSlot = 2 * kHalf;      // a whole 16-bit tile: 32 KB
 constexpr uint32_t kRaw = kTcN * kD;       // a tile of 8-bit codes: 16 KB
-constexpr int kValueShift = 4;             // weights with values' scales over 2^e are held times 2^4
+constexpr int kValueShift = 4, kKeyShift = 6;  // 8-bit values and keys over their references, times 2^this
 constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
 
 template <int FMT>
@@ -67,15 +73,15 @@ struct TcShared {
     uint64_t raw_full[3], raw_empty[3];
     uint64_t s_full[2], p_full[2][2], o_done[2];
     uint64_t sc_full[2], sc_empty[2];   // scales of a key tile
-    uint64_t edge, fin;
+    uint64_t q_full, edge, fin;
     uint32_t tmem;
     int abort;
-    int vexp[2];                        // exponent of the values' reference scale, per tile parity
+    int vexp[2], kexp[2];               // exponents of the values' and keys' references, per tile parity
     __align__(16) uint32_t vnan[2][4];                // keys whose value scale is not finite, a bit each
-    float wmax[4];
+    float wmax[2][4];
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
-    __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
-    __align__(16) float vs[2][WIDE ? 4 : kTcN];  // values' scales over the reference
+    __align__(16) float ks[2][WIDE ? 4 : kTcN];     // keys' scales times the softmax scale
+    uint2 kf[2][WIDE ? 1 : kTcN], vf[2][WIDE ? 1 : kTcN];  // scales over their references, see scale_pair
     float qmul[WIDE ? 4 : 2 * kTcM];             // powers of two taken out of the rows of Q
 };
 
@@ -153,6 +159,19 @@ __device__ __forceinline__ bool meet(int id, bool v) {
         : "memory");
     return r != 0u;
 }
+// A scale as two fp16 numbers, high and low part, each twice; and fp16 pairs times it, rounded
+// once (the low product's own rounding is 2^-22 of the result).
+__device__ __forceinline__ uint2 scale_pair(float f) {
+    const __half hi = __float2half_rn(f), lo = __float2half_rn(f - __half2float(hi));
+    const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&h2), *reinterpret_cast<const uint32_t *>(&l2));
+}
+__device__ __forceinline__ uint32_t scaled(uint32_t y, const uint2 &f) {
+    const __half2 v = *reinterpret_cast<const __half2 *>(&y), hi = *reinterpret_cast<const __half2 *>(&f.x),
+                  lo = *reinterpret_cast<const __half2 *>(&f.y);
+    const __half2 r = __hfma2(v, hi, __hmul2_rn(v, lo));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
 template <int REGS>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
@@ -176,7 +195,8 @@ __device__ __forceinline__ void rescale64(uint32_t at, float f) {
 }  // namespace
 
 // grid (items taken whole + splits of the others), see page_attention_cut
-template <bool QB, int FMT>
+// KFOLD (8-bit): the keys' scales are multiplied into the keys, not the scores.
+template <bool QB, int FMT, bool KFOLD>
 __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     k_page_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ PAttnPlan p) {
@@ -214,35 +234,6 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         n = max(0, min(per, all - split * per));
     }
 
-    // Q: both row tiles, swizzled; rows past the end are zeros.  The sign of a negative scale
-    // goes into Q, so that the maximum of the scores is the maximum of what is exponentiated.
-    {
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        constexpr int CHUNKS = 2 * kTcM * 16, EACH = (CHUNKS + T::THREADS - 1) / T::THREADS;
-        uint4 w[EACH];  // every read in flight before the first is used; whole warps, 16 lanes a row
-#pragma unroll
-        for (int u = 0; u < EACH; u++) {
-            const int x = threadIdx.x + u * T::THREADS, r = r0 + (x >> 4), i = r / p.G;
-            w[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (x < CHUNKS && r < rows)
-                w[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
-                                                             (int64_t)(h * p.G + r - i * p.G) * p.qh) + (x & 15));
-        }
-#pragma unroll
-        for (int u = 0; u < EACH; u++) {
-            const int x = threadIdx.x + u * T::THREADS, row = x >> 4, c = x & 15;
-            if (x >= CHUNKS) break;
-            w[u].x ^= flip; w[u].y ^= flip; w[u].z ^= flip; w[u].w ^= flip;
-            if constexpr (!WIDE) {
-                float mul = 1.f;
-                if constexpr (QB) w[u] = normalised_f16(w[u], mul, 16);
-                if (c == 0) sh.qmul[row] = mul;
-            }
-            const uint32_t at = (row >> 7) * kSlot + (c >> 3) * kHalf + (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4 *>(sQ + at) = w[u];
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; s++) {
             mbar_init(smem_u32(&sh.full[s]), WIDE ? 1 : 4);
@@ -260,6 +251,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             mbar_init(smem_u32(&sh.sc_full[t]), 4);
             mbar_init(smem_u32(&sh.sc_empty[t]), 8 * nt);
         }
+        mbar_init(smem_u32(&sh.q_full), 16);
         mbar_init(smem_u32(&sh.edge), 1);
         mbar_init(smem_u32(&sh.fin), 1);
         sh.abort = 0;
@@ -298,7 +290,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     }
                     tc_commit(smem_u32(&sh.s_full[t]));
                 };
-                bool ok = wait(sh.full[0], 0);
+                bool ok = wait(sh.full[0], 0) && wait(sh.q_full, 0);
                 if (ok) {
                     tc_fence_after();
                     for (int t = 0; t < nt; t++) scores(t, 0);
@@ -452,31 +444,47 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     // the key (and no others)
                     const uint32_t odd = __ballot_sync(0xffffffffu, !is_finite(vs));
                     if (!is_finite(vs)) vs = 0.f;
-                    float m = fabsf(vs);
+                    float m = fabsf(vs), mk = is_finite(ks) ? fabsf(ks) : 0.f;
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    for (int o = 16; o > 0; o >>= 1) {
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        if constexpr (KFOLD) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                    }
                     ok = ok && wait(sh.sc_empty[buf], (j >> 1) + 1);
-                    if (lane == 0) sh.wmax[warp - WIDEN_WARP] = m;
+                    if (lane == 0) {
+                        sh.wmax[0][warp - WIDEN_WARP] = m;
+                        sh.wmax[1][warp - WIDEN_WARP] = mk;
+                    }
                     ok = meet<128>(1, ok);
                     if (!ok) break;  // the four warps leave together
-                    m = fmaxf(fmaxf(sh.wmax[0], sh.wmax[1]), fmaxf(sh.wmax[2], sh.wmax[3]));
-                    meet<128>(1, true);
-                    // the reference moves only when a scale passes it by 2^3: the weights stay
-                    // below 2^8 (kLazy) * 2^3 * 2^4 < fp16's largest
-                    const int ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
+                    auto exponent = [&](const float *w) {
+                        const float big = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+                        return min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 121);
+                    };
+                    // the values' reference moves only when a scale passes it by 2^3: codes of at
+                    // most 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504
+                    const int ee = exponent(sh.wmax[0]);
                     if (j == 0 || ee > e + 2) e = ee;
-                    sh.ks[buf][x] = ks * mult;
-                    sh.vs[buf][x] = vs * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23);
+                    sh.vf[buf][x] = scale_pair(vs * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23));
+                    if constexpr (KFOLD) {
+                        const int ke = exponent(sh.wmax[1]);
+                        sh.kf[buf][x] = scale_pair(ks * __uint_as_float((uint32_t)(127 + kKeyShift - ke) << 23));
+                        if (x == 0) sh.kexp[buf] = ke;
+                    } else {
+                        sh.ks[buf][x] = ks * mult;
+                    }
                     if (lane == 0) sh.vnan[buf][warp - WIDEN_WARP] = odd;
                     if (x == 0) sh.vexp[buf] = e;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
+                    meet<128>(1, true);  // all scales are there; wmax is free again
                     if (j + 1 < n) load_scales(k0 + kTcN + x);
                 }
                 ok = ok && wait(sh.raw_full[raw], it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1);
                 ok = !__any_sync(0xffffffffu, !ok);
                 if (!ok) continue;
-                const bool whole = k0 >= lo && k0 + kTcN <= hi;
+                const bool whole = k0 >= lo && k0 + kTcN <= hi, value = it & 1;
+                const uint2 *factors = (value ? sh.vf[j & 1] : sh.kf[j & 1]) + rb;
                 const unsigned char *src = src0 + raw * kRaw;
                 unsigned char *dst = dst0 + slot * kSlot;
 #pragma unroll 4
@@ -488,8 +496,14 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     }
                     const uint2 y0 = codes_to_f16<FMT == PF_E4M3>(w.x), y1 = codes_to_f16<FMT == PF_E4M3>(w.y),
                                 y2 = codes_to_f16<FMT == PF_E4M3>(w.z), y3 = codes_to_f16<FMT == PF_E4M3>(w.w);
-                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d0) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d1) = make_uint4(y2.x, y2.y, y3.x, y3.y);
+                    uint4 a0 = make_uint4(y0.x, y0.y, y1.x, y1.y), a1 = make_uint4(y2.x, y2.y, y3.x, y3.y);
+                    if (KFOLD || value) {
+                        const uint2 f = factors[u * 16];
+                        a0 = make_uint4(scaled(a0.x, f), scaled(a0.y, f), scaled(a0.z, f), scaled(a0.w, f));
+                        a1 = make_uint4(scaled(a1.x, f), scaled(a1.y, f), scaled(a1.z, f), scaled(a1.w, f));
+                    }
+                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d0) = a0;
+                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d1) = a1;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -503,6 +517,37 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     } else {
         // -------------------------------------------------------------------- softmax
         regs_inc<T::REGS_SOFTMAX>();
+        // Q: both row tiles, swizzled; rows past the end are zeros.  The sign of a negative scale
+        // goes into Q, so that the maximum of the scores is the maximum of what is exponentiated.
+        {
+            const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+            constexpr int CHUNKS = 2 * kTcM * 16, EACH = CHUNKS / 512;
+            uint4 w[EACH];  // every read in flight before the first is used; whole warps, 16 lanes a row
+#pragma unroll
+            for (int u = 0; u < EACH; u++) {
+                const int x = threadIdx.x + u * 512, r = r0 + (x >> 4), i = r / p.G;
+                w[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows)
+                    w[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
+                                                                 (int64_t)(h * p.G + r - i * p.G) * p.qh) + (x & 15));
+            }
+#pragma unroll
+            for (int u = 0; u < EACH; u++) {
+                const int x = threadIdx.x + u * 512, row = x >> 4, c = x & 15;
+                w[u].x ^= flip; w[u].y ^= flip; w[u].z ^= flip; w[u].w ^= flip;
+                if constexpr (!WIDE) {
+                    float mul = 1.f;
+                    if constexpr (QB) w[u] = normalised_f16(w[u], mul, 16);
+                    if (c == 0) sh.qmul[row] = mul;
+                }
+                const uint32_t at = (row >> 7) * kSlot + (c >> 3) * kHalf + (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
+                *reinterpret_cast<uint4 *>(sQ + at) = w[u];
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+            if constexpr (!WIDE) meet<512>(10, true);  // the rows' powers of two are read across warps
+        }
         const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
         const int row = quarter * 32 + lane, r = r0 + t * kTcM + row;
         const int id = 2 + t * 4 + quarter;  // named barrier of the two warps of these rows
@@ -516,8 +561,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 open = (seen_lo(p, sq, z) + kTcN - 1) / kTcN - j0;
                 shut = seen_hi(p, sq, a) / kTcN - j0;
             }
-            const float mult = WIDE ? fabsf(p.scale_log2) : sh.qmul[t * kTcM + row];
-            const float2 sc2 = make_float2(mult, mult);
+            const float row_mult = WIDE ? fabsf(p.scale_log2) : sh.qmul[t * kTcM + row] * (KFOLD ? fabsf(p.scale_log2) : 1.f);
             float m = -INFINITY, l = 0.f;
             int e = 0;
             // (a wait that gives up raises the abort flag: a warp skips its work from then on, but
@@ -528,12 +572,13 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 float s[64];
                 ok = ok && wait(sh.s_full[t], j) && (WIDE || wait(sh.sc_full[buf], j >> 1));
                 ok = !__any_sync(0xffffffffu, !ok);
-                float mx = -INFINITY;
+                float mx = -INFINITY, mult = row_mult;
                 if (ok) {
                     tc_fence_after();
                     tc_ld32(s_at + half * 64, s);
                     tc_ld32(s_at + half * 64 + 32, s + 32);
-                    if constexpr (!WIDE) {
+                    if constexpr (KFOLD) mult *= __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23);
+                    if constexpr (!WIDE && !KFOLD) {
 #pragma unroll
                         for (int c = 0; c < 64; c += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][half * 64 + c]);
@@ -541,6 +586,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                             const float2 y = __fmul2_rn(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
                             s[c] = x.x; s[c + 1] = x.y; s[c + 2] = y.x; s[c + 3] = y.y;
                         }
+                    }
+                    if constexpr (!WIDE) {
                         const uint4 odd = *reinterpret_cast<const uint4 *>(sh.vnan[buf]);
                         if (odd.x | odd.y | odd.z | odd.w) {
                             const int k0 = (j0 + j) * kTcN + half * 64, i = min(r, rows - 1) / p.G;
@@ -600,22 +647,17 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 if (!ok) continue;
                 e = e_new;
                 const float base = exp_base(m);
-                const float2 nb = make_float2(-base, -base);
+                const float2 nb = make_float2(-base, -base), sc2 = make_float2(mult, mult);
                 float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
                 for (int q = 0; q < 64; q += 32) {
                     uint32_t w[16];
-                    float4 vs4 = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
                     for (int c = q; c < q + 32; c += 2) {
                         float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, nb);
                         x.x = fast_exp2(x.x);
                         x.y = fast_exp2(x.y);
                         if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
-                        if constexpr (!WIDE) {
-                            if (!(c & 2)) vs4 = *reinterpret_cast<const float4 *>(&sh.vs[buf][half * 64 + c]);
-                            x = __fmul2_rn(x, c & 2 ? make_float2(vs4.z, vs4.w) : make_float2(vs4.x, vs4.y));
-                        }
                         w[(c - q) >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
                     tc_st16(s_at + half * 32 + (q >> 1), w);
@@ -718,11 +760,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
 }
 
 namespace {
-template <bool QB, int FMT>
+template <bool QB, int FMT, bool KFOLD>
 cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
     using T = TcShape<FMT>;
     constexpr size_t smem = tc_smem<FMT>();
-    const auto kernel = k_page_attn_tc<QB, FMT>;
+    const auto kernel = k_page_attn_tc<QB, FMT, KFOLD>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)p.units * p.H * p.B, grid = p.whole + (items - p.whole) * p.S;
@@ -733,13 +775,15 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
 cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
     CUtensorMap maps[2];
     if (!page_map(p, p.k, p.page, &maps[0]) || !page_map(p, p.v, p.page, &maps[1])) return cudaErrorInvalidValue;
-    if (p.q_dtype == DT_BF16)
-        return p.fmt == PF_E4M3   ? launch_tc<true, PF_E4M3>(p, maps[0], maps[1], st)
-               : p.fmt == PF_INT8 ? launch_tc<true, PF_INT8>(p, maps[0], maps[1], st)
-                                  : launch_tc<true, PF_BF16>(p, maps[0], maps[1], st);
-    return p.fmt == PF_E4M3   ? launch_tc<false, PF_E4M3>(p, maps[0], maps[1], st)
-           : p.fmt == PF_INT8 ? launch_tc<false, PF_INT8>(p, maps[0], maps[1], st)
-                              : launch_tc<false, PF_F16>(p, maps[0], maps[1], st);
+    auto go = [&](auto qb) {
+        constexpr bool QB = decltype(qb)::value;
+        if (p.fmt == PF_E4M3)
+            return p.lse ? launch_tc<QB, PF_E4M3, false>(p, maps[0], maps[1], st) : launch_tc<QB, PF_E4M3, true>(p, maps[0], maps[1], st);
+        if (p.fmt == PF_INT8)
+            return p.lse ? launch_tc<QB, PF_INT8, false>(p, maps[0], maps[1], st) : launch_tc<QB, PF_INT8, true>(p, maps[0], maps[1], st);
+        return launch_tc<QB, QB ? PF_BF16 : PF_F16, false>(p, maps[0], maps[1], st);
+    };
+    return p.q_dtype == DT_BF16 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace qvg
