@@ -22,7 +22,7 @@
 // TMEM: S/P of the two row tiles (128 columns each; the weights of a tile take the first 64 of
 // its scores' columns), then O of the two (128 each): all 512 columns, one CTA an SM.
 //
-// 8-bit pages: four more warps widen the codes to fp16 into the ring, from raw tiles that TMA
+// 8-bit pages: eight more warps widen the codes to fp16 into the ring, from raw tiles that TMA
 // brings.  bf16 queries are made fp16 too, each row scaled by a power of two that brings its
 // largest channel to 1 .. 2: what falls below fp16's range is 2^-25 of that.  The keys' and
 // values' scales are multiplied in while widening, relative to a power of two (of the tile's
@@ -56,11 +56,12 @@ struct TcShape {
     static constexpr int SLOTS = WIDE ? 5 : 3;       // ring of 16-bit tiles
     static constexpr int RAWS = 3;                   // ring of raw 8-bit tiles
     // 16 softmax warps; MMA, loads and two idle ones (registers move by groups of four warps);
-    // 8-bit: four that widen
-    static constexpr int THREADS = WIDE ? 640 : 768;
+    // 8-bit: four that widen keys and four that widen values (four for both keep the tensor
+    // cores waiting)
+    static constexpr int THREADS = WIDE ? 640 : 896;
     // registers at launch (65,536 over the warps of an SM quarter), and after they were shared
     // out anew: the groups' sum stays what the launch had
-    static constexpr int REGS = WIDE ? 96 : 80, REGS_SOFTMAX = WIDE ? 104 : 96, REGS_REST = WIDE ? 64 : 48;
+    static constexpr int REGS = WIDE ? 96 : 72, REGS_SOFTMAX = WIDE ? 104 : 88, REGS_REST = WIDE ? 64 : 48;
     static_assert(512 * REGS_SOFTMAX + (THREADS - 512) * REGS_REST <= THREADS * REGS, "register shares");
     static constexpr uint32_t SMEM_TILES = 2 * kSlot + SLOTS * kSlot + (WIDE ? 0 : RAWS * kRaw);
 };
@@ -78,7 +79,7 @@ struct TcShared {
     int abort;
     int vexp[2], kexp[2];               // exponents of the values' and keys' references, per tile parity
     __align__(16) uint32_t vnan[2][4];                // keys whose value scale is not finite, a bit each
-    float wmax[2][4];
+    float wmax[2][4];                   // largest scales of the widening warps: keys', values'
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
     __align__(16) float ks[2][WIDE ? 4 : kTcN];     // keys' scales times the softmax scale
     uint2 kf[2][WIDE ? 1 : kTcN], vf[2][WIDE ? 1 : kTcN];  // scales over their references, see scale_pair
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             mbar_init(smem_u32(&sh.p_full[t][0]), 8);
             mbar_init(smem_u32(&sh.p_full[t][1]), 8);
             mbar_init(smem_u32(&sh.o_done[t]), 1);
-            mbar_init(smem_u32(&sh.sc_full[t]), 4);
+            mbar_init(smem_u32(&sh.sc_full[t]), 8);
             mbar_init(smem_u32(&sh.sc_empty[t]), 8 * nt);
         }
         mbar_init(smem_u32(&sh.q_full), 16);
@@ -413,22 +414,21 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 mbar_wait_final(smem_u32(WIDE ? &sh.full[it % RING] : &sh.raw_full[it % RING]), (it / RING) & 1u);
         } else if (!WIDE && warp >= WIDEN_WARP) {
             // ---------------------------------------------------------------- 8-bit codes widened
-            const int shift = 31 - __clz(p.page), x = threadIdx.x - 32 * WIDEN_WARP;
-            const float mult = fabsf(p.scale_log2);
+            const bool value = warp >= WIDEN_WARP + 4;  // the first four warps: keys, the others: values
+            const int shift = 31 - __clz(p.page), x = (threadIdx.x - 32 * WIDEN_WARP) & 127, id = 1 + value;
+            const float *scales = value ? p.vs : p.ks;
+            float *wmax = sh.wmax[value];
             int e = -126;
             bool ok = true, bad = false;
             // scales of a tile's keys, one a thread, read one tile ahead; outside what is seen
             // they are 0
-            float ks = 0.f, vs = 0.f;
-            auto load_scales = [&](int key) {
-                ks = vs = 0.f;
-                if (key >= lo && key < hi) {
-                    const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
-                    ks = __ldg(p.ks + row);
-                    vs = __ldg(p.vs + row);
-                }
+            float sc = 0.f;
+            auto load_scale = [&](int key) {
+                sc = 0.f;
+                if (key >= lo && key < hi)
+                    sc = __ldg(scales + ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1)));
             };
-            if (n > 0) load_scales(j0 * kTcN + x);
+            if (n > 0) load_scale(j0 * kTcN + x);
             // 16 codes (chunk c of a row) a thread, rows 16 apart: eight lanes that are served
             // together have eight rows of one chunk, which the swizzle of the raw tile and that
             // of the widened one both spread over all banks
@@ -436,55 +436,41 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             const unsigned char *src0 = sRaw + rb * kD + ((c ^ r8) << 4);
             unsigned char *dst0 = sKV + (c >> 2) * kHalf + rb * 128;
             const int d0 = ((2 * (c & 3)) ^ r8) << 4, d1 = ((2 * (c & 3) + 1) ^ r8) << 4;
-            for (uint32_t it = 0; it < 2u * n; it++) {
-                const int j = it >> 1, k0 = (j0 + j) * kTcN, slot = it % SLOTS, raw = it % T::RAWS;
-                if (!(it & 1)) {
-                    const int buf = j & 1;
-                    // a scale that is not finite: 0 here, and a bit that makes the rows NaN that see
-                    // the key (and no others)
-                    const uint32_t odd = __ballot_sync(0xffffffffu, !is_finite(vs));
-                    if (!is_finite(vs)) vs = 0.f;
-                    float m = fabsf(vs), mk = is_finite(ks) ? fabsf(ks) : 0.f;
+            for (int j = 0; j < n; j++) {
+                const int it = 2 * j + value, k0 = (j0 + j) * kTcN, slot = it % SLOTS, raw = it % T::RAWS, buf = j & 1;
+                // a value scale that is not finite: 0 here, and a bit that makes the rows NaN that
+                // see the key (and no others)
+                const uint32_t odd = __ballot_sync(0xffffffffu, !is_finite(sc));
+                float m = is_finite(sc) ? fabsf(sc) : 0.f;
+                if (value) sc = is_finite(sc) ? sc : 0.f;
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) {
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        if constexpr (KFOLD) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-                    }
-                    ok = ok && wait(sh.sc_empty[buf], (j >> 1) + 1);
-                    if (lane == 0) {
-                        sh.wmax[0][warp - WIDEN_WARP] = m;
-                        sh.wmax[1][warp - WIDEN_WARP] = mk;
-                    }
-                    ok = meet<128>(1, ok);
-                    if (!ok) break;  // the four warps leave together
-                    auto exponent = [&](const float *w) {
-                        const float big = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
-                        return min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 121);
-                    };
-                    // the values' reference moves only when a scale passes it by 2^3: codes of at
-                    // most 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504
-                    const int ee = exponent(sh.wmax[0]);
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                ok = ok && wait(sh.sc_empty[buf], (j >> 1) + 1);
+                if (lane == 0) wmax[warp & 3] = m;
+                ok = meet<128>(id, ok);
+                if (!ok) break;  // the four warps leave together
+                m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+                const int ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
+                if (value) {
+                    // the reference moves only when a scale passes it by 2^3: codes of at most
+                    // 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504
                     if (j == 0 || ee > e + 2) e = ee;
-                    sh.vf[buf][x] = scale_pair(vs * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23));
-                    if constexpr (KFOLD) {
-                        const int ke = exponent(sh.wmax[1]);
-                        sh.kf[buf][x] = scale_pair(ks * __uint_as_float((uint32_t)(127 + kKeyShift - ke) << 23));
-                        if (x == 0) sh.kexp[buf] = ke;
-                    } else {
-                        sh.ks[buf][x] = ks * mult;
-                    }
-                    if (lane == 0) sh.vnan[buf][warp - WIDEN_WARP] = odd;
+                    sh.vf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23));
+                    if (lane == 0) sh.vnan[buf][warp & 3] = odd;
                     if (x == 0) sh.vexp[buf] = e;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
-                    meet<128>(1, true);  // all scales are there; wmax is free again
-                    if (j + 1 < n) load_scales(k0 + kTcN + x);
+                } else if (KFOLD) {
+                    sh.kf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kKeyShift - ee) << 23));
+                    if (x == 0) sh.kexp[buf] = ee;
+                } else {
+                    sh.ks[buf][x] = sc * fabsf(p.scale_log2);
                 }
-                ok = ok && wait(sh.raw_full[raw], it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1);
-                ok = !__any_sync(0xffffffffu, !ok);
-                if (!ok) continue;
-                const bool whole = k0 >= lo && k0 + kTcN <= hi, value = it & 1;
-                const uint2 *factors = (value ? sh.vf[j & 1] : sh.kf[j & 1]) + rb;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
+                if (j + 1 < n) load_scale(k0 + kTcN + x);
+                ok = meet<128>(id, wait(sh.raw_full[raw], it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1));
+                if (!ok) break;  // (otherwise all scales are there, and wmax is free again)
+                const bool whole = k0 >= lo && k0 + kTcN <= hi;
+                const uint2 *factors = (value ? sh.vf[buf] : sh.kf[buf]) + rb;
                 const unsigned char *src = src0 + raw * kRaw;
                 unsigned char *dst = dst0 + slot * kSlot;
 #pragma unroll 4
@@ -546,11 +532,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
-            if constexpr (!WIDE) meet<512>(10, true);  // the rows' powers of two are read across warps
+            if constexpr (!WIDE) meet<512>(11, true);  // the rows' powers of two are read across warps
         }
         const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
         const int row = quarter * 32 + lane, r = r0 + t * kTcM + row;
-        const int id = 2 + t * 4 + quarter;  // named barrier of the two warps of these rows
+        const int id = 3 + t * 4 + quarter;  // named barrier of the two warps of these rows
         if (t < nt) {
             const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128 + half * 64;
