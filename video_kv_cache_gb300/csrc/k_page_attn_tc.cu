@@ -131,6 +131,29 @@ __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t r[16]) {
         : "r"(taddr)
         : "memory");
 }
+// The read of 32 columns in two steps: what it gives may be used after the second.
+__device__ __forceinline__ void tc_ld32_start(uint32_t taddr, float v[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_ld32_wait(float v[32]) {
+    asm volatile(
+        "tcgen05.wait::ld.sync.aligned;"
+        : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+          "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+          "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+          "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+        :
+        : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Descriptor of an MN-major operand (values: 64 channels of a key are one 128-byte row) in the
@@ -312,7 +335,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         tc_fence_after();
                         const uint32_t o = tmem + 256 + t * 128, w = tmem + t * 128;
                         auto product = [&](int s, bool accumulate) {
-                            tc_mma_ts(o, w + s * 8, v + (uint64_t)((s * 2048) >> 4), id_pv, accumulate);
+                            // (the two halves of the weights lie where their scores were)
+                            tc_mma_ts(o, w + s * 8 + (s >= 4 ? 32 : 0), v + (uint64_t)((s * 2048) >> 4), id_pv, accumulate);
                         };
                         // the steps of the first 32 keys of either half, then the others
                         const bool whole = st0 == 0 && st1 == 8;
@@ -555,23 +579,59 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             bool ok = true;
             for (int j = 0; j < n; j++) {
                 const int buf = j & 1;
-                float s[64];
                 ok = ok && wait(sh.s_full[t], j) && (WIDE || wait(sh.sc_full[buf], j >> 1));
                 ok = !__any_sync(0xffffffffu, !ok);
-                float mx = -INFINITY, mult = row_mult;
-                if (ok) {
-                    tc_fence_after();
-                    tc_ld32(s_at + half * 64, s);
-                    tc_ld32(s_at + half * 64 + 32, s + 32);
-                    if constexpr (KFOLD) mult *= __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23);
+                const bool masked = j < open || j >= shut;
+                // 32 of the thread's 64 scores, from column hc of its half on: scaled by their
+                // keys where that was not done before, -infinity where hidden
+                auto finish = [&](int hc, float s[32]) {
                     if constexpr (!WIDE && !KFOLD) {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][half * 64 + c]);
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][half * 64 + hc + c]);
                             const float2 x = __fmul2_rn(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
                             const float2 y = __fmul2_rn(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
                             s[c] = x.x; s[c + 1] = x.y; s[c + 2] = y.x; s[c + 3] = y.y;
                         }
+                    }
+                    if (masked) {
+                        const int k0 = (j0 + j) * kTcN + half * 64 + hc, i = min(r, rows - 1) / p.G;
+                        const int a = seen_lo(p, sq, i) - k0, z = seen_hi(p, sq, i) - k0;
+#pragma unroll
+                        for (int c = 0; c < 32; c++) s[c] = c >= a && c < z ? s[c] : -INFINITY;
+                    }
+                };
+                auto largest = [](const float s[32]) {
+                    float m0 = fmax3(s[0], s[1], s[2]), m1 = fmax3(s[3], s[4], s[5]);
+#pragma unroll
+                    for (int c = 6; c < 30; c += 4) {
+                        m0 = fmax3(m0, s[c], s[c + 1]);
+                        m1 = fmax3(m1, s[c + 2], s[c + 3]);
+                    }
+                    return fmaxf(fmax3(m0, s[30], s[31]), m1);
+                };
+                // 16 bits: the scores stay in registers.  8 bits, with more warps and fewer
+                // registers each, they would spill: they are read twice, for their maximum and
+                // for the weights (2.03 -> 1.94 ms; in 16 bits it costs 643 -> 675 us).
+                constexpr bool TWICE = !WIDE;
+                float s[TWICE ? 32 : 64], mx = -INFINITY, mult = row_mult;
+                if (ok) {
+                    tc_fence_after();
+                    if constexpr (KFOLD) mult *= __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23);
+                    if constexpr (TWICE) {
+                        tc_ld32(s_at + half * 64, s);
+                        finish(0, s);
+                        mx = largest(s);
+                        tc_ld32(s_at + half * 64 + 32, s);
+                        finish(32, s);
+                        mx = fmaxf(mx, largest(s)) * mult;
+                        tc_ld32_start(s_at + half * 64, s);  // arrives during the vote
+                    } else {
+                        tc_ld32(s_at + half * 64, s);
+                        tc_ld32(s_at + half * 64 + 32, s + 32);
+                        finish(0, s);
+                        finish(32, s + 32);
+                        mx = fmaxf(largest(s), largest(s + 32)) * mult;
                     }
                     if constexpr (!WIDE) {
                         const uint4 odd = *reinterpret_cast<const uint4 *>(sh.vnan[buf]);
@@ -582,24 +642,6 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                                 if (bits >> c & 1 && k0 + c >= seen_lo(p, sq, i) && k0 + c < seen_hi(p, sq, i)) l = NAN;
                         }
                     }
-                    if (j < open || j >= shut) {
-                        const int k0 = (j0 + j) * kTcN + half * 64, i = min(r, rows - 1) / p.G;
-                        const int a = seen_lo(p, sq, i) - k0, z = seen_hi(p, sq, i) - k0;
-#pragma unroll
-                        for (int c = 0; c < 64; c++) s[c] = c >= a && c < z ? s[c] : -INFINITY;
-                    }
-                    float m0 = fmax3(s[0], s[1], s[2]), m1 = fmax3(s[3], s[4], s[5]), m2 = fmax3(s[6], s[7], s[8]),
-                          m3 = fmax3(s[9], s[10], s[11]);
-#pragma unroll
-                    for (int c = 12; c < 60; c += 8) {
-                        m0 = fmax3(m0, s[c], s[c + 1]);
-                        m1 = fmax3(m1, s[c + 2], s[c + 3]);
-                        m2 = fmax3(m2, s[c + 4], s[c + 5]);
-                        m3 = fmax3(m3, s[c + 6], s[c + 7]);
-                    }
-                    m0 = fmax3(m0, s[60], s[61]);
-                    m1 = fmax3(m1, s[62], s[63]);
-                    mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * mult;
                 }
                 // The base moves for a row when its scores pass it by 2^8 (the first tile sets
                 // it), for all rows of the two warps that share them together, or when the
@@ -608,6 +650,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 int e_new = e;
                 if constexpr (!WIDE) e_new = ok ? sh.vexp[buf] : e;
                 if (!meet<64>(id, ok && !raise && j > 0 && e_new == e)) {
+                    if (TWICE && ok) tc_ld32_wait(s);  // nothing below may move registers that are still to be written
                     // the larger of the two threads' maxima
                     sh.xmax[t][half][row] = mx;
                     meet<64>(id, true);
@@ -636,22 +679,29 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const float2 nb = make_float2(-base, -base), sc2 = make_float2(mult, mult);
                 float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
-                for (int q = 0; q < 64; q += 32) {
+                for (int hc = 0; hc < 64; hc += 32) {
+                    if constexpr (TWICE) {
+                        if (hc) tc_ld32_start(s_at + half * 64 + hc, s);
+                        tc_ld32_wait(s);
+                        finish(hc, s);
+                    }
+                    const float *y = TWICE ? s : s + hc;
                     uint32_t w[16];
 #pragma unroll
-                    for (int c = q; c < q + 32; c += 2) {
-                        float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, nb);
+                    for (int c = 0; c < 32; c += 2) {
+                        float2 x = __ffma2_rn(make_float2(y[c], y[c + 1]), sc2, nb);
                         x.x = fast_exp2(x.x);
                         x.y = fast_exp2(x.y);
                         if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
-                        w[(c - q) >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
+                        w[c >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
-                    tc_st16(s_at + half * 32 + (q >> 1), w);
-                    // the product starts with the first 32 keys of either half
+                    // weights over scores that were read, so nobody else's: the product starts
+                    // with the first 32 keys of either half
+                    tc_st16(s_at + half * 64 + (hc >> 1), w);
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t][q >> 5]));
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t][hc >> 5]));
                 }
                 const float2 ls = __fadd2_rn(la, lb);
                 l += ls.x + ls.y;
