@@ -289,7 +289,8 @@ def _check(Q, kv, table, kv_lens, q_lens, causal, window, scale=None, out=None, 
                                   torch.tensor(kv_lens, dtype=torch.int32).cuda(), causal=causal,
                                   window=window, scale=scale, out=out, out_dtype=out_dtype, return_lse=True,
                                   status=status, **kw)
-    # without the log-sum-exp: 8-bit keys may meet many rows rounded to fp16
+    # without the log-sum-exp and with a bf16 output: 8-bit keys and values may meet many rows
+    # rounded to fp16
     alone = api.page_attention(Q.cuda() if not Q.is_cuda else Q, kv, table.cuda(),
                                torch.tensor(kv_lens, dtype=torch.int32).cuda(), causal=causal,
                                window=window, scale=scale, out_dtype=got.dtype, status=status, **kw)
@@ -297,7 +298,7 @@ def _check(Q, kv, table, kv_lens, q_lens, causal, window, scale=None, out=None, 
     assert int(status) == 0
     narrow = kv.k.dtype in pm.TOP
     u_p = pm.HALF_EPS[HF if narrow else Q.dtype]
-    u_kv = pm.HALF_EPS[HF] if narrow and max(q_lens) * group > 16 else 0.0
+    u_kv = pm.HALF_EPS[HF] if narrow and got.dtype is BF and max(q_lens) * group > 16 else 0.0
     if not u_kv:
         assert torch.equal(alone, got)
     Qc = Q.double().cpu()
@@ -310,7 +311,7 @@ def _check(Q, kv, table, kv_lens, q_lens, causal, window, scale=None, out=None, 
         for hq in range(Q.shape[1]):
             want, want_lse, bound, lse_bound = pm.attend(
                 Qc[rows, hq], K[hq // group], V[hq // group], 128 ** -0.5 if scale is None else scale,
-                causal, window, u_p, got.dtype, 0.0, u_kv)
+                causal, window, u_p, got.dtype)
             _within(got[rows, hq], want, bound, "sequence %d head %d" % (b, hq))
             if u_kv:
                 _, _, wider, _ = pm.attend(

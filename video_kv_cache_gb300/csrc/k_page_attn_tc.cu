@@ -24,15 +24,14 @@
 //
 // 8-bit pages: eight more warps widen the codes to fp16 into the ring, from raw tiles that TMA
 // brings.  bf16 queries are made fp16 too, each row scaled by a power of two that brings its
-// largest channel to 1 .. 2: what falls below fp16's range is 2^-25 of that.  The keys' and
-// values' scales are multiplied in while widening, relative to a power of two (of the tile's
-// largest scale for keys; for values, whose sums outlive the tile, of the largest so far), and
-// the product rounded to fp16 once: 2^-11 of each key and value, an eighth or less of what the
-// codes' own rounding was.  Taking the scales to the softmax instead keeps the scores exact to
-// fp32, but every one of its threads then reads the scale of every key from shared memory, and
-// that traffic, next to the tensor cores' own, is what the kernel would wait for (2.56 ms
-// instead of 1.6 ms for 4096 x 32768 x 32 heads over E4M3 pages): it is done for the keys only
-// where the caller asks for the log-sum-exp, an fp32 result that shows the difference.
+// largest channel to 1 .. 2: what falls below fp16's range is 2^-25 of that.  Where the output
+// is bf16 and no log-sum-exp is asked for (FOLD), the keys' and values' scales are multiplied in
+// while widening, relative to a power of two (of the tile's largest scale for keys; for values,
+// whose sums outlive the tile, of the largest so far), and the product is rounded to fp16 once:
+// 2^-11 of each key and value, an eighth of what the output's own rounding is.  Otherwise the
+// scales multiply the scores and the weights in the softmax (the weights, in fp16, relative to
+// the same power of two), which costs time: every thread then reads the scales of all keys from
+// shared memory.
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
@@ -61,7 +60,7 @@ struct TcShape {
     static constexpr int THREADS = WIDE ? 640 : 896;
     // registers at launch (65,536 over the warps of an SM quarter), and after they were shared
     // out anew: the groups' sum stays what the launch had
-    static constexpr int REGS = WIDE ? 96 : 72, REGS_SOFTMAX = WIDE ? 104 : 88, REGS_REST = WIDE ? 64 : 48;
+    static constexpr int REGS = WIDE ? 96 : 72, REGS_SOFTMAX = WIDE ? 104 : 80, REGS_REST = WIDE ? 64 : 56;
     static_assert(512 * REGS_SOFTMAX + (THREADS - 512) * REGS_REST <= THREADS * REGS, "register shares");
     static constexpr uint32_t SMEM_TILES = 2 * kSlot + SLOTS * kSlot + (WIDE ? 0 : RAWS * kRaw);
 };
@@ -81,7 +80,8 @@ struct TcShared {
     __align__(16) uint32_t vnan[2][4];                // keys whose value scale is not finite, a bit each
     float wmax[2][4];                   // largest scales of the widening warps: keys', values'
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
-    __align__(16) float ks[2][WIDE ? 4 : kTcN];     // keys' scales times the softmax scale
+    __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
+    __align__(16) float vs[2][WIDE ? 4 : kTcN];  // values' scales over their reference
     uint2 kf[2][WIDE ? 1 : kTcN], vf[2][WIDE ? 1 : kTcN];  // scales over their references, see scale_pair
     float qmul[WIDE ? 4 : 2 * kTcM];             // powers of two taken out of the rows of Q
 };
@@ -219,8 +219,8 @@ __device__ __forceinline__ void rescale64(uint32_t at, float f) {
 }  // namespace
 
 // grid (items taken whole + splits of the others), see page_attention_cut
-// KFOLD (8-bit): the keys' scales are multiplied into the keys, not the scores.
-template <bool QB, int FMT, bool KFOLD>
+// FOLD (8-bit): the scales are multiplied into keys and values, not scores and weights.
+template <bool QB, int FMT, bool FOLD>
 __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     k_page_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ PAttnPlan p) {
@@ -477,12 +477,17 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const int ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
                 if (value) {
                     // the reference moves only when a scale passes it by 2^3: codes of at most
-                    // 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504
+                    // 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504, and so do
+                    // weights of at most 2^kLazy
                     if (j == 0 || ee > e + 2) e = ee;
-                    sh.vf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23));
+                    const float f = sc * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23);
+                    if constexpr (FOLD)
+                        sh.vf[buf][x] = scale_pair(f);
+                    else
+                        sh.vs[buf][x] = f;
                     if (lane == 0) sh.vnan[buf][warp & 3] = odd;
                     if (x == 0) sh.vexp[buf] = e;
-                } else if (KFOLD) {
+                } else if (FOLD) {
                     sh.kf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kKeyShift - ee) << 23));
                     if (x == 0) sh.kexp[buf] = ee;
                 } else {
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const uint2 *factors = (value ? sh.vf[buf] : sh.kf[buf]) + rb;
                 const unsigned char *src = src0 + raw * kRaw;
                 unsigned char *dst = dst0 + slot * kSlot;
-#pragma unroll 4
+#pragma unroll
                 for (int u = 0; u < 8; u++) {
                     uint4 w = *reinterpret_cast<const uint4 *>(src + u * 16 * kD);
                     if (!whole) {  // what no row sees may hold anything
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     const uint2 y0 = codes_to_f16<FMT == PF_E4M3>(w.x), y1 = codes_to_f16<FMT == PF_E4M3>(w.y),
                                 y2 = codes_to_f16<FMT == PF_E4M3>(w.z), y3 = codes_to_f16<FMT == PF_E4M3>(w.w);
                     uint4 a0 = make_uint4(y0.x, y0.y, y1.x, y1.y), a1 = make_uint4(y2.x, y2.y, y3.x, y3.y);
-                    if (KFOLD || value) {
+                    if constexpr (FOLD) {
                         const uint2 f = factors[u * 16];
                         a0 = make_uint4(scaled(a0.x, f), scaled(a0.y, f), scaled(a0.z, f), scaled(a0.w, f));
                         a1 = make_uint4(scaled(a1.x, f), scaled(a1.y, f), scaled(a1.z, f), scaled(a1.w, f));
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 open = (seen_lo(p, sq, z) + kTcN - 1) / kTcN - j0;
                 shut = seen_hi(p, sq, a) / kTcN - j0;
             }
-            const float row_mult = WIDE ? fabsf(p.scale_log2) : sh.qmul[t * kTcM + row] * (KFOLD ? fabsf(p.scale_log2) : 1.f);
+            const float row_mult = WIDE ? fabsf(p.scale_log2) : sh.qmul[t * kTcM + row] * (FOLD ? fabsf(p.scale_log2) : 1.f);
             float m = -INFINITY, l = 0.f;
             int e = 0;
             // (a wait that gives up raises the abort flag: a warp skips its work from then on, but
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 // 32 of the thread's 64 scores, from column hc of its half on: scaled by their
                 // keys where that was not done before, -infinity where hidden
                 auto finish = [&](int hc, float s[32]) {
-                    if constexpr (!WIDE && !KFOLD) {
+                    if constexpr (!WIDE && !FOLD) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(&sh.ks[buf][half * 64 + hc + c]);
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 float s[TWICE ? 32 : 64], mx = -INFINITY, mult = row_mult;
                 if (ok) {
                     tc_fence_after();
-                    if constexpr (KFOLD) mult *= __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23);
+                    if constexpr (FOLD) mult *= __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23);
                     if constexpr (TWICE) {
                         tc_ld32(s_at + half * 64, s);
                         finish(0, s);
@@ -687,12 +692,17 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     }
                     const float *y = TWICE ? s : s + hc;
                     uint32_t w[16];
+                    float4 vs4 = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
                         float2 x = __ffma2_rn(make_float2(y[c], y[c + 1]), sc2, nb);
                         x.x = fast_exp2(x.x);
                         x.y = fast_exp2(x.y);
                         if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
+                        if constexpr (!WIDE && !FOLD) {
+                            if (!(c & 2)) vs4 = *reinterpret_cast<const float4 *>(&sh.vs[buf][half * 64 + hc + c]);
+                            x = __fmul2_rn(x, c & 2 ? make_float2(vs4.z, vs4.w) : make_float2(vs4.x, vs4.y));
+                        }
                         w[c >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
                     // weights over scores that were read, so nobody else's: the product starts
@@ -796,11 +806,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
 }
 
 namespace {
-template <bool QB, int FMT, bool KFOLD>
+template <bool QB, int FMT, bool FOLD>
 cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st) {
     using T = TcShape<FMT>;
     constexpr size_t smem = tc_smem<FMT>();
-    const auto kernel = k_page_attn_tc<QB, FMT, KFOLD>;
+    const auto kernel = k_page_attn_tc<QB, FMT, FOLD>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)p.units * p.H * p.B, grid = p.whole + (items - p.whole) * p.S;
@@ -811,12 +821,13 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
 cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
     CUtensorMap maps[2];
     if (!page_map(p, p.k, p.page, &maps[0]) || !page_map(p, p.v, p.page, &maps[1])) return cudaErrorInvalidValue;
+    const bool fold = !p.lse && p.out_dtype == DT_BF16;
     auto go = [&](auto qb) {
         constexpr bool QB = decltype(qb)::value;
         if (p.fmt == PF_E4M3)
-            return p.lse ? launch_tc<QB, PF_E4M3, false>(p, maps[0], maps[1], st) : launch_tc<QB, PF_E4M3, true>(p, maps[0], maps[1], st);
+            return fold ? launch_tc<QB, PF_E4M3, true>(p, maps[0], maps[1], st) : launch_tc<QB, PF_E4M3, false>(p, maps[0], maps[1], st);
         if (p.fmt == PF_INT8)
-            return p.lse ? launch_tc<QB, PF_INT8, false>(p, maps[0], maps[1], st) : launch_tc<QB, PF_INT8, true>(p, maps[0], maps[1], st);
+            return fold ? launch_tc<QB, PF_INT8, true>(p, maps[0], maps[1], st) : launch_tc<QB, PF_INT8, false>(p, maps[0], maps[1], st);
         return launch_tc<QB, QB ? PF_BF16 : PF_F16, false>(p, maps[0], maps[1], st);
     };
     return p.q_dtype == DT_BF16 ? go(std::true_type{}) : go(std::false_type{});
