@@ -1,8 +1,13 @@
 // The paged cache: new rows written (keys turned by their positions on the way, rounded to 16
 // bits or to 8-bit codes with a scale per row) and rows read back.
 //
-// Both are bound by memory.  Sixteen lanes hold a row; a row's largest magnitude, a maximum of
-// bit patterns (so that a NaN or an infinity is the largest of all), takes four shuffles.
+// Both are bound by memory, the 8-bit write nearly as much by instructions (about 25 a row and
+// warp): sixteen lanes hold a row and take four heads' keys and values of a token, eight rows.
+// The rows' largest magnitudes are maxima of bit patterns (so that a NaN or an infinity is the
+// largest of all), reduced together: at each of four exchanges a lane gives away the rows that
+// the other keeps, and ends with one row of the eight.  The pair of lanes that has a row then
+// makes its two quotients, largest code / magnitude and magnitude / largest code, in one
+// division for all eight rows.
 #include <cuda_fp8.h>
 
 #include "rows.cuh"
@@ -11,65 +16,56 @@ namespace qvg {
 
 namespace {
 constexpr int kWriteHeads = 4;  // heads of one token that a half-warp writes, keys and values
-constexpr float kTop8[2] = {448.f, 127.f};  // largest code: E4M3, INT8
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100: below it a row is stored as zeros
 
-__device__ __forceinline__ uint32_t half_warp_max(uint32_t v, uint32_t mask) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(mask, v, o));
-    return v;
-}
-
+// Four codes of v * r.  INT8: adding 1.5 * 2^23 rounds to a whole number, half to even, whose
+// low byte is the code (conversions to integers run at a quarter of the rate).
 template <int FMT>
 __device__ __forceinline__ uint32_t codes4(const float v[4], float r) {
+    const float2 r2 = make_float2(r, r);
+    float2 x = __fmul2_rn(make_float2(v[0], v[1]), r2), y = __fmul2_rn(make_float2(v[2], v[3]), r2);
     if constexpr (FMT == PF_E4M3) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * r, v[1] * r), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * r, v[3] * r), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
         return lo | hi << 16;
     } else {
-        uint32_t w = 0;
-#pragma unroll
-        for (int k = 0; k < 4; k++) w |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(v[k] * r) << (8 * k);
-        return w;
+        const float2 k = make_float2(12582912.f, 12582912.f);
+        x = __fadd2_rn(x, k);
+        y = __fadd2_rn(y, k);
+        return __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
+                           __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
     }
 }
 
-// One row of one pool: pieces a and b of every lane, at row index `row`.
-template <int FMT>
-__device__ __forceinline__ void put_row(void *pool, float *scales, int64_t row, const Pieces &at, int l,
-                                        const float a[4], const float b[4], uint32_t mask, bool &bad) {
-    if constexpr (FMT == PF_F16 || FMT == PF_BF16) {
-        constexpr int DT = FMT == PF_F16 ? DT_F16 : DT_BF16;
-        store4<DT>(pool, row * kD + at.a, a);
-        store4<DT>(pool, row * kD + at.b, b);
+// Bits of the largest magnitude of a lane's eight channels, as fp32.
+template <int DT>
+__device__ __forceinline__ uint32_t raw_max(const Raw8<DT> &r) {
+    if constexpr (DT == DT_F32) {
+        const uint32_t k = 0x7FFFFFFFu;
+        auto b = [&](float x) { return __float_as_uint(x) & k; };
+        return max(max(max(b(r.a.w.x), b(r.a.w.y)), max(b(r.a.w.z), b(r.a.w.w))),
+                   max(max(b(r.b.w.x), b(r.b.w.y)), max(b(r.b.w.z), b(r.b.w.w))));
     } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            m = max(m, max(__float_as_uint(a[k]) & 0x7FFFFFFFu, __float_as_uint(b[k]) & 0x7FFFFFFFu));
-        m = half_warp_max(m, mask);
-        const float top = FMT == PF_E4M3 ? kTop8[0] : kTop8[1];
-        const float amax = __uint_as_float(m);
-        const bool nonfinite = m >= 0x7F800000u, zero = nonfinite || amax < kTiny;
-        const float r = zero ? 0.f : __fdiv_rn(top, amax);
-        uint32_t wa = 0, wb = 0;
-        if (!zero) {
-            wa = codes4<FMT>(a, r);
-            wb = codes4<FMT>(b, r);
-        }
-        uint8_t *dst = static_cast<uint8_t *>(pool) + row * kD;
-        *reinterpret_cast<uint32_t *>(dst + at.a) = wa;
-        *reinterpret_cast<uint32_t *>(dst + at.b) = wb;
-        if (l == 0)
-            scales[row] = nonfinite ? __uint_as_float(0x7FC00000u) : zero ? 0.f : __fdiv_rn(amax, top);
-        bad |= nonfinite;
+        const uint32_t k = 0x7FFF7FFFu;
+        const uint32_t m = __vmaxu2(__vmaxu2(r.a.w.x & k, r.a.w.y & k), __vmaxu2(r.b.w.x & k, r.b.w.y & k));
+        const uint32_t h = max(m & 0xFFFFu, m >> 16);
+        if constexpr (DT == DT_BF16) return h << 16;
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
     }
+}
+__device__ __forceinline__ uint32_t float_max(const float v[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; k++) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+    return m;
 }
 }  // namespace
 
-template <int DT, int FMT>
+// SPLIT: keys are turned in the half layout.
+template <int DT, int FMT, bool SPLIT>
 __global__ void __launch_bounds__(256) k_page_write(PWritePlan p) {
     pdl_begin();
+    constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
     const int l = threadIdx.x & 15;
     const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
     const int groups = (p.heads + kWriteHeads - 1) / kWriteHeads;
@@ -78,18 +74,18 @@ __global__ void __launch_bounds__(256) k_page_write(PWritePlan p) {
     if (token >= p.n) return;
     const int h0 = (int)(unit - token * groups) * kWriteHeads, nh = min(p.heads - h0, kWriteHeads);
     const Pieces at = pieces_of(l, p.r);
-    Rotary straight = p.r;
-    straight.rot = 0;
-    const Pieces vat = pieces_of(l, straight);
-    Raw4<DT> ka[kWriteHeads], kb[kWriteHeads], va[kWriteHeads], vb[kWriteHeads];
+    Pieces straight;
+    straight.a = 8 * l;
+    straight.b = 8 * l + 4;
+    Raw8<DT> k[kWriteHeads], v[kWriteHeads];
 #pragma unroll
     for (int u = 0; u < kWriteHeads; u++) {
         if (u < nh) {
-            const int64_t k = token * p.kt + (h0 + u) * p.kh, v = token * p.vt + (h0 + u) * p.vh;
-            ka[u] = load_raw4<DT>(p.K, k + at.a);
-            kb[u] = load_raw4<DT>(p.K, k + at.b);
-            va[u] = load_raw4<DT>(p.V, v + vat.a);
-            vb[u] = load_raw4<DT>(p.V, v + vat.b);
+            k[u] = load_raw8<DT, SPLIT>(p.K, token * p.kt + (h0 + u) * p.kh, at);
+            v[u] = load_raw8<DT, false>(p.V, token * p.vt + (h0 + u) * p.vh, straight);
+        } else {
+            k[u] = Raw8<DT>{};
+            v[u] = Raw8<DT>{};
         }
     }
     const int64_t slot = __ldg(reinterpret_cast<const long long *>(p.slots) + token);
@@ -101,42 +97,113 @@ __global__ void __launch_bounds__(256) k_page_write(PWritePlan p) {
         return;
     }
     const int64_t row0 = ((page * p.heads + h0) << shift) + (slot & (p.page - 1));
-    Turn t;
-    if (at.turned) t = turn_of(p.r, token, l, 1.f);
-    bool bad = false;
+    const bool turns = p.r.rot > 0;  // the same for every lane
+    float kf[kWriteHeads][8];
+    if (turns) {
+        Turn t;
+        if (at.turned) t = turn_of(p.r, token, l, 1.f);
 #pragma unroll
-    for (int u = 0; u < kWriteHeads; u++) {
-        if (u < nh) {
-            const int64_t row = row0 + ((int64_t)u << shift);
-            float a[4], b[4];
-            unpack4(ka[u], a);
-            unpack4(kb[u], b);
+        for (int u = 0; u < kWriteHeads; u++) {
+            unpack4(k[u].a, kf[u]);
+            unpack4(k[u].b, kf[u] + 4);
             if (at.turned) {
-                if (p.r.interleaved)
-                    apply_turn<true>(a, b, t);
+                if (SPLIT)
+                    apply_turn<false>(kf[u], kf[u] + 4, t);
                 else
-                    apply_turn<false>(a, b, t);
+                    apply_turn<true>(kf[u], kf[u] + 4, t);
             }
-            put_row<FMT>(p.k, p.ks, row, at, l, a, b, mask, bad);
-            unpack4(va[u], a);
-            unpack4(vb[u], b);
-            put_row<FMT>(p.v, p.vs, row, vat, l, a, b, mask, bad);
         }
     }
-    if (bad && l == 0) or_status(p.status, QVG_DEV_NONFINITE);
+    auto key = [&](int u, float x[8]) {
+        if (turns) {
+#pragma unroll
+            for (int c = 0; c < 8; c++) x[c] = kf[u][c];
+        } else {
+            unpack4(k[u].a, x);
+            unpack4(k[u].b, x + 4);
+        }
+    };
+    if constexpr (WIDE) {
+        constexpr int OUT = FMT == PF_F16 ? DT_F16 : DT_BF16;
+#pragma unroll
+        for (int u = 0; u < kWriteHeads; u++) {
+            if (u < nh) {
+                const int64_t row = row0 + ((int64_t)u << shift);
+                float x[8];
+                key(u, x);
+                store8<OUT, SPLIT>(p.k, row * kD, at, x);
+                unpack4(v[u].a, x);
+                unpack4(v[u].b, x + 4);
+                store8<OUT, false>(p.v, row * kD, straight, x);
+            }
+        }
+    } else {
+        // rows 0-3: keys of the heads, 4-7: values; lanes 2r and 2r + 1 end with row r's maximum
+        uint32_t m[8];
+#pragma unroll
+        for (int u = 0; u < kWriteHeads; u++) {
+            m[u] = turns ? float_max(kf[u]) : raw_max(k[u]);
+            m[4 + u] = raw_max(v[u]);
+        }
+#pragma unroll
+        for (int w = 4; w > 0; w >>= 1) {
+            const bool high = l & (2 * w);
+#pragma unroll
+            for (int r = 0; r < w; r++) {
+                const uint32_t mine = high ? m[r + w] : m[r], theirs = high ? m[r] : m[r + w];
+                m[r] = max(mine, __shfl_xor_sync(mask, theirs, 2 * w));
+            }
+        }
+        const uint32_t bits = max(m[0], __shfl_xor_sync(mask, m[0], 1));
+        const float top = FMT == PF_E4M3 ? 448.f : 127.f, amax = __uint_as_float(bits);
+        const bool nonfinite = bits >= 0x7F800000u, zero = nonfinite || amax < kTiny, scale = l & 1;
+        float f = zero ? 0.f : __fdiv_rn(scale ? amax : top, scale ? top : amax);
+        if (scale) {
+            const int r = l >> 1, u = r & 3;
+            if (nonfinite) f = __uint_as_float(0x7FC00000u);
+            if (u < nh) (r < 4 ? p.ks : p.vs)[row0 + ((int64_t)u << shift)] = f;
+            if (nonfinite && u < nh) or_status(p.status, QVG_DEV_NONFINITE);
+        }
+        // a row of zeros, or one that is not finite, has the quotient 0 and every code 0 (the
+        // products of infinities and NaN are made so)
+#pragma unroll
+        for (int r = 0; r < 8; r++) {
+            const float q = __shfl_sync(mask, f, (threadIdx.x & 16) + 2 * r);
+            const int u = r & 3;
+            if (u < nh) {
+                float x[8];
+                if (r < 4) {
+                    key(u, x);
+                } else {
+                    unpack4(v[u].a, x);
+                    unpack4(v[u].b, x + 4);
+                }
+                uint2 w = make_uint2(codes4<FMT>(x, q), codes4<FMT>(x + 4, q));
+                if (q == 0.f) w = make_uint2(0u, 0u);
+                uint8_t *dst = static_cast<uint8_t *>(r < 4 ? p.k : p.v) + (row0 + ((int64_t)u << shift)) * kD;
+                if (SPLIT && r < 4 && at.b != at.a + 4) {
+                    *reinterpret_cast<uint32_t *>(dst + at.a) = w.x;
+                    *reinterpret_cast<uint32_t *>(dst + at.b) = w.y;
+                } else {
+                    *reinterpret_cast<uint2 *>(dst + 8 * l) = w;
+                }
+            }
+        }
+    }
 }
 
 cudaError_t launch_page_write(const PWritePlan &p, cudaStream_t st) {
     const int64_t units = p.n * ((p.heads + kWriteHeads - 1) / kWriteHeads);
     const dim3 grid((unsigned)((units + 15) / 16));
     auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(256), 0, st, p); };
+    const bool split = p.r.rot > 0 && !p.r.interleaved;
     auto by_format = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         switch (p.fmt) {
-            case PF_F16: return go(k_page_write<DT, PF_F16>);
-            case PF_BF16: return go(k_page_write<DT, PF_BF16>);
-            case PF_E4M3: return go(k_page_write<DT, PF_E4M3>);
-            default: return go(k_page_write<DT, PF_INT8>);
+            case PF_F16: return split ? go(k_page_write<DT, PF_F16, true>) : go(k_page_write<DT, PF_F16, false>);
+            case PF_BF16: return split ? go(k_page_write<DT, PF_BF16, true>) : go(k_page_write<DT, PF_BF16, false>);
+            case PF_E4M3: return split ? go(k_page_write<DT, PF_E4M3, true>) : go(k_page_write<DT, PF_E4M3, false>);
+            default: return split ? go(k_page_write<DT, PF_INT8, true>) : go(k_page_write<DT, PF_INT8, false>);
         }
     };
     return p.dtype == DT_F32    ? by_format(std::integral_constant<int, DT_F32>{})

@@ -26,25 +26,18 @@ __global__ void __launch_bounds__(256) k_rope(RopePlan p) {
     Turn t;
     if (at.turned) t = turn_of(p.r, token, l, p.backward ? -1.f : 1.f);
     for (int h = h0; h < h1; h += kRopeRows) {
-        Raw4<DT> ra[kRopeRows], rb[kRopeRows];
+        Raw8<DT> raw[kRopeRows];
+#pragma unroll
+        for (int u = 0; u < kRopeRows; u++)
+            if (h + u < h1) raw[u] = load_raw8<DT, !INTER>(p.X, token * p.xt + (h + u) * p.xh, at);
 #pragma unroll
         for (int u = 0; u < kRopeRows; u++) {
             if (h + u < h1) {
-                const int64_t x = token * p.xt + (h + u) * p.xh;
-                ra[u] = load_raw4<DT>(p.X, x + at.a);
-                rb[u] = load_raw4<DT>(p.X, x + at.b);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeRows; u++) {
-            if (h + u < h1) {
-                float a[4], b[4];
-                unpack4(ra[u], a);
-                unpack4(rb[u], b);
-                if (at.turned) apply_turn<INTER>(a, b, t);
-                const int64_t y = token * p.yt + (h + u) * p.yh;
-                store4<DT>(p.Y, y + at.a, a);
-                store4<DT>(p.Y, y + at.b, b);
+                float v[8];
+                unpack4(raw[u].a, v);
+                unpack4(raw[u].b, v + 4);
+                if (at.turned) apply_turn<INTER>(v, v + 4, t);
+                store8<DT, !INTER>(p.Y, token * p.yt + (h + u) * p.yh, at, v);
             }
         }
     }

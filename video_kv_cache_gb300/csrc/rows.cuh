@@ -76,6 +76,37 @@ __device__ __forceinline__ void store4(void *Y, int64_t off, const float v[4]) {
             make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
 }
 
+// Both pieces of a lane: eight neighbouring channels in one access, or (SPLIT, for a turned
+// lane of the half layout) four and four.
+template <int DT>
+struct Raw8 {
+    Raw4<DT> a, b;
+};
+template <int DT, bool SPLIT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const void *X, int64_t off, const Pieces &at) {
+    Raw8<DT> r;
+    if (DT == DT_F32 || (SPLIT && at.b != at.a + 4)) {
+        r.a = load_raw4<DT>(X, off + at.a);
+        r.b = load_raw4<DT>(X, off + at.b);
+    } else if constexpr (DT != DT_F32) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(X) + off + at.a));
+        r.a.w = make_uint2(w.x, w.y);
+        r.b.w = make_uint2(w.z, w.w);
+    }
+    return r;
+}
+template <int DT, bool SPLIT>
+__device__ __forceinline__ void store8(void *Y, int64_t off, const Pieces &at, const float v[8]) {
+    if (DT == DT_F32 || (SPLIT && at.b != at.a + 4)) {
+        store4<DT>(Y, off + at.a, v);
+        store4<DT>(Y, off + at.b, v + 4);
+    } else if constexpr (DT != DT_F32) {
+        auto pk = [](float lo, float hi) { return DT == DT_BF16 ? pack_bf16(lo, hi) : pack_f16(lo, hi); };
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(Y) + off + at.a) =
+            make_uint4(pk(v[0], v[1]), pk(v[2], v[3]), pk(v[4], v[5]), pk(v[6], v[7]));
+    }
+}
+
 // The turn of a lane's four pairs for one token: sines and cosines times mscale.  position *
 // frequency is exact modulo a turn in 64 bits; its top 32 bits, read as a signed fraction of
 // a turn, are converted to fp32 (relative error 2^-24) and go to sincospif, which reduces
