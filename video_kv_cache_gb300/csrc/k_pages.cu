@@ -16,6 +16,9 @@ namespace qvg {
 
 namespace {
 constexpr int kWriteHeads = 4;  // heads of one token that a half-warp writes, keys and values
+// 24 warps an SM: 32760 x 12 heads in int8 take 51 us; 16 warps with all the registers they
+// want 61, 32 with spills 62
+constexpr int kWriteThreads = 128, kWriteCtas = 6;
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100: below it a row is stored as zeros
 
 // Four codes of v * r.  INT8: adding 1.5 * 2^23 rounds to a whole number, half to even, whose
@@ -63,13 +66,13 @@ __device__ __forceinline__ uint32_t float_max(const float v[8]) {
 
 // SPLIT: keys are turned in the half layout.
 template <int DT, int FMT, bool SPLIT>
-__global__ void __launch_bounds__(256) k_page_write(PWritePlan p) {
+__global__ void __launch_bounds__(kWriteThreads, kWriteCtas) k_page_write(PWritePlan p) {
     pdl_begin();
     constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
     const int l = threadIdx.x & 15;
     const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
     const int groups = (p.heads + kWriteHeads - 1) / kWriteHeads;
-    const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int64_t unit = (int64_t)blockIdx.x * (kWriteThreads / 16) + (threadIdx.x >> 4);
     const int64_t token = unit / groups;
     if (token >= p.n) return;
     const int h0 = (int)(unit - token * groups) * kWriteHeads, nh = min(p.heads - h0, kWriteHeads);
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(256) k_page_write(PWritePlan p) {
                 uint2 w = make_uint2(codes4<FMT>(x, q), codes4<FMT>(x + 4, q));
                 if (q == 0.f) w = make_uint2(0u, 0u);
                 uint8_t *dst = static_cast<uint8_t *>(r < 4 ? p.k : p.v) + (row0 + ((int64_t)u << shift)) * kD;
-                if (SPLIT && r < 4 && at.b != at.a + 4) {
+                if (SPLIT && r < 4) {
                     *reinterpret_cast<uint32_t *>(dst + at.a) = w.x;
                     *reinterpret_cast<uint32_t *>(dst + at.b) = w.y;
                 } else {
@@ -194,8 +197,9 @@ __global__ void __launch_bounds__(256) k_page_write(PWritePlan p) {
 
 cudaError_t launch_page_write(const PWritePlan &p, cudaStream_t st) {
     const int64_t units = p.n * ((p.heads + kWriteHeads - 1) / kWriteHeads);
-    const dim3 grid((unsigned)((units + 15) / 16));
-    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(256), 0, st, p); };
+    constexpr int per = kWriteThreads / 16;
+    const dim3 grid((unsigned)((units + per - 1) / per));
+    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kWriteThreads), 0, st, p); };
     const bool split = p.r.rot > 0 && !p.r.interleaved;
     auto by_format = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;

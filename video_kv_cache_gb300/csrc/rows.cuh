@@ -76,8 +76,8 @@ __device__ __forceinline__ void store4(void *Y, int64_t off, const float v[4]) {
             make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
 }
 
-// Both pieces of a lane: eight neighbouring channels in one access, or (SPLIT, for a turned
-// lane of the half layout) four and four.
+// Both pieces of a lane: eight neighbouring channels in one access, or (SPLIT, the half layout)
+// four and four.
 template <int DT>
 struct Raw8 {
     Raw4<DT> a, b;
@@ -85,7 +85,7 @@ struct Raw8 {
 template <int DT, bool SPLIT>
 __device__ __forceinline__ Raw8<DT> load_raw8(const void *X, int64_t off, const Pieces &at) {
     Raw8<DT> r;
-    if (DT == DT_F32 || (SPLIT && at.b != at.a + 4)) {
+    if (DT == DT_F32 || SPLIT) {
         r.a = load_raw4<DT>(X, off + at.a);
         r.b = load_raw4<DT>(X, off + at.b);
     } else if constexpr (DT != DT_F32) {
@@ -97,7 +97,7 @@ __device__ __forceinline__ Raw8<DT> load_raw8(const void *X, int64_t off, const 
 }
 template <int DT, bool SPLIT>
 __device__ __forceinline__ void store8(void *Y, int64_t off, const Pieces &at, const float v[8]) {
-    if (DT == DT_F32 || (SPLIT && at.b != at.a + 4)) {
+    if (DT == DT_F32 || SPLIT) {
         store4<DT>(Y, off + at.a, v);
         store4<DT>(Y, off + at.b, v + 4);
     } else if constexpr (DT != DT_F32) {
