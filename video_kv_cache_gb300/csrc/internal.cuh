@@ -446,6 +446,7 @@ cudaError_t launch_page_read(const PReadPlan &p, cudaStream_t st);
 
 struct PAttnPlan {
     int B, HQ, H, G;  // sequences, query heads, key/value heads, query heads per key/value head
+    uint64_t g_inv;   // floor(2^34 / G) + 1: r / G = r * g_inv >> 34 for rows r < 2^26, G <= 128
     int page, max_pages, fmt, q_dtype, out_dtype, causal;
     int64_t n_pages, window, total_q, max_q, max_kv;
     float scale_log2;  // scale * log2(e): the softmax runs in powers of two

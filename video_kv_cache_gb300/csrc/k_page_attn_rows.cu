@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
         int row_lo[RT][2], row_hi[RT][2];
 #pragma unroll
         for (int y = 0; y < RT; y++) {
-            const int r = 8 * y + g, i = min(r, rows - 1) / p.G;
+            const int r = 8 * y + g, i = token_of(p, min(r, rows - 1));
             const uint16_t *src = static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt + (int64_t)(h * p.G + r - i * p.G) * p.qh;
             uint4 w[4];
 #pragma unroll
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
 #pragma unroll
             for (int x = 0; x < 2; x++) {
                 qmul[y][x] = __shfl_sync(0xffffffffu, mul, (2 * q + x) * 4) * p.scale_log2;
-                const int i = min(8 * y + 2 * q + x, rows - 1) / p.G;
+                const int i = token_of(p, min(8 * y + 2 * q + x, rows - 1));
                 row_lo[y][x] = seen_lo(p, sq, i);
                 row_hi[y][x] = seen_hi(p, sq, i);
             }
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             for (int c = 0; c < 16; c++) v[c] += f * s_o[w][r][(c >> 2) * 32 + part * 4 + (c & 3)];
         }
     }
-    const int row_i = min(r, rows - 1) / p.G, hq = h * p.G + min(r, rows - 1) - row_i * p.G;
+    const int row_i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - row_i * p.G;
     bool live = mine && r < rows;
     if (p.S > 1 && !joined) {
         if (!live) return;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
     const int local = (int)(w - t * p.unit), r = (p.units - 1 - u) * p.unit + local;
     const SeqInfo sq = seq_info(p, b, false);
     if (r >= sq.qn * p.G) return;
-    const int i = r / p.G, hq = h * p.G + r - i * p.G;
+    const int i = token_of(p, r), hq = h * p.G + r - i * p.G;
     const int64_t at = t * p.S * p.unit + local;  // + split * unit
     float mx = -INFINITY;
     for (int s = lane; s < p.S; s += 32) mx = fmaxf(mx, p.ml[2 * (at + s * p.unit)]);

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     const int rows = sq.qn * p.G, r0 = pair * 2 * kTcM;
     if (r0 >= rows) return;
     const int nt = rows - r0 > kTcM ? 2 : 1;  // row tiles in use
-    const int lo = seen_lo(p, sq, r0 / p.G), hi = seen_hi(p, sq, (min(rows, r0 + 2 * kTcM) - 1) / p.G);
+    const int lo = seen_lo(p, sq, token_of(p, r0)), hi = seen_hi(p, sq, token_of(p, min(rows, r0 + 2 * kTcM) - 1));
     int n = 0, j0 = 0;  // this split's key tiles
     if (lo < hi) {
         const int t_lo = lo / kTcN, all = (hi + kTcN - 1) / kTcN - t_lo, per = (all + S - 1) / S;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             uint4 w[EACH];  // every read in flight before the first is used; whole warps, 16 lanes a row
 #pragma unroll
             for (int u = 0; u < EACH; u++) {
-                const int x = threadIdx.x + u * 512, r = r0 + (x >> 4), i = r / p.G;
+                const int x = threadIdx.x + u * 512, r = r0 + (x >> 4), i = token_of(p, r);
                 w[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (r < rows)
                     w[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             // the tiles that every row of this warp sees whole: [open, shut)
             int open, shut;
             {
-                const int a = min(r - lane, rows - 1) / p.G, z = min(r - lane + 31, rows - 1) / p.G;
+                const int a = token_of(p, min(r - lane, rows - 1)), z = token_of(p, min(r - lane + 31, rows - 1));
                 open = (seen_lo(p, sq, z) + kTcN - 1) / kTcN - j0;
                 shut = seen_hi(p, sq, a) / kTcN - j0;
             }
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         }
                     }
                     if (masked) {
-                        const int k0 = (j0 + j) * kTcN + half * 64 + hc, i = min(r, rows - 1) / p.G;
+                        const int k0 = (j0 + j) * kTcN + half * 64 + hc, i = token_of(p, min(r, rows - 1));
                         const int a = seen_lo(p, sq, i) - k0, z = seen_hi(p, sq, i) - k0;
 #pragma unroll
                         for (int c = 0; c < 32; c++) s[c] = c >= a && c < z ? s[c] : -INFINITY;
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     if constexpr (!WIDE) {
                         const uint4 odd = *reinterpret_cast<const uint4 *>(sh.vnan[buf]);
                         if (odd.x | odd.y | odd.z | odd.w) {
-                            const int k0 = (j0 + j) * kTcN + half * 64, i = min(r, rows - 1) / p.G;
+                            const int k0 = (j0 + j) * kTcN + half * 64, i = token_of(p, min(r, rows - 1));
                             const uint64_t bits = half ? odd.z | (uint64_t)odd.w << 32 : odd.x | (uint64_t)odd.y << 32;
                             for (int c = 0; c < 64; c++)
                                 if (bits >> c & 1 && k0 + c >= seen_lo(p, sq, i) && k0 + c < seen_hi(p, sq, i)) l = NAN;
@@ -728,21 +728,41 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             l += xl[(half ^ 1) * kTcM + row];
             tc_fence_after();
             if (ok) {
-                const int i = min(r, rows - 1) / p.G, hq = h * p.G + min(r, rows - 1) - i * p.G;
+                const int i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - i * p.G;
                 const bool live = r < rows, whole = S == 1;
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
                 if constexpr (!WIDE) inv = ldexpf(inv, e - kValueShift);
                 const int64_t tok = sq.q0 + i;
                 const int64_t part = (tail * S + split) * p.unit + t * kTcM + row;
-                const int64_t out = tok * p.ot + hq * p.oh;
+                // The rows go out through shared memory, in the place of this tile's Q, which
+                // every product has read: a thread leaves 128 bytes of its row there at a time
+                // (64 channels in 16 bits, 32 in fp32; swizzled), and eight lanes write a row's
+                // 128 bytes out together.  (Each thread writing its own row, 8 bytes at a time
+                // 32 rows apart, took 6 us of a CTA's end.)
+                const bool narrow = whole && p.out_dtype != DT_F32;
+                const int64_t elem = narrow ? 2 : 4, at = (whole ? tok * p.ot + hq * p.oh : part * kD) * elem;
+                unsigned char *dst = static_cast<unsigned char *>(whole ? p.O : p.part);
+                unsigned char *stage = sQ + t * kSlot + half * 128;  // + row * 256
                 bool odd = false;
+                auto leave = [&](int c, uint4 v) { *reinterpret_cast<uint4 *>(stage + row * 256 + ((c ^ (row & 7)) << 4)) = v; };
+                auto write_out = [&](int first_channel) {
+                    __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
+                    for (int u = 0; u < 8; u++) {
+                        const int src = u * 4 + (lane >> 3), c = lane & 7, other = quarter * 32 + src;
+                        const int64_t to = __shfl_sync(0xffffffffu, at, src) + first_channel * elem + c * 16;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + other * 256 + ((c ^ (other & 7)) << 4));
+                        if (__shfl_sync(0xffffffffu, (int)live, src)) *reinterpret_cast<uint4 *>(dst + to) = v;
+                    }
+                    __syncwarp();
+                };
+#pragma unroll
+                for (int hc = 0; hc < 64; hc += 32) {
                     float o[32];
                     __syncwarp();
                     if (n > 0) {
-                        tc_ld32(o_at + c, o);
+                        tc_ld32(o_at + hc, o);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; k++) o[k] = 0.f;
@@ -752,17 +772,21 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         o[k] *= inv;
                         odd |= !is_finite(o[k]);
                     }
-                    if (live) {
-                        const int ch = half * 64 + c;
-                        if (!whole) {
+                    if (narrow) {
+                        auto pk = [&](int k) {
+                            return p.out_dtype == DT_BF16 ? pack_bf16(o[k], o[k + 1]) : pack_f16(o[k], o[k + 1]);
+                        };
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) store4<DT_F32>(p.part, part * kD + ch + k, o + k);
-                        } else {
+                        for (int k = 0; k < 32; k += 8) leave((hc + k) >> 3, make_uint4(pk(k), pk(k + 2), pk(k + 4), pk(k + 6)));
+                    } else {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) store_out4(p, out + ch + k, o + k);
-                        }
+                        for (int k = 0; k < 32; k += 4)
+                            leave(k >> 2, make_uint4(__float_as_uint(o[k]), __float_as_uint(o[k + 1]), __float_as_uint(o[k + 2]),
+                                                     __float_as_uint(o[k + 3])));
+                        write_out(half * 64 + hc);
                     }
                 }
+                if (narrow) write_out(half * 64);
                 if (!whole) {
                     if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, l);
                 } else {

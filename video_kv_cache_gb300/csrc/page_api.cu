@@ -109,6 +109,7 @@ PAttnPlan attention_plan(const qvg_page_attention_params *prm) {
     p.HQ = prm->n_q_heads;
     p.H = prm->n_heads;
     p.G = p.HQ / p.H;
+    p.g_inv = (uint64_t(1) << 34) / (uint64_t)p.G + 1;
     p.page = prm->page_tokens;
     p.max_pages = prm->max_pages;
     p.fmt = prm->format;

@@ -34,6 +34,10 @@ __device__ __forceinline__ SeqInfo seq_info(const PAttnPlan &p, int b, bool repo
     return s;
 }
 
+// Query token of a row (tokens x grouped heads).  r * (G * g_inv - 2^34) <= r * G < 2^34, so the
+// quotient is exact.
+__device__ __forceinline__ int token_of(const PAttnPlan &p, int r) { return (int)((uint64_t)(uint32_t)r * p.g_inv >> 34); }
+
 // Keys [lo, hi) that query i of the sequence sees (empty when lo >= hi).
 __device__ __forceinline__ int seen_lo(const PAttnPlan &p, const SeqInfo &s, int i) {
     if (p.window <= 0) return 0;
