@@ -343,6 +343,9 @@ ATTEND = [  # q lengths, cached lengths, q heads, heads, q type, format, page, c
     ([64], [3000], 1, 1, BF, BF, 64, True, 0),                  # many splits of one tile
     ([31], [31], 128, 1, BF, BF, 16, True, 0),                  # 128 query heads share one
     ([513], [640], 5, 5, HF, HF, 128, True, 0),
+    ([257], [1100], 77, 77, BF, BF, 64, True, 0),               # more than a round: whole items, split ones
+    ([40, 20], [2500, 900], 2, 2, HF, I8, 16, True, 0),         # few items of unlike sequences: all split
+    ([2], [5000], 8, 1, BF, E4, 128, True, 3000),               # 16 rows, splits through memory
 ]
 
 
