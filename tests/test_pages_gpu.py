@@ -457,6 +457,24 @@ def test_what_a_query_does_not_see_cannot_change_it(fmt, nq, n, group):
         assert bool(got[-3:].isnan().all())
 
 
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("size", [0.0, 1e-30, 1e30])
+def test_queries_and_keys_of_extreme_sizes(fmt, size):
+    # rows of zeros in the cache (scale 0), queries whose products with anything vanish
+    g = _gen(15)
+    n, nq = 200, 60
+    kv, table = _cache(g, [n], 1, fmt, 32)
+    for j in range(0, n, 2) if size else range(n):
+        page, row = int(table[0, j // 32]), j % 32
+        kv.k[page, 0, row].view(torch.uint8).zero_()
+        if kv.k_scale is not None:
+            kv.k_scale[page, 0, row] = 0.0
+    Q = (torch.randn((nq, 2, 128), generator=g) * (size or 1e-30)).to(BF)
+    scale = 1e-31 if size > 1 else 0.1
+    _check(Q, kv, table, [n], [nq], True, 0, scale=scale)
+    _check(Q[:4], kv, table, [n], [4], True, 0, scale=scale)
+
+
 def test_page_attention_reports_bad_arguments_on_the_device():
     g = _gen(10)
     kv, table = _cache(g, [60, 60], 1, BF, 16)

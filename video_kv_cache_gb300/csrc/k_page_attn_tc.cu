@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 float s[TWICE ? 32 : 64], mx = -INFINITY, mult = row_mult;
                 if (ok) {
                     tc_fence_after();
-                    if constexpr (FOLD) mult *= __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23);
+                    // (kept above 0, so that -infinity times it stays -infinity)
+                    if constexpr (FOLD) mult = fmaxf(mult * __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23), 1.2e-38f);
                     if constexpr (TWICE) {
                         tc_ld32(s_at + half * 64, s);
                         finish(0, s);

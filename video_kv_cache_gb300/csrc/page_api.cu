@@ -2,6 +2,7 @@
 // qvg_page_read and qvg_page_attention.  Declarations and their contracts are in
 // include/qvg.h.
 #include <cmath>
+#include <limits>
 
 #include "internal.cuh"
 #include "qvg.h"
@@ -123,7 +124,7 @@ PAttnPlan attention_plan(const qvg_page_attention_params *prm) {
     p.max_kv = std::min(prm->max_kv, (int64_t)prm->max_pages * prm->page_tokens);
     // (a scale of zero keeps a trace, so that -infinity times it stays -infinity)
     p.scale_log2 = prm->scale * 1.4426950408889634f;
-    if (std::fabs(p.scale_log2) < 1e-30f) p.scale_log2 = 1e-30f;
+    if (std::fabs(p.scale_log2) < std::numeric_limits<float>::min()) p.scale_log2 = std::numeric_limits<float>::min();
     p.qt = prm->q_token_stride;
     p.qh = prm->q_head_stride;
     p.ot = prm->o_token_stride;
