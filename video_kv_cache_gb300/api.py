@@ -92,7 +92,7 @@ def _stream_handle(stream):
     if stream is not None:
         return stream.cuda_stream
     # the raw handle of the current stream, without the Stream object around it
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def quantize(X: torch.Tensor, C: int, T: int, bits: int, group: int, iters: int, seed: int = 0,

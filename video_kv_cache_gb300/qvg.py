@@ -340,33 +340,33 @@ def qvg_attention(params: qvg_attention_params, Q: int, k_cache: qvg_buffers,
 
 def qvg_rope(params: qvg_rope_params, rotary: qvg_rotary, X: int, Y: int,
              stream: int | None) -> int:
-    return int((_lib or load()).qvg_rope(_ref(params), _ref(rotary), X, Y, stream))
+    return (_lib or load()).qvg_rope(_ref(params), _ref(rotary), X, Y, stream)
 
 
 def qvg_page_write(params: qvg_page_write_params, K: int, V: int, slots: int,
                    rotary: qvg_rotary | None, pages: qvg_pages, dev_status: int | None,
                    stream: int | None) -> int:
-    return int((_lib or load()).qvg_page_write(_ref(params), K, V, slots, _ref(rotary), _ref(pages),
-                                     dev_status, stream))
+    return (_lib or load()).qvg_page_write(_ref(params), K, V, slots, _ref(rotary), _ref(pages),
+                                           dev_status, stream)
 
 
 def qvg_page_read(params: qvg_page_read_params, pages: qvg_pages, page_table: int,
                   seq_lens: int, X: int, dev_status: int | None, stream: int | None) -> int:
-    return int((_lib or load()).qvg_page_read(_ref(params), _ref(pages), page_table, seq_lens, X,
-                                    dev_status, stream))
+    return (_lib or load()).qvg_page_read(_ref(params), _ref(pages), page_table, seq_lens, X,
+                                          dev_status, stream)
 
 
 def qvg_page_attention_workspace_bytes(params: qvg_page_attention_params) -> int:
-    return int((_lib or load()).qvg_page_attention_workspace_bytes(_ref(params)))
+    return (_lib or load()).qvg_page_attention_workspace_bytes(_ref(params))
 
 
 def qvg_page_attention(params: qvg_page_attention_params, Q: int, pages: qvg_pages,
                        page_table: int, seq_lens: int, cu_q: int | None, O: int,
                        lse: int | None, workspace: int | None, workspace_bytes: int,
                        dev_status: int | None, stream: int | None) -> int:
-    return int((_lib or load()).qvg_page_attention(_ref(params), Q, _ref(pages), page_table, seq_lens,
-                                         cu_q, O, lse, workspace, workspace_bytes, dev_status,
-                                         stream))
+    return (_lib or load()).qvg_page_attention(_ref(params), Q, _ref(pages), page_table, seq_lens,
+                                               cu_q, O, lse, workspace, workspace_bytes, dev_status,
+                                               stream)
 
 
 def qvg_status_string(code: int) -> str:
