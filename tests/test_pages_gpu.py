@@ -68,6 +68,20 @@ def test_rope(case):
     assert torch.equal(got[..., rot:].cpu(), X[..., rot:])  # the rest is untouched
 
 
+@pytest.mark.parametrize("far", [1, 3000, 2 ** 20])
+def test_rope_angles_to_the_last_place(far):
+    # sine and cosine within 3/4 of a step below 1 (2^-24), a product and a fused sum rounded by
+    # at most 2^-24 each of |u| + |w|, and the angle cut to 2^-32 of a turn: 2.8 * 2^-24 in all
+    g = _gen(far)
+    freqs, _ = api.rope_frequencies(128)
+    table = api.rope_table(128, freqs=freqs)
+    X = torch.randn((2000, 2, 128), generator=g)
+    pos = torch.randint(-far, far + 1, (1, 2000), generator=g)
+    want, err = pm.rotate(X, pos, freqs.tolist(), table.sections, False)
+    bound = err * (2.8 * 2.0 ** -24 / pm.ROTATE) + 2.0 ** -51 * far * X.double().abs().amax()
+    _within(api.rope(X.cuda(), pos.cuda(), table), want, bound, "rope")
+
+
 def test_rope_strides_in_place_and_broadcast():
     g = _gen(5)
     freqs, _ = api.rope_frequencies(64)

@@ -107,10 +107,34 @@ __device__ __forceinline__ void store8(void *Y, int64_t off, const Pieces &at, c
     }
 }
 
+// Sine and cosine of 2 pi a / 2^32, each within 0.75 of a unit in the last place (a code is
+// rounded after the turn, and an error of the angle moves it across more borders).  The nearest
+// quarter turn is taken off in whole numbers; the rest, at most pi / 4, is the sum th + tl of
+// two fp32 numbers (a 30-bit product with 2 pi / 2^32, itself in two parts).  Then the Taylor
+// series, to th^9 and th^10 (what is left out is below 2^-29), with what rounding 1 - th^2 / 2
+// loses added back.
+__device__ __forceinline__ void sincos_turn(uint32_t a, float &s, float &c) {
+    const uint32_t quarter = (a + 0x20000000u) >> 30;
+    const int rest = (int)(a - (quarter << 30));
+    const float hi = (float)rest, lo = (float)(rest - (int)hi);
+    const float kC = 1.46291807926715969e-9f;                               // 2 pi / 2^32 in fp32
+    const float kD = (float)(1.46291807926715968105e-9 - (double)kC);       // and what that leaves
+    const float th = hi * kC, tl = __fmaf_rn(hi, kC, -th) + __fmaf_rn(hi, kD, lo * kC);
+    const float z = th * th, zl = __fmaf_rn(th, th, -z);
+    const float ps = z * (-1.f / 6 + z * (1.f / 120 + z * (-1.f / 5040 + z * (1.f / 362880))));
+    const float sn = th + __fmaf_rn(th, ps, __fmaf_rn(-0.5f * z, tl, tl));
+    const float h = 0.5f * z, one = 1.f - h, lost = (1.f - one) - h;
+    const float pc = z * (1.f / 24 + z * (-1.f / 720 + z * (1.f / 40320 + z * (-1.f / 3628800))));
+    const float cs = one + (lost + __fmaf_rn(z, pc, __fmaf_rn(-th, tl, -0.5f * zl)));
+    const bool swap = quarter & 1u;
+    s = swap ? cs : sn;
+    c = swap ? sn : cs;
+    if (quarter & 2u) s = -s;
+    if ((quarter + 1u) & 2u) c = -c;
+}
+
 // The turn of a lane's four pairs for one token: sines and cosines times mscale.  position *
-// frequency is exact modulo a turn in 64 bits; its top 32 bits, read as a signed fraction of
-// a turn, are converted to fp32 (relative error 2^-24) and go to sincospif, which reduces
-// nothing and errs by a few units in the last place.
+// frequency is exact modulo a turn in 64 bits, of which the upper 32 are taken (rounded).
 struct Turn {
     float c[4], s[4];
 };
@@ -123,7 +147,7 @@ __device__ __forceinline__ Turn turn_of(const Rotary &r, int64_t token, int l, f
         const uint64_t w = __ldg(reinterpret_cast<const unsigned long long *>(r.freqs) + p) *
                            (uint64_t)__ldg(reinterpret_cast<const long long *>(r.pos) + axis * r.pos_stride + token);
         float s, c;
-        sincospif((float)(int32_t)(uint32_t)(w >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+        sincos_turn((uint32_t)((w + 0x80000000ull) >> 32), s, c);
         t.c[k] = c * r.mscale;
         t.s[k] = s * (r.mscale * sign);
     }
