@@ -45,14 +45,15 @@ constexpr int kTcM = 128;                  // rows of a row tile
 constexpr int kTcN = 128;                  // keys of a key tile
 constexpr uint32_t kHalf = kTcM * 128;     // 64 channels of 128 rows: 16 KB
 constexpr uint32_t kSlot = 2 * kHalf;      // a whole 16-bit tile: 32 KB
-constexpr uint32_t kRaw = kTcN * kD;       // a tile of 8-bit codes: 16 KB
+constexpr int kRawKeys = 64;               // keys of a raw tile of 8-bit codes, half a key tile
+constexpr uint32_t kRaw = kRawKeys * kD;   // 8 KB
 constexpr int kValueShift = 4, kKeyShift = 6;  // 8-bit values and keys over their references, times 2^this
 constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
 
 template <int FMT>
 struct TcShape {
     static constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
-    static constexpr int SLOTS = WIDE ? 5 : 3;       // ring of 16-bit tiles
+    static constexpr int SLOTS = WIDE ? 5 : 4;       // ring of 16-bit tiles
     static constexpr int RAWS = 3;                   // ring of raw 8-bit tiles
     // 16 softmax warps; MMA, loads and two idle ones (registers move by groups of four warps);
     // 8-bit: four that widen keys and four that widen values (four for both keep the tensor
@@ -371,32 +372,39 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             }
         } else if (warp == LOAD_WARP) {
             // ---------------------------------------------------------------- TMA loads
-            const int shift = 31 - __clz(p.page), per_tile = kTcN >> shift;
+            const int page_shift = 31 - __clz(p.page);
+            // what one copy brings: a page, or half of one of 128 tokens where the ring's tiles
+            // have 64
+            const int shift = WIDE ? page_shift : min(page_shift, 6), per_tile = kTcN >> shift;
             bool bad = false, ok = true;
             uint32_t edges = 0, issued = 0;
             constexpr int RING = WIDE ? SLOTS : T::RAWS;
+            constexpr uint32_t PER_KEYS = WIDE ? 2 : 4;  // ring items of a key tile: K and V, or their halves
             // the pages of a tile that hold a key some row sees, a lane each; looked up one
             // tile ahead
             auto in_sight = [&](int k0) {
                 const int token = k0 + (lane << shift);
-                return lane < per_tile && token < hi && token + p.page > lo;
+                return lane < per_tile && token < hi && token + (1 << shift) > lo;
             };
             auto row_of = [&](int k0) {
-                return in_sight(k0) ? (int)((page_of(p, b, k0 + (lane << shift), shift, bad) * p.H + h) << shift) : 0;
+                const int token = k0 + (lane << shift);
+                return in_sight(k0) ? (int)((page_of(p, b, token, page_shift, bad) * p.H + h) << page_shift) +
+                                          (token & (p.page - 1))
+                                    : 0;
             };
             int row = 0, row_next = n > 0 ? row_of(j0 * kTcN) : 0;
-            for (uint32_t it = 0; ok && it < 2u * n; it++) {
-                const int k0 = (j0 + (int)(it >> 1)) * kTcN, slot = it % RING;
-                const bool value = it & 1;
-                if (!value) {
+            for (uint32_t it = 0; ok && it < PER_KEYS * n; it++) {
+                const int k0 = (j0 + (int)(it / PER_KEYS)) * kTcN, slot = it % RING;
+                const bool value = WIDE ? it & 1 : it & 2;
+                if (it % PER_KEYS == 0) {
                     row = row_next;
-                    if (it + 2 < 2u * n) row_next = row_of(k0 + kTcN);
+                    if (it + PER_KEYS < PER_KEYS * n) row_next = row_of(k0 + kTcN);
                 }
                 uint64_t &full = WIDE ? sh.full[slot] : sh.raw_full[slot];
                 ok = wait(WIDE ? sh.empty[slot] : sh.raw_empty[slot], it / RING + 1);
                 ok = !__any_sync(0xffffffffu, !ok);
                 if (!ok) break;
-                const bool mine = in_sight(k0);
+                const bool mine = in_sight(k0) && (WIDE || (uint32_t)(lane << shift) / kRawKeys == (it & 1));
                 const uint32_t pages = __popc(__ballot_sync(0xffffffffu, mine));
                 // a value tile at the edge of what is seen, whose outer rows must be zeroed
                 const bool edge = WIDE && value && (((lo - k0) & 15 && lo > k0) || ((hi - k0) & 15 && hi < k0 + kTcN));
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         tma_load_2d(dst, map, 0, row, bar);
                         tma_load_2d(dst + kHalf, map, 64, row, bar);
                     } else {
-                        tma_load_2d(smem_u32(sRaw) + slot * kRaw + ((uint32_t)lane << shift) * kD, map, 0, row, bar);
+                        tma_load_2d(smem_u32(sRaw) + slot * kRaw + (((uint32_t)lane << shift) & (kRawKeys - 1)) * kD, map, 0, row, bar);
                     }
                 }
                 issued = it + 1;
@@ -461,7 +469,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             unsigned char *dst0 = sKV + (c >> 2) * kHalf + rb * 128;
             const int d0 = ((2 * (c & 3)) ^ r8) << 4, d1 = ((2 * (c & 3) + 1) ^ r8) << 4;
             for (int j = 0; j < n; j++) {
-                const int it = 2 * j + value, k0 = (j0 + j) * kTcN, slot = it % SLOTS, raw = it % T::RAWS, buf = j & 1;
+                const int it = 2 * j + value, k0 = (j0 + j) * kTcN, slot = it % SLOTS, buf = j & 1;
                 // a value scale that is not finite: 0 here, and a bit that makes the rows NaN that
                 // see the key (and no others)
                 const uint32_t odd = __ballot_sync(0xffffffffu, !is_finite(sc));
@@ -496,36 +504,42 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
                 if (j + 1 < n) load_scale(k0 + kTcN + x);
-                ok = meet<128>(id, wait(sh.raw_full[raw], it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1));
+                ok = meet<128>(id, wait(sh.raw_full[2 * it % T::RAWS], 2 * it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1));
                 if (!ok) break;  // (otherwise all scales are there, and wmax is free again)
                 const bool whole = k0 >= lo && k0 + kTcN <= hi;
                 const uint2 *factors = (value ? sh.vf[buf] : sh.kf[buf]) + rb;
-                const unsigned char *src = src0 + raw * kRaw;
                 unsigned char *dst = dst0 + slot * kSlot;
 #pragma unroll
-                for (int u = 0; u < 8; u++) {
-                    uint4 w = *reinterpret_cast<const uint4 *>(src + u * 16 * kD);
-                    if (!whole) {  // what no row sees may hold anything
-                        const int key = k0 + rb + u * 16;
-                        if (key < lo || key >= hi) w = make_uint4(0u, 0u, 0u, 0u);
+                for (int part = 0; part < 2; part++) {
+                    const int raw = (2 * it + part) % T::RAWS;
+                    // (a warp that gives up here meets the others at the next tile)
+                    if (part) ok = wait(sh.raw_full[raw], (2 * it + 1) / T::RAWS);
+                    const unsigned char *src = src0 + raw * kRaw;
+#pragma unroll
+                    for (int v = 0; v < 4; v++) {
+                        const int u = 4 * part + v;
+                        uint4 w = *reinterpret_cast<const uint4 *>(src + v * 16 * kD);
+                        if (!whole) {  // what no row sees may hold anything
+                            const int key = k0 + rb + u * 16;
+                            if (key < lo || key >= hi) w = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        const uint2 y0 = codes_to_f16<FMT == PF_E4M3>(w.x), y1 = codes_to_f16<FMT == PF_E4M3>(w.y),
+                                    y2 = codes_to_f16<FMT == PF_E4M3>(w.z), y3 = codes_to_f16<FMT == PF_E4M3>(w.w);
+                        uint4 a0 = make_uint4(y0.x, y0.y, y1.x, y1.y), a1 = make_uint4(y2.x, y2.y, y3.x, y3.y);
+                        if constexpr (FOLD) {
+                            const uint2 f = factors[u * 16];
+                            a0 = make_uint4(scaled(a0.x, f), scaled(a0.y, f), scaled(a0.z, f), scaled(a0.w, f));
+                            a1 = make_uint4(scaled(a1.x, f), scaled(a1.y, f), scaled(a1.z, f), scaled(a1.w, f));
+                        }
+                        *reinterpret_cast<uint4 *>(dst + u * 2048 + d0) = a0;
+                        *reinterpret_cast<uint4 *>(dst + u * 2048 + d1) = a1;
                     }
-                    const uint2 y0 = codes_to_f16<FMT == PF_E4M3>(w.x), y1 = codes_to_f16<FMT == PF_E4M3>(w.y),
-                                y2 = codes_to_f16<FMT == PF_E4M3>(w.z), y3 = codes_to_f16<FMT == PF_E4M3>(w.w);
-                    uint4 a0 = make_uint4(y0.x, y0.y, y1.x, y1.y), a1 = make_uint4(y2.x, y2.y, y3.x, y3.y);
-                    if constexpr (FOLD) {
-                        const uint2 f = factors[u * 16];
-                        a0 = make_uint4(scaled(a0.x, f), scaled(a0.y, f), scaled(a0.z, f), scaled(a0.w, f));
-                        a1 = make_uint4(scaled(a1.x, f), scaled(a1.y, f), scaled(a1.z, f), scaled(a1.w, f));
-                    }
-                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d0) = a0;
-                    *reinterpret_cast<uint4 *>(dst + u * 2048 + d1) = a1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[raw]));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sh.full[slot]));
-                    mbar_arrive(smem_u32(&sh.raw_empty[raw]));
-                }
+                if (lane == 0) mbar_arrive(smem_u32(&sh.full[slot]));
             }
             if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
         }
@@ -845,7 +859,9 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
 
 cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
     CUtensorMap maps[2];
-    if (!page_map(p, p.k, p.page, &maps[0]) || !page_map(p, p.v, p.page, &maps[1])) return cudaErrorInvalidValue;
+    const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
+    const int box = wide ? p.page : std::min(p.page, kRawKeys);
+    if (!page_map(p, p.k, box, &maps[0]) || !page_map(p, p.v, box, &maps[1])) return cudaErrorInvalidValue;
     const bool fold = !p.lse && p.out_dtype == DT_BF16;
     auto go = [&](auto qb) {
         constexpr bool QB = decltype(qb)::value;
