@@ -617,10 +617,13 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
 // How the work is cut.
 //   Few rows: one item a key/value head and sequence.  As many splits as the SMs, two CTAs
 //   each, hold at once: one round has the least latency (8 sequences of up to 2000 keys, 8
-//   heads: 11.2 us with four splits, one round, 13.9 with eight).  Where 2048 keys remain to a
-//   CTA, up to four times as many, so that sequences of different lengths even out (32 of 9000
-//   to 20000: 169 us, in one round 191).  Up to eight are joined by a cluster; more than that,
-//   through memory, only if twice as many are wanted.  A split keeps 256 keys at least.
+//   heads: 11.2 us with four splits, one round, 13.9 with eight).  Where that is fewer than four
+//   and 2048 keys remain to a CTA, a multiple of it, so that sequences of different lengths even
+//   out (int8, 8 heads: 32 sequences of 9000 to 20000, 166 us with four splits, 197 with one; 16
+//   of them, 99 with four, 104 with two; of 15000 each, 92 and 83, but 109 with seven, which
+//   fill their rounds no better and keep slots of an SM waiting for whole clusters).  Up to
+//   eight are joined by a cluster; more than that, through memory, only if twice as many are
+//   wanted.  A split keeps 256 keys at least.
 //   Many rows: items of 256 rows, a CTA an SM.  Whole items fill whole rounds of the SMs, and
 //   the last round's are split so that they fill it too: the split that takes the least time
 //   is chosen, counting six key tiles' worth of time to start a CTA and four more to join.
@@ -634,11 +637,13 @@ void page_attention_cut(PAttnPlan &p) {
     if (rows <= kRowsM) {
         p.unit = kRowsM;
         p.units = 1;
-        const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = 152 * 2 / cells;
+        const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = std::max<int64_t>(152 * 2 / cells, 1);
         int64_t want = std::min<int64_t>(once, 256);
-        if (once < 2 * kRowsCluster)
-            want = std::min<int64_t>(kRowsCluster, std::max(once, std::min(4 * 152 * 2 / cells, p.max_kv / 2048)));
-        p.S = (int)std::max<int64_t>(1, std::min(want, most));
+        if (once < 2 * kRowsCluster) {
+            while (want < 4 && (want + once) * cells <= 4 * 152 * 2 && (want + once) * 2048 <= p.max_kv) want += once;
+            want = std::min<int64_t>(want, kRowsCluster);
+        }
+        p.S = (int)std::min(want, most);
         return;
     }
     p.unit = 256;
