@@ -4,9 +4,12 @@
 //
 // Bound by memory: every cached byte is read once per key/value head and used for all rows
 // (query tokens x grouped query heads, at most 16).  One warp of a CTA streams the keys' and
-// values' pages by TMA into a ring of stages of 64 or 128 keys (about 100 KB in flight a CTA, two
-// CTAs an SM: several times what the memory's latency needs); four warps take a quarter of each
-// stage, with a running maximum and weight sum per row, on warp-level matrix instructions:
+// values' pages by TMA into a ring of stages of 64 or 128 keys (about 100 KB in flight a CTA,
+// two CTAs an SM: several times what the memory's latency needs).  One query of 32 sequences of
+// 15000 tokens, 8 heads: bf16 275 us (7.1 TB/s), e4m3 and int8 171 us (5.7 TB/s; the latencies
+// of widening and softmax, two computing warps a scheduler).  Of each stage four warps take a
+// quarter, with a running maximum and weight sum per row, on warp-level matrix instructions (the
+// tensor cores' own take 128 rows at a time, at most 16 of which would be in use):
 //   * scores S^T = K Q^T: the keys are the product's 16 rows and the queries its columns, eight
 //     at a time, so that one or two grouped heads' worth of rows wastes little.  A dot product
 //     may take its channels in any order, so lane (g, q) = (lane / 4, lane % 4) reads 16-byte
@@ -19,7 +22,8 @@
 //     2q + 9, pairs them up by byte permutations, and ends with whole runs of channels to
 //     write.  The stages are swizzled (128 bytes), which keeps these reads off each other's
 //     banks.
-// The keys are cut into S splits, a CTA each.  The warps' results are joined in shared memory;
+// Scores, sums and outputs are fp32; the weights are rounded to the product's 16-bit type (fp16
+// over 8-bit pages).  The keys are cut into S splits, a CTA each.  The warps' results are joined in shared memory;
 // the splits', where there are at most eight, by a cluster of the S CTAs through each other's
 // shared memory (one launch, no workspace), else through memory by k_page_combine.
 #include "page_attn.cuh"

@@ -2,36 +2,49 @@
 // + TMA).
 //   O = softmax(scale Q K^T, over the visible keys) V
 //
-// Bound by the tensor cores: 4 * 128 operations per visible (query row, key) pair.  A CTA takes
-// two tiles of 128 rows (query tokens x grouped query heads of one key/value head) and walks
-// the keys in tiles of 128; both row tiles use every key tile that is loaded.  One pass, with a
-// running maximum and weight sum per row:
+// Bound by the tensor cores: 4 * 128 operations per visible (query row, key) pair.  4680 queries
+// of 12 heads over 32760 keys, every one seen: 597 us back to back (1577 TFLOP/s), 640 us with
+// cold caches; 4096 over 32768 of 32 heads, causal: 1268 us (1625).  The tensor cores work 87 %
+// of the cycles of the loop over the keys at the clocks that this load leaves (1.5 to 1.6 GHz);
+// the rest is the start of a CTA (about 8000 cycles: TMEM, Q, the first tile) and the join of
+// the last round's splits.  Shared memory is as busy as they are: a tile pair's products read
+// 192 KB of it and the loads write 64, at 128 bytes a cycle the 2048 cycles of the products.
+// A CTA takes two tiles of 128 rows (query tokens x grouped query heads of one key/value head)
+// and walks the keys in tiles of 128; both row tiles use every key tile that is loaded.  One
+// pass, with a running maximum and weight sum per row:
 //   * one warp loads: a tile's pages by TMA into a ring of 32 KB slots (K and V alternate), in
 //     the 128-byte swizzled layout that serves K as a K-major operand and V as an MN-major one;
 //   * one warp issues S_t = Q_t K^T into TMEM, then O_t += P_t V with P_t read from TMEM;
 //   * warps 0-7 and 8-15: the softmax of row tile 0 and 1, two threads a row with 64 scores
 //     each (one would hold 128 in registers and spill, and its chain of latencies is what the
-//     tensor cores wait for): scores from TMEM, their maximum, exchanged between the two
-//     through shared memory, powers of two against it, and the weights in 16 bits back into
-//     TMEM over the scores.  While one tile's softmax runs, the tensor cores work on the
-//     other's.
+//     tensor cores wait for: 951 us with one, 734 with two): scores from TMEM, their maximum,
+//     powers of two against the row's base, and the weights in 16 bits back into TMEM over the
+//     scores.  While one tile's softmax runs, the tensor cores work on the other's.  A product
+//     starts once the first 32 keys of either half have their weights.
 // The running maximum is raised only when a row's scores pass it by more than 2^8: the weights
 // stay below 2^8 and O_t in TMEM is rescaled (by the softmax warps themselves) a few times in
-// all instead of once a tile; the result is the same, since numerator and weight sum share the
-// base.
-// TMEM: S/P of the two row tiles (128 columns each; the weights of a tile take the first 64 of
-// its scores' columns), then O of the two (128 each): all 512 columns, one CTA an SM.
+// all instead of once a tile, and only then the two threads of a row exchange their maxima; the
+// result is the same, since numerator and weight sum share the base.
+// Scores, weight sums and O are fp32; the weights are rounded to the values' 16-bit type (2^-8
+// or 2^-11 of each at most), as the product's operands have to be.
+// TMEM: S/P of the two row tiles (128 columns each; the weights take columns 0 - 31 and 64 - 95
+// of their scores, so that each thread overwrites only scores that it has read), then O of the
+// two (128 each): all 512 columns, one CTA an SM.
 //
-// 8-bit pages: eight more warps widen the codes to fp16 into the ring, from raw tiles that TMA
-// brings.  bf16 queries are made fp16 too, each row scaled by a power of two that brings its
-// largest channel to 1 .. 2: what falls below fp16's range is 2^-25 of that.  Where the output
-// is bf16 and no log-sum-exp is asked for (FOLD), the keys' and values' scales are multiplied in
-// while widening, relative to a power of two (of the tile's largest scale for keys; for values,
-// whose sums outlive the tile, of the largest so far), and the product is rounded to fp16 once:
-// 2^-11 of each key and value, an eighth of what the output's own rounding is.  Otherwise the
-// scales multiply the scores and the weights in the softmax (the weights, in fp16, relative to
-// the same power of two), which costs time: every thread then reads the scales of all keys from
-// shared memory.
+// 8-bit pages: eight more warps widen the codes to fp16 into the ring, from raw tiles of 64 keys
+// that TMA brings (half a tile each: that leaves room for four slots of widened ones).  bf16
+// queries are made fp16 too, each row scaled by a power of two that brings its largest channel
+// to 1 .. 2: what falls below fp16's range is 2^-25 of that.  Where the output is bf16 and no
+// log-sum-exp is asked for (FOLD), the keys' and values' scales are multiplied in while
+// widening, relative to a power of two (of the tile's largest scale for keys; for values, whose
+// sums outlive the tile, of the largest so far), and the product is rounded to fp16 once: 2^-11
+// of each key and value, an eighth of what the output's own rounding is.  Otherwise the scales
+// multiply the scores and the weights in the softmax (the weights, in fp16, relative to the same
+// power of two), which costs time: every thread then reads the scales of all keys from shared
+// memory.  The case above takes 901 us in e4m3 and 969 in int8, without folding 1087 and 1117.
+// These are bound by instruction issue: 11100 warp instructions a tile against 5900 in 16 bits,
+// 0.8 a cycle where the SM is full; with one factor instead of two (a scale rounded to fp16, an
+// error that all channels of a key share) they would take 881 and 936.
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value

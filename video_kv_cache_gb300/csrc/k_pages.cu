@@ -8,6 +8,8 @@
 // the other keeps, and ends with one row of the eight.  The pair of lanes that has a row then
 // makes its two quotients, largest code / magnitude and magnitude / largest code, in one
 // division for all eight rows.
+// 32760 tokens of 12 heads in int8: 51 us written (301 MB, 5.9 TB/s), 48 us read back (6.3);
+// 280800 in e4m3 read back: 384 us (6.8).
 #include <cuda_fp8.h>
 
 #include "rows.cuh"
