@@ -372,6 +372,34 @@ def test_page_attention(case):
     _check(Q, kv, table, kv_lens, q_lens, causal, window)
 
 
+SHARES = [  # longest and other cached lengths, q lengths, q heads, heads, q type, format, page, causal, window
+    ([2900, 0, 1, 64, 127, 128, 129, 700] * 3, [1], 8, 4, BF, BF, 64, True, 0),
+    ([1500, 0, 1, 64, 127, 128, 129, 700] * 3, [2, 0, 1, 3], 10, 5, BF, I8, 32, True, 0),
+    ([5, 3, 2500], [4], 90, 30, HF, E4, 128, True, 0),           # 12 rows; some see nothing
+    ([300, 900, 40, 2000], [1, 2], 48, 24, HF, HF, 16, True, 250),
+    ([1000, 10, 333], [5, 1], 27, 27, BF, E4, 64, False, 0),
+    ([17] * 11, [1], 8, 8, BF, BF, 16, True, 0),                 # a share each, and none to spare
+    ([1, 0, 2], [1], 40, 40, HF, I8, 16, True, 0),
+    ([0, 0, 0, 0], [1, 0], 20, 20, BF, BF, 16, False, 0),
+    ([600] * 40, [1], 8, 8, BF, I8, 16, True, 0),
+]
+
+
+@pytest.mark.parametrize("case", SHARES)
+def test_page_attention_in_equal_shares(case):
+    # many heads of sequences that may be long, as far as the call can know: their keys are cut
+    # into equal shares, wherever a head ends
+    kv_lens, q_lens, q_heads, heads, dtype, fmt, page, causal, window = case
+    q_lens = [q_lens[b % len(q_lens)] for b in range(len(kv_lens))]
+    g = _gen(sum(q_lens) + sum(kv_lens) + heads)
+    kv, table = _cache(g, kv_lens, heads, fmt, page)
+    longest = 1 + 152 * 2 * 2048 // (heads * len(kv_lens))
+    wide = torch.zeros((len(kv_lens), max(table.shape[1], -(-longest // page))), dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    Q = (1.5 * torch.randn((sum(q_lens), q_heads, 128), generator=g)).to(dtype)
+    _check(Q, kv, wide, kv_lens, q_lens, causal, window, max_kv=longest)
+
+
 @pytest.mark.parametrize("n", [1, 15, 16, 17, 127, 128, 129, 255, 256, 257, 400])
 @pytest.mark.parametrize("nq", [1, 40])
 def test_page_attention_lengths(n, nq):

@@ -461,6 +461,10 @@ struct PAttnPlan {
     // are split S ways, a CTA each, and joined.
     int unit, units, S;
     int64_t whole;
+    // Few rows, long keys: all heads' keys in a row are cut into equal shares instead, a CTA
+    // each, whose first and last stretches may be parts of a head.
+    int stream;
+    int2 *spans;  // [B][H] place of a head's first part, and how many shares follow with more
     float *part;  // [items that are split][S][unit][128] partial outputs, relative to their maximum
     float *ml;    // [..][S][unit][2] running maximum (log2) and weight sum
     uint32_t *status;

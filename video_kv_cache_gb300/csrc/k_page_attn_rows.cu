@@ -6,7 +6,7 @@
 // (query tokens x grouped query heads, at most 16).  One warp of a CTA streams the keys' and
 // values' pages by TMA into a ring of stages of 64 or 128 keys (about 100 KB in flight a CTA,
 // two CTAs an SM: several times what the memory's latency needs).  One query of 32 sequences of
-// 15000 tokens, 8 heads: bf16 275 us (7.1 TB/s), e4m3 and int8 171 us (5.7 TB/s; the latencies
+// 15000 tokens, 8 heads: bf16 275 us (7.1 TB/s), e4m3 and int8 163 us (6.0 TB/s; the latencies
 // of widening and softmax, two computing warps a scheduler).  Of each stage four warps take a
 // quarter, with a running maximum and weight sum per row, on warp-level matrix instructions (the
 // tensor cores' own take 128 rows at a time, at most 16 of which would be in use):
@@ -23,9 +23,14 @@
 //     write.  The stages are swizzled (128 bytes), which keeps these reads off each other's
 //     banks.
 // Scores, sums and outputs are fp32; the weights are rounded to the product's 16-bit type (fp16
-// over 8-bit pages).  The keys are cut into S splits, a CTA each.  The warps' results are joined in shared memory;
+// over 8-bit pages).
+//
+// The keys are cut into S splits, a CTA each.  The warps' results are joined in shared memory;
 // the splits', where there are at most eight, by a cluster of the S CTAs through each other's
-// shared memory (one launch, no workspace), else through memory by k_page_combine.
+// shared memory (one launch, no workspace), else through memory by k_page_combine.  Or
+// (SHARES) the keys of all heads, in a row, are cut into as many equal shares as CTAs run at
+// once, each worked through item by item, the next one's loads running while the last one is
+// joined; a head that more than one share has a part of is joined by k_page_combine.
 #include "page_attn.cuh"
 #include "tcgen.cuh"
 
@@ -34,8 +39,10 @@ namespace qvg {
 namespace {
 constexpr int kRowsWarps = 4;              // warps that compute
 constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+constexpr int kRowsShares = 152 * 2;       // CTAs that run at once
 constexpr int kRowsPad = 132;              // padded row of the join, floats
 constexpr int kRowsCluster = 8;            // most splits joined by a cluster
+constexpr int kRowsShare = 4;              // stages of a share, at least
 
 // RT: groups of eight query rows, one or two.
 template <int FMT, int RT>
@@ -49,21 +56,24 @@ struct RowsShape {
     static constexpr int STAGES = 3;  // 32 KB each; two stages and three CTAs, or smaller stages, are slower
     static constexpr uint32_t TILE = KEYS * kD * (WIDE ? 2 : 1);   // bytes of its keys, or values
 };
-template <int FMT, int RT>
+// SHARES: see PAttnPlan::stream.
+template <int FMT, int RT, bool SHARES>
 struct RowsShared {
     using T = RowsShape<FMT, RT>;
     __align__(16) float ks[T::STAGES][T::WIDE ? 4 : T::KEYS];
     __align__(16) float vs[T::STAGES][T::WIDE ? 4 : T::KEYS];
+    __align__(16) float o[SHARES ? 8 * RT : 1][kRowsPad];  // where the warps' results are joined
     uint64_t full[T::STAGES], empty[T::STAGES];
     float m[kRowsWarps][8 * RT], l[kRowsWarps][8 * RT];
     float2 ml[8 * RT];  // this split's maxima and sums, for the cluster
     int abort;
+    int b0, share;              // the sequence that this CTA's share starts in,
+    int64_t p0, g0, g1, total;  // the stages before it, the share itself, all stages (share: of how many)
 };
-// The join's rows take the ring's place once the keys are through.
-template <int FMT, int RT>
+template <int FMT, int RT, bool SHARES>
 constexpr size_t rows_smem() {
     using T = RowsShape<FMT, RT>;
-    constexpr size_t bytes = T::STAGES * 2 * T::TILE + sizeof(RowsShared<FMT, RT>);
+    constexpr size_t bytes = T::STAGES * 2 * T::TILE + sizeof(RowsShared<FMT, RT, SHARES>);
     static_assert(T::CTAS * (bytes + 1024) <= 228 * 1024, "CTAs of an SM");
     static_assert((kRowsWarps + 1) * 8 * RT * kRowsPad * 4 <= T::STAGES * 2 * T::TILE, "join");
     return bytes;
@@ -108,15 +118,35 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
     asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
     return v;
 }
+// The warps that compute meet.
+__device__ __forceinline__ void rows_meet() { asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kRowsWarps) : "memory"); }
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 }  // namespace
 
-// grid (splits, key/value heads, sequences).  QB: bf16 queries; FMT: the page format, the
-// 16-bit ones (PF_F16 / PF_BF16) equal to the query's type.  joined: the splits are a cluster.
-template <bool QB, int FMT, int RT>
+// A stretch of one key/value head's keys, in stages.
+struct RowsItem {
+    int b, h, first, n;
+    SeqInfo sq;
+    bool whole;  // all of the head's keys (of a share)
+};
+// Stages of a sequence's keys that its rows see, from s_lo on; at least one where there are rows.
+template <int KEYS>
+__device__ __forceinline__ int rows_stages(const PAttnPlan &p, const SeqInfo &sq, int &s_lo) {
+    s_lo = 0;
+    if (sq.qn == 0) return 0;
+    const int lo = seen_lo(p, sq, 0), hi = seen_hi(p, sq, sq.qn - 1);
+    if (lo >= hi) return 1;
+    s_lo = lo / KEYS;
+    return (hi + KEYS - 1) / KEYS - s_lo;
+}
+
+// QB: bf16 queries; FMT: the page format, the 16-bit ones (PF_F16 / PF_BF16) equal to the query's
+// type.  SHARES: grid (shares), each an equal part of all heads' stages in a row; else grid
+// (splits, key/value heads, sequences), joined: the splits are a cluster.
+template <bool QB, int FMT, int RT, bool SHARES>
 __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
     k_page_attn_rows(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PAttnPlan p, int joined) {
@@ -128,23 +158,15 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
     constexpr int NCH = ROWB / 64;              // 16-byte chunks of a row per lane
     constexpr int STAGES = T::STAGES, KT = T::KT, KEYS = T::KEYS, ROWS = 8 * RT;
     extern __shared__ __align__(1024) unsigned char sm[];
-    RowsShared<FMT, RT> &sh = *reinterpret_cast<RowsShared<FMT, RT> *>(sm + STAGES * 2 * T::TILE);
+    RowsShared<FMT, RT, SHARES> &sh = *reinterpret_cast<RowsShared<FMT, RT, SHARES> *>(sm + STAGES * 2 * T::TILE);
     float(*s_o)[ROWS][kRowsPad] = reinterpret_cast<float(*)[ROWS][kRowsPad]>(sm);
     volatile int *abort_flag = &sh.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const SeqInfo sq = seq_info(p, b, threadIdx.x == 0 && blockIdx.x == 0 && h == 0);
-    const int rows = sq.qn * p.G;
-    if (rows == 0) return;
     const int shift = 31 - __clz(p.page);
 
-    // what the rows see, this split's share of it, in stages
-    const int lo = seen_lo(p, sq, 0), hi = seen_hi(p, sq, sq.qn - 1);
-    int first = 0, n = 0;
-    if (lo < hi) {
-        const int s_lo = lo / KEYS, all = (hi + KEYS - 1) / KEYS - s_lo, per = (all + p.S - 1) / p.S;
-        first = s_lo + split * per;
-        n = max(0, min(per, all - split * per));
+    if (!SHARES && seq_info(p, blockIdx.z, false).qn == 0) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) seq_info(p, blockIdx.z, true);
+        return;
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -154,22 +176,94 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (SHARES && warp == 0) {
+        // the stages of all heads, and where among them this CTA's share lies
+        int s_lo;
+        int64_t all = 0;
+        for (int b = lane; b < p.B; b += 32) all += rows_stages<KEYS>(p, seq_info(p, b, blockIdx.x == 0), s_lo);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
+        all *= p.H;
+        const int64_t shares = max(min((int64_t)gridDim.x, all / kRowsShare), (int64_t)1), c = blockIdx.x;
+        const int64_t g0 = c < shares ? c * all / shares : all, g1 = c < shares ? (c + 1) * all / shares : all;
+        int64_t before = 0;
+        int b0 = 0;
+        for (int base = 0; g0 < g1 && base < p.B; base += 32) {
+            int64_t upto = base + lane < p.B ? (int64_t)rows_stages<KEYS>(p, seq_info(p, base + lane, false), s_lo) * p.H : 0;
+            const int64_t own = upto;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+                if (lane >= x) upto += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, before + upto > g0);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                b0 = base + at;
+                before += __shfl_sync(0xffffffffu, upto - own, at);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (lane == 0) {
+            sh.b0 = b0;
+            sh.p0 = before;
+            sh.g0 = g0;
+            sh.g1 = g1;
+            sh.share = (int)shares;
+            sh.total = all;
+        }
+    }
     __syncthreads();
 
-    float o[RT][8][4], m[RT][2], l[RT][2];
-#pragma unroll
-    for (int y = 0; y < RT; y++) {
-        m[y][0] = m[y][1] = -INFINITY;
-        l[y][0] = l[y][1] = 0.f;
-#pragma unroll
-        for (int t = 0; t < 8; t++) o[y][t][0] = o[y][t][1] = o[y][t][2] = o[y][t][3] = 0.f;
-    }
-    int vexp = -100;  // exponent of the reference that the values' scales are taken against
+    // Calls work with each of this CTA's items (the same for all its warps) and the row of its
+    // partial results.
+    auto items = [&](auto &&work) {
+        RowsItem x;
+        int s_lo;
+        if constexpr (!SHARES) {
+            x.b = blockIdx.z;
+            x.h = blockIdx.y;
+            x.sq = seq_info(p, x.b, threadIdx.x == 0 && blockIdx.x == 0 && x.h == 0);
+            const int all = rows_stages<KEYS>(p, x.sq, s_lo), per = (all + p.S - 1) / p.S;
+            x.first = s_lo + blockIdx.x * per;
+            x.n = max(0, min(per, all - (int)blockIdx.x * per));
+            work(x, 0);  // (made again from the grid where it is needed, to keep registers free)
+            return;
+        }
+        int64_t pos = sh.g0, before = sh.p0;
+        const int64_t end = sh.g1;
+        for (x.b = sh.b0; x.b < p.B && pos < end; x.b++) {
+            x.sq = seq_info(p, x.b, false);
+            const int all = rows_stages<KEYS>(p, x.sq, s_lo);
+            for (x.h = all ? (int)((pos - before) / all) : p.H; x.h < p.H && pos < end; x.h++) {
+                const int64_t start = before + (int64_t)x.h * all;
+                x.first = s_lo + (int)(pos - start);
+                x.n = (int)min(start + all - pos, end - pos);
+                x.whole = x.n == all;
+                // a part's place: the second of this CTA's two if the head begins with it
+                const int slot = 2 * blockIdx.x + (pos == start);
+                if (threadIdx.x == 0 && pos == start) {
+                    // the share that the head's last stage lies in
+                    const int last = x.whole ? (int)blockIdx.x : (int)(((start + all) * sh.share - 1) / sh.total);
+                    p.spans[(int64_t)x.b * p.H + x.h] = make_int2(slot, last - (int)blockIdx.x);
+                }
+                pos += x.n;
+                work(x, (int64_t)slot * kRowsM);
+                __syncwarp();
+            }
+            before += (int64_t)all * p.H;
+        }
+    };
+
     if (warp == kRowsWarps) {
         // -------------------------------------------------------------------- TMA loads
         const int box = min(p.page, KEYS), boxes = KEYS / box;
         bool bad = false, ok = true;
         int issued = 0;
+        items([&](const RowsItem &x, int64_t) {
+        const int b = x.b, h = x.h, first = x.first, n = x.n;
+        const int lo = seen_lo(p, x.sq, 0), hi = seen_hi(p, x.sq, x.sq.qn - 1);
         // the boxes of a stage that hold a key some row sees, a lane each; their pages are
         // looked up one stage ahead
         auto in_sight = [&](int k0) {
@@ -182,11 +276,12 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             return (int)(((page_of(p, b, token, shift, bad) * p.H + h) << shift) + (token & (p.page - 1)));
         };
         int next = n > 0 ? row_of(first * KEYS) : 0;
-        for (int it = 0; it < n; it++) {
-            const int k0 = (first + it) * KEYS, s = it % STAGES, row = next;
-            if (it + 1 < n) next = row_of(k0 + KEYS);
+        for (int j = 0; ok && j < n; j++) {
+            const int it = issued, k0 = (first + j) * KEYS, s = it % STAGES, row = next;
+            if (j + 1 < n) next = row_of(k0 + KEYS);
             ok = page_wait(smem_u32(&sh.empty[s]), (it / STAGES + 1) & 1, abort_flag);
-            if (__any_sync(0xffffffffu, !ok)) break;
+            ok = !__any_sync(0xffffffffu, !ok);
+            if (!ok) break;
             const uint32_t bar = smem_u32(&sh.full[s]), count = __popc(__ballot_sync(0xffffffffu, in_sight(k0)));
             if (lane == 0) mbar_expect_tx(bar, count * box * 2 * (ROWB + (WIDE ? 0 : 4)));
             __syncwarp();
@@ -204,12 +299,32 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             }
             issued = it + 1;
         }
+        });
         if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
-        // every copy lands before the CTA goes on to the join (or ends)
+        // every copy lands before the CTA ends
         for (int it = max(0, issued - STAGES); it < issued; it++)
             mbar_wait_final(smem_u32(&sh.full[it % STAGES]), (it / STAGES) & 1);
+        if (joined) {
+            cluster_meet();
+            cluster_meet();
+        }
     } else {
         // -------------------------------------------------------------------- attention
+        int done = 0;  // stages of the items before
+        bool ok = true;
+        items([&](const RowsItem &item, int64_t part_row) {
+        const int b = SHARES ? item.b : blockIdx.z, h = SHARES ? item.h : blockIdx.y, first = item.first, n = item.n;
+        const SeqInfo sq = item.sq;
+        const int rows = sq.qn * p.G, lo = seen_lo(p, sq, 0), hi = seen_hi(p, sq, sq.qn - 1);
+        float o[RT][8][4], m[RT][2], l[RT][2];
+#pragma unroll
+        for (int y = 0; y < RT; y++) {
+            m[y][0] = m[y][1] = -INFINITY;
+            l[y][0] = l[y][1] = 0.f;
+#pragma unroll
+            for (int t = 0; t < 8; t++) o[y][t][0] = o[y][t][1] = o[y][t][2] = o[y][t][3] = 0.f;
+        }
+        int vexp = -100;  // exponent of the reference that the values' scales are taken against
         // Q in the order the keys' chunks come in: lane (g, q) holds row g of each group
         uint32_t qb[RT][8][2];
         float qmul[RT][2];  // 8-bit pages: powers of two taken out of the rows whose scores this lane has
@@ -259,10 +374,12 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
         auto chunk = [](const unsigned char *tile, int r, int c) {
             return *reinterpret_cast<const uint4 *>(tile + (c >> 3) * (T::TILE / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
         };
-        for (int it = 0; it < n; it++) {
-            const int st = it % STAGES, w0 = warp * 16 * KT, t0 = (first + it) * KEYS + w0;  // this warp's first key
-            const bool ok = page_wait(smem_u32(&sh.full[st]), (it / STAGES) & 1, abort_flag);
-            if (__any_sync(0xffffffffu, !ok)) break;
+        // (a warp that gives up a wait keeps meeting the others)
+        for (int j = 0; ok && j < n; j++) {
+            const int it = done + j, st = it % STAGES, w0 = warp * 16 * KT, t0 = (first + j) * KEYS + w0;  // this warp's first key
+            ok = page_wait(smem_u32(&sh.full[st]), (it / STAGES) & 1, abort_flag);
+            ok = !__any_sync(0xffffffffu, !ok);
+            if (!ok) break;
             if (t0 < hi && t0 + 16 * KT > lo) {
                 const unsigned char *kt = sm + st * 2 * T::TILE, *vt = kt + T::TILE;
                 // s[z][y][..]: keys t0 + 16 z + g (0, 1) and + 8 (2, 3), rows 8 y + 2 q, + 1
@@ -443,13 +560,13 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
         }
-    }
+        if (SHARES) done += n;
 
-    // join the warps, in the ring's place
-    __syncthreads();
-    if (threadIdx.x == 0 && *abort_flag) or_status(p.status, QVG_DEV_TIMEOUT);
-    if (warp < kRowsWarps) {
+        // join the warps relative to the largest of their maxima: through the ring, which is
+        // through with its keys, or, where the next item's are on their way, one after another in
+        // a place of its own
         const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp - 8) << 23);
+        if constexpr (!SHARES) rows_meet();
 #pragma unroll
         for (int y = 0; y < RT; y++)
 #pragma unroll
@@ -461,79 +578,114 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                     sh.m[warp][r] = m[y][x];
                     sh.l[warp][r] = l[y][x];
                 }
-#pragma unroll
-                for (int e = 0; e < 2; e++) {  // eight channels each
-                    float *dst = &s_o[warp][r][WIDE ? 64 * e + 8 * g : 16 * g + 8 * e];
-                    *reinterpret_cast<float4 *>(dst) = make_float4(o[y][0][2 * e + x] * unit, o[y][1][2 * e + x] * unit,
-                                                                   o[y][2][2 * e + x] * unit, o[y][3][2 * e + x] * unit);
-                    *reinterpret_cast<float4 *>(dst + 4) = make_float4(o[y][4][2 * e + x] * unit, o[y][5][2 * e + x] * unit,
-                                                                       o[y][6][2 * e + x] * unit, o[y][7][2 * e + x] * unit);
-                }
             }
-    }
-    __syncthreads();
-    // eight lanes a row, 16 channels each (in runs of four, so that the lanes' reads and
-    // writes are next to one another); the other warps only keep the barriers
-    const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
-    float M = -INFINITY, L = 0.f, v[16] = {};
-    const bool mine = r < ROWS;
-    if (mine) {
+        // this lane's channels (two runs of eight of each row), added to what is there or stored
+        auto put = [&](float(*rows_o)[kRowsPad], bool add, bool relative) {
 #pragma unroll
-        for (int w = 0; w < kRowsWarps; w++) M = fmaxf(M, sh.m[w][r]);
-        const float base = exp_base(M);
+            for (int y = 0; y < RT; y++)
 #pragma unroll
-        for (int w = 0; w < kRowsWarps; w++) {
-            const float f = fast_exp2(sh.m[w][r] - base);
-            L += f * sh.l[w][r];
+                for (int x = 0; x < 2; x++) {
+                    const int r = 8 * y + 2 * q + x;
+                    float f = 1.f;
+                    if (relative) {
+                        const float top = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+                        f = fast_exp2(m[y][x] - exp_base(top));
+                    }
 #pragma unroll
-            for (int c = 0; c < 16; c++) v[c] += f * s_o[w][r][(c >> 2) * 32 + part * 4 + (c & 3)];
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int k = 0; k < 8; k += 4) {
+                            float4 *dst = reinterpret_cast<float4 *>(&rows_o[r][(WIDE ? 64 * e + 8 * g : 16 * g + 8 * e) + k]);
+                            float4 v = make_float4(o[y][k][2 * e + x] * unit, o[y][k + 1][2 * e + x] * unit,
+                                                   o[y][k + 2][2 * e + x] * unit, o[y][k + 3][2 * e + x] * unit);
+                            if (relative) {
+                                const float4 a = add ? *dst : make_float4(0.f, 0.f, 0.f, 0.f);
+                                v = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
+                            }
+                            *dst = v;
+                        }
+                }
+        };
+        if constexpr (SHARES) {
+            rows_meet();
+#pragma unroll 1
+            for (int w = 0; w < kRowsWarps; w++) {
+                if (warp == w) put(sh.o, w > 0, true);
+                rows_meet();
+            }
+        } else {
+            put(s_o[warp], false, false);
+            rows_meet();
         }
-    }
-    const int row_i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - row_i * p.G;
-    bool live = mine && r < rows;
-    if (p.S > 1 && !joined) {
-        if (!live) return;
-        const int64_t at = (((int64_t)b * p.H + h) * p.S + split) * kRowsM + r;
-#pragma unroll
-        for (int c = 0; c < 4; c++) store4<DT_F32>(p.part, at * kD + c * 32 + part * 4, v + 4 * c);
-        if (part == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = make_float2(M, L);
-        return;
-    }
-    if (joined) {
-        // each CTA of the cluster finishes the rows r with r % S its rank
+        // eight lanes a row, 16 channels each (in runs of four, so that the lanes' reads and
+        // writes are next to one another); the other warps only keep the barriers
+        const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
+        float M = -INFINITY, L = 0.f, v[16] = {};
+        const bool mine = r < ROWS;
         if (mine) {
 #pragma unroll
-            for (int c = 0; c < 4; c++)
-                *reinterpret_cast<float4 *>(&s_o[kRowsWarps][r][c * 32 + part * 4]) =
-                    make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            if (part == 0) sh.ml[r] = make_float2(M, L);
-        }
-        cluster_meet();
-        live = live && r % p.S == split;
-        if (live) {
-            M = -INFINITY;
-            for (int s = 0; s < p.S; s++) M = fmaxf(M, ld_cluster2(cluster_addr(&sh.ml[r], s)).x);
+            for (int w = 0; w < kRowsWarps; w++) M = fmaxf(M, sh.m[w][r]);
             const float base = exp_base(M);
-            L = 0.f;
 #pragma unroll
-            for (int c = 0; c < 16; c++) v[c] = 0.f;
-            for (int s = 0; s < p.S; s++) {
-                const float2 ml = ld_cluster2(cluster_addr(&sh.ml[r], s));
-                const float f = fast_exp2(ml.x - base);
-                L += f * ml.y;
+            for (int w = 0; w < kRowsWarps; w++) {
+                const float f = fast_exp2(sh.m[w][r] - base);
+                L += f * sh.l[w][r];
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    const float4 y = ld_cluster4(cluster_addr(&s_o[kRowsWarps][r][c * 32 + part * 4], s));
-                    v[4 * c] += f * y.x;
-                    v[4 * c + 1] += f * y.y;
-                    v[4 * c + 2] += f * y.z;
-                    v[4 * c + 3] += f * y.w;
+                for (int c = 0; c < 16; c++) {
+                    const int at = (c >> 2) * 32 + part * 4 + (c & 3);
+                    if constexpr (!SHARES)
+                        v[c] += f * s_o[w][r][at];
+                    else if (w == 0)
+                        v[c] = sh.o[r][at];
                 }
             }
         }
-        cluster_meet();  // nobody leaves while its rows are read
-    }
-    if (!mine) return;
+        const int row_i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - row_i * p.G;
+        bool live = mine && r < rows;
+        if constexpr (SHARES) rows_meet();  // the join's rows are read: the next item's may follow
+        if (SHARES ? !item.whole : p.S > 1 && !joined) {
+            if (!live) return;
+            const int64_t at = (SHARES ? part_row : (((int64_t)blockIdx.z * p.H + blockIdx.y) * p.S + blockIdx.x) * kRowsM) + r;
+#pragma unroll
+            for (int c = 0; c < 4; c++) store4<DT_F32>(p.part, at * kD + c * 32 + part * 4, v + 4 * c);
+            if (part == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = make_float2(M, L);
+            return;
+        }
+        if (!SHARES && joined) {
+            // each CTA of the cluster finishes the rows r with r % S its rank
+            if (mine) {
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    *reinterpret_cast<float4 *>(&s_o[kRowsWarps][r][c * 32 + part * 4]) =
+                        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                if (part == 0) sh.ml[r] = make_float2(M, L);
+            }
+            cluster_meet();
+            live = live && r % p.S == (int)blockIdx.x;
+            if (live) {
+                M = -INFINITY;
+                for (int s = 0; s < p.S; s++) M = fmaxf(M, ld_cluster2(cluster_addr(&sh.ml[r], s)).x);
+                const float base = exp_base(M);
+                L = 0.f;
+#pragma unroll
+                for (int c = 0; c < 16; c++) v[c] = 0.f;
+                for (int s = 0; s < p.S; s++) {
+                    const float2 ml = ld_cluster2(cluster_addr(&sh.ml[r], s));
+                    const float f = fast_exp2(ml.x - base);
+                    L += f * ml.y;
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        const float4 y = ld_cluster4(cluster_addr(&s_o[kRowsWarps][r][c * 32 + part * 4], s));
+                        v[4 * c] += f * y.x;
+                        v[4 * c + 1] += f * y.y;
+                        v[4 * c + 2] += f * y.z;
+                        v[4 * c + 3] += f * y.w;
+                    }
+                }
+            }
+            cluster_meet();  // nobody leaves while its rows are read
+        }
+        if (!mine) return;
     if (redo_possible(p)) {
         bool odd = false;
 #pragma unroll
@@ -564,6 +716,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
 #pragma unroll
     for (int c = 0; c < 4; c++) store_out4(p, at + c * 32 + part * 4, v + 4 * c);
     if (p.lse && part == 0) p.lse[(sq.q0 + row_i) * p.HQ + hq] = row_lse(M, L);
+        });
+        if (threadIdx.x == 0 && *abort_flag) or_status(p.status, QVG_DEV_TIMEOUT);
+    }
 }
 
 // One warp per row of the items that were split: the splits' partial rows rescaled to the
@@ -579,27 +734,39 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
     const SeqInfo sq = seq_info(p, b, false);
     if (r >= sq.qn * p.G) return;
     const int i = token_of(p, r), hq = h * p.G + r - i * p.G;
-    const int64_t at = t * p.S * p.unit + local;  // + split * unit
+    // the parts' rows: S of them, one unit after another, or (PAttnPlan::stream) the second
+    // place of the share that the head begins in and the first places of those after it
+    int S = p.S;
+    int64_t at = t * p.S * p.unit + local, step = p.unit, skip = 0;
+    if (p.stream) {
+        const int2 span = p.spans[cell];
+        S = span.y + 1;
+        if (S == 1) return;  // whole, and written
+        at = (int64_t)span.x * p.unit + local;
+        step = 2 * p.unit;
+        skip = -p.unit;
+    }
+    auto row = [&](int s) { return at + s * step + (int)(s > 0) * skip; };
     float mx = -INFINITY;
-    for (int s = lane; s < p.S; s += 32) mx = fmaxf(mx, p.ml[2 * (at + s * p.unit)]);
+    for (int s = lane; s < S; s += 32) mx = fmaxf(mx, p.ml[2 * row(s)]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
     const float base = exp_base(mx);
     float l = 0.f, o[4] = {};
     constexpr int SB = 8;
-    for (int s0 = 0; s0 < p.S; s0 += SB) {
+    for (int s0 = 0; s0 < S; s0 += SB) {
         float2 ml[SB];
         float4 po[SB];
 #pragma unroll
         for (int k = 0; k < SB; k++)
-            if (s0 + k < p.S) {
-                const int64_t x = at + (s0 + k) * p.unit;
+            if (s0 + k < S) {
+                const int64_t x = row(s0 + k);
                 ml[k] = *reinterpret_cast<const float2 *>(p.ml + 2 * x);
                 po[k] = *reinterpret_cast<const float4 *>(p.part + x * kD + 4 * lane);
             }
 #pragma unroll
         for (int k = 0; k < SB; k++)
-            if (s0 + k < p.S) {
+            if (s0 + k < S) {
                 const float f = fast_exp2(ml[k].x - base);
                 l += f * ml[k].y;
                 o[0] += f * po[k].x;
@@ -621,13 +788,19 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
 // How the work is cut.
 //   Few rows: one item a key/value head and sequence.  As many splits as the SMs, two CTAs
 //   each, hold at once: one round has the least latency (8 sequences of up to 2000 keys, 8
-//   heads: 11.2 us with four splits, one round, 13.9 with eight).  Where that is fewer than four
-//   and 2048 keys remain to a CTA, a multiple of it, so that sequences of different lengths even
-//   out (int8, 8 heads: 32 sequences of 9000 to 20000, 166 us with four splits, 197 with one; 16
-//   of them, 99 with four, 104 with two; of 15000 each, 92 and 83, but 109 with seven, which
-//   fill their rounds no better and keep slots of an SM waiting for whole clusters).  Up to
-//   eight are joined by a cluster; more than that, through memory, only if twice as many are
-//   wanted.  A split keeps 256 keys at least.
+//   heads: 11.2 us with four splits, one round, 13.9 with eight).  Up to eight are joined by a
+//   cluster; more than that, through memory, only if twice as many are wanted.  A split keeps
+//   256 keys at least.  Where one round is fewer than four splits a head and 2048 keys or more
+//   come to a CTA, sequences of different lengths have to even out:
+//     8-bit pages: equal shares of all heads' keys, one round (8 heads, int8: 32 sequences of
+//     9000 to 20000 155 us, four splits 167, one 197; 16 of 15000 each 86, four 92; 20 of 3000 to
+//     30000 with four heads 60, six splits 79).  Up to two rounds of heads: more even out by
+//     themselves, and each item costs a start and a join (300 sequences of up to 3000: 209 us
+//     in shares, 160 without).
+//     16 bits, where the memory's rate bounds and a start costs little beside it: a multiple of
+//     one round's splits, four or more (bf16, the first of these: 267 us, in shares 281; seven
+//     splits fill their rounds no better than four and keep slots of an SM waiting for whole
+//     clusters).
 //   Many rows: items of 256 rows, a CTA an SM.  Whole items fill whole rounds of the SMs, and
 //   the last round's are split so that they fill it too: the split that takes the least time
 //   is chosen, counting six key tiles' worth of time to start a CTA and four more to join.
@@ -638,13 +811,20 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
 void page_attention_cut(PAttnPlan &p) {
     const int64_t rows = p.max_q * p.G, cells = (int64_t)p.H * p.B;
     p.whole = 0;
+    p.stream = 0;
     if (rows <= kRowsM) {
         p.unit = kRowsM;
         p.units = 1;
-        const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = std::max<int64_t>(152 * 2 / cells, 1);
+        const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = std::max<int64_t>(kRowsShares / cells, 1);
         int64_t want = std::min<int64_t>(once, 256);
+        const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
+        if (!wide && once < 4 && cells <= 2 * kRowsShares && cells * p.max_kv >= (int64_t)kRowsShares * 2048) {
+            p.stream = 1;
+            p.S = 1;
+            return;
+        }
         if (once < 2 * kRowsCluster) {
-            while (want < 4 && (want + once) * cells <= 4 * 152 * 2 && (want + once) * 2048 <= p.max_kv) want += once;
+            while (want < 4 && (want + once) * cells <= 4 * kRowsShares && (want + once) * 2048 <= p.max_kv) want += once;
             want = std::min<int64_t>(want, kRowsCluster);
         }
         p.S = (int)std::min(want, most);
@@ -670,28 +850,33 @@ void page_attention_cut(PAttnPlan &p) {
     }
 }
 int64_t page_attention_part_rows(const PAttnPlan &p) {
+    if (p.stream) return 2 * (int64_t)kRowsShares * kRowsM;
     if (p.S == 1 || (p.unit == kRowsM && p.S <= kRowsCluster)) return 0;
     return ((int64_t)p.units * p.H * p.B - p.whole) * p.S * p.unit;
 }
 
 namespace {
-template <bool QB, int FMT, int RT>
+template <bool QB, int FMT, int RT, bool SHARES>
 cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
-    constexpr size_t smem = rows_smem<FMT, RT>();
-    const auto kernel = k_page_attn_rows<QB, FMT, RT>;
+    constexpr size_t smem = rows_smem<FMT, RT, SHARES>();
+    const auto kernel = k_page_attn_rows<QB, FMT, RT, SHARES>;
     CUtensorMap mk, mv;
     const int box = std::min(p.page, RowsShape<FMT, RT>::KEYS);
     if (!page_map(p, p.k, box, &mk) || !page_map(p, p.v, box, &mv)) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int joined = p.S > 1 && p.S <= kRowsCluster;
-    return launch_kernel_cluster(kernel, dim3((unsigned)p.S, p.H, p.B), dim3(kRowsThreads), smem, joined ? p.S : 1, st,
+    const dim3 grid = SHARES ? dim3(kRowsShares) : dim3((unsigned)p.S, p.H, p.B);
+    return launch_kernel_cluster(kernel, grid, dim3(kRowsThreads), smem, joined ? p.S : 1, st,
                                  mk, mv, p, joined);
 }
 
 template <bool QB, int FMT>
 cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
-    return p.max_q * p.G <= 8 ? launch_rows<QB, FMT, 1>(p, st) : launch_rows<QB, FMT, 2>(p, st);
+    const bool one = p.max_q * p.G <= 8;
+    if constexpr (FMT == PF_E4M3 || FMT == PF_INT8)
+        if (p.stream) return one ? launch_rows<QB, FMT, 1, true>(p, st) : launch_rows<QB, FMT, 2, true>(p, st);
+    return one ? launch_rows<QB, FMT, 1, false>(p, st) : launch_rows<QB, FMT, 2, false>(p, st);
 }
 
 cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st) {
@@ -709,7 +894,8 @@ cudaError_t launch_page_attention(const PAttnPlan &p, cudaStream_t st) {
     const cudaError_t e =
         p.max_q * p.G <= kRowsM ? launch_page_attention_rows(p, st) : launch_page_attention_tc(p, st);
     if (e != cudaSuccess || page_attention_part_rows(p) == 0) return e;
-    return launch_kernel(k_page_combine, dim3((unsigned)(page_attention_part_rows(p) / p.S / 8)), dim3(256), 0, st, p);
+    const int64_t combined = p.stream ? (int64_t)p.B * p.H * kRowsM : page_attention_part_rows(p) / p.S;
+    return launch_kernel(k_page_combine, dim3((unsigned)(combined / 8)), dim3(256), 0, st, p);
 }
 
 }  // namespace qvg

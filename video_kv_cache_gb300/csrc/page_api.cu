@@ -133,9 +133,11 @@ PAttnPlan attention_plan(const qvg_page_attention_params *prm) {
     return p;
 }
 
-// Workspace: the splits' partial rows, then their (maximum, sum) pairs.
+// Workspace: the splits' partial rows, then their (maximum, sum) pairs, then the heads' spans.
 size_t attention_part_bytes(const PAttnPlan &p) { return (size_t)page_attention_part_rows(p) * kD * sizeof(float); }
-size_t attention_bytes(const PAttnPlan &p) { return (size_t)page_attention_part_rows(p) * (kD + 2) * sizeof(float); }
+size_t attention_bytes(const PAttnPlan &p) {
+    return (size_t)page_attention_part_rows(p) * (kD + 2) * sizeof(float) + (p.stream ? (size_t)p.B * p.H * sizeof(int2) : 0);
+}
 
 // Checks that come after the arguments': the injected failure, the device.
 qvg_status ready() {
@@ -305,6 +307,7 @@ qvg_status qvg_page_attention(const qvg_page_attention_params *prm, const void *
     p.lse = lse;
     p.part = static_cast<float *>(workspace);
     p.ml = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + attention_part_bytes(p));
+    p.spans = reinterpret_cast<int2 *>(p.ml + 2 * page_attention_part_rows(p));
     p.status = dev_status;
     return launched(launch_page_attention(p, static_cast<cudaStream_t>(stream)));
 }
