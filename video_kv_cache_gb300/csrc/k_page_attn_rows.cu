@@ -119,7 +119,9 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
     return v;
 }
 // The warps that compute meet.
-__device__ __forceinline__ void rows_meet() { asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kRowsWarps) : "memory"); }
+__device__ __forceinline__ void rows_meet() {
+    asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kRowsWarps) : "memory");
+}
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -189,8 +191,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
         int64_t before = 0;
         int b0 = 0;
         for (int base = 0; g0 < g1 && base < p.B; base += 32) {
-            int64_t upto = base + lane < p.B ? (int64_t)rows_stages<KEYS>(p, seq_info(p, base + lane, false), s_lo) * p.H : 0;
-            const int64_t own = upto;
+            const int b = base + lane;
+            const int64_t own = b < p.B ? (int64_t)rows_stages<KEYS>(p, seq_info(p, b, false), s_lo) * p.H : 0;
+            int64_t upto = own;
 #pragma unroll
             for (int x = 1; x < 32; x <<= 1) {
                 const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
@@ -262,43 +265,43 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
         bool bad = false, ok = true;
         int issued = 0;
         items([&](const RowsItem &x, int64_t) {
-        const int b = x.b, h = x.h, first = x.first, n = x.n;
-        const int lo = seen_lo(p, x.sq, 0), hi = seen_hi(p, x.sq, x.sq.qn - 1);
-        // the boxes of a stage that hold a key some row sees, a lane each; their pages are
-        // looked up one stage ahead
-        auto in_sight = [&](int k0) {
-            const int token = k0 + lane * box;
-            return lane < boxes && token < hi && token + box > lo;
-        };
-        auto row_of = [&](int k0) {
-            const int token = k0 + lane * box;
-            if (!in_sight(k0)) return 0;
-            return (int)(((page_of(p, b, token, shift, bad) * p.H + h) << shift) + (token & (p.page - 1)));
-        };
-        int next = n > 0 ? row_of(first * KEYS) : 0;
-        for (int j = 0; ok && j < n; j++) {
-            const int it = issued, k0 = (first + j) * KEYS, s = it % STAGES, row = next;
-            if (j + 1 < n) next = row_of(k0 + KEYS);
-            ok = page_wait(smem_u32(&sh.empty[s]), (it / STAGES + 1) & 1, abort_flag);
-            ok = !__any_sync(0xffffffffu, !ok);
-            if (!ok) break;
-            const uint32_t bar = smem_u32(&sh.full[s]), count = __popc(__ballot_sync(0xffffffffu, in_sight(k0)));
-            if (lane == 0) mbar_expect_tx(bar, count * box * 2 * (ROWB + (WIDE ? 0 : 4)));
-            __syncwarp();
-            if (in_sight(k0)) {
-                const uint32_t at = smem_u32(sm) + s * 2 * T::TILE + lane * box * 128;
-                tma_load_2d(at, &tmK, 0, row, bar);
-                tma_load_2d(at + T::TILE, &tmV, 0, row, bar);
-                if constexpr (WIDE) {
-                    tma_load_2d(at + T::TILE / 2, &tmK, 64, row, bar);
-                    tma_load_2d(at + T::TILE + T::TILE / 2, &tmV, 64, row, bar);
-                } else {
-                    bulk_g2s(smem_u32(&sh.ks[s][lane * box]), p.ks + row, box * 4, bar);
-                    bulk_g2s(smem_u32(&sh.vs[s][lane * box]), p.vs + row, box * 4, bar);
+            const int b = x.b, h = x.h, first = x.first, n = x.n;
+            const int lo = seen_lo(p, x.sq, 0), hi = seen_hi(p, x.sq, x.sq.qn - 1);
+            // the boxes of a stage that hold a key some row sees, a lane each; their pages are
+            // looked up one stage ahead
+            auto in_sight = [&](int k0) {
+                const int token = k0 + lane * box;
+                return lane < boxes && token < hi && token + box > lo;
+            };
+            auto row_of = [&](int k0) {
+                const int token = k0 + lane * box;
+                if (!in_sight(k0)) return 0;
+                return (int)(((page_of(p, b, token, shift, bad) * p.H + h) << shift) + (token & (p.page - 1)));
+            };
+            int next = n > 0 ? row_of(first * KEYS) : 0;
+            for (int j = 0; ok && j < n; j++) {
+                const int it = issued, k0 = (first + j) * KEYS, s = it % STAGES, row = next;
+                if (j + 1 < n) next = row_of(k0 + KEYS);
+                ok = page_wait(smem_u32(&sh.empty[s]), (it / STAGES + 1) & 1, abort_flag);
+                ok = !__any_sync(0xffffffffu, !ok);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&sh.full[s]), count = __popc(__ballot_sync(0xffffffffu, in_sight(k0)));
+                if (lane == 0) mbar_expect_tx(bar, count * box * 2 * (ROWB + (WIDE ? 0 : 4)));
+                __syncwarp();
+                if (in_sight(k0)) {
+                    const uint32_t at = smem_u32(sm) + s * 2 * T::TILE + lane * box * 128;
+                    tma_load_2d(at, &tmK, 0, row, bar);
+                    tma_load_2d(at + T::TILE, &tmV, 0, row, bar);
+                    if constexpr (WIDE) {
+                        tma_load_2d(at + T::TILE / 2, &tmK, 64, row, bar);
+                        tma_load_2d(at + T::TILE + T::TILE / 2, &tmV, 64, row, bar);
+                    } else {
+                        bulk_g2s(smem_u32(&sh.ks[s][lane * box]), p.ks + row, box * 4, bar);
+                        bulk_g2s(smem_u32(&sh.vs[s][lane * box]), p.vs + row, box * 4, bar);
+                    }
                 }
+                issued = it + 1;
             }
-            issued = it + 1;
-        }
         });
         if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
         // every copy lands before the CTA ends
@@ -313,409 +316,413 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
         int done = 0;  // stages of the items before
         bool ok = true;
         items([&](const RowsItem &item, int64_t part_row) {
-        const int b = SHARES ? item.b : blockIdx.z, h = SHARES ? item.h : blockIdx.y, first = item.first, n = item.n;
-        const SeqInfo sq = item.sq;
-        const int rows = sq.qn * p.G, lo = seen_lo(p, sq, 0), hi = seen_hi(p, sq, sq.qn - 1);
-        float o[RT][8][4], m[RT][2], l[RT][2];
+            const int b = SHARES ? item.b : blockIdx.z, h = SHARES ? item.h : blockIdx.y, first = item.first, n = item.n;
+            const SeqInfo sq = item.sq;
+            const int rows = sq.qn * p.G, lo = seen_lo(p, sq, 0), hi = seen_hi(p, sq, sq.qn - 1);
+            float o[RT][8][4], m[RT][2], l[RT][2];
 #pragma unroll
-        for (int y = 0; y < RT; y++) {
-            m[y][0] = m[y][1] = -INFINITY;
-            l[y][0] = l[y][1] = 0.f;
+            for (int y = 0; y < RT; y++) {
+                m[y][0] = m[y][1] = -INFINITY;
+                l[y][0] = l[y][1] = 0.f;
 #pragma unroll
-            for (int t = 0; t < 8; t++) o[y][t][0] = o[y][t][1] = o[y][t][2] = o[y][t][3] = 0.f;
-        }
-        int vexp = -100;  // exponent of the reference that the values' scales are taken against
-        // Q in the order the keys' chunks come in: lane (g, q) holds row g of each group
-        uint32_t qb[RT][8][2];
-        float qmul[RT][2];  // 8-bit pages: powers of two taken out of the rows whose scores this lane has
-        int row_lo[RT][2], row_hi[RT][2];
-#pragma unroll
-        for (int y = 0; y < RT; y++) {
-            const int r = 8 * y + g, i = token_of(p, min(r, rows - 1));
-            const uint16_t *src = static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt + (int64_t)(h * p.G + r - i * p.G) * p.qh;
-            uint4 w[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {  // 8 channels: two steps
-                const int ch = WIDE ? (j * 4 + q) * 8 : ((j >> 1) * 4 + q) * 16 + (j & 1) * 8;
-                w[j] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch)) : make_uint4(0u, 0u, 0u, 0u);
+                for (int t = 0; t < 8; t++) o[y][t][0] = o[y][t][1] = o[y][t][2] = o[y][t][3] = 0.f;
             }
-            float mul = 1.f;
-            if constexpr (!WIDE && QB) {
-                uint32_t big = 0;
+            int vexp = -100;  // exponent of the reference that the values' scales are taken against
+            // Q in the order the keys' chunks come in: lane (g, q) holds row g of each group
+            uint32_t qb[RT][8][2];
+            float qmul[RT][2];  // 8-bit pages: powers of two taken out of the rows whose scores this lane has
+            int row_lo[RT][2], row_hi[RT][2];
 #pragma unroll
-                for (int j = 0; j < 4; j++) big = max(big, bf16x2_max_bits(w[j]));
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                mul = bf16_pow2(big);
-                const float inv = 1.f / mul;
+            for (int y = 0; y < RT; y++) {
+                const int r = 8 * y + g, i = token_of(p, min(r, rows - 1));
+                const uint16_t *src = static_cast<const uint16_t *>(p.Q) + (sq.q0 + i) * p.qt +
+                                      (int64_t)(h * p.G + r - i * p.G) * p.qh;
+                uint4 w[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    w[j] = make_uint4(bf16x2_to_f16x2(w[j].x, inv), bf16x2_to_f16x2(w[j].y, inv),
-                                      bf16x2_to_f16x2(w[j].z, inv), bf16x2_to_f16x2(w[j].w, inv));
+                for (int j = 0; j < 4; j++) {  // 8 channels: two steps
+                    const int ch = WIDE ? (j * 4 + q) * 8 : ((j >> 1) * 4 + q) * 16 + (j & 1) * 8;
+                    w[j] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+                float mul = 1.f;
+                if constexpr (!WIDE && QB) {
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; j++) big = max(big, bf16x2_max_bits(w[j]));
+                    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    mul = bf16_pow2(big);
+                    const float inv = 1.f / mul;
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        w[j] = make_uint4(bf16x2_to_f16x2(w[j].x, inv), bf16x2_to_f16x2(w[j].y, inv),
+                                          bf16x2_to_f16x2(w[j].z, inv), bf16x2_to_f16x2(w[j].w, inv));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    qb[y][2 * j][0] = w[j].x;
+                    qb[y][2 * j][1] = w[j].y;
+                    qb[y][2 * j + 1][0] = w[j].z;
+                    qb[y][2 * j + 1][1] = w[j].w;
+                }
+                // the scores' columns of this lane are rows 2q and 2q + 1
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+                    qmul[y][x] = __shfl_sync(0xffffffffu, mul, (2 * q + x) * 4) * p.scale_log2;
+                    const int i = token_of(p, min(8 * y + 2 * q + x, rows - 1));
+                    row_lo[y][x] = seen_lo(p, sq, i);
+                    row_hi[y][x] = seen_hi(p, sq, i);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                qb[y][2 * j][0] = w[j].x;
-                qb[y][2 * j][1] = w[j].y;
-                qb[y][2 * j + 1][0] = w[j].z;
-                qb[y][2 * j + 1][1] = w[j].w;
-            }
-            // the scores' columns of this lane are rows 2q and 2q + 1
-#pragma unroll
-            for (int x = 0; x < 2; x++) {
-                qmul[y][x] = __shfl_sync(0xffffffffu, mul, (2 * q + x) * 4) * p.scale_log2;
-                const int i = token_of(p, min(8 * y + 2 * q + x, rows - 1));
-                row_lo[y][x] = seen_lo(p, sq, i);
-                row_hi[y][x] = seen_hi(p, sq, i);
-            }
-        }
 
-        // chunk c of row r of a swizzled tile (16 bits: two halves of 128-byte rows)
-        auto chunk = [](const unsigned char *tile, int r, int c) {
-            return *reinterpret_cast<const uint4 *>(tile + (c >> 3) * (T::TILE / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        };
-        // (a warp that gives up a wait keeps meeting the others)
-        for (int j = 0; ok && j < n; j++) {
-            const int it = done + j, st = it % STAGES, w0 = warp * 16 * KT, t0 = (first + j) * KEYS + w0;  // this warp's first key
-            ok = page_wait(smem_u32(&sh.full[st]), (it / STAGES) & 1, abort_flag);
-            ok = !__any_sync(0xffffffffu, !ok);
-            if (!ok) break;
-            if (t0 < hi && t0 + 16 * KT > lo) {
-                const unsigned char *kt = sm + st * 2 * T::TILE, *vt = kt + T::TILE;
-                // s[z][y][..]: keys t0 + 16 z + g (0, 1) and + 8 (2, 3), rows 8 y + 2 q, + 1
-                float s[KT][RT][4] = {};
+            // chunk c of row r of a swizzled tile (16 bits: two halves of 128-byte rows)
+            auto chunk = [](const unsigned char *tile, int r, int c) {
+                return *reinterpret_cast<const uint4 *>(tile + (c >> 3) * (T::TILE / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            };
+            // (a warp that gives up a wait keeps meeting the others)
+            for (int j = 0; ok && j < n; j++) {
+                const int it = done + j, st = it % STAGES;
+                const int w0 = warp * 16 * KT, t0 = (first + j) * KEYS + w0;  // this warp's first key
+                ok = page_wait(smem_u32(&sh.full[st]), (it / STAGES) & 1, abort_flag);
+                ok = !__any_sync(0xffffffffu, !ok);
+                if (!ok) break;
+                if (t0 < hi && t0 + 16 * KT > lo) {
+                    const unsigned char *kt = sm + st * 2 * T::TILE, *vt = kt + T::TILE;
+                    // s[z][y][..]: keys t0 + 16 z + g (0, 1) and + 8 (2, 3), rows 8 y + 2 q, + 1
+                    float s[KT][RT][4] = {};
 #pragma unroll
-                for (int c = 0; c < NCH; c++) {
+                    for (int c = 0; c < NCH; c++) {
+#pragma unroll
+                        for (int z = 0; z < KT; z++) {
+                            const uint4 ka = chunk(kt, w0 + z * 16 + g, c * 4 + q), kb = chunk(kt, w0 + z * 16 + g + 8, c * 4 + q);
+                            if constexpr (WIDE) {
+                                const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
+#pragma unroll
+                                for (int y = 0; y < RT; y++) {
+                                    mma16816<QB>(s[z][y], a0, qb[y][2 * c][0], qb[y][2 * c][1]);
+                                    mma16816<QB>(s[z][y], a1, qb[y][2 * c + 1][0], qb[y][2 * c + 1][1]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int w = 0; w < 4; w++) {
+                                    const uint2 ua = codes_to_f16<FMT == PF_E4M3>(word_of(ka, w)),
+                                                ub = codes_to_f16<FMT == PF_E4M3>(word_of(kb, w));
+                                    const uint32_t a[4] = {ua.x, ub.x, ua.y, ub.y};
+#pragma unroll
+                                    for (int y = 0; y < RT; y++) mma16816<false>(s[z][y], a, qb[y][4 * c + w][0], qb[y][4 * c + w][1]);
+                                }
+                            }
+                        }
+                    }
+                    const bool edge = t0 < lo || t0 + 16 * KT > hi;
+                    float vsc[KT][2];
 #pragma unroll
                     for (int z = 0; z < KT; z++) {
-                        const uint4 ka = chunk(kt, w0 + z * 16 + g, c * 4 + q), kb = chunk(kt, w0 + z * 16 + g + 8, c * 4 + q);
-                        if constexpr (WIDE) {
-                            const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
+                        float k2[2] = {1.f, 1.f};
+                        if constexpr (!WIDE) {
 #pragma unroll
-                            for (int y = 0; y < RT; y++) {
-                                mma16816<QB>(s[z][y], a0, qb[y][2 * c][0], qb[y][2 * c][1]);
-                                mma16816<QB>(s[z][y], a1, qb[y][2 * c + 1][0], qb[y][2 * c + 1][1]);
+                            for (int e = 0; e < 2; e++) {
+                                k2[e] = sh.ks[st][w0 + 16 * z + 8 * e + g];
+                                vsc[z][e] = sh.vs[st][w0 + 16 * z + 8 * e + g];
+                            }
+                        }
+#pragma unroll
+                        for (int y = 0; y < RT; y++) {
+                            s[z][y][0] *= qmul[y][0] * k2[0];
+                            s[z][y][1] *= qmul[y][1] * k2[0];
+                            s[z][y][2] *= qmul[y][0] * k2[1];
+                            s[z][y][3] *= qmul[y][1] * k2[1];
+                        }
+                        if (edge || sq.qn > 1) {
+#pragma unroll
+                            for (int y = 0; y < RT; y++)
+#pragma unroll
+                                for (int e = 0; e < 4; e++) {
+                                    const int key = t0 + 16 * z + 8 * (e >> 1) + g;
+                                    if (key < row_lo[y][e & 1] || key >= row_hi[y][e & 1]) s[z][y][e] = -INFINITY;
+                                }
+                        }
+                    }
+                    // 8-bit: the weights take in the values' scales relative to 2^vexp, an exponent
+                    // that follows the largest scale seen; times 2^8 they fill fp16's range
+                    float vcorr = 1.f;
+                    if constexpr (!WIDE) {
+                        float big = 0.f;
+#pragma unroll
+                        for (int z = 0; z < KT; z++)
+#pragma unroll
+                            for (int e = 0; e < 2; e++) {
+                                const int key = t0 + 16 * z + 8 * e + g;
+                                if (!edge || (key >= lo && key < hi)) big = fmaxf(big, fabsf(vsc[z][e]));
+                            }
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+                        const int ve = max(vexp, min((int)(__float_as_uint(big) >> 23) - 127, 121));
+                        vcorr = __uint_as_float((uint32_t)max(127 + vexp - ve, 0) << 23);
+                        const float vmul = __uint_as_float((uint32_t)(127 + 8 - ve) << 23);
+#pragma unroll
+                        for (int z = 0; z < KT; z++) {
+                            vsc[z][0] *= vmul;
+                            vsc[z][1] *= vmul;
+                        }
+                        vexp = ve;
+                    }
+                    uint32_t pb[KT][RT][2];
+#pragma unroll
+                    for (int y = 0; y < RT; y++) {
+                        float corr[2], base[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            float mx = m[y][x];
+#pragma unroll
+                            for (int z = 0; z < KT; z++) mx = fmax3(mx, s[z][y][x], s[z][y][2 + x]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                            base[x] = exp_base(mx);
+                            corr[x] = fast_exp2(m[y][x] - base[x]);
+                            m[y][x] = mx;
+                        }
+#pragma unroll
+                        for (int z = 0; z < KT; z++)
+#pragma unroll
+                            for (int e = 0; e < 2; e++) {
+                                float w0 = fast_exp2(s[z][y][2 * e] - base[0]), w1 = fast_exp2(s[z][y][2 * e + 1] - base[1]);
+                                sum[0] += w0;
+                                sum[1] += w1;
+                                if constexpr (!WIDE) {
+                                    w0 *= vsc[z][e];
+                                    w1 *= vsc[z][e];
+                                    if (edge || sq.qn > 1) {  // a hidden key's scale may be NaN: its weight stays 0
+                                        if (s[z][y][2 * e] == -INFINITY) w0 = 0.f;
+                                        if (s[z][y][2 * e + 1] == -INFINITY) w1 = 0.f;
+                                    }
+                                }
+                                pb[z][y][e] = transpose8x8(PVB ? pack_bf16(w0, w1) : pack_f16(w0, w1));
+                            }
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            l[y][x] = l[y][x] * corr[x] + sum[x];
+                            corr[x] *= vcorr;
+                        }
+                        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+                            for (int t = 0; t < 8; t++) {
+                                o[y][t][0] *= corr[0];
+                                o[y][t][1] *= corr[1];
+                                o[y][t][2] *= corr[0];
+                                o[y][t][3] *= corr[1];
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int z = 0; z < KT; z++) {
+                        uint4 vr[4][NCH / 2];  // keys 2q, 2q + 1, 2q + 8, 2q + 9
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const int at = 16 * z + 2 * q + (k & 1) + (k >> 1) * 8;
+#pragma unroll
+                            for (int c = 0; c < NCH / 2; c++) {
+                                vr[k][c] = chunk(vt, w0 + at, c * 8 + g);
+                                // values that no row sees may hold anything
+                                if (edge && (t0 + at < lo || t0 + at >= hi)) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        if constexpr (WIDE) {
+#pragma unroll
+                            for (int t = 0; t < 8; t++) {
+                                const int w = t >> 1, sel = t & 1 ? 0x7632 : 0x5410;
+                                const uint32_t a[4] = {__byte_perm(word_of(vr[0][0], w), word_of(vr[1][0], w), sel),
+                                                       __byte_perm(word_of(vr[0][1], w), word_of(vr[1][1], w), sel),
+                                                       __byte_perm(word_of(vr[2][0], w), word_of(vr[3][0], w), sel),
+                                                       __byte_perm(word_of(vr[2][1], w), word_of(vr[3][1], w), sel)};
+#pragma unroll
+                                for (int y = 0; y < RT; y++) mma16816<PVB>(o[y][t], a, pb[z][y][0], pb[z][y][1]);
                             }
                         } else {
 #pragma unroll
-                            for (int w = 0; w < 4; w++) {
-                                const uint2 ua = codes_to_f16<FMT == PF_E4M3>(word_of(ka, w)), ub = codes_to_f16<FMT == PF_E4M3>(word_of(kb, w));
-                                const uint32_t a[4] = {ua.x, ub.x, ua.y, ub.y};
+                            for (int w = 0; w < 2; w++) {
+                                // the codes of two keys interleaved, then widened pair by pair:
+                                // channels 4w .. 4w + 3 of the first and of the last eight
+                                uint2 a[2][2][2];  // [first / last eight][keys 2q.. / 2q + 8..][channels 0, 1 / 2, 3]
 #pragma unroll
-                                for (int y = 0; y < RT; y++) mma16816<false>(s[z][y], a, qb[y][4 * c + w][0], qb[y][4 * c + w][1]);
-                            }
-                        }
-                    }
-                }
-                const bool edge = t0 < lo || t0 + 16 * KT > hi;
-                float vsc[KT][2];
+                                for (int e = 0; e < 2; e++)
 #pragma unroll
-                for (int z = 0; z < KT; z++) {
-                    float k2[2] = {1.f, 1.f};
-                    if constexpr (!WIDE) {
+                                    for (int k = 0; k < 2; k++) {
+                                        const uint32_t v0 = word_of(vr[2 * k][0], w + 2 * e), v1 = word_of(vr[2 * k + 1][0], w + 2 * e);
+                                        a[e][k][0] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x5140));
+                                        a[e][k][1] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x7362));
+                                    }
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            k2[e] = sh.ks[st][w0 + 16 * z + 8 * e + g];
-                            vsc[z][e] = sh.vs[st][w0 + 16 * z + 8 * e + g];
-                        }
-                    }
+                                for (int t = 0; t < 4; t++) {
+                                    const int x = t >> 1;
+                                    const uint32_t f[4] = {t & 1 ? a[0][0][x].y : a[0][0][x].x, t & 1 ? a[1][0][x].y : a[1][0][x].x,
+                                                           t & 1 ? a[0][1][x].y : a[0][1][x].x, t & 1 ? a[1][1][x].y : a[1][1][x].x};
 #pragma unroll
-                    for (int y = 0; y < RT; y++) {
-                        s[z][y][0] *= qmul[y][0] * k2[0];
-                        s[z][y][1] *= qmul[y][1] * k2[0];
-                        s[z][y][2] *= qmul[y][0] * k2[1];
-                        s[z][y][3] *= qmul[y][1] * k2[1];
-                    }
-                    if (edge || sq.qn > 1) {
-#pragma unroll
-                        for (int y = 0; y < RT; y++)
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const int key = t0 + 16 * z + 8 * (e >> 1) + g;
-                                if (key < row_lo[y][e & 1] || key >= row_hi[y][e & 1]) s[z][y][e] = -INFINITY;
-                            }
-                    }
-                }
-                // 8-bit: the weights take in the values' scales relative to 2^vexp, an exponent
-                // that follows the largest scale seen; times 2^8 they fill fp16's range
-                float vcorr = 1.f;
-                if constexpr (!WIDE) {
-                    float big = 0.f;
-#pragma unroll
-                    for (int z = 0; z < KT; z++)
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const int key = t0 + 16 * z + 8 * e + g;
-                            if (!edge || (key >= lo && key < hi)) big = fmaxf(big, fabsf(vsc[z][e]));
-                        }
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-                    const int ve = max(vexp, min((int)(__float_as_uint(big) >> 23) - 127, 121));
-                    vcorr = __uint_as_float((uint32_t)max(127 + vexp - ve, 0) << 23);
-                    const float vmul = __uint_as_float((uint32_t)(127 + 8 - ve) << 23);
-#pragma unroll
-                    for (int z = 0; z < KT; z++) {
-                        vsc[z][0] *= vmul;
-                        vsc[z][1] *= vmul;
-                    }
-                    vexp = ve;
-                }
-                uint32_t pb[KT][RT][2];
-#pragma unroll
-                for (int y = 0; y < RT; y++) {
-                    float corr[2], base[2], sum[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        float mx = m[y][x];
-#pragma unroll
-                        for (int z = 0; z < KT; z++) mx = fmax3(mx, s[z][y][x], s[z][y][2 + x]);
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        base[x] = exp_base(mx);
-                        corr[x] = fast_exp2(m[y][x] - base[x]);
-                        m[y][x] = mx;
-                    }
-#pragma unroll
-                    for (int z = 0; z < KT; z++)
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            float w0 = fast_exp2(s[z][y][2 * e] - base[0]), w1 = fast_exp2(s[z][y][2 * e + 1] - base[1]);
-                            sum[0] += w0;
-                            sum[1] += w1;
-                            if constexpr (!WIDE) {
-                                w0 *= vsc[z][e];
-                                w1 *= vsc[z][e];
-                                if (edge || sq.qn > 1) {  // a hidden key's scale may be NaN: its weight stays 0
-                                    if (s[z][y][2 * e] == -INFINITY) w0 = 0.f;
-                                    if (s[z][y][2 * e + 1] == -INFINITY) w1 = 0.f;
+                                    for (int y = 0; y < RT; y++) mma16816<false>(o[y][4 * w + t], f, pb[z][y][0], pb[z][y][1]);
                                 }
                             }
-                            pb[z][y][e] = transpose8x8(PVB ? pack_bf16(w0, w1) : pack_f16(w0, w1));
-                        }
-#pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        l[y][x] = l[y][x] * corr[x] + sum[x];
-                        corr[x] *= vcorr;
-                    }
-                    if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-                        for (int t = 0; t < 8; t++) {
-                            o[y][t][0] *= corr[0];
-                            o[y][t][1] *= corr[1];
-                            o[y][t][2] *= corr[0];
-                            o[y][t][3] *= corr[1];
                         }
                     }
                 }
-#pragma unroll
-                for (int z = 0; z < KT; z++) {
-                    uint4 vr[4][NCH / 2];  // keys 2q, 2q + 1, 2q + 8, 2q + 9
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const int at = 16 * z + 2 * q + (k & 1) + (k >> 1) * 8;
-#pragma unroll
-                        for (int c = 0; c < NCH / 2; c++) {
-                            vr[k][c] = chunk(vt, w0 + at, c * 8 + g);
-                            // values that no row sees may hold anything
-                            if (edge && (t0 + at < lo || t0 + at >= hi)) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    if constexpr (WIDE) {
-#pragma unroll
-                        for (int t = 0; t < 8; t++) {
-                            const int w = t >> 1, sel = t & 1 ? 0x7632 : 0x5410;
-                            const uint32_t a[4] = {__byte_perm(word_of(vr[0][0], w), word_of(vr[1][0], w), sel),
-                                                   __byte_perm(word_of(vr[0][1], w), word_of(vr[1][1], w), sel),
-                                                   __byte_perm(word_of(vr[2][0], w), word_of(vr[3][0], w), sel),
-                                                   __byte_perm(word_of(vr[2][1], w), word_of(vr[3][1], w), sel)};
-#pragma unroll
-                            for (int y = 0; y < RT; y++) mma16816<PVB>(o[y][t], a, pb[z][y][0], pb[z][y][1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < 2; w++) {
-                            // the codes of two keys interleaved, then widened pair by pair:
-                            // channels 4w .. 4w + 3 of the first and of the last eight
-                            uint2 a[2][2][2];  // [first / last eight][keys 2q.. / 2q + 8..][channels 0, 1 / 2, 3]
-#pragma unroll
-                            for (int e = 0; e < 2; e++)
-#pragma unroll
-                                for (int k = 0; k < 2; k++) {
-                                    const uint32_t v0 = word_of(vr[2 * k][0], w + 2 * e), v1 = word_of(vr[2 * k + 1][0], w + 2 * e);
-                                    a[e][k][0] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x5140));
-                                    a[e][k][1] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x7362));
-                                }
-#pragma unroll
-                            for (int t = 0; t < 4; t++) {
-                                const int x = t >> 1;
-                                const uint32_t f[4] = {t & 1 ? a[0][0][x].y : a[0][0][x].x, t & 1 ? a[1][0][x].y : a[1][0][x].x,
-                                                       t & 1 ? a[0][1][x].y : a[0][1][x].x, t & 1 ? a[1][1][x].y : a[1][1][x].x};
-#pragma unroll
-                                for (int y = 0; y < RT; y++) mma16816<false>(o[y][4 * w + t], f, pb[z][y][0], pb[z][y][1]);
-                            }
-                        }
-                    }
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
-        }
-        if (SHARES) done += n;
+            if (SHARES) done += n;
 
-        // join the warps relative to the largest of their maxima: through the ring, which is
-        // through with its keys, or, where the next item's are on their way, one after another in
-        // a place of its own
-        const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp - 8) << 23);
-        if constexpr (!SHARES) rows_meet();
-#pragma unroll
-        for (int y = 0; y < RT; y++)
-#pragma unroll
-            for (int x = 0; x < 2; x++) {
-                const int r = 8 * y + 2 * q + x;
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[y][x] += __shfl_xor_sync(0xffffffffu, l[y][x], d);
-                if (g == 0) {
-                    sh.m[warp][r] = m[y][x];
-                    sh.l[warp][r] = l[y][x];
-                }
-            }
-        // this lane's channels (two runs of eight of each row), added to what is there or stored
-        auto put = [&](float(*rows_o)[kRowsPad], bool add, bool relative) {
+            // join the warps relative to the largest of their maxima: through the ring, which is
+            // through with its keys, or, where the next item's are on their way, one after another in
+            // a place of its own
+            const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp - 8) << 23);
+            if constexpr (!SHARES) rows_meet();
 #pragma unroll
             for (int y = 0; y < RT; y++)
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
                     const int r = 8 * y + 2 * q + x;
-                    float f = 1.f;
-                    if (relative) {
-                        const float top = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
-                        f = fast_exp2(m[y][x] - exp_base(top));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[y][x] += __shfl_xor_sync(0xffffffffu, l[y][x], d);
+                    if (g == 0) {
+                        sh.m[warp][r] = m[y][x];
+                        sh.l[warp][r] = l[y][x];
                     }
-#pragma unroll
-                    for (int e = 0; e < 2; e++)
-#pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            float4 *dst = reinterpret_cast<float4 *>(&rows_o[r][(WIDE ? 64 * e + 8 * g : 16 * g + 8 * e) + k]);
-                            float4 v = make_float4(o[y][k][2 * e + x] * unit, o[y][k + 1][2 * e + x] * unit,
-                                                   o[y][k + 2][2 * e + x] * unit, o[y][k + 3][2 * e + x] * unit);
-                            if (relative) {
-                                const float4 a = add ? *dst : make_float4(0.f, 0.f, 0.f, 0.f);
-                                v = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
-                            }
-                            *dst = v;
-                        }
                 }
-        };
-        if constexpr (SHARES) {
-            rows_meet();
+            // this lane's channels (two runs of eight of each row), added to what is there or stored
+            auto put = [&](float(*rows_o)[kRowsPad], bool add, bool relative) {
+#pragma unroll
+                for (int y = 0; y < RT; y++)
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const int r = 8 * y + 2 * q + x;
+                        float f = 1.f;
+                        if (relative) {
+                            const float top = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+                            f = fast_exp2(m[y][x] - exp_base(top));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+#pragma unroll
+                            for (int k = 0; k < 8; k += 4) {
+                                float4 *dst = reinterpret_cast<float4 *>(&rows_o[r][(WIDE ? 64 * e + 8 * g : 16 * g + 8 * e) + k]);
+                                float4 v = make_float4(o[y][k][2 * e + x] * unit, o[y][k + 1][2 * e + x] * unit,
+                                                       o[y][k + 2][2 * e + x] * unit, o[y][k + 3][2 * e + x] * unit);
+                                if (relative) {
+                                    const float4 a = add ? *dst : make_float4(0.f, 0.f, 0.f, 0.f);
+                                    v = make_float4(a.x + f * v.x, a.y + f * v.y, a.z + f * v.z, a.w + f * v.w);
+                                }
+                                *dst = v;
+                            }
+                    }
+            };
+            if constexpr (SHARES) {
+                rows_meet();
 #pragma unroll 1
-            for (int w = 0; w < kRowsWarps; w++) {
-                if (warp == w) put(sh.o, w > 0, true);
+                for (int w = 0; w < kRowsWarps; w++) {
+                    if (warp == w) put(sh.o, w > 0, true);
+                    rows_meet();
+                }
+            } else {
+                put(s_o[warp], false, false);
                 rows_meet();
             }
-        } else {
-            put(s_o[warp], false, false);
-            rows_meet();
-        }
-        // eight lanes a row, 16 channels each (in runs of four, so that the lanes' reads and
-        // writes are next to one another); the other warps only keep the barriers
-        const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
-        float M = -INFINITY, L = 0.f, v[16] = {};
-        const bool mine = r < ROWS;
-        if (mine) {
-#pragma unroll
-            for (int w = 0; w < kRowsWarps; w++) M = fmaxf(M, sh.m[w][r]);
-            const float base = exp_base(M);
-#pragma unroll
-            for (int w = 0; w < kRowsWarps; w++) {
-                const float f = fast_exp2(sh.m[w][r] - base);
-                L += f * sh.l[w][r];
-#pragma unroll
-                for (int c = 0; c < 16; c++) {
-                    const int at = (c >> 2) * 32 + part * 4 + (c & 3);
-                    if constexpr (!SHARES)
-                        v[c] += f * s_o[w][r][at];
-                    else if (w == 0)
-                        v[c] = sh.o[r][at];
-                }
-            }
-        }
-        const int row_i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - row_i * p.G;
-        bool live = mine && r < rows;
-        if constexpr (SHARES) rows_meet();  // the join's rows are read: the next item's may follow
-        if (SHARES ? !item.whole : p.S > 1 && !joined) {
-            if (!live) return;
-            const int64_t at = (SHARES ? part_row : (((int64_t)blockIdx.z * p.H + blockIdx.y) * p.S + blockIdx.x) * kRowsM) + r;
-#pragma unroll
-            for (int c = 0; c < 4; c++) store4<DT_F32>(p.part, at * kD + c * 32 + part * 4, v + 4 * c);
-            if (part == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = make_float2(M, L);
-            return;
-        }
-        if (!SHARES && joined) {
-            // each CTA of the cluster finishes the rows r with r % S its rank
+            // eight lanes a row, 16 channels each (in runs of four, so that the lanes' reads and
+            // writes are next to one another); the other warps only keep the barriers
+            const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
+            float M = -INFINITY, L = 0.f, v[16] = {};
+            const bool mine = r < ROWS;
             if (mine) {
 #pragma unroll
-                for (int c = 0; c < 4; c++)
-                    *reinterpret_cast<float4 *>(&s_o[kRowsWarps][r][c * 32 + part * 4]) =
-                        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-                if (part == 0) sh.ml[r] = make_float2(M, L);
-            }
-            cluster_meet();
-            live = live && r % p.S == (int)blockIdx.x;
-            if (live) {
-                M = -INFINITY;
-                for (int s = 0; s < p.S; s++) M = fmaxf(M, ld_cluster2(cluster_addr(&sh.ml[r], s)).x);
+                for (int w = 0; w < kRowsWarps; w++) M = fmaxf(M, sh.m[w][r]);
                 const float base = exp_base(M);
-                L = 0.f;
 #pragma unroll
-                for (int c = 0; c < 16; c++) v[c] = 0.f;
-                for (int s = 0; s < p.S; s++) {
-                    const float2 ml = ld_cluster2(cluster_addr(&sh.ml[r], s));
-                    const float f = fast_exp2(ml.x - base);
-                    L += f * ml.y;
+                for (int w = 0; w < kRowsWarps; w++) {
+                    const float f = fast_exp2(sh.m[w][r] - base);
+                    L += f * sh.l[w][r];
 #pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        const float4 y = ld_cluster4(cluster_addr(&s_o[kRowsWarps][r][c * 32 + part * 4], s));
-                        v[4 * c] += f * y.x;
-                        v[4 * c + 1] += f * y.y;
-                        v[4 * c + 2] += f * y.z;
-                        v[4 * c + 3] += f * y.w;
+                    for (int c = 0; c < 16; c++) {
+                        const int at = (c >> 2) * 32 + part * 4 + (c & 3);
+                        if constexpr (!SHARES)
+                            v[c] += f * s_o[w][r][at];
+                        else if (w == 0)
+                            v[c] = sh.o[r][at];
                     }
                 }
             }
-            cluster_meet();  // nobody leaves while its rows are read
-        }
-        if (!mine) return;
-    if (redo_possible(p)) {
-        bool odd = false;
+            const int row_i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - row_i * p.G;
+            bool live = mine && r < rows;
+            if constexpr (SHARES) rows_meet();  // the join's rows are read: the next item's may follow
+            if (SHARES ? !item.whole : p.S > 1 && !joined) {
+                if (!live) return;
+                const int64_t cell = (int64_t)blockIdx.z * p.H + blockIdx.y;
+                const int64_t at = (SHARES ? part_row : (cell * p.S + blockIdx.x) * kRowsM) + r;
 #pragma unroll
-        for (int c = 0; c < 16; c++) odd |= !is_finite(v[c]);
-        uint32_t todo = __ballot_sync(0xffffffffu, odd && live);
-        while (todo) {
-            const int src = (__ffs(todo) - 1) & ~7;  // the row's first lane
-            todo &= ~(0xFFu << src);
-            float ro[4], rm, rl;
-            redo_row(p, b, __shfl_sync(0xffffffffu, row_i, src), __shfl_sync(0xffffffffu, hq, src), ro, rm, rl);
-            // lane x has channels 4x ..: this thread's are those of lanes part + 8 c
-#pragma unroll
-            for (int c = 0; c < 16; c++) {
-                const float y = __shfl_sync(0xffffffffu, ro[c & 3], (c >> 2) * 8 + part);
-                if ((lane & ~7) == src) v[c] = y;
+                for (int c = 0; c < 4; c++) store4<DT_F32>(p.part, at * kD + c * 32 + part * 4, v + 4 * c);
+                if (part == 0) *reinterpret_cast<float2 *>(p.ml + 2 * at) = make_float2(M, L);
+                return;
             }
-            if ((lane & ~7) == src) {
-                M = rm;
-                L = rl;
+            if (!SHARES && joined) {
+                // each CTA of the cluster finishes the rows r with r % S its rank
+                if (mine) {
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        *reinterpret_cast<float4 *>(&s_o[kRowsWarps][r][c * 32 + part * 4]) =
+                            make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                    if (part == 0) sh.ml[r] = make_float2(M, L);
+                }
+                cluster_meet();
+                live = live && r % p.S == (int)blockIdx.x;
+                if (live) {
+                    M = -INFINITY;
+                    for (int s = 0; s < p.S; s++) M = fmaxf(M, ld_cluster2(cluster_addr(&sh.ml[r], s)).x);
+                    const float base = exp_base(M);
+                    L = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 16; c++) v[c] = 0.f;
+                    for (int s = 0; s < p.S; s++) {
+                        const float2 ml = ld_cluster2(cluster_addr(&sh.ml[r], s));
+                        const float f = fast_exp2(ml.x - base);
+                        L += f * ml.y;
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            const float4 y = ld_cluster4(cluster_addr(&s_o[kRowsWarps][r][c * 32 + part * 4], s));
+                            v[4 * c] += f * y.x;
+                            v[4 * c + 1] += f * y.y;
+                            v[4 * c + 2] += f * y.z;
+                            v[4 * c + 3] += f * y.w;
+                        }
+                    }
+                }
+                cluster_meet();  // nobody leaves while its rows are read
+            }
+            if (!mine) return;
+        if (redo_possible(p)) {
+            bool odd = false;
+#pragma unroll
+            for (int c = 0; c < 16; c++) odd |= !is_finite(v[c]);
+            uint32_t todo = __ballot_sync(0xffffffffu, odd && live);
+            while (todo) {
+                const int src = (__ffs(todo) - 1) & ~7;  // the row's first lane
+                todo &= ~(0xFFu << src);
+                float ro[4], rm, rl;
+                redo_row(p, b, __shfl_sync(0xffffffffu, row_i, src), __shfl_sync(0xffffffffu, hq, src), ro, rm, rl);
+                // lane x has channels 4x ..: this thread's are those of lanes part + 8 c
+#pragma unroll
+                for (int c = 0; c < 16; c++) {
+                    const float y = __shfl_sync(0xffffffffu, ro[c & 3], (c >> 2) * 8 + part);
+                    if ((lane & ~7) == src) v[c] = y;
+                }
+                if ((lane & ~7) == src) {
+                    M = rm;
+                    L = rl;
+                }
             }
         }
-    }
-    if (!live) return;
-    const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
-    const int64_t at = (sq.q0 + row_i) * p.ot + hq * p.oh;
+        if (!live) return;
+        const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+        const int64_t at = (sq.q0 + row_i) * p.ot + hq * p.oh;
 #pragma unroll
-    for (int c = 0; c < 16; c++) v[c] *= inv;
+        for (int c = 0; c < 16; c++) v[c] *= inv;
 #pragma unroll
-    for (int c = 0; c < 4; c++) store_out4(p, at + c * 32 + part * 4, v + 4 * c);
-    if (p.lse && part == 0) p.lse[(sq.q0 + row_i) * p.HQ + hq] = row_lse(M, L);
+        for (int c = 0; c < 4; c++) store_out4(p, at + c * 32 + part * 4, v + 4 * c);
+        if (p.lse && part == 0) p.lse[(sq.q0 + row_i) * p.HQ + hq] = row_lse(M, L);
         });
         if (threadIdx.x == 0 && *abort_flag) or_status(p.status, QVG_DEV_TIMEOUT);
     }

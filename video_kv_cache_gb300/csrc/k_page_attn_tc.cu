@@ -32,19 +32,19 @@
 // two (128 each): all 512 columns, one CTA an SM.
 //
 // 8-bit pages: eight more warps widen the codes to fp16 into the ring, from raw tiles of 64 keys
-// that TMA brings (half a tile each: that leaves room for four slots of widened ones).  bf16
+// that TMA brings (half a tile each: that leaves room for four slots of widened ones). bf16
 // queries are made fp16 too, each row scaled by a power of two that brings its largest channel
-// to 1 .. 2: what falls below fp16's range is 2^-25 of that.  Where the output is bf16 and no
+// to 1 .. 2: what falls below fp16's range is 2^-25 of that. Where the output is bf16 and no
 // log-sum-exp is asked for (FOLD), the keys' and values' scales are multiplied in while
 // widening, relative to a power of two (of the tile's largest scale for keys; for values, whose
 // sums outlive the tile, of the largest so far), and the product is rounded to fp16 once: 2^-11
-// of each key and value, an eighth of what the output's own rounding is.  Otherwise the scales
+// of each key and value, an eighth of what the output's own rounding is. Otherwise the scales
 // multiply the scores and the weights in the softmax (the weights, in fp16, relative to the same
 // power of two), which costs time: every thread then reads the scales of all keys from shared
-// memory.  The case above takes 901 us in e4m3 and 969 in int8, without folding 1087 and 1117.
-// These are bound by instruction issue: 11100 warp instructions a tile against 5900 in 16 bits,
-// 0.8 a cycle where the SM is full; with one factor instead of two (a scale rounded to fp16, an
-// error that all channels of a key share) they would take 881 and 936.
+// memory. The case above takes 901 us in e4m3 and 969 in int8, without folding 1087 and 1117.
+// What costs is instructions: 10300 of a warp a tile pair against 5500 in 16 bits, which share
+// the issue slots with the exponentials; with one factor instead of two (a scale rounded to
+// fp16, an error that all channels of a key share) they would take 881 and 936.
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
