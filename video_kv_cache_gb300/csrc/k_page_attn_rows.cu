@@ -870,7 +870,7 @@ cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
     CUtensorMap mk, mv;
     const int box = std::min(p.page, RowsShape<FMT, RT>::KEYS);
     if (!page_map(p, p.k, box, &mk) || !page_map(p, p.v, box, &mv)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<k_page_attn_rows<QB, FMT, RT, SHARES>>(smem);
     if (e != cudaSuccess) return e;
     const int joined = p.S > 1 && p.S <= kRowsCluster;
     const dim3 grid = SHARES ? dim3(kRowsShares) : dim3((unsigned)p.S, p.H, p.B);

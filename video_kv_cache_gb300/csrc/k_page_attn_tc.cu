@@ -863,7 +863,7 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
     using T = TcShape<FMT>;
     constexpr size_t smem = tc_smem<FMT>();
     const auto kernel = k_page_attn_tc<QB, FMT, FOLD>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<k_page_attn_tc<QB, FMT, FOLD>>(smem);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)p.units * p.H * p.B, grid = p.whole + (items - p.whole) * p.S;
     return launch_kernel(kernel, dim3((unsigned)grid), dim3(T::THREADS), smem, st, mk, mv, p);
