@@ -372,6 +372,22 @@ def test_page_attention(case):
     _check(Q, kv, table, kv_lens, q_lens, causal, window)
 
 
+RAGGED = [  # as ATTEND: more items than SMs, those that see the most first
+    ([300, 0, 70, 513], [400, 50, 70, 1200], 44, 44, BF, BF, 32, True, 0),
+    ([40, 260], [41, 700], 90, 90, HF, I8, 16, True, 300),
+    ([33, 1, 0, 257, 257], [20, 0, 9, 300, 300], 40, 40, BF, E4, 64, False, 0),
+]
+
+
+@pytest.mark.parametrize("case", RAGGED)
+def test_page_attention_of_many_heads_and_unlike_sequences(case):
+    q_lens, kv_lens, q_heads, heads, dtype, fmt, page, causal, window = case
+    g = _gen(sum(q_lens) + heads)
+    kv, table = _cache(g, kv_lens, heads, fmt, page)
+    Q = torch.randn((sum(q_lens), q_heads, 128), generator=g).to(dtype)
+    _check(Q, kv, table, kv_lens, q_lens, causal, window)
+
+
 SHARES = [  # longest and other cached lengths, q lengths, q heads, heads, q type, format, page, causal, window
     ([2900, 0, 1, 64, 127, 128, 129, 700] * 3, [1], 8, 4, BF, BF, 64, True, 0),
     ([1500, 0, 1, 64, 127, 128, 129, 700] * 3, [2, 0, 1, 3], 10, 5, BF, I8, 32, True, 0),

@@ -473,6 +473,7 @@ struct PAttnPlan {
     // are split S ways, a CTA each, and joined.
     int unit, units, S;
     int64_t whole;
+    int by_length;  // many rows: the items of few sequences (at most 32) in the order of what they see
     // Few rows, long keys: all heads' keys in a row are cut into equal shares instead, a CTA
     // each, whose first and last stretches may be parts of a head.
     int stream;

@@ -814,11 +814,14 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
 //   (Splitting every item alike would write 57 MB of partial results for 4680 x 32760 x 12
 //   heads, one and a half rounds, instead of 19.)  Sequences with different numbers of queries
 //   leave items empty, and the last ones say nothing about the last round: there all items
-//   are split alike, if they are too few for one round.
+//   are split alike, if they are too few for one round; else, up to 16 sequences, the items of
+//   those that see the most come first, so that the last round is one of short ones (six
+//   sequences of up to 2000 queries over 500 to 9000 keys, 32 query heads on 8: 238 -> 208 us,
+//   301 -> 278; thirty even out by themselves: 1701 us, in order 1762).
 void page_attention_cut(PAttnPlan &p) {
     const int64_t rows = p.max_q * p.G, cells = (int64_t)p.H * p.B;
     p.whole = 0;
-    p.stream = 0;
+    p.stream = p.by_length = 0;
     if (rows <= kRowsM) {
         p.unit = kRowsM;
         p.units = 1;
@@ -855,6 +858,7 @@ void page_attention_cut(PAttnPlan &p) {
             p.whole = alike ? items - rest : 0;
         }
     }
+    p.by_length = p.S == 1 && !alike && p.B <= 16;
 }
 int64_t page_attention_part_rows(const PAttnPlan &p) {
     if (p.stream) return 2 * (int64_t)kRowsShares * kRowsM;

@@ -258,9 +258,31 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     const int64_t tail = whole_item ? 0 : (blockIdx.x - p.whole) / p.S;
     const int split = whole_item ? 0 : (int)((blockIdx.x - p.whole) - tail * p.S), S = whole_item ? 1 : p.S;
     const int64_t item = whole_item ? blockIdx.x : p.whole + tail;
-    const int cell = (int)(item / p.units), pair = p.units - 1 - (int)(item - (int64_t)cell * p.units);
-    const int b = cell / p.H, h = cell - b * p.H;
-    const SeqInfo sq = seq_info(p, b, threadIdx.x == 0 && pair == 0 && split == 0 && h == 0);
+    const int cell = (int)(item / p.units);
+    int b = cell / p.H, h = cell - b * p.H, pair = p.units - 1 - (int)(item - (int64_t)cell * p.units);
+    if (p.by_length) {
+        // the sequences, a lane each, those whose last rows see the most first, and only the
+        // items that they have
+        SeqInfo s = {0, 0, 0};
+        if (lane < p.B) s = seq_info(p, lane, blockIdx.x == 0 && warp == 0);
+        const int units = (s.qn * p.G + 2 * kTcM - 1) / (2 * kTcM);
+        const int seen = units ? seen_hi(p, s, s.qn - 1) - seen_lo(p, s, token_of(p, (units - 1) * 2 * kTcM)) : 0;
+        int ahead = 0;
+        for (int x = 0; x < p.B; x++) {
+            const int their = __shfl_sync(0xffffffffu, seen, x), n = __shfl_sync(0xffffffffu, units, x);
+            if (their > seen || (their == seen && x < lane)) ahead += n;
+        }
+        const int64_t in = blockIdx.x - (int64_t)ahead * p.H;
+        const bool mine = in >= 0 && in < (int64_t)units * p.H;
+        const uint32_t owner = __ballot_sync(0xffffffffu, mine);
+        if (!owner) return;
+        // (reductions leave their results in uniform registers, of which there are enough)
+        const int n = (int)__reduce_max_sync(0xffffffffu, mine ? units : 0), at = (int)__reduce_max_sync(0xffffffffu, mine ? (int)in : 0);
+        b = __ffs(owner) - 1;
+        h = at / n;
+        pair = n - 1 - (at - h * n);
+    }
+    const SeqInfo sq = seq_info(p, b, !p.by_length && threadIdx.x == 0 && pair == 0 && split == 0 && h == 0);
     const int rows = sq.qn * p.G, r0 = pair * 2 * kTcM;
     if (r0 >= rows) return;
     const int nt = rows - r0 > kTcM ? 2 : 1;  // row tiles in use
