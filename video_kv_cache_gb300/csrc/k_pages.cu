@@ -94,6 +94,10 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteCtas) k_page_write(PWrite
         }
     }
     const int64_t slot = __ldg(reinterpret_cast<const long long *>(p.slots) + token);
+    // positions and frequencies arrive beside the rows and the slot
+    const bool turns = p.r.rot > 0;  // the same for every lane
+    Turn t;
+    if (turns && at.turned) t = turn_of(p.r, token, l, 1.f);
     if (slot < 0) return;
     const int shift = 31 - __clz(p.page);
     const int64_t page = slot >> shift;
@@ -102,11 +106,8 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteCtas) k_page_write(PWrite
         return;
     }
     const int64_t row0 = ((page * p.heads + h0) << shift) + (slot & (p.page - 1));
-    const bool turns = p.r.rot > 0;  // the same for every lane
     float kf[kWriteHeads][8];
     if (turns) {
-        Turn t;
-        if (at.turned) t = turn_of(p.r, token, l, 1.f);
 #pragma unroll
         for (int u = 0; u < kWriteHeads; u++) {
             unpack4(k[u].a, kf[u]);

@@ -4,7 +4,8 @@
 // Bound by memory: each row is read and written once (512 bytes a row in 16 bits against
 // about 20 warp instructions).  Sixteen lanes hold a row (rows.cuh) and take up to eight heads
 // of one token, so the sines and cosines, four pairs a lane, are computed once for all of them.
-// 65536 tokens of 32 heads in bf16: 161 us (6.7 TB/s); 4680 of 12: 6 us.
+// 65536 tokens of 32 heads in bf16: 153 us (7.0 TB/s); 4680 of 12: 6 us.  The first rows are
+// asked for before the positions (after them: 163 us).
 #include "rows.cuh"
 
 namespace qvg {
@@ -24,13 +25,17 @@ __global__ void __launch_bounds__(256) k_rope(RopePlan p) {
     if (token >= p.n) return;
     const int h0 = (int)(unit - token * groups) * kRopeHeads, h1 = min(p.heads, h0 + kRopeHeads);
     const Pieces at = pieces_of(l, p.r);
-    Turn t;
-    if (at.turned) t = turn_of(p.r, token, l, p.backward ? -1.f : 1.f);
-    for (int h = h0; h < h1; h += kRopeRows) {
-        Raw8<DT> raw[kRopeRows];
+    Raw8<DT> raw[kRopeRows];
+    auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < kRopeRows; u++)
             if (h + u < h1) raw[u] = load_raw8<DT, !INTER>(p.X, token * p.xt + (h + u) * p.xh, at);
+    };
+    load(h0);  // the first rows arrive beside the positions
+    Turn t;
+    if (at.turned) t = turn_of(p.r, token, l, p.backward ? -1.f : 1.f);
+    for (int h = h0; h < h1; h += kRopeRows) {
+        if (h > h0) load(h);
 #pragma unroll
         for (int u = 0; u < kRopeRows; u++) {
             if (h + u < h1) {
