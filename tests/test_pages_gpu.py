@@ -568,6 +568,35 @@ def test_page_attention_reports_bad_arguments_on_the_device():
         assert not bool((out[:-1] == 7).all(-1).any())
 
 
+@pytest.mark.parametrize("nq,heads,fmt", [(1, 90, I8), (300, 90, BF)])
+def test_many_heads_report_bad_arguments_on_the_device(nq, heads, fmt):
+    # equal shares, and items in the order of what they see: what is bad is reported all the same
+    g = _gen(12)
+    kv, table = _cache(g, [300, 0], heads, fmt, 16)
+    table = torch.cat([table, torch.zeros((2, 300), dtype=torch.int32)], 1)
+    total = nq + 1
+    Q = torch.randn((total, heads, 128), generator=g).to(BF).cuda()
+
+    def status_of(table=table, lens=(300, 0), cu=(0, nq, total)):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full_like(Q, 7.0)
+        api.page_attention(Q, kv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                           cu_q=torch.tensor(cu, dtype=torch.int32).cuda(), max_q=nq, status=st, out=out)
+        return int(st), out
+    st, good = status_of()
+    assert st == 0 and not good[nq:].any() and not bool((good == 7).all(-1).any())
+    bad = table.clone()
+    bad[0, 3] = kv.n_pages
+    assert status_of(table=bad)[0] == qvg.QVG_DEV_BAD_INDEX
+    bad[0, 3] = -1
+    assert status_of(table=bad)[0] == qvg.QVG_DEV_BAD_INDEX
+    st, out = status_of(lens=(300, -5))
+    assert st == qvg.QVG_DEV_BAD_INDEX and torch.equal(out, good)
+    assert status_of(lens=(table.shape[1] * 16 + 1, 0))[0] == qvg.QVG_DEV_BAD_INDEX
+    for cu in ((0, nq, total + 9), (0, -3, nq), (nq, 0, nq)):
+        assert status_of(cu=cu)[0] == qvg.QVG_DEV_BAD_INDEX
+
+
 @pytest.mark.parametrize("nq", [1, 100])
 def test_capture_replay_and_other_streams(nq):
     g = _gen(11)
