@@ -636,6 +636,28 @@ def test_capture_replay_and_other_streams(nq):
         assert all(torch.equal(a, b) for a, b in zip(outs, ref))
 
 
+@pytest.mark.parametrize("fmt", [BF, I8, E4])
+@pytest.mark.parametrize("nq", [1, 5])
+def test_split_calls_back_to_back(nq, fmt):
+    # long sequences in parts, launched one behind the other without a pause: every call the same
+    g = _gen(nq)
+    n, heads, page, seqs = 15000, 8, 64, 4
+    per = -(-n // page)
+    kv = api.allocate_pages(seqs * per, heads, page, fmt)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    for t in (kv.k, kv.v):
+        t.copy_((torch.randn(t.shape, generator=gen, device="cuda") * (1 if kv.k_scale is None else 60)).clamp(-127, 127).to(fmt))
+    if kv.k_scale is not None:
+        kv.k_scale.fill_(0.02)
+        kv.v_scale.fill_(0.02)
+    table = torch.randperm(seqs * per, generator=g).to(torch.int32).view(seqs, per).cuda()
+    lens = torch.full((seqs,), n, dtype=torch.int32).cuda()
+    Q = torch.randn((seqs * nq, 32, 128), generator=g).to(BF).cuda()
+    outs = [api.page_attention(Q, kv, table, lens, max_kv=n) for _ in range(60)]
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    assert bool(outs[0].float().abs().sum(-1).gt(0).all()) and bool(torch.isfinite(outs[0].float()).all())
+
+
 def test_offsets_past_32_bits():
     # a pool of 2^31 + bytes per array: rows at its end, in 16 bits
     heads, page = 8, 128

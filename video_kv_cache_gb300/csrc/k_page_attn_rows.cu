@@ -120,9 +120,11 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
 }
 // The warps that compute meet.
 __device__ __forceinline__ void rows_meet() {
+    __syncwarp();
     asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kRowsWarps) : "memory");
 }
 __device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

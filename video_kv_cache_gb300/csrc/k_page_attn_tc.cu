@@ -3,7 +3,7 @@
 //   O = softmax(scale Q K^T, over the visible keys) V
 //
 // Bound by the tensor cores: 4 * 128 operations per visible (query row, key) pair.  4680 queries
-// of 12 heads over 32760 keys, every one seen: 597 us back to back (1577 TFLOP/s), 640 us with
+// of 12 heads over 32760 keys, every one seen: 592 us back to back (1590 TFLOP/s), 640 us with
 // cold caches; 4096 over 32768 of 32 heads, causal: 1268 us (1625).  The tensor cores work 87 %
 // of the cycles of the loop over the keys at the clocks that this load leaves (1.5 to 1.6 GHz);
 // the rest is the start of a CTA (about 8000 cycles: TMEM, Q, the first tile) and the join of
@@ -107,6 +107,16 @@ constexpr size_t tc_smem() {
     return bytes;
 }
 
+// One arrival where it holds; the lanes stay together, as the tensor-memory instructions around
+// it need them.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool holds) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}\n" ::"r"(bar),
+        "r"((uint32_t)holds)
+        : "memory");
+}
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -514,6 +524,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                 ok = ok && wait(sh.sc_empty[buf], (j >> 1) + 1);
                 if (lane == 0) wmax[warp & 3] = m;
+                __syncwarp();  // (lanes may come from a wait one by one; a barrier wants the whole warp)
                 ok = meet<128>(id, ok);
                 if (!ok) break;  // the four warps leave together
                 m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
@@ -539,7 +550,9 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
                 if (j + 1 < n) load_scale(k0 + kTcN + x);
-                ok = meet<128>(id, wait(sh.raw_full[2 * it % T::RAWS], 2 * it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1));
+                ok = wait(sh.raw_full[2 * it % T::RAWS], 2 * it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1);
+                __syncwarp();
+                ok = meet<128>(id, ok);
                 if (!ok) break;  // (otherwise all scales are there, and wmax is free again)
                 const bool whole = k0 >= lo && k0 + kTcN <= hi;
                 const uint2 *factors = (value ? sh.vf[buf] : sh.kf[buf]) + rb;
@@ -761,15 +774,16 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t][hc >> 5]));
+                    mbar_arrive_if(smem_u32(&sh.p_full[t][hc >> 5]), lane == 0);
                 }
                 const float2 ls = __fadd2_rn(la, lb);
                 l += ls.x + ls.y;
                 if constexpr (!WIDE) {
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.sc_empty[buf]));
+                    mbar_arrive_if(smem_u32(&sh.sc_empty[buf]), lane == 0);
                 }
             }
             if (n > 0) ok = ok && wait(sh.o_done[t], n - 1);
+            __syncwarp();
             // the row's weight sum
             float *xl = sh.xmax[t][0];
             meet<64>(id, true);
@@ -870,6 +884,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         }
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) or_status(p.status, QVG_DEV_TIMEOUT);
