@@ -41,10 +41,10 @@
 // of each key and value, an eighth of what the output's own rounding is. Otherwise the scales
 // multiply the scores and the weights in the softmax (the weights, in fp16, relative to the same
 // power of two), which costs time: every thread then reads the scales of all keys from shared
-// memory. The case above takes 901 us in e4m3 and 969 in int8, without folding 1087 and 1117.
+// memory. The case above takes 893 us in e4m3 and 1020 in int8, without folding 1086 and 1107.
 // What costs is instructions: 10300 of a warp a tile pair against 5500 in 16 bits, which share
 // the issue slots with the exponentials; with one factor instead of two (a scale rounded to
-// fp16, an error that all channels of a key share) they would take 881 and 936.
+// fp16, an error that all channels of a key share) the first two took 20 and 34 us less.
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
@@ -84,7 +84,9 @@ template <int FMT>
 struct TcShared {
     static constexpr bool WIDE = TcShape<FMT>::WIDE;
     uint64_t full[5], empty[5];         // ring of 16-bit tiles
-    uint64_t raw_full[3], raw_empty[3];
+    // raw tiles: keys and values share the places, but each has a barrier of its own for them.  A
+    // phase is told by its parity, so whoever waits on a barrier has to wait for every phase of it.
+    uint64_t raw_full[2][3], raw_empty[3];
     uint64_t s_full[2], p_full[2][2], o_done[2];
     uint64_t sc_full[2], sc_empty[2];   // scales of a key tile
     uint64_t q_full, edge, fin;
@@ -310,7 +312,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         for (int s = 0; s < T::RAWS; s++) {
-            mbar_init(smem_u32(&sh.raw_full[s]), 1);
+            mbar_init(smem_u32(&sh.raw_full[0][s]), 1);
+            mbar_init(smem_u32(&sh.raw_full[1][s]), 1);
             mbar_init(smem_u32(&sh.raw_empty[s]), 4);
         }
         for (int t = 0; t < 2; t++) {
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             // have 64
             const int shift = WIDE ? page_shift : min(page_shift, 6), per_tile = kTcN >> shift;
             bool bad = false, ok = true;
-            uint32_t edges = 0, issued = 0;
+            uint32_t edges = 0, issued = 0, used = 0, odd = 0;  // raw tiles: barriers in use, and those used an odd number of times
             constexpr int RING = WIDE ? SLOTS : T::RAWS;
             constexpr uint32_t PER_KEYS = WIDE ? 2 : 4;  // ring items of a key tile: K and V, or their halves
             // the pages of a tile that hold a key some row sees, a lane each; looked up one
@@ -445,7 +448,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     row = row_next;
                     if (it + PER_KEYS < PER_KEYS * n) row_next = row_of(k0 + kTcN);
                 }
-                uint64_t &full = WIDE ? sh.full[slot] : sh.raw_full[slot];
+                uint64_t &full = WIDE ? sh.full[slot] : sh.raw_full[value][slot];
                 ok = wait(WIDE ? sh.empty[slot] : sh.raw_empty[slot], it / RING + 1);
                 ok = !__any_sync(0xffffffffu, !ok);
                 if (!ok) break;
@@ -467,6 +470,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     }
                 }
                 issued = it + 1;
+                used |= 1u << (3 * value + slot % 3);
+                odd ^= 1u << (3 * value + slot % 3);
                 if (edge) {
                     // rows of the outer 16-key steps that no row of the CTA sees: zeros
                     mbar_wait_final(bar, edges++ & 1u);
@@ -486,9 +491,13 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
             // every copy this CTA started lands before the CTA ends (edge tiles were waited for;
             // their slots' phases were completed by hand)
-            const uint32_t from = issued > (uint32_t)RING ? issued - RING : 0u;
-            for (uint32_t it = from; it < issued; it++)
-                mbar_wait_final(smem_u32(WIDE ? &sh.full[it % RING] : &sh.raw_full[it % RING]), (it / RING) & 1u);
+            if constexpr (WIDE) {
+                const uint32_t from = issued > (uint32_t)RING ? issued - RING : 0u;
+                for (uint32_t it = from; it < issued; it++) mbar_wait_final(smem_u32(&sh.full[it % RING]), (it / RING) & 1u);
+            } else {
+                for (int k = 0; k < 6; k++)
+                    if (used >> k & 1u) mbar_wait_final(smem_u32(&sh.raw_full[k / 3][k % 3]), ~(odd >> k) & 1u);
+            }
         } else if (!WIDE && warp >= WIDEN_WARP) {
             // ---------------------------------------------------------------- 8-bit codes widened
             const bool value = warp >= WIDEN_WARP + 4;  // the first four warps: keys, the others: values
@@ -513,6 +522,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             const unsigned char *src0 = sRaw + rb * kD + ((c ^ r8) << 4);
             unsigned char *dst0 = sKV + (c >> 2) * kHalf + rb * 128;
             const int d0 = ((2 * (c & 3)) ^ r8) << 4, d1 = ((2 * (c & 3) + 1) ^ r8) << 4;
+            uint32_t phases = 0;  // of this operand's barriers of the raw tiles, a bit each
             for (int j = 0; j < n; j++) {
                 const int it = 2 * j + value, k0 = (j0 + j) * kTcN, slot = it % SLOTS, buf = j & 1;
                 // a value scale that is not finite: 0 here, and a bit that makes the rows NaN that
@@ -550,7 +560,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
                 if (j + 1 < n) load_scale(k0 + kTcN + x);
-                ok = wait(sh.raw_full[2 * it % T::RAWS], 2 * it / T::RAWS) && wait(sh.empty[slot], it / SLOTS + 1);
+                int raw = 2 * it % T::RAWS;
+                ok = wait(sh.raw_full[value][raw], phases >> raw) && wait(sh.empty[slot], it / SLOTS + 1);
                 __syncwarp();
                 ok = meet<128>(id, ok);
                 if (!ok) break;  // (otherwise all scales are there, and wmax is free again)
@@ -559,9 +570,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 unsigned char *dst = dst0 + slot * kSlot;
 #pragma unroll
                 for (int part = 0; part < 2; part++) {
-                    const int raw = (2 * it + part) % T::RAWS;
-                    // (a warp that gives up here meets the others at the next tile)
-                    if (part) ok = wait(sh.raw_full[raw], (2 * it + 1) / T::RAWS);
+                    if (part) {
+                        raw = raw == T::RAWS - 1 ? 0 : raw + 1;
+                        ok = wait(sh.raw_full[value][raw], phases >> raw);  // (who gives up here meets the others at the next tile)
+                    }
+                    phases ^= 1u << raw;
                     const unsigned char *src = src0 + raw * kRaw;
 #pragma unroll
                     for (int v = 0; v < 4; v++) {
