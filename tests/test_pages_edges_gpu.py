@@ -1,0 +1,45 @@
+"""GPU checks of attention over pages where a query sees nothing, or where what it does not see is
+far from what it sees, against 64 bits."""
+import math
+
+import pytest
+import torch
+
+from tests import test_pages_gpu as tp
+from video_kv_cache_gb300 import api
+from video_kv_cache_gb300 import build as qbuild
+from video_kv_cache_gb300 import qvg
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32, E4, I8 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn, torch.int8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    qbuild.build()
+    qvg.load()
+    torch.cuda.set_device(0)
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+@pytest.mark.parametrize("fmt", [BF, HF, E4])
+@pytest.mark.parametrize("nq,n,heads,causal", [(4680, 0, 12, False), (513, 100, 40, True), (700, 0, 3, True)])
+def test_queries_that_see_no_key(fmt, nq, n, heads, causal):
+    # a chunk before anything is cached, and more causal queries than cached tokens: whole tiles
+    # of rows that see nothing are zeros, log-sum-exp -infinity, in every call
+    g = _gen(nq)
+    dtype = BF if fmt is E4 else fmt
+    kv, table = tp._cache(g, [n], heads, fmt, 64)
+    lens, table = torch.tensor([n], dtype=torch.int32).cuda(), table.cuda()
+    Q = torch.randn((nq, heads, 128), generator=g).to(dtype).cuda()
+    blind = nq - n if causal else nq
+    first = None
+    for _ in range(40):
+        out, lse = api.page_attention(Q, kv, table, lens, causal=causal, return_lse=True)
+        assert not out[:blind].any() and bool((lse[:blind] == -math.inf).all())
+        assert bool(lse[blind:].isfinite().all())
+        first = out if first is None else first
+        assert torch.equal(out, first)

@@ -636,7 +636,9 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
-            if constexpr (!WIDE) meet<512>(11, true);  // the rows' powers of two are read across warps
+            // 8 bits: the rows' powers of two are read across warps.  No key in sight: the output's
+            // rows go where Q lies, and no product's end says that every warp is through with it.
+            if (!WIDE || n == 0) meet<512>(11, true);
         }
         const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
         const int row = quarter * 32 + lane, r = r0 + t * kTcM + row;
