@@ -43,3 +43,23 @@ def test_queries_that_see_no_key(fmt, nq, n, heads, causal):
         assert bool(lse[blind:].isfinite().all())
         first = out if first is None else first
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("nq,n,window", [(600, 600, 0), (777, 2000, 300)])
+def test_masked_rows_keep_their_weight_sums(nq, n, window):
+    # whole items of 16-bit pages under a mask: the rows' sums and the search for rows to do again
+    # are exchanged by pairs of warps that run apart; every call gives the same, and values of one
+    # give outputs of one, whatever the weights: a sum of n weights of at most 1 in fp32 and their
+    # bf16 roundings (2^-8), then the output's (2^-8)
+    g = _gen(nq + window)
+    heads = 8
+    kv, table = tp._cache(g, [n], heads, BF, 64)
+    lens, table = torch.tensor([n], dtype=torch.int32).cuda(), table.cuda()
+    Q = torch.randn((nq, heads, 128), generator=g).to(BF).cuda()
+    want = api.page_attention(Q, kv, table, lens, window=window)
+    for _ in range(100):
+        assert torch.equal(api.page_attention(Q, kv, table, lens, window=window), want)
+    kv.v.copy_(torch.where(kv.v.isnan(), kv.v, torch.ones_like(kv.v)))
+    for _ in range(100):
+        out = api.page_attention(Q, kv, table, lens, window=window)
+        assert float((out.float() - 1).abs().max()) <= 2.0 ** -7 + n * 2.0 ** -23

@@ -96,6 +96,7 @@ struct TcShared {
     __align__(16) uint32_t vnan[2][4];                // keys whose value scale is not finite, a bit each
     float wmax[2][4];                   // largest scales of the widening warps: keys', values'
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
+    uint32_t odd[2][4][2];              // rows that did not come out finite, a bit each: row tile, quarter, half
     __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
     __align__(16) float vs[2][WIDE ? 4 : kTcN];  // values' scales over their reference
     uint2 kf[2][WIDE ? 1 : kTcN], vf[2][WIDE ? 1 : kTcN];  // scales over their references, see scale_pair
@@ -873,13 +874,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     if (redo_possible(p)) {
                         // both halves written, then the first half's warp takes its share of
                         // the rows that either found odd
-                        uint32_t *xo = reinterpret_cast<uint32_t *>(xl + half * kTcM) + quarter;
                         const uint32_t mine = __ballot_sync(0xffffffffu, odd && live);
-                        meet<64>(id, true);
-                        if (lane == 0) *xo = mine;
+                        if (lane == 0) sh.odd[t][quarter][half] = mine;
                         __threadfence_block();
                         meet<64>(id, true);
-                        uint32_t todo = mine | *(reinterpret_cast<uint32_t *>(xl + (half ^ 1) * kTcM) + quarter);
+                        uint32_t todo = mine | sh.odd[t][quarter][half ^ 1];
                         todo &= half ? 0xAAAAAAAAu : 0x55555555u;
                         while (todo) {
                             const int src = __ffs(todo) - 1;
