@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+from tests import pages_model as pm
 from tests import test_pages_gpu as tp
 from video_kv_cache_gb300 import api
 from video_kv_cache_gb300 import build as qbuild
@@ -63,3 +64,39 @@ def test_masked_rows_keep_their_weight_sums(nq, n, window):
     for _ in range(100):
         out = api.page_attention(Q, kv, table, lens, window=window)
         assert float((out.float() - 1).abs().max()) <= 2.0 ** -7 + n * 2.0 ** -23
+
+
+def _seen(n, nq, window):
+    """Keys [a, z) that each causal query sees."""
+    pos = [n - nq + i for i in range(nq)]
+    return [(max(0, p + 1 - window) if window else 0, max(0, p + 1)) for p in pos]
+
+
+def _check_lse(Q, kv, table, n, window, lse):
+    """Every row's log-sum-exp against 64 bits over the keys that it sees and no others."""
+    K = pm.pool_rows(kv.k, kv.k_scale, table[0].cpu(), n, kv.page_tokens)[0]
+    for i, (a, z) in enumerate(_seen(n, Q.shape[0], window)):
+        for hq in range(Q.shape[1]):
+            _, want, _, bound = pm.attend(Q[i:i + 1, hq].double().cpu(), K[a:z], K[a:z], 128 ** -0.5, False, 0, 2.0 ** -11, F32)
+            tp._within(lse[i:i + 1, hq], want, bound, "lse %d head %d" % (i, hq))
+
+
+SPANS = [  # queries, cached tokens, query heads, window, a key that only some queries see
+    (5, 300, 2, 0, 297), (16, 2000, 1, 0, 1990), (7, 900, 2, 300, 596), (140, 300, 1, 0, 297),
+    (140, 300, 1, 0, 200), (140, 2600, 1, 0, 2597), (140, 1200, 1, 500, 566), (300, 300, 1, 0, 131),
+]
+
+
+@pytest.mark.parametrize("fmt", [E4, I8])
+@pytest.mark.parametrize("nq,n,group,window,j", SPANS)
+def test_a_value_that_is_not_finite_leaves_the_log_sum_exp(fmt, nq, n, group, window, j):
+    # the log-sum-exp is of the scores alone, whole or split, few rows or many
+    g = _gen(nq + n)
+    kv, table = tp._cache(g, [n], 1, fmt, 32)
+    Q = torch.randn((nq, group, 128), generator=g).to(BF)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    kv.v_scale[int(table[0, j // 32]), 0, j % 32] = math.nan
+    out, lse = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32, return_lse=True)
+    for i, (a, z) in enumerate(_seen(n, nq, window)):
+        assert bool(out[i].isnan().all()) if a <= j < z else bool(out[i].isfinite().all())
+    _check_lse(Q, kv, table, n, window, lse)

@@ -97,6 +97,7 @@ struct TcShared {
     float wmax[2][4];                   // largest scales of the widening warps: keys', values'
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
     uint32_t odd[2][4][2];              // rows that did not come out finite, a bit each: row tile, quarter, half
+    uint32_t bad[2][4];                 // rows that see a value whose scale is not finite: their output is NaN, their weight sum is not
     __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
     __align__(16) float vs[2][WIDE ? 4 : kTcN];  // values' scales over their reference
     uint2 kf[2][WIDE ? 1 : kTcN], vf[2][WIDE ? 1 : kTcN];  // scales over their references, see scale_pair
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             mbar_init(smem_u32(&sh.o_done[t]), 1);
             mbar_init(smem_u32(&sh.sc_full[t]), 8);
             mbar_init(smem_u32(&sh.sc_empty[t]), 8 * nt);
+            for (int x = 0; x < 4; x++) sh.bad[t][x] = 0u;
         }
         mbar_init(smem_u32(&sh.q_full), 16);
         mbar_init(smem_u32(&sh.edge), 1);
@@ -526,8 +528,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             uint32_t phases = 0;  // of this operand's barriers of the raw tiles, a bit each
             for (int j = 0; j < n; j++) {
                 const int it = 2 * j + value, k0 = (j0 + j) * kTcN, slot = it % SLOTS, buf = j & 1;
-                // a value scale that is not finite: 0 here, and a bit that makes the rows NaN that
-                // see the key (and no others)
+                // a value scale that is not finite: 0 here, and a bit that makes the outputs of the
+                // rows NaN that see the key (and no others)
                 const uint32_t odd = __ballot_sync(0xffffffffu, !is_finite(sc));
                 float m = is_finite(sc) ? fabsf(sc) : 0.f;
                 if (value) sc = is_finite(sc) ? sc : 0.f;
@@ -723,7 +725,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                             const int k0 = (j0 + j) * kTcN + half * 64, i = token_of(p, min(r, rows - 1));
                             const uint64_t bits = half ? odd.z | (uint64_t)odd.w << 32 : odd.x | (uint64_t)odd.y << 32;
                             for (int c = 0; c < 64; c++)
-                                if (bits >> c & 1 && k0 + c >= seen_lo(p, sq, i) && k0 + c < seen_hi(p, sq, i)) l = NAN;
+                                if (bits >> c & 1 && k0 + c >= seen_lo(p, sq, i) && k0 + c < seen_hi(p, sq, i)) atomicOr(&sh.bad[t][quarter], 1u << lane);
                         }
                     }
                 }
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const bool live = r < rows, whole = S == 1;
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-                if constexpr (!WIDE) inv = ldexpf(inv, e - kValueShift);
+                if constexpr (!WIDE) inv = sh.bad[t][quarter] >> lane & 1u ? NAN : ldexpf(inv, e - kValueShift);
                 const int64_t tok = sq.q0 + i;
                 const int64_t part = (tail * S + split) * p.unit + t * kTcM + row;
                 // The rows go out through shared memory, in the place of this tile's Q, which
