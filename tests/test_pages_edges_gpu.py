@@ -100,3 +100,50 @@ def test_a_value_that_is_not_finite_leaves_the_log_sum_exp(fmt, nq, n, group, wi
     for i, (a, z) in enumerate(_seen(n, nq, window)):
         assert bool(out[i].isnan().all()) if a <= j < z else bool(out[i].isfinite().all())
     _check_lse(Q, kv, table, n, window, lse)
+
+
+def _check_rows(Q, kv, table, n, window, rows, out, lse=None, u_kv=0.0):
+    """Rows against 64 bits over the keys that each sees and no others, so that a bound knows no
+    other keys' sizes either."""
+    group = Q.shape[1] // kv.heads
+    u_p = pm.HALF_EPS[HF if kv.k.dtype in pm.TOP else Q.dtype]
+    seen = _seen(n, Q.shape[0], window)
+    for h in range(kv.heads):
+        K = pm.pool_rows(kv.k, kv.k_scale, table[0].cpu(), n, kv.page_tokens)[h]
+        V = pm.pool_rows(kv.v, kv.v_scale, table[0].cpu(), n, kv.page_tokens)[h]
+        for i in rows:
+            a, z = seen[i]
+            for hq in range(h * group, (h + 1) * group):
+                want, want_lse, bound, lse_bound = pm.attend(Q[i:i + 1, hq].double().cpu(), K[a:z], V[a:z], 128 ** -0.5,
+                                                             False, 0, u_p, out.dtype, u_kv, u_kv)
+                tp._within(out[i:i + 1, hq], want, bound, "row %d head %d" % (i, hq))
+                if lse is not None:
+                    tp._within(lse[i:i + 1, hq], want_lse, lse_bound, "lse %d head %d" % (i, hq))
+
+
+FEW = [s for s in SPANS if s[0] * s[2] <= 16]  # query rows that the warp-level kernel takes
+
+
+@pytest.mark.parametrize("fmt", [E4, I8])
+@pytest.mark.parametrize("nq,n,group,window,j", FEW)
+@pytest.mark.parametrize("which,size", [("v", math.inf), ("v", 2.0 ** 40), ("v", 2.0 ** 20), ("v", math.nan),
+                                        ("k", 2.0 ** 40), ("k", math.nan)])
+def test_scales_of_keys_that_some_queries_do_not_see(fmt, nq, n, group, window, j, which, size):
+    # a key far larger than all that the other queries see
+    g = _gen(nq + n)
+    kv, table = tp._cache(g, [n], 1, fmt, 32)
+    Q = torch.randn((nq, group, 128), generator=g).to(BF)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    getattr(kv, which + "_scale")[int(table[0, j // 32]), 0, j % 32] = size
+    out, lse = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32, return_lse=True)
+    alone = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window)
+    sees = [i for i, (a, z) in enumerate(_seen(n, nq, window)) if a <= j < z]
+    blind = [i for i in range(nq) if i not in sees]
+    assert blind and sees
+    rows = range(nq) if math.isfinite(size) else blind
+    _check_rows(Q, kv, table, n, window, rows, out, lse)
+    _check_rows(Q, kv, table, n, window, rows, alone, u_kv=0.0 if nq * group <= 16 else 2.0 ** -11)
+    if not math.isfinite(size):
+        assert not bool(out[sees].isfinite().any()) and not bool(alone[sees].isfinite().any())
+        if which == "k":
+            assert bool(lse[sees].isnan().all())

@@ -321,15 +321,19 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             const int b = SHARES ? item.b : blockIdx.z, h = SHARES ? item.h : blockIdx.y, first = item.first, n = item.n;
             const SeqInfo sq = item.sq;
             const int rows = sq.qn * p.G, lo = seen_lo(p, sq, 0), hi = seen_hi(p, sq, sq.qn - 1);
+            const int all_lo = seen_lo(p, sq, sq.qn - 1), all_hi = seen_hi(p, sq, 0);  // what every row sees
             float o[RT][8][4], m[RT][2], l[RT][2];
+            // exponents of the references that the values' scales are taken against: a row's own, so
+            // that no key which it does not see has a part in it
+            int vexp[RT][2];
 #pragma unroll
             for (int y = 0; y < RT; y++) {
                 m[y][0] = m[y][1] = -INFINITY;
                 l[y][0] = l[y][1] = 0.f;
+                vexp[y][0] = vexp[y][1] = -100;
 #pragma unroll
                 for (int t = 0; t < 8; t++) o[y][t][0] = o[y][t][1] = o[y][t][2] = o[y][t][3] = 0.f;
             }
-            int vexp = -100;  // exponent of the reference that the values' scales are taken against
             // Q in the order the keys' chunks come in: lane (g, q) holds row g of each group
             uint32_t qb[RT][8][2];
             float qmul[RT][2];  // 8-bit pages: powers of two taken out of the rows whose scores this lane has
@@ -445,28 +449,44 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                         }
                     }
                     // 8-bit: the weights take in the values' scales relative to 2^vexp, an exponent
-                    // that follows the largest scale seen; times 2^8 they fill fp16's range
-                    float vcorr = 1.f;
+                    // that follows the largest finite scale the row has seen; times 2^8 they fill
+                    // fp16's range
+                    float vcorr[RT][2], vmul[RT][2];
                     if constexpr (!WIDE) {
-                        float big = 0.f;
+                        float big[RT][2] = {};
+                        auto take = [&](float &to, float scale) { to = fmaxf(to, is_finite(scale) ? fabsf(scale) : 0.f); };
+                        if (t0 >= all_lo && t0 + 16 * KT <= all_hi) {
 #pragma unroll
-                        for (int z = 0; z < KT; z++)
+                            for (int z = 0; z < KT; z++)
 #pragma unroll
-                            for (int e = 0; e < 2; e++) {
-                                const int key = t0 + 16 * z + 8 * e + g;
-                                if (!edge || (key >= lo && key < hi)) big = fmaxf(big, fabsf(vsc[z][e]));
-                            }
+                                for (int e = 0; e < 2; e++) take(big[0][0], vsc[z][e]);
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-                        const int ve = max(vexp, min((int)(__float_as_uint(big) >> 23) - 127, 121));
-                        vcorr = __uint_as_float((uint32_t)max(127 + vexp - ve, 0) << 23);
-                        const float vmul = __uint_as_float((uint32_t)(127 + 8 - ve) << 23);
+                            for (int x = 4; x < 32; x <<= 1) big[0][0] = fmaxf(big[0][0], __shfl_xor_sync(0xffffffffu, big[0][0], x));
 #pragma unroll
-                        for (int z = 0; z < KT; z++) {
-                            vsc[z][0] *= vmul;
-                            vsc[z][1] *= vmul;
+                            for (int y = 0; y < RT; y++) big[y][0] = big[y][1] = big[0][0];
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < RT; y++)
+#pragma unroll
+                                for (int x = 0; x < 2; x++) {
+#pragma unroll
+                                    for (int z = 0; z < KT; z++)
+#pragma unroll
+                                        for (int e = 0; e < 2; e++)
+                                            if (s[z][y][2 * e + x] != -INFINITY) take(big[y][x], vsc[z][e]);
+#pragma unroll
+                                    for (int d = 4; d < 32; d <<= 1) big[y][x] = fmaxf(big[y][x], __shfl_xor_sync(0xffffffffu, big[y][x], d));
+                                }
                         }
-                        vexp = ve;
+#pragma unroll
+                        for (int y = 0; y < RT; y++)
+#pragma unroll
+                            for (int x = 0; x < 2; x++) {
+                                const int ve = max(vexp[y][x], min((int)(__float_as_uint(big[y][x]) >> 23) - 127, 121));
+                                vcorr[y][x] = __uint_as_float((uint32_t)max(127 + vexp[y][x] - ve, 0) << 23);
+                                vmul[y][x] = __uint_as_float((uint32_t)(127 + 8 - ve) << 23);
+                                vexp[y][x] = ve;
+                            }
                     }
                     uint32_t pb[KT][RT][2];
 #pragma unroll
@@ -491,8 +511,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                                 sum[0] += w0;
                                 sum[1] += w1;
                                 if constexpr (!WIDE) {
-                                    w0 *= vsc[z][e];
-                                    w1 *= vsc[z][e];
+                                    w0 *= vsc[z][e] * vmul[y][0];
+                                    w1 *= vsc[z][e] * vmul[y][1];
                                     if (edge || sq.qn > 1) {  // a hidden key's scale may be NaN: its weight stays 0
                                         if (s[z][y][2 * e] == -INFINITY) w0 = 0.f;
                                         if (s[z][y][2 * e + 1] == -INFINITY) w1 = 0.f;
@@ -503,7 +523,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
 #pragma unroll
                         for (int x = 0; x < 2; x++) {
                             l[y][x] = l[y][x] * corr[x] + sum[x];
-                            corr[x] *= vcorr;
+                            if constexpr (!WIDE) corr[x] *= vcorr[y][x];
                         }
                         if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
@@ -573,7 +593,6 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             // join the warps relative to the largest of their maxima: through the ring, which is
             // through with its keys, or, where the next item's are on their way, one after another in
             // a place of its own
-            const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp - 8) << 23);
             if constexpr (!SHARES) rows_meet();
 #pragma unroll
             for (int y = 0; y < RT; y++)
@@ -594,6 +613,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
                         const int r = 8 * y + 2 * q + x;
+                        const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp[y][x] - 8) << 23);
                         float f = 1.f;
                         if (relative) {
                             const float top = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
