@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                 cluster_meet();  // nobody leaves while its rows are read
             }
             if (!mine) return;
-        if (redo_possible(p)) {
+        if (wide_pages(p) && redo_possible(p)) {
             bool odd = false;
 #pragma unroll
             for (int c = 0; c < 16; c++) odd |= !is_finite(v[c]);
@@ -782,6 +782,7 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
     for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
     const float base = exp_base(mx);
     float l = 0.f, o[4] = {};
+    bool again = false;
     constexpr int SB = 8;
     for (int s0 = 0; s0 < S; s0 += SB) {
         float2 ml[SB];
@@ -797,6 +798,7 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
         for (int k = 0; k < SB; k++)
             if (s0 + k < S) {
                 const float f = fast_exp2(ml[k].x - base);
+                again |= ml[k].y == kRedo;
                 l += f * ml[k].y;
                 o[0] += f * po[k].x;
                 o[1] += f * po[k].y;
@@ -804,8 +806,9 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
                 o[3] += f * po[k].w;
             }
     }
-    if (redo_possible(p) &&
-        __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3])))
+    if (wide_pages(p) && redo_possible(p))
+        again = __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3]));
+    if (again)
         redo_row(p, b, i, hq, o, mx, l);
     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll

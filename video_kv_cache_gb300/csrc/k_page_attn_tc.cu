@@ -61,6 +61,13 @@ constexpr uint32_t kSlot = 2 * kHalf;      // a whole 16-bit tile: 32 KB
 constexpr int kRawKeys = 64;               // keys of a raw tile of 8-bit codes, half a key tile
 constexpr uint32_t kRaw = kRawKeys * kD;   // 8 KB
 constexpr int kValueShift = 4, kKeyShift = 6;  // 8-bit values and keys over their references, times 2^this
+// How far (log2) a scale that a row does not see may lie above the largest that it sees before the
+// row is done again.  Values: a weight times a scale over the reference 2^e is rounded by at most
+// 2^-25 times 2^(e - kValueShift) and a code, 2^-25 of the largest value that the row sees if 2^e is
+// at most kValueShift above it (folded values, rounded alone, by 2^-7 of that).  Keys: channels by
+// 2^-25 times 2^(e - kKeyShift), which is 2^-30 of the row's largest key, 127 codes of its scale at
+// least, if 2^e is at most kKeyShift + 2 above.
+constexpr int kValueFar = kValueShift, kKeyFar = kKeyShift + 2;
 constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
 
 template <int FMT>
@@ -95,6 +102,8 @@ struct TcShared {
     int vexp[2], kexp[2];               // exponents of the values' and keys' references, per tile parity
     __align__(16) uint32_t vnan[2][4];                // keys whose value scale is not finite, a bit each
     float wmax[2][4];                   // largest scales of the widening warps: keys', values'
+    uint64_t sizes;
+    uint32_t some[2], all[2];           // bits of the largest scale of keys, values that some rows see only, and of others
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
     uint32_t odd[2][4][2];              // rows that did not come out finite, a bit each: row tile, quarter, half
     uint32_t bad[2][4];                 // rows that see a value whose scale is not finite: their output is NaN, their weight sum is not
@@ -330,6 +339,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         mbar_init(smem_u32(&sh.q_full), 16);
         mbar_init(smem_u32(&sh.edge), 1);
         mbar_init(smem_u32(&sh.fin), 1);
+        mbar_init(smem_u32(&sh.sizes), 8);
+        sh.some[0] = sh.some[1] = sh.all[0] = sh.all[1] = 0u;
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -606,6 +617,30 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&sh.full[slot]));
             }
             if (bad) or_status(p.status, QVG_DEV_BAD_INDEX);
+            // The references are of what any row sees.  Should one lie too far above what a row sees
+            // itself, the row is done again; for that, how large the scales are that only some rows
+            // see (the softmax is still busy with the last tile), and 256 that all of them see.
+            if (n > 0 && redo_possible(p)) {
+                const KeySpans sp = key_spans(p, sq, r0, min(rows, r0 + 2 * kTcM), max(lo, j0 * kTcN), min(hi, (j0 + n) * kTcN));
+                auto largest_of = [&](int from, int to, uint32_t *most) {
+                    float m = 0.f;
+#pragma unroll 1
+                    for (int key = from + x; key < to; key += 128) {
+                        const float s = __ldg(scales + ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1)));
+                        m = fmaxf(m, is_finite(s) ? fabsf(s) : 0.f);
+                    }
+                    __syncwarp();
+                    const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+                    if (lane == 0 && w) atomicMax(most, w);
+                };
+                if ((value || FOLD) && (sp.a0 < sp.a1 || sp.z0 < sp.z1)) {
+                    largest_of(sp.a0, sp.a1, &sh.some[value]);
+                    largest_of(sp.z0, sp.z1, &sh.some[value]);
+                    largest_of(max(sp.a1, sp.z0 - 256), sp.z0, &sh.all[value]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.sizes));
+            }
         }
     } else {
         // -------------------------------------------------------------------- softmax
@@ -800,7 +835,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     mbar_arrive_if(smem_u32(&sh.sc_empty[buf]), lane == 0);
                 }
             }
-            if (n > 0) ok = ok && wait(sh.o_done[t], n - 1);
+            if (n > 0) ok = ok && wait(sh.o_done[t], n - 1) && (WIDE || !redo_possible(p) || wait(sh.sizes, 0));
             __syncwarp();
             // the row's weight sum
             float *xl = sh.xmax[t][0];
@@ -812,6 +847,15 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             if (ok) {
                 const int i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - i * p.G;
                 const bool live = r < rows, whole = S == 1;
+                bool odd = false;
+                if constexpr (!WIDE) {
+                    const uint32_t v_some = sh.some[1], v_all = sh.all[1], k_some = sh.some[0], k_all = sh.all[0];
+                    if (too_far(v_some, __uint_as_float(v_all), kValueFar) || too_far(k_some, __uint_as_float(k_all), kKeyFar)) {
+                        const KeySpans sp = key_spans(p, sq, r0, min(rows, r0 + 2 * kTcM), max(lo, j0 * kTcN), min(hi, (j0 + n) * kTcN));
+                        odd = sees_too_little(p, p.vs, b, h, sp, i, v_some, v_all, kValueFar);
+                        odd |= sees_too_little(p, p.ks, b, h, sp, i, k_some, k_all, kKeyFar);
+                    }
+                }
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
                 if constexpr (!WIDE) inv = sh.bad[t][quarter] >> lane & 1u ? NAN : ldexpf(inv, e - kValueShift);
@@ -826,7 +870,6 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const int64_t elem = narrow ? 2 : 4, at = (whole ? tok * p.ot + hq * p.oh : part * kD) * elem;
                 unsigned char *dst = static_cast<unsigned char *>(whole ? p.O : p.part);
                 unsigned char *stage = sQ + t * kSlot + half * 128;  // + row * 256
-                bool odd = false;
                 auto leave = [&](int c, uint4 v) { *reinterpret_cast<uint4 *>(stage + row * 256 + ((c ^ (row & 7)) << 4)) = v; };
                 auto write_out = [&](int first_channel) {
                     __syncwarp();
@@ -852,7 +895,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
                         o[k] *= inv;
-                        odd |= !is_finite(o[k]);
+                        if constexpr (WIDE) odd |= !is_finite(o[k]);
                     }
                     if (narrow) {
                         auto pk = [&](int k) {
@@ -870,12 +913,12 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 }
                 if (narrow) write_out(half * 64);
                 if (!whole) {
-                    if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, l);
+                    if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, !WIDE && odd ? kRedo : l);
                 } else {
                     if (live && half == 0 && p.lse) p.lse[tok * p.HQ + hq] = row_lse(m, l);
                     if (redo_possible(p)) {
-                        // both halves written, then the first half's warp takes its share of
-                        // the rows that either found odd
+                        // both halves written, then each of the two warps takes its share of the
+                        // rows that either found odd
                         const uint32_t mine = __ballot_sync(0xffffffffu, odd && live);
                         if (lane == 0) sh.odd[t][quarter][half] = mine;
                         __threadfence_block();

@@ -75,13 +75,76 @@ __device__ __forceinline__ bool is_finite(float x) {
     return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
 
-// A 16-bit value that is NaN or infinite, multiplied by the zero weight of a query that does
-// not see its key, makes that query's row NaN.  So a row that did not come out finite, where
-// a mask hides keys from some rows of a tile, is computed once more by one warp, over the
-// keys that it sees and no others.  (8-bit codes are finite, and a hidden key's scale is
-// never multiplied in: they need none of this.)
-__device__ __forceinline__ bool redo_possible(const PAttnPlan &p) {
-    return (p.causal || p.window > 0) && (p.fmt == PF_F16 || p.fmt == PF_BF16);
+// Where a mask hides keys from some rows of a tile, a row may have to be computed once more by one
+// warp, over the keys that it sees and no others:
+//   * 16-bit pages: a value that is NaN or infinite, multiplied by the zero weight of a query that
+//     does not see its key, makes that query's row NaN.  Rows that did not come out finite.
+//   * 8-bit pages, many rows: a scale that the row does not see, far above all that it sees, has
+//     taken its values' or keys' bits (k_page_attn_tc.cu).
+__device__ __forceinline__ bool redo_possible(const PAttnPlan &p) { return p.causal || p.window > 0; }
+__device__ __forceinline__ bool wide_pages(const PAttnPlan &p) { return p.fmt == PF_F16 || p.fmt == PF_BF16; }
+constexpr float kRedo = -1.f;  // in the place of a split's weight sum: the row is to be done again
+
+// Of keys [x0, x1): those that only some of a tile's rows [first, last) see, [a0, a1) before and
+// [z0, z1) behind what all of them see (if anything, then [a1, z0)).
+struct KeySpans {
+    int a0, a1, z0, z1;
+};
+__device__ __forceinline__ KeySpans key_spans(const PAttnPlan &p, const SeqInfo &s, int first, int last, int x0, int x1) {
+    const int all_lo = seen_lo(p, s, token_of(p, last - 1)), all_hi = seen_hi(p, s, token_of(p, first));
+    KeySpans k;
+    k.a0 = x0;
+    k.a1 = min(max(all_lo, x0), x1);
+    k.z0 = min(max(all_hi, k.a1), x1);
+    k.z1 = x1;
+    return k;
+}
+// The largest finite scale of those spans' keys that this lane's row, which sees [a, z), sees, or
+// top.  The lanes of a warp go through the same keys.
+__device__ __forceinline__ float largest_scale(const PAttnPlan &p, const float *scales, int b, int h, KeySpans sp,
+                                                   int a, int z, float top) {
+    const int lane = threadIdx.x & 31, shift = 31 - __clz(p.page);
+    for (int x = sp.a0; x < sp.z1; x += 32) {
+        if (x >= sp.a1 && x < sp.z0) x = sp.z0;
+        const int key = x + lane;
+        float mine = 0.f;
+        if (key < sp.z1) {
+            bool bad = false;
+            mine = __ldg(scales + ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1)));
+            mine = is_finite(mine) ? fabsf(mine) : 0.f;
+        }
+        for (int k = 0; k < 32; k++) {
+            const float s = __shfl_sync(0xffffffffu, mine, k);
+            if (x + k >= a && x + k < z) top = fmaxf(top, s);
+        }
+    }
+    return top;
+}
+
+// Whether a scale of those spans lies too far (log2) above the largest that this lane's row sees: of
+// `some`, the largest of the spans, and `all`, of keys that every row sees (bits).  Of scales of zero
+// only, nothing is lost.
+__device__ __forceinline__ bool too_far(uint32_t some, float seen, int limit) {
+    return (int)(some >> 23) > (int)(__float_as_uint(seen) >> 23) + limit;
+}
+static __device__ __noinline__ bool sees_too_little(const PAttnPlan &p, const float *scales, int b, int h, const KeySpans &sp, int i,
+                                                    uint32_t some, uint32_t all, int limit) {
+    const SeqInfo s = seq_info(p, b, false);
+    const float v = largest_scale(p, scales, b, h, sp, seen_lo(p, s, i), seen_hi(p, s, i), __uint_as_float(all));
+    return v > 0.f && too_far(some, v, limit);
+}
+
+// Four channels of a cached row, codes as they are.
+__device__ __forceinline__ void load_cached4(const PAttnPlan &p, const void *pool, int64_t off, float v[4]) {
+    if (p.fmt == PF_BF16) {
+        unpack4(load_raw4<DT_BF16>(pool, off), v);
+    } else if (p.fmt == PF_F16) {
+        unpack4(load_raw4<DT_F16>(pool, off), v);
+    } else {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(pool) + off));
+        const uint2 y = p.fmt == PF_E4M3 ? codes_to_f16<true>(w) : codes_to_f16<false>(w);
+        unpack4(Raw4<DT_F16>{y}, v);
+    }
 }
 // Row (query i of sequence b, query head hq): lane l gets channels 4l .. 4l+3, unnormalised.
 static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, int hq, float o[4], float &m,
@@ -97,23 +160,47 @@ static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, i
     m = -INFINITY;
     l = 0.f;
     o[0] = o[1] = o[2] = o[3] = 0.f;
-    const int dt = p.fmt == PF_F16 ? DT_F16 : DT_BF16;
-    for (int j = lo; j < hi; j++) {
-        bool bad = false;
-        const int64_t row = ((page_of(p, b, j, shift, bad) * p.H + h) << shift) + (j & (p.page - 1));
-        float d = 0.f, v[4];
+    const bool wide = wide_pages(p);
+    constexpr int N = 4;  // keys at a time: what this costs is waiting for memory
+    for (int j = lo; j < hi; j += N) {
+        float d[N], v[N][4], vs[N], mn = m;
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-            d += q[c] * load_x1(p.k, dt, row * kD + 4 * lane + c);
-            v[c] = load_x1(p.v, dt, row * kD + 4 * lane + c);
+        for (int k = 0; k < N; k++) {
+            d[k] = 0.f;
+            vs[k] = 1.f;
+            v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.f;
+            if (j + k < hi) {
+                bool bad = false;
+                const int64_t row = ((page_of(p, b, j + k, shift, bad) * p.H + h) << shift) + ((j + k) & (p.page - 1));
+                float y[4];
+                load_cached4(p, p.k, row * kD + 4 * lane, y);
+                load_cached4(p, p.v, row * kD + 4 * lane, v[k]);
+#pragma unroll
+                for (int c = 0; c < 4; c++) d[k] += q[c] * y[c];
+                if (!wide) {
+                    d[k] *= __ldg(p.ks + row);
+                    vs[k] = __ldg(p.vs + row);
+                }
+            }
         }
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-        const float sc = d * p.scale_log2, mn = fmaxf(m, sc), base = exp_base(mn);
-        const float corr = fast_exp2(m - base), w = fast_exp2(sc - base);
-        l = l * corr + w;
+        for (int k = 0; k < N; k++) {
 #pragma unroll
-        for (int c = 0; c < 4; c++) o[c] = o[c] * corr + w * v[c];
+            for (int x = 16; x > 0; x >>= 1) d[k] += __shfl_xor_sync(0xffffffffu, d[k], x);
+            d[k] = j + k < hi ? d[k] * p.scale_log2 : -INFINITY;
+            mn = fmaxf(mn, d[k]);
+        }
+        const float base = exp_base(mn), corr = fast_exp2(m - base);
+        l *= corr;
+#pragma unroll
+        for (int c = 0; c < 4; c++) o[c] *= corr;
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const float w = fast_exp2(d[k] - base);
+            l += w;
+#pragma unroll
+            for (int c = 0; c < 4; c++) o[c] += w * (wide ? v[k][c] : v[k][c] * vs[k]);
+        }
         m = mn;
     }
 }
