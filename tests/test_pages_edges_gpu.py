@@ -144,3 +144,34 @@ def test_scales_of_keys_that_some_queries_do_not_see(fmt, nq, n, group, window, 
         assert not bool(out[sees].isfinite().any()) and not bool(alone[sees].isfinite().any())
         if which == "k":
             assert bool(lse[sees].isnan().all())
+
+
+@pytest.mark.parametrize("fmt", [BF, HF, E4, I8])
+@pytest.mark.parametrize("nq,n", [(3, 300), (140, 300), (140, 2600)])
+def test_scores_far_past_the_exponential(fmt, nq, n):
+    # scores of 2^30 and more, where fp32 steps are whole powers of two: a query's largest score
+    # has all the weight, and the output is its value, to the roundings of weight, value and output
+    g = _gen(nq + n)
+    kv, table = tp._cache(g, [n], 1, fmt, 32)
+    dtype = HF if fmt is HF else BF
+    Q = torch.randn((nq, 2, 128), generator=g).to(dtype)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    scale = 3.0e8
+    K = pm.pool_rows(kv.k, kv.k_scale, table[0], n, 32)[0]
+    V = pm.pool_rows(kv.v, kv.v_scale, table[0], n, 32)[0]
+    s = torch.einsum("ihd,jd->hij", Q.double(), K) * scale
+    seen = torch.arange(n)[None] <= torch.arange(n - nq, n)[:, None]
+    s = s.masked_fill(~seen, -math.inf)
+    two = s.topk(2, -1).values
+    # the gap to the second is thousands of the score's roundings for all but a few rows
+    clear = two[..., 0] - two[..., 1] > 128 * 2.0 ** -22 * (Q.double().abs().amax() * K.abs().amax() * 128 * scale)
+    assert float(clear.double().mean()) > 0.5
+    want = V[s.argmax(-1)]
+    for kw in (dict(), dict(return_lse=True, out_dtype=F32)):
+        out = api.page_attention(Q.cuda(), kv, table.cuda(), lens, scale=scale, **kw)
+        if kw:
+            out, lse = out
+            assert float(((lse.cpu().double().T - two[..., 0]) / two[..., 0].abs()).abs().max()) <= 2.0 ** -16
+        assert bool(out.isfinite().all())
+        off = (out.double().cpu().transpose(0, 1) - want).abs()
+        assert float(off[clear].max()) <= 3 * 2.0 ** -8 * float(V.abs().max())

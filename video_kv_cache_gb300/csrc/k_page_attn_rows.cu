@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
             }
     }
     if (wide_pages(p) && redo_possible(p))
-        again = __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3]));
+        again |= __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3]));
     if (again)
         redo_row(p, b, i, hq, o, mx, l);
     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);

@@ -69,6 +69,9 @@ constexpr int kValueShift = 4, kKeyShift = 6;  // 8-bit values and keys over the
 // least, if 2^e is at most kKeyShift + 2 above.
 constexpr int kValueFar = kValueShift, kKeyFar = kKeyShift + 2;
 constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
+// The largest score less its base, from the unrounded product, is what the base was rounded by: at
+// most 1/2 up to here, and weights stay below fp16's largest.  Past it the row is done again.
+constexpr float kHugeScore = 8388608.f;
 
 template <int FMT>
 struct TcShape {
@@ -105,7 +108,7 @@ struct TcShared {
     uint64_t sizes;
     uint32_t some[2], all[2];           // bits of the largest scale of keys, values that some rows see only, and of others
     float xmax[2][2][kTcM];             // the two threads of a row: their maxima; at the end their weight sums
-    uint32_t odd[2][4][2];              // rows that did not come out finite, a bit each: row tile, quarter, half
+    uint32_t odd[2][4][2];              // rows to be done again, a bit each: row tile, quarter, half
     uint32_t bad[2][4];                 // rows that see a value whose scale is not finite: their output is NaN, their weight sum is not
     __align__(16) float ks[2][WIDE ? 4 : kTcN];  // keys' scales times the softmax scale
     __align__(16) float vs[2][WIDE ? 4 : kTcN];  // values' scales over their reference
@@ -847,13 +850,15 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             if (ok) {
                 const int i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - i * p.G;
                 const bool live = r < rows, whole = S == 1;
-                bool odd = false;
+                // rows to be done again: for their scores' size, or (8 bits) what they see is too small
+                // for a reference
+                bool again = is_finite(m) && fabsf(m) > kHugeScore, odd = false;
                 if constexpr (!WIDE) {
                     const uint32_t v_some = sh.some[1], v_all = sh.all[1], k_some = sh.some[0], k_all = sh.all[0];
                     if (too_far(v_some, __uint_as_float(v_all), kValueFar) || too_far(k_some, __uint_as_float(k_all), kKeyFar)) {
                         const KeySpans sp = key_spans(p, sq, r0, min(rows, r0 + 2 * kTcM), max(lo, j0 * kTcN), min(hi, (j0 + n) * kTcN));
-                        odd = sees_too_little(p, p.vs, b, h, sp, i, v_some, v_all, kValueFar);
-                        odd |= sees_too_little(p, p.ks, b, h, sp, i, k_some, k_all, kKeyFar);
+                        again |= sees_too_little(p, p.vs, b, h, sp, i, v_some, v_all, kValueFar);
+                        again |= sees_too_little(p, p.ks, b, h, sp, i, k_some, k_all, kKeyFar);
                     }
                 }
                 float inv = 1.f;
@@ -913,30 +918,28 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 }
                 if (narrow) write_out(half * 64);
                 if (!whole) {
-                    if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, !WIDE && odd ? kRedo : l);
+                    if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, again ? kRedo : l);
                 } else {
                     if (live && half == 0 && p.lse) p.lse[tok * p.HQ + hq] = row_lse(m, l);
-                    if (redo_possible(p)) {
-                        // both halves written, then each of the two warps takes its share of the
-                        // rows that either found odd
-                        const uint32_t mine = __ballot_sync(0xffffffffu, odd && live);
-                        if (lane == 0) sh.odd[t][quarter][half] = mine;
-                        __threadfence_block();
-                        meet<64>(id, true);
-                        uint32_t todo = mine | sh.odd[t][quarter][half ^ 1];
-                        todo &= half ? 0xAAAAAAAAu : 0x55555555u;
-                        while (todo) {
-                            const int src = __ffs(todo) - 1;
-                            todo &= todo - 1;
-                            const int ri = __shfl_sync(0xffffffffu, i, src), rh = __shfl_sync(0xffffffffu, hq, src);
-                            float ro[4], rm, rl;
-                            redo_row(p, b, ri, rh, ro, rm, rl);
-                            const float f = rl == 0.f ? 0.f : __fdiv_rn(1.f, rl);
+                    // both halves written, then each of the two warps takes its share of the rows
+                    // that either found odd
+                    const uint32_t mine = __ballot_sync(0xffffffffu, live && (again || (odd && redo_possible(p))));
+                    if (lane == 0) sh.odd[t][quarter][half] = mine;
+                    __threadfence_block();
+                    meet<64>(id, true);
+                    uint32_t todo = mine | sh.odd[t][quarter][half ^ 1];
+                    todo &= half ? 0xAAAAAAAAu : 0x55555555u;
+                    while (todo) {
+                        const int src = __ffs(todo) - 1;
+                        todo &= todo - 1;
+                        const int ri = __shfl_sync(0xffffffffu, i, src), rh = __shfl_sync(0xffffffffu, hq, src);
+                        float ro[4], rm, rl;
+                        redo_row(p, b, ri, rh, ro, rm, rl);
+                        const float f = rl == 0.f ? 0.f : __fdiv_rn(1.f, rl);
 #pragma unroll
-                            for (int c = 0; c < 4; c++) ro[c] *= f;
-                            store_out4(p, (sq.q0 + ri) * p.ot + rh * p.oh + 4 * lane, ro);
-                            if (p.lse && lane == 0) p.lse[(sq.q0 + ri) * p.HQ + rh] = row_lse(rm, rl);
-                        }
+                        for (int c = 0; c < 4; c++) ro[c] *= f;
+                        store_out4(p, (sq.q0 + ri) * p.ot + rh * p.oh + 4 * lane, ro);
+                        if (p.lse && lane == 0) p.lse[(sq.q0 + ri) * p.HQ + rh] = row_lse(rm, rl);
                     }
                 }
             }

@@ -75,12 +75,13 @@ __device__ __forceinline__ bool is_finite(float x) {
     return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
 
-// Where a mask hides keys from some rows of a tile, a row may have to be computed once more by one
-// warp, over the keys that it sees and no others:
+// A row may have to be computed once more by one warp, over the keys that it sees and no others,
+// where a mask hides keys from some rows of a tile:
 //   * 16-bit pages: a value that is NaN or infinite, multiplied by the zero weight of a query that
 //     does not see its key, makes that query's row NaN.  Rows that did not come out finite.
 //   * 8-bit pages, many rows: a scale that the row does not see, far above all that it sees, has
 //     taken its values' or keys' bits (k_page_attn_tc.cu).
+// And, many rows, where scores are past 2^23.
 __device__ __forceinline__ bool redo_possible(const PAttnPlan &p) { return p.causal || p.window > 0; }
 __device__ __forceinline__ bool wide_pages(const PAttnPlan &p) { return p.fmt == PF_F16 || p.fmt == PF_BF16; }
 constexpr float kRedo = -1.f;  // in the place of a split's weight sum: the row is to be done again
