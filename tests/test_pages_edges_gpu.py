@@ -175,3 +175,38 @@ def test_scores_far_past_the_exponential(fmt, nq, n):
         assert bool(out.isfinite().all())
         off = (out.double().cpu().transpose(0, 1) - want).abs()
         assert float(off[clear].max()) <= 3 * 2.0 ** -8 * float(V.abs().max())
+
+
+def _time(f):
+    f()
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    a.record()
+    f()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b)
+
+
+@pytest.mark.parametrize("nq,n,heads,window", [(1, 20000, 4, 0), (4, 20000, 4, 0), (300, 6000, 2, 0), (300, 6000, 2, 1000),
+                                               (64, 9000, 1, 0)])
+def test_a_visible_value_that_is_not_finite_costs_little(nq, n, heads, window):
+    # only rows that such a value spoilt without being seen are done again; done again key by key,
+    # all rows that see it would take more than thirty times as long
+    g = _gen(nq)
+    kv, table = tp._cache(g, [n], heads, BF, 64)
+    lens, table = torch.tensor([n], dtype=torch.int32).cuda(), table.cuda()
+    Q = torch.randn((nq, heads, 128), generator=g).to(BF).cuda()
+
+    def call():
+        return api.page_attention(Q, kv, table, lens, window=window, return_lse=True)
+    clean, clean_lse = call()
+    clean_time = min(_time(call) for _ in range(3))
+    j = n - nq - (window // 2) if window else 70  # seen by every query
+    kv.v[int(table[0, j // 64]), :, j % 64, 9] = math.inf
+    kv.v[int(table[0, j // 64]), :, j % 64, 10] = math.nan
+    out, lse = call()
+    keep = [c for c in range(128) if c not in (9, 10)]
+    assert torch.equal(out[..., keep], clean[..., keep]) and torch.equal(lse, clean_lse)
+    assert bool((out[..., 9] == math.inf).all()) and bool(out[..., 10].isnan().all())
+    assert min(_time(call) for _ in range(3)) <= 8 * clean_time

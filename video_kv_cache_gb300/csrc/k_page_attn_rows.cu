@@ -723,8 +723,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             while (todo) {
                 const int src = (__ffs(todo) - 1) & ~7;  // the row's first lane
                 todo &= ~(0xFFu << src);
+                const int ri = __shfl_sync(0xffffffffu, row_i, src), rh = __shfl_sync(0xffffffffu, hq, src);
                 float ro[4], rm, rl;
-                redo_row(p, b, __shfl_sync(0xffffffffu, row_i, src), __shfl_sync(0xffffffffu, hq, src), ro, rm, rl);
+                if (!redo_if_shared(p, b, ri, rh, 0, sq.qn - 1, false, ro, rm, rl)) continue;
                 // lane x has channels 4x ..: this thread's are those of lanes part + 8 c
 #pragma unroll
                 for (int c = 0; c < 16; c++) {
@@ -806,10 +807,16 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
                 o[3] += f * po[k].w;
             }
     }
-    if (wide_pages(p) && redo_possible(p))
-        again |= __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3]));
-    if (again)
-        redo_row(p, b, i, hq, o, mx, l);
+    const bool odd = wide_pages(p) && redo_possible(p) &&
+                     __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3]));
+    if (again || odd) {  // (an item's rows end where the sequence's do)
+        float y[4], ym, yl;
+        if (redo_if_shared(p, b, i, hq, token_of(p, r - local), min(token_of(p, r - local + p.unit - 1), sq.qn - 1), again, y, ym, yl)) {
+            o[0] = y[0]; o[1] = y[1]; o[2] = y[2]; o[3] = y[3];
+            mx = ym;
+            l = yl;
+        }
+    }
     const float inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll
     for (int c = 0; c < 4; c++) o[c] *= inv;

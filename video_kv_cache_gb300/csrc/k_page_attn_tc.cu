@@ -921,9 +921,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, again ? kRedo : l);
                 } else {
                     if (live && half == 0 && p.lse) p.lse[tok * p.HQ + hq] = row_lse(m, l);
+                    if (WIDE && redo_possible(p) && __any_sync(0xffffffffu, odd && live)) again |= odd & spoilt(p, b, h, i, lo, hi);
                     // both halves written, then each of the two warps takes its share of the rows
-                    // that either found odd
-                    const uint32_t mine = __ballot_sync(0xffffffffu, live && (again || (odd && redo_possible(p))));
+                    // that are to be done again
+                    const uint32_t mine = __ballot_sync(0xffffffffu, live && again);
                     if (lane == 0) sh.odd[t][quarter][half] = mine;
                     __threadfence_block();
                     meet<64>(id, true);

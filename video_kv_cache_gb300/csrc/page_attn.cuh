@@ -2,6 +2,8 @@
 // finished row is written.
 #pragma once
 
+#include <climits>
+
 #include "page_codes.cuh"
 #include "rows.cuh"
 #include "tcgen.cuh"
@@ -78,7 +80,10 @@ __device__ __forceinline__ bool is_finite(float x) {
 // A row may have to be computed once more by one warp, over the keys that it sees and no others,
 // where a mask hides keys from some rows of a tile:
 //   * 16-bit pages: a value that is NaN or infinite, multiplied by the zero weight of a query that
-//     does not see its key, makes that query's row NaN.  Rows that did not come out finite.
+//     does not see its key, makes that query's row NaN.  Rows that did not come out finite and
+//     shared a tile with such a key, which they do not see.  (Those that see one themselves are
+//     what they should be.  Doing them again too, a key at a time, took seconds where a NaN is early
+//     in a long cache: 44 us became 1600 for one query of four heads over 4096 keys.)
 //   * 8-bit pages, many rows: a scale that the row does not see, far above all that it sees, has
 //     taken its values' or keys' bits (k_page_attn_tc.cu).
 // And, many rows, where scores are past 2^23.
@@ -135,6 +140,31 @@ static __device__ __noinline__ bool sees_too_little(const PAttnPlan &p, const fl
     return v > 0.f && too_far(some, v, limit);
 }
 
+// First and last of keys [from, to) with a value that is not finite, looked for by a whole warp;
+// first > last where there is none.
+struct BadKeys {
+    int first, last;
+};
+__device__ __forceinline__ BadKeys bad_values(const PAttnPlan &p, int b, int h, int from, int to) {
+    const int lane = threadIdx.x & 31, shift = 31 - __clz(p.page);
+    const uint32_t ones = p.fmt == PF_F16 ? 0x7C007C00u : 0x7F807F80u;
+    BadKeys k = {INT_MAX, -1};
+#pragma unroll 4
+    for (int key = from + (lane >> 4); key < to; key += 2) {  // 16 lanes a row
+        bool bad = false;
+        const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) + row * kD) + (lane & 15));
+        auto odd = [&](uint32_t x) { return __vcmpeq2(x & ones, ones); };
+        if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
+            k.first = min(k.first, key);
+            k.last = key;
+        }
+    }
+    __syncwarp();
+    k.first = __reduce_min_sync(0xffffffffu, k.first);
+    k.last = __reduce_max_sync(0xffffffffu, k.last);
+    return k;
+}
 // Four channels of a cached row, codes as they are.
 __device__ __forceinline__ void load_cached4(const PAttnPlan &p, const void *pool, int64_t off, float v[4]) {
     if (p.fmt == PF_BF16) {
@@ -204,6 +234,30 @@ static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, i
         }
         m = mn;
     }
+}
+
+// Whether this lane's row (query i of head h) did not come out finite for a value that it does not see,
+// among keys [lo, hi) of its tile; the lanes' rows follow one another.
+static __device__ __noinline__ bool spoilt(const PAttnPlan &p, int b, int h, int i, int lo, int hi) {
+    const SeqInfo s = seq_info(p, b, false);
+    const int a = seen_lo(p, s, i), z = seen_hi(p, s, i);
+    const BadKeys before = bad_values(p, b, h, lo, min(__shfl_sync(0xffffffffu, a, 31), hi));
+    const BadKeys behind = bad_values(p, b, h, max(__shfl_sync(0xffffffffu, z, 0), lo), hi);
+    return before.first < a || behind.last >= max(z, 0);
+}
+
+// The same if it must be, or if query i, in a tile of the sequence's queries [i0, i1], shares it with a
+// value that is not finite and that it does not see.  Otherwise nothing changes.
+static __device__ __noinline__ bool redo_if_shared(const PAttnPlan &p, int b, int i, int hq, int i0, int i1, bool must,
+                                                   float o[4], float &m, float &l) {
+    if (!must) {
+        const SeqInfo s = seq_info(p, b, false);
+        const int lo = seen_lo(p, s, i0), hi = seen_hi(p, s, i1);
+        const int a = max(seen_lo(p, s, i), lo), z = max(seen_hi(p, s, i), a), h = hq / p.G;
+        if (bad_values(p, b, h, lo, min(a, hi)).last < 0 && bad_values(p, b, h, z, hi).last < 0) return false;
+    }
+    redo_row(p, b, i, hq, o, m, l);
+    return true;
 }
 
 __device__ __forceinline__ void store_out1(const PAttnPlan &p, int64_t off, float v) {
