@@ -210,3 +210,29 @@ def test_a_visible_value_that_is_not_finite_costs_little(nq, n, heads, window):
     assert torch.equal(out[..., keep], clean[..., keep]) and torch.equal(lse, clean_lse)
     assert bool((out[..., 9] == math.inf).all()) and bool(out[..., 10].isnan().all())
     assert min(_time(call) for _ in range(3)) <= 8 * clean_time
+
+
+@pytest.mark.parametrize("nq,n,group,window,j", SPANS + [(5, 15000, 8, 0, 14998)])
+def test_nan_codes_of_keys_that_some_queries_do_not_see(nq, n, group, window, j):
+    # E4M3 has codes that are NaN; page_write stores none, but pages may come from elsewhere
+    g = _gen(nq + n)
+    kv, table = tp._cache(g, [n], 1, E4, 32)
+    Q = torch.randn((nq, group, 128), generator=g).to(BF)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    kv.v.view(torch.uint8)[int(table[0, j // 32]), 0, j % 32, 5] = 0x7F
+    kv.v.view(torch.uint8)[int(table[0, j // 32]), 0, j % 32, 77] = 0xFF
+    out, lse = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32, return_lse=True)
+    alone = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window)
+    sees = [i for i, (a, z) in enumerate(_seen(n, nq, window)) if a <= j < z]
+    blind = [i for i in range(nq) if i not in sees]
+    assert blind and sees
+    _check_rows(Q, kv, table, n, window, blind, out, lse)
+    _check_rows(Q, kv, table, n, window, blind, alone, u_kv=0.0 if nq * group <= 16 else 2.0 ** -11)
+    keep = [c for c in range(128) if c not in (5, 77)]
+    for o in (out, alone):
+        assert bool(o[sees][..., [5, 77]].isnan().all()) and bool(o[sees][..., keep].isfinite().all())
+    _check_lse(Q, kv, table, n, window, lse)
+    kv.k.view(torch.uint8)[int(table[0, j // 32]), 0, j % 32, 5] = 0x7F
+    out = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32)
+    assert bool(out[sees].isnan().all())
+    _check_rows(Q, kv, table, n, window, blind, out)

@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                 cluster_meet();  // nobody leaves while its rows are read
             }
             if (!mine) return;
-        if (wide_pages(p) && redo_possible(p)) {
+        if (rows_to_check(p)) {
             bool odd = false;
 #pragma unroll
             for (int c = 0; c < 16; c++) odd |= !is_finite(v[c]);
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
                 o[3] += f * po[k].w;
             }
     }
-    const bool odd = wide_pages(p) && redo_possible(p) &&
+    const bool odd = rows_to_check(p) &&
                      __any_sync(0xffffffffu, !is_finite(o[0]) || !is_finite(o[1]) || !is_finite(o[2]) || !is_finite(o[3]));
     if (again || odd) {  // (an item's rows end where the sequence's do)
         float y[4], ym, yl;

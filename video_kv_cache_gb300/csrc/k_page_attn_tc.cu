@@ -852,15 +852,18 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const bool live = r < rows, whole = S == 1;
                 // rows to be done again: for their scores' size, or (8 bits) what they see is too small
                 // for a reference
-                bool again = is_finite(m) && fabsf(m) > kHugeScore, odd = false;
-                if constexpr (!WIDE) {
+                bool again = is_finite(m) && fabsf(m) > kHugeScore;
+                auto check_sizes = [&] {
                     const uint32_t v_some = sh.some[1], v_all = sh.all[1], k_some = sh.some[0], k_all = sh.all[0];
                     if (too_far(v_some, __uint_as_float(v_all), kValueFar) || too_far(k_some, __uint_as_float(k_all), kKeyFar)) {
                         const KeySpans sp = key_spans(p, sq, r0, min(rows, r0 + 2 * kTcM), max(lo, j0 * kTcN), min(hi, (j0 + n) * kTcN));
                         again |= sees_too_little(p, p.vs, b, h, sp, i, v_some, v_all, kValueFar);
                         again |= sees_too_little(p, p.ks, b, h, sp, i, k_some, k_all, kKeyFar);
                     }
-                }
+                };
+                // (behind the output, the compiler spills less of the loop over e4m3 pages, 918 -> 904 us
+                // for 4680 x 32760 x 12 heads, and more over int8, 957 -> 1000)
+                if constexpr (!WIDE && FMT != PF_E4M3) check_sizes();
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
                 if constexpr (!WIDE) inv = sh.bad[t][quarter] >> lane & 1u ? NAN : ldexpf(inv, e - kValueShift);
@@ -875,6 +878,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const int64_t elem = narrow ? 2 : 4, at = (whole ? tok * p.ot + hq * p.oh : part * kD) * elem;
                 unsigned char *dst = static_cast<unsigned char *>(whole ? p.O : p.part);
                 unsigned char *stage = sQ + t * kSlot + half * 128;  // + row * 256
+                bool odd = false;
                 auto leave = [&](int c, uint4 v) { *reinterpret_cast<uint4 *>(stage + row * 256 + ((c ^ (row & 7)) << 4)) = v; };
                 auto write_out = [&](int first_channel) {
                     __syncwarp();
@@ -900,7 +904,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 32; k++) {
                         o[k] *= inv;
-                        if constexpr (WIDE) odd |= !is_finite(o[k]);
+                        if constexpr (FMT != PF_INT8) odd |= !is_finite(o[k]);
                     }
                     if (narrow) {
                         auto pk = [&](int k) {
@@ -917,11 +921,16 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     }
                 }
                 if (narrow) write_out(half * 64);
+                if constexpr (FMT == PF_E4M3) check_sizes();
                 if (!whole) {
                     if (live && half == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m, again ? kRedo : l);
                 } else {
                     if (live && half == 0 && p.lse) p.lse[tok * p.HQ + hq] = row_lse(m, l);
-                    if (WIDE && redo_possible(p) && __any_sync(0xffffffffu, odd && live)) again |= odd & spoilt(p, b, h, i, lo, hi);
+                    if constexpr (FMT != PF_INT8) {
+                        // (with 8 bits, lo and hi kept until here would cost registers in the loop)
+                        if (redo_possible(p) && __any_sync(0xffffffffu, odd && live))
+                            again |= odd & (WIDE ? spoilt(p, b, h, i, lo, hi) : spoilt_in(p, b, h, i, r0));
+                    }
                     // both halves written, then each of the two warps takes its share of the rows
                     // that are to be done again
                     const uint32_t mine = __ballot_sync(0xffffffffu, live && again);

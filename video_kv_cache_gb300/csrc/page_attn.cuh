@@ -79,9 +79,9 @@ __device__ __forceinline__ bool is_finite(float x) {
 
 // A row may have to be computed once more by one warp, over the keys that it sees and no others,
 // where a mask hides keys from some rows of a tile:
-//   * 16-bit pages: a value that is NaN or infinite, multiplied by the zero weight of a query that
-//     does not see its key, makes that query's row NaN.  Rows that did not come out finite and
-//     shared a tile with such a key, which they do not see.  (Those that see one themselves are
+//   * 16-bit or E4M3 pages: a value that is NaN or infinite (a code that is NaN), multiplied by the
+//     zero weight of a query that does not see its key, makes that query's row NaN.  Rows that did
+//     not come out finite and shared a tile with such a key, which they do not see.  (Those that see one themselves are
 //     what they should be.  Doing them again too, a key at a time, took seconds where a NaN is early
 //     in a long cache: 44 us became 1600 for one query of four heads over 4096 keys.)
 //   * 8-bit pages, many rows: a scale that the row does not see, far above all that it sees, has
@@ -89,6 +89,7 @@ __device__ __forceinline__ bool is_finite(float x) {
 // And, many rows, where scores are past 2^23.
 __device__ __forceinline__ bool redo_possible(const PAttnPlan &p) { return p.causal || p.window > 0; }
 __device__ __forceinline__ bool wide_pages(const PAttnPlan &p) { return p.fmt == PF_F16 || p.fmt == PF_BF16; }
+__device__ __forceinline__ bool rows_to_check(const PAttnPlan &p) { return p.fmt != PF_INT8 && redo_possible(p); }
 constexpr float kRedo = -1.f;  // in the place of a split's weight sum: the row is to be done again
 
 // Of keys [x0, x1): those that only some of a tile's rows [first, last) see, [a0, a1) before and
@@ -153,9 +154,15 @@ __device__ __forceinline__ BadKeys bad_values(const PAttnPlan &p, int b, int h, 
     for (int key = from + (lane >> 4); key < to; key += 2) {  // 16 lanes a row
         bool bad = false;
         const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) + row * kD) + (lane & 15));
-        auto odd = [&](uint32_t x) { return __vcmpeq2(x & ones, ones); };
-        if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
+        bool odd;
+        if (p.fmt == PF_E4M3) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.v) + row * kD) + (lane & 15));
+            odd = __vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        } else {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) + row * kD) + (lane & 15));
+            odd = __vcmpeq2(w.x & ones, ones) | __vcmpeq2(w.y & ones, ones) | __vcmpeq2(w.z & ones, ones) | __vcmpeq2(w.w & ones, ones);
+        }
+        if (odd) {
             k.first = min(k.first, key);
             k.last = key;
         }
@@ -236,14 +243,20 @@ static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, i
     }
 }
 
-// Whether this lane's row (query i of head h) did not come out finite for a value that it does not see,
-// among keys [lo, hi) of its tile; the lanes' rows follow one another.
+// Whether this lane's row (query i of head h) shares its tile, whose rows see keys [lo, hi), with a value
+// that is not finite and that it does not see; the lanes' rows follow one another.
 static __device__ __noinline__ bool spoilt(const PAttnPlan &p, int b, int h, int i, int lo, int hi) {
     const SeqInfo s = seq_info(p, b, false);
     const int a = seen_lo(p, s, i), z = seen_hi(p, s, i);
     const BadKeys before = bad_values(p, b, h, lo, min(__shfl_sync(0xffffffffu, a, 31), hi));
     const BadKeys behind = bad_values(p, b, h, max(__shfl_sync(0xffffffffu, z, 0), lo), hi);
     return before.first < a || behind.last >= max(z, 0);
+}
+
+// For a tile of rows [r0, r0 + p.unit).
+static __device__ __noinline__ bool spoilt_in(const PAttnPlan &p, int b, int h, int i, int r0) {
+    const SeqInfo s = seq_info(p, b, false);
+    return spoilt(p, b, h, i, seen_lo(p, s, token_of(p, r0)), seen_hi(p, s, token_of(p, min(s.qn * p.G, r0 + p.unit) - 1)));
 }
 
 // The same if it must be, or if query i, in a tile of the sequence's queries [i0, i1], shares it with a
