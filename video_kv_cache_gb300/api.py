@@ -239,20 +239,36 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _rows(x: torch.Tensor, what: str):
+def _gpu(x: torch.Tensor, what: str) -> int:
+    """The GPU that x is on, which is the one that the call launches on: the current one."""
+    dev = x.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("%s must be on the current GPU" % what)
+    return dev
+
+
+def _rows(x: torch.Tensor, what: str, dev: int):
     """(tokens, heads, token stride, head stride) of rows [tokens][heads][128] of contiguous
     channels; a stride is 0 where there is one row only, whose stride says nothing."""
     shape, stride = x.shape, x.stride()
-    if not (x.is_cuda and len(shape) == 3 and shape[2] == D and stride[2] == 1 and x.dtype in _DT):
-        _need(x.is_cuda and len(shape) == 3 and shape[2] == D and (stride[2] == 1 or x.numel() == 0),
-              "%s must be a CUDA tensor [tokens][heads][128] with contiguous channels" % what)
+    if not (x.get_device() == dev and len(shape) == 3 and shape[2] == D and stride[2] == 1 and x.dtype in _DT):
+        _need(x.get_device() == dev and len(shape) == 3 and shape[2] == D and (stride[2] == 1 or x.numel() == 0),
+              "%s must be a tensor [tokens][heads][128] on the call's GPU, with contiguous channels" % what)
         _need(x.dtype in _DT, "%s must be fp16, bf16 or fp32" % what)
     return (shape[0], shape[1], stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
 
 
-def _index(x: torch.Tensor, dtype, shape, what: str):
-    if not (x.dtype == dtype and x.shape == shape and x.is_cuda and x.is_contiguous()):
-        raise ValueError("%s must be a contiguous CUDA tensor %s of %s" % (what, list(shape), dtype))
+def _index(x: torch.Tensor, dtype, shape, what: str, dev: int | None = None):
+    if not (x.dtype == dtype and x.shape == shape and x.is_contiguous()
+            and (x.is_cuda if dev is None else x.get_device() == dev)):
+        raise ValueError("%s must be a contiguous tensor %s of %s on the call's GPU" % (what, list(shape), dtype))
+
+
+def _check_scratch(status, workspace, dev: int):
+    if status is not None and not (status.get_device() == dev and status.dtype == torch.int32 and status.numel() >= 1):
+        raise ValueError("status must be an int32 tensor on the call's GPU")
+    if workspace is not None and not (workspace.get_device() == dev and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the call's GPU")
 
 
 def _empty(shape, dtype, device, stream):
@@ -295,12 +311,13 @@ class RopeTable:
             self.mscale, 0, None, self.freqs.data_ptr()))
 
     def rotary(self, positions: torch.Tensor, n: int) -> _c.qvg_rotary:
+        dev = self.freqs.get_device()
         axes, shape, stride = len(self.sections), positions.shape, positions.stride()
         if len(shape) == 1:
             shape, stride = (1, shape[0]), (n, stride[0])
-        if not (positions.is_cuda and positions.dtype == torch.int64 and shape == (axes, n)
+        if not (positions.get_device() == dev and positions.dtype == torch.int64 and shape == (axes, n)
                 and (n <= 1 or stride[1] == 1) and (axes == 1 or stride[0] >= n)):
-            raise ValueError("positions must be int64 [%d][%d] on the GPU, each axis contiguous" % (axes, n))
+            raise ValueError("positions must be int64 [%d][%d] on the table's GPU, each axis contiguous" % (axes, n))
         r = _c.qvg_rotary.from_buffer_copy(self._fixed)
         r.pos_stride = stride[0]
         r.positions = positions.data_ptr()
@@ -361,12 +378,14 @@ def rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, *,
     """Turn X [n][heads][128] (fp16 / bf16 / fp32, any token and head strides) by its positions
     (int64 [n], or [axes][n] for a table with several axes).  ``out`` may be X itself.
     ``backward`` gives the gradient of X from that of the result."""
-    n, heads, xt, xh = _rows(X, "X")
+    dev = _gpu(X, "X")
+    n, heads, xt, xh = _rows(X, "X", dev)
+    _need(table.freqs.get_device() == dev, "the table must be on the GPU of X")
     if out is None:
         out = _empty_as(X, (n, heads, D), X.dtype, stream)
         yt, yh = heads * D, D
     else:
-        on, oh, yt, yh = _rows(out, "out")
+        on, oh, yt, yh = _rows(out, "out", dev)
         _need(on == n and oh == heads and out.dtype == X.dtype, "out must have the shape and type of X")
     prm = _c.qvg_rope_params(n, heads, D, _DT[X.dtype], 1 if backward else 0, xt, xh, yt, yh)
     rc = _c.qvg_rope(prm, table.rotary(positions, n), X.data_ptr(), out.data_ptr(),
@@ -389,16 +408,18 @@ class PagedKV:
         shape = self.k.shape
         _need(len(shape) == 4 and shape[3] == D and self.k.dtype in _PAGE_FORMAT,
               "pages are [pages][heads][page_tokens][128] of fp16, bf16, float8_e4m3fn or int8")
+        dev = self.k.get_device()
         for t in (self.k, self.v):
             _index(t, self.k.dtype, shape, "k and v")
+            _need(t.get_device() == dev, "k and v must be on one GPU")
         wide = self.k.dtype in (torch.float16, torch.bfloat16)
         for t in (self.k_scale, self.v_scale):
             if wide:
                 _need(t is None, "16-bit pages have no scales")
             else:
                 _need(t is not None, "8-bit pages need k_scale and v_scale")
-                _index(t, torch.float32, shape[:3], "scales")
-        for name, value in (("n_pages", shape[0]), ("heads", shape[1]), ("page_tokens", shape[2]),
+                _index(t, torch.float32, shape[:3], "scales", dev)
+        for name, value in (("gpu", dev), ("n_pages", shape[0]), ("heads", shape[1]), ("page_tokens", shape[2]),
                             ("format", _PAGE_FORMAT[self.k.dtype]),
                             ("_buffers", _c.qvg_pages(self.k.data_ptr(), self.v.data_ptr(),
                                                       _ptr(self.k_scale), _ptr(self.v_scale)))):
@@ -431,12 +452,16 @@ def page_write(kv: PagedKV, K: torch.Tensor, V: torch.Tensor, slots: torch.Tenso
     """Store new tokens K and V [n][heads][128] at ``slots`` (int64 [n]: page * page_tokens +
     row; negative: skipped), rounded to the pages' format; with ``rope`` the keys are first
     turned by their positions."""
-    n, heads, kt, kh = _rows(K, "K")
-    vn, v_heads, vt, vh = _rows(V, "V")
+    dev = _gpu(K, "K")
+    n, heads, kt, kh = _rows(K, "K", dev)
+    vn, v_heads, vt, vh = _rows(V, "V", dev)
+    _need(kv.gpu == dev, "the pages must be on the GPU of K and V")
     _need(vn == n and v_heads == heads == kv.heads and K.dtype == V.dtype,
           "K and V must be [n][heads][128] of one type, with the heads of the pages")
-    _index(slots, torch.int64, (n,), "slots")
+    _index(slots, torch.int64, (n,), "slots", dev)
     _need((rope is None) == (positions is None), "rope and positions go together")
+    _need(rope is None or rope.freqs.get_device() == dev, "the table must be on the GPU of K and V")
+    _check_scratch(status, None, dev)
     prm = _c.qvg_page_write_params(n, heads, D, kv.page_tokens, kv.format, kv.n_pages,
                                    _DT[K.dtype], kt, kh, vt, vh)
     rc = _c.qvg_page_write(prm, K.data_ptr(), V.data_ptr(), slots.data_ptr(),
@@ -446,11 +471,11 @@ def page_write(kv: PagedKV, K: torch.Tensor, V: torch.Tensor, slots: torch.Tenso
         raise _c.QVGError(rc, "qvg_page_write")
 
 
-def _tables(page_table, seq_lens):
+def _tables(page_table, seq_lens, dev: int):
     shape = page_table.shape
     _need(len(shape) == 2, "page_table must be [sequences][pages]")
-    _index(page_table, torch.int32, shape, "page_table")
-    _index(seq_lens, torch.int32, shape[:1], "seq_lens")
+    _index(page_table, torch.int32, shape, "page_table", dev)
+    _index(seq_lens, torch.int32, shape[:1], "seq_lens", dev)
     return shape[0], shape[1]
 
 
@@ -460,14 +485,16 @@ def page_read(kv: PagedKV, page_table: torch.Tensor, seq_lens: torch.Tensor, cou
     """Tokens [first, first + count) of every sequence as [sequences][2 * heads][count][128],
     keys and values interleaved: ``out[b]`` is an X of ``quantize``.  Rows past a sequence's
     length are zeros.  ``out`` may have larger sequence and tensor strides."""
-    n_seqs, max_pages = _tables(page_table, seq_lens)
+    dev = _gpu(kv.k, "pages")
+    n_seqs, max_pages = _tables(page_table, seq_lens, dev)
+    _check_scratch(status, None, dev)
     shape = (n_seqs, 2 * kv.heads, count, D)
     if out is None:
         out = _empty(shape, out_dtype, kv.k.device, stream)
     stride = out.stride()
-    _need(out.is_cuda and out.shape == shape and out.dtype in _DT and
+    _need(out.get_device() == dev and out.shape == shape and out.dtype in _DT and
           (count == 0 or (stride[3] == 1 and (count == 1 or stride[2] == D))),
-          "out must be [sequences][2 * heads][count][128] with contiguous tokens")
+          "out must be [sequences][2 * heads][count][128] on the pages' GPU, with contiguous tokens")
     prm = _c.qvg_page_read_params(n_seqs, kv.heads, D, kv.page_tokens, kv.format, _DT[out.dtype],
                                   kv.n_pages, max_pages, first, count,
                                   stride[0] if n_seqs > 1 else 0, stride[1])
@@ -492,25 +519,28 @@ def page_attention(Q: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
     ``max_kv`` (about the longest sequence, the page table's capacity by default) sizes the
     split of the work.  Returns the output, and with ``return_lse`` the fp32 log-sum-exp
     [total_q][q_heads] beside it."""
-    total, q_heads, qt, qh = _rows(Q, "Q")
-    n_seqs, max_pages = _tables(page_table, seq_lens)
+    dev = _gpu(Q, "Q")
+    total, q_heads, qt, qh = _rows(Q, "Q", dev)
+    n_seqs, max_pages = _tables(page_table, seq_lens, dev)
+    _need(kv.gpu == dev, "the pages must be on the GPU of Q")
+    _check_scratch(status, workspace, dev)
     if cu_q is None:
         _need(total % n_seqs == 0 and (max_q is None or max_q == total // n_seqs),
               "without cu_q every sequence has total_q / sequences queries")
         max_q = total // n_seqs
     else:
-        _index(cu_q, torch.int32, (n_seqs + 1,), "cu_q")
+        _index(cu_q, torch.int32, (n_seqs + 1,), "cu_q", dev)
         max_q = total if max_q is None else max_q
     if out is None:
         out = _empty_as(Q, (total, q_heads, D), Q.dtype if out_dtype is None else out_dtype, stream)
         ot, oh = q_heads * D, D
     else:
-        on, o_heads, ot, oh = _rows(out, "out")
+        on, o_heads, ot, oh = _rows(out, "out", dev)
         _need(on == total and o_heads == q_heads, "out must have the shape of Q")
     if lse is None and return_lse:
         lse = _empty((total, q_heads), torch.float32, Q.device, stream)
     elif lse is not None:
-        _index(lse, torch.float32, (total, q_heads), "lse")
+        _index(lse, torch.float32, (total, q_heads), "lse", dev)
     prm = _c.qvg_page_attention_params(
         n_seqs, q_heads, kv.heads, D, kv.page_tokens, kv.format, _DT[Q.dtype], _DT[out.dtype],
         kv.n_pages, max_pages, 1 if causal else 0, window, total, max_q,
