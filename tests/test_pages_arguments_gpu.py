@@ -88,3 +88,14 @@ def test_tensors_of_another_gpu_are_refused(made, monkeypatch):
     for call in (_attend, _write, _read, _rope):
         with pytest.raises(ValueError):
             call(m)
+
+
+def test_no_sequences_are_refused(made):
+    m = made
+    none, no_pages = torch.zeros((0, 3), dtype=torch.int32, device="cuda"), torch.zeros((1, 0), dtype=torch.int32, device="cuda")
+    for call in (_attend, _read):
+        with pytest.raises(ValueError):
+            call(m, page_table=none, seq_lens=m["lens"][:0])
+        with pytest.raises(ValueError):
+            call(m, page_table=no_pages)
+    assert _attend(m, Q=m["x"][:0]).shape == (0, 2, 128)  # no queries are nothing to do

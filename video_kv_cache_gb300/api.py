@@ -473,7 +473,7 @@ def page_write(kv: PagedKV, K: torch.Tensor, V: torch.Tensor, slots: torch.Tenso
 
 def _tables(page_table, seq_lens, dev: int):
     shape = page_table.shape
-    _need(len(shape) == 2, "page_table must be [sequences][pages]")
+    _need(len(shape) == 2 and shape[0] > 0 and shape[1] > 0, "page_table must be [sequences][pages], one of each at least")
     _index(page_table, torch.int32, shape, "page_table", dev)
     _index(seq_lens, torch.int32, shape[:1], "seq_lens", dev)
     return shape[0], shape[1]
