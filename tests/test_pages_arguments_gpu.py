@@ -99,3 +99,26 @@ def test_no_sequences_are_refused(made):
         with pytest.raises(ValueError):
             call(m, page_table=no_pages)
     assert _attend(m, Q=m["x"][:0]).shape == (0, 2, 128)  # no queries are nothing to do
+
+
+def test_rope_does_not_lose_a_gradient(made):
+    m = made
+    x = torch.randn((20, 2, 128), device="cuda", requires_grad=True)
+    with pytest.raises(ValueError):
+        api.rope(x, m["pos"], m["rope"])
+    with torch.no_grad():
+        want = api.rope(x, m["pos"], m["rope"])
+
+    class Turn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return api.rope(x, m["pos"], m["rope"])
+
+        @staticmethod
+        def backward(ctx, dy):
+            return api.rope(dy, m["pos"], m["rope"], backward=True)
+    y = Turn.apply(x)
+    assert torch.equal(y, want)
+    dy = torch.randn_like(want)
+    y.backward(dy)
+    assert torch.equal(x.grad, api.rope(dy, m["pos"], m["rope"], backward=True))

@@ -377,8 +377,13 @@ def rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, *,
          out: torch.Tensor | None = None, backward: bool = False, stream=None) -> torch.Tensor:
     """Turn X [n][heads][128] (fp16 / bf16 / fp32, any token and head strides) by its positions
     (int64 [n], or [axes][n] for a table with several axes).  ``out`` may be X itself.
-    ``backward`` gives the gradient of X from that of the result."""
+    ``backward`` gives the gradient of X from that of the result.  Autograd does not record the
+    call, so an X whose gradient it would have to carry is refused: call it under
+    ``torch.no_grad()`` or from a ``torch.autograd.Function``, whose backward is
+    ``backward=True``."""
     dev = _gpu(X, "X")
+    _need(not (X.requires_grad and torch.is_grad_enabled()),
+          "autograd would lose X's gradient here: call rope without gradient recording, and backward=True for it")
     n, heads, xt, xh = _rows(X, "X", dev)
     _need(table.freqs.get_device() == dev, "the table must be on the GPU of X")
     if out is None:
