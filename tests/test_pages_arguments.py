@@ -21,3 +21,10 @@ def test_host_tensors_are_refused_by_every_call():
         api.allocate_pages(2, 1, 16, torch.bfloat16, device="cpu")
     with pytest.raises(ValueError):
         api.rope_table(64, device="cpu")
+
+
+@pytest.mark.parametrize("bad", [dict(fast_turns=1.0), dict(fast_turns=2.0, slow_turns=2.0), dict(fast_turns=1.0, slow_turns=4.0),
+                                 dict(fast_turns=float("nan")), dict(original_len=0)])
+def test_frequency_ramps_that_are_none(bad):
+    with pytest.raises(ValueError):
+        api.rope_frequencies(64, scaling="by_parts", factor=4.0, **bad)

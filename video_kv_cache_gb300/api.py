@@ -338,6 +338,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, sections=None, scaling
     _need(scaling in ("none", "linear", "stretched", "by_parts"), "unknown scaling %r" % (scaling,))
     _need(rot_dim >= 2 and rot_dim % 2 == 0 and base > 0 and factor >= 1,
           "rot_dim must be even, base positive and factor at least 1")
+    _need(fast_turns > slow_turns and original_len > 0,
+          "fast_turns must be above slow_turns, and original_len positive")
     sections = (rot_dim // 2,) if sections is None else tuple(sections)
     _need(sum(sections) == rot_dim // 2, "sections must add up to rot_dim / 2")
     out, mscale = [], 1.0
