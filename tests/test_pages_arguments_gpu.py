@@ -1,5 +1,8 @@
 """What the paged-cache calls refuse before anything is launched, on a GPU machine: tensors in other
 places than the call's, of the wrong type or shape."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -122,3 +125,20 @@ def test_rope_does_not_lose_a_gradient(made):
     dy = torch.randn_like(want)
     y.backward(dy)
     assert torch.equal(x.grad, api.rope(dy, m["pos"], m["rope"], backward=True))
+
+
+@pytest.mark.parametrize("fmt", [BF, torch.int8])
+def test_handles_can_be_copied(made, fmt):
+    # a copy is of the pages and the table, not of where they lie
+    m = made
+    kv = api.allocate_pages(4, 2, 16, fmt)
+    x = torch.randn((20, 2, 128), generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    api.page_write(kv, x, x, m["slots"], rope=m["rope"], positions=m["pos"])
+    want = api.page_attention(x, kv, m["table"], m["lens"])
+    for again in (copy.copy(kv), copy.deepcopy(kv), pickle.loads(pickle.dumps(kv))):
+        assert torch.equal(api.page_attention(x, again, m["table"], m["lens"]), want)
+    far = copy.deepcopy(kv)
+    kv.k.zero_()
+    assert torch.equal(api.page_attention(x, far, m["table"], m["lens"]), want)
+    for rope in (copy.copy(m["rope"]), copy.deepcopy(m["rope"]), pickle.loads(pickle.dumps(m["rope"]))):
+        assert torch.equal(api.rope(x, m["pos"], rope), api.rope(x, m["pos"], m["rope"]))

@@ -310,6 +310,9 @@ class RopeTable:
             self.rot_dim, int(self.interleaved), axes, (*sections, *(0,) * (4 - axes)),
             self.mscale, 0, None, self.freqs.data_ptr()))
 
+    def __reduce__(self):  # a copy describes its own tensor's memory
+        return RopeTable, (self.freqs, self.rot_dim, self.sections, self.interleaved, self.mscale)
+
     def rotary(self, positions: torch.Tensor, n: int) -> _c.qvg_rotary:
         dev = self.freqs.get_device()
         axes, shape, stride = len(self.sections), positions.shape, positions.stride()
@@ -431,6 +434,9 @@ class PagedKV:
                             ("_buffers", _c.qvg_pages(self.k.data_ptr(), self.v.data_ptr(),
                                                       _ptr(self.k_scale), _ptr(self.v_scale)))):
             object.__setattr__(self, name, value)
+
+    def __reduce__(self):  # a copy describes its own tensors' memory
+        return PagedKV, (self.k, self.v, self.k_scale, self.v_scale)
 
     def buffers(self) -> _c.qvg_pages:
         return self._buffers
