@@ -236,3 +236,45 @@ def test_nan_codes_of_keys_that_some_queries_do_not_see(nq, n, group, window, j)
     out = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32)
     assert bool(out[sees].isnan().all())
     _check_rows(Q, kv, table, n, window, blind, out)
+
+
+UNLIKE = [  # q lengths, cached lengths, q heads, heads, type, format, page, causal, window
+    ([5, 0, 200, 1, 0, 60], [900, 700, 3000, 1, 0, 2000], 4, 2, BF, BF, 32, True, 0),
+    ([0, 0, 290], [10, 0, 2000], 1, 1, HF, HF, 64, False, 0),
+    ([1 + b % 3 if b % 5 else 0 for b in range(69)] + [130], [3 * b + 3 for b in range(69)] + [1700], 20, 1, BF, I8, 16, True, 0),
+    ([100, 0, 0, 70], [1500, 0, 0, 2100], 3, 3, BF, E4, 128, True, 600),
+]
+
+
+@pytest.mark.parametrize("case", UNLIKE)
+def test_split_items_of_unlike_sequences(case):
+    q_lens, kv_lens, q_heads, heads, dtype, fmt, page, causal, window = case
+    g = _gen(sum(q_lens))
+    kv, table = tp._cache(g, kv_lens, heads, fmt, page)
+    Q = torch.randn((sum(q_lens), q_heads, 128), generator=g).to(dtype)
+    tp._check(Q, kv, table, kv_lens, q_lens, causal, window)
+    # any of them may be the longest, as far as the call knows
+    tp._check(Q, kv, table, kv_lens, q_lens, causal, window, max_q=sum(q_lens))
+
+
+def test_split_items_report_bad_arguments():
+    g = _gen(4)
+    kv, table = tp._cache(g, [2000, 5, 900], 1, BF, 32)
+    Q = torch.randn((130, 1, 128), generator=g).to(BF).cuda()
+
+    def status_of(cu=(0, 90, 90, 130), lens=(2000, 5, 900), max_q=130):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full_like(Q, 7.0)
+        api.page_attention(Q, kv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), max_q=max_q,
+                           cu_q=torch.tensor(cu, dtype=torch.int32).cuda(), status=st, out=out)
+        return int(st), out
+    st, good = status_of()
+    assert st == 0 and not bool((good == 7).all(-1).any())
+    for bad in (dict(cu=(0, 130, 0, 130)), dict(cu=(0, 90, 90, 140)), dict(cu=(-2, 90, 90, 130)), dict(lens=(2000, -5, 900)),
+                dict(lens=(2000, 5, 99999)), dict(max_q=80)):
+        st, out = status_of(**bad)
+        assert st == qvg.QVG_DEV_BAD_INDEX, bad
+    st, out = status_of(lens=(2000, -5, 900))  # a sequence without queries, cut
+    assert torch.equal(out, good)
+    st, out = status_of(max_q=80)
+    assert bool((out[80:90] == 7).all()) and torch.equal(out[90:], good[90:])

@@ -473,7 +473,11 @@ struct PAttnPlan {
     // are split S ways, a CTA each, and joined.
     int unit, units, S;
     int64_t whole;
-    int by_length;  // many rows: the items of few sequences (at most 32) in the order of what they see
+    int by_length;  // many rows: the items of few sequences (at most 16) in the order of what they see
+    // Sequences with different numbers of queries, their items split: numbered one sequence after
+    // another, those that there are and no others, of which there are at most `items`.
+    int compact;
+    int64_t items;
     // Few rows, long keys: all heads' keys in a row are cut into equal shares instead, a CTA
     // each, whose first and last stretches may be parts of a head.
     int stream;

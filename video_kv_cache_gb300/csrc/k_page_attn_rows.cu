@@ -757,10 +757,14 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
     pdl_begin();
     const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    const int64_t cells = (int64_t)p.B * p.H, t = w / p.unit, item = p.whole + t;
-    if (item >= p.units * cells) return;
-    const int cell = (int)(item / p.units), u = (int)(item - (int64_t)cell * p.units), b = cell / p.H, h = cell - b * p.H;
-    const int local = (int)(w - t * p.unit), r = (p.units - 1 - u) * p.unit + local;
+    const int64_t t = w / p.unit, item = p.whole + t;
+    if (item >= p.items) return;
+    int cell = (int)(item / p.units), b = cell / p.H, h = cell - b * p.H, pair = p.units - 1 - (int)(item - (int64_t)cell * p.units);
+    if (p.compact) {
+        if (!compact_item(p, t, false, b, h, pair)) return;
+        cell = b * p.H + h;
+    }
+    const int local = (int)(w - t * p.unit), r = pair * p.unit + local;
     const SeqInfo sq = seq_info(p, b, false);
     if (r >= sq.qn * p.G) return;
     const int i = token_of(p, r), hq = h * p.G + r - i * p.G;
@@ -846,14 +850,18 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
 //   (Splitting every item alike would write 57 MB of partial results for 4680 x 32760 x 12
 //   heads, one and a half rounds, instead of 19.)  Sequences with different numbers of queries
 //   leave items empty, and the last ones say nothing about the last round: there all items
-//   are split alike, if they are too few for one round; else, up to 16 sequences, the items of
+//   are split alike, if they are too few for one round (only those that the sequences can have
+//   get CTAs and room for partial results: 16 sequences that share 512 queries of 16 heads on 2
+//   over up to 32768 keys ask for 60 MB, room for 512 of each for 477; with 2000 keys each, 65 ->
+//   33 us); else, up to 16 sequences, the items of
 //   those that see the most come first, so that the last round is one of short ones (six
 //   sequences of up to 2000 queries over 500 to 9000 keys, 32 query heads on 8: 238 -> 208 us,
 //   301 -> 278; thirty even out by themselves: 1701 us, in order 1762).
 void page_attention_cut(PAttnPlan &p) {
     const int64_t rows = p.max_q * p.G, cells = (int64_t)p.H * p.B;
     p.whole = 0;
-    p.stream = p.by_length = 0;
+    p.items = cells;
+    p.stream = p.by_length = p.compact = 0;
     if (rows <= kRowsM) {
         p.unit = kRowsM;
         p.units = 1;
@@ -878,7 +886,7 @@ void page_attention_cut(PAttnPlan &p) {
     const bool alike = p.total_q == p.max_q * p.B;
     const int64_t busy = alike ? items : std::min(items, p.total_q * p.G / 256 * p.H + cells);
     const int64_t rest = alike ? items % 152 : busy < 152 ? busy : 0, rounds = alike ? items / 152 : 0;
-    p.whole = items;
+    p.whole = p.items = items;
     p.S = 1;
     double least = (double)((rounds + 1) * (tiles + 6));
     for (int s = 2; rest && s <= 64 && s <= tiles / 4; s++) {
@@ -891,11 +899,15 @@ void page_attention_cut(PAttnPlan &p) {
         }
     }
     p.by_length = p.S == 1 && !alike && p.B <= 16;
+    if (p.S > 1 && !alike && busy < items) {
+        p.compact = 1;
+        p.items = busy;
+    }
 }
 int64_t page_attention_part_rows(const PAttnPlan &p) {
     if (p.stream) return 2 * (int64_t)kRowsShares * kRowsM;
     if (p.S == 1 || (p.unit == kRowsM && p.S <= kRowsCluster)) return 0;
-    return ((int64_t)p.units * p.H * p.B - p.whole) * p.S * p.unit;
+    return (p.items - p.whole) * p.S * p.unit;
 }
 
 namespace {

@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
         h = at / n;
         pair = n - 1 - (at - h * n);
     }
-    const SeqInfo sq = seq_info(p, b, !p.by_length && threadIdx.x == 0 && pair == 0 && split == 0 && h == 0);
+    if (p.compact && !compact_item(p, tail, blockIdx.x == 0 && warp == 0, b, h, pair)) return;
+    const SeqInfo sq = seq_info(p, b, !p.by_length && !p.compact && threadIdx.x == 0 && pair == 0 && split == 0 && h == 0);
     const int rows = sq.qn * p.G, r0 = pair * 2 * kTcM;
     if (r0 >= rows) return;
     const int nt = rows - r0 > kTcM ? 2 : 1;  // row tiles in use
@@ -974,7 +975,7 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
     const auto kernel = k_page_attn_tc<QB, FMT, FOLD>;
     cudaError_t e = allow_smem<k_page_attn_tc<QB, FMT, FOLD>>(smem);
     if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)p.units * p.H * p.B, grid = p.whole + (items - p.whole) * p.S;
+    const int64_t grid = p.whole + (p.items - p.whole) * p.S;
     return launch_kernel(kernel, dim3((unsigned)grid), dim3(T::THREADS), smem, st, mk, mv, p);
 }
 }  // namespace

@@ -40,6 +40,33 @@ __device__ __forceinline__ SeqInfo seq_info(const PAttnPlan &p, int b, bool repo
 // quotient is exact.
 __device__ __forceinline__ int token_of(const PAttnPlan &p, int r) { return (int)((uint64_t)(uint32_t)r * p.g_inv >> 34); }
 
+// The item with this number among those of all sequences in a row (PAttnPlan::compact), for a whole
+// warp: false if there are fewer.  A sequence's last rows come first.  With report, what is cut of
+// any sequence is reported.
+__device__ __forceinline__ bool compact_item(const PAttnPlan &p, int64_t number, bool report, int &b, int &h, int &pair) {
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < p.B; base += 32) {
+        const int units = base + lane < p.B ? (seq_info(p, base + lane, report).qn * p.G + p.unit - 1) / p.unit : 0;
+        int upto = units;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, x);
+            if (lane >= x) upto += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, (int64_t)upto * p.H > number);
+        if (past) {
+            const int at = __ffs(past) - 1, n = __shfl_sync(0xffffffffu, units, at);
+            const int in = (int)(number - (int64_t)(__shfl_sync(0xffffffffu, upto, at) - n) * p.H);
+            b = base + at;
+            h = in / n;
+            pair = n - 1 - (in - h * n);
+            return true;
+        }
+        number -= (int64_t)__shfl_sync(0xffffffffu, upto, 31) * p.H;
+    }
+    return false;
+}
+
 // Keys [lo, hi) that query i of the sequence sees (empty when lo >= hi).
 __device__ __forceinline__ int seen_lo(const PAttnPlan &p, const SeqInfo &s, int i) {
     if (p.window <= 0) return 0;
