@@ -278,3 +278,77 @@ def test_split_items_report_bad_arguments():
     assert torch.equal(out, good)
     st, out = status_of(max_q=80)
     assert bool((out[80:90] == 7).all()) and torch.equal(out[90:], good[90:])
+
+
+SHARED = [  # cached lengths, q lengths (in turn), q heads, heads, q type, format, page, causal, window
+    ([2900, 0, 1, 64, 127, 128, 129, 700] * 3, [1], 8, 4, BF, E4, 64, True, 0),
+    ([300, 900, 40, 2000], [1, 2], 48, 24, HF, I8, 16, True, 250),   # a window that begins in the middle
+    ([2000, 1500] * 2, [5], 60, 30, BF, E4, 32, True, 700),
+    ([17] * 11, [1], 8, 8, BF, I8, 16, True, 0),                     # fewer stages than shares would like
+    ([0, 0, 0, 0], [1, 0], 40, 40, BF, E4, 16, False, 0),            # no keys: a stage each where there is a query
+    ([0, 0, 0, 0], [0, 0, 1, 0], 40, 40, HF, I8, 16, False, 0),
+    ([300, 20], [0], 100, 100, BF, I8, 16, True, 0),                 # no stages at all (one query follows)
+    ([64] * 304, [1], 2, 1, HF, I8, 64, True, 0),                    # one stage a head, four a share
+    ([65] * 152, [1], 4, 2, BF, E4, 32, True, 0),
+]
+
+
+@pytest.mark.parametrize("case", SHARED)
+def test_equal_shares_of_8_bit_keys(case):
+    # the keys of all heads cut into equal shares, and the sizes where shares and stages nearly
+    # run out; the workspace says that the call takes this way
+    kv_lens, q_lens, q_heads, heads, dtype, fmt, page, causal, window = case
+    q_lens = [q_lens[b % len(q_lens)] for b in range(len(kv_lens))]
+    if not any(q_lens):
+        kv_lens, q_lens = kv_lens + [5], q_lens + [1]
+    g = _gen(sum(q_lens) + sum(kv_lens) + heads)
+    kv, table = tp._cache(g, kv_lens, heads, fmt, page)
+    cells = heads * len(kv_lens)
+    assert 76 < cells <= 608
+    longest = 1 + 152 * 2 * 2048 // cells
+    wide = torch.zeros((len(kv_lens), max(table.shape[1], -(-longest // page))), dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    prm = qvg.qvg_page_attention_params(
+        n_seqs=len(kv_lens), n_q_heads=q_heads, n_heads=heads, d=128, page_tokens=page, format=kv.format,
+        q_dtype=api._DT[dtype], out_dtype=api._DT[dtype], n_pages=kv.n_pages, max_pages=wide.shape[1], causal=int(causal),
+        window=window, total_q=sum(q_lens), max_q=max(q_lens), max_kv=longest, scale=0.1, q_token_stride=q_heads * 128,
+        q_head_stride=128, o_token_stride=q_heads * 128, o_head_stride=128)
+    assert qvg.qvg_page_attention_workspace_bytes(prm) == 2 * 304 * 16 * (128 + 2) * 4 + cells * 8
+    Q = (1.5 * torch.randn((sum(q_lens), q_heads, 128), generator=g)).to(dtype)
+    tp._check(Q, kv, wide, kv_lens, q_lens, causal, window, max_kv=longest)
+
+
+@pytest.mark.parametrize("fmt", [E4, I8])
+@pytest.mark.parametrize("window", [0, 400])
+def test_hidden_keys_in_equal_shares(fmt, window):
+    # five queries of 40 heads over shares that end anywhere: a scale, and a NaN code, of a key that
+    # only the last two queries see
+    g = _gen(window + 1)
+    n, heads, nq = 1900, 40, 5
+    kv, table = tp._cache(g, [n, n], heads, fmt, 32)
+    longest = 1 + 152 * 2 * 2048 // (2 * heads)
+    wide = torch.zeros((2, -(-longest // 32)), dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    Q = torch.randn((2 * nq, heads, 128), generator=g).to(BF)
+    lens = torch.tensor([n, n], dtype=torch.int32).cuda()
+
+    def call():
+        return api.page_attention(Q.cuda(), kv, wide.cuda(), lens, max_kv=longest, window=window, out_dtype=F32, return_lse=True)
+    clean, clean_lse = call()
+    page, row = int(table[0, (n - 2) // 32]), (n - 2) % 32
+    for size in (2.0 ** 40, math.inf, math.nan):
+        was = kv.v_scale[page, :, row].clone()
+        kv.v_scale[page, :, row] = size
+        out, lse = call()
+        assert torch.equal(out[:3], clean[:3]) and torch.equal(out[5:], clean[5:]) and torch.equal(lse, clean_lse)
+        if not math.isfinite(size):
+            assert not bool(out[3:5].isfinite().any())
+        kv.v_scale[page, :, row] = was
+    if fmt is E4:
+        kv.v.view(torch.uint8)[page, :, row, 7] = 0x7F
+        out, lse = call()
+        # (rows done again: each is within its roundings, fp16 weights, of the same value)
+        near = 8 * 2.0 ** -11 * float(pm.pool_rows(kv.v, kv.v_scale, table[0], n - 2, 32).abs().max())
+        assert float((out[:3] - clean[:3]).abs().max()) <= near and torch.equal(out[5:], clean[5:])
+        assert bool(out[3:5][..., 7].isnan().all()) and int(out.isnan().sum()) == 2 * heads
+        assert float((lse - clean_lse).abs().max()) <= 2.0 ** -12
