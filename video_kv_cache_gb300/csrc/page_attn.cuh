@@ -199,74 +199,90 @@ __device__ __forceinline__ BadKeys bad_values(const PAttnPlan &p, int b, int h, 
     k.last = __reduce_max_sync(0xffffffffu, k.last);
     return k;
 }
-// Four channels of a cached row, codes as they are.
-__device__ __forceinline__ void load_cached4(const PAttnPlan &p, const void *pool, int64_t off, float v[4]) {
-    if (p.fmt == PF_BF16) {
-        unpack4(load_raw4<DT_BF16>(pool, off), v);
-    } else if (p.fmt == PF_F16) {
-        unpack4(load_raw4<DT_F16>(pool, off), v);
-    } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(pool) + off));
-        const uint2 y = p.fmt == PF_E4M3 ? codes_to_f16<true>(w) : codes_to_f16<false>(w);
-        unpack4(Raw4<DT_F16>{y}, v);
-    }
+// Eight channels of a row, as they lie in memory and as numbers (codes without their scale).
+__device__ __forceinline__ uint4 load_cached8(const PAttnPlan &p, const void *pool, int64_t off) {
+    if (wide_pages(p)) return __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(pool) + off));
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pool) + off));
+    return make_uint4(w.x, w.y, 0u, 0u);
 }
-// Row (query i of sequence b, query head hq): lane l gets channels 4l .. 4l+3, unnormalised.
-static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, int hq, float o[4], float &m,
-                                      float &l) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void unpack8(int fmt, uint4 w, float v[8]) {
+    if (fmt == PF_BF16) {
+        unpack4(Raw4<DT_BF16>{make_uint2(w.x, w.y)}, v);
+        unpack4(Raw4<DT_BF16>{make_uint2(w.z, w.w)}, v + 4);
+        return;
+    }
+    if (fmt != PF_F16) {
+        const uint2 y = fmt == PF_E4M3 ? codes_to_f16<true>(w.x) : codes_to_f16<false>(w.x);
+        const uint2 z = fmt == PF_E4M3 ? codes_to_f16<true>(w.y) : codes_to_f16<false>(w.y);
+        w = make_uint4(y.x, y.y, z.x, z.y);
+    }
+    unpack4(Raw4<DT_F16>{make_uint2(w.x, w.y)}, v);
+    unpack4(Raw4<DT_F16>{make_uint2(w.z, w.w)}, v + 4);
+}
+// Row (query i of sequence b, query head hq): lane l gets channels 4l .. 4l+3, unnormalised.  Half
+// a warp takes a key, eight channels a lane, each half every other key with a maximum and sums of
+// its own; the next keys are asked for before these are worked on, their pages looked up before that.
+static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, int hq, float o4[4], float &m4, float &l4) {
+    const int lane = threadIdx.x & 31, part = lane & 15;
     const SeqInfo s = seq_info(p, b, false);
     const int shift = 31 - __clz(p.page), h = hq / p.G;
     const int lo = seen_lo(p, s, i), hi = seen_hi(p, s, i);
-    float q[4];
-#pragma unroll
-    for (int c = 0; c < 4; c++)
-        q[c] = load_x1(p.Q, p.q_dtype, (s.q0 + i) * p.qt + hq * p.qh + 4 * lane + c);
-    m = -INFINITY;
-    l = 0.f;
-    o[0] = o[1] = o[2] = o[3] = 0.f;
     const bool wide = wide_pages(p);
-    constexpr int N = 4;  // keys at a time: what this costs is waiting for memory
-    for (int j = lo; j < hi; j += N) {
-        float d[N], v[N][4], vs[N], mn = m;
-#pragma unroll
-        for (int k = 0; k < N; k++) {
-            d[k] = 0.f;
-            vs[k] = 1.f;
-            v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.f;
-            if (j + k < hi) {
-                bool bad = false;
-                const int64_t row = ((page_of(p, b, j + k, shift, bad) * p.H + h) << shift) + ((j + k) & (p.page - 1));
-                float y[4];
-                load_cached4(p, p.k, row * kD + 4 * lane, y);
-                load_cached4(p, p.v, row * kD + 4 * lane, v[k]);
-#pragma unroll
-                for (int c = 0; c < 4; c++) d[k] += q[c] * y[c];
-                if (!wide) {
-                    d[k] *= __ldg(p.ks + row);
-                    vs[k] = __ldg(p.vs + row);
-                }
+    float q[8], o[8] = {}, m = -INFINITY, l = 0.f;
+    unpack8(p.q_dtype == DT_BF16 ? PF_BF16 : PF_F16,
+            __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.Q) + (s.q0 + i) * p.qt + hq * p.qh + 8 * part)), q);
+    auto row_of = [&](int key) {
+        bool bad = false;
+        return key < hi ? (int)(((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1))) : -1;
+    };
+    uint4 kn, vn;
+    float ksn, vsn;
+    auto ask = [&](int row) {
+        kn = vn = make_uint4(0u, 0u, 0u, 0u);
+        ksn = vsn = 1.f;
+        if (row >= 0) {
+            kn = load_cached8(p, p.k, (int64_t)row * kD + 8 * part);
+            vn = load_cached8(p, p.v, (int64_t)row * kD + 8 * part);
+            if (!wide) {
+                ksn = __ldg(p.ks + row);
+                vsn = __ldg(p.vs + row);
             }
         }
+    };
+    const int first = lo + (lane >> 4);
+    ask(row_of(first));
+    int next = row_of(first + 2);
+    for (int key = first; key - (lane >> 4) < hi; key += 2) {
+        float y[8], d = 0.f;
+        unpack8(p.fmt, kn, y);
 #pragma unroll
-        for (int k = 0; k < N; k++) {
+        for (int c = 0; c < 8; c++) d += q[c] * y[c];
+        d *= ksn;
+        const uint4 v = vn;
+        const float vs = vsn;
+        ask(next);
+        next = row_of(key + 4);
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) d[k] += __shfl_xor_sync(0xffffffffu, d[k], x);
-            d[k] = j + k < hi ? d[k] * p.scale_log2 : -INFINITY;
-            mn = fmaxf(mn, d[k]);
-        }
-        const float base = exp_base(mn), corr = fast_exp2(m - base);
-        l *= corr;
+        for (int x = 8; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+        d = key < hi ? d * p.scale_log2 : -INFINITY;
+        const float mn = fmaxf(m, d), base = exp_base(mn), corr = fast_exp2(m - base), w = fast_exp2(d - base);
+        l = l * corr + w;
+        unpack8(p.fmt, v, y);
 #pragma unroll
-        for (int c = 0; c < 4; c++) o[c] *= corr;
-#pragma unroll
-        for (int k = 0; k < N; k++) {
-            const float w = fast_exp2(d[k] - base);
-            l += w;
-#pragma unroll
-            for (int c = 0; c < 4; c++) o[c] += w * (wide ? v[k][c] : v[k][c] * vs[k]);
-        }
+        for (int c = 0; c < 8; c++) o[c] = o[c] * corr + w * (y[c] * vs);
         m = mn;
+    }
+    // the halves joined, and lane l's four channels from the lanes that have them
+    m4 = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    const float f = fast_exp2(m - exp_base(m4));
+    l4 = l * f;
+    l4 += __shfl_xor_sync(0xffffffffu, l4, 16);
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+        float y = o[c] * f;
+        y += __shfl_xor_sync(0xffffffffu, y, 16);
+        y = __shfl_sync(0xffffffffu, y, lane >> 1);
+        if ((c >> 2) == (lane & 1)) o4[c & 3] = y;
     }
 }
 
