@@ -6,8 +6,8 @@
 // (query tokens x grouped query heads, at most 16).  One warp of a CTA streams the keys' and
 // values' pages by TMA into a ring of stages of 64 or 128 keys (about 100 KB in flight a CTA,
 // two CTAs an SM: several times what the memory's latency needs).  One query of 32 sequences of
-// 15000 tokens, 8 heads: bf16 275 us (7.1 TB/s), e4m3 and int8 163 us (6.0 TB/s; the latencies
-// of widening and softmax, two computing warps a scheduler).  Of each stage four warps take a
+// 15000 tokens, 8 heads, back to back: bf16 278 us (7.1 TB/s), e4m3 and int8 161 us (6.1 TB/s; the
+// latencies of widening and softmax, two computing warps a scheduler).  Of each stage four warps take a
 // quarter, with a running maximum and weight sum per row, on warp-level matrix instructions (the
 // tensor cores' own take 128 rows at a time, at most 16 of which would be in use):
 //   * scores S^T = K Q^T: the keys are the product's 16 rows and the queries its columns, eight
@@ -854,9 +854,11 @@ __global__ void __launch_bounds__(256) k_page_combine(PAttnPlan p) {
 //   get CTAs and room for partial results: 16 sequences that share 512 queries of 16 heads on 2
 //   over up to 32768 keys ask for 60 MB, room for 512 of each for 477; with 2000 keys each, 65 ->
 //   33 us); else, up to 16 sequences, the items of
-//   those that see the most come first, so that the last round is one of short ones (six
-//   sequences of up to 2000 queries over 500 to 9000 keys, 32 query heads on 8: 238 -> 208 us,
-//   301 -> 278; thirty even out by themselves: 1701 us, in order 1762).
+//   those that see the most come first, so that the last round is one of short ones (four draws
+//   of six prompts of 17 to 2000 queries over 500 to 9000 keys, 32 query heads on 8, bf16, causal,
+//   on warm caches: 241 -> 211 us, 250 -> 220, 306 -> 281, 561 -> 521; the last but one in fp16
+//   with a window of 4096, which makes the items more alike, 250 either way; thirty prompts even
+//   out by themselves: 1999, 1640, 1735, 1570 us, in order 2000, 1640, 1725, 1575).
 void page_attention_cut(PAttnPlan &p) {
     const int64_t rows = p.max_q * p.G, cells = (int64_t)p.H * p.B;
     p.whole = 0;

@@ -3,9 +3,10 @@
 //   O = softmax(scale Q K^T, over the visible keys) V
 //
 // Bound by the tensor cores: 4 * 128 operations per visible (query row, key) pair.  4680 queries
-// of 12 heads over 32760 keys, every one seen: 592 us back to back (1590 TFLOP/s), 640 us with
-// cold caches; 4096 over 32768 of 32 heads, causal: 1268 us (1625).  The tensor cores work 87 %
-// of the cycles of the loop over the keys at the clocks that this load leaves (1.5 to 1.6 GHz);
+// of 12 heads over 32760 keys, every one seen: 601 us back to back on warm caches (1567 TFLOP/s),
+// 643 us with cold ones; 4096 over 32768 of 32 heads, causal, warm: 1280 us (1610).  The tensor
+// cores work 87 % of the cycles of the loop over the keys at the clocks that this load leaves
+// (1.5 to 1.6 GHz);
 // the rest is the start of a CTA (about 8000 cycles: TMEM, Q, the first tile) and the join of
 // the last round's splits.  Shared memory is as busy as they are: a tile pair's products read
 // 192 KB of it and the loads write 64, at 128 bytes a cycle the 2048 cycles of the products.
@@ -41,14 +42,18 @@
 // of each key and value, an eighth of what the output's own rounding is. Otherwise the scales
 // multiply the scores and the weights in the softmax (the weights, in fp16, relative to the same
 // power of two), which costs time: every thread then reads the scales of all keys from shared
-// memory. The case above takes 893 us in e4m3 and 1020 in int8, without folding 1086 and 1107.
-// What costs is instructions: 10300 of a warp a tile pair against 5500 in 16 bits, which share
+// memory. The case above takes 908 us in e4m3 and 974 in int8 on warm caches, without folding 1097
+// and 1152; 4096 over 32768 of 32 heads, causal, in e4m3 1913, with cold caches 1924.
+// What costs is instructions: 10500 of a warp a tile pair against 5400 in 16 bits, which share
 // the issue slots with the exponentials; with one factor instead of two (a scale rounded to
 // fp16, an error that all channels of a key share) the first two took 20 and 34 us less.
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
-// product runs over the 16-key steps in sight, and the rest of the outer steps is zeroed.
+// product runs over the 16-key steps in sight, and the rest of the outer steps is zeroed.  What some
+// rows of a tile see and others do not can still spoil those (page_attn.cuh says how); they are
+// found at an item's end and computed once more, a key at a time.  For that the widening warps look,
+// while the last tile is under way, at the scales of the keys that only some rows see.
 #include "page_attn.cuh"
 
 namespace qvg {
@@ -735,8 +740,9 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     return fmaxf(fmax3(m0, s[30], s[31]), m1);
                 };
                 // 16 bits: the scores stay in registers.  8 bits, with more warps and fewer
-                // registers each, they would spill: they are read twice, for their maximum and
-                // for the weights (2.03 -> 1.94 ms; in 16 bits it costs 643 -> 675 us).
+                // registers each, many would spill (some values do as it is, 20 to 76 bytes a thread
+                // in all forms): they are read twice, for their maximum and for the weights (2.03 ->
+                // 1.94 ms; in 16 bits it costs 643 -> 675 us).
                 constexpr bool TWICE = !WIDE;
                 float s[TWICE ? 32 : 64], mx = -INFINITY, mult = row_mult;
                 if (ok) {

@@ -18,8 +18,9 @@ namespace qvg {
 
 namespace {
 constexpr int kWriteHeads = 4;  // heads of one token that a half-warp writes, keys and values
-// 24 warps an SM: 32760 x 12 heads in int8 take 51 us; 16 warps with all the registers they
-// want 61, 32 with spills 62
+// 24 warps an SM, 80 registers: 32760 x 12 heads in int8 take 51 us; 16 warps with all the
+// registers they want 61, 32 with 64 registers 62.  Some registers spill at 80 too: 12 to 104 bytes
+// a thread from 16-bit inputs, 160 from fp32 to 8 bits, 350 from fp32 to 16 bits.
 constexpr int kWriteThreads = 128, kWriteCtas = 6;
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100: below it a row is stored as zeros
 
