@@ -352,3 +352,23 @@ def test_hidden_keys_in_equal_shares(fmt, window):
         assert float((out[:3] - clean[:3]).abs().max()) <= near and torch.equal(out[5:], clean[5:])
         assert bool(out[3:5][..., 7].isnan().all()) and int(out.isnan().sum()) == 2 * heads
         assert float((lse - clean_lse).abs().max()) <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("nq,n,window", [(300, 6000, 0), (64, 9000, 0), (300, 6000, 3000)])
+@pytest.mark.parametrize("lse", [False, True])
+def test_a_large_scale_that_all_have_seen_before_costs_little(nq, n, window, lse):
+    # a value sixty times the nearest ones among the newest keys, and as large a one that every
+    # query sees far back: no query needs to be done again
+    g = _gen(nq + n)
+    kv, table = tp._cache(g, [n], 2, E4, 64)
+    lens, table = torch.tensor([n], dtype=torch.int32).cuda(), table.cuda()
+    Q = torch.randn((nq, 2, 128), generator=g).to(BF).cuda()
+
+    def call():
+        return api.page_attention(Q, kv, table, lens, window=window, return_lse=lse)
+    call()
+    clean_time = min(_time(call) for _ in range(3))
+    for j in (n - window + 5 if window else 70, n - 3):
+        kv.v_scale[int(table[0, j // 64]), :, j % 64] *= 60.0
+    call()
+    assert min(_time(call) for _ in range(3)) <= 8 * clean_time

@@ -69,10 +69,11 @@ constexpr int kValueShift = 4, kKeyShift = 6;  // 8-bit values and keys over the
 // How far (log2) a scale that a row does not see may lie above the largest that it sees before the
 // row is done again.  Values: a weight times a scale over the reference 2^e is rounded by at most
 // 2^-25 times 2^(e - kValueShift) and a code, 2^-25 of the largest value that the row sees if 2^e is
-// at most kValueShift above it (folded values, rounded alone, by 2^-7 of that).  Keys: channels by
+// at most kValueShift above it.  Folded values are rounded alone, by 2^-25 times 2^(e - kValueShift):
+// the same of a largest value of 127 codes at least if 2^e is 2^7 further up.  Keys: channels by
 // 2^-25 times 2^(e - kKeyShift), which is 2^-30 of the row's largest key, 127 codes of its scale at
 // least, if 2^e is at most kKeyShift + 2 above.
-constexpr int kValueFar = kValueShift, kKeyFar = kKeyShift + 2;
+constexpr int kValueFar = kValueShift, kFoldedFar = kValueShift + 7, kKeyFar = kKeyShift + 2;
 constexpr float kLazy = 8.f;               // how far (log2) scores may pass the running maximum
 // The largest score less its base, from the unrounded product, is what the base was rounded by: at
 // most 1/2 up to here, and weights stay below fp16's largest.  Past it the row is done again.
@@ -862,10 +863,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 bool again = is_finite(m) && fabsf(m) > kHugeScore;
                 auto check_sizes = [&] {
                     const uint32_t v_some = sh.some[1], v_all = sh.all[1], k_some = sh.some[0], k_all = sh.all[0];
-                    if (too_far(v_some, __uint_as_float(v_all), kValueFar) || too_far(k_some, __uint_as_float(k_all), kKeyFar)) {
+                    constexpr int VALUE_FAR = FOLD ? kFoldedFar : kValueFar;
+                    if (too_far(v_some, __uint_as_float(v_all), VALUE_FAR) || too_far(k_some, __uint_as_float(k_all), kKeyFar)) {
                         const KeySpans sp = key_spans(p, sq, r0, min(rows, r0 + 2 * kTcM), max(lo, j0 * kTcN), min(hi, (j0 + n) * kTcN));
-                        again |= sees_too_little(p, p.vs, b, h, sp, i, v_some, v_all, kValueFar);
-                        again |= sees_too_little(p, p.ks, b, h, sp, i, k_some, k_all, kKeyFar);
+                        again |= sees_too_little(p, p.vs, b, h, sp, r0, i, v_some, v_all, VALUE_FAR);
+                        again |= sees_too_little(p, p.ks, b, h, sp, r0, i, k_some, k_all, kKeyFar);
                     }
                 };
                 // (behind the output, the compiler spills less of the loop over e4m3 pages, 918 -> 904 us

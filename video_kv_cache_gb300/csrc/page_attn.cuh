@@ -156,15 +156,32 @@ __device__ __forceinline__ float largest_scale(const PAttnPlan &p, const float *
 }
 
 // Whether a scale of those spans lies too far (log2) above the largest that this lane's row sees: of
-// `some`, the largest of the spans, and `all`, of keys that every row sees (bits).  Of scales of zero
-// only, nothing is lost.
+// `some`, the largest of the spans, and `all`, of the nearest keys that every row sees (bits); if
+// those are too small, of as many more as it takes, in other splits too.  Of scales of zero only,
+// nothing is lost.  The tile's first row is r0.
 __device__ __forceinline__ bool too_far(uint32_t some, float seen, int limit) {
     return (int)(some >> 23) > (int)(__float_as_uint(seen) >> 23) + limit;
 }
-static __device__ __noinline__ bool sees_too_little(const PAttnPlan &p, const float *scales, int b, int h, const KeySpans &sp, int i,
+static __device__ __noinline__ bool sees_too_little(const PAttnPlan &p, const float *scales, int b, int h, const KeySpans &sp, int r0, int i,
                                                     uint32_t some, uint32_t all, int limit) {
     const SeqInfo s = seq_info(p, b, false);
-    const float v = largest_scale(p, scales, b, h, sp, seen_lo(p, s, i), seen_hi(p, s, i), __uint_as_float(all));
+    float v = largest_scale(p, scales, b, h, sp, seen_lo(p, s, i), seen_hi(p, s, i), __uint_as_float(all));
+    if (__any_sync(0xffffffffu, v > 0.f && too_far(some, v, limit))) {
+        const int shift = 31 - __clz(p.page);
+        const int all_lo = seen_lo(p, s, token_of(p, min(s.qn * p.G, r0 + p.unit) - 1)), all_hi = seen_hi(p, s, token_of(p, r0));
+        uint32_t most = 0;
+        for (int x = all_hi; x > all_lo && too_far(some, __uint_as_float(most), limit); x -= 256) {
+            float m = 0.f;
+            for (int key = x - 1 - (threadIdx.x & 31); key >= max(all_lo, x - 256); key -= 32) {
+                bool bad = false;
+                const float y = __ldg(scales + ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1)));
+                m = fmaxf(m, is_finite(y) ? fabsf(y) : 0.f);
+            }
+            __syncwarp();
+            most = max(most, __reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+        }
+        v = fmaxf(v, __uint_as_float(most));
+    }
     return v > 0.f && too_far(some, v, limit);
 }
 
