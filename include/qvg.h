@@ -335,7 +335,8 @@ qvg_status qvg_attention(const qvg_attention_params *params, const void *Q,
  * A page holds page_tokens consecutive tokens of one sequence, all heads.  Arrays
  * (row-major, caller-owned device memory, 16-byte aligned):
  *   k, v              [n_pages][n_heads][page_tokens][128] of the page format
- *   k_scale, v_scale  float [n_pages][n_heads][page_tokens], 8-bit formats only
+ *   k_scale, v_scale  float [n_pages][n_heads][page_tokens], 8-bit and 4-bit formats only
+ *   k_group, v_group  4-bit formats only, see there
  * A slot is page * page_tokens + row.  Token t of sequence b is row t % page_tokens of page
  * page_table[b][t / page_tokens]; page_table is int32 [n_seqs][max_pages], and entries that
  * no token below the sequence's length falls in are never read.
@@ -353,14 +354,30 @@ typedef enum {
     QVG_PAGE_F16 = 0,
     QVG_PAGE_BF16 = 1,
     QVG_PAGE_E4M3 = 2,
-    QVG_PAGE_INT8 = 3
+    QVG_PAGE_INT8 = 3,
+    QVG_PAGE_E2M1 = 8, /* 4 to 7 are refused */
+    QVG_PAGE_INT4 = 9
 } qvg_page_format;
 
+/* The 4-bit formats hold codes of 4 bits (E2M1: sign, two bits of exponent, one of mantissa,
+ * largest code 6; INT4: two's complement, largest 7), a scale for each group of 16 channels
+ * and one for the row.  With a as above, a_g = max_k |x_k| over a group and TOP the largest code:
+ *   s = a / (64 TOP) in fp32,  t_g = E4M3(64 a_g / a), at most 64,
+ *   code = x * 64 TOP / (a t_g) rounded to the format, to nearest even, at most TOP,
+ * and the stored value is s * t_g * code.  Quotients are rounded correctly, so that values
+ * halfway between two codes go to the even one.  Rows of zeros, tiny rows and rows that are not
+ * finite as in 8 bits.
+ *   k, v              two codes a byte, channel 2i in the low four bits: [..][64] bytes
+ *   k_group, v_group  E4M3 [n_pages][n_heads][page_tokens][8], group g channels 16g .. 16g + 15
+ * Group scales that a caller writes itself may be any E4M3 number up to 64 in magnitude, or NaN;
+ * larger ones leave the attention over rows that see them unspecified. */
 typedef struct {
     void *k;
     void *v;
     float *k_scale; /* NULL for the 16-bit formats */
     float *v_scale;
+    uint8_t *k_group; /* read for the 4-bit formats only */
+    uint8_t *v_group;
 } qvg_pages;
 
 /* Rotary positions.  Pair p of a row, 0 <= p < rot_dim / 2, is turned by the angle
@@ -448,7 +465,7 @@ typedef struct {
     int32_t d;           /* 128 */
     int32_t page_tokens;
     int32_t format;      /* QVG_PAGE_F16 with fp16 queries, QVG_PAGE_BF16 with bf16 queries,
-                            or an 8-bit format */
+                            or an 8-bit or 4-bit format */
     int32_t q_dtype;     /* QVG_F16 or QVG_BF16 */
     int32_t out_dtype;   /* qvg_dtype of O */
     int64_t n_pages;

@@ -231,7 +231,11 @@ def attention(Q: torch.Tensor, k_cache: CompressedKV, v_cache: CompressedKV | No
 # ------------------------------------------------------------------------------------
 
 _PAGE_FORMAT = {torch.float16: _c.QVG_PAGE_F16, torch.bfloat16: _c.QVG_PAGE_BF16,
-                torch.float8_e4m3fn: _c.QVG_PAGE_E4M3, torch.int8: _c.QVG_PAGE_INT8}
+                torch.float8_e4m3fn: _c.QVG_PAGE_E4M3, torch.int8: _c.QVG_PAGE_INT8,
+                torch.float4_e2m1fn_x2: _c.QVG_PAGE_E2M1, torch.uint8: _c.QVG_PAGE_INT4}
+_WIDE = (torch.float16, torch.bfloat16)
+_FOUR = (torch.float4_e2m1fn_x2, torch.uint8)  # two codes an element
+GROUP = 16  # channels that share a scale in a 4-bit row
 
 
 def _need(ok, what):
@@ -408,55 +412,72 @@ def rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, *,
 @dataclass(frozen=True)
 class PagedKV:
     """Pages of recent keys and values (layouts as in include/qvg.h).  The type of ``k`` and
-    ``v`` is the page format: fp16, bf16, float8_e4m3fn or int8; the last two have scales."""
-    k: torch.Tensor                        # [pages][heads][page_tokens][128]
+    ``v`` is the page format: fp16, bf16, float8_e4m3fn or int8, or, with two 4-bit codes an
+    element, float4_e2m1fn_x2 (E2M1) or uint8 (INT4).  8-bit and 4-bit pages have a scale for
+    each row, 4-bit ones another for each group of 16 channels."""
+    k: torch.Tensor                        # [pages][heads][page_tokens][128], 4 bits: [..][64]
     v: torch.Tensor
     k_scale: torch.Tensor | None = None    # fp32 [pages][heads][page_tokens]
     v_scale: torch.Tensor | None = None
+    k_group: torch.Tensor | None = None    # float8_e4m3fn [pages][heads][page_tokens][8]
+    v_group: torch.Tensor | None = None
 
     def __post_init__(self):
         shape = self.k.shape
-        _need(len(shape) == 4 and shape[3] == D and self.k.dtype in _PAGE_FORMAT,
-              "pages are [pages][heads][page_tokens][128] of fp16, bf16, float8_e4m3fn or int8")
+        four = self.k.dtype in _FOUR
+        _need(len(shape) == 4 and shape[3] == (D // 2 if four else D) and self.k.dtype in _PAGE_FORMAT,
+              "pages are [pages][heads][page_tokens][128] of fp16, bf16, float8_e4m3fn or int8, "
+              "or [pages][heads][page_tokens][64] of float4_e2m1fn_x2 or uint8 (INT4)")
         dev = self.k.get_device()
         for t in (self.k, self.v):
             _index(t, self.k.dtype, shape, "k and v")
             _need(t.get_device() == dev, "k and v must be on one GPU")
-        wide = self.k.dtype in (torch.float16, torch.bfloat16)
         for t in (self.k_scale, self.v_scale):
-            if wide:
+            if self.k.dtype in _WIDE:
                 _need(t is None, "16-bit pages have no scales")
             else:
-                _need(t is not None, "8-bit pages need k_scale and v_scale")
+                _need(t is not None, "8-bit and 4-bit pages need k_scale and v_scale")
                 _index(t, torch.float32, shape[:3], "scales", dev)
+        for t in (self.k_group, self.v_group):
+            if four:
+                _need(t is not None, "4-bit pages need k_group and v_group")
+                _index(t, torch.float8_e4m3fn, (*shape[:3], D // GROUP), "group scales", dev)
+            else:
+                _need(t is None, "only 4-bit pages have group scales")
         for name, value in (("gpu", dev), ("n_pages", shape[0]), ("heads", shape[1]), ("page_tokens", shape[2]),
                             ("format", _PAGE_FORMAT[self.k.dtype]),
                             ("_buffers", _c.qvg_pages(self.k.data_ptr(), self.v.data_ptr(),
-                                                      _ptr(self.k_scale), _ptr(self.v_scale)))):
+                                                      _ptr(self.k_scale), _ptr(self.v_scale),
+                                                      _ptr(self.k_group), _ptr(self.v_group)))):
             object.__setattr__(self, name, value)
 
     def __reduce__(self):  # a copy describes its own tensors' memory
-        return PagedKV, (self.k, self.v, self.k_scale, self.v_scale)
+        return PagedKV, (self.k, self.v, self.k_scale, self.v_scale, self.k_group, self.v_group)
 
     def buffers(self) -> _c.qvg_pages:
         return self._buffers
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
-                   (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
+                   (self.k, self.v, self.k_scale, self.v_scale, self.k_group, self.v_group) if t is not None)
 
 
 def allocate_pages(n_pages: int, heads: int, page_tokens: int = 64, dtype=torch.bfloat16,
                    device="cuda") -> PagedKV:
     """An empty paged cache; ``dtype`` picks the page format."""
-    _need(dtype in _PAGE_FORMAT, "pages are fp16, bf16, float8_e4m3fn or int8")
+    _need(dtype in _PAGE_FORMAT, "pages are fp16, bf16, float8_e4m3fn, int8, float4_e2m1fn_x2 or uint8 (INT4)")
     shape = (n_pages, heads, page_tokens)
-    wide = dtype in (torch.float16, torch.bfloat16)
+    four = dtype in _FOUR
+
+    def codes():
+        return torch.empty((*shape, D // 2 if four else D), dtype=dtype, device=device)
 
     def scales():
-        return None if wide else torch.empty(shape, dtype=torch.float32, device=device)
-    return PagedKV(torch.empty((*shape, D), dtype=dtype, device=device),
-                   torch.empty((*shape, D), dtype=dtype, device=device), scales(), scales())
+        return None if dtype in _WIDE else torch.empty(shape, dtype=torch.float32, device=device)
+
+    def groups():
+        return torch.empty((*shape, D // GROUP), dtype=torch.float8_e4m3fn, device=device) if four else None
+    return PagedKV(codes(), codes(), scales(), scales(), groups(), groups())
 
 
 def page_write(kv: PagedKV, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, *,

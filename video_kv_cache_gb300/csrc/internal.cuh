@@ -410,7 +410,11 @@ cudaError_t launch_attention(const APlan &p, cudaStream_t st);
 // ------------------------------------------------------------------------------------
 // The paged cache
 // ------------------------------------------------------------------------------------
-enum : int { PF_F16 = 0, PF_BF16 = 1, PF_E4M3 = 2, PF_INT8 = 3 };
+enum : int { PF_F16 = 0, PF_BF16 = 1, PF_E4M3 = 2, PF_INT8 = 3, PF_E2M1 = 8, PF_INT4 = 9 };
+__host__ __device__ constexpr bool wide_format(int fmt) { return fmt == PF_F16 || fmt == PF_BF16; }
+__host__ __device__ constexpr bool four_bits(int fmt) { return fmt == PF_E2M1 || fmt == PF_INT4; }
+constexpr int kGroup = 16;               // channels that share a scale in a 4-bit row
+constexpr int kGroups = 128 / kGroup;
 
 struct Rotary {
     int rot, interleaved;  // rot = 0: no turn
@@ -441,8 +445,10 @@ struct PWritePlan {
     const int64_t *slots;
     void *k, *v;
     float *ks, *vs;
+    uint8_t *kg, *vg;  // 4-bit pages: the groups' scales
     uint32_t *status;
 };
+cudaError_t launch_page_write4(const PWritePlan &p, cudaStream_t st);
 cudaError_t launch_page_write(const PWritePlan &p, cudaStream_t st);
 
 struct PReadPlan {
@@ -450,10 +456,12 @@ struct PReadPlan {
     int64_t n_pages, first, count, xs, xt;
     const void *k, *v;
     const float *ks, *vs;
+    const uint8_t *kg, *vg;
     const int32_t *table, *lens;
     void *X;
     uint32_t *status;
 };
+cudaError_t launch_page_read4(const PReadPlan &p, cudaStream_t st);
 cudaError_t launch_page_read(const PReadPlan &p, cudaStream_t st);
 
 struct PAttnPlan {
@@ -465,6 +473,7 @@ struct PAttnPlan {
     int64_t qt, qh, ot, oh;
     const void *Q, *k, *v;
     const float *ks, *vs;
+    const uint8_t *kg, *vg;  // 4-bit pages: the groups' scales
     const int32_t *table, *lens, *cu;
     void *O;
     float *lse;

@@ -37,8 +37,6 @@
 namespace qvg {
 
 namespace {
-constexpr int kRowsWarps = 4;              // warps that compute
-constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
 constexpr int kRowsShares = 152 * 2;       // CTAs that run at once
 constexpr int kRowsPad = 132;              // padded row of the join, floats
 constexpr int kRowsCluster = 8;            // most splits joined by a cluster
@@ -47,14 +45,18 @@ constexpr int kRowsShare = 4;              // stages of a share, at least
 // RT: groups of eight query rows, one or two.
 template <int FMT, int RT>
 struct RowsShape {
-    static constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
+    static constexpr bool WIDE = wide_format(FMT), FOUR = four_bits(FMT);
+    static constexpr int WARPS = FOUR && RT == 1 ? 8 : 4;  // that compute
+    static constexpr int THREADS = 32 * (WARPS + 1);
     // 16-key tiles that a warp takes at a time: widening codes is a chain of short
     // instructions, which needs more of them side by side than feeding 16-bit rows does
-    static constexpr int KT = WIDE ? 1 : 2;
-    static constexpr int KEYS = 16 * KT * kRowsWarps;              // of a stage
+    static constexpr int KT = WIDE || (FOUR && RT == 1) ? 1 : 2;
+    static constexpr int KEYS = 16 * KT * WARPS;                   // of a stage
     static constexpr int CTAS = 2;    // an SM
-    static constexpr int STAGES = 3;  // 32 KB each; two stages and three CTAs, or smaller stages, are slower
-    static constexpr uint32_t TILE = KEYS * kD * (WIDE ? 2 : 1);   // bytes of its keys, or values
+    // 8 and 16 bits: 32 KB each; two stages and three CTAs, or smaller stages, are slower
+    static constexpr int STAGES = FOUR ? 5 : 3;
+    static constexpr int ROWB = WIDE ? 2 * kD : FOUR ? kD / 2 : kD;  // bytes of a cached row
+    static constexpr uint32_t TILE = KEYS * ROWB;                  // bytes of its keys, or values
 };
 // SHARES: see PAttnPlan::stream.
 template <int FMT, int RT, bool SHARES>
@@ -62,9 +64,11 @@ struct RowsShared {
     using T = RowsShape<FMT, RT>;
     __align__(16) float ks[T::STAGES][T::WIDE ? 4 : T::KEYS];
     __align__(16) float vs[T::STAGES][T::WIDE ? 4 : T::KEYS];
+    __align__(16) uint8_t kg[T::STAGES][T::FOUR ? T::KEYS * kGroups : 16];
+    __align__(16) uint8_t vg[T::STAGES][T::FOUR ? T::KEYS * kGroups : 16];
     __align__(16) float o[SHARES ? 8 * RT : 1][kRowsPad];  // where the warps' results are joined
     uint64_t full[T::STAGES], empty[T::STAGES];
-    float m[kRowsWarps][8 * RT], l[kRowsWarps][8 * RT];
+    float m[T::WARPS][8 * RT], l[T::WARPS][8 * RT];
     float2 ml[8 * RT];  // this split's maxima and sums, for the cluster
     int abort;
     int b0, share;              // the sequence that this CTA's share starts in,
@@ -75,7 +79,7 @@ constexpr size_t rows_smem() {
     using T = RowsShape<FMT, RT>;
     constexpr size_t bytes = T::STAGES * 2 * T::TILE + sizeof(RowsShared<FMT, RT, SHARES>);
     static_assert(T::CTAS * (bytes + 1024) <= 228 * 1024, "CTAs of an SM");
-    static_assert((kRowsWarps + 1) * 8 * RT * kRowsPad * 4 <= T::STAGES * 2 * T::TILE, "join");
+    static_assert((T::WARPS + 1) * 8 * RT * kRowsPad * 4 <= T::STAGES * 2 * T::TILE, "join");
     return bytes;
 }
 
@@ -119,9 +123,10 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
     return v;
 }
 // The warps that compute meet.
+template <int WARPS>
 __device__ __forceinline__ void rows_meet() {
     __syncwarp();
-    asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * kRowsWarps) : "memory");
+    asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
 __device__ __forceinline__ void cluster_meet() {
     __syncwarp();
@@ -151,14 +156,14 @@ __device__ __forceinline__ int rows_stages(const PAttnPlan &p, const SeqInfo &sq
 // type.  SHARES: grid (shares), each an equal part of all heads' stages in a row; else grid
 // (splits, key/value heads, sequences), joined: the splits are a cluster.
 template <bool QB, int FMT, int RT, bool SHARES>
-__global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
+__global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT>::CTAS)
     k_page_attn_rows(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PAttnPlan p, int joined) {
     pdl_begin();
     using T = RowsShape<FMT, RT>;
-    constexpr bool WIDE = T::WIDE;
-    constexpr bool PVB = WIDE && QB;            // type of all operands; 8-bit pages: fp16
-    constexpr int ROWB = WIDE ? 2 * kD : kD;    // bytes of a cached row
+    constexpr bool WIDE = T::WIDE, FOUR = T::FOUR;
+    constexpr bool PVB = WIDE && QB;            // type of all operands; 8-bit and 4-bit pages: fp16
+    constexpr int ROWB = T::ROWB, WARPS = T::WARPS;
     constexpr int NCH = ROWB / 64;              // 16-byte chunks of a row per lane
     constexpr int STAGES = T::STAGES, KT = T::KT, KEYS = T::KEYS, ROWS = 8 * RT;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
             mbar_init(smem_u32(&sh.full[s]), 1);
-            mbar_init(smem_u32(&sh.empty[s]), kRowsWarps);
+            mbar_init(smem_u32(&sh.empty[s]), WARPS);
         }
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
         }
     };
 
-    if (warp == kRowsWarps) {
+    if (warp == WARPS) {
         // -------------------------------------------------------------------- TMA loads
         const int box = min(p.page, KEYS), boxes = KEYS / box;
         bool bad = false, ok = true;
@@ -288,18 +293,22 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                 ok = !__any_sync(0xffffffffu, !ok);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&sh.full[s]), count = __popc(__ballot_sync(0xffffffffu, in_sight(k0)));
-                if (lane == 0) mbar_expect_tx(bar, count * box * 2 * (ROWB + (WIDE ? 0 : 4)));
+                if (lane == 0) mbar_expect_tx(bar, count * box * 2 * (ROWB + (WIDE ? 0 : 4) + (FOUR ? kGroups : 0)));
                 __syncwarp();
                 if (in_sight(k0)) {
-                    const uint32_t at = smem_u32(sm) + s * 2 * T::TILE + lane * box * 128;
-                    tma_load_2d(at, &tmK, 0, row, bar);
-                    tma_load_2d(at + T::TILE, &tmV, 0, row, bar);
+                    const uint32_t at = smem_u32(sm) + s * 2 * T::TILE + lane * box * (FOUR ? 64 : 128);
+                    tma_load_2d(at, &tmK, 0, FOUR ? row / 2 : row, bar);
+                    tma_load_2d(at + T::TILE, &tmV, 0, FOUR ? row / 2 : row, bar);
                     if constexpr (WIDE) {
                         tma_load_2d(at + T::TILE / 2, &tmK, 64, row, bar);
                         tma_load_2d(at + T::TILE + T::TILE / 2, &tmV, 64, row, bar);
                     } else {
                         bulk_g2s(smem_u32(&sh.ks[s][lane * box]), p.ks + row, box * 4, bar);
                         bulk_g2s(smem_u32(&sh.vs[s][lane * box]), p.vs + row, box * 4, bar);
+                        if constexpr (FOUR) {
+                            bulk_g2s(smem_u32(&sh.kg[s][lane * box * kGroups]), p.kg + (int64_t)row * kGroups, box * kGroups, bar);
+                            bulk_g2s(smem_u32(&sh.vg[s][lane * box * kGroups]), p.vg + (int64_t)row * kGroups, box * kGroups, bar);
+                        }
                     }
                 }
                 issued = it + 1;
@@ -346,8 +355,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                 uint4 w[4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {  // 8 channels: two steps
-                    const int ch = WIDE ? (j * 4 + q) * 8 : ((j >> 1) * 4 + q) * 16 + (j & 1) * 8;
+                    const int ch = WIDE ? (j * 4 + q) * 8 : FOUR ? 32 * q + 8 * j : ((j >> 1) * 4 + q) * 16 + (j & 1) * 8;
                     w[j] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(src + ch)) : make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (FOUR) w[j] = in_pair_order<FMT>(w[j]);
                 }
                 float mul = 1.f;
                 if constexpr (!WIDE && QB) {
@@ -382,8 +392,14 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
 
             // chunk c of row r of a swizzled tile (16 bits: two halves of 128-byte rows)
             auto chunk = [](const unsigned char *tile, int r, int c) {
+                // (4 bits: lines of two rows)
+                if constexpr (FOUR) return *reinterpret_cast<const uint4 *>(tile + (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r >> 1 & 7)) << 4));
                 return *reinterpret_cast<const uint4 *>(tile + (c >> 3) * (T::TILE / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
             };
+            // The key that the scores' rows g + 8 e stand for, of 16.  4 bits: such that a lane's values
+            // are those of keys 4q .. 4q + 3, whose places in their lines are on different banks for the
+            // lanes that read together.
+            auto key_row = [&](int e) { return FOUR ? 4 * (g >> 1) + (g & 1) + 2 * e : g + 8 * e; };
             // (a warp that gives up a wait keeps meeting the others)
             for (int j = 0; ok && j < n; j++) {
                 const int it = done + j, st = it % STAGES;
@@ -399,8 +415,29 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                     for (int c = 0; c < NCH; c++) {
 #pragma unroll
                         for (int z = 0; z < KT; z++) {
-                            const uint4 ka = chunk(kt, w0 + z * 16 + g, c * 4 + q), kb = chunk(kt, w0 + z * 16 + g + 8, c * 4 + q);
-                            if constexpr (WIDE) {
+                            const int ra = w0 + z * 16 + key_row(0), rb = w0 + z * 16 + key_row(1);
+                            const uint4 ka = chunk(kt, ra, c * 4 + q), kb = chunk(kt, rb, c * 4 + q);
+                            if constexpr (FOUR) {
+                                // two groups of channels a lane
+                                const uint32_t ta = group_pair(*reinterpret_cast<const uint16_t *>(&sh.kg[st][ra * kGroups + 2 * q]));
+                                const uint32_t tb = group_pair(*reinterpret_cast<const uint16_t *>(&sh.kg[st][rb * kGroups + 2 * q]));
+#pragma unroll
+                                for (int x = 0; x < 2; x++) {
+                                    const GroupScale<FMT> fa(__byte_perm(ta, 0u, x ? 0x3232 : 0x1010)), fb(__byte_perm(tb, 0u, x ? 0x3232 : 0x1010));
+#pragma unroll
+                                    for (int w = 2 * x; w < 2 * x + 2; w++) {
+                                        uint32_t ha[4], hb[4];
+                                        widen4<FMT>(word_of(ka, w), fa, ha);
+                                        widen4<FMT>(word_of(kb, w), fb, hb);
+                                        const uint32_t a0[4] = {ha[0], hb[0], ha[1], hb[1]}, a1[4] = {ha[2], hb[2], ha[3], hb[3]};
+#pragma unroll
+                                        for (int y = 0; y < RT; y++) {
+                                            mma16816<false>(s[z][y], a0, qb[y][2 * w][0], qb[y][2 * w][1]);
+                                            mma16816<false>(s[z][y], a1, qb[y][2 * w + 1][0], qb[y][2 * w + 1][1]);
+                                        }
+                                    }
+                                }
+                            } else if constexpr (WIDE) {
                                 const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
 #pragma unroll
                                 for (int y = 0; y < RT; y++) {
@@ -427,8 +464,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                         if constexpr (!WIDE) {
 #pragma unroll
                             for (int e = 0; e < 2; e++) {
-                                k2[e] = sh.ks[st][w0 + 16 * z + 8 * e + g];
-                                vsc[z][e] = sh.vs[st][w0 + 16 * z + 8 * e + g];
+                                k2[e] = sh.ks[st][w0 + 16 * z + key_row(e)];
+                                vsc[z][e] = sh.vs[st][w0 + 16 * z + key_row(e)];
                             }
                         }
 #pragma unroll
@@ -443,7 +480,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                             for (int y = 0; y < RT; y++)
 #pragma unroll
                                 for (int e = 0; e < 4; e++) {
-                                    const int key = t0 + 16 * z + 8 * (e >> 1) + g;
+                                    const int key = t0 + 16 * z + key_row(e >> 1);
                                     if (key < row_lo[y][e & 1] || key >= row_hi[y][e & 1]) s[z][y][e] = -INFINITY;
                                 }
                         }
@@ -537,49 +574,89 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                     }
 #pragma unroll
                     for (int z = 0; z < KT; z++) {
-                        uint4 vr[4][NCH / 2];  // keys 2q, 2q + 1, 2q + 8, 2q + 9
+                        if constexpr (FOUR) {
+                            // keys 4q .. 4q + 3 (the product's 2q, 2q + 1, 2q + 8, 2q + 9), channels of group g
+                            uint2 vr[4];
+                            uint32_t tg[4];
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const int at = 16 * z + 2 * q + (k & 1) + (k >> 1) * 8;
-#pragma unroll
-                            for (int c = 0; c < NCH / 2; c++) {
-                                vr[k][c] = chunk(vt, w0 + at, c * 8 + g);
-                                // values that no row sees may hold anything
-                                if (edge && (t0 + at < lo || t0 + at >= hi)) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int k = 0; k < 4; k++) {
+                                const int at = 16 * z + 4 * q + k, r = w0 + at;
+                                vr[k] = *reinterpret_cast<const uint2 *>(
+                                    vt + (r >> 1) * 128 + ((((r & 1) * 4 + (g >> 1)) ^ (r >> 1 & 7)) << 4) + (g & 1) * 8);
+                                tg[k] = sh.vg[st][r * kGroups + g];
+                                // values that no row sees may hold anything: their scale is 0
+                                if (edge && (t0 + at < lo || t0 + at >= hi)) tg[k] = 0u;
                             }
-                        }
-                        if constexpr (WIDE) {
+                            const GroupScale<FMT> f0(group_pair(tg[0] | tg[1] << 8)), f1(group_pair(tg[2] | tg[3] << 8));
+                            // pairs of two keys' codes of a channel
+                            auto pairs = [&](uint32_t v0, uint32_t v1, const GroupScale<FMT> &f, uint32_t c[8]) {
+                                uint32_t h[4];
+                                if constexpr (FMT == PF_E2M1) {
+                                    widen4<FMT>((v0 & 0x0F0F0F0Fu) | ((v1 << 4) & 0xF0F0F0F0u), f, h);
+                                    c[0] = h[0]; c[2] = h[1]; c[4] = h[2]; c[6] = h[3];
+                                    widen4<FMT>(((v0 >> 4) & 0x0F0F0F0Fu) | (v1 & 0xF0F0F0F0u), f, h);
+                                    c[1] = h[0]; c[3] = h[1]; c[5] = h[2]; c[7] = h[3];
+                                } else {
+                                    widen4<FMT>(__byte_perm(v0, v1, 0x5410), f, c);
+                                    widen4<FMT>(__byte_perm(v0, v1, 0x7632), f, c + 4);
+                                }
+                            };
+                            uint32_t a0[8], a1[8], a2[8], a3[8];  // first / last eight channels of the keys' pairs
+                            pairs(vr[0].x, vr[1].x, f0, a0);
+                            pairs(vr[0].y, vr[1].y, f0, a1);
+                            pairs(vr[2].x, vr[3].x, f1, a2);
+                            pairs(vr[2].y, vr[3].y, f1, a3);
 #pragma unroll
                             for (int t = 0; t < 8; t++) {
-                                const int w = t >> 1, sel = t & 1 ? 0x7632 : 0x5410;
-                                const uint32_t a[4] = {__byte_perm(word_of(vr[0][0], w), word_of(vr[1][0], w), sel),
-                                                       __byte_perm(word_of(vr[0][1], w), word_of(vr[1][1], w), sel),
-                                                       __byte_perm(word_of(vr[2][0], w), word_of(vr[3][0], w), sel),
-                                                       __byte_perm(word_of(vr[2][1], w), word_of(vr[3][1], w), sel)};
+                                const uint32_t a[4] = {a0[t], a1[t], a2[t], a3[t]};
 #pragma unroll
-                                for (int y = 0; y < RT; y++) mma16816<PVB>(o[y][t], a, pb[z][y][0], pb[z][y][1]);
+                                for (int y = 0; y < RT; y++) mma16816<false>(o[y][t], a, pb[z][y][0], pb[z][y][1]);
                             }
                         } else {
-#pragma unroll
-                            for (int w = 0; w < 2; w++) {
-                                // the codes of two keys interleaved, then widened pair by pair:
-                                // channels 4w .. 4w + 3 of the first and of the last eight
-                                uint2 a[2][2][2];  // [first / last eight][keys 2q.. / 2q + 8..][channels 0, 1 / 2, 3]
-#pragma unroll
-                                for (int e = 0; e < 2; e++)
-#pragma unroll
-                                    for (int k = 0; k < 2; k++) {
-                                        const uint32_t v0 = word_of(vr[2 * k][0], w + 2 * e), v1 = word_of(vr[2 * k + 1][0], w + 2 * e);
-                                        a[e][k][0] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x5140));
-                                        a[e][k][1] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x7362));
+                            uint4 vr[4][FOUR ? 1 : NCH / 2];  // keys 2q, 2q + 1, 2q + 8, 2q + 9
+    #pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const int at = 16 * z + 2 * q + (k & 1) + (k >> 1) * 8;
+    #pragma unroll
+                                for (int c = 0; c < NCH / 2; c++) {
+                                    vr[k][c] = chunk(vt, w0 + at, c * 8 + g);
+                                    // values that no row sees may hold anything
+                                    if (edge && (t0 + at < lo || t0 + at >= hi)) vr[k][c] = make_uint4(0u, 0u, 0u, 0u);
+                                }
+                            }
+                            if constexpr (WIDE) {
+    #pragma unroll
+                                for (int t = 0; t < 8; t++) {
+                                    const int w = t >> 1, sel = t & 1 ? 0x7632 : 0x5410;
+                                    const uint32_t a[4] = {__byte_perm(word_of(vr[0][0], w), word_of(vr[1][0], w), sel),
+                                                           __byte_perm(word_of(vr[0][1], w), word_of(vr[1][1], w), sel),
+                                                           __byte_perm(word_of(vr[2][0], w), word_of(vr[3][0], w), sel),
+                                                           __byte_perm(word_of(vr[2][1], w), word_of(vr[3][1], w), sel)};
+    #pragma unroll
+                                    for (int y = 0; y < RT; y++) mma16816<PVB>(o[y][t], a, pb[z][y][0], pb[z][y][1]);
+                                }
+                            } else {
+    #pragma unroll
+                                for (int w = 0; w < 2; w++) {
+                                    // the codes of two keys interleaved, then widened pair by pair:
+                                    // channels 4w .. 4w + 3 of the first and of the last eight
+                                    uint2 a[2][2][2];  // [first / last eight][keys 2q.. / 2q + 8..][channels 0, 1 / 2, 3]
+    #pragma unroll
+                                    for (int e = 0; e < 2; e++)
+    #pragma unroll
+                                        for (int k = 0; k < 2; k++) {
+                                            const uint32_t v0 = word_of(vr[2 * k][0], w + 2 * e), v1 = word_of(vr[2 * k + 1][0], w + 2 * e);
+                                            a[e][k][0] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x5140));
+                                            a[e][k][1] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x7362));
+                                        }
+    #pragma unroll
+                                    for (int t = 0; t < 4; t++) {
+                                        const int x = t >> 1;
+                                        const uint32_t f[4] = {t & 1 ? a[0][0][x].y : a[0][0][x].x, t & 1 ? a[1][0][x].y : a[1][0][x].x,
+                                                               t & 1 ? a[0][1][x].y : a[0][1][x].x, t & 1 ? a[1][1][x].y : a[1][1][x].x};
+    #pragma unroll
+                                        for (int y = 0; y < RT; y++) mma16816<false>(o[y][4 * w + t], f, pb[z][y][0], pb[z][y][1]);
                                     }
-#pragma unroll
-                                for (int t = 0; t < 4; t++) {
-                                    const int x = t >> 1;
-                                    const uint32_t f[4] = {t & 1 ? a[0][0][x].y : a[0][0][x].x, t & 1 ? a[1][0][x].y : a[1][0][x].x,
-                                                           t & 1 ? a[0][1][x].y : a[0][1][x].x, t & 1 ? a[1][1][x].y : a[1][1][x].x};
-#pragma unroll
-                                    for (int y = 0; y < RT; y++) mma16816<false>(o[y][4 * w + t], f, pb[z][y][0], pb[z][y][1]);
                                 }
                             }
                         }
@@ -593,7 +670,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             // join the warps relative to the largest of their maxima: through the ring, which is
             // through with its keys, or, where the next item's are on their way, one after another in
             // a place of its own
-            if constexpr (!SHARES) rows_meet();
+            if constexpr (!SHARES) rows_meet<WARPS>();
 #pragma unroll
             for (int y = 0; y < RT; y++)
 #pragma unroll
@@ -616,7 +693,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                         const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp[y][x] - 8) << 23);
                         float f = 1.f;
                         if (relative) {
-                            const float top = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+                            float top = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+#pragma unroll
+                            for (int w = 4; w < WARPS; w++) top = fmaxf(top, sh.m[w][r]);
                             f = fast_exp2(m[y][x] - exp_base(top));
                         }
 #pragma unroll
@@ -635,15 +714,15 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                     }
             };
             if constexpr (SHARES) {
-                rows_meet();
+                rows_meet<WARPS>();
 #pragma unroll 1
-                for (int w = 0; w < kRowsWarps; w++) {
+                for (int w = 0; w < WARPS; w++) {
                     if (warp == w) put(sh.o, w > 0, true);
-                    rows_meet();
+                    rows_meet<WARPS>();
                 }
             } else {
                 put(s_o[warp], false, false);
-                rows_meet();
+                rows_meet<WARPS>();
             }
             // eight lanes a row, 16 channels each (in runs of four, so that the lanes' reads and
             // writes are next to one another); the other warps only keep the barriers
@@ -652,10 +731,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             const bool mine = r < ROWS;
             if (mine) {
 #pragma unroll
-                for (int w = 0; w < kRowsWarps; w++) M = fmaxf(M, sh.m[w][r]);
+                for (int w = 0; w < WARPS; w++) M = fmaxf(M, sh.m[w][r]);
                 const float base = exp_base(M);
 #pragma unroll
-                for (int w = 0; w < kRowsWarps; w++) {
+                for (int w = 0; w < WARPS; w++) {
                     const float f = fast_exp2(sh.m[w][r] - base);
                     L += f * sh.l[w][r];
 #pragma unroll
@@ -670,7 +749,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
             }
             const int row_i = token_of(p, min(r, rows - 1)), hq = h * p.G + min(r, rows - 1) - row_i * p.G;
             bool live = mine && r < rows;
-            if constexpr (SHARES) rows_meet();  // the join's rows are read: the next item's may follow
+            if constexpr (SHARES) rows_meet<WARPS>();  // the join's rows are read: the next item's may follow
             if (SHARES ? !item.whole : p.S > 1 && !joined) {
                 if (!live) return;
                 const int64_t cell = (int64_t)blockIdx.z * p.H + blockIdx.y;
@@ -685,7 +764,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                 if (mine) {
 #pragma unroll
                     for (int c = 0; c < 4; c++)
-                        *reinterpret_cast<float4 *>(&s_o[kRowsWarps][r][c * 32 + part * 4]) =
+                        *reinterpret_cast<float4 *>(&s_o[WARPS][r][c * 32 + part * 4]) =
                             make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                     if (part == 0) sh.ml[r] = make_float2(M, L);
                 }
@@ -704,7 +783,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, RT>::CTAS)
                         L += f * ml.y;
 #pragma unroll
                         for (int c = 0; c < 4; c++) {
-                            const float4 y = ld_cluster4(cluster_addr(&s_o[kRowsWarps][r][c * 32 + part * 4], s));
+                            const float4 y = ld_cluster4(cluster_addr(&s_o[WARPS][r][c * 32 + part * 4], s));
                             v[4 * c] += f * y.x;
                             v[4 * c + 1] += f * y.y;
                             v[4 * c + 2] += f * y.z;
@@ -869,7 +948,7 @@ void page_attention_cut(PAttnPlan &p) {
         p.units = 1;
         const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = std::max<int64_t>(kRowsShares / cells, 1);
         int64_t want = std::min<int64_t>(once, 256);
-        const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
+        const bool wide = wide_format(p.fmt);
         if (!wide && once < 4 && cells <= 2 * kRowsShares && cells * p.max_kv >= (int64_t)kRowsShares * 2048) {
             p.stream = 1;
             p.S = 1;
@@ -924,26 +1003,30 @@ cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int joined = p.S > 1 && p.S <= kRowsCluster;
     const dim3 grid = SHARES ? dim3(kRowsShares) : dim3((unsigned)p.S, p.H, p.B);
-    return launch_kernel_cluster(kernel, grid, dim3(kRowsThreads), smem, joined ? p.S : 1, st,
+    return launch_kernel_cluster(kernel, grid, dim3(RowsShape<FMT, RT>::THREADS), smem, joined ? p.S : 1, st,
                                  mk, mv, p, joined);
 }
 
 template <bool QB, int FMT>
 cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
     const bool one = p.max_q * p.G <= 8;
-    if constexpr (FMT == PF_E4M3 || FMT == PF_INT8)
+    if constexpr (!wide_format(FMT))
         if (p.stream) return one ? launch_rows<QB, FMT, 1, true>(p, st) : launch_rows<QB, FMT, 2, true>(p, st);
     return one ? launch_rows<QB, FMT, 1, false>(p, st) : launch_rows<QB, FMT, 2, false>(p, st);
 }
 
 cudaError_t launch_page_attention_rows(const PAttnPlan &p, cudaStream_t st) {
-    if (p.q_dtype == DT_BF16)
-        return p.fmt == PF_E4M3   ? launch_rows<true, PF_E4M3>(p, st)
-               : p.fmt == PF_INT8 ? launch_rows<true, PF_INT8>(p, st)
-                                  : launch_rows<true, PF_BF16>(p, st);
-    return p.fmt == PF_E4M3   ? launch_rows<false, PF_E4M3>(p, st)
-           : p.fmt == PF_INT8 ? launch_rows<false, PF_INT8>(p, st)
-                              : launch_rows<false, PF_F16>(p, st);
+    auto go = [&](auto qb) {
+        constexpr bool QB = decltype(qb)::value;
+        switch (p.fmt) {
+            case PF_E4M3: return launch_rows<QB, PF_E4M3>(p, st);
+            case PF_INT8: return launch_rows<QB, PF_INT8>(p, st);
+            case PF_E2M1: return launch_rows<QB, PF_E2M1>(p, st);
+            case PF_INT4: return launch_rows<QB, PF_INT4>(p, st);
+            default: return launch_rows<QB, QB ? PF_BF16 : PF_F16>(p, st);
+        }
+    };
+    return p.q_dtype == DT_BF16 ? go(std::true_type{}) : go(std::false_type{});
 }
 }  // namespace
 

@@ -63,8 +63,7 @@ constexpr int kTcM = 128;                  // rows of a row tile
 constexpr int kTcN = 128;                  // keys of a key tile
 constexpr uint32_t kHalf = kTcM * 128;     // 64 channels of 128 rows: 16 KB
 constexpr uint32_t kSlot = 2 * kHalf;      // a whole 16-bit tile: 32 KB
-constexpr int kRawKeys = 64;               // keys of a raw tile of 8-bit codes, half a key tile
-constexpr uint32_t kRaw = kRawKeys * kD;   // 8 KB
+constexpr int kRawKeys = 64;               // keys of a raw tile of 8-bit or 4-bit codes, half a key tile
 constexpr int kValueShift = 4, kKeyShift = 6;  // 8-bit values and keys over their references, times 2^this
 // How far (log2) a scale that a row does not see may lie above the largest that it sees before the
 // row is done again.  Values: a weight times a scale over the reference 2^e is rounded by at most
@@ -81,7 +80,9 @@ constexpr float kHugeScore = 8388608.f;
 
 template <int FMT>
 struct TcShape {
-    static constexpr bool WIDE = FMT == PF_F16 || FMT == PF_BF16;
+    static constexpr bool WIDE = wide_format(FMT), FOUR = four_bits(FMT);
+    static constexpr uint32_t RAW = kRawKeys * (FOUR ? kD / 2 : kD);       // bytes of a raw tile's codes: 8 or 4 KB
+    static constexpr uint32_t RAW_GROUPS = FOUR ? kRawKeys * kGroups : 0;  // and of its groups' scales
     static constexpr int SLOTS = WIDE ? 5 : 4;       // ring of 16-bit tiles
     static constexpr int RAWS = 3;                   // ring of raw 8-bit tiles
     // 16 softmax warps; MMA, loads and two idle ones (registers move by groups of four warps);
@@ -92,7 +93,7 @@ struct TcShape {
     // out anew: the groups' sum stays what the launch had
     static constexpr int REGS = WIDE ? 96 : 72, REGS_SOFTMAX = WIDE ? 104 : 80, REGS_REST = WIDE ? 64 : 56;
     static_assert(512 * REGS_SOFTMAX + (THREADS - 512) * REGS_REST <= THREADS * REGS, "register shares");
-    static constexpr uint32_t SMEM_TILES = 2 * kSlot + SLOTS * kSlot + (WIDE ? 0 : RAWS * kRaw);
+    static constexpr uint32_t SMEM_TILES = 2 * kSlot + SLOTS * kSlot + (WIDE ? 0 : RAWS * (RAW + RAW_GROUPS));
 };
 
 // Everything the roles share besides the tiles (the 16-bit formats have no scales).
@@ -272,12 +273,12 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                    const __grid_constant__ PAttnPlan p) {
     pdl_begin();
     using T = TcShape<FMT>;
-    constexpr bool WIDE = T::WIDE;
-    constexpr bool BF = WIDE && QB;  // type of all operands; 8-bit pages: fp16
+    constexpr bool WIDE = T::WIDE, FOUR = T::FOUR;
+    constexpr bool BF = WIDE && QB;  // type of all operands; 8-bit and 4-bit pages: fp16
     constexpr int SLOTS = T::SLOTS;
     constexpr int MMA_WARP = 16, LOAD_WARP = 17, WIDEN_WARP = 20;
     extern __shared__ __align__(1024) unsigned char sm[];
-    unsigned char *sQ = sm, *sKV = sm + 2 * kSlot, *sRaw = sKV + SLOTS * kSlot;
+    unsigned char *sQ = sm, *sKV = sm + 2 * kSlot, *sRaw = sKV + SLOTS * kSlot, *sGroups = sRaw + T::RAWS * T::RAW;
     TcShared<FMT> &sh = *reinterpret_cast<TcShared<FMT> *>(sm + T::SMEM_TILES);
     volatile int *abort_flag = &sh.abort;
 
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 // a value tile at the edge of what is seen, whose outer rows must be zeroed
                 const bool edge = WIDE && value && (((lo - k0) & 15 && lo > k0) || ((hi - k0) & 15 && hi < k0 + kTcN));
                 const uint32_t bar = smem_u32(edge ? &sh.edge : &full);
-                if (lane == 0) mbar_expect_tx(bar, (pages << shift) * (WIDE ? 2u * kD : (uint32_t)kD));
+                if (lane == 0) mbar_expect_tx(bar, (pages << shift) * (WIDE ? 2u * kD : FOUR ? kD / 2 + kGroups : (uint32_t)kD));
                 __syncwarp();
                 if (mine) {
                     const CUtensorMap *map = value ? &tmV : &tmK;
@@ -490,7 +491,11 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         tma_load_2d(dst, map, 0, row, bar);
                         tma_load_2d(dst + kHalf, map, 64, row, bar);
                     } else {
-                        tma_load_2d(smem_u32(sRaw) + slot * kRaw + (((uint32_t)lane << shift) & (kRawKeys - 1)) * kD, map, 0, row, bar);
+                        const uint32_t key = ((uint32_t)lane << shift) & (kRawKeys - 1);
+                        tma_load_2d(smem_u32(sRaw) + slot * T::RAW + key * (T::RAW / kRawKeys), map, 0, FOUR ? row / 2 : row, bar);
+                        if constexpr (FOUR)
+                            bulk_g2s(smem_u32(sGroups) + slot * T::RAW_GROUPS + key * kGroups,
+                                     (value ? p.vg : p.kg) + (int64_t)row * kGroups, (uint32_t)kGroups << shift, bar);
                     }
                 }
                 issued = it + 1;
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     if (used >> k & 1u) mbar_wait_final(smem_u32(&sh.raw_full[k / 3][k % 3]), ~(odd >> k) & 1u);
             }
         } else if (!WIDE && warp >= WIDEN_WARP) {
-            // ---------------------------------------------------------------- 8-bit codes widened
+            // ---------------------------------------------------------------- 8-bit and 4-bit codes widened
             const bool value = warp >= WIDEN_WARP + 4;  // the first four warps: keys, the others: values
             const int shift = 31 - __clz(p.page), x = (threadIdx.x - 32 * WIDEN_WARP) & 127, id = 1 + value;
             const float *scales = value ? p.vs : p.ks;
@@ -543,7 +548,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             // together have eight rows of one chunk, which the swizzle of the raw tile and that
             // of the widened one both spread over all banks
             const int c = (x >> 3) & 7, r8 = x & 7, rb = r8 + ((x >> 6) << 3);
-            const unsigned char *src0 = sRaw + rb * kD + ((c ^ r8) << 4);
+            // (4 bits: 8 bytes, group c of a row; lines of 128 bytes hold two rows)
+            const unsigned char *src0 = FOUR ? sRaw + (rb >> 1) * 128 + ((((rb & 1) * 4 + (c >> 1)) ^ (rb >> 1 & 7)) << 4) + (c & 1) * 8
+                                             : sRaw + rb * kD + ((c ^ r8) << 4);
+            const unsigned char *grp0 = sGroups + rb * kGroups + c;
             unsigned char *dst0 = sKV + (c >> 2) * kHalf + rb * 128;
             const int d0 = ((2 * (c & 3)) ^ r8) << 4, d1 = ((2 * (c & 3) + 1) ^ r8) << 4;
             uint32_t phases = 0;  // of this operand's barriers of the raw tiles, a bit each
@@ -599,18 +607,34 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         ok = wait(sh.raw_full[value][raw], phases >> raw);  // (who gives up here meets the others at the next tile)
                     }
                     phases ^= 1u << raw;
-                    const unsigned char *src = src0 + raw * kRaw;
+                    const unsigned char *src = src0 + raw * T::RAW;
 #pragma unroll
                     for (int v = 0; v < 4; v++) {
                         const int u = 4 * part + v;
-                        uint4 w = *reinterpret_cast<const uint4 *>(src + v * 16 * kD);
-                        if (!whole) {  // what no row sees may hold anything
-                            const int key = k0 + rb + u * 16;
-                            if (key < lo || key >= hi) w = make_uint4(0u, 0u, 0u, 0u);
+                        uint4 a0, a1;
+                        if constexpr (FOUR) {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(src + v * 16 * (kD / 2));
+                            uint32_t t = grp0[raw * T::RAW_GROUPS + v * 16 * kGroups], h[8];
+                            if (!whole) {  // what no row sees may hold anything: its scale is 0
+                                const int key = k0 + rb + u * 16;
+                                if (key < lo || key >= hi) t = 0u;
+                            }
+                            const GroupScale<FMT> f(__byte_perm(group_pair(t), 0u, 0x1010));
+                            widen4<FMT>(w.x, f, h);
+                            widen4<FMT>(w.y, f, h + 4);
+                            a0 = make_uint4(h[0], h[1], h[2], h[3]);
+                            a1 = make_uint4(h[4], h[5], h[6], h[7]);
+                        } else {
+                            uint4 w = *reinterpret_cast<const uint4 *>(src + v * 16 * kD);
+                            if (!whole) {  // what no row sees may hold anything
+                                const int key = k0 + rb + u * 16;
+                                if (key < lo || key >= hi) w = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            const uint2 y0 = codes_to_f16<FMT == PF_E4M3>(w.x), y1 = codes_to_f16<FMT == PF_E4M3>(w.y),
+                                        y2 = codes_to_f16<FMT == PF_E4M3>(w.z), y3 = codes_to_f16<FMT == PF_E4M3>(w.w);
+                            a0 = make_uint4(y0.x, y0.y, y1.x, y1.y);
+                            a1 = make_uint4(y2.x, y2.y, y3.x, y3.y);
                         }
-                        const uint2 y0 = codes_to_f16<FMT == PF_E4M3>(w.x), y1 = codes_to_f16<FMT == PF_E4M3>(w.y),
-                                    y2 = codes_to_f16<FMT == PF_E4M3>(w.z), y3 = codes_to_f16<FMT == PF_E4M3>(w.w);
-                        uint4 a0 = make_uint4(y0.x, y0.y, y1.x, y1.y), a1 = make_uint4(y2.x, y2.y, y3.x, y3.y);
                         if constexpr (FOLD) {
                             const uint2 f = factors[u * 16];
                             a0 = make_uint4(scaled(a0.x, f), scaled(a0.y, f), scaled(a0.z, f), scaled(a0.w, f));
@@ -673,6 +697,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             for (int u = 0; u < EACH; u++) {
                 const int x = threadIdx.x + u * 512, row = x >> 4, c = x & 15;
                 w[u].x ^= flip; w[u].y ^= flip; w[u].z ^= flip; w[u].w ^= flip;
+                if constexpr (FOUR) w[u] = in_pair_order<FMT>(w[u]);
                 if constexpr (!WIDE) {
                     float mul = 1.f;
                     if constexpr (QB) w[u] = normalised_f16(w[u], mul, 16);
@@ -915,6 +940,16 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         o[k] *= inv;
                         if constexpr (FMT != PF_INT8) odd |= !is_finite(o[k]);
                     }
+                    if constexpr (FMT == PF_INT4) {  // columns 2i and 2i + 1 of eight are channels i and i + 4
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            float y[8];
+#pragma unroll
+                            for (int c = 0; c < 8; c++) y[c] = o[k + c];
+#pragma unroll
+                            for (int c = 0; c < 8; c++) o[k + pair_channel<FMT>(c >> 1, c & 1)] = y[c];
+                        }
+                    }
                     if (narrow) {
                         auto pk = [&](int k) {
                             return p.out_dtype == DT_BF16 ? pack_bf16(o[k], o[k + 1]) : pack_f16(o[k], o[k + 1]);
@@ -990,7 +1025,7 @@ cudaError_t launch_tc(const PAttnPlan &p, const CUtensorMap &mk, const CUtensorM
 
 cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
     CUtensorMap maps[2];
-    const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
+    const bool wide = wide_format(p.fmt);
     const int box = wide ? p.page : std::min(p.page, kRawKeys);
     if (!page_map(p, p.k, box, &maps[0]) || !page_map(p, p.v, box, &maps[1])) return cudaErrorInvalidValue;
     const bool fold = !p.lse && p.out_dtype == DT_BF16;
@@ -1000,6 +1035,10 @@ cudaError_t launch_page_attention_tc(const PAttnPlan &p, cudaStream_t st) {
             return fold ? launch_tc<QB, PF_E4M3, true>(p, maps[0], maps[1], st) : launch_tc<QB, PF_E4M3, false>(p, maps[0], maps[1], st);
         if (p.fmt == PF_INT8)
             return fold ? launch_tc<QB, PF_INT8, true>(p, maps[0], maps[1], st) : launch_tc<QB, PF_INT8, false>(p, maps[0], maps[1], st);
+        if (p.fmt == PF_E2M1)
+            return fold ? launch_tc<QB, PF_E2M1, true>(p, maps[0], maps[1], st) : launch_tc<QB, PF_E2M1, false>(p, maps[0], maps[1], st);
+        if (p.fmt == PF_INT4)
+            return fold ? launch_tc<QB, PF_INT4, true>(p, maps[0], maps[1], st) : launch_tc<QB, PF_INT4, false>(p, maps[0], maps[1], st);
         return launch_tc<QB, QB ? PF_BF16 : PF_F16, false>(p, maps[0], maps[1], st);
     };
     return p.q_dtype == DT_BF16 ? go(std::true_type{}) : go(std::false_type{});

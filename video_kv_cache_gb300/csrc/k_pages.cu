@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kWriteThreads, kWriteCtas) k_page_write(PWrite
 }
 
 cudaError_t launch_page_write(const PWritePlan &p, cudaStream_t st) {
+    if (four_bits(p.fmt)) return launch_page_write4(p, st);
     const int64_t units = p.n * ((p.heads + kWriteHeads - 1) / kWriteHeads);
     constexpr int per = kWriteThreads / 16;
     const dim3 grid((unsigned)((units + per - 1) / per));
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(256) k_page_read(PReadPlan p) {
 }
 
 cudaError_t launch_page_read(const PReadPlan &p, cudaStream_t st) {
+    if (four_bits(p.fmt)) return launch_page_read4(p, st);
     const dim3 grid((unsigned)((p.count + kReadTokens - 1) / kReadTokens), 2 * p.heads, p.B);
     auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(256), 0, st, p); };
     auto by_dtype = [&](auto fmt) {

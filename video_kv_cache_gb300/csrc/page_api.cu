@@ -53,14 +53,12 @@ Rotary make_rotary(const qvg_rotary *r) {
     return o;
 }
 
-bool wide_format(int format) { return format == QVG_PAGE_F16 || format == QVG_PAGE_BF16; }
-
 qvg_status check_pool(int32_t n_heads, int32_t d, int32_t page_tokens, int32_t format, int64_t n_pages) {
     if (n_heads < 1 || n_pages < 1) return QVG_ERR_INVALID_ARG;
     if (d != kD || n_heads > 32767) return QVG_ERR_UNSUPPORTED;
     if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128)
         return QVG_ERR_UNSUPPORTED;
-    if (format < QVG_PAGE_F16 || format > QVG_PAGE_INT8) return QVG_ERR_UNSUPPORTED;
+    if ((format < QVG_PAGE_F16 || format > QVG_PAGE_INT8) && !four_bits(format)) return QVG_ERR_UNSUPPORTED;
     if (n_pages >= (int64_t(1) << 31) || n_pages * n_heads * page_tokens >= (int64_t(1) << 31))
         return QVG_ERR_UNSUPPORTED;
     return QVG_OK;
@@ -71,8 +69,13 @@ qvg_status check_pages(const qvg_pages *g, int32_t format) {
     if (!wide_format(format) &&
         (!g->k_scale || !g->v_scale || !aligned(g->k_scale, 16) || !aligned(g->v_scale, 16)))
         return QVG_ERR_INVALID_ARG;
+    if (four_bits(format) && (!g->k_group || !g->v_group || !aligned(g->k_group, 16) || !aligned(g->v_group, 16)))
+        return QVG_ERR_INVALID_ARG;
     return QVG_OK;
 }
+// The groups' scales, which only the 4-bit formats have (a caller of the others may have no room
+// for them in its struct).
+uint8_t *groups_of(uint8_t *const &groups, int32_t format) { return four_bits(format) ? groups : nullptr; }
 
 qvg_status check_attention(const qvg_page_attention_params *p) {
     if (!p) return QVG_ERR_INVALID_ARG;
@@ -228,6 +231,8 @@ qvg_status qvg_page_write(const qvg_page_write_params *prm, const void *K, const
     p.v = pages->v;
     p.ks = pages->k_scale;
     p.vs = pages->v_scale;
+    p.kg = groups_of(pages->k_group, p.fmt);
+    p.vg = groups_of(pages->v_group, p.fmt);
     p.status = dev_status;
     return launched(launch_page_write(p, static_cast<cudaStream_t>(stream)));
 }
@@ -266,6 +271,8 @@ qvg_status qvg_page_read(const qvg_page_read_params *prm, const qvg_pages *pages
     p.v = pages->v;
     p.ks = pages->k_scale;
     p.vs = pages->v_scale;
+    p.kg = groups_of(pages->k_group, p.fmt);
+    p.vg = groups_of(pages->v_group, p.fmt);
     p.table = page_table;
     p.lens = seq_lens;
     p.X = X;
@@ -300,6 +307,8 @@ qvg_status qvg_page_attention(const qvg_page_attention_params *prm, const void *
     p.v = pages->v;
     p.ks = pages->k_scale;
     p.vs = pages->v_scale;
+    p.kg = groups_of(pages->k_group, p.fmt);
+    p.vg = groups_of(pages->v_group, p.fmt);
     p.table = page_table;
     p.lens = seq_lens;
     p.cu = cu_q;

@@ -115,7 +115,7 @@ __device__ __forceinline__ bool is_finite(float x) {
 //     taken its values' or keys' bits (k_page_attn_tc.cu).
 // And, many rows, where scores are past 2^23.
 __device__ __forceinline__ bool redo_possible(const PAttnPlan &p) { return p.causal || p.window > 0; }
-__device__ __forceinline__ bool wide_pages(const PAttnPlan &p) { return p.fmt == PF_F16 || p.fmt == PF_BF16; }
+__device__ __forceinline__ bool wide_pages(const PAttnPlan &p) { return wide_format(p.fmt); }
 __device__ __forceinline__ bool rows_to_check(const PAttnPlan &p) { return p.fmt != PF_INT8 && redo_possible(p); }
 constexpr float kRedo = -1.f;  // in the place of a split's weight sum: the row is to be done again
 
@@ -199,7 +199,10 @@ __device__ __forceinline__ BadKeys bad_values(const PAttnPlan &p, int b, int h, 
         bool bad = false;
         const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
         bool odd;
-        if (p.fmt == PF_E4M3) {
+        if (four_bits(p.fmt)) {  // (a group's scale that is NaN)
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.vg + row * kGroups));
+            odd = __vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        } else if (p.fmt == PF_E4M3) {
             const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.v) + row * kD) + (lane & 15));
             odd = __vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         } else {
@@ -216,8 +219,11 @@ __device__ __forceinline__ BadKeys bad_values(const PAttnPlan &p, int b, int h, 
     k.last = __reduce_max_sync(0xffffffffu, k.last);
     return k;
 }
-// Eight channels of a row, as they lie in memory and as numbers (codes without their scale).
-__device__ __forceinline__ uint4 load_cached8(const PAttnPlan &p, const void *pool, int64_t off) {
+// Eight channels of a row, as they lie in memory and as numbers (codes without their row's scale).
+__device__ __forceinline__ uint4 load_cached8(const PAttnPlan &p, const void *pool, const uint8_t *groups, int64_t off) {
+    if (four_bits(p.fmt))
+        return make_uint4(__ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(pool) + off / 2)),
+                          __ldg(groups + off / kGroup), 0u, 0u);
     if (wide_pages(p)) return __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(pool) + off));
     const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pool) + off));
     return make_uint4(w.x, w.y, 0u, 0u);
@@ -228,7 +234,19 @@ __device__ __forceinline__ void unpack8(int fmt, uint4 w, float v[8]) {
         unpack4(Raw4<DT_BF16>{make_uint2(w.z, w.w)}, v + 4);
         return;
     }
-    if (fmt != PF_F16) {
+    if (four_bits(fmt)) {
+        const uint32_t t = __byte_perm(group_pair(w.y), 0u, 0x1010);
+        uint32_t h[4];
+        if (fmt == PF_INT4) {
+            widen4<PF_INT4>(w.x, GroupScale<PF_INT4>(t), h);
+            const uint4 y = make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410),
+                                       __byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
+            w = y;
+        } else {
+            widen4<PF_E2M1>(w.x, GroupScale<PF_E2M1>(t), h);
+            w = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    } else if (fmt != PF_F16) {
         const uint2 y = fmt == PF_E4M3 ? codes_to_f16<true>(w.x) : codes_to_f16<false>(w.x);
         const uint2 z = fmt == PF_E4M3 ? codes_to_f16<true>(w.y) : codes_to_f16<false>(w.y);
         w = make_uint4(y.x, y.y, z.x, z.y);
@@ -258,8 +276,8 @@ static __device__ __noinline__ void redo_row(const PAttnPlan &p, int b, int i, i
         kn = vn = make_uint4(0u, 0u, 0u, 0u);
         ksn = vsn = 1.f;
         if (row >= 0) {
-            kn = load_cached8(p, p.k, (int64_t)row * kD + 8 * part);
-            vn = load_cached8(p, p.v, (int64_t)row * kD + 8 * part);
+            kn = load_cached8(p, p.k, p.kg, (int64_t)row * kD + 8 * part);
+            vn = load_cached8(p, p.v, p.vg, (int64_t)row * kD + 8 * part);
             if (!wide) {
                 ksn = __ldg(p.ks + row);
                 vsn = __ldg(p.vs + row);
@@ -379,17 +397,18 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 }
 
 // The pool as rows of 128 channels, in boxes of `rows` rows that are 128 bytes wide (of a row
-// of 8-bit codes, or of 64 channels in 16 bits), swizzled.
+// of 8-bit codes, of 64 channels in 16 bits, or of two rows of 4-bit codes), swizzled.
 inline bool page_map(const PAttnPlan &p, const void *pool, int rows, CUtensorMap *map) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    const bool wide = p.fmt == PF_F16 || p.fmt == PF_BF16;
+    const bool wide = wide_format(p.fmt);
+    const int per = four_bits(p.fmt) ? 2 : 1;  // rows of a line of 128 bytes
     const CUtensorMapDataType dt = !wide              ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : p.fmt == PF_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)(p.n_pages * p.H * p.page)};
+    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)(p.n_pages * p.H * p.page / per)};
     const cuuint64_t strides[1] = {(cuuint64_t)(wide ? 2 * kD : kD)};
-    const cuuint32_t box[2] = {wide ? 64u : (cuuint32_t)kD, (cuuint32_t)rows}, estr[2] = {1, 1};
+    const cuuint32_t box[2] = {wide ? 64u : (cuuint32_t)kD, (cuuint32_t)(rows / per)}, estr[2] = {1, 1};
     return enc(map, dt, 2, const_cast<void *>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -31,6 +31,7 @@ QVG_QSCHEME_SYMMETRIC, QVG_QSCHEME_MIDRISE = 0, 1
 QVG_STEP_PLANES, QVG_STEP_GEMM, QVG_STEP_REFINE = 1, 2, 4
 QVG_CENTROIDS_F32, QVG_CENTROIDS_F16, QVG_CENTROIDS_BF16 = 0, 1, 2
 QVG_PAGE_F16, QVG_PAGE_BF16, QVG_PAGE_E4M3, QVG_PAGE_INT8 = 0, 1, 2, 3
+QVG_PAGE_E2M1, QVG_PAGE_INT4 = 8, 9
 
 
 class qvg_quant_params(ctypes.Structure):
@@ -113,6 +114,8 @@ class qvg_pages(ctypes.Structure):
         ("v", ctypes.c_void_p),
         ("k_scale", ctypes.c_void_p),
         ("v_scale", ctypes.c_void_p),
+        ("k_group", ctypes.c_void_p),
+        ("v_group", ctypes.c_void_p),
     ]
 
 
