@@ -86,6 +86,7 @@ typedef enum {
 #define QVG_DEV_TIMEOUT 0x2u   /* a pipeline wait in a tensor-core kernel gave up */
 #define QVG_DEV_BAD_INDEX 0x4u /* a stored cluster index was >= C (it was clamped to C-1), or a
                                   slot, page or length out of range */
+#define QVG_DEV_NO_PAGES 0x8u  /* a sequence did not get the pages that it asked for */
 
 typedef enum { QVG_F16 = 0, QVG_BF16 = 1, QVG_F32 = 2 } qvg_dtype;
 
@@ -511,6 +512,91 @@ qvg_status qvg_page_attention(const qvg_page_attention_params *params, const voi
                               void *workspace, size_t workspace_bytes, uint32_t *dev_status,
                               void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * Pages of sequences.  refs (int32 [n_pages]) counts, for each page, the entries of the page table
+ * that name it; 0 is free.  A sequence of n tokens holds the first ceil(n / page_tokens) entries of its
+ * row; what the others hold is not read.  qvg_page_append gives sequences the pages of new tokens,
+ * qvg_page_fork lets one begin as a copy of another, sharing its whole pages, qvg_page_free gives
+ * pages back, qvg_page_compact moves what is live into another pool, qvg_page_copy copies single pages.
+ * They change refs, page_table and seq_lens on the device, in stream order, and need no word from the
+ * host about what is free.  Pages are always taken in ascending order, for sequences in order, so that
+ * the outcome is the same in every run.
+ *
+ * Several layers with a cache each and one page table: qvg_page_append and qvg_page_fork copy pages of
+ * the one cache that they are given and leave what they copied in `copies`, with which qvg_page_copy
+ * does the same in another layer's cache; qvg_page_compact moves the same pages for every cache.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+    int32_t n_seqs;      /* rows of the page table: 1 .. 65535 */
+    int32_t n_heads;
+    int32_t d;           /* 128 */
+    int32_t page_tokens;
+    int32_t format;
+    int32_t max_pages;   /* entries of a page-table row, at most 2^27 / page_tokens */
+    int64_t n_pages;
+    int64_t total;       /* qvg_page_append: entries of slots and positions, < 2^31 */
+    int64_t out_pages;   /* qvg_page_compact: pages of the other pool */
+} qvg_page_table_params;
+
+/* Workspace bytes that qvg_page_append, qvg_page_fork and qvg_page_compact need (0 if the parameters
+ * are invalid). */
+size_t qvg_page_table_workspace_bytes(const qvg_page_table_params *params);
+
+/* Page src[i]'s rows [0, rows[i]) (all with rows NULL), of every head, keys and values, with their
+ * scales, to page dst[i] of `to`, a pool of the same heads, page_tokens and format, which may be
+ * `pages` itself; the rows behind stay as they were.  src, dst, rows: int32 [n].  A negative src or dst
+ * skips its copy; one past its pool skips it, and rows out of range are cut, with QVG_DEV_BAD_INDEX.  No
+ * page may be a destination twice, nor in one pool both a destination and a source. */
+qvg_status qvg_page_copy(const qvg_page_table_params *params, int64_t n, const qvg_pages *pages,
+                         const int32_t *src, const int32_t *dst, const int32_t *rows,
+                         const qvg_pages *to, int64_t to_pages, uint32_t *dev_status, void *stream);
+
+/* Sequence b grows by counts[b] tokens (int32 [n_seqs], 0: none): seq_lens and the page table are
+ * brought up to date, and slots and positions (int64 [total]) of the new tokens are written, sequence
+ * after sequence, as qvg_page_write and qvg_rope take them; entries behind the last token are -1.
+ * A last page that is part filled and that other entries name too (refs > 1) is first replaced by a copy
+ * of its rows in use; copies (int32 [3][n_seqs]) holds source, destination and rows of it, -1, -1, 0 where
+ * there is none.
+ * A sequence whose pages, with those of the sequences before it, are more than the free ones, or
+ * that would pass its row of the table, stays as it is, with QVG_DEV_NO_PAGES and -1 for its tokens (a
+ * sequence that needs no page grows all the same); so does one that counts or lengths out of range,
+ * or more tokens than total, keep from it, with QVG_DEV_BAD_INDEX. */
+qvg_status qvg_page_append(const qvg_page_table_params *params, const qvg_pages *pages, int32_t *refs,
+                           int32_t *page_table, int32_t *seq_lens, const int32_t *counts,
+                           int64_t *slots, int64_t *positions, int32_t *copies, void *workspace,
+                           size_t workspace_bytes, uint32_t *dev_status, void *stream);
+
+/* Sequence b, which has to be empty, becomes a fork of sequence parents[b] (int32 [n_seqs], negative:
+ * none): the parent's whole pages are shared, its last one, if part filled, is copied as far as it
+ * is filled (copies as in qvg_page_append).  A parent may have many forks in a call but be none itself.
+ * Sequences that are not empty, and parents that are not valid, are left out with
+ * QVG_DEV_BAD_INDEX, those for which free pages do not suffice (as above) with QVG_DEV_NO_PAGES. */
+qvg_status qvg_page_fork(const qvg_page_table_params *params, const qvg_pages *pages, int32_t *refs,
+                         int32_t *page_table, int32_t *seq_lens, const int32_t *parents,
+                         int32_t *copies, void *workspace, size_t workspace_bytes,
+                         uint32_t *dev_status, void *stream);
+
+/* Sequence b gives up its first drop_first[b] tokens, as far as they fill whole pages, and its last
+ * drop_last[b] (int32 [n_seqs] each, one of them may be NULL; anything past the length means all of it).  The
+ * entries that stay move to the front of the row, the ones behind them become -1, and the length
+ * is what is left.  Pages that no entry names any more are free.  Negative counts are 0, entries out of
+ * the pool or of free pages are dropped, lengths past the table cut, with QVG_DEV_BAD_INDEX. */
+qvg_status qvg_page_free(const qvg_page_table_params *params, int32_t *refs, int32_t *page_table,
+                         int32_t *seq_lens, const int32_t *drop_first, const int32_t *drop_last,
+                         uint32_t *dev_status, void *stream);
+
+/* Pages in use (refs > 0), in ascending order, become pages 0, 1, ... of `to`, another pool of
+ * params->out_pages pages; out_table ([n_seqs][max_pages], -1 behind each sequence's entries) and out_refs
+ * ([out_pages]) are the page table and the counts for it, *live the number of pages in use.  The first
+ * pool, page_table and refs stay as they are.  What out_pages has no room for is left out, its entries
+ * -1, with QVG_DEV_NO_PAGES; entries out of the pool or of free pages become -1 with
+ * QVG_DEV_BAD_INDEX. */
+qvg_status qvg_page_compact(const qvg_page_table_params *params, const qvg_pages *pages,
+                            const int32_t *refs, const int32_t *page_table, const int32_t *seq_lens,
+                            const qvg_pages *to, int32_t *out_table, int32_t *out_refs, int32_t *live,
+                            void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                            void *stream);
+
 /* Static description of a status code. */
 const char *qvg_status_string(qvg_status status);
 
@@ -518,7 +604,9 @@ const char *qvg_status_string(qvg_status status);
  *   1.0  quantize, reassign, dequantize, the static-scratch quantize.
  *   1.1  qvg_quant_params.qscheme and .centroid_format, qvg_dequant_params.qscheme (both
  *        structs grew: rebuild callers), qvg_attention.  The paged cache (qvg_rope,
- *        qvg_page_*) came later without a change to what 1.1 had. */
+ *        qvg_page_*) came later without a change to what 1.1 had, and later still its 4-bit
+ *        formats (qvg_pages grew by two pointers that the others do not read) and the calls on
+ *        the pages of sequences. */
 uint32_t qvg_version(void);
 
 #ifdef __cplusplus

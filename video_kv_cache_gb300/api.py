@@ -591,3 +591,136 @@ def page_attention(Q: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_page_attention")
     return (out, lse) if return_lse else out
+
+
+# ------------------------------------------------------------------------------------
+# The pages of sequences.  refs (int32 [pages]) counts the table entries that name a page, 0 is
+# free; refs, page_table and seq_lens change on the device, in stream order.  Pages are taken in
+# ascending order, for sequences in order: every run has the same outcome.
+# ------------------------------------------------------------------------------------
+
+def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int = 0, out_pages: int = 0):
+    """(GPU, sequences, entries of a row, parameters) of a call on the pages of sequences."""
+    dev = _gpu(kv.k, "pages")
+    n_seqs, max_pages = _tables(page_table, seq_lens, dev)
+    _index(refs, torch.int32, (kv.n_pages,), "refs", dev)
+    _check_scratch(status, workspace, dev)
+    return dev, n_seqs, max_pages, _c.qvg_page_table_params(n_seqs, kv.heads, D, kv.page_tokens, kv.format, max_pages,
+                                                            kv.n_pages, total, out_pages)
+
+
+def _book_workspace(prm, kv: PagedKV, workspace, stream):
+    if workspace is None:
+        workspace = _empty((max(_c.qvg_page_table_workspace_bytes(prm), 64),), torch.uint8, kv.k.device, stream)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _copies(copies, kv: PagedKV, n_seqs: int, dev: int, stream):
+    if copies is None:
+        return _empty((3, n_seqs), torch.int32, kv.k.device, stream)
+    _index(copies, torch.int32, (3, n_seqs), "copies", dev)
+    return copies
+
+
+def page_copy(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, *, rows: torch.Tensor | None = None,
+              out: PagedKV | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """Copy pages ``src`` to ``dst`` (int32 [n]; negative: skipped), of all heads, keys and values
+    with their scales, the first ``rows`` tokens of each (int32 [n]) or all.  ``out`` is the pool of
+    ``dst``, ``kv`` itself by default.  No page may be written twice, nor, in one pool, be written and
+    read."""
+    dev = _gpu(kv.k, "pages")
+    out = kv if out is None else out
+    n = src.shape[0] if src.dim() == 1 else -1
+    for t, what in ((src, "src"), (dst, "dst"), (rows, "rows")):
+        if t is not None:
+            _index(t, torch.int32, (n,), what, dev)
+    _need(out.gpu == dev and out.heads == kv.heads and out.page_tokens == kv.page_tokens and out.format == kv.format,
+          "out must be pages of the same heads, page_tokens and format, on the same GPU")
+    _check_scratch(status, None, dev)
+    prm = _c.qvg_page_table_params(1, kv.heads, D, kv.page_tokens, kv.format, 1, kv.n_pages, 0, 0)
+    rc = _c.qvg_page_copy(prm, n, kv._buffers, src.data_ptr(), dst.data_ptr(), _ptr(rows), out._buffers,
+                          out.n_pages, _ptr(status), _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_copy")
+
+
+def page_append(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                counts: torch.Tensor, total: int, *, copies: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Let sequence b grow by ``counts[b]`` tokens (int32 [sequences]), ``total`` in all, taking free
+    pages where its own are full (qvg_page_append).  Returns the new tokens' slots and positions
+    (int64 [total], sequence after sequence) for ``page_write`` and ``rope``.  A part-filled last page
+    that others share is replaced by a copy first, recorded in ``copies`` (int32 [3][sequences]: source,
+    destination, rows) if given, with which ``page_copy`` does the same for another layer's pages.  A
+    sequence for which pages do not suffice stays as it is, its slots are -1 and ``status`` gets
+    QVG_DEV_NO_PAGES."""
+    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace, total=total)
+    _index(counts, torch.int32, (n_seqs,), "counts", dev)
+    _need(total >= 0, "total must not be negative")
+    copies = _copies(copies, kv, n_seqs, dev, stream)
+    workspace, size = _book_workspace(prm, kv, workspace, stream)
+    slots, positions = (_empty((total,), torch.int64, kv.k.device, stream) for _ in range(2))
+    rc = _c.qvg_page_append(prm, kv._buffers, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                            counts.data_ptr(), slots.data_ptr(), positions.data_ptr(), copies.data_ptr(),
+                            workspace.data_ptr(), size, _ptr(status), _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_append")
+    return slots, positions
+
+
+def page_fork(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+              parents: torch.Tensor, *, copies: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Let the empty sequence b begin as a fork of sequence ``parents[b]`` (int32 [sequences],
+    negative: none): whole pages are shared, a part-filled last one is copied (qvg_page_fork).
+    Returns the copies made (int32 [3][sequences]: source, destination, rows), with which
+    ``page_copy`` does the same for another layer's pages."""
+    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace)
+    _index(parents, torch.int32, (n_seqs,), "parents", dev)
+    copies = _copies(copies, kv, n_seqs, dev, stream)
+    workspace, size = _book_workspace(prm, kv, workspace, stream)
+    rc = _c.qvg_page_fork(prm, kv._buffers, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                          parents.data_ptr(), copies.data_ptr(), workspace.data_ptr(), size, _ptr(status),
+                          _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_fork")
+    return copies
+
+
+def page_free(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
+              first: torch.Tensor | None = None, last: torch.Tensor | None = None,
+              status: torch.Tensor | None = None, stream=None) -> None:
+    """Sequence b gives up its ``first[b]`` oldest tokens, as far as they fill whole pages, and its
+    ``last[b]`` newest (int32 [sequences] each; past the length: all), and the pages that hold
+    nothing else of it (qvg_page_free).  Its entries move to the front of its row."""
+    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, None)
+    _need(first is not None or last is not None, "first or last says how many tokens go")
+    for t, what in ((first, "first"), (last, "last")):
+        if t is not None:
+            _index(t, torch.int32, (n_seqs,), what, dev)
+    rc = _c.qvg_page_free(prm, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(first), _ptr(last),
+                          _ptr(status), _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_free")
+
+
+def page_compact(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                 out: PagedKV, *, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                 stream=None):
+    """Copy the pages in use to the front of another pool ``out``, in order (qvg_page_compact).
+    Returns the page table and the refs for it, and the number of pages in use (int32 [1]).  The first
+    pool with its table and refs stays as it is; what ``out`` has no room for is left out, with
+    QVG_DEV_NO_PAGES."""
+    dev, n_seqs, max_pages, prm = _book(kv, refs, page_table, seq_lens, status, workspace, out_pages=out.n_pages)
+    _need(out.gpu == dev and out.heads == kv.heads and out.page_tokens == kv.page_tokens and out.format == kv.format,
+          "out must be pages of the same heads, page_tokens and format, on the same GPU")
+    workspace, size = _book_workspace(prm, kv, workspace, stream)
+    table = _empty((n_seqs, max_pages), torch.int32, kv.k.device, stream)
+    new_refs = _empty((out.n_pages,), torch.int32, kv.k.device, stream)
+    live = _empty((1,), torch.int32, kv.k.device, stream)
+    rc = _c.qvg_page_compact(prm, kv._buffers, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), out._buffers,
+                             table.data_ptr(), new_refs.data_ptr(), live.data_ptr(), workspace.data_ptr(), size,
+                             _ptr(status), _stream_handle(stream))
+    if rc != _c.QVG_OK:
+        raise _c.QVGError(rc, "qvg_page_compact")
+    return table, new_refs, live

@@ -499,6 +499,70 @@ cudaError_t launch_page_attention(const PAttnPlan &p, cudaStream_t st);
 void page_attention_cut(PAttnPlan &p);
 int64_t page_attention_part_rows(const PAttnPlan &p);  // rows of partial results in the workspace
 
+// A page's arrays as 16-byte pieces, one array after another: codes, scales and group scales of keys
+// and values, those that the format has.
+struct PoolCopy {
+    const uint8_t *src[6];
+    uint8_t *dst[6];
+    int64_t bytes[6];  // of a page
+    int64_t from[7];   // first piece of each array; [6]: pieces of a page
+    int row_shift[6];  // log2 of a row's bytes
+    int page;
+};
+int64_t copy_blocks_per_page(const PoolCopy &c);
+
+struct PCopyPlan {
+    PoolCopy pool;
+    int64_t n, per, src_pages, dst_pages;
+    const int32_t *src, *dst, *rows;
+    uint32_t *status;
+};
+cudaError_t launch_page_copy(const PCopyPlan &p, cudaStream_t st);
+
+// What a sequence wants of the free pages.
+struct TakeRow {
+    int first, need;   // its places among the pages taken
+    int len, count;    // tokens before, new tokens
+    int entries;       // table entries that stay before the new ones
+    int src, rows;     // page to be copied (-1: none), and its rows
+    int token;         // first of its tokens among all
+    int ok;
+};
+struct PTakePlan {
+    PoolCopy pool;
+    int B, max_pages, page;
+    int64_t n_pages, total;
+    int32_t *refs, *table, *lens, *copies;
+    const int32_t *wants;  // parents, or counts of new tokens
+    int64_t *slots, *positions;
+    int *head;             // places wanted, tokens, copies, places taken; [8 ..]: free pages of each CTA
+    TakeRow *rows;         // [B]
+    int *list, *moves;     // pages by place [n_pages]; sequences by place [B]
+    uint32_t *status;
+};
+cudaError_t launch_page_append(const PTakePlan &p, cudaStream_t st);
+cudaError_t launch_page_fork(const PTakePlan &p, cudaStream_t st);
+
+struct PFreePlan {
+    int B, max_pages, page;
+    int64_t n_pages;
+    int32_t *refs, *table, *lens;
+    const int32_t *first, *last;
+    uint32_t *status;
+};
+cudaError_t launch_page_free(const PFreePlan &p, cudaStream_t st);
+
+struct PCompactPlan {
+    PoolCopy pool;
+    int B, max_pages;
+    int64_t n_pages, out_pages;
+    const int32_t *refs, *table, *lens;
+    int32_t *out_refs, *out_table, *live;
+    int *head, *place, *old;  // [..8 ..] live pages of each CTA; [n_pages]; [out_pages]
+    uint32_t *status;
+};
+cudaError_t launch_page_compact(const PCompactPlan &p, cudaStream_t st);
+
 // Entry-point helpers shared by the C ABI's translation units (qvg_api.cu).
 qvg_status device_info(int *num_sms);
 bool fault_inject_launch();

@@ -1,0 +1,540 @@
+// The pages of sequences: copied, taken for new tokens, shared by forks, given back, and packed
+// into another pool.  refs[p] counts the table entries that name page p; 0 is free.
+//
+// Data movement (copies, the part-filled pages of forks, compaction) is bound by memory: pages are
+// whole arrays of 16-byte pieces, read and written once.  The bookkeeping is bound by latency: one
+// thread-block cluster finds the lowest free (or live) pages by counting, in tiles of 16 pages a
+// thread, so that what is taken does not depend on the order in which threads run, and a call is one
+// launch, or two where pages are copied.
+#include "internal.cuh"
+#include "tcgen.cuh"
+
+namespace qvg {
+
+namespace {
+constexpr int kCopyThreads = 256;
+constexpr int kCopyEach = 4;                         // 16-byte pieces of a thread, all in flight
+constexpr int kCopyPieces = kCopyThreads * kCopyEach;
+constexpr int kBookThreads = 1024;
+constexpr int kTilePages = kBookThreads * 16;        // pages that a CTA counts at a time
+constexpr int kBookCluster = 8;
+
+__device__ __forceinline__ bool in_pool(int page, int64_t n_pages) { return (unsigned)page < (uint64_t)n_pages; }
+__device__ __forceinline__ int pages_for(int64_t tokens, int shift) { return (int)((tokens + (1 << shift) - 1) >> shift); }
+
+// Piece x of a page: which array, and where in the page's part of it.  Rows [0, rows) are copied.
+__device__ __forceinline__ void copy_piece(const PoolCopy &c, int64_t src, int64_t dst, int64_t x, int rows, uint4 *held, bool store) {
+    int a = 0;
+#pragma unroll
+    for (int k = 1; k < 6; k++) a += x >= c.from[k];
+    const int64_t at = x - c.from[a], bytes = c.bytes[a];
+    const int row = (int)((at * 16) >> c.row_shift[a]) & (c.page - 1);
+    if (row >= rows) return;
+    if (!store) {
+        *held = __ldg(reinterpret_cast<const uint4 *>(c.src[a] + src * bytes) + at);
+        return;
+    }
+    uint8_t *to = c.dst[a] + dst * bytes + at * 16;
+    const int units = (rows - row) << c.row_shift[a];  // bytes of the piece's rows that are copied
+    if (units >= 16) {
+        *reinterpret_cast<uint4 *>(to) = *held;
+    } else {  // scales of 4 bytes, group scales of 8
+        const uint32_t w[4] = {held->x, held->y, held->z, held->w};
+#pragma unroll
+        for (int k = 0; k < 3; k++)
+            if (4 * k < units) reinterpret_cast<uint32_t *>(to)[k] = w[k];
+    }
+}
+__device__ __forceinline__ void copy_block(const PoolCopy &c, int64_t src, int64_t dst, int64_t block, int rows) {
+    uint4 held[kCopyEach];
+    const int64_t x0 = block * kCopyPieces + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kCopyEach; k++)
+        if (x0 + k * kCopyThreads < c.from[6]) copy_piece(c, src, dst, x0 + k * kCopyThreads, rows, &held[k], false);
+#pragma unroll
+    for (int k = 0; k < kCopyEach; k++)
+        if (x0 + k * kCopyThreads < c.from[6]) copy_piece(c, src, dst, x0 + k * kCopyThreads, rows, &held[k], true);
+}
+
+// Sum over the threads before this one, and over all, of a CTA of 1024.
+__device__ __forceinline__ int block_scan(int v, int *s_warp, int &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int upto = v;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, x);
+        if (lane >= x) upto += y;
+    }
+    __syncthreads();  // (s_warp may still be read from the scan before)
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    const int w = s_warp[lane];
+    int before = w;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, x);
+        if (lane >= x) before += y;
+    }
+    all = __shfl_sync(0xffffffffu, before, 31);
+    return upto - v + __shfl_sync(0xffffffffu, before - w, warp);
+}
+__device__ __forceinline__ void book_meet(int ctas) {
+    if (ctas > 1) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+}
+
+// Bits of this thread's 16 pages from p0 on: free ones, or those in use.
+__device__ __forceinline__ uint32_t page_bits(const int32_t *refs, int64_t p0, int64_t end, bool in_use) {
+    uint32_t bits = 0;
+    if (p0 + 16 <= end) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int4 r = *reinterpret_cast<const int4 *>(refs + p0 + 4 * k);
+            bits |= ((uint32_t)(r.x > 0) | (uint32_t)(r.y > 0) << 1 | (uint32_t)(r.z > 0) << 2 | (uint32_t)(r.w > 0) << 3) << (4 * k);
+        }
+        return in_use ? bits : ~bits & 0xFFFFu;
+    }
+    for (int k = 0; k < 16; k++)
+        if (p0 + k < end && (refs[p0 + k] > 0) == in_use) bits |= 1u << k;
+    return bits;
+}
+// This CTA's pages: whole tiles, as many for each.
+__device__ __forceinline__ void book_span(int64_t n_pages, int rank, int ctas, int64_t &from, int64_t &to) {
+    const int64_t tiles = (n_pages + kTilePages - 1) / kTilePages, per = (tiles + ctas - 1) / ctas;
+    from = min(rank * per * kTilePages, n_pages);
+    to = min(from + per * kTilePages, n_pages);
+}
+__device__ __forceinline__ int book_count(const int32_t *refs, int64_t n_pages, int rank, int ctas, bool in_use, int *s_warp) {
+    int64_t from, to;
+    book_span(n_pages, rank, ctas, from, to);
+    int n = 0, all;
+    for (int64_t p = from + threadIdx.x * 16; p < to; p += kTilePages) n += __popc(page_bits(refs, p, n_pages, in_use));
+    block_scan(n, s_warp, all);
+    return all;
+}
+// Calls take(place, page) for each such page of this CTA's, place counting from `first`, until `limit`.
+template <typename F>
+__device__ __forceinline__ void book_each(const int32_t *refs, int64_t n_pages, int rank, int ctas, bool in_use, int first, int limit,
+                                          int *s_warp, F &&take) {
+    int64_t from, to;
+    book_span(n_pages, rank, ctas, from, to);
+    for (int64_t tile = from; tile < to && first < limit; tile += kTilePages) {
+        const int64_t p0 = tile + threadIdx.x * 16;
+        uint32_t bits = p0 < n_pages ? page_bits(refs, p0, n_pages, in_use) : 0u;
+        int all, at = block_scan(__popc(bits), s_warp, all) + first;
+        while (bits && at < limit) {
+            const int k = __ffs(bits) - 1;
+            bits &= bits - 1;
+            take(at++, (int)(p0 + k));
+        }
+        first += all;
+    }
+}
+
+// Last row whose first place is at most x, of n > 0 rows in order.
+template <typename F>
+__device__ __forceinline__ int row_of_place(F &&first, int n, int64_t x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first(mid) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+}  // namespace
+
+// ------------------------------------------------------------------------------------ copies
+
+__global__ void __launch_bounds__(kCopyThreads) k_page_copy(const __grid_constant__ PCopyPlan p) {
+    pdl_begin();
+    const int64_t i = blockIdx.x / p.per;
+    const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+    int rows = p.rows ? __ldg(p.rows + i) : p.pool.page;
+    if (src < 0 || dst < 0) return;
+    if (!in_pool(src, p.src_pages) || !in_pool(dst, p.dst_pages) || rows < 0 || rows > p.pool.page) {
+        if (threadIdx.x == 0 && blockIdx.x == i * p.per) or_status(p.status, QVG_DEV_BAD_INDEX);
+        if (!in_pool(src, p.src_pages) || !in_pool(dst, p.dst_pages)) return;
+        rows = min(max(rows, 0), p.pool.page);
+    }
+    copy_block(p.pool, src, dst, blockIdx.x - i * p.per, rows);
+}
+
+// ------------------------------------------------------------------------------------ pages taken
+
+// One cluster.  Sequence b wants need pages: for a fork, one if its parent's last page is part
+// filled; for new tokens, what they fill, and one more in place of a part-filled last page that others
+// share.  The wants in order of sequence are places 0, 1, ... of the free pages in ascending order;
+// from the first sequence that they do not suffice for, none that wants any is served.
+template <bool FORK>
+__global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_constant__ PTakePlan p) {
+    pdl_begin();
+    __shared__ int s_warp[32], s_cow;
+    const int ctas = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
+    const int shift = 31 - __clz(p.page);
+    const int64_t cap = (int64_t)p.max_pages << shift;
+    if (rank == 0) {
+        // what each sequence wants, and where its places begin
+        if (tid == 0) s_cow = 0;
+        __syncthreads();
+        int places = 0;
+        int64_t tokens = 0;
+        for (int b0 = 0; b0 < p.B; b0 += kBookThreads) {
+            const int b = b0 + tid;
+            TakeRow r = {};
+            r.src = -1;
+            int64_t n = 0;
+            if (b < p.B) {
+                int64_t len = p.lens[b];
+                if constexpr (FORK) {
+                    const int parent = p.wants[b];
+                    if (parent >= 0) {
+                        bool ok = parent < p.B && len == 0 && p.wants[parent] < 0;
+                        if (ok) {
+                            len = p.lens[parent];
+                            ok = len >= 0 && len <= cap;
+                        }
+                        if (ok) {
+                            r.entries = (int)(len >> shift);
+                            r.len = (int)len;
+                            r.rows = (int)(len & (p.page - 1));
+                            r.need = r.rows > 0;
+                            r.ok = 1;
+                            if (r.need) r.src = p.table[(int64_t)parent * p.max_pages + r.entries];
+                        } else {
+                            or_status(p.status, QVG_DEV_BAD_INDEX);
+                        }
+                    }
+                } else {
+                    n = p.wants[b];
+                    if (n < 0) {
+                        or_status(p.status, QVG_DEV_BAD_INDEX);
+                        n = 0;
+                    }
+                    r.count = (int)n;
+                    if (n > 0) {
+                        if (len < 0 || len > cap) {
+                            or_status(p.status, QVG_DEV_BAD_INDEX);
+                        } else if (len + n > cap) {
+                            or_status(p.status, QVG_DEV_NO_PAGES);
+                        } else {
+                            const int have = pages_for(len, shift);
+                            r.len = (int)len;
+                            r.entries = have;
+                            r.need = pages_for(len + n, shift) - have;
+                            r.rows = (int)(len & (p.page - 1));
+                            r.ok = 1;
+                            if (r.rows) {
+                                const int last = p.table[(int64_t)b * p.max_pages + have - 1];
+                                if (in_pool(last, p.n_pages) && p.refs[last] > 1) {
+                                    r.src = last;
+                                    r.need++;
+                                    r.entries--;
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            int all;
+            if constexpr (!FORK) {
+                // tokens in 64 bits: the low and the high part of a thread's count
+                int low, high;
+                const int bl = block_scan((int)(n & 0xFFFF), s_warp, low), bh = block_scan((int)(n >> 16), s_warp, high);
+                const int64_t at = tokens + bl + ((int64_t)bh << 16);
+                tokens += low + ((int64_t)high << 16);
+                r.token = (int)min(at, (int64_t)0x7FFFFFFF);
+                if (r.ok && at + n > p.total) {
+                    r.ok = r.need = 0;
+                    or_status(p.status, QVG_DEV_BAD_INDEX);
+                }
+                if (r.ok && r.src >= 0) atomicAdd(&s_cow, 1);
+            }
+            const int before = block_scan(r.need, s_warp, all);
+            r.first = places + before;
+            places += all;
+            if (b < p.B) p.rows[b] = r;
+        }
+        if (tid == 0) {
+            p.head[0] = places;
+            p.head[1] = (int)min(tokens, (int64_t)0x7FFFFFFF);
+        }
+        __syncthreads();
+        if (tid == 0) p.head[2] = s_cow;
+    }
+    const int mine = book_count(p.refs, p.n_pages, rank, ctas, false, s_warp);
+    if (tid == 0) p.head[8 + rank] = mine;
+    book_meet(ctas);
+    int before = 0, free_pages = 0;
+    for (int c = 0; c < ctas; c++) {
+        if (c < rank) before += p.head[8 + c];
+        free_pages += p.head[8 + c];
+    }
+    // a sequence that wants nothing is served; others, if all up to it are
+    auto served = [&](const TakeRow &r) { return r.ok && (r.need == 0 || r.first + r.need <= free_pages); };
+    int take = p.head[0];
+    if (take > free_pages) {
+        take = 0;
+        for (int b = tid; b < p.B; b += kBookThreads) {
+            const int end = p.rows[b].first + p.rows[b].need;
+            if (end <= free_pages) take = max(take, end);
+        }
+        __syncthreads();
+        take = (int)__reduce_max_sync(0xffffffffu, (unsigned)take);
+        if ((tid & 31) == 0) s_warp[tid >> 5] = take;
+        __syncthreads();
+        take = (int)__reduce_max_sync(0xffffffffu, (unsigned)s_warp[tid & 31]);
+    }
+    book_each(p.refs, p.n_pages, rank, ctas, false, before, take, s_warp, [&](int place, int page) { p.list[place] = page; });
+    book_meet(ctas);  // (nobody looks for free pages any more)
+    const int grid = ctas * kBookThreads, me = rank * kBookThreads + tid;
+    for (int b = me; b < p.B; b += grid) {
+        const TakeRow r = p.rows[b];
+        const bool ok = served(r);
+        const bool copied = ok && (FORK ? r.need > 0 : r.src >= 0);
+        const int dst = copied ? p.list[r.first] : -1;
+        p.copies[b] = copied ? r.src : -1;
+        p.copies[p.B + b] = dst;
+        p.copies[2 * p.B + b] = copied ? r.rows : 0;
+        if (r.ok && !ok) or_status(p.status, QVG_DEV_NO_PAGES);
+        if constexpr (FORK) {
+            // (the entries that are shared, and the copies, are left to the next kernel)
+            if (copied) {
+                if (!in_pool(r.src, p.n_pages)) or_status(p.status, QVG_DEV_BAD_INDEX);
+                p.table[(int64_t)b * p.max_pages + r.entries] = dst;
+                p.refs[dst] = 1;
+                p.moves[r.first] = b;
+            }
+            p.rows[b].need = ok ? r.entries : 0;
+            if (ok) p.lens[b] = r.len;
+        } else if (ok) {
+            p.lens[b] = r.len + r.count;
+            if (r.src >= 0) atomicSub(p.refs + r.src, 1);
+        }
+    }
+    if constexpr (FORK) {
+        if (me == 0) p.head[3] = take;
+    } else {
+        for (int x = me; x < take; x += grid) {
+            const int b = row_of_place([&](int k) { return p.rows[k].first; }, p.B, x);
+            const TakeRow r = p.rows[b];
+            const int page = p.list[x];
+            p.table[(int64_t)b * p.max_pages + r.entries + x - r.first] = page;
+            p.refs[page] = 1;
+        }
+        const int64_t tokens = min((int64_t)p.head[1], p.total);
+        for (int64_t x = me; x < p.total; x += grid) {
+            int64_t slot = -1, pos = -1;
+            if (x < tokens) {
+                const int b = row_of_place([&](int k) { return p.rows[k].token; }, p.B, x);
+                const TakeRow r = p.rows[b];
+                if (served(r)) {
+                    pos = r.len + (x - r.token);
+                    const int entry = (int)(pos >> shift);
+                    const int page = entry < r.entries ? p.table[(int64_t)b * p.max_pages + entry] : p.list[r.first + entry - r.entries];
+                    if (in_pool(page, p.n_pages))
+                        slot = ((int64_t)page << shift) + (pos & (p.page - 1));
+                    else
+                        or_status(p.status, QVG_DEV_BAD_INDEX);
+                }
+            }
+            p.slots[x] = slot;
+            p.positions[x] = pos;
+        }
+        // shared last pages, which nobody else of this call writes: seldom any
+        if (p.head[2] > 0) {
+            for (int b = 0; b < p.B; b++) {
+                const TakeRow r = p.rows[b];
+                if (r.src < 0 || !served(r)) continue;
+                const int dst = p.list[r.first];
+                for (int64_t x = me; x < p.pool.from[6]; x += grid) {
+                    uint4 v;
+                    copy_piece(p.pool, r.src, dst, x, r.rows, &v, false);
+                    copy_piece(p.pool, r.src, dst, x, r.rows, &v, true);
+                }
+            }
+        }
+    }
+}
+
+// The rest of a fork: blocks [0, copy_blocks) copy the part-filled pages, the others take the shared
+// entries, a sequence at a time.
+__global__ void __launch_bounds__(kCopyThreads) k_page_fork(const __grid_constant__ PTakePlan p, int copy_blocks, int per) {
+    pdl_begin();
+    if (blockIdx.x < copy_blocks) {
+        const int64_t items = (int64_t)p.head[3] * per;
+        for (int64_t x = blockIdx.x; x < items; x += copy_blocks) {
+            const int b = p.moves[x / per], src = p.copies[b];
+            if (in_pool(src, p.n_pages)) copy_block(p.pool, src, p.copies[p.B + b], x % per, p.copies[2 * p.B + b]);
+        }
+        return;
+    }
+    for (int b = blockIdx.x - copy_blocks; b < p.B; b += gridDim.x - copy_blocks) {
+        const int n = p.rows[b].need;
+        const int32_t *from = p.table + (int64_t)(n > 0 ? p.wants[b] : b) * p.max_pages;
+        for (int j = threadIdx.x; j < n; j += kCopyThreads) {
+            const int page = from[j];
+            p.table[(int64_t)b * p.max_pages + j] = page;
+            if (in_pool(page, p.n_pages))
+                atomicAdd(p.refs + page, 1);
+            else
+                or_status(p.status, QVG_DEV_BAD_INDEX);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------ pages given back
+
+__global__ void __launch_bounds__(256) k_page_free(const __grid_constant__ PFreePlan p) {
+    pdl_begin();
+    const int shift = 31 - __clz(p.page), tid = threadIdx.x;
+    const int64_t cap = (int64_t)p.max_pages << shift;
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int64_t first = p.first ? p.first[b] : 0, last = p.last ? p.last[b] : 0, given = p.lens[b];
+        const int64_t len = min(max(given, (int64_t)0), cap);
+        if (first <= 0 && last <= 0) {
+            if (tid == 0 && (first < 0 || last < 0)) or_status(p.status, QVG_DEV_BAD_INDEX);
+            continue;
+        }
+        if (tid == 0 && (first < 0 || last < 0 || len != given)) or_status(p.status, QVG_DEV_BAD_INDEX);
+        // tokens [a, z) stay, a at the start of a page
+        const int64_t z = len - min(max(last, (int64_t)0), len);
+        const int64_t a = max(first, (int64_t)0) >= z ? z : (max(first, (int64_t)0) >> shift) << shift;
+        const int have = pages_for(len, shift);
+        const int e0 = a == z ? have : (int)(a >> shift), e1 = a == z ? have : pages_for(z, shift);  // entries that stay
+        int32_t *row = p.table + (int64_t)b * p.max_pages;
+        for (int j = tid; j < have; j += 256) {
+            if (j >= e0 && j < e1) continue;
+            const int page = row[j];
+            bool ok = in_pool(page, p.n_pages);
+            if (ok && atomicSub(p.refs + page, 1) <= 0) {  // it was free
+                atomicAdd(p.refs + page, 1);
+                ok = false;
+            }
+            if (!ok) or_status(p.status, QVG_DEV_BAD_INDEX);
+        }
+        __syncthreads();
+        // entries move up, chunk by chunk: a chunk is read before any of it is written, and what is
+        // read lies behind what was written before
+        for (int j0 = e0 ? 0 : e1; j0 < have; j0 += 256) {
+            const int j = j0 + tid;
+            const int page = j + e0 < e1 ? row[j + e0] : -1;
+            __syncthreads();
+            if (j < have) row[j] = page;
+        }
+        if (tid == 0) p.lens[b] = (int)(z - a);
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------------------------ compaction
+
+__global__ void __launch_bounds__(kBookThreads, 1) k_page_rank(const __grid_constant__ PCompactPlan p) {
+    pdl_begin();
+    __shared__ int s_warp[32];
+    const int ctas = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
+    const int mine = book_count(p.refs, p.n_pages, rank, ctas, true, s_warp);
+    if (tid == 0) p.head[8 + rank] = mine;
+    book_meet(ctas);
+    int before = 0, live = 0;
+    for (int c = 0; c < ctas; c++) {
+        if (c < rank) before += p.head[8 + c];
+        live += p.head[8 + c];
+    }
+    book_each(p.refs, p.n_pages, rank, ctas, true, before, 0x7FFFFFFF, s_warp, [&](int place, int page) {
+        p.place[page] = place;
+        if (place < p.out_pages) {
+            p.old[place] = page;
+            p.out_refs[place] = p.refs[page];
+        }
+    });
+    for (int64_t x = (int64_t)rank * kBookThreads + tid; x < p.out_pages; x += ctas * kBookThreads)
+        if (x >= live) p.out_refs[x] = 0;
+    if (rank == 0 && tid == 0) {
+        *p.live = live;
+        if (live > p.out_pages) or_status(p.status, QVG_DEV_NO_PAGES);
+    }
+}
+
+// Blocks [0, copy_blocks) copy live pages, the others renumber the table.
+__global__ void __launch_bounds__(kCopyThreads) k_page_compact(const __grid_constant__ PCompactPlan p, int copy_blocks, int per) {
+    pdl_begin();
+    if (blockIdx.x < copy_blocks) {
+        const int64_t items = min((int64_t)*p.live, p.out_pages) * per;
+        for (int64_t x = blockIdx.x; x < items; x += copy_blocks) {
+            const int64_t to = x / per;
+            copy_block(p.pool, p.old[to], to, x - to * per, p.pool.page);
+        }
+        return;
+    }
+    const int shift = 31 - __clz(p.pool.page);
+    const int64_t cap = (int64_t)p.max_pages << shift;
+    for (int b = blockIdx.x - copy_blocks; b < p.B; b += gridDim.x - copy_blocks) {
+        const int64_t len = p.lens[b];
+        if (threadIdx.x == 0 && (len < 0 || len > cap)) or_status(p.status, QVG_DEV_BAD_INDEX);
+        const int have = pages_for(min(max(len, (int64_t)0), cap), shift);
+        for (int j = threadIdx.x; j < p.max_pages; j += kCopyThreads) {
+            int to = -1;
+            if (j < have) {
+                const int page = p.table[(int64_t)b * p.max_pages + j];
+                if (in_pool(page, p.n_pages) && p.refs[page] > 0) {
+                    to = p.place[page];
+                    if (to >= p.out_pages) to = -1;  // (no room: reported)
+                } else {
+                    or_status(p.status, QVG_DEV_BAD_INDEX);
+                }
+            }
+            p.out_table[(int64_t)b * p.max_pages + j] = to;
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------ launches
+
+namespace {
+// CTAs of the bookkeeping's cluster: one for small pools and few tokens, where a barrier among CTAs
+// costs more than it saves.
+int book_ctas(int64_t n_pages, int64_t tokens) {
+    int ctas = 1;
+    while (ctas < kBookCluster && (n_pages > (int64_t)ctas * kTilePages || tokens > (int64_t)ctas * kBookThreads * 4)) ctas *= 2;
+    return ctas;
+}
+int copy_grid(int64_t items) { return (int)std::min<int64_t>(std::max<int64_t>(items, 1), 152 * 8); }
+}  // namespace
+
+int64_t copy_blocks_per_page(const PoolCopy &c) { return (c.from[6] + kCopyPieces - 1) / kCopyPieces; }
+
+cudaError_t launch_page_copy(const PCopyPlan &p, cudaStream_t st) {
+    return launch_kernel(k_page_copy, dim3((unsigned)(p.n * p.per)), dim3(kCopyThreads), 0, st, p);
+}
+
+cudaError_t launch_page_append(const PTakePlan &p, cudaStream_t st) {
+    const int ctas = book_ctas(p.n_pages, p.total);
+    return launch_kernel_cluster(k_page_take<false>, dim3(ctas), dim3(kBookThreads), 0, ctas, st, p);
+}
+
+cudaError_t launch_page_fork(const PTakePlan &p, cudaStream_t st) {
+    const int ctas = book_ctas(p.n_pages, 0);
+    cudaError_t e = launch_kernel_cluster(k_page_take<true>, dim3(ctas), dim3(kBookThreads), 0, ctas, st, p);
+    if (e != cudaSuccess) return e;
+    const int per = (int)copy_blocks_per_page(p.pool), copies = copy_grid((int64_t)p.B * per), rows = std::min(p.B, 152 * 4);
+    return launch_kernel(k_page_fork, dim3((unsigned)(copies + rows)), dim3(kCopyThreads), 0, st, p, copies, per);
+}
+
+cudaError_t launch_page_free(const PFreePlan &p, cudaStream_t st) {
+    return launch_kernel(k_page_free, dim3((unsigned)std::min(p.B, 152 * 8)), dim3(256), 0, st, p);
+}
+
+cudaError_t launch_page_compact(const PCompactPlan &p, cudaStream_t st) {
+    const int ctas = book_ctas(p.n_pages, 0);
+    cudaError_t e = launch_kernel_cluster(k_page_rank, dim3(ctas), dim3(kBookThreads), 0, ctas, st, p);
+    if (e != cudaSuccess) return e;
+    const int per = (int)copy_blocks_per_page(p.pool), copies = copy_grid(p.out_pages * per), rows = std::min(p.B, 152 * 4);
+    return launch_kernel(k_page_compact, dim3((unsigned)(copies + rows)), dim3(kCopyThreads), 0, st, p, copies, per);
+}
+
+}  // namespace qvg

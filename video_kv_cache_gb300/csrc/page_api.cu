@@ -1,5 +1,5 @@
 // C ABI of the paged cache: argument checks and plans of qvg_rope, qvg_page_write,
-// qvg_page_read and qvg_page_attention.  Declarations and their contracts are in
+// qvg_page_read, qvg_page_attention, and of the calls on the pages of sequences.  Declarations and their contracts are in
 // include/qvg.h.
 #include <cmath>
 #include <limits>
@@ -140,6 +140,74 @@ PAttnPlan attention_plan(const qvg_page_attention_params *prm) {
 size_t attention_part_bytes(const PAttnPlan &p) { return (size_t)page_attention_part_rows(p) * kD * sizeof(float); }
 size_t attention_bytes(const PAttnPlan &p) {
     return (size_t)page_attention_part_rows(p) * (kD + 2) * sizeof(float) + (p.stream ? (size_t)p.B * p.H * sizeof(int2) : 0);
+}
+
+// ---- pages of sequences
+
+qvg_status check_table(const qvg_page_table_params *p) {
+    if (!p || p->n_seqs < 1 || p->max_pages < 1) return QVG_ERR_INVALID_ARG;
+    qvg_status rc = check_pool(p->n_heads, p->d, p->page_tokens, p->format, p->n_pages);
+    if (rc != QVG_OK) return rc;
+    if (p->n_seqs > 65535 || (int64_t)p->max_pages * p->page_tokens > (int64_t(1) << 27)) return QVG_ERR_UNSUPPORTED;
+    if (p->total < 0 || p->out_pages < 0) return QVG_ERR_INVALID_ARG;
+    if (p->total >= (int64_t(1) << 31) || p->out_pages * p->n_heads * p->page_tokens >= (int64_t(1) << 31) ||
+        p->out_pages >= (int64_t(1) << 31))
+        return QVG_ERR_UNSUPPORTED;
+    return QVG_OK;
+}
+
+PoolCopy pool_copy(const qvg_page_table_params *prm, const qvg_pages *from, const qvg_pages *to) {
+    PoolCopy c{};
+    c.page = prm->page_tokens;
+    const bool wide = wide_format(prm->format), four = four_bits(prm->format);
+    const int shift[3] = {wide ? 8 : four ? 6 : 7, 2, 3};
+    auto set = [&](int a, const void *s, void *d, bool has) {
+        c.src[a] = static_cast<const uint8_t *>(s);
+        c.dst[a] = static_cast<uint8_t *>(d);
+        c.row_shift[a] = shift[a / 2];
+        c.bytes[a] = ((int64_t)prm->n_heads * prm->page_tokens) << shift[a / 2];
+        c.from[a + 1] = c.from[a] + (has ? c.bytes[a] / 16 : 0);
+    };
+    set(0, from->k, to->k, true);
+    set(1, from->v, to->v, true);
+    set(2, wide ? nullptr : from->k_scale, wide ? nullptr : to->k_scale, !wide);
+    set(3, wide ? nullptr : from->v_scale, wide ? nullptr : to->v_scale, !wide);
+    set(4, groups_of(from->k_group, prm->format), groups_of(to->k_group, prm->format), four);
+    set(5, groups_of(from->v_group, prm->format), groups_of(to->v_group, prm->format), four);
+    return c;
+}
+
+// Workspace of the calls that take or count pages: a head, then the sequences' wants, the pages and the
+// sequences by place; or the new number of each page, and the old one of each new page.
+constexpr size_t kHeadBytes = 64;
+inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+size_t take_bytes(const qvg_page_table_params *p) {
+    return kHeadBytes + up16((size_t)p->n_seqs * sizeof(TakeRow)) + up16((size_t)p->n_pages * 4) + up16((size_t)p->n_seqs * 4);
+}
+size_t compact_bytes(const qvg_page_table_params *p) { return kHeadBytes + up16((size_t)p->n_pages * 4) + up16((size_t)p->out_pages * 4); }
+
+PTakePlan take_plan(const qvg_page_table_params *prm, const qvg_pages *pages, int32_t *refs, int32_t *table, int32_t *lens,
+                    int32_t *copies, void *workspace, uint32_t *status) {
+    PTakePlan p{};
+    p.pool = pool_copy(prm, pages, pages);
+    p.B = prm->n_seqs;
+    p.max_pages = prm->max_pages;
+    p.page = prm->page_tokens;
+    p.n_pages = prm->n_pages;
+    p.refs = refs;
+    p.table = table;
+    p.lens = lens;
+    p.copies = copies;
+    unsigned char *at = static_cast<unsigned char *>(workspace);
+    p.head = reinterpret_cast<int *>(at);
+    at += kHeadBytes;
+    p.rows = reinterpret_cast<TakeRow *>(at);
+    at += up16((size_t)p.B * sizeof(TakeRow));
+    p.list = reinterpret_cast<int *>(at);
+    at += up16((size_t)p.n_pages * 4);
+    p.moves = reinterpret_cast<int *>(at);
+    p.status = status;
+    return p;
 }
 
 // Checks that come after the arguments': the injected failure, the device.
@@ -319,6 +387,132 @@ qvg_status qvg_page_attention(const qvg_page_attention_params *prm, const void *
     p.spans = reinterpret_cast<int2 *>(p.ml + 2 * page_attention_part_rows(p));
     p.status = dev_status;
     return launched(launch_page_attention(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t qvg_page_table_workspace_bytes(const qvg_page_table_params *prm) {
+    if (check_table(prm) != QVG_OK) return 0;
+    return std::max(take_bytes(prm), compact_bytes(prm));
+}
+
+qvg_status qvg_page_copy(const qvg_page_table_params *prm, int64_t n, const qvg_pages *pages, const int32_t *src,
+                         const int32_t *dst, const int32_t *rows, const qvg_pages *to, int64_t to_pages,
+                         uint32_t *dev_status, void *stream) {
+    if (!prm || n < 0 || to_pages < 1) return QVG_ERR_INVALID_ARG;
+    qvg_status rc = check_pool(prm->n_heads, prm->d, prm->page_tokens, prm->format, prm->n_pages);
+    if (rc == QVG_OK) rc = check_pool(prm->n_heads, prm->d, prm->page_tokens, prm->format, to_pages);
+    if (rc == QVG_OK) rc = check_pages(pages, prm->format);
+    if (rc == QVG_OK) rc = check_pages(to, prm->format);
+    if (rc != QVG_OK) return rc;
+    if (n == 0) return QVG_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(rows, 4)) return QVG_ERR_INVALID_ARG;
+    PCopyPlan p{};
+    p.pool = pool_copy(prm, pages, to);
+    p.per = copy_blocks_per_page(p.pool);
+    if (n >= (int64_t(1) << 31) || n * p.per >= (int64_t(1) << 31)) return QVG_ERR_UNSUPPORTED;
+    if ((rc = ready()) != QVG_OK) return rc;
+    p.n = n;
+    p.src_pages = prm->n_pages;
+    p.dst_pages = to_pages;
+    p.src = src;
+    p.dst = dst;
+    p.rows = rows;
+    p.status = dev_status;
+    return launched(launch_page_copy(p, static_cast<cudaStream_t>(stream)));
+}
+
+qvg_status qvg_page_append(const qvg_page_table_params *prm, const qvg_pages *pages, int32_t *refs, int32_t *page_table,
+                           int32_t *seq_lens, const int32_t *counts, int64_t *slots, int64_t *positions,
+                           int32_t *copies, void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    qvg_status rc = check_table(prm);
+    if (rc == QVG_OK) rc = check_pages(pages, prm->format);
+    if (rc != QVG_OK) return rc;
+    if (!refs || !page_table || !seq_lens || !counts || !copies || !aligned(refs, 16) || !aligned(page_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(counts, 4) || !aligned(copies, 4) || !aligned(slots, 8) || !aligned(positions, 8) ||
+        (prm->total > 0 && (!slots || !positions)))
+        return QVG_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < take_bytes(prm) || !aligned(workspace, 16)) return QVG_ERR_WORKSPACE;
+    if ((rc = ready()) != QVG_OK) return rc;
+    PTakePlan p = take_plan(prm, pages, refs, page_table, seq_lens, copies, workspace, dev_status);
+    p.total = prm->total;
+    p.wants = counts;
+    p.slots = slots;
+    p.positions = positions;
+    return launched(launch_page_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+qvg_status qvg_page_fork(const qvg_page_table_params *prm, const qvg_pages *pages, int32_t *refs, int32_t *page_table,
+                         int32_t *seq_lens, const int32_t *parents, int32_t *copies, void *workspace,
+                         size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+    qvg_status rc = check_table(prm);
+    if (rc == QVG_OK) rc = check_pages(pages, prm->format);
+    if (rc != QVG_OK) return rc;
+    if (!refs || !page_table || !seq_lens || !parents || !copies || !aligned(refs, 16) || !aligned(page_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(copies, 4))
+        return QVG_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < take_bytes(prm) || !aligned(workspace, 16)) return QVG_ERR_WORKSPACE;
+    if ((rc = ready()) != QVG_OK) return rc;
+    PTakePlan p = take_plan(prm, pages, refs, page_table, seq_lens, copies, workspace, dev_status);
+    p.wants = parents;
+    return launched(launch_page_fork(p, static_cast<cudaStream_t>(stream)));
+}
+
+qvg_status qvg_page_free(const qvg_page_table_params *prm, int32_t *refs, int32_t *page_table, int32_t *seq_lens,
+                         const int32_t *drop_first, const int32_t *drop_last, uint32_t *dev_status, void *stream) {
+    qvg_status rc = check_table(prm);
+    if (rc != QVG_OK) return rc;
+    if (!refs || !page_table || !seq_lens || (!drop_first && !drop_last) || !aligned(refs, 16) || !aligned(page_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(drop_first, 4) || !aligned(drop_last, 4))
+        return QVG_ERR_INVALID_ARG;
+    if ((rc = ready()) != QVG_OK) return rc;
+    PFreePlan p{};
+    p.B = prm->n_seqs;
+    p.max_pages = prm->max_pages;
+    p.page = prm->page_tokens;
+    p.n_pages = prm->n_pages;
+    p.refs = refs;
+    p.table = page_table;
+    p.lens = seq_lens;
+    p.first = drop_first;
+    p.last = drop_last;
+    p.status = dev_status;
+    return launched(launch_page_free(p, static_cast<cudaStream_t>(stream)));
+}
+
+qvg_status qvg_page_compact(const qvg_page_table_params *prm, const qvg_pages *pages, const int32_t *refs,
+                            const int32_t *page_table, const int32_t *seq_lens, const qvg_pages *to, int32_t *out_table,
+                            int32_t *out_refs, int32_t *live, void *workspace, size_t workspace_bytes,
+                            uint32_t *dev_status, void *stream) {
+    qvg_status rc = check_table(prm);
+    if (rc == QVG_OK) rc = check_pages(pages, prm->format);
+    if (rc == QVG_OK) rc = check_pages(to, prm->format);
+    if (rc != QVG_OK) return rc;
+    if (prm->out_pages < 1 || to->k == pages->k || to->v == pages->v || out_table == page_table || out_refs == refs)
+        return QVG_ERR_INVALID_ARG;
+    if (!refs || !page_table || !seq_lens || !out_table || !out_refs || !live || !aligned(refs, 16) || !aligned(page_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(out_table, 4) || !aligned(out_refs, 4) || !aligned(live, 4))
+        return QVG_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < compact_bytes(prm) || !aligned(workspace, 16)) return QVG_ERR_WORKSPACE;
+    if ((rc = ready()) != QVG_OK) return rc;
+    PCompactPlan p{};
+    p.pool = pool_copy(prm, pages, to);
+    p.B = prm->n_seqs;
+    p.max_pages = prm->max_pages;
+    p.n_pages = prm->n_pages;
+    p.out_pages = prm->out_pages;
+    p.refs = refs;
+    p.table = page_table;
+    p.lens = seq_lens;
+    p.out_refs = out_refs;
+    p.out_table = out_table;
+    p.live = live;
+    unsigned char *at = static_cast<unsigned char *>(workspace);
+    p.head = reinterpret_cast<int *>(at);
+    at += kHeadBytes;
+    p.place = reinterpret_cast<int *>(at);
+    at += up16((size_t)p.n_pages * 4);
+    p.old = reinterpret_cast<int *>(at);
+    p.status = dev_status;
+    return launched(launch_page_compact(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@ QVG_STATIC_SCRATCH_BYTES = 64 << 20
 QVG_DEV_NONFINITE = 0x1
 QVG_DEV_TIMEOUT = 0x2
 QVG_DEV_BAD_INDEX = 0x4
+QVG_DEV_NO_PAGES = 0x8
 
 QVG_F16, QVG_BF16, QVG_F32 = 0, 1, 2
 QVG_QSCHEME_SYMMETRIC, QVG_QSCHEME_MIDRISE = 0, 1
@@ -204,6 +205,20 @@ class qvg_page_attention_params(ctypes.Structure):
     ]
 
 
+class qvg_page_table_params(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("total", ctypes.c_int64),
+        ("out_pages", ctypes.c_int64),
+    ]
+
+
 # Every symbol include/qvg.h declares, with its ctypes signature.
 SIGNATURES = {
     "qvg_quantize_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(qvg_quant_params)]),
@@ -249,6 +264,30 @@ SIGNATURES = {
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_page_table_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(qvg_page_table_params)]),
+    "qvg_page_copy": (ctypes.c_int, [ctypes.POINTER(qvg_page_table_params), ctypes.c_int64,
+                                     ctypes.POINTER(qvg_pages), ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.POINTER(qvg_pages), ctypes.c_int64,
+                                     ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_page_append": (ctypes.c_int, [ctypes.POINTER(qvg_page_table_params),
+                                       ctypes.POINTER(qvg_pages), ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_page_fork": (ctypes.c_int, [ctypes.POINTER(qvg_page_table_params),
+                                     ctypes.POINTER(qvg_pages), ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                     ctypes.c_void_p]),
+    "qvg_page_free": (ctypes.c_int, [ctypes.POINTER(qvg_page_table_params), ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "qvg_page_compact": (ctypes.c_int, [ctypes.POINTER(qvg_page_table_params),
+                                        ctypes.POINTER(qvg_pages), ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.POINTER(qvg_pages),
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                        ctypes.c_void_p]),
     "qvg_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "qvg_version": (ctypes.c_uint32, []),
 }
@@ -370,6 +409,50 @@ def qvg_page_attention(params: qvg_page_attention_params, Q: int, pages: qvg_pag
     return (_lib or load()).qvg_page_attention(_ref(params), Q, _ref(pages), page_table, seq_lens,
                                                cu_q, O, lse, workspace, workspace_bytes, dev_status,
                                                stream)
+
+
+def qvg_page_table_workspace_bytes(params: qvg_page_table_params) -> int:
+    return (_lib or load()).qvg_page_table_workspace_bytes(_ref(params))
+
+
+def qvg_page_copy(params: qvg_page_table_params, n: int, pages: qvg_pages, src: int, dst: int,
+                  rows: int | None, to: qvg_pages, to_pages: int, dev_status: int | None,
+                  stream: int | None) -> int:
+    return (_lib or load()).qvg_page_copy(_ref(params), n, _ref(pages), src, dst, rows, _ref(to),
+                                          to_pages, dev_status, stream)
+
+
+def qvg_page_append(params: qvg_page_table_params, pages: qvg_pages, refs: int, page_table: int,
+                    seq_lens: int, counts: int, slots: int | None, positions: int | None,
+                    copies: int, workspace: int, workspace_bytes: int, dev_status: int | None,
+                    stream: int | None) -> int:
+    return (_lib or load()).qvg_page_append(_ref(params), _ref(pages), refs, page_table, seq_lens,
+                                            counts, slots, positions, copies, workspace,
+                                            workspace_bytes, dev_status, stream)
+
+
+def qvg_page_fork(params: qvg_page_table_params, pages: qvg_pages, refs: int, page_table: int,
+                  seq_lens: int, parents: int, copies: int, workspace: int, workspace_bytes: int,
+                  dev_status: int | None, stream: int | None) -> int:
+    return (_lib or load()).qvg_page_fork(_ref(params), _ref(pages), refs, page_table, seq_lens,
+                                          parents, copies, workspace, workspace_bytes, dev_status,
+                                          stream)
+
+
+def qvg_page_free(params: qvg_page_table_params, refs: int, page_table: int, seq_lens: int,
+                  drop_first: int | None, drop_last: int | None, dev_status: int | None,
+                  stream: int | None) -> int:
+    return (_lib or load()).qvg_page_free(_ref(params), refs, page_table, seq_lens, drop_first,
+                                          drop_last, dev_status, stream)
+
+
+def qvg_page_compact(params: qvg_page_table_params, pages: qvg_pages, refs: int, page_table: int,
+                     seq_lens: int, to: qvg_pages, out_table: int, out_refs: int, live: int,
+                     workspace: int, workspace_bytes: int, dev_status: int | None,
+                     stream: int | None) -> int:
+    return (_lib or load()).qvg_page_compact(_ref(params), _ref(pages), refs, page_table, seq_lens,
+                                             _ref(to), out_table, out_refs, live, workspace,
+                                             workspace_bytes, dev_status, stream)
 
 
 def qvg_status_string(code: int) -> str:
