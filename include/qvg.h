@@ -523,8 +523,8 @@ qvg_status qvg_page_attention(const qvg_page_attention_params *params, const voi
  * the outcome is the same in every run.
  *
  * Several layers with a cache each and one page table: qvg_page_append and qvg_page_fork copy pages of
- * the one cache that they are given and leave what they copied in `copies`, with which qvg_page_copy
- * does the same in another layer's cache; qvg_page_compact moves the same pages for every cache.
+ * the one cache that they are given and leave what they copied in `copies`, with whose first three
+ * rows qvg_page_copy does the same in another layer's cache; qvg_page_compact moves the same pages for every cache.
  * ------------------------------------------------------------------------------------ */
 typedef struct {
     int32_t n_seqs;      /* rows of the page table: 1 .. 65535 */
@@ -538,8 +538,8 @@ typedef struct {
     int64_t out_pages;   /* qvg_page_compact: pages of the other pool */
 } qvg_page_table_params;
 
-/* Workspace bytes that qvg_page_append, qvg_page_fork and qvg_page_compact need (0 if the parameters
- * are invalid). */
+/* Workspace bytes that qvg_page_append and qvg_page_fork need (out_pages 0), or qvg_page_compact does;
+ * 0 if none is needed, or the parameters are invalid. */
 size_t qvg_page_table_workspace_bytes(const qvg_page_table_params *params);
 
 /* Page src[i]'s rows [0, rows[i]) (all with rows NULL), of every head, keys and values, with their
@@ -555,8 +555,8 @@ qvg_status qvg_page_copy(const qvg_page_table_params *params, int64_t n, const q
  * brought up to date, and slots and positions (int64 [total]) of the new tokens are written, sequence
  * after sequence, as qvg_page_write and qvg_rope take them; entries behind the last token are -1.
  * A last page that is part filled and that other entries name too (refs > 1) is first replaced by a copy
- * of its rows in use; copies (int32 [3][n_seqs]) holds source, destination and rows of it, -1, -1, 0 where
- * there is none.
+ * of its rows in use; copies (int32 [3][n_seqs], or NULL) gets source, destination and rows of it, -1, -1, 0
+ * where there is none.
  * A sequence whose pages, with those of the sequences before it, are more than the free ones, or
  * that would pass its row of the table, stays as it is, with QVG_DEV_NO_PAGES and -1 for its tokens (a
  * sequence that needs no page grows all the same); so does one that counts or lengths out of range,
@@ -568,7 +568,8 @@ qvg_status qvg_page_append(const qvg_page_table_params *params, const qvg_pages 
 
 /* Sequence b, which has to be empty, becomes a fork of sequence parents[b] (int32 [n_seqs], negative:
  * none): the parent's whole pages are shared, its last one, if part filled, is copied as far as it
- * is filled (copies as in qvg_page_append).  A parent may have many forks in a call but be none itself.
+ * is filled.  copies (int32 [4][n_seqs]) gets source, destination and rows of that copy, -1, -1, 0 where
+ * there is none, and the whole pages shared, -1 where there is no fork.  A parent may have many forks in a call but be none itself.
  * Sequences that are not empty, and parents that are not valid, are left out with
  * QVG_DEV_BAD_INDEX, those for which free pages do not suffice (as above) with QVG_DEV_NO_PAGES. */
 qvg_status qvg_page_fork(const qvg_page_table_params *params, const qvg_pages *pages, int32_t *refs,

@@ -74,11 +74,16 @@ def test_refusals(lib, mem, monkeypatch):
             assert call(_prm(**bad)) == code, bad
         for bad in (dict(refs=None), dict(refs=mem + 4), dict(table=None), dict(table=mem + 2), dict(lens=None)):
             assert call(**bad) == 1, bad
-    for call in (append, fork, compact):
+    for call, p in ((append, dict(n_seqs=1025, out_pages=0)), (fork, dict(n_seqs=1025, out_pages=0)), (compact, {})):
         assert call(g=qvg.qvg_pages(mem, None, mem, mem)) == 1
-        for bad in (dict(ws=None), dict(ws=mem + 8), dict(size=100)):
-            assert call(**bad) == qvg.QVG_ERR_WORKSPACE
-    assert append(counts=None) == append(slots=None) == append(pos=mem + 4) == append(copies=None) == 1
+        need = qvg.qvg_page_table_workspace_bytes(_prm(**p))
+        assert need > 0 and call(_prm(**p), size=need) == qvg.QVG_ERR_CUDA
+        for bad in (dict(ws=None), dict(ws=mem + 8), dict(size=need - 1)):
+            assert call(_prm(**p), **dict(dict(size=need), **bad)) == qvg.QVG_ERR_WORKSPACE
+    for call in (append, fork):  # the wants of few sequences take none
+        assert qvg.qvg_page_table_workspace_bytes(_prm(out_pages=0)) == 0 and call(ws=None, size=0) == qvg.QVG_ERR_CUDA
+    assert append(counts=None) == append(slots=None) == append(pos=mem + 4) == append(copies=mem + 2) == 1
+    assert append(copies=None) == qvg.QVG_ERR_CUDA and fork(copies=None) == 1
     assert append(_prm(total=0), slots=None, pos=None) == qvg.QVG_ERR_CUDA
     assert fork(parents=None) == fork(copies=mem + 1) == 1
     assert free(first=None) == free(first=mem + 2) == free(last=mem + 2) == 1 and free(first=None, last=mem) == qvg.QVG_ERR_CUDA
@@ -87,7 +92,7 @@ def test_refusals(lib, mem, monkeypatch):
     assert copies(to_pages=0) == 1 and copies(to_pages=1 << 28) == 2 and copies(n=1 << 31) == 2
     assert copies(n=0, src=None, dst=None) == 0
     monkeypatch.delenv("QVG_FAULT_INJECT")
-    assert qvg.qvg_page_table_workspace_bytes(_prm()) >= 64 + 4 * 36 + 9 * 4
+    assert qvg.qvg_page_table_workspace_bytes(_prm()) >= 9 * 4 + 3 * 4
     assert qvg.qvg_page_table_workspace_bytes(_prm(d=1)) == 0
 
 

@@ -179,8 +179,11 @@ def _append(kv, s, counts, total=None, **kw):
 
 def _fork(kv, s, parents, **kw):
     status = _int([0])
-    copies = api.page_fork(kv, *s, _int(parents), status=status, **kw)
-    return copies.tolist(), int(status)
+    copies = api.page_fork(kv, *s, _int(parents), status=status, **kw).tolist()
+    lens = s[2].tolist()
+    for b, p in enumerate(parents):  # the fourth row: whole pages shared
+        assert copies[3][b] == -1 if p < 0 or copies[3][b] < 0 else copies[3][b] == lens[b] // kv.page_tokens
+    return copies[:3], int(status)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -358,6 +361,21 @@ def test_sharers_that_grow_in_one_call():
     m.check(kv, *s)
 
 
+@pytest.mark.parametrize("rows,pages", [(1024, 3000), (1025, 3000), (2500, 40000)])
+def test_many_sequences(rows, pages):
+    # more than a CTA's threads and than shared memory has room for, in one CTA and in a cluster of them
+    kv = _filled(pages, 1, 16, I8, rows)
+    s, m = _state(kv, rows, 3), Model(kv, rows, 3)
+    r = random.Random(rows)
+    counts = [r.randint(0, 40) if b % 3 == 0 else 0 for b in range(rows)]
+    assert _append(kv, s, counts) == m.append(counts, sum(counts))
+    parents = [b // 3 * 3 if b % 3 else -1 for b in range(rows)]
+    assert _fork(kv, s, parents) == m.fork(parents)
+    counts = [r.randint(0, 20) for b in range(rows)]
+    assert _append(kv, s, counts) == m.append(counts, sum(counts))
+    m.check(kv, *s)
+
+
 def test_what_cannot_be_done_is_left_and_reported():
     kv = _filled(6, 1, 16, HF, 7)
     s, m = _state(kv, 4, 3), Model(kv, 4, 3)
@@ -513,7 +531,9 @@ def test_refused_arguments():
     with pytest.raises(qvg.QVGError):  # into itself
         api.page_compact(kv, *s, kv)
     small = torch.empty(16, dtype=torch.uint8, device="cuda")
-    for call in (lambda: api.page_append(kv, *s, one, 0, workspace=small), lambda: api.page_fork(kv, *s, one, workspace=small),
+    many = _state(kv, 1025, 4)  # the wants of up to 1024 sequences need no workspace
+    none = torch.full((1025,), -1, dtype=torch.int32, device="cuda")
+    for call in (lambda: api.page_append(kv, *many, none, 0, workspace=small), lambda: api.page_fork(kv, *many, none, workspace=small),
                  lambda: api.page_compact(kv, *s, api.allocate_pages(2, 1, 16, BF), workspace=small)):
         with pytest.raises(qvg.QVGError) as e:
             call()

@@ -610,16 +610,13 @@ def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int
 
 
 def _book_workspace(prm, kv: PagedKV, workspace, stream):
+    """The workspace, which has to live as long as the call, its address and its bytes."""
     if workspace is None:
-        workspace = _empty((max(_c.qvg_page_table_workspace_bytes(prm), 64),), torch.uint8, kv.k.device, stream)
-    return workspace, workspace.numel() * workspace.element_size()
-
-
-def _copies(copies, kv: PagedKV, n_seqs: int, dev: int, stream):
-    if copies is None:
-        return _empty((3, n_seqs), torch.int32, kv.k.device, stream)
-    _index(copies, torch.int32, (3, n_seqs), "copies", dev)
-    return copies
+        need = _c.qvg_page_table_workspace_bytes(prm)
+        if not need:
+            return None, None, 0
+        workspace = _empty((need,), torch.uint8, kv.k.device, stream)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def page_copy(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, *, rows: torch.Tensor | None = None,
@@ -657,12 +654,13 @@ def page_append(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_l
     dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace, total=total)
     _index(counts, torch.int32, (n_seqs,), "counts", dev)
     _need(total >= 0, "total must not be negative")
-    copies = _copies(copies, kv, n_seqs, dev, stream)
-    workspace, size = _book_workspace(prm, kv, workspace, stream)
+    if copies is not None:
+        _index(copies, torch.int32, (3, n_seqs), "copies", dev)
+    workspace, scratch, size = _book_workspace(prm, kv, workspace, stream)
     slots, positions = (_empty((total,), torch.int64, kv.k.device, stream) for _ in range(2))
     rc = _c.qvg_page_append(prm, kv._buffers, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-                            counts.data_ptr(), slots.data_ptr(), positions.data_ptr(), copies.data_ptr(),
-                            workspace.data_ptr(), size, _ptr(status), _stream_handle(stream))
+                            counts.data_ptr(), slots.data_ptr(), positions.data_ptr(), _ptr(copies),
+                            scratch, size, _ptr(status), _stream_handle(stream))
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_page_append")
     return slots, positions
@@ -673,14 +671,17 @@ def page_fork(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_len
               workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Let the empty sequence b begin as a fork of sequence ``parents[b]`` (int32 [sequences],
     negative: none): whole pages are shared, a part-filled last one is copied (qvg_page_fork).
-    Returns the copies made (int32 [3][sequences]: source, destination, rows), with which
-    ``page_copy`` does the same for another layer's pages."""
+    Returns the copies made (int32 [4][sequences]: source, destination, rows, and whole pages shared, -1
+    where there is no fork), with which ``page_copy`` does the same for another layer's pages."""
     dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace)
     _index(parents, torch.int32, (n_seqs,), "parents", dev)
-    copies = _copies(copies, kv, n_seqs, dev, stream)
-    workspace, size = _book_workspace(prm, kv, workspace, stream)
+    if copies is None:
+        copies = _empty((4, n_seqs), torch.int32, kv.k.device, stream)
+    else:
+        _index(copies, torch.int32, (4, n_seqs), "copies", dev)
+    workspace, scratch, size = _book_workspace(prm, kv, workspace, stream)
     rc = _c.qvg_page_fork(prm, kv._buffers, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-                          parents.data_ptr(), copies.data_ptr(), workspace.data_ptr(), size, _ptr(status),
+                          parents.data_ptr(), copies.data_ptr(), scratch, size, _ptr(status),
                           _stream_handle(stream))
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_page_fork")
@@ -714,12 +715,12 @@ def page_compact(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_
     dev, n_seqs, max_pages, prm = _book(kv, refs, page_table, seq_lens, status, workspace, out_pages=out.n_pages)
     _need(out.gpu == dev and out.heads == kv.heads and out.page_tokens == kv.page_tokens and out.format == kv.format,
           "out must be pages of the same heads, page_tokens and format, on the same GPU")
-    workspace, size = _book_workspace(prm, kv, workspace, stream)
+    workspace, scratch, size = _book_workspace(prm, kv, workspace, stream)
     table = _empty((n_seqs, max_pages), torch.int32, kv.k.device, stream)
     new_refs = _empty((out.n_pages,), torch.int32, kv.k.device, stream)
     live = _empty((1,), torch.int32, kv.k.device, stream)
     rc = _c.qvg_page_compact(prm, kv._buffers, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), out._buffers,
-                             table.data_ptr(), new_refs.data_ptr(), live.data_ptr(), workspace.data_ptr(), size,
+                             table.data_ptr(), new_refs.data_ptr(), live.data_ptr(), scratch, size,
                              _ptr(status), _stream_handle(stream))
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_page_compact")

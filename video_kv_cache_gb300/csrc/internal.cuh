@@ -519,15 +519,8 @@ struct PCopyPlan {
 };
 cudaError_t launch_page_copy(const PCopyPlan &p, cudaStream_t st);
 
-// What a sequence wants of the free pages.
-struct TakeRow {
-    int first, need;   // its places among the pages taken
-    int len, count;    // tokens before, new tokens
-    int entries;       // table entries that stay before the new ones
-    int src, rows;     // page to be copied (-1: none), and its rows
-    int token;         // first of its tokens among all
-    int ok;
-};
+constexpr int kBookSharedRows = 1024;      // sequences whose wants are worked out in shared memory
+size_t take_bytes(int64_t sequences);      // else in this much of the workspace
 struct PTakePlan {
     PoolCopy pool;
     int B, max_pages, page;
@@ -535,9 +528,7 @@ struct PTakePlan {
     int32_t *refs, *table, *lens, *copies;
     const int32_t *wants;  // parents, or counts of new tokens
     int64_t *slots, *positions;
-    int *head;             // places wanted, tokens, copies, places taken; [8 ..]: free pages of each CTA
-    TakeRow *rows;         // [B]
-    int *list, *moves;     // pages by place [n_pages]; sequences by place [B]
+    void *rows;            // workspace, see take_bytes
     uint32_t *status;
 };
 cudaError_t launch_page_append(const PTakePlan &p, cudaStream_t st);
@@ -558,7 +549,7 @@ struct PCompactPlan {
     int64_t n_pages, out_pages;
     const int32_t *refs, *table, *lens;
     int32_t *out_refs, *out_table, *live;
-    int *head, *place, *old;  // [..8 ..] live pages of each CTA; [n_pages]; [out_pages]
+    int *place, *old;  // new number of each page; old number of each new page
     uint32_t *status;
 };
 cudaError_t launch_page_compact(const PCompactPlan &p, cudaStream_t st);

@@ -18,6 +18,7 @@ constexpr int kCopyPieces = kCopyThreads * kCopyEach;
 constexpr int kBookThreads = 1024;
 constexpr int kTilePages = kBookThreads * 16;        // pages that a CTA counts at a time
 constexpr int kBookCluster = 8;
+constexpr int kBookRows = kBookSharedRows;
 
 __device__ __forceinline__ bool in_pool(int page, int64_t n_pages) { return (unsigned)page < (uint64_t)n_pages; }
 __device__ __forceinline__ int pages_for(int64_t tokens, int shift) { return (int)((tokens + (1 << shift) - 1) >> shift); }
@@ -85,6 +86,23 @@ __device__ __forceinline__ void book_meet(int ctas) {
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     } else {
         __syncthreads();
+    }
+}
+
+// Counts of the CTAs before this one, and of all, from their shared memory; they meet once more before
+// any of them leaves.
+__device__ __forceinline__ void book_counts(int *s_count, int rank, int ctas, int &before, int &all) {
+    before = 0;
+    all = *s_count;
+    if (ctas == 1) return;
+    all = 0;
+    for (int c = 0; c < ctas; c++) {
+        uint32_t at;
+        int n;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(s_count)), "r"(c));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n) : "r"(at));
+        if (c < rank) before += n;
+        all += n;
     }
 }
 
@@ -166,121 +184,126 @@ __global__ void __launch_bounds__(kCopyThreads) k_page_copy(const __grid_constan
 
 // ------------------------------------------------------------------------------------ pages taken
 
+// What a sequence wants of the free pages.
+struct TakeRow {
+    int first, need;   // its places among the pages taken
+    int len, count;    // tokens before, new tokens
+    int entries;       // table entries that stay before the new ones
+    int src;           // page to be copied, -1: none
+    int token;         // first of its tokens among all
+    int ok;
+};
+
 // One cluster.  Sequence b wants need pages: for a fork, one if its parent's last page is part
 // filled; for new tokens, what they fill, and one more in place of a part-filled last page that others
 // share.  The wants in order of sequence are places 0, 1, ... of the free pages in ascending order;
-// from the first sequence that they do not suffice for, none that wants any is served.
+// from the first sequence that they do not suffice for, none that wants any is served.  Every CTA
+// works out all wants (so that only the counts of free pages have to be exchanged), in shared memory
+// where there is room.
 template <bool FORK>
 __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_constant__ PTakePlan p) {
     pdl_begin();
-    __shared__ int s_warp[32], s_cow;
+    __shared__ TakeRow s_rows[kBookRows];
+    __shared__ int s_warp[32], s_cow, s_count;
     const int ctas = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
     const int shift = 31 - __clz(p.page);
     const int64_t cap = (int64_t)p.max_pages << shift;
-    if (rank == 0) {
-        // what each sequence wants, and where its places begin
-        if (tid == 0) s_cow = 0;
-        __syncthreads();
-        int places = 0;
-        int64_t tokens = 0;
-        for (int b0 = 0; b0 < p.B; b0 += kBookThreads) {
-            const int b = b0 + tid;
-            TakeRow r = {};
-            r.src = -1;
-            int64_t n = 0;
-            if (b < p.B) {
-                int64_t len = p.lens[b];
-                if constexpr (FORK) {
-                    const int parent = p.wants[b];
-                    if (parent >= 0) {
-                        bool ok = parent < p.B && len == 0 && p.wants[parent] < 0;
-                        if (ok) {
-                            len = p.lens[parent];
-                            ok = len >= 0 && len <= cap;
-                        }
-                        if (ok) {
-                            r.entries = (int)(len >> shift);
-                            r.len = (int)len;
-                            r.rows = (int)(len & (p.page - 1));
-                            r.need = r.rows > 0;
-                            r.ok = 1;
-                            if (r.need) r.src = p.table[(int64_t)parent * p.max_pages + r.entries];
-                        } else {
-                            or_status(p.status, QVG_DEV_BAD_INDEX);
-                        }
+    TakeRow *rows = p.B <= kBookRows ? s_rows : static_cast<TakeRow *>(p.rows);
+    uint32_t *status = rank == 0 ? p.status : nullptr;
+    if (tid == 0) s_cow = 0;
+    __syncthreads();
+    int places = 0;
+    int64_t tokens = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kBookThreads) {
+        const int b = b0 + tid;
+        TakeRow r = {};
+        r.src = -1;
+        int64_t n = 0;
+        if (b < p.B) {
+            int64_t len = p.lens[b];
+            if constexpr (FORK) {
+                const int parent = p.wants[b];
+                if (parent >= 0) {
+                    bool ok = parent < p.B && len == 0 && p.wants[parent] < 0;
+                    if (ok) {
+                        len = p.lens[parent];
+                        ok = len >= 0 && len <= cap;
                     }
-                } else {
-                    n = p.wants[b];
-                    if (n < 0) {
-                        or_status(p.status, QVG_DEV_BAD_INDEX);
-                        n = 0;
+                    if (ok) {
+                        r.entries = (int)(len >> shift);
+                        r.len = (int)len;
+                        r.need = (len & (p.page - 1)) > 0;
+                        r.ok = 1;
+                        if (r.need) r.src = p.table[(int64_t)parent * p.max_pages + r.entries];
+                    } else {
+                        or_status(status, QVG_DEV_BAD_INDEX);
                     }
-                    r.count = (int)n;
-                    if (n > 0) {
-                        if (len < 0 || len > cap) {
-                            or_status(p.status, QVG_DEV_BAD_INDEX);
-                        } else if (len + n > cap) {
-                            or_status(p.status, QVG_DEV_NO_PAGES);
-                        } else {
-                            const int have = pages_for(len, shift);
-                            r.len = (int)len;
-                            r.entries = have;
-                            r.need = pages_for(len + n, shift) - have;
-                            r.rows = (int)(len & (p.page - 1));
-                            r.ok = 1;
-                            if (r.rows) {
-                                const int last = p.table[(int64_t)b * p.max_pages + have - 1];
-                                if (in_pool(last, p.n_pages) && p.refs[last] > 1) {
-                                    r.src = last;
-                                    r.need++;
-                                    r.entries--;
-                                }
+                }
+            } else {
+                n = p.wants[b];
+                if (n < 0) {
+                    or_status(status, QVG_DEV_BAD_INDEX);
+                    n = 0;
+                }
+                r.count = (int)n;
+                if (n > 0) {
+                    if (len < 0 || len > cap) {
+                        or_status(status, QVG_DEV_BAD_INDEX);
+                    } else if (len + n > cap) {
+                        or_status(status, QVG_DEV_NO_PAGES);
+                    } else {
+                        const int have = pages_for(len, shift);
+                        r.len = (int)len;
+                        r.entries = have;
+                        r.need = pages_for(len + n, shift) - have;
+                        r.ok = 1;
+                        if (len & (p.page - 1)) {
+                            const int last = p.table[(int64_t)b * p.max_pages + have - 1];
+                            if (in_pool(last, p.n_pages) && p.refs[last] > 1) {
+                                r.src = last;
+                                r.need++;
+                                r.entries--;
                             }
                         }
                     }
                 }
             }
-            int all;
-            if constexpr (!FORK) {
-                // tokens in 64 bits: the low and the high part of a thread's count
-                int low, high;
-                const int bl = block_scan((int)(n & 0xFFFF), s_warp, low), bh = block_scan((int)(n >> 16), s_warp, high);
-                const int64_t at = tokens + bl + ((int64_t)bh << 16);
-                tokens += low + ((int64_t)high << 16);
-                r.token = (int)min(at, (int64_t)0x7FFFFFFF);
-                if (r.ok && at + n > p.total) {
-                    r.ok = r.need = 0;
-                    or_status(p.status, QVG_DEV_BAD_INDEX);
-                }
-                if (r.ok && r.src >= 0) atomicAdd(&s_cow, 1);
+        }
+        int all;
+        if constexpr (!FORK) {
+            // tokens in 64 bits: the low and the high part of a thread's count
+            int low, high;
+            const int bl = block_scan((int)(n & 0xFFFF), s_warp, low);
+            int64_t at = tokens + bl;
+            tokens += low;
+            if (__syncthreads_or(n >> 16 != 0)) {
+                at += (int64_t)block_scan((int)(n >> 16), s_warp, high) << 16;
+                tokens += (int64_t)high << 16;
             }
-            const int before = block_scan(r.need, s_warp, all);
-            r.first = places + before;
-            places += all;
-            if (b < p.B) p.rows[b] = r;
+            r.token = (int)min(at, (int64_t)0x7FFFFFFF);
+            if (r.ok && at + n > p.total) {
+                r.ok = r.need = 0;
+                or_status(status, QVG_DEV_BAD_INDEX);
+            }
+            if (r.ok && r.src >= 0) atomicAdd(&s_cow, 1);
         }
-        if (tid == 0) {
-            p.head[0] = places;
-            p.head[1] = (int)min(tokens, (int64_t)0x7FFFFFFF);
-        }
-        __syncthreads();
-        if (tid == 0) p.head[2] = s_cow;
+        const int before = block_scan(r.need, s_warp, all);
+        r.first = places + before;
+        places += all;
+        if (b < p.B) rows[b] = r;
     }
     const int mine = book_count(p.refs, p.n_pages, rank, ctas, false, s_warp);
-    if (tid == 0) p.head[8 + rank] = mine;
+    if (tid == 0) s_count = mine;
     book_meet(ctas);
-    int before = 0, free_pages = 0;
-    for (int c = 0; c < ctas; c++) {
-        if (c < rank) before += p.head[8 + c];
-        free_pages += p.head[8 + c];
-    }
+    int before, free_pages;
+    book_counts(&s_count, rank, ctas, before, free_pages);
     // a sequence that wants nothing is served; others, if all up to it are
     auto served = [&](const TakeRow &r) { return r.ok && (r.need == 0 || r.first + r.need <= free_pages); };
-    int take = p.head[0];
+    int take = places;
     if (take > free_pages) {
         take = 0;
         for (int b = tid; b < p.B; b += kBookThreads) {
-            const int end = p.rows[b].first + p.rows[b].need;
+            const int end = rows[b].first + rows[b].need;
             if (end <= free_pages) take = max(take, end);
         }
         __syncthreads();
@@ -289,53 +312,47 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
         __syncthreads();
         take = (int)__reduce_max_sync(0xffffffffu, (unsigned)s_warp[tid & 31]);
     }
-    book_each(p.refs, p.n_pages, rank, ctas, false, before, take, s_warp, [&](int place, int page) { p.list[place] = page; });
-    book_meet(ctas);  // (nobody looks for free pages any more)
+    book_each(p.refs, p.n_pages, rank, ctas, false, before, take, s_warp, [&](int place, int page) {
+        const int b = row_of_place([&](int k) { return rows[k].first; }, p.B, place);
+        p.table[(int64_t)b * p.max_pages + rows[b].entries + place - rows[b].first] = page;
+        p.refs[page] = 1;  // (this thread alone looks at this count)
+        if constexpr (FORK) p.copies[p.B + b] = page;
+    });
+    if (!FORK || ctas > 1) book_meet(ctas);  // the table is complete; nobody leaves while its count is read
     const int grid = ctas * kBookThreads, me = rank * kBookThreads + tid;
     for (int b = me; b < p.B; b += grid) {
-        const TakeRow r = p.rows[b];
-        const bool ok = served(r);
-        const bool copied = ok && (FORK ? r.need > 0 : r.src >= 0);
-        const int dst = copied ? p.list[r.first] : -1;
-        p.copies[b] = copied ? r.src : -1;
-        p.copies[p.B + b] = dst;
-        p.copies[2 * p.B + b] = copied ? r.rows : 0;
+        const TakeRow r = rows[b];
+        const bool ok = served(r), copied = ok && r.src >= 0 && r.need > 0;
         if (r.ok && !ok) or_status(p.status, QVG_DEV_NO_PAGES);
         if constexpr (FORK) {
             // (the entries that are shared, and the copies, are left to the next kernel)
-            if (copied) {
-                if (!in_pool(r.src, p.n_pages)) or_status(p.status, QVG_DEV_BAD_INDEX);
-                p.table[(int64_t)b * p.max_pages + r.entries] = dst;
-                p.refs[dst] = 1;
-                p.moves[r.first] = b;
-            }
-            p.rows[b].need = ok ? r.entries : 0;
+            const bool lost = ok && r.need > 0 && !in_pool(r.src, p.n_pages);  // the parent's table is bad
+            if (lost) or_status(p.status, QVG_DEV_BAD_INDEX);
+            p.copies[b] = ok && r.need > 0 && !lost ? r.src : -1;
+            if (!ok || r.need == 0) p.copies[p.B + b] = -1;
+            p.copies[2 * p.B + b] = ok && r.need > 0 ? r.len & (p.page - 1) : 0;
+            p.copies[3 * p.B + b] = ok ? r.entries : -1;
             if (ok) p.lens[b] = r.len;
-        } else if (ok) {
-            p.lens[b] = r.len + r.count;
-            if (r.src >= 0) atomicSub(p.refs + r.src, 1);
+        } else {
+            if (ok && r.count > 0) p.lens[b] = r.len + r.count;
+            if (copied) atomicSub(p.refs + r.src, 1);
+            if (p.copies) {
+                p.copies[b] = copied ? r.src : -1;
+                p.copies[p.B + b] = copied ? p.table[(int64_t)b * p.max_pages + r.entries] : -1;
+                p.copies[2 * p.B + b] = copied ? r.len & (p.page - 1) : 0;
+            }
         }
     }
-    if constexpr (FORK) {
-        if (me == 0) p.head[3] = take;
-    } else {
-        for (int x = me; x < take; x += grid) {
-            const int b = row_of_place([&](int k) { return p.rows[k].first; }, p.B, x);
-            const TakeRow r = p.rows[b];
-            const int page = p.list[x];
-            p.table[(int64_t)b * p.max_pages + r.entries + x - r.first] = page;
-            p.refs[page] = 1;
-        }
-        const int64_t tokens = min((int64_t)p.head[1], p.total);
+    if constexpr (!FORK) {
+        tokens = min(tokens, p.total);
         for (int64_t x = me; x < p.total; x += grid) {
             int64_t slot = -1, pos = -1;
             if (x < tokens) {
-                const int b = row_of_place([&](int k) { return p.rows[k].token; }, p.B, x);
-                const TakeRow r = p.rows[b];
+                const int b = row_of_place([&](int k) { return rows[k].token; }, p.B, x);
+                const TakeRow r = rows[b];
                 if (served(r)) {
                     pos = r.len + (x - r.token);
-                    const int entry = (int)(pos >> shift);
-                    const int page = entry < r.entries ? p.table[(int64_t)b * p.max_pages + entry] : p.list[r.first + entry - r.entries];
+                    const int page = p.table[(int64_t)b * p.max_pages + (pos >> shift)];
                     if (in_pool(page, p.n_pages))
                         slot = ((int64_t)page << shift) + (pos & (p.page - 1));
                     else
@@ -346,45 +363,39 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
             p.positions[x] = pos;
         }
         // shared last pages, which nobody else of this call writes: seldom any
-        if (p.head[2] > 0) {
+        if (s_cow > 0) {
             for (int b = 0; b < p.B; b++) {
-                const TakeRow r = p.rows[b];
+                const TakeRow r = rows[b];
                 if (r.src < 0 || !served(r)) continue;
-                const int dst = p.list[r.first];
+                const int dst = p.table[(int64_t)b * p.max_pages + r.entries];
                 for (int64_t x = me; x < p.pool.from[6]; x += grid) {
                     uint4 v;
-                    copy_piece(p.pool, r.src, dst, x, r.rows, &v, false);
-                    copy_piece(p.pool, r.src, dst, x, r.rows, &v, true);
+                    copy_piece(p.pool, r.src, dst, x, r.len & (p.page - 1), &v, false);
+                    copy_piece(p.pool, r.src, dst, x, r.len & (p.page - 1), &v, true);
                 }
             }
         }
     }
 }
 
-// The rest of a fork: blocks [0, copy_blocks) copy the part-filled pages, the others take the shared
-// entries, a sequence at a time.
-__global__ void __launch_bounds__(kCopyThreads) k_page_fork(const __grid_constant__ PTakePlan p, int copy_blocks, int per) {
+// The rest of a fork, `split` blocks a sequence: its shared entries, and its part-filled page's rows.
+__global__ void __launch_bounds__(kCopyThreads) k_page_fork(const __grid_constant__ PTakePlan p, int split, int per) {
     pdl_begin();
-    if (blockIdx.x < copy_blocks) {
-        const int64_t items = (int64_t)p.head[3] * per;
-        for (int64_t x = blockIdx.x; x < items; x += copy_blocks) {
-            const int b = p.moves[x / per], src = p.copies[b];
-            if (in_pool(src, p.n_pages)) copy_block(p.pool, src, p.copies[p.B + b], x % per, p.copies[2 * p.B + b]);
-        }
-        return;
+    const int b = blockIdx.x / split, part = blockIdx.x - b * split;
+    const int n = p.copies[3 * p.B + b];
+    if (n < 0) return;
+    const int src = p.copies[b], dst = p.copies[p.B + b], rows = p.copies[2 * p.B + b];
+    const int32_t *from = p.table + (int64_t)p.wants[b] * p.max_pages;
+    for (int j = part * kCopyThreads + threadIdx.x; j < n; j += split * kCopyThreads) {
+        const int page = from[j];
+        p.table[(int64_t)b * p.max_pages + j] = page;
+        if (in_pool(page, p.n_pages))
+            atomicAdd(p.refs + page, 1);
+        else
+            or_status(p.status, QVG_DEV_BAD_INDEX);
     }
-    for (int b = blockIdx.x - copy_blocks; b < p.B; b += gridDim.x - copy_blocks) {
-        const int n = p.rows[b].need;
-        const int32_t *from = p.table + (int64_t)(n > 0 ? p.wants[b] : b) * p.max_pages;
-        for (int j = threadIdx.x; j < n; j += kCopyThreads) {
-            const int page = from[j];
-            p.table[(int64_t)b * p.max_pages + j] = page;
-            if (in_pool(page, p.n_pages))
-                atomicAdd(p.refs + page, 1);
-            else
-                or_status(p.status, QVG_DEV_BAD_INDEX);
-        }
-    }
+    if (src >= 0)
+        for (int x = part; x < per; x += split) copy_block(p.pool, src, dst, x, rows);
 }
 
 // ------------------------------------------------------------------------------------ pages given back
@@ -435,16 +446,13 @@ __global__ void __launch_bounds__(256) k_page_free(const __grid_constant__ PFree
 
 __global__ void __launch_bounds__(kBookThreads, 1) k_page_rank(const __grid_constant__ PCompactPlan p) {
     pdl_begin();
-    __shared__ int s_warp[32];
+    __shared__ int s_warp[32], s_count;
     const int ctas = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
     const int mine = book_count(p.refs, p.n_pages, rank, ctas, true, s_warp);
-    if (tid == 0) p.head[8 + rank] = mine;
+    if (tid == 0) s_count = mine;
     book_meet(ctas);
-    int before = 0, live = 0;
-    for (int c = 0; c < ctas; c++) {
-        if (c < rank) before += p.head[8 + c];
-        live += p.head[8 + c];
-    }
+    int before, live;
+    book_counts(&s_count, rank, ctas, before, live);
     book_each(p.refs, p.n_pages, rank, ctas, true, before, 0x7FFFFFFF, s_warp, [&](int place, int page) {
         p.place[page] = place;
         if (place < p.out_pages) {
@@ -458,6 +466,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_rank(const __grid_cons
         *p.live = live;
         if (live > p.out_pages) or_status(p.status, QVG_DEV_NO_PAGES);
     }
+    if (ctas > 1) book_meet(ctas);
 }
 
 // Blocks [0, copy_blocks) copy live pages, the others renumber the table.
@@ -506,6 +515,8 @@ int book_ctas(int64_t n_pages, int64_t tokens) {
 int copy_grid(int64_t items) { return (int)std::min<int64_t>(std::max<int64_t>(items, 1), 152 * 8); }
 }  // namespace
 
+size_t take_bytes(int64_t sequences) { return sequences <= kBookRows ? 0 : (size_t)sequences * sizeof(TakeRow); }
+
 int64_t copy_blocks_per_page(const PoolCopy &c) { return (c.from[6] + kCopyPieces - 1) / kCopyPieces; }
 
 cudaError_t launch_page_copy(const PCopyPlan &p, cudaStream_t st) {
@@ -521,8 +532,8 @@ cudaError_t launch_page_fork(const PTakePlan &p, cudaStream_t st) {
     const int ctas = book_ctas(p.n_pages, 0);
     cudaError_t e = launch_kernel_cluster(k_page_take<true>, dim3(ctas), dim3(kBookThreads), 0, ctas, st, p);
     if (e != cudaSuccess) return e;
-    const int per = (int)copy_blocks_per_page(p.pool), copies = copy_grid((int64_t)p.B * per), rows = std::min(p.B, 152 * 4);
-    return launch_kernel(k_page_fork, dim3((unsigned)(copies + rows)), dim3(kCopyThreads), 0, st, p, copies, per);
+    const int per = (int)copy_blocks_per_page(p.pool), split = std::min(per, std::max(1, 152 * 8 / p.B));
+    return launch_kernel(k_page_fork, dim3((unsigned)(p.B * split)), dim3(kCopyThreads), 0, st, p, split, per);
 }
 
 cudaError_t launch_page_free(const PFreePlan &p, cudaStream_t st) {

@@ -177,14 +177,9 @@ PoolCopy pool_copy(const qvg_page_table_params *prm, const qvg_pages *from, cons
     return c;
 }
 
-// Workspace of the calls that take or count pages: a head, then the sequences' wants, the pages and the
-// sequences by place; or the new number of each page, and the old one of each new page.
-constexpr size_t kHeadBytes = 64;
+// Workspace of a compaction: the new number of each page, and the old one of each new page.
 inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }
-size_t take_bytes(const qvg_page_table_params *p) {
-    return kHeadBytes + up16((size_t)p->n_seqs * sizeof(TakeRow)) + up16((size_t)p->n_pages * 4) + up16((size_t)p->n_seqs * 4);
-}
-size_t compact_bytes(const qvg_page_table_params *p) { return kHeadBytes + up16((size_t)p->n_pages * 4) + up16((size_t)p->out_pages * 4); }
+size_t compact_bytes(const qvg_page_table_params *p) { return up16((size_t)p->n_pages * 4) + up16((size_t)p->out_pages * 4); }
 
 PTakePlan take_plan(const qvg_page_table_params *prm, const qvg_pages *pages, int32_t *refs, int32_t *table, int32_t *lens,
                     int32_t *copies, void *workspace, uint32_t *status) {
@@ -198,14 +193,7 @@ PTakePlan take_plan(const qvg_page_table_params *prm, const qvg_pages *pages, in
     p.table = table;
     p.lens = lens;
     p.copies = copies;
-    unsigned char *at = static_cast<unsigned char *>(workspace);
-    p.head = reinterpret_cast<int *>(at);
-    at += kHeadBytes;
-    p.rows = reinterpret_cast<TakeRow *>(at);
-    at += up16((size_t)p.B * sizeof(TakeRow));
-    p.list = reinterpret_cast<int *>(at);
-    at += up16((size_t)p.n_pages * 4);
-    p.moves = reinterpret_cast<int *>(at);
+    p.rows = workspace;
     p.status = status;
     return p;
 }
@@ -391,7 +379,7 @@ qvg_status qvg_page_attention(const qvg_page_attention_params *prm, const void *
 
 size_t qvg_page_table_workspace_bytes(const qvg_page_table_params *prm) {
     if (check_table(prm) != QVG_OK) return 0;
-    return std::max(take_bytes(prm), compact_bytes(prm));
+    return prm->out_pages > 0 ? compact_bytes(prm) : take_bytes(prm->n_seqs);
 }
 
 qvg_status qvg_page_copy(const qvg_page_table_params *prm, int64_t n, const qvg_pages *pages, const int32_t *src,
@@ -426,11 +414,12 @@ qvg_status qvg_page_append(const qvg_page_table_params *prm, const qvg_pages *pa
     qvg_status rc = check_table(prm);
     if (rc == QVG_OK) rc = check_pages(pages, prm->format);
     if (rc != QVG_OK) return rc;
-    if (!refs || !page_table || !seq_lens || !counts || !copies || !aligned(refs, 16) || !aligned(page_table, 4) ||
+    if (!refs || !page_table || !seq_lens || !counts || !aligned(refs, 16) || !aligned(page_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(counts, 4) || !aligned(copies, 4) || !aligned(slots, 8) || !aligned(positions, 8) ||
         (prm->total > 0 && (!slots || !positions)))
         return QVG_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < take_bytes(prm) || !aligned(workspace, 16)) return QVG_ERR_WORKSPACE;
+    const size_t need = take_bytes(prm->n_seqs);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return QVG_ERR_WORKSPACE;
     if ((rc = ready()) != QVG_OK) return rc;
     PTakePlan p = take_plan(prm, pages, refs, page_table, seq_lens, copies, workspace, dev_status);
     p.total = prm->total;
@@ -449,7 +438,8 @@ qvg_status qvg_page_fork(const qvg_page_table_params *prm, const qvg_pages *page
     if (!refs || !page_table || !seq_lens || !parents || !copies || !aligned(refs, 16) || !aligned(page_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(copies, 4))
         return QVG_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < take_bytes(prm) || !aligned(workspace, 16)) return QVG_ERR_WORKSPACE;
+    const size_t need = take_bytes(prm->n_seqs);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return QVG_ERR_WORKSPACE;
     if ((rc = ready()) != QVG_OK) return rc;
     PTakePlan p = take_plan(prm, pages, refs, page_table, seq_lens, copies, workspace, dev_status);
     p.wants = parents;
@@ -505,12 +495,8 @@ qvg_status qvg_page_compact(const qvg_page_table_params *prm, const qvg_pages *p
     p.out_refs = out_refs;
     p.out_table = out_table;
     p.live = live;
-    unsigned char *at = static_cast<unsigned char *>(workspace);
-    p.head = reinterpret_cast<int *>(at);
-    at += kHeadBytes;
-    p.place = reinterpret_cast<int *>(at);
-    at += up16((size_t)p.n_pages * 4);
-    p.old = reinterpret_cast<int *>(at);
+    p.place = static_cast<int *>(workspace);
+    p.old = reinterpret_cast<int *>(static_cast<unsigned char *>(workspace) + up16((size_t)p.n_pages * 4));
     p.status = dev_status;
     return launched(launch_page_compact(p, static_cast<cudaStream_t>(stream)));
 }
