@@ -37,7 +37,6 @@
 namespace qvg {
 
 namespace {
-constexpr int kRowsShares = 152 * 2;       // CTAs that run at once
 constexpr int kRowsPad = 132;              // padded row of the join, floats
 constexpr int kRowsCluster = 8;            // most splits joined by a cluster
 constexpr int kRowsShare = 4;              // stages of a share, at least
@@ -46,18 +45,28 @@ constexpr int kRowsShare = 4;              // stages of a share, at least
 template <int FMT, int RT>
 struct RowsShape {
     static constexpr bool WIDE = wide_format(FMT), FOUR = four_bits(FMT);
-    static constexpr int WARPS = FOUR && RT == 1 ? 8 : 4;  // that compute
+    // Warps that compute.  4 bits, up to eight rows: what bounds them is instructions, of which a stage
+    // of 64 keys a warp needs the fewest for each key; four small CTAs an SM, and not two of four warps,
+    // leave fewer of them waiting (one query of 32 sequences of 9000 to 20000, 8 heads of 4 queries each:
+    // 128 us in INT4; two CTAs of four warps 131, of 32 keys a warp 141; three CTAs 138).
+    static constexpr bool SMALL = FOUR && RT == 1;
+    static constexpr int WARPS = SMALL ? 2 : 4;
     static constexpr int THREADS = 32 * (WARPS + 1);
     // 16-key tiles that a warp takes at a time: widening codes is a chain of short
     // instructions, which needs more of them side by side than feeding 16-bit rows does
-    static constexpr int KT = WIDE || (FOUR && RT == 1) ? 1 : 2;
+    static constexpr int KT = WIDE ? 1 : SMALL ? 4 : 2;
     static constexpr int KEYS = 16 * KT * WARPS;                   // of a stage
-    static constexpr int CTAS = 2;    // an SM
+    static constexpr int BOX = FOUR ? 64 : KEYS;                   // most that one copy brings
+    static constexpr int CTAS = SMALL ? 4 : 2;    // an SM
     // 8 and 16 bits: 32 KB each; two stages and three CTAs, or smaller stages, are slower
-    static constexpr int STAGES = FOUR ? 5 : 3;
+    static constexpr int STAGES = SMALL ? 2 : FOUR ? 5 : 3;
     static constexpr int ROWB = WIDE ? 2 * kD : FOUR ? kD / 2 : kD;  // bytes of a cached row
     static constexpr uint32_t TILE = KEYS * ROWB;                  // bytes of its keys, or values
 };
+// CTAs that run at once.
+inline int rows_ctas(const PAttnPlan &p) {
+    return 152 * (four_bits(p.fmt) && p.max_q * p.G <= 8 ? RowsShape<PF_INT4, 1>::CTAS : RowsShape<PF_INT8, 1>::CTAS);
+}
 // SHARES: see PAttnPlan::stream.
 template <int FMT, int RT, bool SHARES>
 struct RowsShared {
@@ -164,6 +173,7 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
     constexpr bool WIDE = T::WIDE, FOUR = T::FOUR;
     constexpr bool PVB = WIDE && QB;            // type of all operands; 8-bit and 4-bit pages: fp16
     constexpr int ROWB = T::ROWB, WARPS = T::WARPS;
+    constexpr float kUnwiden = FOUR ? 1.f / kWiden<FMT> : 1.f;
     constexpr int NCH = ROWB / 64;              // 16-byte chunks of a row per lane
     constexpr int STAGES = T::STAGES, KT = T::KT, KEYS = T::KEYS, ROWS = 8 * RT;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -268,7 +278,7 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
 
     if (warp == WARPS) {
         // -------------------------------------------------------------------- TMA loads
-        const int box = min(p.page, KEYS), boxes = KEYS / box;
+        const int box = min(p.page, T::BOX), boxes = KEYS / box;
         bool bad = false, ok = true;
         int issued = 0;
         items([&](const RowsItem &x, int64_t) {
@@ -383,7 +393,7 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
                 // the scores' columns of this lane are rows 2q and 2q + 1
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
-                    qmul[y][x] = __shfl_sync(0xffffffffu, mul, (2 * q + x) * 4) * p.scale_log2;
+                    qmul[y][x] = __shfl_sync(0xffffffffu, mul, (2 * q + x) * 4) * (p.scale_log2 * kUnwiden);
                     const int i = token_of(p, min(8 * y + 2 * q + x, rows - 1));
                     row_lo[y][x] = seen_lo(p, sq, i);
                     row_hi[y][x] = seen_hi(p, sq, i);
@@ -392,14 +402,24 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
 
             // chunk c of row r of a swizzled tile (16 bits: two halves of 128-byte rows)
             auto chunk = [](const unsigned char *tile, int r, int c) {
-                // (4 bits: lines of two rows)
-                if constexpr (FOUR) return *reinterpret_cast<const uint4 *>(tile + (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r >> 1 & 7)) << 4));
                 return *reinterpret_cast<const uint4 *>(tile + (c >> 3) * (T::TILE / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
             };
             // The key that the scores' rows g + 8 e stand for, of 16.  4 bits: such that a lane's values
             // are those of keys 4q .. 4q + 3, whose places in their lines are on different banks for the
             // lanes that read together.
             auto key_row = [&](int e) { return FOUR ? 4 * (g >> 1) + (g & 1) + 2 * e : g + 8 * e; };
+            const CodeBits code_bits((uint32_t)(p.n_pages >> 32));  // (there are fewer pages than 2^31)
+            // Where a lane's keys and values lie in the first 16 of the warp's (lines of two rows; the
+            // next 16 follow 1024 bytes on), worked out once: addresses cost as much as widening.
+            int k_at[2] = {0, 0}, v_at[2] = {0, 0};
+            if constexpr (FOUR) {
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int r = key_row(e), line = 2 * q + e;
+                    k_at[e] = (r >> 1) * 128 + ((((r & 1) * 4 + q) ^ (r >> 1)) << 4);
+                    v_at[e] = line * 128 + (((g >> 1) ^ line) << 4) + (g & 1) * 8;  // keys 4q + 2e; + 1: ^ 64
+                }
+            }
             // (a warp that gives up a wait keeps meeting the others)
             for (int j = 0; ok && j < n; j++) {
                 const int it = done + j, st = it % STAGES;
@@ -415,20 +435,27 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
                     for (int c = 0; c < NCH; c++) {
 #pragma unroll
                         for (int z = 0; z < KT; z++) {
-                            const int ra = w0 + z * 16 + key_row(0), rb = w0 + z * 16 + key_row(1);
-                            const uint4 ka = chunk(kt, ra, c * 4 + q), kb = chunk(kt, rb, c * 4 + q);
+                            uint4 ka, kb;
+                            if constexpr (FOUR) {
+                                ka = *reinterpret_cast<const uint4 *>(kt + w0 * ROWB + k_at[0] + z * 16 * ROWB);
+                                kb = *reinterpret_cast<const uint4 *>(kt + w0 * ROWB + k_at[1] + z * 16 * ROWB);
+                            } else {
+                                ka = chunk(kt, w0 + z * 16 + g, c * 4 + q);
+                                kb = chunk(kt, w0 + z * 16 + g + 8, c * 4 + q);
+                            }
                             if constexpr (FOUR) {
                                 // two groups of channels a lane
-                                const uint32_t ta = group_pair(*reinterpret_cast<const uint16_t *>(&sh.kg[st][ra * kGroups + 2 * q]));
-                                const uint32_t tb = group_pair(*reinterpret_cast<const uint16_t *>(&sh.kg[st][rb * kGroups + 2 * q]));
+                                const uint8_t *kg = &sh.kg[st][(w0 + key_row(0)) * kGroups + 2 * q] + z * 16 * kGroups;
+                                const __half2 ta = as_half2(group_pair(*reinterpret_cast<const uint16_t *>(kg)));
+                                const __half2 tb = as_half2(group_pair(*reinterpret_cast<const uint16_t *>(kg + 2 * kGroups)));
 #pragma unroll
                                 for (int x = 0; x < 2; x++) {
-                                    const GroupScale<FMT> fa(__byte_perm(ta, 0u, x ? 0x3232 : 0x1010)), fb(__byte_perm(tb, 0u, x ? 0x3232 : 0x1010));
+                                    const GroupScale<FMT> fa(x ? __high2half2(ta) : __low2half2(ta)), fb(x ? __high2half2(tb) : __low2half2(tb));
 #pragma unroll
                                     for (int w = 2 * x; w < 2 * x + 2; w++) {
                                         uint32_t ha[4], hb[4];
-                                        widen4<FMT>(word_of(ka, w), fa, ha);
-                                        widen4<FMT>(word_of(kb, w), fb, hb);
+                                        widen4<FMT>(word_of(ka, w), fa, code_bits, ha);
+                                        widen4<FMT>(word_of(kb, w), fb, code_bits, hb);
                                         const uint32_t a0[4] = {ha[0], hb[0], ha[1], hb[1]}, a1[4] = {ha[2], hb[2], ha[3], hb[3]};
 #pragma unroll
                                         for (int y = 0; y < RT; y++) {
@@ -580,25 +607,28 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
                             uint32_t tg[4];
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
-                                const int at = 16 * z + 4 * q + k, r = w0 + at;
-                                vr[k] = *reinterpret_cast<const uint2 *>(
-                                    vt + (r >> 1) * 128 + ((((r & 1) * 4 + (g >> 1)) ^ (r >> 1 & 7)) << 4) + (g & 1) * 8);
-                                tg[k] = sh.vg[st][r * kGroups + g];
-                                // values that no row sees may hold anything: their scale is 0
-                                if (edge && (t0 + at < lo || t0 + at >= hi)) tg[k] = 0u;
+                                vr[k] = *reinterpret_cast<const uint2 *>(vt + w0 * ROWB + (k & 1 ? v_at[k >> 1] ^ 64 : v_at[k >> 1]) + z * 16 * ROWB);
+                                tg[k] = sh.vg[st][(w0 + 4 * q) * kGroups + g + (16 * z + k) * kGroups];
                             }
-                            const GroupScale<FMT> f0(group_pair(tg[0] | tg[1] << 8)), f1(group_pair(tg[2] | tg[3] << 8));
+                            if (edge) {  // values that no row sees may hold anything: their scale is 0
+#pragma unroll
+                                for (int k = 0; k < 4; k++) {
+                                    const int key = t0 + 16 * z + 4 * q + k;
+                                    if (key < lo || key >= hi) tg[k] = 0u;
+                                }
+                            }
+                            const GroupScale<FMT> f0(as_half2(group_pair(__byte_perm(tg[0], tg[1], 0x0040)))), f1(as_half2(group_pair(__byte_perm(tg[2], tg[3], 0x0040))));
                             // pairs of two keys' codes of a channel
                             auto pairs = [&](uint32_t v0, uint32_t v1, const GroupScale<FMT> &f, uint32_t c[8]) {
                                 uint32_t h[4];
                                 if constexpr (FMT == PF_E2M1) {
-                                    widen4<FMT>((v0 & 0x0F0F0F0Fu) | ((v1 << 4) & 0xF0F0F0F0u), f, h);
+                                    widen4<FMT>(bit_select(v0, 0x0F0F0F0Fu, v1 << 4), f, code_bits, h);
                                     c[0] = h[0]; c[2] = h[1]; c[4] = h[2]; c[6] = h[3];
-                                    widen4<FMT>(((v0 >> 4) & 0x0F0F0F0Fu) | (v1 & 0xF0F0F0F0u), f, h);
+                                    widen4<FMT>(bit_select(v0 >> 4, 0x0F0F0F0Fu, v1), f, code_bits, h);
                                     c[1] = h[0]; c[3] = h[1]; c[5] = h[2]; c[7] = h[3];
                                 } else {
-                                    widen4<FMT>(__byte_perm(v0, v1, 0x5410), f, c);
-                                    widen4<FMT>(__byte_perm(v0, v1, 0x7632), f, c + 4);
+                                    widen4<FMT>(__byte_perm(v0, v1, 0x5410), f, code_bits, c);
+                                    widen4<FMT>(__byte_perm(v0, v1, 0x7632), f, code_bits, c + 4);
                                 }
                             };
                             uint32_t a0[8], a1[8], a2[8], a3[8];  // first / last eight channels of the keys' pairs
@@ -690,12 +720,12 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
                         const int r = 8 * y + 2 * q + x;
-                        const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp[y][x] - 8) << 23);
+                        const float unit = WIDE ? 1.f : __uint_as_float((uint32_t)(127 + vexp[y][x] - 8) << 23) * kUnwiden;
                         float f = 1.f;
                         if (relative) {
-                            float top = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+                            float top = sh.m[0][r];
 #pragma unroll
-                            for (int w = 4; w < WARPS; w++) top = fmaxf(top, sh.m[w][r]);
+                            for (int w = 1; w < WARPS; w++) top = fmaxf(top, sh.m[w][r]);
                             f = fast_exp2(m[y][x] - exp_base(top));
                         }
 #pragma unroll
@@ -946,16 +976,17 @@ void page_attention_cut(PAttnPlan &p) {
     if (rows <= kRowsM) {
         p.unit = kRowsM;
         p.units = 1;
-        const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = std::max<int64_t>(kRowsShares / cells, 1);
+        const int64_t ctas = rows_ctas(p);
+        const int64_t most = std::max<int64_t>((p.max_kv + 255) / 256, 1), once = std::max<int64_t>(ctas / cells, 1);
         int64_t want = std::min<int64_t>(once, 256);
         const bool wide = wide_format(p.fmt);
-        if (!wide && once < 4 && cells <= 2 * kRowsShares && cells * p.max_kv >= (int64_t)kRowsShares * 2048) {
+        if (!wide && once < 4 && cells <= 2 * ctas && cells * p.max_kv >= ctas * 2048) {
             p.stream = 1;
             p.S = 1;
             return;
         }
         if (once < 2 * kRowsCluster) {
-            while (want < 4 && (want + once) * cells <= 4 * kRowsShares && (want + once) * 2048 <= p.max_kv) want += once;
+            while (want < 4 && (want + once) * cells <= 4 * ctas && (want + once) * 2048 <= p.max_kv) want += once;
             want = std::min<int64_t>(want, kRowsCluster);
         }
         p.S = (int)std::min(want, most);
@@ -986,7 +1017,7 @@ void page_attention_cut(PAttnPlan &p) {
     }
 }
 int64_t page_attention_part_rows(const PAttnPlan &p) {
-    if (p.stream) return 2 * (int64_t)kRowsShares * kRowsM;
+    if (p.stream) return 2 * (int64_t)rows_ctas(p) * kRowsM;
     if (p.S == 1 || (p.unit == kRowsM && p.S <= kRowsCluster)) return 0;
     return (p.items - p.whole) * p.S * p.unit;
 }
@@ -997,12 +1028,12 @@ cudaError_t launch_rows(const PAttnPlan &p, cudaStream_t st) {
     constexpr size_t smem = rows_smem<FMT, RT, SHARES>();
     const auto kernel = k_page_attn_rows<QB, FMT, RT, SHARES>;
     CUtensorMap mk, mv;
-    const int box = std::min(p.page, RowsShape<FMT, RT>::KEYS);
+    const int box = std::min(p.page, RowsShape<FMT, RT>::BOX);
     if (!page_map(p, p.k, box, &mk) || !page_map(p, p.v, box, &mv)) return cudaErrorInvalidValue;
     cudaError_t e = allow_smem<k_page_attn_rows<QB, FMT, RT, SHARES>>(smem);
     if (e != cudaSuccess) return e;
     const int joined = p.S > 1 && p.S <= kRowsCluster;
-    const dim3 grid = SHARES ? dim3(kRowsShares) : dim3((unsigned)p.S, p.H, p.B);
+    const dim3 grid = SHARES ? dim3(rows_ctas(p)) : dim3((unsigned)p.S, p.H, p.B);
     return launch_kernel_cluster(kernel, grid, dim3(RowsShape<FMT, RT>::THREADS), smem, joined ? p.S : 1, st,
                                  mk, mv, p, joined);
 }

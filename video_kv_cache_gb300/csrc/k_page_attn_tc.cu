@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     constexpr bool WIDE = T::WIDE, FOUR = T::FOUR;
     constexpr bool BF = WIDE && QB;  // type of all operands; 8-bit and 4-bit pages: fp16
     constexpr int SLOTS = T::SLOTS;
+    constexpr int kUnwiden = FMT == PF_INT4 ? 1 : 0;  // INT4 codes are widened to half of what they stand for
     constexpr int MMA_WARP = 16, LOAD_WARP = 17, WIDEN_WARP = 20;
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *sQ = sm, *sKV = sm + 2 * kSlot, *sRaw = sKV + SLOTS * kSlot, *sGroups = sRaw + T::RAWS * T::RAW;
@@ -552,6 +553,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
             const unsigned char *src0 = FOUR ? sRaw + (rb >> 1) * 128 + ((((rb & 1) * 4 + (c >> 1)) ^ (rb >> 1 & 7)) << 4) + (c & 1) * 8
                                              : sRaw + rb * kD + ((c ^ r8) << 4);
             const unsigned char *grp0 = sGroups + rb * kGroups + c;
+            const CodeBits code_bits((uint32_t)(p.n_pages >> 32));  // (there are fewer pages than 2^31)
             unsigned char *dst0 = sKV + (c >> 2) * kHalf + rb * 128;
             const int d0 = ((2 * (c & 3)) ^ r8) << 4, d1 = ((2 * (c & 3) + 1) ^ r8) << 4;
             uint32_t phases = 0;  // of this operand's barriers of the raw tiles, a bit each
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     // 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504, and so do
                     // weights of at most 2^kLazy
                     if (j == 0 || ee > e + 2) e = ee;
-                    const float f = sc * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23);
+                    const float f = sc * __uint_as_float((uint32_t)(127 + kValueShift + kUnwiden - e) << 23);
                     if constexpr (FOLD)
                         sh.vf[buf][x] = scale_pair(f);
                     else
@@ -584,10 +586,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     if (lane == 0) sh.vnan[buf][warp & 3] = odd;
                     if (x == 0) sh.vexp[buf] = e;
                 } else if (FOLD) {
-                    sh.kf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kKeyShift - ee) << 23));
+                    sh.kf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kKeyShift + kUnwiden - ee) << 23));
                     if (x == 0) sh.kexp[buf] = ee;
                 } else {
-                    sh.ks[buf][x] = sc * fabsf(p.scale_log2);
+                    sh.ks[buf][x] = sc * (fabsf(p.scale_log2) * (1 << kUnwiden));
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
@@ -619,9 +621,9 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                                 const int key = k0 + rb + u * 16;
                                 if (key < lo || key >= hi) t = 0u;
                             }
-                            const GroupScale<FMT> f(__byte_perm(group_pair(t), 0u, 0x1010));
-                            widen4<FMT>(w.x, f, h);
-                            widen4<FMT>(w.y, f, h + 4);
+                            const GroupScale<FMT> f(__low2half2(as_half2(group_pair(t))));
+                            widen4<FMT>(w.x, f, code_bits, h);
+                            widen4<FMT>(w.y, f, code_bits, h + 4);
                             a0 = make_uint4(h[0], h[1], h[2], h[3]);
                             a1 = make_uint4(h[4], h[5], h[6], h[7]);
                         } else {

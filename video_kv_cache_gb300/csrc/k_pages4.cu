@@ -270,13 +270,13 @@ __global__ void __launch_bounds__(256) k_page_read4(PReadPlan p) {
     for (int u = 0; u < kReadRows; u++) {
         if (i0 + 16 * u >= p.count) break;
         uint32_t w[4];
-        widen4<FMT>(raw[u], GroupScale<FMT>(__byte_perm(group_pair(t[u]), 0u, 0x1010)), w);
+        widen4<FMT>(raw[u], GroupScale<FMT>(__low2half2(as_half2(group_pair(t[u])))), CodeBits(0), w);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            v[pair_channel<FMT>(i, 0)] = f.x * s[u];
-            v[pair_channel<FMT>(i, 1)] = f.y * s[u];
+            v[pair_channel<FMT>(i, 0)] = f.x * (1.f / kWiden<FMT>) * s[u];
+            v[pair_channel<FMT>(i, 1)] = f.y * (1.f / kWiden<FMT>) * s[u];
         }
         const int64_t x = b * p.xs + tensor * p.xt + (i0 + 16 * u) * kD + 8 * l;
         if constexpr (DT == DT_F32) {

@@ -235,15 +235,14 @@ __device__ __forceinline__ void unpack8(int fmt, uint4 w, float v[8]) {
         return;
     }
     if (four_bits(fmt)) {
-        const uint32_t t = __byte_perm(group_pair(w.y), 0u, 0x1010);
+        const __half2 t = __low2half2(as_half2(group_pair(w.y)));
         uint32_t h[4];
         if (fmt == PF_INT4) {
-            widen4<PF_INT4>(w.x, GroupScale<PF_INT4>(t), h);
-            const uint4 y = make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410),
-                                       __byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
-            w = y;
+            widen4<PF_INT4>(w.x, GroupScale<PF_INT4>(t), CodeBits(0), h);
+            w = make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410), __byte_perm(h[0], h[1], 0x7632),
+                           __byte_perm(h[2], h[3], 0x7632));
         } else {
-            widen4<PF_E2M1>(w.x, GroupScale<PF_E2M1>(t), h);
+            widen4<PF_E2M1>(w.x, GroupScale<PF_E2M1>(t), CodeBits(0), h);
             w = make_uint4(h[0], h[1], h[2], h[3]);
         }
     } else if (fmt != PF_F16) {
@@ -253,6 +252,10 @@ __device__ __forceinline__ void unpack8(int fmt, uint4 w, float v[8]) {
     }
     unpack4(Raw4<DT_F16>{make_uint2(w.x, w.y)}, v);
     unpack4(Raw4<DT_F16>{make_uint2(w.z, w.w)}, v + 4);
+    if (fmt == PF_INT4) {
+#pragma unroll
+        for (int c = 0; c < 8; c++) v[c] *= 1.f / kWiden<PF_INT4>;
+    }
 }
 // Row (query i of sequence b, query head hq): lane l gets channels 4l .. 4l+3, unnormalised.  Half
 // a warp takes a key, eight channels a lane, each half every other key with a maximum and sums of

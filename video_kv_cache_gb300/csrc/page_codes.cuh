@@ -29,9 +29,16 @@ __device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
 }
 
 // 4-bit codes times their group's scale, as fp16: a code has at most three significant bits and an
-// E4M3 scale four, and with scales up to 64 the product stays below 448, so it is exact.
+// E4M3 scale four, and with scales up to 64 the product stays below 448, so it is exact.  INT4 codes come
+// out at half that size (kWiden): what multiplies them next makes up for it.
 //
-// A group's scale, twice, from its E4M3 byte; of two bytes, a pair.
+// What bounds widening is the pipe of integer, logic and conversion instructions, which issues every
+// other cycle: a word of eight codes takes four of them in E2M1 and five in INT4, and four
+// multiplications.
+template <int FMT>
+constexpr float kWiden = FMT == PF_INT4 ? 0.5f : 1.f;  // what widen4 gives, over scale times code
+
+// Two group scales from their E4M3 bytes.
 __device__ __forceinline__ uint32_t group_pair(uint32_t two_bytes) {
     uint32_t r;
     asm("{\n\t.reg .b16 lo;\n\t"
@@ -41,29 +48,49 @@ __device__ __forceinline__ uint32_t group_pair(uint32_t two_bytes) {
         : "r"(two_bytes));
     return r;
 }
-__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
+__device__ __forceinline__ __half2 as_half2(uint32_t a) { return *reinterpret_cast<const __half2 *>(&a); }
+__device__ __forceinline__ uint32_t as_word(__half2 a) { return *reinterpret_cast<const uint32_t *>(&a); }
+// (a & mask) ^ c in one instruction, which holds one constant: c has to be in a register that the
+// compiler does not know the value of.
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(a), "r"(mask), "r"(c));
+    return r;
 }
-__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
-                              *reinterpret_cast<const __half2 *>(&c));
-    return *reinterpret_cast<const uint32_t *>(&r);
+// (a & mask) | (b & ~mask)
+__device__ __forceinline__ uint32_t bit_select(uint32_t a, uint32_t mask, uint32_t b) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xe2;" : "=r"(r) : "r"(a), "r"(mask), "r"(b));
+    return r;
 }
-// What the widening of a group multiplies by: E2M1 codes are converted and multiplied.  INT4 codes
-// n - 8 become 64 + n by putting n = code ^ 8 into a mantissa; (64 + n) t - 72 t is one fused
-// operation, and exact (72 t has seven significant bits).
+
+// What widens a group's codes: its scale t, twice (or those of two keys).
+//   E2M1: codes are converted, and multiplied by t.
+//   INT4: n = code ^ 8 = code + 8 is put into the mantissa of 512 (bits 0 - 3: 512 + n / 2) or of 64
+//   (bits 4 - 7: 64 + n); (512 + n / 2) t - 516 t and (64 + n) t / 2 - 36 t are one fused operation each,
+//   and exact: 516 = 4 * 129, and 129 times four bits has eleven.
 template <int FMT>
 struct GroupScale {
-    uint32_t t, off;
-    __device__ __forceinline__ explicit GroupScale(uint32_t t2) : t(t2) {
-        if constexpr (FMT == PF_INT4) off = h2mul(t2, 0xD480D480u);  // -72
-    }
+    __half2 t;
+    __device__ __forceinline__ explicit GroupScale(__half2 t2) : t(t2) {}
+};
+template <>
+struct GroupScale<PF_INT4> {
+    __half2 t, half, off_low, off_high;
+    __device__ __forceinline__ explicit GroupScale(__half2 t2)
+        : t(t2), half(__hmul2(t2, as_half2(0x38003800u))), off_low(__hmul2(t2, as_half2(0xE008E008u))),
+          off_high(__hmul2(t2, as_half2(0xD080D080u))) {}
+};
+// The exponents that INT4 codes are put under, with their topmost bit flipped.
+struct CodeBits {
+    uint32_t low, high;
+    // zero: a number that is 0 and that the compiler cannot know
+    __device__ __forceinline__ explicit CodeBits(uint32_t zero) : low(0x60086008u ^ zero), high(0x54805480u ^ zero) {}
 };
 // Eight codes of a word.  E2M1: the fp16 pairs of neighbouring channels (2i, 2i + 1); INT4: pairs
 // (i, i + 4), which need no bytes moved.
 template <int FMT>
-__device__ __forceinline__ void widen4(uint32_t w, const GroupScale<FMT> &s, uint32_t h[4]) {
+__device__ __forceinline__ void widen4(uint32_t w, const GroupScale<FMT> &s, const CodeBits &bits, uint32_t h[4]) {
     if constexpr (FMT == PF_E2M1) {
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -74,13 +101,13 @@ __device__ __forceinline__ void widen4(uint32_t w, const GroupScale<FMT> &s, uin
             : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
             : "r"(w));
 #pragma unroll
-        for (int i = 0; i < 4; i++) h[i] = h2mul(h[i], s.t);
+        for (int i = 0; i < 4; i++) h[i] = as_word(__hmul2(as_half2(h[i]), s.t));
     } else {
-        const uint32_t m = 0x00F000F0u, one = 0x54805480u;  // bits of 64 + n at 2^4 a step, n = code ^ 8
-        h[0] = h2fma(((w << 4) & m) ^ one, s.t, s.off);
-        h[1] = h2fma((w & m) ^ one, s.t, s.off);
-        h[2] = h2fma(((w >> 4) & m) ^ one, s.t, s.off);
-        h[3] = h2fma(((w >> 8) & m) ^ one, s.t, s.off);
+        const uint32_t v = w >> 8;
+        h[0] = as_word(__hfma2(as_half2(and_xor(w, 0x000F000Fu, bits.low)), s.t, s.off_low));
+        h[1] = as_word(__hfma2(as_half2(and_xor(w, 0x00F000F0u, bits.high)), s.half, s.off_high));
+        h[2] = as_word(__hfma2(as_half2(and_xor(v, 0x000F000Fu, bits.low)), s.t, s.off_low));
+        h[3] = as_word(__hfma2(as_half2(and_xor(v, 0x00F000F0u, bits.high)), s.half, s.off_high));
     }
 }
 // Channel of the low and high half of pair i of widen4, of eight.
