@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     constexpr bool WIDE = T::WIDE, FOUR = T::FOUR;
     constexpr bool BF = WIDE && QB;  // type of all operands; 8-bit and 4-bit pages: fp16
     constexpr int SLOTS = T::SLOTS;
-    constexpr int kUnwiden = FMT == PF_INT4 ? 1 : 0;  // INT4 codes are widened to half of what they stand for
+    constexpr int kUnwiden = FMT == PF_INT4 && !FOLD ? 1 : 0;  // INT4 keys are widened to half of what they stand for
     constexpr int MMA_WARP = 16, LOAD_WARP = 17, WIDEN_WARP = 20;
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *sQ = sm, *sKV = sm + 2 * kSlot, *sRaw = sKV + SLOTS * kSlot, *sGroups = sRaw + T::RAWS * T::RAW;
@@ -564,15 +564,21 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 const uint32_t odd = __ballot_sync(0xffffffffu, !is_finite(sc));
                 float m = is_finite(sc) ? fabsf(sc) : 0.f;
                 if (value) sc = is_finite(sc) ? sc : 0.f;
+                const bool reference = !FOUR || FOLD || value;  // (keys that are not folded have none)
+                if (reference) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
                 ok = ok && wait(sh.sc_empty[buf], (j >> 1) + 1);
-                if (lane == 0) wmax[warp & 3] = m;
-                __syncwarp();  // (lanes may come from a wait one by one; a barrier wants the whole warp)
-                ok = meet<128>(id, ok);
-                if (!ok) break;  // the four warps leave together
-                m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
-                const int ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
+                int ee = 0;
+                if (reference) {
+                    if (lane == 0) wmax[warp & 3] = m;
+                    __syncwarp();  // (lanes may come from a wait one by one; a barrier wants the whole warp)
+                    ok = meet<128>(id, ok);
+                    if (!ok) break;  // the four warps leave together
+                    m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+                    ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
+                }
                 if (value) {
                     // the reference moves only when a scale passes it by 2^3: codes of at most
                     // 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504, and so do
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     if (lane == 0) sh.vnan[buf][warp & 3] = odd;
                     if (x == 0) sh.vexp[buf] = e;
                 } else if (FOLD) {
-                    sh.kf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kKeyShift + kUnwiden - ee) << 23));
+                    sh.kf[buf][x] = scale_pair(sc * __uint_as_float((uint32_t)(127 + kKeyShift - ee) << 23));
                     if (x == 0) sh.kexp[buf] = ee;
                 } else {
                     sh.ks[buf][x] = sc * (fabsf(p.scale_log2) * (1 << kUnwiden));
@@ -595,14 +601,15 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&sh.sc_full[buf]));
                 if (j + 1 < n) load_scale(k0 + kTcN + x);
                 int raw = 2 * it % T::RAWS;
-                ok = wait(sh.raw_full[value][raw], phases >> raw) && wait(sh.empty[slot], it / SLOTS + 1);
+                ok = ok && wait(sh.raw_full[value][raw], phases >> raw) && wait(sh.empty[slot], it / SLOTS + 1);
                 __syncwarp();
                 ok = meet<128>(id, ok);
                 if (!ok) break;  // (otherwise all scales are there, and wmax is free again)
                 const bool whole = k0 >= lo && k0 + kTcN <= hi;
                 const uint2 *factors = (value ? sh.vf[buf] : sh.kf[buf]) + rb;
                 unsigned char *dst = dst0 + slot * kSlot;
-#pragma unroll
+#pragma unroll(FMT == PF_INT4 ? 1 : 2)  // (INT4's code is longer than the instruction cache likes: 435 -> 426 us for
+                                        // six prompts of 17 to 2000 queries over 500 to 9000 keys, fp16)
                 for (int part = 0; part < 2; part++) {
                     if (part) {
                         raw = raw == T::RAWS - 1 ? 0 : raw + 1;
@@ -610,20 +617,37 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     }
                     phases ^= 1u << raw;
                     const unsigned char *src = src0 + raw * T::RAW;
+                    uint2 four_w[4];
+                    uint32_t four_t[4];
+                    if constexpr (FOUR) {
+#pragma unroll
+                        for (int v = 0; v < 4; v++) {
+                            four_w[v] = *reinterpret_cast<const uint2 *>(src + v * 16 * (kD / 2));
+                            four_t[v] = grp0[raw * T::RAW_GROUPS + v * 16 * kGroups];
+                        }
+                        if (!whole) {  // what no row sees may hold anything: its scale is 0
+#pragma unroll
+                            for (int v = 0; v < 4; v++) {
+                                const int key = k0 + rb + (4 * part + v) * 16;
+                                if (key < lo || key >= hi) four_t[v] = 0u;
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int v = 0; v < 4; v++) {
                         const int u = 4 * part + v;
                         uint4 a0, a1;
                         if constexpr (FOUR) {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(src + v * 16 * (kD / 2));
-                            uint32_t t = grp0[raw * T::RAW_GROUPS + v * 16 * kGroups], h[8];
-                            if (!whole) {  // what no row sees may hold anything: its scale is 0
-                                const int key = k0 + rb + u * 16;
-                                if (key < lo || key >= hi) t = 0u;
+                            uint32_t h[8];
+                            if constexpr (FOLD) {
+                                const __half2 f = __hmul2(__low2half2(as_half2(group_pair(four_t[v]))), as_half2(factors[u * 16].x));
+                                widen4_by<FMT>(four_w[v].x, f, code_bits, h);
+                                widen4_by<FMT>(four_w[v].y, f, code_bits, h + 4);
+                            } else {
+                                const GroupScale<FMT> f(__low2half2(as_half2(group_pair(four_t[v]))));
+                                widen4<FMT>(four_w[v].x, f, code_bits, h);
+                                widen4<FMT>(four_w[v].y, f, code_bits, h + 4);
                             }
-                            const GroupScale<FMT> f(__low2half2(as_half2(group_pair(t))));
-                            widen4<FMT>(w.x, f, code_bits, h);
-                            widen4<FMT>(w.y, f, code_bits, h + 4);
                             a0 = make_uint4(h[0], h[1], h[2], h[3]);
                             a1 = make_uint4(h[4], h[5], h[6], h[7]);
                         } else {
@@ -637,7 +661,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                             a0 = make_uint4(y0.x, y0.y, y1.x, y1.y);
                             a1 = make_uint4(y2.x, y2.y, y3.x, y3.y);
                         }
-                        if constexpr (FOLD) {
+                        if constexpr (FOLD && !FOUR) {
                             const uint2 f = factors[u * 16];
                             a0 = make_uint4(scaled(a0.x, f), scaled(a0.y, f), scaled(a0.z, f), scaled(a0.w, f));
                             a1 = make_uint4(scaled(a1.x, f), scaled(a1.y, f), scaled(a1.z, f), scaled(a1.w, f));
@@ -771,13 +795,47 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 // registers each, many would spill (some values do as it is, 20 to 76 bytes a thread
                 // in all forms): they are read twice, for their maximum and for the weights (2.03 ->
                 // 1.94 ms; in 16 bits it costs 643 -> 675 us).
-                constexpr bool TWICE = !WIDE;
+                constexpr bool TWICE = !WIDE, ONCE = FOUR && !FOLD;
                 float s[TWICE ? 32 : 64], mx = -INFINITY, mult = row_mult;
+                // weights of 32 scores against the base, and their sum
+                float2 nb, sc2, la, lb;
+                uint32_t w[ONCE ? 32 : 16];
+                auto set_base = [&] {
+                    const float base = exp_base(m);
+                    nb = make_float2(-base, -base);
+                    sc2 = make_float2(mult, mult);
+                    la = lb = make_float2(0.f, 0.f);
+                };
+                auto weigh = [&](int hc, const float *y, uint32_t w[16]) {
+                    float4 vs4 = make_float4(1.f, 1.f, 1.f, 1.f);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float2 x = __ffma2_rn(make_float2(y[c], y[c + 1]), sc2, nb);
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                        if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
+                        if constexpr (!WIDE && !FOLD) {
+                            if (!(c & 2)) vs4 = *reinterpret_cast<const float4 *>(&sh.vs[buf][half * 64 + hc + c]);
+                            x = __fmul2_rn(x, c & 2 ? make_float2(vs4.z, vs4.w) : make_float2(vs4.x, vs4.y));
+                        }
+                        w[c >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
+                    }
+                };
                 if (ok) {
                     tc_fence_after();
                     // (kept above 0, so that -infinity times it stays -infinity)
                     if constexpr (FOLD) mult = fmaxf(mult * __uint_as_float((uint32_t)(127 + sh.kexp[buf] - kKeyShift) << 23), 1.2e-38f);
-                    if constexpr (TWICE) {
+                    if constexpr (ONCE) {
+                        set_base();
+#pragma unroll
+                        for (int hc = 0; hc < 64; hc += 32) {
+                            tc_ld32(s_at + half * 64 + hc, s);
+                            finish(hc, s);
+                            mx = fmaxf(mx, largest(s));
+                            weigh(hc, s, w + (hc >> 1));
+                        }
+                        mx *= mult;
+                    } else if constexpr (TWICE) {
                         tc_ld32(s_at + half * 64, s);
                         finish(0, s);
                         mx = largest(s);
@@ -809,7 +867,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 int e_new = e;
                 if constexpr (!WIDE) e_new = ok ? sh.vexp[buf] : e;
                 if (!meet<64>(id, ok && !raise && j > 0 && e_new == e)) {
-                    if (TWICE && ok) tc_ld32_wait(s);  // nothing below may move registers that are still to be written
+                    if (TWICE && !ONCE && ok) tc_ld32_wait(s);  // nothing below may move registers that are still to be written
                     // the larger of the two threads' maxima
                     sh.xmax[t][half][row] = mx;
                     meet<64>(id, true);
@@ -831,37 +889,31 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         tc_fence_before();
                         meet<64>(id, true);
                     }
+                    if (ONCE && ok) {
+                        e = e_new;
+                        set_base();
+#pragma unroll
+                        for (int hc = 0; hc < 64; hc += 32) {
+                            tc_ld32(s_at + half * 64 + hc, s);
+                            finish(hc, s);
+                            weigh(hc, s, w + (hc >> 1));
+                        }
+                    }
                 }
                 if (!ok) continue;
                 e = e_new;
-                const float base = exp_base(m);
-                const float2 nb = make_float2(-base, -base), sc2 = make_float2(mult, mult);
-                float2 la = make_float2(0.f, 0.f), lb = la;
+                if constexpr (!ONCE) set_base();
 #pragma unroll
                 for (int hc = 0; hc < 64; hc += 32) {
-                    if constexpr (TWICE) {
+                    if constexpr (TWICE && !ONCE) {
                         if (hc) tc_ld32_start(s_at + half * 64 + hc, s);
                         tc_ld32_wait(s);
                         finish(hc, s);
                     }
-                    const float *y = TWICE ? s : s + hc;
-                    uint32_t w[16];
-                    float4 vs4 = make_float4(1.f, 1.f, 1.f, 1.f);
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        float2 x = __ffma2_rn(make_float2(y[c], y[c + 1]), sc2, nb);
-                        x.x = fast_exp2(x.x);
-                        x.y = fast_exp2(x.y);
-                        if (c & 2) lb = __fadd2_rn(lb, x); else la = __fadd2_rn(la, x);
-                        if constexpr (!WIDE && !FOLD) {
-                            if (!(c & 2)) vs4 = *reinterpret_cast<const float4 *>(&sh.vs[buf][half * 64 + hc + c]);
-                            x = __fmul2_rn(x, c & 2 ? make_float2(vs4.z, vs4.w) : make_float2(vs4.x, vs4.y));
-                        }
-                        w[c >> 1] = BF ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
-                    }
+                    if constexpr (!ONCE) weigh(hc, TWICE ? s : s + hc, w);
                     // weights over scores that were read, so nobody else's: the product starts
                     // with the first 32 keys of either half
-                    tc_st16(s_at + half * 64 + (hc >> 1), w);
+                    tc_st16(s_at + half * 64 + (hc >> 1), w + (ONCE ? hc >> 1 : 0));
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();

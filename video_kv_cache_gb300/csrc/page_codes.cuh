@@ -110,6 +110,21 @@ __device__ __forceinline__ void widen4(uint32_t w, const GroupScale<FMT> &s, con
         h[3] = as_word(__hfma2(as_half2(and_xor(v, 0x00F000F0u, bits.high)), s.half, s.off_high));
     }
 }
+// The same codes times any factor f (twice), rounded once: in INT4, code + 8 less 8 first, which is exact.
+template <int FMT>
+__device__ __forceinline__ void widen4_by(uint32_t w, __half2 f, const CodeBits &bits, uint32_t h[4]) {
+    if constexpr (FMT == PF_E2M1) {
+        widen4<FMT>(w, GroupScale<FMT>(f), bits, h);
+    } else {
+        const uint32_t v = w >> 8;
+        const __half2 low = as_half2(0xE008E008u), high = as_half2(0xD480D480u);  // -516, -72
+        const __half2 f2 = __hadd2(f, f);
+        h[0] = as_word(__hmul2(__hadd2(as_half2(and_xor(w, 0x000F000Fu, bits.low)), low), f2));
+        h[1] = as_word(__hmul2(__hadd2(as_half2(and_xor(w, 0x00F000F0u, bits.high)), high), f));
+        h[2] = as_word(__hmul2(__hadd2(as_half2(and_xor(v, 0x000F000Fu, bits.low)), low), f2));
+        h[3] = as_word(__hmul2(__hadd2(as_half2(and_xor(v, 0x00F000F0u, bits.high)), high), f));
+    }
+}
 // Channel of the low and high half of pair i of widen4, of eight.
 template <int FMT>
 __device__ __forceinline__ constexpr int pair_channel(int i, int half) {
