@@ -539,7 +539,9 @@ typedef struct {
 } qvg_page_table_params;
 
 /* Workspace bytes that qvg_page_append and qvg_page_fork need (out_pages 0), or qvg_page_compact does;
- * 0 if none is needed, or the parameters are invalid. */
+ * 0 if none is needed, or the parameters are invalid.  The first two need none for up to
+ * QVG_FEW_SEQS sequences. */
+#define QVG_FEW_SEQS 1024
 size_t qvg_page_table_workspace_bytes(const qvg_page_table_params *params);
 
 /* Page src[i]'s rows [0, rows[i]) (all with rows NULL), of every head, keys and values, with their

@@ -601,10 +601,18 @@ def page_attention(Q: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
 
 def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int = 0, out_pages: int = 0):
     """(GPU, sequences, entries of a row, parameters) of a call on the pages of sequences."""
-    dev = _gpu(kv.k, "pages")
-    n_seqs, max_pages = _tables(page_table, seq_lens, dev)
-    _index(refs, torch.int32, (kv.n_pages,), "refs", dev)
+    dev, shape = kv.gpu, page_table.shape
+    # (one condition for what is as it should be, the checks one by one for what is not)
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and len(shape) == 2 and len(seq_lens) == shape[0] > 0 < shape[1]
+            and len(refs) == kv.n_pages and seq_lens.dim() == refs.dim() == 1
+            and page_table.dtype is torch.int32 is seq_lens.dtype is refs.dtype
+            and page_table.get_device() == seq_lens.get_device() == refs.get_device() == dev
+            and page_table.is_contiguous() and seq_lens.is_contiguous() and refs.is_contiguous()):
+        dev = _gpu(kv.k, "pages")
+        _tables(page_table, seq_lens, dev)
+        _index(refs, torch.int32, (kv.n_pages,), "refs", dev)
     _check_scratch(status, workspace, dev)
+    n_seqs, max_pages = shape
     return dev, n_seqs, max_pages, _c.qvg_page_table_params(n_seqs, kv.heads, D, kv.page_tokens, kv.format, max_pages,
                                                             kv.n_pages, total, out_pages)
 
@@ -612,6 +620,8 @@ def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int
 def _book_workspace(prm, kv: PagedKV, workspace, stream):
     """The workspace, which has to live as long as the call, its address and its bytes."""
     if workspace is None:
+        if prm.n_seqs <= _c.QVG_FEW_SEQS and not prm.out_pages:
+            return None, None, 0
         need = _c.qvg_page_table_workspace_bytes(prm)
         if not need:
             return None, None, 0

@@ -519,7 +519,7 @@ struct PCopyPlan {
 };
 cudaError_t launch_page_copy(const PCopyPlan &p, cudaStream_t st);
 
-constexpr int kBookSharedRows = 1024;      // sequences whose wants are worked out in shared memory
+constexpr int kBookSharedRows = QVG_FEW_SEQS;  // sequences whose wants are worked out in shared memory
 size_t take_bytes(int64_t sequences);      // else in this much of the workspace
 struct PTakePlan {
     PoolCopy pool;

@@ -19,6 +19,7 @@ constexpr int kBookThreads = 1024;
 constexpr int kTilePages = kBookThreads * 16;        // pages that a CTA counts at a time
 constexpr int kBookCluster = 8;
 constexpr int kBookRows = kBookSharedRows;
+constexpr int kBookFew = 1024;                       // pages taken that are handed over in shared memory
 
 __device__ __forceinline__ bool in_pool(int page, int64_t n_pages) { return (unsigned)page < (uint64_t)n_pages; }
 __device__ __forceinline__ int pages_for(int64_t tokens, int shift) { return (int)((tokens + (1 << shift) - 1) >> shift); }
@@ -57,27 +58,45 @@ __device__ __forceinline__ void copy_block(const PoolCopy &c, int64_t src, int64
         if (x0 + k * kCopyThreads < c.from[6]) copy_piece(c, src, dst, x0 + k * kCopyThreads, rows, &held[k], true);
 }
 
-// Sum over the threads before this one, and over all, of a CTA of 1024.
-__device__ __forceinline__ int block_scan(int v, int *s_warp, int &all) {
+// Sums over the threads before this one, and over all, of a CTA of 1024: N numbers at a time, none
+// negative, cut at the largest (what comes to that much is too much for any call).
+constexpr uint32_t kMost = 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t add_cut(uint32_t a, uint32_t b) { return min(a + b, kMost); }
+template <int N>
+__device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t (*s_warp)[32], uint32_t (&all)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int upto = v;
+    uint32_t upto[N], before[N];
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, x);
-        if (lane >= x) upto += y;
+    for (int k = 0; k < N; k++) upto[k] = v[k];
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto[k], x);
+            if (lane >= x) upto[k] = add_cut(upto[k], y);
+        }
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        before[k] = __shfl_up_sync(0xffffffffu, upto[k], 1);
+        if (lane == 0) before[k] = 0;
     }
     __syncthreads();  // (s_warp may still be read from the scan before)
-    if (lane == 31) s_warp[warp] = upto;
-    __syncthreads();
-    const int w = s_warp[lane];
-    int before = w;
+    if (lane == 31)
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, before, x);
-        if (lane >= x) before += y;
+        for (int k = 0; k < N; k++) s_warp[k][warp] = upto[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        uint32_t w = s_warp[k][lane];
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, w, x);
+            if (lane >= x) w = add_cut(w, y);
+        }
+        all[k] = __shfl_sync(0xffffffffu, w, 31);
+        const uint32_t warps = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+        v[k] = add_cut(before[k], warp ? warps : 0u);
     }
-    all = __shfl_sync(0xffffffffu, before, 31);
-    return upto - v + __shfl_sync(0xffffffffu, before - w, warp);
 }
 __device__ __forceinline__ void book_meet(int ctas) {
     if (ctas > 1) {
@@ -91,16 +110,15 @@ __device__ __forceinline__ void book_meet(int ctas) {
 
 // Counts of the CTAs before this one, and of all, from their shared memory; they meet once more before
 // any of them leaves.
-__device__ __forceinline__ void book_counts(int *s_count, int rank, int ctas, int &before, int &all) {
+__device__ __forceinline__ void book_counts(uint32_t *s_count, int rank, int ctas, uint32_t &before, uint32_t &all) {
     before = 0;
     all = *s_count;
     if (ctas == 1) return;
     all = 0;
     for (int c = 0; c < ctas; c++) {
-        uint32_t at;
-        int n;
+        uint32_t at, n;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(s_count)), "r"(c));
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n) : "r"(at));
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(n) : "r"(at));
         if (c < rank) before += n;
         all += n;
     }
@@ -127,32 +145,50 @@ __device__ __forceinline__ void book_span(int64_t n_pages, int rank, int ctas, i
     from = min(rank * per * kTilePages, n_pages);
     to = min(from + per * kTilePages, n_pages);
 }
-__device__ __forceinline__ int book_count(const int32_t *refs, int64_t n_pages, int rank, int ctas, bool in_use, int *s_warp) {
-    int64_t from, to;
-    book_span(n_pages, rank, ctas, from, to);
-    int n = 0, all;
-    for (int64_t p = from + threadIdx.x * 16; p < to; p += kTilePages) n += __popc(page_bits(refs, p, n_pages, in_use));
-    block_scan(n, s_warp, all);
-    return all;
-}
-// Calls take(place, page) for each such page of this CTA's, place counting from `first`, until `limit`.
-template <typename F>
-__device__ __forceinline__ void book_each(const int32_t *refs, int64_t n_pages, int rank, int ctas, bool in_use, int first, int limit,
-                                          int *s_warp, F &&take) {
-    int64_t from, to;
-    book_span(n_pages, rank, ctas, from, to);
-    for (int64_t tile = from; tile < to && first < limit; tile += kTilePages) {
-        const int64_t p0 = tile + threadIdx.x * 16;
-        uint32_t bits = p0 < n_pages ? page_bits(refs, p0, n_pages, in_use) : 0u;
-        int all, at = block_scan(__popc(bits), s_warp, all) + first;
-        while (bits && at < limit) {
-            const int k = __ffs(bits) - 1;
-            bits &= bits - 1;
-            take(at++, (int)(p0 + k));
-        }
-        first += all;
+// Pages of this CTA, in use or free.  The first tile is looked at once, at the start, and kept.
+struct BookPages {
+    const int32_t *refs;
+    int64_t n_pages, from, to;
+    bool in_use;
+    uint32_t bits, at;  // the first tile's, and this thread's place in it
+    uint32_t tile, count;  // pages found in the first tile, and in all
+    __device__ __forceinline__ BookPages(const int32_t *r, int64_t n, int rank, int ctas, bool used) : refs(r), n_pages(n), in_use(used) {
+        book_span(n, rank, ctas, from, to);
+        const int64_t p0 = from + threadIdx.x * 16;
+        bits = p0 < to ? page_bits(refs, p0, n_pages, in_use) : 0u;
     }
-}
+    // `scanned`: the first tile's scan, if it was made with others
+    __device__ __forceinline__ void count_all(uint32_t before, uint32_t all, uint32_t (*s_warp)[32]) {
+        at = before;
+        tile = count = all;
+        if (to - from <= kTilePages) return;
+        uint32_t n[1] = {0}, rest[1];
+        for (int64_t p = from + kTilePages + threadIdx.x * 16; p < to; p += kTilePages) n[0] += __popc(page_bits(refs, p, n_pages, in_use));
+        block_scan(n, s_warp, rest);
+        count += rest[0];
+    }
+    // Calls take(place, page) for each page, place counting from `first`, until `limit`.
+    template <typename F>
+    __device__ __forceinline__ void each(uint32_t first, uint32_t limit, uint32_t (*s_warp)[32], F &&take) {
+        auto go = [&](uint32_t b, uint32_t place, int64_t p0) {
+            while (b && place < limit) {
+                const int k = __ffs(b) - 1;
+                b &= b - 1;
+                take((int)place++, (int)(p0 + k));
+            }
+        };
+        go(bits, first + at, from + threadIdx.x * 16);
+        first += tile;
+        for (int64_t t = from + kTilePages; t < to && first < limit; t += kTilePages) {
+            const int64_t p0 = t + threadIdx.x * 16;
+            const uint32_t b = p0 < n_pages ? page_bits(refs, p0, n_pages, in_use) : 0u;
+            uint32_t n[1] = {(uint32_t)__popc(b)}, all[1];
+            block_scan(n, s_warp, all);
+            go(b, first + n[0], p0);
+            first += all[0];
+        }
+    }
+};
 
 // Last row whose first place is at most x, of n > 0 rows in order.
 template <typename F>
@@ -190,6 +226,7 @@ struct TakeRow {
     int len, count;    // tokens before, new tokens
     int entries;       // table entries that stay before the new ones
     int src;           // page to be copied, -1: none
+    int last;          // page of the last of those entries, where tokens are in it
     int token;         // first of its tokens among all
     int ok;
 };
@@ -204,21 +241,25 @@ template <bool FORK>
 __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_constant__ PTakePlan p) {
     pdl_begin();
     __shared__ TakeRow s_rows[kBookRows];
-    __shared__ int s_warp[32], s_cow, s_count;
+    __shared__ uint32_t s_warp[3][32], s_count;
+    __shared__ int s_cow, s_list[kBookFew];
     const int ctas = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
     const int shift = 31 - __clz(p.page);
     const int64_t cap = (int64_t)p.max_pages << shift;
     TakeRow *rows = p.B <= kBookRows ? s_rows : static_cast<TakeRow *>(p.rows);
     uint32_t *status = rank == 0 ? p.status : nullptr;
+    BookPages pages(p.refs, p.n_pages, rank, ctas, false);
     if (tid == 0) s_cow = 0;
-    __syncthreads();
-    int places = 0;
-    int64_t tokens = 0;
+    uint32_t places = 0, tokens = 0;
+    // Few pages and tokens for each sequence, all in one CTA: each thread sees to one sequence, with
+    // the pages by place in shared memory.  (Else a thread has a page, or a token, and looks its sequence
+    // up.)
+    bool few = FORK || p.total <= kBookThreads * 16;
     for (int b0 = 0; b0 < p.B; b0 += kBookThreads) {
         const int b = b0 + tid;
         TakeRow r = {};
         r.src = -1;
-        int64_t n = 0;
+        uint32_t n = 0;
         if (b < p.B) {
             int64_t len = p.lens[b];
             if constexpr (FORK) {
@@ -240,11 +281,9 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                     }
                 }
             } else {
-                n = p.wants[b];
-                if (n < 0) {
-                    or_status(status, QVG_DEV_BAD_INDEX);
-                    n = 0;
-                }
+                const int wanted = p.wants[b];
+                if (wanted < 0) or_status(status, QVG_DEV_BAD_INDEX);
+                n = (uint32_t)max(wanted, 0);
                 r.count = (int)n;
                 if (n > 0) {
                     if (len < 0 || len > cap) {
@@ -258,7 +297,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                         r.need = pages_for(len + n, shift) - have;
                         r.ok = 1;
                         if (len & (p.page - 1)) {
-                            const int last = p.table[(int64_t)b * p.max_pages + have - 1];
+                            const int last = r.last = p.table[(int64_t)b * p.max_pages + have - 1];
                             if (in_pool(last, p.n_pages) && p.refs[last] > 1) {
                                 r.src = last;
                                 r.need++;
@@ -269,61 +308,74 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                 }
             }
         }
-        int all;
+        // one scan for the tokens, the wants and, the first time, the free pages.  (A sequence whose tokens
+        // pass the total wants no page, which only a scan of the tokens can tell: then the wants are
+        // scanned again.)
+        const uint32_t wanted = r.need;
+        uint32_t v[3] = {n, wanted, b0 == 0 ? (uint32_t)__popc(pages.bits) : 0u}, all[3];
+        block_scan(v, s_warp, all);
+        if (b0 == 0) pages.count_all(v[2], all[2], s_warp);
         if constexpr (!FORK) {
-            // tokens in 64 bits: the low and the high part of a thread's count
-            int low, high;
-            const int bl = block_scan((int)(n & 0xFFFF), s_warp, low);
-            int64_t at = tokens + bl;
-            tokens += low;
-            if (__syncthreads_or(n >> 16 != 0)) {
-                at += (int64_t)block_scan((int)(n >> 16), s_warp, high) << 16;
-                tokens += (int64_t)high << 16;
-            }
-            r.token = (int)min(at, (int64_t)0x7FFFFFFF);
-            if (r.ok && at + n > p.total) {
+            r.token = (int)add_cut(tokens, v[0]);
+            const bool over = r.ok && (int64_t)r.token + n > p.total;
+            tokens = add_cut(tokens, all[0]);
+            if (over) {
                 r.ok = r.need = 0;
                 or_status(status, QVG_DEV_BAD_INDEX);
             }
+            few &= !__syncthreads_or(n > 16);
+            if (__syncthreads_or(over)) {
+                uint32_t w[1] = {(uint32_t)r.need}, sum[1];
+                block_scan(w, s_warp, sum);
+                v[1] = w[0];
+                all[1] = sum[0];
+            }
             if (r.ok && r.src >= 0) atomicAdd(&s_cow, 1);
         }
-        const int before = block_scan(r.need, s_warp, all);
-        r.first = places + before;
-        places += all;
+        r.first = (int)add_cut(places, v[1]);
+        places = add_cut(places, all[1]);
         if (b < p.B) rows[b] = r;
     }
-    const int mine = book_count(p.refs, p.n_pages, rank, ctas, false, s_warp);
-    if (tid == 0) s_count = mine;
+    if (tid == 0) s_count = pages.count;
     book_meet(ctas);
-    int before, free_pages;
+    uint32_t before, free_pages;
     book_counts(&s_count, rank, ctas, before, free_pages);
     // a sequence that wants nothing is served; others, if all up to it are
-    auto served = [&](const TakeRow &r) { return r.ok && (r.need == 0 || r.first + r.need <= free_pages); };
-    int take = places;
+    auto served = [&](const TakeRow &r) { return r.ok && (r.need == 0 || (uint32_t)r.first + (uint32_t)r.need <= free_pages); };
+    uint32_t take = places;
     if (take > free_pages) {
         take = 0;
         for (int b = tid; b < p.B; b += kBookThreads) {
-            const int end = rows[b].first + rows[b].need;
+            const uint32_t end = (uint32_t)rows[b].first + (uint32_t)rows[b].need;
             if (end <= free_pages) take = max(take, end);
         }
         __syncthreads();
-        take = (int)__reduce_max_sync(0xffffffffu, (unsigned)take);
-        if ((tid & 31) == 0) s_warp[tid >> 5] = take;
+        take = __reduce_max_sync(0xffffffffu, take);
+        if ((tid & 31) == 0) s_warp[0][tid >> 5] = take;
         __syncthreads();
-        take = (int)__reduce_max_sync(0xffffffffu, (unsigned)s_warp[tid & 31]);
+        take = __reduce_max_sync(0xffffffffu, s_warp[0][tid & 31]);
     }
-    book_each(p.refs, p.n_pages, rank, ctas, false, before, take, s_warp, [&](int place, int page) {
+    few &= ctas == 1 && p.B <= kBookRows && take <= kBookFew;
+    pages.each(before, take, s_warp, [&](int place, int page) {
+        p.refs[page] = 1;  // (this thread alone looks at this count)
+        if (few) {
+            s_list[place] = page;
+            return;
+        }
         const int b = row_of_place([&](int k) { return rows[k].first; }, p.B, place);
         p.table[(int64_t)b * p.max_pages + rows[b].entries + place - rows[b].first] = page;
-        p.refs[page] = 1;  // (this thread alone looks at this count)
         if constexpr (FORK) p.copies[p.B + b] = page;
     });
-    if (!FORK || ctas > 1) book_meet(ctas);  // the table is complete; nobody leaves while its count is read
+    if (few || !FORK || ctas > 1) book_meet(ctas);  // the table is complete; nobody leaves while its count is read
     const int grid = ctas * kBookThreads, me = rank * kBookThreads + tid;
     for (int b = me; b < p.B; b += grid) {
         const TakeRow r = rows[b];
         const bool ok = served(r), copied = ok && r.src >= 0 && r.need > 0;
         if (r.ok && !ok) or_status(p.status, QVG_DEV_NO_PAGES);
+        if (few && ok) {
+            for (int j = 0; j < r.need; j++) p.table[(int64_t)b * p.max_pages + r.entries + j] = s_list[r.first + j];
+            if (FORK && r.need > 0) p.copies[p.B + b] = s_list[r.first];
+        }
         if constexpr (FORK) {
             // (the entries that are shared, and the copies, are left to the next kernel)
             const bool lost = ok && r.need > 0 && !in_pool(r.src, p.n_pages);  // the parent's table is bad
@@ -341,11 +393,25 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                 p.copies[p.B + b] = copied ? p.table[(int64_t)b * p.max_pages + r.entries] : -1;
                 p.copies[2 * p.B + b] = copied ? r.len & (p.page - 1) : 0;
             }
+            if (few) {
+                for (int k = 0; k < r.count && r.token + k < p.total; k++) {
+                    int64_t slot = -1, pos = -1;
+                    if (ok) {
+                        pos = r.len + k;
+                        const int entry = (int)(pos >> shift), page = entry < r.entries ? r.last : s_list[r.first + entry - r.entries];
+                        if (in_pool(page, p.n_pages))
+                            slot = ((int64_t)page << shift) + (pos & (p.page - 1));
+                        else
+                            or_status(p.status, QVG_DEV_BAD_INDEX);
+                    }
+                    p.slots[r.token + k] = slot;
+                    p.positions[r.token + k] = pos;
+                }
+            }
         }
     }
     if constexpr (!FORK) {
-        tokens = min(tokens, p.total);
-        for (int64_t x = me; x < p.total; x += grid) {
+        for (int64_t x = few ? (int64_t)tokens + me : me; x < p.total; x += grid) {  // (few: what no sequence has)
             int64_t slot = -1, pos = -1;
             if (x < tokens) {
                 const int b = row_of_place([&](int k) { return rows[k].token; }, p.B, x);
@@ -364,6 +430,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
         }
         // shared last pages, which nobody else of this call writes: seldom any
         if (s_cow > 0) {
+            if (few) __syncthreads();  // (the table has its copies)
             for (int b = 0; b < p.B; b++) {
                 const TakeRow r = rows[b];
                 if (r.src < 0 || !served(r)) continue;
@@ -446,14 +513,17 @@ __global__ void __launch_bounds__(256) k_page_free(const __grid_constant__ PFree
 
 __global__ void __launch_bounds__(kBookThreads, 1) k_page_rank(const __grid_constant__ PCompactPlan p) {
     pdl_begin();
-    __shared__ int s_warp[32], s_count;
+    __shared__ uint32_t s_warp[1][32], s_count;
     const int ctas = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
-    const int mine = book_count(p.refs, p.n_pages, rank, ctas, true, s_warp);
-    if (tid == 0) s_count = mine;
+    BookPages pages(p.refs, p.n_pages, rank, ctas, true);
+    uint32_t v[1] = {(uint32_t)__popc(pages.bits)}, all[1];
+    block_scan(v, s_warp, all);
+    pages.count_all(v[0], all[0], s_warp);
+    if (tid == 0) s_count = pages.count;
     book_meet(ctas);
-    int before, live;
+    uint32_t before, live;
     book_counts(&s_count, rank, ctas, before, live);
-    book_each(p.refs, p.n_pages, rank, ctas, true, before, 0x7FFFFFFF, s_warp, [&](int place, int page) {
+    pages.each(before, kMost, s_warp, [&](int place, int page) {
         p.place[page] = place;
         if (place < p.out_pages) {
             p.old[place] = page;
@@ -512,7 +582,9 @@ int book_ctas(int64_t n_pages, int64_t tokens) {
     while (ctas < kBookCluster && (n_pages > (int64_t)ctas * kTilePages || tokens > (int64_t)ctas * kBookThreads * 4)) ctas *= 2;
     return ctas;
 }
-int copy_grid(int64_t items) { return (int)std::min<int64_t>(std::max<int64_t>(items, 1), 152 * 8); }
+// Blocks of a copy whose size only the device knows: so many that a block has one or a few 16 KB pieces
+// (24500 INT4 pages of 8 x 32 tokens, a third shared: 170 us; eight blocks an SM in a loop 202).
+int copy_grid(int64_t items) { return (int)std::min<int64_t>(std::max<int64_t>(items, 1), 152 * 256); }
 }  // namespace
 
 size_t take_bytes(int64_t sequences) { return sequences <= kBookRows ? 0 : (size_t)sequences * sizeof(TakeRow); }

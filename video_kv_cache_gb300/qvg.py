@@ -26,6 +26,7 @@ QVG_DEV_NONFINITE = 0x1
 QVG_DEV_TIMEOUT = 0x2
 QVG_DEV_BAD_INDEX = 0x4
 QVG_DEV_NO_PAGES = 0x8
+QVG_FEW_SEQS = 1024
 
 QVG_F16, QVG_BF16, QVG_F32 = 0, 1, 2
 QVG_QSCHEME_SYMMETRIC, QVG_QSCHEME_MIDRISE = 0, 1
