@@ -45,21 +45,22 @@ constexpr int kRowsShare = 4;              // stages of a share, at least
 template <int FMT, int RT>
 struct RowsShape {
     static constexpr bool WIDE = wide_format(FMT), FOUR = four_bits(FMT);
-    // Warps that compute.  4 bits, up to eight rows: what bounds them is instructions, of which a stage
-    // of 64 keys a warp needs the fewest for each key; four small CTAs an SM, and not two of four warps,
+    // Warps that compute.  4 bits: what bounds them is instructions, of which a stage of 64 keys a warp
+    // needs the fewest for each key; up to eight rows, four small CTAs an SM, and not two of four warps,
     // leave fewer of them waiting (one query of 32 sequences of 9000 to 20000, 8 heads of 4 queries each:
-    // 128 us in INT4; two CTAs of four warps 131, of 32 keys a warp 141; three CTAs 138).
+    // 128 us in INT4; two CTAs of four warps 131, of 32 keys a warp 141; three CTAs 138.  Four queries, in
+    // two CTAs: 223 us; of 32 keys a warp 237).
     static constexpr bool SMALL = FOUR && RT == 1;
     static constexpr int WARPS = SMALL ? 2 : 4;
     static constexpr int THREADS = 32 * (WARPS + 1);
     // 16-key tiles that a warp takes at a time: widening codes is a chain of short
     // instructions, which needs more of them side by side than feeding 16-bit rows does
-    static constexpr int KT = WIDE ? 1 : SMALL ? 4 : 2;
+    static constexpr int KT = WIDE ? 1 : FOUR ? 4 : 2;
     static constexpr int KEYS = 16 * KT * WARPS;                   // of a stage
     static constexpr int BOX = FOUR ? 64 : KEYS;                   // most that one copy brings
     static constexpr int CTAS = SMALL ? 4 : 2;    // an SM
     // 8 and 16 bits: 32 KB each; two stages and three CTAs, or smaller stages, are slower
-    static constexpr int STAGES = SMALL ? 2 : FOUR ? 5 : 3;
+    static constexpr int STAGES = FOUR ? 2 : 3;
     static constexpr int ROWB = WIDE ? 2 * kD : FOUR ? kD / 2 : kD;  // bytes of a cached row
     static constexpr uint32_t TILE = KEYS * ROWB;                  // bytes of its keys, or values
 };
@@ -88,6 +89,7 @@ constexpr size_t rows_smem() {
     using T = RowsShape<FMT, RT>;
     constexpr size_t bytes = T::STAGES * 2 * T::TILE + sizeof(RowsShared<FMT, RT, SHARES>);
     static_assert(T::CTAS * (bytes + 1024) <= 228 * 1024, "CTAs of an SM");
+    static_assert(32 * T::WARPS >= 8 * 8 * RT, "eight lanes for each row join the warps");
     static_assert((T::WARPS + 1) * 8 * RT * kRowsPad * 4 <= T::STAGES * 2 * T::TILE, "join");
     return bytes;
 }
