@@ -370,8 +370,9 @@ typedef enum {
  * finite as in 8 bits.
  *   k, v              two codes a byte, channel 2i in the low four bits: [..][64] bytes
  *   k_group, v_group  E4M3 [n_pages][n_heads][page_tokens][8], group g channels 16g .. 16g + 15
- * Group scales that a caller writes itself may be any E4M3 number up to 64 in magnitude, or NaN;
- * larger ones leave the attention over rows that see them unspecified. */
+ * Group scales that a caller writes itself may be any E4M3 number up to 64 in magnitude, or NaN; larger
+ * ones, and codes of -8, which qvg_page_write does not store, leave the attention over rows that see them
+ * unspecified (qvg_page_read gives what they stand for). */
 typedef struct {
     void *k;
     void *v;
@@ -492,16 +493,18 @@ size_t qvg_page_attention_workspace_bytes(const qvg_page_attention_params *param
  *   O_i = sum_j p_j v_j,  p = softmax over the keys j that i sees of scale * (q_i . k_j)
  *   lse_i = log sum_j exp(scale * (q_i . k_j))    (lse: float [total_q][n_q_heads] or NULL)
  * A query that sees no key gets O = 0 and lse = -infinity.  What a query does not see cannot
- * change its row, NaN, infinities and E4M3 codes that are NaN included, nor may a scale that it
+ * change its row, NaN, infinities, E4M3 codes and group scales that are NaN included, nor may a scale that it
  * does not see cost it more than the roundings below.  Values that are not finite leave lse as
  * the scores give it.
  * Scores, softmax and sums are fp32.  The weights p enter the product with the values in
- * 16 bits, relative to a running maximum: in q_dtype, or for the 8-bit formats in fp16, after
+ * 16 bits, relative to a running maximum: in q_dtype, or for the 8-bit and 4-bit formats in fp16, after
  * the value's scale is multiplied in (a relative 2^-11 each, or 2^-25 of the largest value that
  * the query sees); O is rounded once to out_dtype.  Over 8-bit pages, with more than 16 query
  * rows (tokens x grouped heads) a key/value head, a bf16 output and no lse, keys and values are
  * multiplied by their scales and rounded to fp16 instead (a relative 2^-11 each, or 2^-30 and
- * 2^-25 of the largest key and value that the query sees).
+ * 2^-25 of the largest key and value that the query sees).  4-bit pages are like 8-bit ones in all of
+ * this, with a group's scale times a code, which is exact, in the place of the code; where scales are
+ * multiplied in, the product of the row's and the group's is rounded to fp16 too (2^-10 in all).
  * Out-of-range page-table entries (read as page 0), lengths past the table (cut), and cu_q
  * out of order, past total_q or with more than max_q queries (cut; the rows left out are
  * not written) are reported as QVG_DEV_BAD_INDEX; a wait in a kernel's pipeline that gives

@@ -45,7 +45,7 @@ def _prm(**kw):
 
 
 def test_refusals(lib, mem, monkeypatch):
-    pages, other = qvg.qvg_pages(mem, mem, mem, mem), qvg.qvg_pages(mem + 256, mem + 256, mem, mem)
+    pages, other = qvg.qvg_pages(mem, mem, mem, mem), qvg.qvg_pages(*(mem + (k << 20) for k in (1, 2, 3, 4)))  # (never read)
     far = mem + 4096
 
     def append(p=None, g=pages, refs=mem, table=mem, lens=mem, counts=mem, slots=mem, pos=mem, copies=mem, ws=mem, size=4096):
@@ -88,6 +88,9 @@ def test_refusals(lib, mem, monkeypatch):
     assert fork(parents=None) == fork(copies=mem + 1) == 1
     assert free(first=None) == free(first=mem + 2) == free(last=mem + 2) == 1 and free(first=None, last=mem) == qvg.QVG_ERR_CUDA
     assert compact(_prm(out_pages=0)) == compact(to=pages) == compact(out_table=mem) == compact(out_refs=mem) == compact(live=None) == 1
+    inside = qvg.qvg_pages(mem + 8 * 2 * 16 * 128, mem + (2 << 20), mem + (3 << 20), mem + (4 << 20))  # its last page of keys
+    behind = qvg.qvg_pages(mem + 9 * 2 * 16 * 128, mem + (2 << 20), mem + (3 << 20), mem + (4 << 20))
+    assert compact(to=inside) == 1 and compact(to=behind) == qvg.QVG_ERR_CUDA
     assert copies(n=-1) == copies(src=None) == copies(dst=mem + 2) == copies(rows=mem + 1) == copies(to=None) == 1
     assert copies(to_pages=0) == 1 and copies(to_pages=1 << 28) == 2 and copies(n=1 << 31) == 2
     assert copies(n=0, src=None, dst=None) == 0

@@ -452,7 +452,10 @@ class PagedKV:
             object.__setattr__(self, name, value)
 
     def __reduce__(self):  # a copy describes its own tensors' memory
-        return PagedKV, (self.k, self.v, self.k_scale, self.v_scale, self.k_group, self.v_group)
+        parts = (self.k, self.v, self.k_scale, self.v_scale, self.k_group, self.v_group)
+        # (torch does not pickle tensors of 8-bit and 4-bit floats: their bytes go, and their type)
+        odd = (torch.float8_e4m3fn, torch.float4_e2m1fn_x2)
+        return _pages_of, tuple((t.dtype, t.view(torch.uint8)) if t is not None and t.dtype in odd else (None, t) for t in parts)
 
     def buffers(self) -> _c.qvg_pages:
         return self._buffers
@@ -460,6 +463,10 @@ class PagedKV:
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
                    (self.k, self.v, self.k_scale, self.v_scale, self.k_group, self.v_group) if t is not None)
+
+
+def _pages_of(*parts):
+    return PagedKV(*(t if dtype is None else t.view(dtype) for dtype, t in parts))
 
 
 def allocate_pages(n_pages: int, heads: int, page_tokens: int = 64, dtype=torch.bfloat16,
@@ -524,11 +531,14 @@ def page_read(kv: PagedKV, page_table: torch.Tensor, seq_lens: torch.Tensor, cou
     _check_scratch(status, None, dev)
     shape = (n_seqs, 2 * kv.heads, count, D)
     if out is None:
+        _need(out_dtype in _DT, "out_dtype must be fp16, bf16 or fp32")
         out = _empty(shape, out_dtype, kv.k.device, stream)
-    stride = out.stride()
-    _need(out.get_device() == dev and out.shape == shape and out.dtype in _DT and
-          (count == 0 or (stride[3] == 1 and (count == 1 or stride[2] == D))),
-          "out must be [sequences][2 * heads][count][128] on the pages' GPU, with contiguous tokens")
+        stride = (2 * kv.heads * count * D, count * D)
+    else:
+        stride = out.stride()
+        _need(out.get_device() == dev and out.shape == shape and out.dtype in _DT and
+              (count == 0 or (stride[3] == 1 and (count == 1 or stride[2] == D))),
+              "out must be [sequences][2 * heads][count][128] on the pages' GPU, with contiguous tokens")
     prm = _c.qvg_page_read_params(n_seqs, kv.heads, D, kv.page_tokens, kv.format, _DT[out.dtype],
                                   kv.n_pages, max_pages, first, count,
                                   stride[0] if n_seqs > 1 else 0, stride[1])

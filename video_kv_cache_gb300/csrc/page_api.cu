@@ -476,15 +476,19 @@ qvg_status qvg_page_compact(const qvg_page_table_params *prm, const qvg_pages *p
     if (rc == QVG_OK) rc = check_pages(pages, prm->format);
     if (rc == QVG_OK) rc = check_pages(to, prm->format);
     if (rc != QVG_OK) return rc;
-    if (prm->out_pages < 1 || to->k == pages->k || to->v == pages->v || out_table == page_table || out_refs == refs)
-        return QVG_ERR_INVALID_ARG;
+    if (prm->out_pages < 1 || out_table == page_table || out_refs == refs) return QVG_ERR_INVALID_ARG;
+    const PoolCopy pool = pool_copy(prm, pages, to);
+    for (int a = 0; a < 6; a++)  // another pool, not a part of this one
+        if (pool.src[a] && pool.src[a] < pool.dst[a] + pool.bytes[a] * prm->out_pages &&
+            pool.dst[a] < pool.src[a] + pool.bytes[a] * prm->n_pages)
+            return QVG_ERR_INVALID_ARG;
     if (!refs || !page_table || !seq_lens || !out_table || !out_refs || !live || !aligned(refs, 16) || !aligned(page_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(out_table, 4) || !aligned(out_refs, 4) || !aligned(live, 4))
         return QVG_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < compact_bytes(prm) || !aligned(workspace, 16)) return QVG_ERR_WORKSPACE;
     if ((rc = ready()) != QVG_OK) return rc;
     PCompactPlan p{};
-    p.pool = pool_copy(prm, pages, to);
+    p.pool = pool;
     p.B = prm->n_seqs;
     p.max_pages = prm->max_pages;
     p.n_pages = prm->n_pages;
