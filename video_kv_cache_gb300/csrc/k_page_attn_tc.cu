@@ -48,6 +48,21 @@
 // the issue slots with the exponentials; with one factor instead of two (a scale rounded to
 // fp16, an error that all channels of a key share) the first two took 20 and 34 us less.
 //
+// 4-bit pages: the same, with a group's scale times a code, exact in fp16, in the place of an 8-bit code
+// (page_codes.cuh).  Raw tiles are 4 KB of codes, in lines of two rows, and 512 bytes of group scales; a
+// thread widens a group of 16 channels.  INT4 codes come out in pairs of channels (i, i + 4) of eight:
+// keys meet queries that are put in that order, and the outputs' columns are put back at the end.  FOLD
+// multiplies the row's scale into the group's, in fp16, and widens by that.  Otherwise the softmax
+// reads and scales its scores once, weighs them against the old base before the vote, and does so again
+// if the base moves (twice, as for 8 bits, leaves the tensor cores waiting longer: 4680 x 32760 x 12
+// heads of E2M1 with the log-sum-exp 1121 us; folded, where scores need no scales, it is the other way
+// round, 864 and 920).  Scales of values multiplied into them there too: 1147.
+// 4680 over 32760 of 12 heads, cold caches: E2M1 873 us (1079 TFLOP/s), INT4 1003; with the log-sum-exp
+// 1045 and 1080; six causal prompts of 17 to 2000 queries over 500 to 9000 keys, 32 heads on 8, fp16, window
+// 4096: 419 and 421.  What bounds: 52 % of the issue slots are busy, a tile pair takes three times its
+// products' time (tensor pipes idle while scores wait for softmax instructions, 12900 of a warp in all,
+// and those for shared memory, barriers and the instruction cache).
+//
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
 // product runs over the 16-key steps in sight, and the rest of the outer steps is zeroed.  What some
@@ -640,7 +655,10 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                         if constexpr (FOUR) {
                             uint32_t h[8];
                             if constexpr (FOLD) {
-                                const __half2 f = __hmul2(__low2half2(as_half2(group_pair(four_t[v]))), as_half2(factors[u * 16].x));
+                                // the group's scale times the row's, rounded once
+                                const uint2 row = factors[u * 16];
+                                const __half2 t2 = __low2half2(as_half2(group_pair(four_t[v])));
+                                const __half2 f = __hfma2(t2, as_half2(row.x), __hmul2(t2, as_half2(row.y)));
                                 widen4_by<FMT>(four_w[v].x, f, code_bits, h);
                                 widen4_by<FMT>(four_w[v].y, f, code_bits, h + 4);
                             } else {
