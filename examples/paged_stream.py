@@ -8,6 +8,7 @@ Once more than ``window`` chunks are cached, the oldest is read back, compressed
 
     python examples/paged_stream.py                 # 12 heads, chunks of 3 x 32 x 48 tokens
     python examples/paged_stream.py --format bf16 --window 2
+    python examples/paged_stream.py --format int4
 
 Inputs are seeded random numbers in the place of a model's projections.
 """
@@ -25,7 +26,8 @@ import torch
 
 from video_kv_cache_gb300 import api
 
-FORMATS = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+FORMATS = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8,
+           "e2m1": torch.float4_e2m1fn_x2, "int4": torch.uint8}
 
 
 @dataclass

@@ -553,6 +553,32 @@ def test_calls_back_to_back(nq, seqs, n, fmt):
     assert bool(outs[0].float().abs().sum(-1).gt(0).all()) and bool(torch.isfinite(outs[0].float()).all())
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "int4"])
+def test_the_example_streams_through_4_bit_pages(fmt):
+    # chunks written, attended to, read back and compressed: every chunk's attention against 64 bits
+    import importlib.util
+    import os
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("paged_stream4", os.path.join(root, "examples", "paged_stream.py"))
+    example = importlib.util.module_from_spec(spec)
+    sys.modules["paged_stream4"] = example
+    spec.loader.exec_module(example)
+    s = example.make_stream(heads=2, grid=(2, 6, 8), window=2, chunks=4, fmt=fmt, page=16, C=8)
+    for k in range(4):
+        Q, K, V = example.inputs(s, k, "cuda")
+        pos = example.positions(s, "cpu")
+        out = example.step(s, Q, K, V)
+        assert s.packed == max(0, k - 2) and len(s.table) == min(k + 1, 3) * 6
+        n = len(s.table) * 16
+        tab = torch.tensor(s.table, dtype=torch.int32)
+        Kp, Vp = m4.pool_rows(s.pages, "k", tab, n), m4.pool_rows(s.pages, "v", tab, n)
+        Qr = api.rope(Q, pos.cuda(), s.rope).double().cpu()
+        for h in range(2):
+            want, _, bound, _ = pm.attend(Qr[:, h], Kp[h], Vp[h], 128 ** -0.5, False, 0, 2.0 ** -11, BF, 2.0 ** -10, 2.0 ** -10)
+            tp._within(out[:, h], want, bound, "chunk %d head %d" % (k, h))
+
+
 def test_offsets_past_32_bits():
     # rows past 2^32 bytes of codes: at the end of the pool, in 4 bits
     heads, page = 8, 128
