@@ -450,6 +450,8 @@ class PagedKV:
                                                       _ptr(self.k_scale), _ptr(self.v_scale),
                                                       _ptr(self.k_group), _ptr(self.v_group)))):
             object.__setattr__(self, name, value)
+        object.__setattr__(self, "_copy_params", _c.qvg_page_table_params(
+            1, self.heads, D, self.page_tokens, self.format, 1, self.n_pages, 0, 0))
 
     def __reduce__(self):  # a copy describes its own tensors' memory
         parts = (self.k, self.v, self.k_scale, self.v_scale, self.k_group, self.v_group)
@@ -639,6 +641,11 @@ def _book_workspace(prm, kv: PagedKV, workspace, stream):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _same_pages(kv: PagedKV, out: PagedKV, dev: int):
+    _need(out.gpu == dev and out.heads == kv.heads and out.page_tokens == kv.page_tokens and out.format == kv.format,
+          "out must be pages of the same heads, page_tokens and format, on the same GPU")
+
+
 def page_copy(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, *, rows: torch.Tensor | None = None,
               out: PagedKV | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """Copy pages ``src`` to ``dst`` (int32 [n]; negative: skipped), of all heads, keys and values
@@ -646,16 +653,18 @@ def page_copy(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, *, rows: torch.
     ``dst``, ``kv`` itself by default.  No page may be written twice, nor, in one pool, be written and
     read."""
     dev = _gpu(kv.k, "pages")
-    out = kv if out is None else out
     n = src.shape[0] if src.dim() == 1 else -1
-    for t, what in ((src, "src"), (dst, "dst"), (rows, "rows")):
-        if t is not None:
-            _index(t, torch.int32, (n,), what, dev)
-    _need(out.gpu == dev and out.heads == kv.heads and out.page_tokens == kv.page_tokens and out.format == kv.format,
-          "out must be pages of the same heads, page_tokens and format, on the same GPU")
-    _check_scratch(status, None, dev)
-    prm = _c.qvg_page_table_params(1, kv.heads, D, kv.page_tokens, kv.format, 1, kv.n_pages, 0, 0)
-    rc = _c.qvg_page_copy(prm, n, kv._buffers, src.data_ptr(), dst.data_ptr(), _ptr(rows), out._buffers,
+    _index(src, torch.int32, (n,), "src", dev)
+    _index(dst, torch.int32, (n,), "dst", dev)
+    if rows is not None:
+        _index(rows, torch.int32, (n,), "rows", dev)
+    if out is None:
+        out = kv
+    else:
+        _same_pages(kv, out, dev)
+    if status is not None:
+        _check_scratch(status, None, dev)
+    rc = _c.qvg_page_copy(kv._copy_params, n, kv._buffers, src.data_ptr(), dst.data_ptr(), _ptr(rows), out._buffers,
                           out.n_pages, _ptr(status), _stream_handle(stream))
     if rc != _c.QVG_OK:
         raise _c.QVGError(rc, "qvg_page_copy")
@@ -733,10 +742,9 @@ def page_compact(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_
     pool with its table and refs stays as it is; what ``out`` has no room for is left out, with
     QVG_DEV_NO_PAGES."""
     dev, n_seqs, max_pages, prm = _book(kv, refs, page_table, seq_lens, status, workspace, out_pages=out.n_pages)
-    _need(out.gpu == dev and out.heads == kv.heads and out.page_tokens == kv.page_tokens and out.format == kv.format,
-          "out must be pages of the same heads, page_tokens and format, on the same GPU")
+    _same_pages(kv, out, dev)
     workspace, scratch, size = _book_workspace(prm, kv, workspace, stream)
-    table = _empty((n_seqs, max_pages), torch.int32, kv.k.device, stream)
+    table = _empty_as(page_table, (n_seqs, max_pages), torch.int32, stream)
     new_refs = _empty((out.n_pages,), torch.int32, kv.k.device, stream)
     live = _empty((1,), torch.int32, kv.k.device, stream)
     rc = _c.qvg_page_compact(prm, kv._buffers, refs.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), out._buffers,
