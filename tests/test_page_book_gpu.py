@@ -374,6 +374,14 @@ def test_many_sequences(rows, pages):
     counts = [r.randint(0, 20) for b in range(rows)]
     assert _append(kv, s, counts) == m.append(counts, sum(counts))
     m.check(kv, *s)
+    # all cut back to the prompts' first rows, many into a page that they share: whoever grows copies it
+    drop = [max(0, n - 13) for n in m.size]
+    api.page_free(kv, *s, last=_int(drop))
+    m.give([0] * rows, drop)
+    for counts in ([1 if b % 5 == 0 else 0 for b in range(rows)], [b % 3 for b in range(rows)]):
+        got, want = _append(kv, s, counts), m.append(counts, sum(counts))
+        assert got == want
+    m.check(kv, *s)
 
 
 def test_what_cannot_be_done_is_left_and_reported():
@@ -460,6 +468,28 @@ def test_capture_replay_other_streams_and_layers():
         m.check(layers[0], *s)
         for got, want in zip(_pools(layers[1]), m2.pools):
             assert torch.equal(m2._rows(got, layers[1]), want)
+
+
+def test_a_cluster_of_ctas_is_captured_and_replayed():
+    kv = api.allocate_pages(100000, 1, 16, I8)
+    g = torch.Generator().manual_seed(3)
+    start = torch.randint(0, 2, (kv.n_pages,), generator=g).to(torch.int32)
+    refs, table, lens = start.cuda(), torch.full((3, 4000), -1, dtype=torch.int32, device="cuda"), _int([0, 0, 0])
+    counts, total = _int([60000, 1, 17]), 60018
+    api.page_append(kv, refs, table, lens, counts, total)   # (once before, as a capture wants)
+    want = [t.clone() for t in (refs, table, lens)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        slots, _ = api.page_append(kv, refs, table, lens, counts, total)
+    free = (start == 0).nonzero()[:, 0]
+    for _ in range(3):
+        for t, v in ((refs, start.cuda()), (table, torch.full_like(table, -1)), (lens, torch.zeros_like(lens))):
+            t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((refs, table, lens), want))
+        i = torch.arange(60000)
+        assert torch.equal(slots[:60000].cpu(), free[i // 16] * 16 + i % 16) and int(slots[60000]) == int(free[3750]) * 16
 
 
 @pytest.mark.parametrize("fmt", [BF, E4, m4.E2M1])

@@ -19,6 +19,7 @@ constexpr int kBookThreads = 1024;
 constexpr int kTilePages = kBookThreads * 16;        // pages that a CTA counts at a time
 constexpr int kBookCluster = 8;
 constexpr int kBookRows = kBookSharedRows;
+constexpr int kBookCows = 256;
 constexpr int kBookFew = 1024;                       // pages taken that are handed over in shared memory
 
 __device__ __forceinline__ bool in_pool(int page, int64_t n_pages) { return (unsigned)page < (uint64_t)n_pages; }
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
     pdl_begin();
     __shared__ TakeRow s_rows[kBookRows];
     __shared__ uint32_t s_warp[3][32], s_count;
-    __shared__ int s_cow, s_list[kBookFew];
+    __shared__ int s_cow, s_list[kBookFew], s_cows[kBookCows];  // shared last pages: how many, whose
     const int ctas = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
     const int shift = 31 - __clz(p.page);
     const int64_t cap = (int64_t)p.max_pages << shift;
@@ -330,7 +331,10 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                 v[1] = w[0];
                 all[1] = sum[0];
             }
-            if (r.ok && r.src >= 0) atomicAdd(&s_cow, 1);
+            if (r.ok && r.src >= 0) {
+                const int k = atomicAdd(&s_cow, 1);
+                if (k < kBookCows) s_cows[k] = b;
+            }
         }
         r.first = (int)add_cut(places, v[1]);
         places = add_cut(places, all[1]);
@@ -431,7 +435,9 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
         // shared last pages, which nobody else of this call writes: seldom any
         if (s_cow > 0) {
             if (few) __syncthreads();  // (the table has its copies)
-            for (int b = 0; b < p.B; b++) {
+            const bool listed = s_cow <= kBookCows;  // (in any order: nothing depends on it)
+            for (int c = 0; c < (listed ? s_cow : p.B); c++) {
+                const int b = listed ? s_cows[c] : c;
                 const TakeRow r = rows[b];
                 if (r.src < 0 || !served(r)) continue;
                 const int dst = p.table[(int64_t)b * p.max_pages + r.entries];
