@@ -568,3 +568,11 @@ def test_refused_arguments():
         with pytest.raises(qvg.QVGError) as e:
             call()
         assert e.value.code == qvg.QVG_ERR_WORKSPACE
+
+
+def test_numbers_in_the_place_of_vectors_are_refused():
+    kv = api.allocate_pages(8, 1, 16, BF)
+    refs, table, lens = _state(kv, 1, 4)
+    for args in ((refs, table, lens[0]), (lens[0], table, lens), (refs, lens[0], lens), (refs, table[0], lens)):
+        with pytest.raises(ValueError):
+            api.page_free(kv, *args, last=_int([ALL]))

@@ -615,8 +615,8 @@ def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int
     """(GPU, sequences, entries of a row, parameters) of a call on the pages of sequences."""
     dev, shape = kv.gpu, page_table.shape
     # (one condition for what is as it should be, the checks one by one for what is not)
-    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and len(shape) == 2 and len(seq_lens) == shape[0] > 0 < shape[1]
-            and len(refs) == kv.n_pages and seq_lens.dim() == refs.dim() == 1
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and len(shape) == 2 and seq_lens.dim() == refs.dim() == 1
+            and len(seq_lens) == shape[0] > 0 < shape[1] and len(refs) == kv.n_pages
             and page_table.dtype is torch.int32 is seq_lens.dtype is refs.dtype
             and page_table.get_device() == seq_lens.get_device() == refs.get_device() == dev
             and page_table.is_contiguous() and seq_lens.is_contiguous() and refs.is_contiguous()):
