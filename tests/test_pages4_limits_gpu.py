@@ -1,0 +1,74 @@
+"""GPU checks of 4-bit pages at the ends of their ranges: weights and value scales as large as the running
+references let them get."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import pages4_model as m4
+from tests import pages_model as pm
+from tests import test_pages_gpu as tp
+from video_kv_cache_gb300 import api
+from video_kv_cache_gb300 import build as qbuild
+from video_kv_cache_gb300 import qvg
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32, E2M1, INT4 = torch.bfloat16, torch.float16, torch.float32, m4.E2M1, m4.INT4
+JUST_BELOW_8 = float(np.nextafter(np.float32(8), np.float32(0)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    qbuild.build()
+    qvg.load()
+    torch.cuda.set_device(0)
+
+
+def _one_key_above(fmt, n, at, base, above, size):
+    """n keys of score `base` and value 1, but for key `at`: score base + above, value `size`."""
+    page = 64
+    kv = api.allocate_pages(-(-n // page), 1, page, fmt)
+    code = {v: c for c, v in enumerate(m4.VALUES[fmt])}
+    kv.k.view(torch.uint8).zero_()
+    kv.k.view(torch.uint8)[..., 0] = code[4.0]                # channel 0 of the keys alone
+    kv.k_group.view(torch.uint8).fill_(0x40)                  # 2
+    kv.k_scale.fill_(base / 8)
+    kv.v.view(torch.uint8).fill_(code[1.0] * 17)
+    kv.v_group.view(torch.uint8).fill_(0x38)                  # 1
+    kv.v_scale.fill_(1.0)
+    kv.k_scale[at // page, 0, at % page] = (base + above) / 8
+    kv.v_scale[at // page, 0, at % page] = size
+    return kv, torch.arange(kv.n_pages, dtype=torch.int32).view(1, -1)
+
+
+@pytest.mark.parametrize("fmt", [E2M1, INT4])
+@pytest.mark.parametrize("n", [256, 2048])        # one item, and four splits of it
+@pytest.mark.parametrize("base,above,size", [
+    (0.0, 7.9999, JUST_BELOW_8),                  # neither the base of the weights nor the values' reference moves
+    (0.0, 7.9999, -JUST_BELOW_8),
+    (0.0, 7.999, 7.9),
+    (2.0 ** 20, 8.0, 7.0),
+    (2.0 ** 22, 7.5, JUST_BELOW_8),
+    (2.0 ** 23 - 16, 8.0, 7.0),
+])
+def test_a_weight_and_a_value_scale_at_their_limits(fmt, n, base, above, size):
+    # key 200 lies in the second tile, which goes by the first one's references: its weight may be 2^8, and
+    # its value's scale eight times the first tile's.  Weights meet the values in fp16
+    nq, at = 40, 200
+    kv, table = _one_key_above(fmt, n, at, base, above, size)
+    Q = torch.zeros((nq, 1, 128), dtype=HF)
+    Q[:, :, 0] = 1.0
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    K, V = m4.pool_rows(kv, "k", table[0], n)[0], m4.pool_rows(kv, "v", table[0], n)[0]
+    for causal in (False, True):
+        for out_dtype, lse in ((F32, False), (HF, True), (BF, True)):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            got = api.page_attention(Q.cuda(), kv, table.cuda(), lens, causal=causal, scale=math.log(2), out_dtype=out_dtype,
+                                     return_lse=lse, status=status)
+            want, want_lse, bound, lse_bound = pm.attend(Q[:, 0].double(), K, V, math.log(2), causal, 0, 2.0 ** -11, out_dtype)
+            if lse:
+                tp._within(got[1][:, 0], want_lse, lse_bound, "lse")
+                got = got[0]
+            assert int(status) == 0
+            tp._within(got[:, 0], want, bound, "output")

@@ -291,7 +291,9 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
     constexpr bool WIDE = T::WIDE, FOUR = T::FOUR;
     constexpr bool BF = WIDE && QB;  // type of all operands; 8-bit and 4-bit pages: fp16
     constexpr int SLOTS = T::SLOTS;
-    constexpr int kUnwiden = FMT == PF_INT4 && !FOLD ? 1 : 0;  // INT4 keys are widened to half of what they stand for
+    // INT4 codes, not folded, are widened to half of what they stand for: the keys' scales make up for it,
+    // and for values the outputs at the end (in their factors, weights would pass fp16's range)
+    constexpr int kUnwiden = FMT == PF_INT4 && !FOLD ? 1 : 0;
     constexpr int MMA_WARP = 16, LOAD_WARP = 17, WIDEN_WARP = 20;
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *sQ = sm, *sKV = sm + 2 * kSlot, *sRaw = sKV + SLOTS * kSlot, *sGroups = sRaw + T::RAWS * T::RAW;
@@ -597,9 +599,9 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 if (value) {
                     // the reference moves only when a scale passes it by 2^3: codes of at most
                     // 448 times 2^3 * 2^kValueShift stay below fp16's largest, 65504, and so do
-                    // weights of at most 2^kLazy
+                    // weights of at most 2^kLazy times that (2^15)
                     if (j == 0 || ee > e + 2) e = ee;
-                    const float f = sc * __uint_as_float((uint32_t)(127 + kValueShift + kUnwiden - e) << 23);
+                    const float f = sc * __uint_as_float((uint32_t)(127 + kValueShift - e) << 23);
                     if constexpr (FOLD)
                         sh.vf[buf][x] = scale_pair(f);
                     else
@@ -972,7 +974,7 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                 if constexpr (!WIDE && FMT != PF_E4M3) check_sizes();
                 float inv = 1.f;
                 if (whole) inv = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-                if constexpr (!WIDE) inv = sh.bad[t][quarter] >> lane & 1u ? NAN : ldexpf(inv, e - kValueShift);
+                if constexpr (!WIDE) inv = sh.bad[t][quarter] >> lane & 1u ? NAN : ldexpf(inv, e - kValueShift + kUnwiden);
                 const int64_t tok = sq.q0 + i;
                 const int64_t part = (tail * S + split) * p.unit + t * kTcM + row;
                 // The rows go out through shared memory, in the place of this tile's Q, which
