@@ -1,5 +1,5 @@
 """GPU checks of 4-bit pages at the ends of their ranges: weights and value scales as large as the running
-references let them get."""
+references let them get, every group scale read back."""
 import math
 
 import numpy as np
@@ -72,3 +72,24 @@ def test_a_weight_and_a_value_scale_at_their_limits(fmt, n, base, above, size):
                 got = got[0]
             assert int(status) == 0
             tp._within(got[:, 0], want, bound, "output")
+
+
+@pytest.mark.parametrize("fmt", [E2M1, INT4])
+def test_reads_give_what_every_group_scale_stands_for(fmt):
+    # all 256 bytes, over 64 (which page_write does not store) and NaN among them, with all 16 codes each: a
+    # scale times a code is exact, and one rounding is left, that of the row's scale
+    kv = api.allocate_pages(2, 1, 16, fmt)
+    codes = torch.tensor([(2 * i) | (2 * i + 1) << 4 for i in range(8)], dtype=torch.uint8).repeat(8)
+    scales = torch.arange(256).to(torch.uint8).view(2, 1, 16, 8)
+    for pool, group in ((kv.k, kv.k_group), (kv.v, kv.v_group)):
+        pool.view(torch.uint8).copy_(codes.expand(2, 1, 16, 64))
+        group.view(torch.uint8).copy_(scales)
+    table, lens = torch.tensor([[0, 1]], dtype=torch.int32), torch.tensor([32], dtype=torch.int32).cuda()
+    for ks, vs in ((1.0, 0.3), (0.0, -2.0 ** 100)):
+        kv.k_scale.fill_(ks)
+        kv.v_scale.fill_(vs)
+        X = api.page_read(kv, table.cuda(), lens, 32, out_dtype=F32)[0].cpu()
+        for which, name in enumerate(("k", "v")):
+            want = m4.pool_rows(kv, name, table[0], 32)[0].float()
+            assert torch.equal(X[which].isnan(), want.isnan()) and int(want.isnan().sum()) == 32
+            assert torch.equal(X[which].nan_to_num(), want.nan_to_num())

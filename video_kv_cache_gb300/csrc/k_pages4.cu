@@ -337,13 +337,15 @@ __global__ void __launch_bounds__(256) k_page_read4(PReadPlan p) {
     for (int u = 0; u < kReadRows; u++) {
         if (i0 + 16 * u >= p.count) break;
         uint32_t w[4];
-        widen4<FMT>(raw[u], GroupScale<FMT>(__low2half2(as_half2(group_pair(t[u])))), CodeBits(0), w);
+        // (the code first, then its scale: exact for scales up to E4M3's largest, 448, where widen4's
+        // offsets pass fp16's range from 128 on)
+        widen4_by<FMT>(raw[u], __low2half2(as_half2(group_pair(t[u]))), CodeBits(0), w);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            v[pair_channel<FMT>(i, 0)] = f.x * (1.f / kWiden<FMT>) * s[u];
-            v[pair_channel<FMT>(i, 1)] = f.y * (1.f / kWiden<FMT>) * s[u];
+            v[pair_channel<FMT>(i, 0)] = f.x * s[u];
+            v[pair_channel<FMT>(i, 1)] = f.y * s[u];
         }
         const int64_t x = b * p.xs + tensor * p.xt + (i0 + 16 * u) * kD + 8 * l;
         if constexpr (DT == DT_F32) {
