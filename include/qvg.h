@@ -539,6 +539,9 @@ typedef struct {
     int64_t n_pages;
     int64_t total;       /* qvg_page_append: entries of slots and positions, < 2^31 */
     int64_t out_pages;   /* qvg_page_compact: pages of the other pool */
+    int64_t *starts;     /* device int64 [n_seqs], or NULL (0 for every sequence): the position of the
+                            token that is each sequence's first now.  qvg_page_free moves it on,
+                            qvg_page_fork copies it, qvg_page_append counts from it */
 } qvg_page_table_params;
 
 /* Workspace bytes that qvg_page_append and qvg_page_fork need (out_pages 0), or qvg_page_compact does;
@@ -559,6 +562,9 @@ qvg_status qvg_page_copy(const qvg_page_table_params *params, int64_t n, const q
 /* Sequence b grows by counts[b] tokens (int32 [n_seqs], 0: none): seq_lens and the page table are
  * brought up to date, and slots and positions (int64 [total]) of the new tokens are written, sequence
  * after sequence, as qvg_page_write and qvg_rope take them; entries behind the last token are -1.
+ * A token's position is its place in the sequence plus starts[b].  Without starts it is the place alone,
+ * which is no position to turn by once qvg_page_free has dropped first tokens: what is kept was turned by
+ * positions that lie as many tokens further on.
  * A last page that is part filled and that other entries name too (refs > 1) is first replaced by a copy
  * of its rows in use; copies (int32 [3][n_seqs], or NULL) gets source, destination and rows of it, -1, -1, 0
  * where there is none.
@@ -573,7 +579,7 @@ qvg_status qvg_page_append(const qvg_page_table_params *params, const qvg_pages 
 
 /* Sequence b, which has to be empty, becomes a fork of sequence parents[b] (int32 [n_seqs], negative:
  * none): the parent's whole pages are shared, its last one, if part filled, is copied as far as it
- * is filled.  copies (int32 [4][n_seqs]) gets source, destination and rows of that copy, -1, -1, 0 where
+ * is filled, starts[b] becomes the parent's.  copies (int32 [4][n_seqs]) gets source, destination and rows of that copy, -1, -1, 0 where
  * there is none, and the whole pages shared, -1 where there is no fork.  A parent may have many forks in a call but be none itself.
  * Sequences that are not empty, and parents that are not valid, are left out with
  * QVG_DEV_BAD_INDEX, those for which free pages do not suffice (as above) with QVG_DEV_NO_PAGES. */
@@ -585,7 +591,10 @@ qvg_status qvg_page_fork(const qvg_page_table_params *params, const qvg_pages *p
 /* Sequence b gives up its first drop_first[b] tokens, as far as they fill whole pages, and its last
  * drop_last[b] (int32 [n_seqs] each, one of them may be NULL; anything past the length means all of it).  The
  * entries that stay move to the front of the row, the ones behind them become -1, and the length
- * is what is left.  Pages that no entry names any more are free.  Negative counts are 0, entries out of
+ * is what is left.  Pages that no entry names any more are free.  starts[b] grows by the first tokens
+ * given up (one whose tokens were all first ones goes on where it was); it becomes 0 for a sequence
+ * that drop_last leaves without tokens, which has ended.
+ * Negative counts are 0, entries out of
  * the pool or of free pages are dropped, lengths past the table cut, with QVG_DEV_BAD_INDEX. */
 qvg_status qvg_page_free(const qvg_page_table_params *params, int32_t *refs, int32_t *page_table,
                          int32_t *seq_lens, const int32_t *drop_first, const int32_t *drop_last,
@@ -612,7 +621,7 @@ const char *qvg_status_string(qvg_status status);
  *        structs grew: rebuild callers), qvg_attention.  The paged cache (qvg_rope,
  *        qvg_page_*) came later without a change to what 1.1 had, and later still its 4-bit
  *        formats (qvg_pages grew by two pointers that the others do not read) and the calls on
- *        the pages of sequences. */
+ *        the pages of sequences (whose qvg_page_table_params then grew by starts: rebuild callers). */
 uint32_t qvg_version(void);
 
 #ifdef __cplusplus

@@ -608,10 +608,12 @@ def page_attention(Q: torch.Tensor, kv: PagedKV, page_table: torch.Tensor,
 # ------------------------------------------------------------------------------------
 # The pages of sequences.  refs (int32 [pages]) counts the table entries that name a page, 0 is
 # free; refs, page_table and seq_lens change on the device, in stream order.  Pages are taken in
-# ascending order, for sequences in order: every run has the same outcome.
+# ascending order, for sequences in order: every run has the same outcome.  Where first tokens are
+# dropped (a sliding window), ``starts`` (int64 [sequences], zeros at first) goes into page_append,
+# page_fork and page_free: the position of each sequence's first token, from which new ones count on.
 # ------------------------------------------------------------------------------------
 
-def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int = 0, out_pages: int = 0):
+def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int = 0, out_pages: int = 0, starts=None):
     """(GPU, sequences, entries of a row, parameters) of a call on the pages of sequences."""
     dev, shape = kv.gpu, page_table.shape
     # (one condition for what is as it should be, the checks one by one for what is not)
@@ -625,8 +627,10 @@ def _book(kv: PagedKV, refs, page_table, seq_lens, status, workspace, total: int
         _index(refs, torch.int32, (kv.n_pages,), "refs", dev)
     _check_scratch(status, workspace, dev)
     n_seqs, max_pages = shape
+    if starts is not None:
+        _index(starts, torch.int64, shape[:1], "starts", dev)
     return dev, n_seqs, max_pages, _c.qvg_page_table_params(n_seqs, kv.heads, D, kv.page_tokens, kv.format, max_pages,
-                                                            kv.n_pages, total, out_pages)
+                                                            kv.n_pages, total, out_pages, _ptr(starts))
 
 
 def _book_workspace(prm, kv: PagedKV, workspace, stream):
@@ -671,16 +675,18 @@ def page_copy(kv: PagedKV, src: torch.Tensor, dst: torch.Tensor, *, rows: torch.
 
 
 def page_append(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
-                counts: torch.Tensor, total: int, *, copies: torch.Tensor | None = None,
+                counts: torch.Tensor, total: int, *, starts: torch.Tensor | None = None, copies: torch.Tensor | None = None,
                 workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
     """Let sequence b grow by ``counts[b]`` tokens (int32 [sequences]), ``total`` in all, taking free
     pages where its own are full (qvg_page_append).  Returns the new tokens' slots and positions
-    (int64 [total], sequence after sequence) for ``page_write`` and ``rope``.  A part-filled last page
+    (int64 [total], sequence after sequence) for ``page_write`` and ``rope``.  Positions count from
+    ``starts``; without it they are places in the sequence, which are none to turn by once first tokens
+    were dropped.  A part-filled last page
     that others share is replaced by a copy first, recorded in ``copies`` (int32 [3][sequences]: source,
     destination, rows) if given, with which ``page_copy`` does the same for another layer's pages.  A
     sequence for which pages do not suffice stays as it is, its slots are -1 and ``status`` gets
     QVG_DEV_NO_PAGES."""
-    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace, total=total)
+    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace, total=total, starts=starts)
     _index(counts, torch.int32, (n_seqs,), "counts", dev)
     _need(total >= 0, "total must not be negative")
     if copies is not None:
@@ -696,13 +702,14 @@ def page_append(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_l
 
 
 def page_fork(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
-              parents: torch.Tensor, *, copies: torch.Tensor | None = None,
+              parents: torch.Tensor, *, starts: torch.Tensor | None = None, copies: torch.Tensor | None = None,
               workspace: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Let the empty sequence b begin as a fork of sequence ``parents[b]`` (int32 [sequences],
-    negative: none): whole pages are shared, a part-filled last one is copied (qvg_page_fork).
+    negative: none): whole pages are shared, a part-filled last one is copied, ``starts[b]`` becomes
+    the parent's (qvg_page_fork).
     Returns the copies made (int32 [4][sequences]: source, destination, rows, and whole pages shared, -1
     where there is no fork), with which ``page_copy`` does the same for another layer's pages."""
-    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace)
+    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, workspace, starts=starts)
     _index(parents, torch.int32, (n_seqs,), "parents", dev)
     if copies is None:
         copies = _empty((4, n_seqs), torch.int32, kv.k.device, stream)
@@ -719,11 +726,12 @@ def page_fork(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_len
 
 def page_free(kv: PagedKV, refs: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
               first: torch.Tensor | None = None, last: torch.Tensor | None = None,
-              status: torch.Tensor | None = None, stream=None) -> None:
+              starts: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
     """Sequence b gives up its ``first[b]`` oldest tokens, as far as they fill whole pages, and its
     ``last[b]`` newest (int32 [sequences] each; past the length: all), and the pages that hold
-    nothing else of it (qvg_page_free).  Its entries move to the front of its row."""
-    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, None)
+    nothing else of it (qvg_page_free).  Its entries move to the front of its row, and ``starts[b]``
+    grows by the first tokens given up, or becomes 0 where all that it has goes as its newest."""
+    dev, n_seqs, _, prm = _book(kv, refs, page_table, seq_lens, status, None, starts=starts)
     _need(first is not None or last is not None, "first or last says how many tokens go")
     for t, what in ((first, "first"), (last, "last")):
         if t is not None:

@@ -528,6 +528,7 @@ struct PTakePlan {
     int32_t *refs, *table, *lens, *copies;
     const int32_t *wants;  // parents, or counts of new tokens
     int64_t *slots, *positions;
+    int64_t *starts;       // position of each sequence's first token, or NULL
     void *rows;            // workspace, see take_bytes
     uint32_t *status;
 };
@@ -538,6 +539,7 @@ struct PFreePlan {
     int B, max_pages, page;
     int64_t n_pages;
     int32_t *refs, *table, *lens;
+    int64_t *starts;
     const int32_t *first, *last;
     uint32_t *status;
 };

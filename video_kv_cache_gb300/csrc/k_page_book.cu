@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
             p.copies[2 * p.B + b] = ok && r.need > 0 ? r.len & (p.page - 1) : 0;
             p.copies[3 * p.B + b] = ok ? r.entries : -1;
             if (ok) p.lens[b] = r.len;
+            if (ok && p.starts) p.starts[b] = p.starts[p.wants[b]];
         } else {
             if (ok && r.count > 0) p.lens[b] = r.len + r.count;
             if (copied) atomicSub(p.refs + r.src, 1);
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                 p.copies[2 * p.B + b] = copied ? r.len & (p.page - 1) : 0;
             }
             if (few) {
+                const int64_t start = ok && r.count > 0 && p.starts ? p.starts[b] : 0;
                 for (int k = 0; k < r.count && r.token + k < p.total; k++) {
                     int64_t slot = -1, pos = -1;
                     if (ok) {
@@ -407,6 +409,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                             slot = ((int64_t)page << shift) + (pos & (p.page - 1));
                         else
                             or_status(p.status, QVG_DEV_BAD_INDEX);
+                        pos += start;
                     }
                     p.slots[r.token + k] = slot;
                     p.positions[r.token + k] = pos;
@@ -427,6 +430,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                         slot = ((int64_t)page << shift) + (pos & (p.page - 1));
                     else
                         or_status(p.status, QVG_DEV_BAD_INDEX);
+                    if (p.starts) pos += p.starts[b];
                 }
             }
             p.slots[x] = slot;
@@ -510,7 +514,10 @@ __global__ void __launch_bounds__(256) k_page_free(const __grid_constant__ PFree
             __syncthreads();
             if (j < have) row[j] = page;
         }
-        if (tid == 0) p.lens[b] = (int)(z - a);
+        if (tid == 0) {
+            p.lens[b] = (int)(z - a);
+            if (p.starts) p.starts[b] = z == 0 && last > 0 ? 0 : p.starts[b] + a;
+        }
         __syncthreads();
     }
 }

@@ -149,7 +149,7 @@ qvg_status check_table(const qvg_page_table_params *p) {
     qvg_status rc = check_pool(p->n_heads, p->d, p->page_tokens, p->format, p->n_pages);
     if (rc != QVG_OK) return rc;
     if (p->n_seqs > 65535 || (int64_t)p->max_pages * p->page_tokens > (int64_t(1) << 27)) return QVG_ERR_UNSUPPORTED;
-    if (p->total < 0 || p->out_pages < 0) return QVG_ERR_INVALID_ARG;
+    if (p->total < 0 || p->out_pages < 0 || !aligned(p->starts, 8)) return QVG_ERR_INVALID_ARG;
     if (p->total >= (int64_t(1) << 31) || p->out_pages * p->n_heads * p->page_tokens >= (int64_t(1) << 31) ||
         p->out_pages >= (int64_t(1) << 31))
         return QVG_ERR_UNSUPPORTED;
@@ -193,6 +193,7 @@ PTakePlan take_plan(const qvg_page_table_params *prm, const qvg_pages *pages, in
     p.table = table;
     p.lens = lens;
     p.copies = copies;
+    p.starts = prm->starts;
     p.rows = workspace;
     p.status = status;
     return p;
@@ -462,6 +463,7 @@ qvg_status qvg_page_free(const qvg_page_table_params *prm, int32_t *refs, int32_
     p.refs = refs;
     p.table = page_table;
     p.lens = seq_lens;
+    p.starts = prm->starts;
     p.first = drop_first;
     p.last = drop_last;
     p.status = dev_status;

@@ -217,6 +217,7 @@ class qvg_page_table_params(ctypes.Structure):
         ("n_pages", ctypes.c_int64),
         ("total", ctypes.c_int64),
         ("out_pages", ctypes.c_int64),
+        ("starts", ctypes.c_void_p),
     ]
 
 
