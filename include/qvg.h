@@ -570,8 +570,9 @@ qvg_status qvg_page_copy(const qvg_page_table_params *params, int64_t n, const q
  * where there is none.
  * A sequence whose pages, with those of the sequences before it, are more than the free ones, or
  * that would pass its row of the table, stays as it is, with QVG_DEV_NO_PAGES and -1 for its tokens (a
- * sequence that needs no page grows all the same); so does one that counts or lengths out of range,
- * or more tokens than total, keep from it, with QVG_DEV_BAD_INDEX. */
+ * sequence that needs no page grows all the same); so does one that counts or lengths out of range, more
+ * tokens than total, or a part-filled last page that is out of the pool or free keep from it, with
+ * QVG_DEV_BAD_INDEX. */
 qvg_status qvg_page_append(const qvg_page_table_params *params, const qvg_pages *pages, int32_t *refs,
                            int32_t *page_table, int32_t *seq_lens, const int32_t *counts,
                            int64_t *slots, int64_t *positions, int32_t *copies, void *workspace,
@@ -581,8 +582,9 @@ qvg_status qvg_page_append(const qvg_page_table_params *params, const qvg_pages 
  * none): the parent's whole pages are shared, its last one, if part filled, is copied as far as it
  * is filled, starts[b] becomes the parent's.  copies (int32 [4][n_seqs]) gets source, destination and rows of that copy, -1, -1, 0 where
  * there is none, and the whole pages shared, -1 where there is no fork.  A parent may have many forks in a call but be none itself.
- * Sequences that are not empty, and parents that are not valid, are left out with
- * QVG_DEV_BAD_INDEX, those for which free pages do not suffice (as above) with QVG_DEV_NO_PAGES. */
+ * Sequences that are not empty, and parents that are not valid or whose part-filled last page is out
+ * of the pool or free, are left out with QVG_DEV_BAD_INDEX (whole pages out of the pool are shared as the
+ * entries that they are, with QVG_DEV_BAD_INDEX), those for which free pages do not suffice (as above) with QVG_DEV_NO_PAGES. */
 qvg_status qvg_page_fork(const qvg_page_table_params *params, const qvg_pages *pages, int32_t *refs,
                          int32_t *page_table, int32_t *seq_lens, const int32_t *parents,
                          int32_t *copies, void *workspace, size_t workspace_bytes,

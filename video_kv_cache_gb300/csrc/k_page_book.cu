@@ -227,10 +227,12 @@ struct TakeRow {
     int len, count;    // tokens before, new tokens
     int entries;       // table entries that stay before the new ones
     int src;           // page to be copied, -1: none
-    int last;          // page of the last of those entries, where tokens are in it
+    int last;          // page of the last of those entries, where it is part filled
     int token;         // first of its tokens among all
     int ok;
 };
+
+__device__ __forceinline__ bool in_use(const PTakePlan &p, int page) { return in_pool(page, p.n_pages) && p.refs[page] > 0; }
 
 // One cluster.  Sequence b wants need pages: for a fork, one if its parent's last page is part
 // filled; for new tokens, what they fill, and one more in place of a part-filled last page that others
@@ -274,10 +276,16 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                     if (ok) {
                         r.entries = (int)(len >> shift);
                         r.len = (int)len;
-                        r.need = (len & (p.page - 1)) > 0;
                         r.ok = 1;
-                        if (r.need) r.src = p.table[(int64_t)parent * p.max_pages + r.entries];
-                    } else {
+                        if (len & (p.page - 1)) {
+                            r.need = 1;
+                            r.src = p.table[(int64_t)parent * p.max_pages + r.entries];
+                            ok = in_use(p, r.src);
+                        }
+                    }
+                    if (!ok) {
+                        r = {};
+                        r.src = -1;
                         or_status(status, QVG_DEV_BAD_INDEX);
                     }
                 }
@@ -299,7 +307,10 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                         r.ok = 1;
                         if (len & (p.page - 1)) {
                             const int last = r.last = p.table[(int64_t)b * p.max_pages + have - 1];
-                            if (in_pool(last, p.n_pages) && p.refs[last] > 1) {
+                            if (!in_use(p, last)) {
+                                r.ok = r.need = 0;
+                                or_status(status, QVG_DEV_BAD_INDEX);
+                            } else if (p.refs[last] > 1) {
                                 r.src = last;
                                 r.need++;
                                 r.entries--;
@@ -378,15 +389,13 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
         if (r.ok && !ok) or_status(p.status, QVG_DEV_NO_PAGES);
         if (few && ok) {
             for (int j = 0; j < r.need; j++) p.table[(int64_t)b * p.max_pages + r.entries + j] = s_list[r.first + j];
-            if (FORK && r.need > 0) p.copies[p.B + b] = s_list[r.first];
+            if (FORK && copied) p.copies[p.B + b] = s_list[r.first];
         }
         if constexpr (FORK) {
             // (the entries that are shared, and the copies, are left to the next kernel)
-            const bool lost = ok && r.need > 0 && !in_pool(r.src, p.n_pages);  // the parent's table is bad
-            if (lost) or_status(p.status, QVG_DEV_BAD_INDEX);
-            p.copies[b] = ok && r.need > 0 && !lost ? r.src : -1;
-            if (!ok || r.need == 0) p.copies[p.B + b] = -1;
-            p.copies[2 * p.B + b] = ok && r.need > 0 ? r.len & (p.page - 1) : 0;
+            p.copies[b] = copied ? r.src : -1;
+            if (!copied) p.copies[p.B + b] = -1;
+            p.copies[2 * p.B + b] = copied ? r.len & (p.page - 1) : 0;
             p.copies[3 * p.B + b] = ok ? r.entries : -1;
             if (ok) p.lens[b] = r.len;
             if (ok && p.starts) p.starts[b] = p.starts[p.wants[b]];
@@ -405,10 +414,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                     if (ok) {
                         pos = r.len + k;
                         const int entry = (int)(pos >> shift), page = entry < r.entries ? r.last : s_list[r.first + entry - r.entries];
-                        if (in_pool(page, p.n_pages))
-                            slot = ((int64_t)page << shift) + (pos & (p.page - 1));
-                        else
-                            or_status(p.status, QVG_DEV_BAD_INDEX);
+                        slot = ((int64_t)page << shift) + (pos & (p.page - 1));
                         pos += start;
                     }
                     p.slots[r.token + k] = slot;
@@ -425,11 +431,8 @@ __global__ void __launch_bounds__(kBookThreads, 1) k_page_take(const __grid_cons
                 const TakeRow r = rows[b];
                 if (served(r)) {
                     pos = r.len + (x - r.token);
-                    const int page = p.table[(int64_t)b * p.max_pages + (pos >> shift)];
-                    if (in_pool(page, p.n_pages))
-                        slot = ((int64_t)page << shift) + (pos & (p.page - 1));
-                    else
-                        or_status(p.status, QVG_DEV_BAD_INDEX);
+                    const int64_t page = p.table[(int64_t)b * p.max_pages + (pos >> shift)];
+                    slot = (page << shift) + (pos & (p.page - 1));
                     if (p.starts) pos += p.starts[b];
                 }
             }
