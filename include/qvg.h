@@ -595,9 +595,9 @@ qvg_status qvg_page_fork(const qvg_page_table_params *params, const qvg_pages *p
  * entries that stay move to the front of the row, the ones behind them become -1, and the length
  * is what is left.  Pages that no entry names any more are free.  starts[b] grows by the first tokens
  * given up (one whose tokens were all first ones goes on where it was); it becomes 0 for a sequence
- * that drop_last leaves without tokens, which has ended.
- * Negative counts are 0, entries out of
- * the pool or of free pages are dropped, lengths past the table cut, with QVG_DEV_BAD_INDEX. */
+ * that drop_last leaves without tokens, which has ended.  Negative counts are 0, entries out of the
+ * pool or of free pages are dropped, lengths past the table cut (of sequences that give up nothing
+ * too), with QVG_DEV_BAD_INDEX. */
 qvg_status qvg_page_free(const qvg_page_table_params *params, int32_t *refs, int32_t *page_table,
                          int32_t *seq_lens, const int32_t *drop_first, const int32_t *drop_last,
                          uint32_t *dev_status, void *stream);

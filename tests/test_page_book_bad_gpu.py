@@ -1,5 +1,5 @@
-"""GPU checks of what the calls on the pages of sequences do with tables that cannot be: the
-sequence is left as it is, the others are served, and it is reported."""
+"""GPU checks of what the calls on the pages of sequences do with tables and lengths that cannot be: the
+sequence is left as it is, or its length cut, the others are served, and it is reported."""
 import pytest
 import torch
 
@@ -69,3 +69,17 @@ def test_whole_pages_that_cannot_be_are_shared_as_they_are():
     copies, status = tb._fork(kv, s, [-1, -1, -1, 2, -1, -1])
     assert status == qvg.QVG_DEV_BAD_INDEX and s[2].tolist() == [20, 7, 33, 33, 0, 0]
     assert s[1][3, :3].tolist() == [40, s[1][2, 1].item(), copies[1][3]]
+
+
+def test_lengths_past_the_table_are_cut_where_nothing_is_given_up_too():
+    kv, s, m = _four(6, 40, 4)
+    table, refs = s[1].clone(), s[0].clone()
+    s[2].copy_(tb._int([20, 129, 33, -4, 0, 128]))
+    for kw in (dict(last=tb._int([0] * 6)), dict(first=tb._int([0] * 6)), dict(first=tb._int([0] * 6), last=tb._int([0] * 6))):
+        lens, status = s[2].clone(), tb._int([0])
+        api.page_free(kv, refs, table, lens, status=status, **kw)
+        assert int(status) == qvg.QVG_DEV_BAD_INDEX and lens.tolist() == [20, 128, 33, 0, 0, 128]
+        assert torch.equal(table, s[1]) and torch.equal(refs, s[0])
+        status.zero_()
+        api.page_free(kv, refs, table, lens, status=status, **kw)
+        assert int(status) == 0

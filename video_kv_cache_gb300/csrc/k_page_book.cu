@@ -487,11 +487,11 @@ __global__ void __launch_bounds__(256) k_page_free(const __grid_constant__ PFree
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const int64_t first = p.first ? p.first[b] : 0, last = p.last ? p.last[b] : 0, given = p.lens[b];
         const int64_t len = min(max(given, (int64_t)0), cap);
+        if (tid == 0 && (first < 0 || last < 0 || len != given)) or_status(p.status, QVG_DEV_BAD_INDEX);
         if (first <= 0 && last <= 0) {
-            if (tid == 0 && (first < 0 || last < 0)) or_status(p.status, QVG_DEV_BAD_INDEX);
+            if (tid == 0 && len != given) p.lens[b] = (int)len;
             continue;
         }
-        if (tid == 0 && (first < 0 || last < 0 || len != given)) or_status(p.status, QVG_DEV_BAD_INDEX);
         // tokens [a, z) stay, a at the start of a page
         const int64_t z = len - min(max(last, (int64_t)0), len);
         const int64_t a = max(first, (int64_t)0) >= z ? z : (max(first, (int64_t)0) >> shift) << shift;
