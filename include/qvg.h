@@ -605,9 +605,10 @@ qvg_status qvg_page_free(const qvg_page_table_params *params, int32_t *refs, int
 /* Pages in use (refs > 0), in ascending order, become pages 0, 1, ... of `to`, another pool of
  * params->out_pages pages; out_table ([n_seqs][max_pages], -1 behind each sequence's entries) and out_refs
  * ([out_pages]) are the page table and the counts for it, *live the number of pages in use.  The first
- * pool, page_table and refs stay as they are.  What out_pages has no room for is left out, its entries
- * -1, with QVG_DEV_NO_PAGES; entries out of the pool or of free pages become -1 with
- * QVG_DEV_BAD_INDEX. */
+ * pool, page_table and refs stay as they are, so nothing that is written may share memory with them
+ * (arrays of the pools, the tables and the counts that do are refused).  What out_pages has no room
+ * for is left out, its entries -1, with QVG_DEV_NO_PAGES; entries out of the pool or of free pages
+ * become -1 with QVG_DEV_BAD_INDEX. */
 qvg_status qvg_page_compact(const qvg_page_table_params *params, const qvg_pages *pages,
                             const int32_t *refs, const int32_t *page_table, const int32_t *seq_lens,
                             const qvg_pages *to, int32_t *out_table, int32_t *out_refs, int32_t *live,

@@ -10,6 +10,11 @@
 namespace qvg {
 namespace {
 
+// Whether two stretches of memory share a byte (NULL: it is not there).
+inline bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x && y && x < y + (uint64_t)b_bytes && y < x + (uint64_t)a_bytes;
+}
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline int64_t elem(int dtype) { return dtype == DT_F32 ? 4 : 2; }
 inline bool is_dtype(int dtype) { return dtype >= QVG_F16 && dtype <= QVG_F32; }
@@ -478,12 +483,15 @@ qvg_status qvg_page_compact(const qvg_page_table_params *prm, const qvg_pages *p
     if (rc == QVG_OK) rc = check_pages(pages, prm->format);
     if (rc == QVG_OK) rc = check_pages(to, prm->format);
     if (rc != QVG_OK) return rc;
-    if (prm->out_pages < 1 || out_table == page_table || out_refs == refs) return QVG_ERR_INVALID_ARG;
+    const int64_t entries = (int64_t)prm->n_seqs * prm->max_pages;
+    if (prm->out_pages < 1 || overlap(out_table, entries * 4, page_table, entries * 4) ||
+        overlap(out_refs, prm->out_pages * 4, refs, prm->n_pages * 4))
+        return QVG_ERR_INVALID_ARG;
     const PoolCopy pool = pool_copy(prm, pages, to);
-    for (int a = 0; a < 6; a++)  // another pool, not a part of this one
-        if (pool.src[a] && pool.src[a] < pool.dst[a] + pool.bytes[a] * prm->out_pages &&
-            pool.dst[a] < pool.src[a] + pool.bytes[a] * prm->n_pages)
-            return QVG_ERR_INVALID_ARG;
+    for (int a = 0; a < 6; a++)  // another pool: no array of it shares memory with any of this one
+        for (int b = 0; b < 6; b++)
+            if (overlap(pool.src[a], pool.bytes[a] * prm->n_pages, pool.dst[b], pool.bytes[b] * prm->out_pages))
+                return QVG_ERR_INVALID_ARG;
     if (!refs || !page_table || !seq_lens || !out_table || !out_refs || !live || !aligned(refs, 16) || !aligned(page_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(out_table, 4) || !aligned(out_refs, 4) || !aligned(live, 4))
         return QVG_ERR_INVALID_ARG;
