@@ -365,9 +365,11 @@ typedef enum {
  * and one for the row.  With a as above, a_g = max_k |x_k| over a group and TOP the largest code:
  *   s = a / (64 TOP) in fp32,  t_g = E4M3(64 a_g / a), at most 64,
  *   code = x * 64 TOP / (a t_g) rounded to the format, to nearest even, at most TOP,
- * and the stored value is s * t_g * code.  Quotients are rounded correctly, so that values
- * halfway between two codes go to the even one.  Rows of zeros, tiny rows and rows that are not
- * finite as in 8 bits.
+ * and the stored value is s * t_g * code.  From 16-bit rows that are not turned the codes and group
+ * scales are exactly these: values halfway between two codes go to the even one.  From fp32 rows and
+ * turned keys the quotients are worked out in fp32, within 2^-21 of them, so that a value that near to a
+ * halfway one may go to either code (and a group's scale likewise).  Rows of zeros, tiny rows and rows
+ * that are not finite as in 8 bits.
  *   k, v              two codes a byte, channel 2i in the low four bits: [..][64] bytes
  *   k_group, v_group  E4M3 [n_pages][n_heads][page_tokens][8], group g channels 16g .. 16g + 15
  * Group scales that a caller writes itself may be any E4M3 number up to 64 in magnitude, or NaN; larger

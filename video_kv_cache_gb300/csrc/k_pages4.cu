@@ -6,10 +6,11 @@
 // Sixteen lanes hold a row, eight neighbouring channels each, so that two lanes share a group; they
 // take four heads' keys and values of a token, eight rows.  Keys that are turned in the half layout
 // are worked on in split pieces (rows.cuh) and change places through shared memory.
-// Quotients are rounded correctly, since halves are common among them (x = a / 2 is 3.5 of INT4's
-// codes): x is multiplied by 64 TOP and the power of two that brings a to 1 .. 2, both exact in 16
-// bits, and the product with an approximate reciprocal is corrected once by its exact remainder
-// (Markstein's division).
+// Halves are common among the quotients (x = a / 2 is 3.5 of INT4's codes) and have to come out as
+// halves: x is multiplied by 64 TOP and the power of two that brings a to 1 .. 2, and a by t, both
+// exact for rows that come in 16 bits, and the product with an approximate reciprocal is corrected once
+// by its exact remainder (Markstein's division).  For fp32 rows and turned keys those two products are
+// rounded, 2^-24 each, so that a quotient next to a half may become one.
 //
 // Bound by instructions, which issue in 77 % of the cycles: about 170 for two rows and a warp, with the
 // turn, against 332 bytes of a row's traffic in bf16.  32760 tokens of 12 heads from bf16 to INT4 pages:
