@@ -1,5 +1,5 @@
 """GPU checks of 4-bit pages at the ends of their ranges: weights and value scales as large as the running
-references let them get, every group scale read back."""
+references let them get, every group scale read back, keys of any bits that a mask hides."""
 import math
 
 import numpy as np
@@ -93,3 +93,55 @@ def test_reads_give_what_every_group_scale_stands_for(fmt):
             want = m4.pool_rows(kv, name, table[0], 32)[0].float()
             assert torch.equal(X[which].isnan(), want.isnan()) and int(want.isnan().sum()) == 32
             assert torch.equal(X[which].nan_to_num(), want.nan_to_num())
+
+
+SPANS = [  # queries, cached tokens, query heads, window, a key that only some queries see
+    (5, 300, 2, 0, 297), (7, 900, 2, 300, 596), (140, 300, 1, 0, 200), (140, 2600, 1, 0, 2597), (140, 1200, 1, 500, 566),
+]
+
+
+@pytest.mark.parametrize("fmt", [E2M1, INT4])
+@pytest.mark.parametrize("nq,n,group,window,j", SPANS)
+def test_any_bits_of_a_key_leave_the_queries_that_do_not_see_it(fmt, nq, n, group, window, j):
+    # what page_write never stores, group scales past 64 and codes of -8, in a row whose scale is anything
+    g = torch.Generator().manual_seed(nq + n)
+    kv, table = m4.cache(g, [n], 1, fmt, 32)
+    Q = torch.randn((nq, group, 128), generator=g).to(BF)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    page, row = int(table[0, j // 32]), j % 32
+    was = [getattr(kv, name)[page, 0, row].clone() for name in m4.POOLS]
+    spans = m4.seen(n, nq, window)
+    blind = [i for i, (a, z) in enumerate(spans) if not a <= j < z]
+    assert 0 < len(blind) < nq
+    K, V = m4.pool_rows(kv, "k", table[0], n)[0], m4.pool_rows(kv, "v", table[0], n)[0]
+    wide = [m4.attend_rows(Q[:, h].double(), K, V, blind, spans, F32, 0.0) for h in range(group)]
+    narrow = [m4.attend_rows(Q[:, h].double(), K, V, blind, spans, BF, 2.0 ** -10 if nq * group > 16 else 0.0) for h in range(group)]
+    # as large a scale as the reference lets stay below it
+    near = 2.0 ** math.floor(math.log2(float(kv.v_scale[page, 0].nan_to_num().max()))) * JUST_BELOW_8
+    rows = [(0x7E, 0x77, near), (0xFE, 0x99 if fmt is INT4 else 0xFF, near), (0x70, 0x77, 1.0), (0x68, 0x88, near),
+            (0xE8, 0x88, near), (0x7E, 0x80, 0.0)]
+    for trial in range(len(rows) + 24):
+        if trial < len(rows):
+            t, c, s = rows[trial]
+            for name in m4.POOLS:
+                x = getattr(kv, name)
+                if name.endswith("scale"):
+                    x[page, 0, row] = s
+                else:
+                    x.view(torch.uint8)[page, 0, row] = t if name.endswith("group") else c
+        else:
+            for name in m4.POOLS:
+                x = getattr(kv, name)[page, 0, row]
+                x = x.view(1) if x.dim() == 0 else x
+                bits = x.view(torch.uint8)
+                bits.copy_(torch.randint(0, 256, bits.shape, generator=g, dtype=torch.uint8))
+        out, lse = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32, return_lse=True)
+        alone = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window)
+        for h in range(group):
+            tp._within(out[blind, h], wide[h][0], wide[h][2], "trial %d" % trial)
+            tp._within(lse[blind, h], wide[h][1], wide[h][3], "lse, trial %d" % trial)
+            tp._within(alone[blind, h], narrow[h][0], narrow[h][2], "alone, trial %d" % trial)
+    for name, x in zip(m4.POOLS, was):
+        getattr(kv, name)[page, 0, row] = x
+    out = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32)
+    assert bool(out.isfinite().all())

@@ -106,8 +106,8 @@ __device__ __forceinline__ bool is_finite(float x) {
 
 // A row may have to be computed once more by one warp, over the keys that it sees and no others,
 // where a mask hides keys from some rows of a tile:
-//   * 16-bit or E4M3 pages: a value that is NaN or infinite (a code that is NaN), multiplied by the
-//     zero weight of a query that does not see its key, makes that query's row NaN.  Rows that did
+//   * 16-bit, E4M3 or 4-bit pages: a value that is NaN or infinite (a code or a group's scale that is
+//     NaN, or of 4 bits that page_write does not store), multiplied by the zero weight of a query that does not see its key, makes that query's row NaN.  Rows that did
 //     not come out finite and shared a tile with such a key, which they do not see.  (Those that see one themselves are
 //     what they should be.  Doing them again too, a key at a time, took seconds where a NaN is early
 //     in a long cache: 44 us became 1600 for one query of four heads over 4096 keys.)
@@ -185,7 +185,7 @@ static __device__ __noinline__ bool sees_too_little(const PAttnPlan &p, const fl
     return v > 0.f && too_far(some, v, limit);
 }
 
-// First and last of keys [from, to) with a value that is not finite, looked for by a whole warp;
+// First and last of keys [from, to) with a value that is not finite, or may not be once widened, looked for by a whole warp;
 // first > last where there is none.
 struct BadKeys {
     int first, last;
@@ -199,9 +199,16 @@ __device__ __forceinline__ BadKeys bad_values(const PAttnPlan &p, int b, int h, 
         bool bad = false;
         const int64_t row = ((page_of(p, b, key, shift, bad) * p.H + h) << shift) + (key & (p.page - 1));
         bool odd;
-        if (four_bits(p.fmt)) {  // (a group's scale that is NaN)
+        if (four_bits(p.fmt)) {
+            // a group's scale that is NaN or past 64 (0x68), or an INT4 code of -8: widened, and multiplied by
+            // the row's scale, they may pass fp16's range
             const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.vg + row * kGroups));
-            odd = __vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            odd = __vcmpgtu4(w.x & 0x7F7F7F7Fu, 0x68686868u) | __vcmpgtu4(w.y & 0x7F7F7F7Fu, 0x68686868u);
+            if (p.fmt == PF_INT4) {  // (a half-byte of 8 is one of 0 here, from which a 1 is borrowed)
+                const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(p.v) + row * (kD / 2)) +
+                                         (lane & 15)) ^ 0x88888888u;
+                odd |= ((c - 0x11111111u) & ~c & 0x88888888u) != 0;
+            }
         } else if (p.fmt == PF_E4M3) {
             const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.v) + row * kD) + (lane & 15));
             odd = __vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
