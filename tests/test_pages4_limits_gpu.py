@@ -145,3 +145,35 @@ def test_any_bits_of_a_key_leave_the_queries_that_do_not_see_it(fmt, nq, n, grou
         getattr(kv, name)[page, 0, row] = x
     out = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, out_dtype=F32)
     assert bool(out.isfinite().all())
+
+
+@pytest.mark.parametrize("fmt", [torch.float8_e4m3fn, torch.int8, E2M1, INT4])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("size", [2.0 ** 125, -3.4028234663852886e38])
+def test_the_largest_scale_of_a_hidden_key_in_a_part_that_shows_a_query_nothing(fmt, size, which):
+    # the keys are split: queries 30 and on of the first tile see keys of other parts than key 1487's only
+    nq, n, group, window, page = 300, 1800, 2, 30, 128
+    four = fmt in (E2M1, INT4)
+    g = torch.Generator().manual_seed(7)
+    kv, table = (m4.cache if four else tp._cache)(g, [n], 1, fmt, page)
+    if four:
+        K, V = (m4.pool_rows(kv, x, table[0], n)[0] for x in ("k", "v"))
+    else:
+        K, V = (pm.pool_rows(getattr(kv, x), getattr(kv, x + "_scale"), table[0], n, page)[0] for x in ("k", "v"))
+    Q = torch.randn((nq, group, 128), generator=g).to(HF)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    top = {torch.float8_e4m3fn: 0x7E, torch.int8: 0x7F, E2M1: 0x77, INT4: 0x77}[fmt]
+    at = (int(table[0, 1487 // page]), 0, 1487 % page)
+    getattr(kv, which + "_scale")[at] = size
+    getattr(kv, which).view(torch.uint8)[at] = top
+    if four:
+        getattr(kv, which + "_group").view(torch.uint8)[at] = 0x68   # 64
+    spans = m4.seen(n, nq, window)
+    blind = [i for i, (a, z) in enumerate(spans) if not a <= 1487 < z][::7]
+    u_kv = 2.0 ** -10 if four else 2.0 ** -11
+    for kw, u in ((dict(out_dtype=BF), u_kv), (dict(out_dtype=F32), 0.0), (dict(out_dtype=HF), 0.0)):
+        for max_kv in (None, n):
+            out = api.page_attention(Q.cuda(), kv, table.cuda(), lens, window=window, max_kv=max_kv, **kw)
+            for h in range(group):
+                want, _, bound, _ = m4.attend_rows(Q[:, h].double(), K, V, blind, spans, kw["out_dtype"], u)
+                tp._within(out[blind, h], want, bound, "head %d" % h)

@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(TcShape<FMT>::THREADS, 1)
                     ok = meet<128>(id, ok);
                     if (!ok) break;  // the four warps leave together
                     m = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
-                    ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 121);
+                    // (up to the largest scale there is, so that no factor below passes fp16's range)
+                    ee = min(max((int)(__float_as_uint(m) >> 23) - 127, -100), 127);
                 }
                 if (value) {
                     // the reference moves only when a scale passes it by 2^3: codes of at most
