@@ -29,7 +29,8 @@
 // and chunk q of a key is two groups, eight bytes of a value the one group g.  They are widened to a
 // group's scale times a code, exact in fp16 (page_codes.cuh).  Bound by instructions, 333 of a warp for 16
 // keys and a head, which issue in 58 % of the cycles: one query of 32 sequences of 9000 to 20000, 8 heads,
-// cold caches: INT4 128 us (4.4 TB/s), E2M1 119.
+// from a graph, cold caches: INT4 128 us (4.4 TB/s), E2M1 119, and 1 more with the log-sum-exp in INT4; called
+// with other inputs in turn 140 (4.1 TB/s).
 //
 // The keys are cut into S splits, a CTA each.  The warps' results are joined in shared memory;
 // the splits', where there are at most eight, by a cluster of the S CTAs through each other's
@@ -652,10 +653,10 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
                             }
                         } else {
                             uint4 vr[4][FOUR ? 1 : NCH / 2];  // keys 2q, 2q + 1, 2q + 8, 2q + 9
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 4; k++) {
                                 const int at = 16 * z + 2 * q + (k & 1) + (k >> 1) * 8;
-    #pragma unroll
+#pragma unroll
                                 for (int c = 0; c < NCH / 2; c++) {
                                     vr[k][c] = chunk(vt, w0 + at, c * 8 + g);
                                     // values that no row sees may hold anything
@@ -663,36 +664,36 @@ __global__ void __launch_bounds__(RowsShape<FMT, RT>::THREADS, RowsShape<FMT, RT
                                 }
                             }
                             if constexpr (WIDE) {
-    #pragma unroll
+#pragma unroll
                                 for (int t = 0; t < 8; t++) {
                                     const int w = t >> 1, sel = t & 1 ? 0x7632 : 0x5410;
                                     const uint32_t a[4] = {__byte_perm(word_of(vr[0][0], w), word_of(vr[1][0], w), sel),
                                                            __byte_perm(word_of(vr[0][1], w), word_of(vr[1][1], w), sel),
                                                            __byte_perm(word_of(vr[2][0], w), word_of(vr[3][0], w), sel),
                                                            __byte_perm(word_of(vr[2][1], w), word_of(vr[3][1], w), sel)};
-    #pragma unroll
+#pragma unroll
                                     for (int y = 0; y < RT; y++) mma16816<PVB>(o[y][t], a, pb[z][y][0], pb[z][y][1]);
                                 }
                             } else {
-    #pragma unroll
+#pragma unroll
                                 for (int w = 0; w < 2; w++) {
                                     // the codes of two keys interleaved, then widened pair by pair:
                                     // channels 4w .. 4w + 3 of the first and of the last eight
                                     uint2 a[2][2][2];  // [first / last eight][keys 2q.. / 2q + 8..][channels 0, 1 / 2, 3]
-    #pragma unroll
+#pragma unroll
                                     for (int e = 0; e < 2; e++)
-    #pragma unroll
+#pragma unroll
                                         for (int k = 0; k < 2; k++) {
                                             const uint32_t v0 = word_of(vr[2 * k][0], w + 2 * e), v1 = word_of(vr[2 * k + 1][0], w + 2 * e);
                                             a[e][k][0] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x5140));
                                             a[e][k][1] = codes_to_f16<FMT == PF_E4M3>(__byte_perm(v0, v1, 0x7362));
                                         }
-    #pragma unroll
+#pragma unroll
                                     for (int t = 0; t < 4; t++) {
                                         const int x = t >> 1;
                                         const uint32_t f[4] = {t & 1 ? a[0][0][x].y : a[0][0][x].x, t & 1 ? a[1][0][x].y : a[1][0][x].x,
                                                                t & 1 ? a[0][1][x].y : a[0][1][x].x, t & 1 ? a[1][1][x].y : a[1][1][x].x};
-    #pragma unroll
+#pragma unroll
                                         for (int y = 0; y < RT; y++) mma16816<false>(o[y][4 * w + t], f, pb[z][y][0], pb[z][y][1]);
                                     }
                                 }
