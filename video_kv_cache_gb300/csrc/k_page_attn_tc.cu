@@ -57,11 +57,13 @@
 // if the base moves (twice, as for 8 bits, leaves the tensor cores waiting longer: 4680 x 32760 x 12
 // heads of E2M1 with the log-sum-exp 1121 us; folded, where scores need no scales, it is the other way
 // round, 864 and 920).  Scales of values multiplied into them there too: 1083 instead of 1046.
-// 4680 over 32760 of 12 heads, cold caches: E2M1 873 us (1079 TFLOP/s), INT4 1000; with the log-sum-exp
+// 4680 over 32760 of 12 heads, cold caches: E2M1 873 us (1079 TFLOP/s), INT4 1005; with the log-sum-exp
 // 1046 and 1075; six causal prompts of 17 to 2000 queries over 500 to 9000 keys, 32 heads on 8, fp16, window
 // 4096: 419 and 422.  What bounds: 52 % of the issue slots are busy, a tile pair takes three times its
-// products' time (tensor pipes idle while scores wait for softmax instructions, 12900 of a warp in all,
-// and those for shared memory, barriers and the instruction cache).
+// products' time.  The widening, done anew for every 256 rows, and the softmax share the issue slots (10300
+// instructions of a warp for a pair of row tiles and a key tile folded, 11900 not), and wait for shared
+// memory, barriers and the instruction cache; with a quarter of the widening left out the first took 795
+// instead of 869, not folded 1040 instead of 1046.  (bf16 pages: 602.)
 //
 // Masks: a tile that some row does not see whole is compared key by key; a weight that is
 // hidden is 0.  Memory that no row sees (rows past the length) is not multiplied: the value
